@@ -60,6 +60,10 @@ typedef enum dsa_status {
 /* Limits. sel_width may not exceed DSA_MAX_SEL_WIDTH. */
 #define DSA_LATENT_DIM 512
 #define DSA_MAX_SEL_WIDTH 8192
+#define DSA_INDEX_DIM 128        /* width of an index key */
+#define DSA_MAX_INDEX_HEADS 128  /* dsa_pool_scores: num_heads */
+#define DSA_MAX_KPOOL 128        /* dsa_pool_scores: kpool */
+#define DSA_MAX_PLAN_SEQS 16384  /* dsa_plan_step: num_seqs */
 
 /* Version of this ABI (incremented on any incompatible change). */
 int32_t dsa_abi_version(void);
@@ -321,8 +325,130 @@ int32_t dsa_mla_decode_static(const void* q, const void* k_cache, const void* v_
                               float v_scale, float sm_scale, void* out, void* stream);
 
 /*
+ * dsa_plan_step: the pages and slots of a step's new tokens, built on the device from the
+ * requests' lengths (decode_k.rs, decode_k: slot = physical_page*block_size + position %
+ * block_size; the pages' host does this per row). For request s with base = base_lens[s]
+ * tokens already cached and new_lens[s] new ones (0 allowed), pages
+ *   ceil(base/block_size) .. ceil((base+new)/block_size) - 1
+ * of its block table are new: they are taken from free_pages in order (request by request)
+ * and written into block_tables; all other entries stay as they are. Every new token has a
+ * row:
+ *   rows_per_seq = 0   packed rows: the tokens of request 0, then of request 1, ...
+ *   rows_per_seq > 0   row s*rows_per_seq + i is token i of request s (the decode's and the
+ *                      verify rows' order); max_rows must be num_seqs*rows_per_seq
+ * and each of the max_rows rows is written: slots = the token's cache slot, positions =
+ * base + i, row_lens = positions + 1 (what a decode row sees), row_seqs = s. A row without a
+ * token gets slot -1, position -1, length 0 and request -1, which the writers skip, the
+ * selector answers with holes and the decode with zeros, so a captured step of a fixed
+ * number of rows serves fewer requests.
+ *  base_lens, new_lens  int32 [num_seqs].  free_pages  int32 [num_free] page ids >= 0.
+ *  block_tables  int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq >= 1.
+ *  slots  int64 [max_rows], 8-byte aligned; positions, row_lens, row_seqs  int32 [max_rows].
+ *  info   int32 [4]: rows with a token, pages taken, status, 0. A caller advances its free
+ *         list by info[1]. The status is DSA_ERR_DEVICE_BOUNDS when a length is negative
+ *         (taken as 0), a request has more new tokens than rows_per_seq (cut to it) or than
+ *         its table holds (the tokens past the table have rows without a token), the packed
+ *         rows exceed max_rows (the last ones are dropped; their pages are assigned), the
+ *         free pages run out (their table entries become -1, the slots of their tokens too)
+ *         or a table entry that cached tokens already need is negative; else DSA_OK.
+ *  num_seqs 0..DSA_MAX_PLAN_SEQS, num_free >= 0, max_rows >= 0; max_blocks_per_seq*
+ *  block_size below 2^31 (DSA_ERR_UNSUPPORTED otherwise). Pointers to empty arrays may be
+ *  null. The call is idempotent: run again on the same input it writes the same values.
+ */
+int32_t dsa_plan_step(const int32_t* base_lens, const int32_t* new_lens, int32_t num_seqs,
+                      int32_t rows_per_seq, int32_t max_rows, const int32_t* free_pages,
+                      int32_t num_free, int32_t block_size, int32_t* block_tables,
+                      int32_t max_blocks_per_seq, int64_t* slots, int32_t* positions,
+                      int32_t* row_lens, int32_t* row_seqs, int32_t* info, void* stream);
+
+/*
+ * dsa_index_write: the writer of the index cache that dsa_pool_scores reads. For each row i
+ * with slots[i] >= 0:
+ *   y = (x - mean x) / sqrt(mean (x - mean x)^2 + eps) * norm_weight + norm_bias  over the
+ *       128 dims (y = x when norm_weight is null; norm_bias may be null on its own),
+ *   s = max(max_c |y[c]|, 2^-100) / 448,  codes = E4M3(y / s), round to nearest even.
+ * Page p of the index cache starts at byte p*page_stride_bytes and holds block_size rows of
+ * 128 codes, then block_size float32 scales; slot = page*block_size + row of the page, the
+ * same slots as the latent cache's. A row with a NaN or an infinity stores a NaN scale or
+ * NaN codes.
+ *  keys         bf16 [rows, 128], norm_weight and norm_bias bf16 [128]; 16-byte aligned.
+ *  slots        int64 [rows], 8-byte aligned; a negative slot writes nothing. Rows with the
+ *               same slot race.
+ *  rows >= 0 (keys and slots may be null when rows == 0); eps >= 0 and finite; block_size
+ *  >= 1; page_stride_bytes >= block_size*132 and a multiple of 16; index_cache 16-byte
+ *  aligned. The pool's size is not an argument, as for dsa_latent_write.
+ */
+int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* norm_bias,
+                        const int64_t* slots, int32_t rows, float eps, int32_t block_size,
+                        int64_t page_stride_bytes, void* index_cache, void* stream);
+
+/*
+ * dsa_pool_scores: the pooled indexer scores that dsa_select_pools ranks (decode_k.rs,
+ * decode_k: the indexer runs before the selection; its kernel body is not on the pages and
+ * this is the reading taken). With key codes k_j and scale s_j of position j from the paged
+ * index cache, for decode row r (sequence r / rows_per_seq):
+ *   I[r,j]      = s_j * sum_h head_weights[r,h] * max(0, q[r,h,:] . k_j)
+ *   scores[r,p] = max of I[r,j] over the kpool positions j of pool p, when the whole pool
+ *                 lies at or before q_pos[r] ((p+1)*kpool - 1 <= q_pos[r]), else -inf.
+ * Positions past a row's last visible pool are not read for it. A NaN in a visible key or
+ * its scale makes its pool's score NaN, one in a row's q or head_weights (or an infinity
+ * in q) the row's visible scores; the selector ranks NaN last.
+ *  q             bf16 [R, num_heads, 128], R = num_seqs*rows_per_seq; 16-byte aligned.
+ *  head_weights  float32 [R, num_heads], 4-byte aligned (any head or softmax scale folded in).
+ *  index_cache   pages as dsa_index_write stores them; 16-byte aligned.
+ *  block_tables, max_blocks_per_seq  as for dsa_mla_decode (0: one shared table).
+ *  q_pos         int32 [R]; -1 sees nothing.
+ *  scores        float32 [R, n_pools], 4-byte aligned; every element is written.
+ *  device_status int32 device word or null: DSA_ERR_DEVICE_BOUNDS is put there (when it
+ *                holds 0) if a visible position's block-table entry is negative or past
+ *                max_blocks_per_seq (the pool's score is then -inf or that of its other
+ *                positions), DSA_ERR_TIMEOUT if a pipeline wait ran out of time. The call
+ *                never clears it.
+ *  num_seqs, rows_per_seq >= 1; num_heads 1..DSA_MAX_INDEX_HEADS and kpool 1..DSA_MAX_KPOOL
+ *  (DSA_ERR_UNSUPPORTED above); n_pools >= 0 (scores may be null at 0); n_pools*kpool and
+ *  R*num_heads below 2^31 (DSA_ERR_UNSUPPORTED otherwise).
+ */
+int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* index_cache,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* q_pos, int32_t num_seqs, int32_t rows_per_seq,
+                        int32_t num_heads, int32_t block_size, int64_t page_stride_bytes,
+                        int32_t kpool, int32_t n_pools, float* scores, int32_t* device_status,
+                        void* stream);
+
+/*
+ * dsa_mla_decode_full: the decode over a row's WHOLE cache, for layers and contexts without
+ * a selection. For row r (sequence seq = r / rows_per_seq) and head h, with K_j, V_j as for
+ * dsa_mla_decode:
+ *   out[r,h,:] = sum_{j < len(r)} softmax_j(sm_scale * q[r,h,:].(k_scale*K_j)) (v_scale*V_j)
+ *                and 0 when len(r) <= 0.
+ * Arguments as dsa_mla_decode without the selection (any length the block table holds; a
+ * length past max_blocks_per_seq*block_size, or a negative entry, is a device-side
+ * DSA_ERR_DEVICE_BOUNDS and its positions are skipped), except:
+ *  seq_lens     verify_rows = 0: int32 [R], len(r) = seq_lens[r]; verify_rows = 1: int32
+ *               [num_seqs], len of row i of sequence s = seq_lens[s] + i + 1 (decode_k.rs,
+ *               decode_k). A position past every row's length is never read; a NaN there or
+ *               at a position that only other rows see does not reach a row's output, and
+ *               one that a row sees makes that row NaN.
+ *  workspace    device memory, 256-byte aligned, at least
+ *               dsa_mla_decode_full_workspace_bytes of the same num_seqs, rows_per_seq and
+ *               num_q_heads. The call never allocates and can be captured. Its first 256
+ *               bytes hold the device status word (dsa_read_device_status). Calls that may
+ *               overlap on the GPU need workspaces of their own.
+ *  num_seqs*rows_per_seq*num_q_heads at most 2^22 (DSA_ERR_UNSUPPORTED above).
+ */
+size_t dsa_mla_decode_full_workspace_bytes(int32_t num_seqs, int32_t rows_per_seq,
+                                           int32_t num_q_heads);
+int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                            const int32_t* seq_lens, int32_t num_seqs, int32_t rows_per_seq,
+                            int32_t num_q_heads, int32_t block_size, int64_t cache_stride_bytes,
+                            float k_scale, float v_scale, float sm_scale, void* out,
+                            int32_t verify_rows, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
  * Device status of the latest call on a caller workspace (dsa_mla_decode_ws /
- * dsa_mla_decode_host), on the library workspace of the current device
+ * dsa_mla_decode_host / dsa_mla_decode_full), on the library workspace of the current device
  * (dsa_last_device_status), or on the fixed array of dsa_mla_decode_static
  * (dsa_static_device_status; like that entry point it allocates nothing). Each
  * synchronises the stream, writes the status to *status_out and returns DSA_OK, or

@@ -50,6 +50,12 @@ SIGNATURES = {
     "dsa_resolve_indices": ([_P, _P, _I32, _I32, _P, _P, _P], _I32),
     "dsa_latent_write": ([_P, _P, _P, _I32, _F32, _F32, _I32, _I64, _P, _P], _I32),
     "dsa_select_pools": ([_P, _P, _I32, _I32, _I32, _I32, _P, _P], _I32),
+    "dsa_plan_step": ([_P, _P, _I32, _I32, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _P], _I32),
+    "dsa_index_write": ([_P, _P, _P, _P, _I32, _F32, _I32, _I64, _P, _P], _I32),
+    "dsa_pool_scores": ([_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _I32, _I32, _P, _P, _P], _I32),
+    "dsa_mla_decode_full_workspace_bytes": ([_I32, _I32, _I32], _SZ),
+    "dsa_mla_decode_full": ([_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P, _I32, _P,
+                             _SZ, _P], _I32),
     "dsa_absorb_q": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "dsa_absorb_o": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "dsa_read_device_status": ([_P, _P, _P], _I32),

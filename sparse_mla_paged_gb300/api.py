@@ -6,7 +6,7 @@ raise DsaError on a non-OK status.
 """
 from __future__ import annotations
 
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -14,6 +14,7 @@ from . import _lib
 from ._lib import DsaError, check  # noqa: F401
 
 LATENT = 512
+INDEX = 128
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -232,6 +233,189 @@ def absorb_o(o_proj: torch.Tensor, kv_b: torch.Tensor, heads: int, nope: int, vd
     out, code = _absorb_out((hidden, heads * kvl), dtype, o_proj.device, out)
     check(_lib.load().dsa_absorb_o(_ptr(o_proj), _ptr(kv_b), heads, nope, vd, kvl, hidden, _ptr(out), code,
                                    _stream(stream)), "dsa_absorb_o")
+    return out
+
+
+def _on(t: torch.Tensor, *others):
+    """Device guard of t's device; every other tensor has to be there too."""
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+    return torch.cuda.device(t.device)
+
+
+def _current(stream, device):
+    """The stream of a call (default: the device's current one) as a torch stream, for allocations."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(_stream(stream), device=device)
+
+
+class StepPlan(NamedTuple):
+    """dsa_plan_step's outputs, a row per new token: slots int64, positions, row_lens and row_seqs
+    int32 [rows]; info int32 [4] (rows with a token, pages taken, status, 0)."""
+    slots: torch.Tensor
+    positions: torch.Tensor
+    row_lens: torch.Tensor
+    row_seqs: torch.Tensor
+    info: torch.Tensor
+
+
+def alloc_step_plan(rows: int, device=None) -> StepPlan:
+    """Output buffers of plan_step, to be kept from step to step (a captured step needs fixed ones)."""
+    i32 = dict(dtype=torch.int32, device=device or "cuda")
+    return StepPlan(torch.empty(rows, dtype=torch.int64, device=device or "cuda"), torch.empty(rows, **i32),
+                    torch.empty(rows, **i32), torch.empty(rows, **i32), torch.empty(4, **i32))
+
+
+def plan_step(base_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_size: int,
+              block_tables: torch.Tensor, rows_per_seq: int = 0, max_rows: Optional[int] = None,
+              out: Optional[StepPlan] = None, stream=None) -> StepPlan:
+    """dsa_plan_step: pages for every request's new tokens into block_tables (in place), and each
+    new token's slot, position, visible length and request. rows_per_seq 0 packs the rows
+    (max_rows is then needed, unless out gives it), else row s*rows_per_seq + i is token i of
+    request s."""
+    for t, n in ((base_lens, "base_lens"), (new_lens, "new_lens"), (free_pages, "free_pages"),
+                 (block_tables, "block_tables")):
+        _need(t, torch.int32, n)
+    n = base_lens.numel()
+    if new_lens.numel() != n or block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("base_lens [num_seqs], new_lens [num_seqs], block_tables [num_seqs, max_blocks_per_seq]")
+    rows = n * int(rows_per_seq) if rows_per_seq else (max_rows if out is None else out.slots.numel())
+    if rows is None or (max_rows is not None and int(max_rows) != rows):
+        raise ValueError("max_rows must be the number of rows to write (num_seqs*rows_per_seq unless packed)")
+    with _on(base_lens, new_lens, free_pages, block_tables, *(out or ())):
+        s = _current(stream, base_lens.device)
+        if out is None:
+            with torch.cuda.stream(s):
+                out = alloc_step_plan(int(rows), base_lens.device)
+        _need(out.slots, torch.int64, "out.slots")
+        if out.slots.numel() != rows or out.info.numel() < 4:
+            raise ValueError(f"out must hold {rows} rows")
+        for t in out[1:]:
+            _need(t, torch.int32, "out")
+            if t is not out.info and t.numel() != rows:
+                raise ValueError(f"out must hold {rows} rows")
+        check(_lib.load().dsa_plan_step(_ptr(base_lens), _ptr(new_lens), n, int(rows_per_seq), int(rows),
+                                        _ptr(free_pages), free_pages.numel(), int(block_size), _ptr(block_tables),
+                                        int(block_tables.shape[1]), _ptr(out.slots), _ptr(out.positions),
+                                        _ptr(out.row_lens), _ptr(out.row_seqs), _ptr(out.info), s.cuda_stream),
+              "dsa_plan_step")
+    return out
+
+
+def index_page_stride(block_size: int) -> int:
+    """Smallest page stride of the index cache: block_size*(128 codes + a float32 scale), in 16s."""
+    return (block_size * (INDEX + 4) + 15) // 16 * 16
+
+
+def index_write(keys: torch.Tensor, slots: torch.Tensor, block_size: int, page_stride_bytes: int,
+                index_cache: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+                norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> torch.Tensor:
+    """dsa_index_write: the (layer-normalised) index keys bf16 [rows, 128] as E4M3 codes and a
+    float32 scale per row into each row's slot (negative: skipped). Returns index_cache."""
+    _need(keys, torch.bfloat16, "keys")
+    _need(slots, torch.int64, "slots")
+    _need(index_cache, torch.uint8, "index_cache")
+    if keys.shape[-1] != INDEX or slots.numel() * INDEX != keys.numel():
+        raise ValueError("keys [rows, 128], slots [rows]")
+    for t, n in ((norm_weight, "norm_weight"), (norm_bias, "norm_bias")):
+        if t is not None:
+            _need(t, torch.bfloat16, n)
+            if t.numel() != INDEX:
+                raise ValueError(f"{n} [128]")
+    with _on(index_cache, keys, slots, norm_weight, norm_bias):
+        check(_lib.load().dsa_index_write(_ptr(keys), _ptr(norm_weight), _ptr(norm_bias), _ptr(slots),
+                                          int(slots.numel()), float(eps), int(block_size), int(page_stride_bytes),
+                                          _ptr(index_cache), _stream(stream)), "dsa_index_write")
+    return index_cache
+
+
+def _table_rows(block_tables, max_blocks_per_seq, num_seqs):
+    need = num_seqs * max_blocks_per_seq if max_blocks_per_seq > 0 else 1
+    if block_tables.numel() < need:
+        raise ValueError(f"block_tables must hold {need} entries")
+
+
+def pool_scores(q: torch.Tensor, head_weights: torch.Tensor, index_cache: torch.Tensor, block_tables: torch.Tensor,
+                max_blocks_per_seq: int, q_pos: torch.Tensor, num_seqs: int, rows_per_seq: int, num_heads: int,
+                block_size: int, page_stride_bytes: int, kpool: int, n_pools: int, out=None, device_status=None,
+                stream=None) -> torch.Tensor:
+    """dsa_pool_scores: float32 [R, n_pools], per row the maximum over each pool's kpool positions of
+    scale_j * sum_h head_weights[h] * max(0, q[h] . k_j); -inf for pools that end after q_pos."""
+    _need(q, torch.bfloat16, "q")
+    _need(head_weights, torch.float32, "head_weights")
+    _need(index_cache, torch.uint8, "index_cache")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(q_pos, torch.int32, "q_pos")
+    rows = num_seqs * rows_per_seq
+    if q.numel() != rows * num_heads * INDEX or head_weights.numel() != rows * num_heads or q_pos.numel() != rows:
+        raise ValueError("q [R, num_heads, 128], head_weights [R, num_heads], q_pos [R]")
+    _table_rows(block_tables, max_blocks_per_seq, num_seqs)
+    if device_status is not None:
+        _need(device_status, torch.int32, "device_status")
+    with _on(q, head_weights, index_cache, block_tables, q_pos, out, device_status):
+        s = _current(stream, q.device)
+        if out is None:
+            with torch.cuda.stream(s):
+                out = torch.empty((rows, n_pools), dtype=torch.float32, device=q.device)
+        _need(out, torch.float32, "out")
+        if out.numel() != rows * n_pools:
+            raise ValueError(f"out must hold [{rows}, {n_pools}]")
+        check(_lib.load().dsa_pool_scores(_ptr(q), _ptr(head_weights), _ptr(index_cache), _ptr(block_tables),
+                                          int(max_blocks_per_seq), _ptr(q_pos), int(num_seqs), int(rows_per_seq),
+                                          int(num_heads), int(block_size), int(page_stride_bytes), int(kpool),
+                                          int(n_pools), _ptr(out), _ptr(device_status), s.cuda_stream),
+              "dsa_pool_scores")
+    return out
+
+
+def full_workspace_bytes(num_seqs: int, rows_per_seq: int, num_q_heads: int) -> int:
+    return int(_lib.load().dsa_mla_decode_full_workspace_bytes(int(num_seqs), int(rows_per_seq), int(num_q_heads)))
+
+
+def alloc_full_workspace(num_seqs: int, rows_per_seq: int, num_q_heads: int, device=None) -> torch.Tensor:
+    """A workspace for decode_full, to be kept from call to call (one per stream or captured graph)."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = full_workspace_bytes(num_seqs, rows_per_seq, num_q_heads)
+    if n == 0:
+        raise DsaError(2, "dsa_mla_decode_full_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_full(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, num_seqs, rows_per_seq, num_q_heads,
+                block_size, cache_stride_bytes, k_scale, v_scale, sm_scale, out=None, verify_rows=0, workspace=None,
+                stream=None) -> torch.Tensor:
+    """dsa_mla_decode_full: every row attends to its whole cache; seq_lens per row, or with
+    verify_rows per sequence before its rows. Returns out (bf16 [R, H, 512]). Without a
+    workspace one is allocated for the call."""
+    _need(q, torch.bfloat16, "q")
+    _need(k_cache, torch.uint8, "k_cache")
+    _need(v_cache, torch.uint8, "v_cache")
+    _need(block_tables, torch.int32, "block_tables")
+    _need(seq_lens, torch.int32, "seq_lens")
+    rows = num_seqs * rows_per_seq
+    if q.numel() != rows * num_q_heads * LATENT or seq_lens.numel() != (num_seqs if verify_rows else rows):
+        raise ValueError("q [R, num_q_heads, 512], seq_lens [R] ([num_seqs] for verify rows)")
+    _table_rows(block_tables, max_blocks_per_seq, num_seqs)
+    with _on(q, k_cache, v_cache, block_tables, seq_lens, out, workspace):
+        s = _current(stream, q.device)
+        with torch.cuda.stream(s):
+            out = torch.empty_like(q) if out is None else out
+            if workspace is None:
+                workspace = alloc_full_workspace(num_seqs, rows_per_seq, num_q_heads, q.device)
+        _need(out, torch.bfloat16, "out")
+        _need(workspace, torch.uint8, "workspace")
+        if out.numel() != q.numel():
+            raise ValueError("out [R, num_q_heads, 512]")
+        check(_lib.load().dsa_mla_decode_full(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), int(max_blocks_per_seq), _ptr(seq_lens),
+            int(num_seqs), int(rows_per_seq), int(num_q_heads), int(block_size), int(cache_stride_bytes),
+            float(k_scale), float(v_scale), float(sm_scale), _ptr(out), int(verify_rows), _ptr(workspace),
+            workspace.numel(), s.cuda_stream), "dsa_mla_decode_full")
     return out
 
 

@@ -100,6 +100,8 @@ int32_t current_device(DeviceState** out) {
             if (d.status == DSA_OK) d.status = from_cuda(prologue_kernel_setup());
             if (d.status == DSA_OK) d.status = from_cuda(combine_kernel_setup());
             if (d.status == DSA_OK) d.status = from_cuda(select_kernel_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(plan_kernel_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(pool_scores_kernel_setup());
         }
         d.checked = true;
     }
@@ -618,6 +620,157 @@ int32_t dsa_select_pools(const float* scores, const int32_t* q_pos, int32_t rows
     p.kpool = kpool;
     p.topk = topk;
     return from_cuda(launch_select(p, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dsa_plan_step(const int32_t* base_lens, const int32_t* new_lens, int32_t num_seqs, int32_t rows_per_seq,
+                      int32_t max_rows, const int32_t* free_pages, int32_t num_free, int32_t block_size,
+                      int32_t* block_tables, int32_t max_blocks_per_seq, int64_t* slots, int32_t* positions,
+                      int32_t* row_lens, int32_t* row_seqs, int32_t* info, void* stream) {
+    if (num_seqs < 0 || rows_per_seq < 0 || max_rows < 0 || num_free < 0 || block_size < 1 || max_blocks_per_seq < 1 || !info)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (num_seqs > 0 && (!base_lens || !new_lens || !block_tables)) return DSA_ERR_INVALID_ARGUMENT;
+    if (max_rows > 0 && (!slots || !positions || !row_lens || !row_seqs)) return DSA_ERR_INVALID_ARGUMENT;
+    if (num_free > 0 && !free_pages) return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(base_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) || !aligned(block_tables, 4) ||
+        !aligned(slots, 8) || !aligned(positions, 4) || !aligned(row_lens, 4) || !aligned(row_seqs, 4) || !aligned(info, 4))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (num_seqs > DSA_MAX_PLAN_SEQS || static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX)
+        return DSA_ERR_UNSUPPORTED;
+    if (rows_per_seq > 0 && static_cast<int64_t>(num_seqs) * rows_per_seq != max_rows) return DSA_ERR_INVALID_ARGUMENT;
+    DeviceState* d = nullptr;
+    int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    PlanParams p{};
+    p.base_lens = base_lens;
+    p.new_lens = new_lens;
+    p.free_pages = free_pages;
+    p.tables = block_tables;
+    p.slots = reinterpret_cast<long long*>(slots);
+    p.positions = positions;
+    p.row_lens = row_lens;
+    p.row_seqs = row_seqs;
+    p.info = info;
+    p.num_seqs = num_seqs;
+    p.rows_per_seq = rows_per_seq;
+    p.rows = max_rows;
+    p.num_free = num_free;
+    p.block_size = block_size;
+    p.max_blocks = max_blocks_per_seq;
+    return from_cuda(launch_plan(p, d->sms, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* norm_bias, const int64_t* slots,
+                        int32_t rows, float eps, int32_t block_size, int64_t page_stride_bytes, void* index_cache,
+                        void* stream) {
+    if (!index_cache || rows < 0 || block_size < 1 || (norm_bias && !norm_weight)) return DSA_ERR_INVALID_ARGUMENT;
+    if (rows > 0 && (!keys || !slots)) return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(keys, 16) || !aligned(norm_weight, 16) || !aligned(norm_bias, 16) || !aligned(slots, 8) ||
+        !aligned(index_cache, 16))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (page_stride_bytes < static_cast<int64_t>(block_size) * (kIndexDim + 4) || page_stride_bytes % 16 != 0)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return DSA_ERR_INVALID_ARGUMENT;
+    if (rows == 0) return DSA_OK;
+    DeviceState* d = nullptr;
+    int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    IndexWriteParams p{};
+    p.x = static_cast<const uint16_t*>(keys);
+    p.weight = static_cast<const uint16_t*>(norm_weight);
+    p.bias = static_cast<const uint16_t*>(norm_bias);
+    p.slots = reinterpret_cast<const long long*>(slots);
+    p.cache = static_cast<uint8_t*>(index_cache);
+    p.page_stride = page_stride_bytes;
+    p.rows = rows;
+    p.block_size = block_size;
+    p.eps = eps;
+    return from_cuda(launch_index_write(p, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* index_cache, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* q_pos, int32_t num_seqs, int32_t rows_per_seq,
+                        int32_t num_heads, int32_t block_size, int64_t page_stride_bytes, int32_t kpool, int32_t n_pools,
+                        float* scores, int32_t* device_status, void* stream) {
+    if (!q || !head_weights || !index_cache || !block_tables || !q_pos || (n_pools > 0 && !scores))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (num_seqs < 1 || rows_per_seq < 1 || num_heads < 1 || block_size < 1 || kpool < 1 || n_pools < 0 ||
+        max_blocks_per_seq < 0)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (page_stride_bytes < static_cast<int64_t>(block_size) * (kIndexDim + 4) || page_stride_bytes % 16 != 0)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(head_weights, 4) || !aligned(index_cache, 16) || !aligned(block_tables, 4) ||
+        !aligned(q_pos, 4) || !aligned(scores, 4) || !aligned(device_status, 4))
+        return DSA_ERR_INVALID_ARGUMENT;
+    const int64_t rows = static_cast<int64_t>(num_seqs) * rows_per_seq;
+    if (num_heads > DSA_MAX_INDEX_HEADS || kpool > DSA_MAX_KPOOL || static_cast<int64_t>(n_pools) * kpool > INT32_MAX ||
+        rows > INT32_MAX / num_heads)
+        return DSA_ERR_UNSUPPORTED;
+    if (n_pools == 0) return DSA_OK;
+    DeviceState* d = nullptr;
+    int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    PoolScoresParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.w = head_weights;
+    p.cache = static_cast<const uint8_t*>(index_cache);
+    p.block_tables = block_tables;
+    p.q_pos = q_pos;
+    p.scores = scores;
+    p.status = device_status;
+    p.page_stride = page_stride_bytes;
+    p.num_seqs = num_seqs;
+    p.rows_per_seq = rows_per_seq;
+    p.heads = num_heads;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.kpool = kpool;
+    p.n_pools = n_pools;
+    return from_cuda(launch_pool_scores(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t dsa_mla_decode_full_workspace_bytes(int32_t num_seqs, int32_t rows_per_seq, int32_t num_q_heads) {
+    if (num_seqs < 1 || rows_per_seq < 1 || num_q_heads < 1) return 0;
+    if (static_cast<int64_t>(num_seqs) * rows_per_seq > kMaxFullRowHeads / num_q_heads) return 0;
+    return 256;
+}
+
+int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs, int32_t rows_per_seq,
+                            int32_t num_q_heads, int32_t block_size, int64_t cache_stride_bytes, float k_scale,
+                            float v_scale, float sm_scale, void* out, int32_t verify_rows, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !out || !workspace) return DSA_ERR_INVALID_ARGUMENT;
+    if (num_seqs < 1 || rows_per_seq < 1 || num_q_heads < 1 || block_size < 1 || max_blocks_per_seq < 0)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (cache_stride_bytes < static_cast<int64_t>(block_size) * kLatent || cache_stride_bytes % 16 != 0)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (verify_rows != 0 && verify_rows != 1) return DSA_ERR_INVALID_ARGUMENT;
+    if (static_cast<int64_t>(num_seqs) * rows_per_seq > kMaxFullRowHeads / num_q_heads) return DSA_ERR_UNSUPPORTED;
+    DeviceState* d = nullptr;
+    int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    if (workspace_bytes < dsa_mla_decode_full_workspace_bytes(num_seqs, rows_per_seq, num_q_heads)) return DSA_ERR_WORKSPACE;
+    FullParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.out = static_cast<uint16_t*>(out);
+    p.status = static_cast<int*>(workspace);
+    p.cache_stride = cache_stride_bytes;
+    p.num_seqs = num_seqs;
+    p.rows_per_seq = rows_per_seq;
+    p.heads = num_q_heads;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.verify_rows = verify_rows;
+    p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
+    p.v_scale = v_scale;
+    return from_cuda(launch_full(p, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t dsa_read_device_status(const void* workspace, int32_t* status_out, void* stream) {

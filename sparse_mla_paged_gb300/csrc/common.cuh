@@ -13,6 +13,7 @@
 namespace dsa {
 
 constexpr int kLatent = 512;           // kv_lora_rank: the whole cache token (NoPE)
+constexpr int kIndexDim = DSA_INDEX_DIM;  // width of an index key
 constexpr int kCtaMinSlots = 128;      // default grid: at least this many slots per CTA
 // From this many slots per decode CTA on, the decode and combine kernels let the next
 // kernel on the stream launch early (measured: a gain on long decodes, a loss on short).
@@ -23,6 +24,7 @@ constexpr int kHeadsPerCta = 64;       // query heads per work unit
 constexpr int kQImageBytes = 2 * kHeadsPerCta * kLatent;  // 64 KB
 constexpr int kBitmapWords = 8192;     // resolve bitmap: seq_len up to 262144 tokens
 constexpr int kResolveThreads = 256;
+constexpr int64_t kMaxFullRowHeads = 1 << 22;  // dsa_mla_decode_full: rows * heads of a call
 
 // Probabilities are carried as P' = 2^(x - m + kPBias) (x, m in log2 units) split into two
 // E4M3 terms. A head's reference m is reset to its tile max plus kRescaleSlack when the
@@ -211,6 +213,56 @@ struct SelectParams {
     int32_t rows, n_pools, kpool, topk;
 };
 
+struct PlanParams {
+    const int32_t* base_lens;  // [num_seqs] cached tokens
+    const int32_t* new_lens;   // [num_seqs] new tokens
+    const int32_t* free_pages; // [num_free]
+    int32_t* tables;           // [num_seqs, max_blocks]
+    long long* slots;          // [rows]
+    int32_t* positions;        // [rows]
+    int32_t* row_lens;         // [rows]
+    int32_t* row_seqs;         // [rows]
+    int32_t* info;             // rows with a token, pages taken, status, 0
+    int32_t num_seqs, rows_per_seq, rows, num_free, block_size, max_blocks;
+};
+
+struct IndexWriteParams {
+    const uint16_t* x;         // bf16 bits [rows, 128]
+    const uint16_t* weight;    // bf16 bits [128], or null: no norm
+    const uint16_t* bias;      // bf16 bits [128], or null
+    const long long* slots;    // [rows]; a negative slot writes nothing
+    uint8_t* cache;
+    int64_t page_stride;
+    int32_t rows, block_size;
+    float eps;
+};
+
+struct PoolScoresParams {
+    const uint16_t* q;         // bf16 bits [R, heads, 128]
+    const float* w;            // [R, heads]
+    const uint8_t* cache;
+    const int32_t* block_tables;
+    const int32_t* q_pos;      // [R]
+    float* scores;             // [R, n_pools]
+    int* status;               // or null
+    int64_t page_stride;
+    int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, kpool, n_pools;
+};
+
+struct FullParams {
+    const uint16_t* q;         // bf16 bits [R, heads, 512]
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;   // [R], or [num_seqs] before the verify rows
+    uint16_t* out;             // bf16 bits [R, heads, 512]
+    int* status;
+    int64_t cache_stride;
+    int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, verify_rows;
+    float score_scale;         // sm_scale * k_scale * log2(e)
+    float v_scale;
+};
+
 // Launchers (each defined next to its kernel).
 // The decode and combine kernels are launched as programmatic dependents of the kernel
 // before them on the stream (they start their set-up early and wait on the grid
@@ -232,6 +284,12 @@ cudaError_t launch_combine(const CombineParams& p, int units, int max_pieces, cu
 cudaError_t launch_latent_write(const LatentWriteParams& p, cudaStream_t stream);
 int32_t check_device();  // DSA_OK when the current device is an sm_103 with the kernels loaded
 cudaError_t select_kernel_setup();
+cudaError_t plan_kernel_setup();
+cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_index_write(const IndexWriteParams& p, cudaStream_t stream);
+cudaError_t pool_scores_kernel_setup();
+cudaError_t launch_pool_scores(const PoolScoresParams& p, cudaStream_t stream);
+cudaError_t launch_full(const FullParams& p, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t decode_kernel_setup_64();
 cudaError_t decode_kernel_setup_128();

@@ -1,0 +1,179 @@
+// The step plan: from every request's cached and new token counts, the physical pages of the
+// new tokens (written into the block tables) and each new token's cache slot, position,
+// visible length and request, as the cache writers, the selector and the decode take them
+// (decode_k.rs, decode_k: slot = physical*block_size + pos % block_size).
+//
+//   have(s) = ceil(base(s)/bs), want(s) = ceil((base(s)+new(s))/bs), both at most the table's width
+//   table[s][have(s)+i] = free[g0(s)+i] (or -1 past the free list), g0 = exclusive sum of want - have
+//   row of token i of s: pos = base(s)+i, slot = table[s][pos/bs]*bs + pos%bs, len = pos+1
+//
+// One launch. Both prefix sums (tokens, pages) over the requests are made by every block for
+// itself in shared memory: 8 bytes a request, served by L2 after the first block, cost less
+// than a second launch. Rows and new table entries are then spread over all blocks. A packed
+// row finds its request by a binary search of the token prefix sums in shared memory. A new
+// page's id is read from the free list, not from the table entry that another block writes,
+// so no block waits for another. Block 0 alone reports what it finds wrong.
+#include <climits>
+
+#include "common.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+__device__ __forceinline__ int32_t saturate(int64_t x) { return x > INT_MAX ? INT_MAX : static_cast<int32_t>(x); }
+
+// Token counts of a request as the plan uses them; `bad` when they had to be cut.
+struct Request {
+    int64_t base, fresh;   // cached and new tokens
+    int32_t have, want;    // pages before and after, at most the table's width
+    bool bad;
+};
+__device__ __forceinline__ Request request(const PlanParams& p, int32_t s) {
+    Request r;
+    const int32_t b = p.base_lens[s], n = p.new_lens[s];
+    r.base = b < 0 ? 0 : b;
+    r.fresh = n < 0 ? 0 : n;
+    r.bad = b < 0 || n < 0;
+    if (p.rows_per_seq > 0 && r.fresh > p.rows_per_seq) {
+        r.fresh = p.rows_per_seq;
+        r.bad = true;
+    }
+    const int64_t have = (r.base + p.block_size - 1) / p.block_size;
+    const int64_t want = (r.base + r.fresh + p.block_size - 1) / p.block_size;
+    r.bad |= want > p.max_blocks;
+    r.have = static_cast<int32_t>(have < p.max_blocks ? have : p.max_blocks);
+    r.want = static_cast<int32_t>(want < p.max_blocks ? want : p.max_blocks);
+    return r;
+}
+
+// Index of the last entry of the ascending array a[0..n] that is <= x (a[0] = 0 <= x < a[n]).
+__device__ __forceinline__ int32_t last_at_most(const int32_t* a, int32_t n, int32_t x) {
+    int32_t lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int32_t mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+    extern __shared__ int32_t prefix[];  // tokens t0[0..n], then pages g0[0..n]
+    __shared__ int64_t warp_tokens[kPlanWarps], warp_pages[kPlanWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t n = p.num_seqs;
+    int32_t* t0 = prefix;
+    int32_t* g0 = prefix + n + 1;
+
+    // Thread t sums requests [t*per, (t+1)*per), a block scan gives its start, and a second
+    // sweep writes the prefix sums (saturated: rows and pages past 2^31 - 1 do not exist).
+    const int32_t per = (n + kPlanThreads - 1) / kPlanThreads;
+    const int32_t lo = min(n, tid * per), hi = min(n, lo + per);
+    int64_t tokens = 0, pages = 0;
+    for (int32_t s = lo; s < hi; ++s) {
+        const Request r = request(p, s);
+        tokens += r.fresh;
+        pages += r.want - r.have;
+    }
+    int64_t it = tokens, ip = pages;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, it, o), b = __shfl_up_sync(0xffffffffu, ip, o);
+        if (lane >= o) {
+            it += a;
+            ip += b;
+        }
+    }
+    if (lane == 31) {
+        warp_tokens[warp] = it;
+        warp_pages[warp] = ip;
+    }
+    __syncthreads();
+    int64_t ct = it - tokens, cp = ip - pages;
+    for (int w = 0; w < warp; ++w) {
+        ct += warp_tokens[w];
+        cp += warp_pages[w];
+    }
+    bool bad = false;
+    for (int32_t s = lo; s < hi; ++s) {
+        const Request r = request(p, s);
+        t0[s] = saturate(ct);
+        g0[s] = saturate(cp);
+        ct += r.fresh;
+        cp += r.want - r.have;
+        bad |= r.bad;
+        // The page that the first new token shares with cached ones has to be there already.
+        if (blockIdx.x == 0 && r.fresh > 0 && r.base % p.block_size != 0 && r.base / p.block_size < p.max_blocks)
+            bad |= p.tables[static_cast<int64_t>(s) * p.max_blocks + r.base / p.block_size] < 0;
+    }
+    if (hi == n && (lo < n || (n == 0 && tid == 0))) {  // the last thread with a request; no request: thread 0
+        t0[n] = saturate(ct);
+        g0[n] = saturate(cp);
+    }
+    bad = __syncthreads_or(bad);
+    const int32_t all_tokens = t0[n], all_pages = g0[n];
+    if (blockIdx.x == 0 && tid == 0) {
+        bad |= all_pages > p.num_free || (p.rows_per_seq == 0 && all_tokens > p.rows);
+        p.info[0] = p.rows_per_seq == 0 ? min(all_tokens, p.rows) : all_tokens;
+        p.info[1] = min(all_pages, p.num_free);
+        p.info[2] = bad ? DSA_ERR_DEVICE_BOUNDS : DSA_OK;
+        p.info[3] = 0;
+    }
+
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
+    for (int64_t e = first; e < all_pages; e += step) {
+        const int32_t s = last_at_most(g0, n, static_cast<int32_t>(e));
+        const int64_t have = request(p, s).have;
+        p.tables[static_cast<int64_t>(s) * p.max_blocks + have + (e - g0[s])] = e < p.num_free ? p.free_pages[e] : -1;
+    }
+    for (int64_t row = first; row < p.rows; row += step) {
+        int32_t s = -1;
+        int64_t i = 0;
+        if (p.rows_per_seq > 0) {
+            s = static_cast<int32_t>(row / p.rows_per_seq);
+            i = row % p.rows_per_seq;
+        } else if (row < all_tokens) {
+            s = last_at_most(t0, n, static_cast<int32_t>(row));
+            i = row - t0[s];
+        }
+        int64_t slot = -1, pos = -1;
+        if (s >= 0) {
+            const Request r = request(p, s);
+            pos = r.base + i;
+            const int64_t blk = pos / p.block_size;
+            if (i >= r.fresh || blk >= p.max_blocks) {
+                s = -1;
+                pos = -1;
+            } else {
+                const int64_t g = g0[s] + blk - r.have;
+                const int32_t page = blk < r.have ? p.tables[static_cast<int64_t>(s) * p.max_blocks + blk]
+                                                  : (g < p.num_free ? p.free_pages[g] : -1);
+                if (page >= 0) slot = static_cast<int64_t>(page) * p.block_size + pos % p.block_size;
+            }
+        }
+        p.slots[row] = slot;
+        p.positions[row] = static_cast<int32_t>(pos);
+        p.row_lens[row] = static_cast<int32_t>(pos + 1);
+        p.row_seqs[row] = s;
+    }
+}
+
+}  // namespace
+
+cudaError_t plan_kernel_setup() {
+    return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                2 * (DSA_MAX_PLAN_SEQS + 1) * 4);
+}
+
+cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream) {
+    // Four rows a thread before another block is worth its own prefix sums.
+    const int64_t want = (static_cast<int64_t>(p.rows) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+    const int blocks = static_cast<int>(want < 1 ? 1 : (want > 2 * sms ? 2 * sms : want));
+    plan_kernel<<<blocks, kPlanThreads, 2 * (p.num_seqs + 1) * 4, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace dsa
