@@ -405,8 +405,8 @@ int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* n
  *                positions), DSA_ERR_TIMEOUT if a pipeline wait ran out of time. The call
  *                never clears it.
  *  num_seqs, rows_per_seq >= 1; num_heads 1..DSA_MAX_INDEX_HEADS and kpool 1..DSA_MAX_KPOOL
- *  (DSA_ERR_UNSUPPORTED above); n_pools >= 0 (scores may be null at 0); n_pools*kpool and
- *  R*num_heads below 2^31 (DSA_ERR_UNSUPPORTED otherwise).
+ *  (DSA_ERR_UNSUPPORTED above); n_pools >= 0 (scores may be null at 0); n_pools*kpool at most
+ *  2^30 and R*num_heads below 2^31 (DSA_ERR_UNSUPPORTED otherwise).
  */
 int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* index_cache,
                         const int32_t* block_tables, int32_t max_blocks_per_seq,

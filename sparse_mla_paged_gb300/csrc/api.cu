@@ -702,7 +702,7 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
         !aligned(q_pos, 4) || !aligned(scores, 4) || !aligned(device_status, 4))
         return DSA_ERR_INVALID_ARGUMENT;
     const int64_t rows = static_cast<int64_t>(num_seqs) * rows_per_seq;
-    if (num_heads > DSA_MAX_INDEX_HEADS || kpool > DSA_MAX_KPOOL || static_cast<int64_t>(n_pools) * kpool > INT32_MAX ||
+    if (num_heads > DSA_MAX_INDEX_HEADS || kpool > DSA_MAX_KPOOL || static_cast<int64_t>(n_pools) * kpool > (1 << 30) ||
         rows > INT32_MAX / num_heads)
         return DSA_ERR_UNSUPPORTED;
     if (n_pools == 0) return DSA_OK;
@@ -725,7 +725,7 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.kpool = kpool;
     p.n_pools = n_pools;
-    return from_cuda(launch_pool_scores(p, static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_pool_scores(p, d->sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t dsa_mla_decode_full_workspace_bytes(int32_t num_seqs, int32_t rows_per_seq, int32_t num_q_heads) {

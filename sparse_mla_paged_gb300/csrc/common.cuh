@@ -288,7 +288,7 @@ cudaError_t plan_kernel_setup();
 cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_index_write(const IndexWriteParams& p, cudaStream_t stream);
 cudaError_t pool_scores_kernel_setup();
-cudaError_t launch_pool_scores(const PoolScoresParams& p, cudaStream_t stream);
+cudaError_t launch_pool_scores(const PoolScoresParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_full(const FullParams& p, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t decode_kernel_setup_64();
