@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "full.cuh"
 
 using namespace dsa;
 
@@ -102,6 +103,8 @@ int32_t current_device(DeviceState** out) {
             if (d.status == DSA_OK) d.status = from_cuda(select_kernel_setup());
             if (d.status == DSA_OK) d.status = from_cuda(plan_kernel_setup());
             if (d.status == DSA_OK) d.status = from_cuda(pool_scores_kernel_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(full_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(full_plan_setup());
         }
         d.checked = true;
     }
@@ -213,6 +216,22 @@ bool encode_cache_map(const void* base, size_t mem_bytes, CUtensorMap* m) {
     const cuuint32_t estride[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D map of a paged cache, [page][row of the page][512 bytes], pages enough to span the
+// device's memory, read as boxes of 128 bytes x `rows` rows of one page into the
+// 128-byte-swizzled operand layout; a page outside the map (a negative one) gives zeros.
+bool encode_page_map(const void* base, size_t mem_bytes, int32_t block_size, int64_t stride, int32_t rows, CUtensorMap* m) {
+    const auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t pages = std::min<cuuint64_t>(mem_bytes / static_cast<size_t>(stride) + 1, (1ull << 31) - 1);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(block_size), pages};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(stride)};
+    const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(rows), 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -728,10 +747,21 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     return from_cuda(launch_pool_scores(p, d->sms, static_cast<cudaStream_t>(stream)));
 }
 
-size_t dsa_mla_decode_full_workspace_bytes(int32_t num_seqs, int32_t rows_per_seq, int32_t num_q_heads) {
+namespace {
+// (row, head) groups of 64 of a full-cache decode, 0 when the shape is refused.
+int64_t full_units(int32_t num_seqs, int32_t rows_per_seq, int32_t num_q_heads) {
     if (num_seqs < 1 || rows_per_seq < 1 || num_q_heads < 1) return 0;
     if (static_cast<int64_t>(num_seqs) * rows_per_seq > kMaxFullRowHeads / num_q_heads) return 0;
-    return 256;
+    return static_cast<int64_t>(num_seqs) *
+           ((static_cast<int64_t>(rows_per_seq) * num_q_heads + kHeadsPerCta - 1) / kHeadsPerCta);
+}
+}  // namespace
+
+size_t dsa_mla_decode_full_workspace_bytes(int32_t num_seqs, int32_t rows_per_seq, int32_t num_q_heads) {
+    const int64_t units = full_units(num_seqs, rows_per_seq, num_q_heads);
+    DeviceState* d = nullptr;
+    if (units == 0 || current_device(&d) != DSA_OK) return 0;
+    return full::layout(units, d->sms).total;
 }
 
 int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -748,29 +778,63 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 256))
         return DSA_ERR_INVALID_ARGUMENT;
     if (verify_rows != 0 && verify_rows != 1) return DSA_ERR_INVALID_ARGUMENT;
-    if (static_cast<int64_t>(num_seqs) * rows_per_seq > kMaxFullRowHeads / num_q_heads) return DSA_ERR_UNSUPPORTED;
+    const int64_t units = full_units(num_seqs, rows_per_seq, num_q_heads);
+    if (units == 0) return DSA_ERR_UNSUPPORTED;
     DeviceState* d = nullptr;
     int32_t st = current_device(&d);
     if (st != DSA_OK) return st;
-    if (workspace_bytes < dsa_mla_decode_full_workspace_bytes(num_seqs, rows_per_seq, num_q_heads)) return DSA_ERR_WORKSPACE;
-    FullParams p{};
+    const full::Layout L = full::layout(units, d->sms);
+    if (workspace_bytes < L.total) return DSA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    full::Params p{};
     p.q = static_cast<const uint16_t*>(q);
     p.k_cache = static_cast<const uint8_t*>(k_cache);
     p.v_cache = static_cast<const uint8_t*>(v_cache);
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
     p.out = static_cast<uint16_t*>(out);
-    p.status = static_cast<int*>(workspace);
+    p.status = reinterpret_cast<int*>(ws + L.status);
+    p.plan.head = reinterpret_cast<full::PlanHead*>(ws + L.head);
+    p.plan.start = reinterpret_cast<int64_t*>(ws + L.start);
+    p.plan.unit = reinterpret_cast<int32_t*>(ws + L.unit);
+    p.plan.max_len = reinterpret_cast<int32_t*>(ws + L.max_len);
+    p.plan.min_len = reinterpret_cast<int32_t*>(ws + L.min_len);
+    p.plan.unit_k = reinterpret_cast<int32_t*>(ws + L.unit_k);
+    p.plan.cta_k = reinterpret_cast<int32_t*>(ws + L.cta_k);
+    p.qimg = ws + L.qimg;
+    p.qscale = reinterpret_cast<float*>(ws + L.qscale);
+    p.part_o = reinterpret_cast<uint16_t*>(ws + L.part_o);
+    p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
     p.cache_stride = cache_stride_bytes;
     p.num_seqs = num_seqs;
     p.rows_per_seq = rows_per_seq;
     p.heads = num_q_heads;
+    p.pairs = rows_per_seq * num_q_heads;
+    p.groups = static_cast<int32_t>(units / num_seqs);
+    p.units = static_cast<int32_t>(units);
+    p.max_ctas = d->sms;
     p.block_size = block_size;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.verify_rows = verify_rows;
+    p.kv_same = k_cache == v_cache ? 1 : 0;
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;
-    return from_cuda(launch_full(p, static_cast<cudaStream_t>(stream)));
+    // Tensor-map boxes hold rows of one page and fill tiles evenly: a page of 16, 32, 64 or 128
+    // tokens, or of a multiple of 128. Other page sizes take per-thread copies.
+    if (block_size >= 16 && full::kTile % block_size == 0) p.box_rows = block_size;
+    else if (block_size % full::kTile == 0) p.box_rows = full::kTile;
+    CUtensorMap kmap, vmap;
+    std::memset(&kmap, 0, sizeof kmap);
+    std::memset(&vmap, 0, sizeof vmap);
+    if (p.box_rows > 0 &&
+        !(encode_page_map(k_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &kmap) &&
+          (p.kv_same || encode_page_map(v_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &vmap))))
+        p.box_rows = 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = from_cuda(launch_full_plan(p, s));
+    if (st == DSA_OK) st = from_cuda(launch_full(p, kmap, vmap, s));
+    if (st == DSA_OK) st = from_cuda(launch_full_combine(p, s));
+    return st;
 }
 
 int32_t dsa_read_device_status(const void* workspace, int32_t* status_out, void* stream) {

@@ -249,20 +249,6 @@ struct PoolScoresParams {
     int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, kpool, n_pools;
 };
 
-struct FullParams {
-    const uint16_t* q;         // bf16 bits [R, heads, 512]
-    const uint8_t* k_cache;
-    const uint8_t* v_cache;
-    const int32_t* block_tables;
-    const int32_t* seq_lens;   // [R], or [num_seqs] before the verify rows
-    uint16_t* out;             // bf16 bits [R, heads, 512]
-    int* status;
-    int64_t cache_stride;
-    int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, verify_rows;
-    float score_scale;         // sm_scale * k_scale * log2(e)
-    float v_scale;
-};
-
 // Launchers (each defined next to its kernel).
 // The decode and combine kernels are launched as programmatic dependents of the kernel
 // before them on the stream (they start their set-up early and wait on the grid
@@ -289,7 +275,6 @@ cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_index_write(const IndexWriteParams& p, cudaStream_t stream);
 cudaError_t pool_scores_kernel_setup();
 cudaError_t launch_pool_scores(const PoolScoresParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_full(const FullParams& p, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t decode_kernel_setup_64();
 cudaError_t decode_kernel_setup_128();

@@ -2,74 +2,750 @@
 //
 //   out[r,h,:] = sum_{j < len(r)} softmax_j(sm_scale * q[r,h,:] . (k_scale*K_j)) (v_scale*V_j)
 //
-// One warp per (row, head): lane l holds dims 16l .. 16l+15 of the query and of the running
-// weighted sum, and walks the row's tokens with a running maximum and sum.
+// One persistent CTA per SM over the line of 128-token tiles that the prologue planned (see
+// full.cuh). Arithmetic as in the selected decode: keys and values are the cached E4M3 codes
+// themselves, the operands of both products as they lie in the ring; a query is two E4M3
+// terms (M = 128 query rows: 64 (row, head) pairs x {hi, lo}, in tensor memory); S[128 x 128
+// tokens] goes to tensor memory, P' = 2^(x - m + kPBias) back to shared memory as two E4M3
+// terms; O^T[512 x 64 pairs] accumulates in tensor memory in FP32, rescaled only when a
+// pair's reference maximum m moves (kRescale* in common.cuh).
+//
+//   load     tiles into a ring of three, [4 blocks of 128 dims][128 tokens][128 bytes] with
+//            the 128-byte swizzle: one warp with tensor-map boxes of a page's rows when pages
+//            and tiles fit each other, else four warps with 16-byte copies
+//   MMA      one warp: Q.K^T of a tile and P.V of the tile before, whichever is ready
+//   softmax  eight warps, two per TMEM lane quarter; the same warps write the output
+//
+// A tile that holds tokens which some row of the unit does not see ("edge" tile: the last
+// ones, or those past a shorter row) is masked per pair, and its V bytes are made safe
+// before P.V reads them: a hidden token's zero weight would not silence a NaN code. Tokens
+// past every row are cleared, a partly visible token with a NaN code is cleared and its
+// score made NaN for the pairs that see it.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
-#include "common.cuh"
+#include "full.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
+namespace full {
 namespace {
 
-constexpr int kFullWarps = 4;
+constexpr int kTileBytes = kTile * kLatent;  // 64 KB
+constexpr int kBlockBytes = kTile * 128;     // one block of 128 dims
+constexpr int kRingTiles = 3;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
+constexpr int kHalfCols = kTile / 2;         // S columns per softmax warp
+constexpr int kScores = kHalfCols / 2;       // scores per softmax thread: 32, one bit each of a word
+constexpr int kPTermBytes = kHeadsPerCta * kTile;
 
-__device__ __forceinline__ void decode16(const uint4 v, float* f) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int b = 0; b < 16; ++b)
-        f[b] = __half2float(__half(__nv_cvt_fp8_to_halfraw((u[b >> 2] >> (8 * (b & 3))) & 255u, __NV_E4M3)));
+constexpr int kBarSoftmax = 1;
+constexpr int kBarPair0 = 2;  // 2..5: the two softmax warps of a lane quarter
+
+constexpr int kOffP = kRingTiles * kTileBytes;               // P' [2 buffers][hi, lo]; epilogue staging
+constexpr int kOffHm = kOffP + 4 * kPTermBytes;              // float [2 token halves][64] tile maxima
+constexpr int kOffAlpha = kOffHm + 2 * kHeadsPerCta * 4;     // float [2 tile parities][64] rescale factors
+constexpr int kOffL = kOffAlpha + 2 * kHeadsPerCta * 4;      // float [2 token halves][64] row sums
+constexpr int kOffF = kOffL + 2 * kHeadsPerCta * 4;          // float [64] output factors
+constexpr int kOffFlags = kOffF + kHeadsPerCta * 4;          // u32 [2 tile parities][4 lane quarters]
+constexpr int kOffBroken = kOffFlags + 2 * 4 * 4;            // 128 bits: an edge tile's tokens with a NaN code
+constexpr int kOffBars = kOffBroken + kTile / 8;
+enum {
+    BAR_FULL0 = 0,                        // ring slot loaded
+    BAR_EMPTY0 = BAR_FULL0 + kRingTiles,  // ring slot free: its P.V is done
+    BAR_SFULL = BAR_EMPTY0 + kRingTiles,  // S written
+    BAR_SEMPTY,                           // S read
+    BAR_PFULL0,                           // 2: P' buffer written
+    BAR_PVDONE0 = BAR_PFULL0 + 2,         // 2: the P.V reading it is done
+    BAR_QFULL = BAR_PVDONE0 + 2,
+    BAR_QEMPTY,
+    BAR_OEMPTY,
+    BAR_DRAIN,
+    BAR_DONE,
+    kNumBars
+};
+constexpr int kOffTmem = kOffBars + kNumBars * 8;
+constexpr int kOffAbort = kOffTmem + 4;
+constexpr int kSmem = kOffAbort + 4 + 1024;  // slack for the 1024-byte alignment
+static_assert(kSmem <= 227 * 1024, "shared memory");
+static_assert(kSoftmaxWarps * 2048 <= 4 * kPTermBytes, "epilogue staging fits the P buffers");
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 0;    // O^T: dims 128c.. of all 64 pairs at column 64c
+constexpr uint32_t kTmemQ = 256;  // query operand
+constexpr uint32_t kTmemS = 384;
+
+constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Warps of the two variants (tensor-map boxes need one loading warp).
+template <bool kTma>
+struct Roles {
+    static constexpr int kLoadWarps = kTma ? 1 : 4;
+    static constexpr int kMmaWarp = kLoadWarps;
+    static constexpr int kSoftmax0 = kMmaWarp + 1;
+    static constexpr int kThreads = (kSoftmax0 + kSoftmaxWarps) * 32;
+};
+
+__device__ __forceinline__ void tma_box3(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
-__global__ void __launch_bounds__(kFullWarps * 32) full_kernel(const FullParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t rh = static_cast<int64_t>(blockIdx.x) * kFullWarps + (threadIdx.x >> 5);
-    if (rh >= static_cast<int64_t>(p.num_seqs) * p.rows_per_seq * p.heads) return;
-    const int64_t r = rh / p.heads, seq = r / p.rows_per_seq;
-    const int64_t given = p.verify_rows ? static_cast<int64_t>(p.seq_lens[seq]) + r % p.rows_per_seq + 1 : p.seq_lens[r];
-    const int64_t room = p.max_blocks_per_seq > 0 ? static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size : given;
-    const int64_t len = min(given, room);
-    bool bad = given > room;
-    float q[16], o[16] = {}, m = -__builtin_huge_valf(), l = 0.0f;
-    const uint16_t* qp = p.q + rh * kLatent + lane * 16;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __uint_as_float(static_cast<uint32_t>(qp[i]) << 16) * p.score_scale;
-    for (int64_t j = 0; j < len; ++j) {
-        const int32_t page = p.block_tables[seq * p.max_blocks_per_seq + j / p.block_size];
-        if (page < 0) {
-            bad = true;
-            continue;
-        }
-        const int64_t at = page * p.cache_stride + (j % p.block_size) * kLatent + lane * 16;
-        float k[16], x = 0.0f;
-        decode16(__ldg(reinterpret_cast<const uint4*>(p.k_cache + at)), k);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x = fmaf(q[i], k[i], x);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-        if (p.v_cache != p.k_cache) decode16(__ldg(reinterpret_cast<const uint4*>(p.v_cache + at)), k);
-        const float top = fmaxf(m, x), a = exp2f(m - top), e = exp2f(x - top);
-        m = top;
-        l = l * a + e;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fmaf(e, k[i], o[i] * a);
+// What every role of a CTA has in hand.
+struct Cta {
+    const Params& p;
+    uint8_t* smem;
+    uint32_t sbase, tmem;
+    volatile int* abort_flag;
+    int64_t begin, end;  // tiles of the line
+    int32_t first_k;
+
+    __device__ uint32_t bar(int i) const { return sbase + kOffBars + 8 * i; }
+    __device__ void fail(int code) const {
+        atomicCAS(p.status, 0, code);
+        *abort_flag = 1;
     }
-    const float f = l > 0.0f ? p.v_scale / l : 0.0f;
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + rh * kLatent + lane * 16;
+    __device__ void wait(int b, uint32_t parity) const {
+        if (!mbar_wait(bar(b), parity, abort_flag, kWaitNs)) fail(kStatusTimeout);
+        __syncwarp();
+    }
+    __device__ Segment seg(int32_t k) const { return segment(p, begin, end, blockIdx.x, first_k, k); }
+};
+
+// Page of the block that holds position pos, or -1 (reported).
+__device__ __forceinline__ int32_t page_of(const Params& p, int32_t seq, int32_t pos, int32_t* row) {
+    const int32_t blk = pos / p.block_size;
+    *row = pos - blk * p.block_size;
+    const int32_t page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
+    return page;
+}
+
+// ------------------------------------------------------------------------------------
+// load: tensor-map boxes (warp 0; lane = 4*box + block of 128 dims)
+// ------------------------------------------------------------------------------------
+__device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtensorMap* vmap) {
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31, box = lane >> 2, kb = lane & 3;
+    const bool mine = box * p.box_rows < kTile;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
+    const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
+    const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
+    uint32_t tau = 0;
+    bool stop = false;
+    for (int32_t k = c.first_k; !stop; ++k) {
+        const Segment s = c.seg(k);
+        const int32_t seq = s.unit / p.groups;
+        // This lane's page of tile t (requested a tile ahead), its first row there, and
+        // whether any row of the unit sees the box.
+        auto look = [&](int32_t t, int32_t* row, bool* live) {
+            const int32_t pos = t * kTile + box * p.box_rows;
+            *live = mine && t < s.t1 && pos < s.max_len;
+            return *live ? page_of(p, seq, pos, row) : -1;
+        };
+        int32_t row = 0, row_next = 0;
+        bool live, live_next;
+        int32_t page_next = look(s.t0, &row_next, &live_next);
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int32_t page = page_next;
+            row = row_next;
+            live = live_next;
+            page_next = look(t + 1, &row_next, &live_next);
+            if (live && page < 0) atomicCAS(p.status, 0, kStatusBounds);
+            const int e = static_cast<int>(tau % slots);
+            if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e, (tau / slots - 1) & 1);
+            // After a failed wait nothing more is issued (the drain below finds what is in flight).
+            if (__shfl_sync(0xffffffffu, *c.abort_flag, 0)) {
+                stop = true;
+                break;
+            }
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, live)) * (p.kv_same ? 1 : 2);
+            if (lane == 0) mbar_arrive_expect_tx(c.bar(BAR_FULL0 + e), boxes * box_bytes);
+            __syncwarp();
+            if (live) {  // a negative page lies outside the map: zeros
+                const uint32_t dst = c.sbase + e * slot_bytes + kb * kBlockBytes + box * box_bytes;
+                tma_box3(dst, kmap, kb * 128, row, page, c.bar(BAR_FULL0 + e));
+                if (!p.kv_same) tma_box3(dst + kTileBytes, vmap, kb * 128, row, page, c.bar(BAR_FULL0 + e));
+            }
+            __syncwarp();
+        }
+        if (s.last) break;
+    }
+    // No copy into shared memory is in flight when the CTA exits: the last tiles' bytes.
+    if (lane == 0) {
+        for (uint32_t i = tau > static_cast<uint32_t>(slots) ? tau - slots : 0; i < tau; ++i) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(c.bar(BAR_FULL0 + static_cast<int>(i % slots)), (i / slots) & 1) &&
+                   globaltimer_ns() - t0 < kDrainLimitNs) {
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------------------------
+// load: 16-byte copies (warps 0-3, 32 tokens of a tile each; lane l resolves token l's page)
+// ------------------------------------------------------------------------------------
+__device__ void run_load_copies(const Cta& c) {
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
+    const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
+    uint32_t tau = 0;
+    for (int32_t k = c.first_k;; ++k) {
+        const Segment s = c.seg(k);
+        const int32_t seq = s.unit / p.groups;
+        auto look = [&](int32_t t) -> int64_t {
+            const int32_t pos = t * kTile + 32 * w + lane;
+            if (t >= s.t1 || pos >= s.max_len) return -1;
+            int32_t row;
+            const int32_t page = page_of(p, seq, pos, &row);
+            if (page < 0) atomicCAS(p.status, 0, kStatusBounds);
+            return page < 0 ? -1 : page * p.cache_stride + static_cast<int64_t>(row) * kLatent;
+        };
+        int64_t next = look(s.t0);
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int64_t mine = next;
+            next = look(t + 1);
+            const int e = static_cast<int>(tau % slots);
+            if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e, (tau / slots - 1) & 1);
+            const uint32_t dst = c.sbase + e * slot_bytes + (lane >> 3) * kBlockBytes + 32 * w * 128;
+#pragma unroll 8
+            for (int j = 0; j < 32; ++j) {
+                const int64_t at = __shfl_sync(0xffffffffu, mine, j);
+                const uint32_t d = dst + j * 128 + (((lane & 7) ^ (j & 7)) << 4);
+                const uint64_t src = at >= 0 ? static_cast<uint64_t>(at) + lane * 16 : 0;
+                cp_async_16_zfill(d, p.k_cache + src, at >= 0 ? 16u : 0u);
+                if (!p.kv_same) cp_async_16_zfill(d + kTileBytes, p.v_cache + src, at >= 0 ? 16u : 0u);
+            }
+            cp_async_arrive_noinc(c.bar(BAR_FULL0 + e));
+        }
+        if (s.last) break;
+    }
+    cp_async_wait_all();
+}
+
+// ------------------------------------------------------------------------------------
+// MMA warp: runs converged, one elected lane issues
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) != 0);
+}
+
+__device__ void run_mma(const Cta& c) {
+    const Params& p = c.p;
+    const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
+    const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
+    const uint32_t idq = idesc_e4m3(128, kTile, false, false);
+    const uint32_t idp = idesc_e4m3(128, kHeadsPerCta, true, false);
+    const uint32_t el = elect_one();
+    int units = 0;  // entered so far
+
+    const uint64_t pdesc0 = smem_desc(c.sbase + kOffP, 1024, 128, kSwizzleNone);
+    auto issue_pv = [&](uint32_t tp, bool first) {
+        const int pb = tp & 1, e = static_cast<int>(tp % slots);
+        c.wait(BAR_PFULL0 + pb, (tp >> 1) & 1);
+        if (first && units > 0) c.wait(BAR_OEMPTY, (units - 1) & 1);
+        tc_fence_after();
+        // V^T: 128 dims of block mc x 32 tokens (four 8-token swizzle groups of 1 KB), MN-major.
+        // P'^T: 64 pairs x 32 tokens, K-major core matrices.
+        const uint64_t vdesc = smem_desc(c.sbase + e * slot_bytes + (p.kv_same ? 0u : kTileBytes), kBlockBytes, 1024, kSwizzle128B);
+        const uint64_t pdesc = pdesc0 + static_cast<uint64_t>((pb * 2 * kPTermBytes) >> 4);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) out[i] = __float2bfloat16_rn(o[i] * f);
-    if (bad && lane == 0) atomicCAS(p.status, 0, kStatusBounds);
+        for (int mc = 0; mc < 4; ++mc) {
+#pragma unroll
+            for (int ks = 0; ks < kTile / 32; ++ks) {
+                const uint64_t a = vdesc + static_cast<uint64_t>((mc * kBlockBytes + ks * 4096) >> 4);
+                const uint64_t bh = pdesc + static_cast<uint64_t>((ks * 2048) >> 4);
+                const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + ks * 2048) >> 4);
+                const uint32_t d = c.tmem + kTmemO + mc * 64;
+                if (ks == 0) mma_e4m3_el(d, a, bh, idp, first ? 0u : 1u, el);
+                else mma_e4m3_acc_el(d, a, bh, idp, el);
+                mma_e4m3_acc_el(d, a, bl, idp, el);
+            }
+        }
+        tc_commit_el(c.bar(BAR_PVDONE0 + pb), el);
+        tc_commit_el(c.bar(BAR_EMPTY0 + e), el);
+    };
+    auto issue_qk = [&](uint32_t tq) {
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint64_t kdesc = smem_desc(c.sbase + static_cast<uint32_t>(tq % slots) * slot_bytes, 16, 1024, kSwizzle128B);
+        const uint32_t d = c.tmem + kTmemS;
+        mma_e4m3_ta_el(d, c.tmem + kTmemQ, kdesc, idq, 0u, el);
+#pragma unroll
+        for (int ks = 1; ks < 16; ++ks)
+            mma_e4m3_ta_acc_el(d, c.tmem + kTmemQ + ks * 8,
+                               kdesc + static_cast<uint64_t>(((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), idq, el);
+        tc_commit_el(c.bar(BAR_SFULL), el);
+    };
+    auto qk_ready = [&](uint32_t tq) {
+        return warp_poll(c.bar(BAR_FULL0 + static_cast<int>(tq % slots)), (tq / slots) & 1) &&
+               (tq == 0 || warp_poll(c.bar(BAR_SEMPTY), (tq - 1) & 1));
+    };
+
+    uint32_t tau = 0;
+    for (int32_t k = c.first_k;; ++k) {
+        const Segment s = c.seg(k);
+        c.wait(BAR_QFULL, units & 1);
+        tc_fence_after();
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            // Q.K of this tile and P.V of the one before are independent: whichever is ready.
+            bool qk = false, pv = t == s.t0;
+            const uint64_t t_start = globaltimer_ns();
+            while (!qk || !pv) {
+                if (!qk && qk_ready(tau)) {
+                    issue_qk(tau);
+                    if (t == s.t1 - 1) tc_commit_el(c.bar(BAR_QEMPTY), el);
+                    qk = true;
+                }
+                if (!pv && warp_poll(c.bar(BAR_PFULL0 + ((tau - 1) & 1)), ((tau - 1) >> 1) & 1)) {
+                    issue_pv(tau - 1, t - 1 == s.t0);
+                    pv = true;
+                }
+                if (!qk || !pv) {
+                    if (__shfl_sync(0xffffffffu, (*c.abort_flag != 0) || globaltimer_ns() - t_start > kWaitNs, 0)) {
+                        c.fail(kStatusTimeout);
+                        break;
+                    }
+                    if (!pv) mbar_try_wait_hint(c.bar(BAR_PFULL0 + ((tau - 1) & 1)), ((tau - 1) >> 1) & 1, kPollHintNs);
+                    else mbar_try_wait_hint(c.bar(BAR_FULL0 + static_cast<int>(tau % slots)), (tau / slots) & 1, kPollHintNs);
+                }
+            }
+        }
+        issue_pv(tau - 1, s.t1 - s.t0 == 1);
+        ++units;
+        if (s.last) break;
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// softmax / output warps
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float x, float y) {
+    return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(x, y) << 16);
+}
+// x rounded to 4 significant bits (round half up on the magnitude), an E4M3 value in its
+// normal range; the remainder is at most half a unit in its last place.
+__device__ __forceinline__ float hi_part(float x) {
+    return __uint_as_float((__float_as_uint(x) + 0x00080000u) & 0xFFF00000u);
+}
+
+// Makes one token's V bytes of an edge tile safe; returns whether it held a NaN code. Lanes
+// l and l + 16 share a token, 256 bytes each.
+__device__ __forceinline__ bool clean_token(uint8_t* v_tile, int token, int part, bool hidden) {
+    uint4* at[16];
+    uint32_t nan = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        // blocks 2*part and 2*part + 1 of 128 dims, all eight 16-byte pieces of the token's row
+        at[i] = reinterpret_cast<uint4*>(v_tile + (2 * part + (i >> 3)) * kBlockBytes + token * 128 + (i & 7) * 16);
+        if (!hidden) {
+            const uint4 v = *at[i];
+            nan |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                   ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
+        }
+    }
+    const bool broken = ((nan | __shfl_xor_sync(0xffffffffu, nan, 16)) & 0x80808080u) != 0u;
+    if (hidden || broken)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *at[i] = make_uint4(0, 0, 0, 0);
+    return broken;
+}
+
+// A warp's 32 dims x 32 pairs block (dims on lanes) scaled and written to bf16 rows through
+// the warp's 2 KB staging area with 16-byte stores.
+__device__ __forceinline__ void store_block(__nv_bfloat16* rows, int h0, int hvalid, int dim0, const uint32_t* v, const float* f,
+                                            uint8_t* stage, int lane) {
+    __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(stage);  // [32 pairs][32 dims]
+#pragma unroll
+    for (int k = 0; k < 32; ++k) stg[k * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[k]) * f[k]);
+    __syncwarp();
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const int hk = pass * 8 + lane / 4, col = (lane % 4) * 8;
+        const uint4 val = *reinterpret_cast<const uint4*>(stg + hk * 32 + col);
+        if (h0 + hk < hvalid) *reinterpret_cast<uint4*>(rows + static_cast<int64_t>(h0 + hk) * kLatent + dim0 + col) = val;
+    }
+    __syncwarp();
+}
+
+template <bool kTma>
+__device__ void run_softmax(const Cta& c) {
+    const Params& p = c.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sw = warp - Roles<kTma>::kSoftmax0;  // 0..7
+    const int q4 = warp & 3;                       // TMEM lane quarter
+    const int half = sw >> 2;                      // token half of each tile
+    const int term = lane & 1;                     // 0: hi row, 1: lo row
+    const int hq = 16 * q4 + (lane >> 1);          // pair of this thread within the unit
+    float* hm_s = reinterpret_cast<float*>(c.smem + kOffHm);
+    float* alpha_s = reinterpret_cast<float*>(c.smem + kOffAlpha);
+    float* l_s = reinterpret_cast<float*>(c.smem + kOffL);
+    float* f_s = reinterpret_cast<float*>(c.smem + kOffF);
+    uint32_t* flag_s = reinterpret_cast<uint32_t*>(c.smem + kOffFlags);
+    uint16_t* broken_s = reinterpret_cast<uint16_t*>(c.smem + kOffBroken);
+    uint8_t* stage = c.smem + kOffP + sw * 2048;
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    // This thread's first 16-byte row in a P' term: K-major core matrices of 8 pairs x 16 tokens.
+    const uint32_t p_off = (((half * kHalfCols + term * kScores) / 16) * 8 + (hq >> 3)) * 128 + (hq & 7) * 16;
+    const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
+    const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
+    uint32_t tau = 0;
+    int units = 0;
+
+    auto load_q = [&](int32_t unit) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.qimg + static_cast<int64_t>(unit) * kQImageBytes + half * 16 * 2048 +
+                                                          (q4 * 32 + lane) * 16);
+        uint32_t a[2][32];
+#pragma unroll
+        for (int hc = 0; hc < 2; ++hc)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = src[(hc * 8 + i) * (2048 / 16)];
+                a[hc][4 * i] = v.x;
+                a[hc][4 * i + 1] = v.y;
+                a[hc][4 * i + 2] = v.z;
+                a[hc][4 * i + 3] = v.w;
+            }
+#pragma unroll
+        for (int hc = 0; hc < 2; ++hc) tmem_st_x32(c.tmem + lane_base + kTmemQ + half * 64 + hc * 32, a[hc]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(BAR_QFULL));
+    };
+    // Length that this thread's pair sees.
+    auto pair_len = [&](int32_t unit) -> int32_t {
+        const int32_t pair = (unit % p.groups) * kHeadsPerCta + hq;
+        bool over;
+        return pair < p.pairs ? row_len(p, unit / p.groups, pair / p.heads, &over) : 0;
+    };
+
+    Segment next = c.seg(c.first_k);
+    float c_next = p.qscale[static_cast<int64_t>(next.unit) * kHeadsPerCta + hq];
+    int32_t len_next = pair_len(next.unit);
+    bool q_loaded = false;  // the unit's query operand was loaded during the unit before
+    bool pv_seen = false;   // the P.V two tiles back was already waited for
+    for (;;) {
+        const Segment s = next;
+        const float qs = c_next;
+        const int32_t len = len_next;
+        if (!s.last) {
+            next = c.seg(s.k + 1);
+            c_next = p.qscale[static_cast<int64_t>(next.unit) * kHeadsPerCta + hq];
+            len_next = pair_len(next.unit);
+        }
+        if (!q_loaded) {
+            if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
+            load_q(s.unit);
+        }
+        q_loaded = false;
+        float m_ref = kNegInf;  // reference max of the pair (log2 units)
+        float m_top = kNegInf;  // highest reference so far
+        float l_part = 0.0f;    // this thread's share of the sum of P'
+
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            c.wait(BAR_SFULL, tau & 1);
+            tc_fence_after();
+            uint32_t v[kHalfCols];
+#pragma unroll
+            for (int i = 0; i < kHalfCols / 32; ++i)
+                tmem_ld_x32(c.tmem + lane_base + kTmemS + half * kHalfCols + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * i));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bar(BAR_SEMPTY));
+
+            // Scores of pair hq for tokens tok0 .. tok0+31 of the tile: this lane's term plus
+            // the neighbouring lane's other one.
+            const int tok0 = half * kHalfCols + term * kScores;
+            float x[kScores];
+#pragma unroll
+            for (int j = 0; j < kScores; ++j) {
+                const float send = __uint_as_float(term ? v[j] : v[kScores + j]);
+                const float mine = __uint_as_float(term ? v[kScores + j] : v[j]);
+                x[j] = (mine + __shfl_xor_sync(0xffffffffu, send, 1)) * qs;
+            }
+            if ((t + 1) * kTile > s.min_len) {  // an edge tile
+                uint8_t* v_tile = c.smem + static_cast<uint32_t>(tau % slots) * slot_bytes + (p.kv_same ? 0 : kTileBytes);
+                const int token = 16 * sw + (lane & 15);
+                const int32_t pos = t * kTile + token;
+                bool broken = false;
+                c.wait(BAR_FULL0 + static_cast<int>(tau % slots), (tau / slots) & 1);  // passed: the copied bytes
+                if (__any_sync(0xffffffffu, pos >= s.min_len))
+                    broken = clean_token(v_tile, token, lane >> 4, pos >= s.max_len) && pos < s.max_len;
+                const uint32_t bits = __ballot_sync(0xffffffffu, broken);
+                if (lane == 0) broken_s[sw] = static_cast<uint16_t>(bits);
+                named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
+                const int32_t lim = len - t * kTile;
+                const uint32_t nan = reinterpret_cast<const uint32_t*>(broken_s)[tok0 / kScores];
+#pragma unroll
+                for (int j = 0; j < kScores; ++j) {
+                    if (tok0 + j >= lim) x[j] = kNegInf;
+                    else if (nan >> j & 1u) x[j] = __uint_as_float(0x7FC00000u);
+                }
+            }
+            float hm4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+            for (int j = 0; j < kScores; ++j) hm4[j & 3] = fmaxf(hm4[j & 3], x[j]);
+            float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
+            hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1));
+            if (term == 0) hm_s[half * kHeadsPerCta + hq] = hmax;
+            named_bar_sync_id(kBarPair0 + q4, 64);
+            const float tm = fmaxf(hm_s[hq], hm_s[kHeadsPerCta + hq]);
+            // The reference moves when the tile's max exceeds it by more than the margin or
+            // lies far below it (never for a tile of which the pair sees nothing).
+            const bool change = tm > m_ref + kRescaleMargin ||
+                                (tm < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && tm != kNegInf);
+            float alpha = 1.0f;
+            if (change) {
+                const float m_new = fmaxf(tm + kRescaleSlack, m_top - kRescaleFloor);
+                alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
+                l_part *= alpha;
+                m_ref = m_new;
+                m_top = fmaxf(m_top, m_new);
+            }
+            const float* alpha_t = alpha_s + (tau & 1) * kHeadsPerCta;
+            if (term == 0 && half == 0) alpha_s[(tau & 1) * kHeadsPerCta + hq] = alpha;
+            const uint32_t changed = __ballot_sync(0xffffffffu, change);
+            if (half == 0 && lane == 0) flag_s[(tau & 1) * 4 + q4] = changed;
+            const bool any_change = named_bar_any<kBarSoftmax, kSoftmaxThreads>(change);
+            bool resc[2] = {false, false};
+            if (any_change && t > s.t0) {
+                const uint4 f = *reinterpret_cast<const uint4*>(flag_s + (tau & 1) * 4);
+                resc[0] = (f.x | f.y) != 0u;
+                resc[1] = (f.z | f.w) != 0u;
+            }
+
+            uint32_t hw[kScores / 4], lw[kScores / 4];
+            float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
+#pragma unroll
+            for (int g = 0; g < kScores / 4; ++g) {
+                float ph[4], pl[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float pp = ex2_approx(x[4 * g + e] + off);
+                    ls4[e] += pp;
+                    ph[e] = hi_part(pp);
+                    pl[e] = pp - ph[e];
+                }
+                hw[g] = pack_e4m3x4(ph[0], ph[1], ph[2], ph[3]);
+                lw[g] = pack_e4m3x4(pl[0], pl[1], pl[2], pl[3]);
+            }
+            l_part += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+            if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
+            pv_seen = false;
+            const uint32_t pb = c.sbase + kOffP + (tau & 1) * 2 * kPTermBytes;
+#pragma unroll
+            for (int i = 0; i < kScores / 16; ++i) {
+                st_shared_v4(pb + p_off + i * 1024, hw[4 * i], hw[4 * i + 1], hw[4 * i + 2], hw[4 * i + 3]);
+                st_shared_v4(pb + kPTermBytes + p_off + i * 1024, lw[4 * i], lw[4 * i + 1], lw[4 * i + 2], lw[4 * i + 3]);
+            }
+            fence_proxy_async_smem();
+            if (resc[0] || resc[1]) {
+                // After the P.V before this tile, and before this tile's (P-full below): the
+                // changed 32-pair blocks of this warp's two dim chunks.
+                c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
+                pv_seen = true;
+                tc_fence_after();
+#pragma unroll 1
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (!resc[hh]) continue;
+                    const uint32_t ta = c.tmem + lane_base + kTmemO + 2 * half * 64 + hh * 32;
+                    uint32_t o0[32], o1[32];
+                    tmem_ld_2x32(ta, ta + 64, o0, o1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float f = alpha_t[hh * 32 + i];
+                        o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
+                        o1[i] = __float_as_uint(__uint_as_float(o1[i]) * f);
+                    }
+                    tmem_st_x32(ta, o0);
+                    tmem_st_x32(ta + 64, o1);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bar(BAR_PFULL0 + (tau & 1)));
+        }
+
+        // The next unit's query operand goes in while this unit's last P.V runs.
+        if (!s.last) {
+            c.wait(BAR_QEMPTY, units & 1);
+            load_q(next.unit);
+            q_loaded = true;
+        }
+
+        // ---- output of the unit ----
+        c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
+        pv_seen = true;
+        tc_fence_after();
+        const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
+        if (term == 0) l_s[half * kHeadsPerCta + hq] = lpair;
+        named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
+        const bool whole = s.part < 0;
+        if (term == 0 && half == 0) {
+            const float l = l_s[hq] + l_s[kHeadsPerCta + hq];
+            f_s[hq] = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
+            if (!whole) p.part_lse[s.part * kHeadsPerCta + hq] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
+        }
+        named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
+        const int32_t seq = s.unit / p.groups, first = (s.unit % p.groups) * kHeadsPerCta;
+        const int hvalid = min(kHeadsPerCta, p.pairs - first);
+        const int64_t pair0 = static_cast<int64_t>(seq) * p.pairs + first;
+#pragma unroll 1
+        for (int mc2 = 0; mc2 < 2; ++mc2) {
+            const int mc = 2 * half + mc2;
+            const int dim0 = mc * 128 + q4 * 32;
+            uint32_t v64[64];
+            tmem_ld_x64(c.tmem + lane_base + kTmemO + mc * 64, v64);
+            if (whole) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    store_block(reinterpret_cast<__nv_bfloat16*>(p.out) + pair0 * kLatent, hh * 32, hvalid, dim0, v64 + hh * 32,
+                                f_s + hh * 32, stage, lane);
+            } else {
+                __half* part = reinterpret_cast<__half*>(p.part_o) + static_cast<int64_t>(s.part) * kHeadsPerCta * kLatent;
+#pragma unroll
+                for (int i = 0; i < kHeadsPerCta; i += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 hv = __floats2half2_rn(__uint_as_float(v64[i + 2 * e]) * f_s[i + 2 * e],
+                                                             __uint_as_float(v64[i + 2 * e + 1]) * f_s[i + 2 * e + 1]);
+                        h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                    }
+                    *reinterpret_cast<uint4*>(part + ((static_cast<int64_t>(dim0 / 32) * 8 + i / 8) * 32 + lane) * 8) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.bar(BAR_OEMPTY));
+        // The staging area is the P buffer; l_s and f_s are used again.
+        named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
+        ++units;
+        if (s.last) break;
+    }
+}
+
+template <bool kTma>
+__global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
+    full_kernel(const Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using R = Roles<kTma>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    Cta c{p, smem, smem_u32(smem), 0u, reinterpret_cast<volatile int*>(smem + kOffAbort)};
+
+    if (tid == 0) {
+        for (int e = 0; e < kRingTiles; ++e) {
+            mbar_init(c.bar(BAR_FULL0 + e), kTma ? 1 : 32 * R::kLoadWarps);
+            mbar_init(c.bar(BAR_EMPTY0 + e), 1);
+        }
+        mbar_init(c.bar(BAR_SFULL), 1);
+        mbar_init(c.bar(BAR_SEMPTY), kSoftmaxWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(c.bar(BAR_PFULL0 + i), kSoftmaxWarps);
+            mbar_init(c.bar(BAR_PVDONE0 + i), 1);
+        }
+        mbar_init(c.bar(BAR_QFULL), kSoftmaxWarps);
+        mbar_init(c.bar(BAR_QEMPTY), 1);
+        mbar_init(c.bar(BAR_OEMPTY), kSoftmaxWarps);
+        mbar_init(c.bar(BAR_DRAIN), 1);
+        mbar_init(c.bar(BAR_DONE), kSoftmaxWarps);
+        *c.abort_flag = 0;
+        fence_mbar_init();
+        if (kTma) {
+            prefetch_tmap(&kmap);
+            if (!p.kv_same) prefetch_tmap(&vmap);
+        }
+    }
+    if (warp == R::kMmaWarp) {
+        tmem_alloc(c.sbase + kOffTmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    c.tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
+    // Everything above overlaps the prologue; its plan is read only after this.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const PlanHead head = *p.plan.head;
+    const int32_t cta = blockIdx.x;
+    if (cta < head.ctas) {
+        c.begin = cta * head.tiles / head.ctas;
+        c.end = (cta + 1) * head.tiles / head.ctas;
+        c.first_k = p.plan.cta_k[cta];
+        if (warp < R::kLoadWarps) {
+            if constexpr (kTma) run_load_tma(c, &kmap, &vmap);
+            else run_load_copies(c);
+        } else if (warp == R::kMmaWarp) {
+            run_mma(c);
+            // Until every MMA has completed and the softmax warps have read tensor memory.
+            tc_commit_el(c.bar(BAR_DRAIN), elect_one());
+            uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(c.bar(BAR_DRAIN), 0) && globaltimer_ns() - t0 < kDrainLimitNs) {
+            }
+            t0 = globaltimer_ns();
+            while (!mbar_try_wait(c.bar(BAR_DONE), 0) && globaltimer_ns() - t0 < kDrainLimitNs) {
+            }
+            __syncwarp();
+        } else {
+            run_softmax<kTma>(c);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.bar(BAR_DONE));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == R::kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(c.tmem, kTmemCols);
+    }
+}
+
+template <bool kTma>
+cudaError_t setup() {
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, full_kernel<kTma>);
+    if (e != cudaSuccess) return e;
+    if (attr.maxThreadsPerBlock < Roles<kTma>::kThreads) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(full_kernel<kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(full_kernel<kTma>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
 }
 
 }  // namespace
+}  // namespace full
 
-cudaError_t launch_full(const FullParams& p, cudaStream_t stream) {
-    cudaError_t e = cudaMemsetAsync(p.status, 0, 4, stream);
-    if (e != cudaSuccess) return e;
-    const int64_t warps = static_cast<int64_t>(p.num_seqs) * p.rows_per_seq * p.heads;
-    full_kernel<<<static_cast<unsigned>((warps + kFullWarps - 1) / kFullWarps), kFullWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t full_setup() {
+    const cudaError_t e = full::setup<true>();
+    return e != cudaSuccess ? e : full::setup<false>();
+}
+
+cudaError_t launch_full(const full::Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.max_ctas);
+    cfg.blockDim = dim3(p.box_rows > 0 ? full::Roles<true>::kThreads : full::Roles<false>::kThreads);
+    cfg.dynamicSmemBytes = full::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return p.box_rows > 0 ? cudaLaunchKernelEx(&cfg, full::full_kernel<true>, p, kmap, vmap)
+                          : cudaLaunchKernelEx(&cfg, full::full_kernel<false>, p, kmap, vmap);
 }
 
 }  // namespace dsa

@@ -1,0 +1,134 @@
+// Shared by the kernels of the full-cache decode (full_plan.cu, full.cu): geometry, workspace
+// layout, parameters and the device-side work plan.
+//
+// A sequence's rows_per_seq*heads (row, head) pairs all read the same cache, so they are cut
+// into groups of 64 whatever their rows, and a work unit is (sequence, group): few heads and
+// several verify rows fill one unit together. A unit's tokens are [0, max of its rows'
+// lengths); rows that see fewer mask theirs. The units with any token, in order, form a line
+// of 128-token tiles, T in all, that is cut into `ctas` equal ranges: CTA c takes tiles
+// [c*T/ctas, (c+1)*T/ctas). The lengths are on the device, so the plan is made there. A unit
+// inside one range is written straight to the output; one that several ranges share leaves a
+// partial per CTA (slot 2c for the CTA's first unit, 2c+1 for its last) that the combine
+// kernel joins.
+#pragma once
+
+#include "common.cuh"
+
+namespace dsa {
+namespace full {
+
+constexpr int kTile = 128;
+constexpr int64_t kMaxLen = (int64_t{1} << 31) - 2 * kTile;  // positions stay in 32 bits
+
+struct PlanHead {
+    int64_t tiles;   // T
+    int32_t ctas;    // ranges that T is cut into (0 when T is 0)
+    int32_t live;    // units with a token
+};
+
+// The plan's arrays, indexed by a live unit's number k but for unit_k.
+struct PlanArrays {
+    PlanHead* head;
+    int64_t* start;     // [units + 1] first tile of live unit k on the line
+    int32_t* unit;      // [units] its unit
+    int32_t* max_len;   // [units] longest length of its rows
+    int32_t* min_len;   // [units] shortest
+    int32_t* unit_k;    // [units] k of each unit, -1 without a token
+    int32_t* cta_k;     // [ctas] live unit that a range starts in
+};
+
+struct Layout {
+    size_t status, head, start, unit, max_len, min_len, unit_k, cta_k, qimg, qscale, part_o, part_lse, total;
+};
+
+inline Layout layout(int64_t units, int64_t ctas) {
+    Layout L;
+    size_t o = 0;
+    auto put = [&](size_t bytes) {
+        const size_t at = o;
+        o = align256(o + bytes);
+        return at;
+    };
+    L.status = put(256);
+    L.head = put(sizeof(PlanHead));
+    L.start = put(static_cast<size_t>(units + 1) * 8);
+    L.unit = put(static_cast<size_t>(units) * 4);
+    L.max_len = put(static_cast<size_t>(units) * 4);
+    L.min_len = put(static_cast<size_t>(units) * 4);
+    L.unit_k = put(static_cast<size_t>(units) * 4);
+    L.cta_k = put(static_cast<size_t>(ctas) * 4);
+    L.qimg = put(static_cast<size_t>(units) * kQImageBytes);
+    L.qscale = put(static_cast<size_t>(units) * kHeadsPerCta * 4);
+    L.part_o = put(static_cast<size_t>(2 * ctas) * kHeadsPerCta * kLatent * 2);
+    L.part_lse = put(static_cast<size_t>(2 * ctas) * kHeadsPerCta * 4);
+    L.total = o;
+    return L;
+}
+
+struct Params {
+    const uint16_t* q;         // bf16 bits [R, heads, 512]
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;   // [R], or [num_seqs] before the verify rows
+    uint16_t* out;             // bf16 bits [R, heads, 512]
+    int* status;
+    PlanArrays plan;
+    uint8_t* qimg;             // [units, 64 KB]
+    float* qscale;             // [units, 64]
+    uint16_t* part_o;          // f16 bits [2*ctas, 64, 512], laid out as the selected decode's partials
+    float* part_lse;           // [2*ctas, 64]
+    int64_t cache_stride;
+    int32_t num_seqs, rows_per_seq, heads, pairs, groups, units, max_ctas;
+    int32_t block_size, max_blocks_per_seq, verify_rows;
+    int32_t box_rows;          // tokens of a tensor-map box, 0: per-thread copies
+    int32_t kv_same;
+    float score_scale;         // sm_scale * k_scale * log2(e)
+    float v_scale;
+};
+
+#ifdef __CUDACC__
+// Tokens that a row sees. `given` may pass the block table's room: *over says so.
+__device__ __forceinline__ int32_t row_len(const Params& p, int64_t seq, int32_t i, bool* over) {
+    int64_t n = p.verify_rows ? static_cast<int64_t>(p.seq_lens[seq]) + i + 1 : p.seq_lens[seq * p.rows_per_seq + i];
+    int64_t room = p.max_blocks_per_seq > 0 ? static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size : kMaxLen;
+    if (room > kMaxLen) room = kMaxLen;
+    *over = n > room;
+    if (n > room) n = room;
+    return n > 0 ? static_cast<int32_t>(n) : 0;
+}
+
+// One CTA's stretch of one unit.
+struct Segment {
+    int32_t k, unit;
+    int32_t t0, t1;            // tiles of the unit
+    int32_t max_len, min_len;  // of the unit's rows
+    int32_t part;              // partial slot, -1: the whole unit
+    bool last;                 // the CTA's last unit
+};
+__device__ __forceinline__ Segment segment(const Params& p, int64_t begin, int64_t end, int32_t cta, int32_t first_k, int32_t k) {
+    Segment s;
+    const int64_t b = p.plan.start[k], e = p.plan.start[k + 1];
+    s.k = k;
+    s.unit = p.plan.unit[k];
+    s.max_len = p.plan.max_len[k];
+    s.min_len = p.plan.min_len[k];
+    s.t0 = static_cast<int32_t>((begin > b ? begin : b) - b);
+    s.t1 = static_cast<int32_t>((end < e ? end : e) - b);
+    s.part = begin <= b && e <= end ? -1 : 2 * cta + (k == first_k ? 0 : 1);
+    s.last = e >= end;
+    return s;
+}
+#endif
+
+}  // namespace full
+
+cudaError_t full_setup();
+// kmap / vmap: 3-D tensor maps of the caches ([page][row][512 bytes], box 128 bytes x
+// p.box_rows rows), read only when p.box_rows > 0.
+cudaError_t launch_full(const full::Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream);
+cudaError_t full_plan_setup();
+cudaError_t launch_full_plan(const full::Params& p, cudaStream_t stream);
+cudaError_t launch_full_combine(const full::Params& p, cudaStream_t stream);
+
+}  // namespace dsa

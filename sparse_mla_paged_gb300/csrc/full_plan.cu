@@ -1,0 +1,311 @@
+// Before and after the full-cache decode kernel: the prologue (work plan and query operands)
+// and the join of units that several CTAs shared.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "full.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace full {
+namespace {
+
+constexpr int kPrologueThreads = 256;
+constexpr int kWarps = kPrologueThreads / 32;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ void scan2(int64_t& a, int32_t& b, int64_t* sa, int32_t* sb, int64_t* ta, int32_t* tb) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t ia = a;
+    int32_t ib = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, ia, o);
+        const int32_t y = __shfl_up_sync(0xffffffffu, ib, o);
+        if (lane >= o) {
+            ia += x;
+            ib += y;
+        }
+    }
+    __syncthreads();  // the previous round's sums are read
+    if (lane == 31) {
+        sa[warp] = ia;
+        sb[warp] = ib;
+    }
+    __syncthreads();
+    int64_t pa = 0;
+    int32_t pb = 0;
+    *ta = 0;
+    *tb = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) {
+            pa += sa[w];
+            pb += sb[w];
+        }
+        *ta += sa[w];
+        *tb += sb[w];
+    }
+    a = pa + ia - a;
+    b = pb + ib - b;
+}
+
+// One block: the line of tiles (see full.cuh), units in order, kPrologueThreads at a time.
+__device__ void make_plan(const Params& p) {
+    __shared__ int64_t sa[kWarps];
+    __shared__ int32_t sb[kWarps];
+    if (threadIdx.x == 0) atomicExch(p.status, 0);
+    int64_t tiles = 0;
+    int32_t live = 0;
+    bool any_over = false;
+    for (int32_t u0 = 0; u0 < p.units; u0 += kPrologueThreads) {
+        const int32_t u = u0 + threadIdx.x;
+        int32_t top = 0, low = 0;
+        if (u < p.units) {
+            const int32_t seq = u / p.groups, first = (u % p.groups) * kHeadsPerCta;
+            const int32_t r0 = first / p.heads, r1 = min(first + kHeadsPerCta, p.pairs) - 1;
+            low = INT32_MAX;
+            for (int32_t i = r0; i <= r1 / p.heads; ++i) {
+                bool over;
+                const int32_t n = row_len(p, seq, i, &over);
+                any_over |= over;
+                top = max(top, n);
+                low = min(low, n);
+            }
+        }
+        int64_t at = (top + kTile - 1) / kTile;
+        const int64_t mine = at;
+        int32_t k = top > 0 ? 1 : 0;
+        int64_t sum_t;
+        int32_t sum_k;
+        scan2(at, k, sa, sb, &sum_t, &sum_k);
+        if (u < p.units) {
+            p.plan.unit_k[u] = top > 0 ? live + k : -1;
+            if (top > 0) {
+                p.plan.start[live + k] = tiles + at;
+                p.plan.start[live + k + 1] = tiles + at + mine;  // the next unit writes the same value
+                p.plan.unit[live + k] = u;
+                p.plan.max_len[live + k] = top;
+                p.plan.min_len[live + k] = low;
+            }
+        }
+        tiles += sum_t;
+        live += sum_k;
+    }
+    const int32_t ctas = static_cast<int32_t>(min(tiles, static_cast<int64_t>(p.max_ctas)));
+    if (threadIdx.x == 0) *p.plan.head = PlanHead{tiles, ctas, live};
+    if (any_over) atomicCAS(p.status, 0, kStatusBounds);
+    __syncthreads();
+    // Range c starts at tile floor(c*T/ctas), which lies in unit k for the c with
+    // ceil(start[k]*ctas/T) <= c < ceil(start[k+1]*ctas/T).
+    for (int32_t k = threadIdx.x; k < live; k += kPrologueThreads) {
+        const int64_t c0 = (p.plan.start[k] * ctas + tiles - 1) / tiles, c1 = (p.plan.start[k + 1] * ctas + tiles - 1) / tiles;
+        for (int64_t c = c0; c < c1; ++c) p.plan.cta_k[c] = k;
+    }
+}
+
+// Query operand of one unit, as the selected decode's prologue makes it: 8 warps x 8 pairs,
+// lane l dims [16l, 16l+16); a head's bf16 query as two E4M3 terms after a scaling by a power
+// of two (exact for elements above 2^-10 of its largest), rows 2k and 2k+1 of a quarter the
+// two terms of pair 16q + k, stored chunk-major. A head with a NaN or an infinity gets zero
+// codes and a NaN scale, which makes all its scores NaN. A unit without a token writes its
+// zeros here.
+__device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t seq = unit / p.groups, first = (unit % p.groups) * kHeadsPerCta;
+    const int32_t valid = min(kHeadsPerCta, p.pairs - first);
+    const int64_t pair0 = static_cast<int64_t>(seq) * p.pairs + first;
+    bool none = true;
+    for (int32_t i = first / p.heads; i <= (first + valid - 1) / p.heads; ++i) {
+        bool over;
+        none &= row_len(p, seq, i, &over) == 0;
+    }
+    if (none) {
+        uint4* o = reinterpret_cast<uint4*>(p.out + pair0 * kLatent);
+        for (int e = threadIdx.x; e < valid * kLatent / 8; e += kPrologueThreads) o[e] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    uint4 raw[kHeadsPerCta / kWarps][2];
+#pragma unroll
+    for (int i = 0; i < kHeadsPerCta / kWarps; ++i) {
+        const int hl = warp + i * kWarps;
+        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+        if (hl < valid) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (pair0 + hl) * kLatent + lane * 16);
+            raw[i][0] = src[0];
+            raw[i][1] = src[1];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadsPerCta / kWarps; ++i) {
+        const int hl = warp + i * kWarps;
+        const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
+                               raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+        uint32_t amax = 0;  // magnitudes as bits: NaN and infinity are the largest
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        const int E = static_cast<int>(amax >> 23);
+        const bool broken = E == 255;
+        int e = amax > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
+        e = e > 126 ? 126 : (e < -126 ? -126 : e);
+        const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float vh[4], vl[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t bits = m & 1 ? w[2 * k + m / 2] & 0xFFFF0000u : w[2 * k + m / 2] << 16;
+                const float v = broken ? 0.0f : __uint_as_float(bits) * sc;
+                vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
+                vl[m] = v - vh[m];
+            }
+            hi[k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
+            lo[k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
+        }
+        const int rh = 32 * (hl >> 4) + 2 * (hl & 15);
+        *reinterpret_cast<uint4*>(stage + rh * 512 + ((lane ^ (rh & 31)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(stage + (rh + 1) * 512 + ((lane ^ ((rh + 1) & 31)) << 4)) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (lane == 0)
+            p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hl] =
+                broken ? __uint_as_float(0x7FC00000u) : p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+    __syncthreads();
+    uint8_t* img = p.qimg + static_cast<int64_t>(unit) * kQImageBytes;
+    for (int k = threadIdx.x; k < kQImageBytes / 16; k += kPrologueThreads) {
+        const int c = k >> 7, r = k & 127;
+        *reinterpret_cast<uint4*>(img + c * 2048 + r * 16) =
+            *reinterpret_cast<const uint4*>(stage + r * 512 + ((c ^ (r & 31)) << 4));
+    }
+}
+
+__global__ void __launch_bounds__(kPrologueThreads) full_prologue_kernel(const Params p) {
+    extern __shared__ __align__(16) uint8_t stage[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0) make_plan(p);
+    else prepare(p, blockIdx.x - 1, stage);
+}
+
+// ------------------------------------------------------------------------------------
+// Join of the pieces of split units
+// ------------------------------------------------------------------------------------
+constexpr int kCombineThreads = 256;
+constexpr int kCombineWarps = kCombineThreads / 32;  // one per group of 8 heads
+constexpr int kDims = 32;                            // dims of a block: the lanes of a warp
+constexpr int kChunk = 16;                           // pieces in flight at once
+static_assert(kCombineWarps * 8 == kHeadsPerCta, "a warp per 8-head group");
+
+// Block (unit, 32 dims). Partial k holds O_k / l_k (f16, E4M3 code units) and lse_k =
+// m_k + log2 l_k; out = v_scale * sum_k 2^(lse_k - M) O_k / sum_k 2^(lse_k - M). Pieces come
+// in chunks of 16 with all their loads in flight and a running maximum per head.
+__global__ void __launch_bounds__(kCombineThreads) full_combine_kernel(const Params p) {
+    __shared__ float w_s[kCombineWarps][kChunk][8];
+    __shared__ __align__(16) float a_s[kCombineWarps][8];
+    __shared__ __align__(16) __nv_bfloat16 out_s[kHeadsPerCta][kDims];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int32_t unit = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int32_t k = p.plan.unit_k[unit];
+    if (k < 0) return;  // zeros already
+    const PlanHead head = *p.plan.head;
+    const int64_t begin = p.plan.start[k], end = p.plan.start[k + 1];
+    // The range holding tile x is the last one starting at or before it.
+    const int32_t c_lo = static_cast<int32_t>(((begin + 1) * head.ctas - 1) / head.tiles);
+    const int32_t c_hi = static_cast<int32_t>((end * head.ctas - 1) / head.tiles);
+    if (c_lo == c_hi) return;  // written whole
+    // Every range between holds this unit first, and so may the first one.
+    const int32_t slot_lo = 2 * c_lo + (p.plan.cta_k[c_lo] == k ? 0 : 1);
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot_lo : 2 * (c_lo + i)); };
+    const int pieces = c_hi - c_lo + 1;
+    const __half* po = reinterpret_cast<const __half*>(p.part_o);
+    float acc[8] = {};
+    float m_run = kNegInf, s_run = 0.0f;  // lanes 0..7: head 8*warp + lane
+    for (int k0 = 0; k0 < pieces; k0 += kChunk) {
+        uint4 raw[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (k0 + i < pieces)
+                raw[i] = *reinterpret_cast<const uint4*>(
+                    po + slot(k0 + i) * kHeadsPerCta * kLatent +
+                    ((static_cast<int64_t>(blockIdx.y) * kCombineWarps + warp) * kDims + lane) * 8);
+        }
+        __syncwarp();  // the previous chunk's weights are read
+        if (lane < 8) {
+            float lse[kChunk], top = m_run;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                lse[i] = k0 + i < pieces ? p.part_lse[slot(k0 + i) * kHeadsPerCta + warp * 8 + lane] : kNegInf;
+                top = fmaxf(top, lse[i]);
+            }
+            const float a = m_run != kNegInf ? exp2f(m_run - top) : 0.0f;
+            s_run *= a;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+                const float w = lse[i] != kNegInf ? exp2f(lse[i] - top) : 0.0f;
+                s_run += w;
+                w_s[warp][i][lane] = w;
+            }
+            a_s[warp][lane] = a;
+            m_run = top;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= a_s[warp][e];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+            if (k0 + i >= pieces) continue;
+            const __half2* hv = reinterpret_cast<const __half2*>(&raw[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = __half22float2(hv[e]);
+                acc[2 * e] = fmaf(w_s[warp][i][2 * e], f.x, acc[2 * e]);
+                acc[2 * e + 1] = fmaf(w_s[warp][i][2 * e + 1], f.y, acc[2 * e + 1]);
+            }
+        }
+    }
+    __syncwarp();
+    if (lane < 8) a_s[warp][lane] = s_run == 0.0f ? 0.0f : p.v_scale / s_run;
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out_s[warp * 8 + e][lane] = __float2bfloat16_rn(acc[e] * a_s[warp][e]);
+    __syncthreads();
+    const int32_t seq = unit / p.groups, first = (unit % p.groups) * kHeadsPerCta;
+    const int hl = t / 4, c = (t % 4) * 8;
+    if (hl < p.pairs - first)
+        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(seq) * p.pairs + first + hl) * kLatent + blockIdx.y * kDims + c) =
+            *reinterpret_cast<const uint4*>(&out_s[hl][c]);
+}
+
+}  // namespace
+}  // namespace full
+
+cudaError_t full_plan_setup() {
+    cudaError_t e = cudaFuncSetAttribute(full::full_prologue_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQImageBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(full::full_prologue_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(full::full_combine_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+}
+
+cudaError_t launch_full_plan(const full::Params& p, cudaStream_t stream) {
+    full::full_prologue_kernel<<<p.units + 1, full::kPrologueThreads, kQImageBytes, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_full_combine(const full::Params& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.units, kLatent / full::kDims);
+    cfg.blockDim = dim3(full::kCombineThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, full::full_combine_kernel, p);
+}
+
+}  // namespace dsa
