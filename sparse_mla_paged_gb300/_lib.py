@@ -76,6 +76,8 @@ class DsaError(RuntimeError):
 def load(path: str = LIB_PATH):
     """Load and declare the library (raises if it is missing: there is no other path)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -6,6 +6,7 @@ raise DsaError on a non-OK status.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -236,21 +237,47 @@ def absorb_o(o_proj: torch.Tensor, kv_b: torch.Tensor, heads: int, nope: int, vd
     return out
 
 
-def _on(t: torch.Tensor, *others):
-    """Device guard of t's device; every other tensor has to be there too."""
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {o.device}")
-    return torch.cuda.device(t.device)
+def _device_of(t: torch.Tensor, name: str) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return i
 
 
-def _current(stream, device):
-    """The stream of a call (default: the device's current one) as a torch stream, for allocations."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    return torch.cuda.ExternalStream(_stream(stream), device=device)
+def _need_on(t: torch.Tensor, dtype, name: str, index: int):
+    if t.get_device() != index or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on cuda:{index}")
+
+
+class _Launch:
+    """What a call needs of its device: makes it current for the call (when it is not), and
+    gives the raw stream and the context in which its outputs are allocated (the given
+    stream's, so that their memory is not handed out again while that stream uses it)."""
+    __slots__ = ("index", "raw", "stream", "guard")
+
+    def __init__(self, index: int, stream):
+        self.index = index
+        self.guard = None
+        if stream is None:
+            self.stream = None
+            self.raw = torch._C._cuda_getCurrentRawStream(index)
+        else:
+            self.raw = _stream(stream)
+            self.stream = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.raw, device=index)
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+    def allocating(self):
+        return contextlib.nullcontext() if self.stream is None else torch.cuda.stream(self.stream)
 
 
 class StepPlan(NamedTuple):
@@ -265,9 +292,10 @@ class StepPlan(NamedTuple):
 
 def alloc_step_plan(rows: int, device=None) -> StepPlan:
     """Output buffers of plan_step, to be kept from step to step (a captured step needs fixed ones)."""
-    i32 = dict(dtype=torch.int32, device=device or "cuda")
-    return StepPlan(torch.empty(rows, dtype=torch.int64, device=device or "cuda"), torch.empty(rows, **i32),
-                    torch.empty(rows, **i32), torch.empty(rows, **i32), torch.empty(4, **i32))
+    # One allocation for all five: five of them cost more on the host than the plan on the GPU.
+    buf = torch.empty(5 * rows + 4, dtype=torch.int32, device=device or "cuda")
+    slots, positions, row_lens, row_seqs, info = buf.split_with_sizes((2 * rows, rows, rows, rows, 4))
+    return StepPlan(slots.view(torch.int64), positions, row_lens, row_seqs, info)
 
 
 def plan_step(base_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_size: int,
@@ -277,31 +305,30 @@ def plan_step(base_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch
     new token's slot, position, visible length and request. rows_per_seq 0 packs the rows
     (max_rows is then needed, unless out gives it), else row s*rows_per_seq + i is token i of
     request s."""
+    i = _device_of(base_lens, "base_lens")
     for t, n in ((base_lens, "base_lens"), (new_lens, "new_lens"), (free_pages, "free_pages"),
                  (block_tables, "block_tables")):
-        _need(t, torch.int32, n)
+        _need_on(t, torch.int32, n, i)
     n = base_lens.numel()
     if new_lens.numel() != n or block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("base_lens [num_seqs], new_lens [num_seqs], block_tables [num_seqs, max_blocks_per_seq]")
-    rows = n * int(rows_per_seq) if rows_per_seq else (max_rows if out is None else out.slots.numel())
-    if rows is None or (max_rows is not None and int(max_rows) != rows):
+    rows = n * rows_per_seq if rows_per_seq else (max_rows if out is None else out.slots.numel())
+    if rows is None or (max_rows is not None and max_rows != rows):
         raise ValueError("max_rows must be the number of rows to write (num_seqs*rows_per_seq unless packed)")
-    with _on(base_lens, new_lens, free_pages, block_tables, *(out or ())):
-        s = _current(stream, base_lens.device)
+    with _Launch(i, stream) as at:
         if out is None:
-            with torch.cuda.stream(s):
-                out = alloc_step_plan(int(rows), base_lens.device)
-        _need(out.slots, torch.int64, "out.slots")
-        if out.slots.numel() != rows or out.info.numel() < 4:
-            raise ValueError(f"out must hold {rows} rows")
-        for t in out[1:]:
-            _need(t, torch.int32, "out")
-            if t is not out.info and t.numel() != rows:
+            with at.allocating():
+                out = alloc_step_plan(rows, base_lens.device)
+        else:
+            _need_on(out.slots, torch.int64, "out.slots", i)
+            for t in out[1:]:
+                _need_on(t, torch.int32, "out", i)
+            if out.info.numel() < 4 or any(t.numel() != rows for t in out[:4]):
                 raise ValueError(f"out must hold {rows} rows")
-        check(_lib.load().dsa_plan_step(_ptr(base_lens), _ptr(new_lens), n, int(rows_per_seq), int(rows),
-                                        _ptr(free_pages), free_pages.numel(), int(block_size), _ptr(block_tables),
-                                        int(block_tables.shape[1]), _ptr(out.slots), _ptr(out.positions),
-                                        _ptr(out.row_lens), _ptr(out.row_seqs), _ptr(out.info), s.cuda_stream),
+        check(_lib.load().dsa_plan_step(base_lens.data_ptr(), new_lens.data_ptr(), n, rows_per_seq, rows,
+                                        free_pages.data_ptr(), free_pages.numel(), block_size, block_tables.data_ptr(),
+                                        block_tables.shape[1], out.slots.data_ptr(), out.positions.data_ptr(),
+                                        out.row_lens.data_ptr(), out.row_seqs.data_ptr(), out.info.data_ptr(), at.raw),
               "dsa_plan_step")
     return out
 
@@ -316,20 +343,22 @@ def index_write(keys: torch.Tensor, slots: torch.Tensor, block_size: int, page_s
                 norm_bias: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> torch.Tensor:
     """dsa_index_write: the (layer-normalised) index keys bf16 [rows, 128] as E4M3 codes and a
     float32 scale per row into each row's slot (negative: skipped). Returns index_cache."""
-    _need(keys, torch.bfloat16, "keys")
-    _need(slots, torch.int64, "slots")
-    _need(index_cache, torch.uint8, "index_cache")
-    if keys.shape[-1] != INDEX or slots.numel() * INDEX != keys.numel():
+    i = _device_of(index_cache, "index_cache")
+    _need_on(keys, torch.bfloat16, "keys", i)
+    _need_on(slots, torch.int64, "slots", i)
+    _need_on(index_cache, torch.uint8, "index_cache", i)
+    rows = slots.numel()
+    if keys.shape[-1] != INDEX or rows * INDEX != keys.numel():
         raise ValueError("keys [rows, 128], slots [rows]")
     for t, n in ((norm_weight, "norm_weight"), (norm_bias, "norm_bias")):
         if t is not None:
-            _need(t, torch.bfloat16, n)
+            _need_on(t, torch.bfloat16, n, i)
             if t.numel() != INDEX:
                 raise ValueError(f"{n} [128]")
-    with _on(index_cache, keys, slots, norm_weight, norm_bias):
-        check(_lib.load().dsa_index_write(_ptr(keys), _ptr(norm_weight), _ptr(norm_bias), _ptr(slots),
-                                          int(slots.numel()), float(eps), int(block_size), int(page_stride_bytes),
-                                          _ptr(index_cache), _stream(stream)), "dsa_index_write")
+    with _Launch(i, stream) as at:
+        check(_lib.load().dsa_index_write(keys.data_ptr(), _ptr(norm_weight), _ptr(norm_bias), slots.data_ptr(), rows,
+                                          eps, block_size, page_stride_bytes, index_cache.data_ptr(), at.raw),
+              "dsa_index_write")
     return index_cache
 
 
@@ -345,30 +374,30 @@ def pool_scores(q: torch.Tensor, head_weights: torch.Tensor, index_cache: torch.
                 stream=None) -> torch.Tensor:
     """dsa_pool_scores: float32 [R, n_pools], per row the maximum over each pool's kpool positions of
     scale_j * sum_h head_weights[h] * max(0, q[h] . k_j); -inf for pools that end after q_pos."""
-    _need(q, torch.bfloat16, "q")
-    _need(head_weights, torch.float32, "head_weights")
-    _need(index_cache, torch.uint8, "index_cache")
-    _need(block_tables, torch.int32, "block_tables")
-    _need(q_pos, torch.int32, "q_pos")
+    i = _device_of(q, "q")
+    _need_on(q, torch.bfloat16, "q", i)
+    _need_on(head_weights, torch.float32, "head_weights", i)
+    _need_on(index_cache, torch.uint8, "index_cache", i)
+    _need_on(block_tables, torch.int32, "block_tables", i)
+    _need_on(q_pos, torch.int32, "q_pos", i)
     rows = num_seqs * rows_per_seq
     if q.numel() != rows * num_heads * INDEX or head_weights.numel() != rows * num_heads or q_pos.numel() != rows:
         raise ValueError("q [R, num_heads, 128], head_weights [R, num_heads], q_pos [R]")
     _table_rows(block_tables, max_blocks_per_seq, num_seqs)
     if device_status is not None:
-        _need(device_status, torch.int32, "device_status")
-    with _on(q, head_weights, index_cache, block_tables, q_pos, out, device_status):
-        s = _current(stream, q.device)
+        _need_on(device_status, torch.int32, "device_status", i)
+    with _Launch(i, stream) as at:
         if out is None:
-            with torch.cuda.stream(s):
+            with at.allocating():
                 out = torch.empty((rows, n_pools), dtype=torch.float32, device=q.device)
-        _need(out, torch.float32, "out")
-        if out.numel() != rows * n_pools:
-            raise ValueError(f"out must hold [{rows}, {n_pools}]")
-        check(_lib.load().dsa_pool_scores(_ptr(q), _ptr(head_weights), _ptr(index_cache), _ptr(block_tables),
-                                          int(max_blocks_per_seq), _ptr(q_pos), int(num_seqs), int(rows_per_seq),
-                                          int(num_heads), int(block_size), int(page_stride_bytes), int(kpool),
-                                          int(n_pools), _ptr(out), _ptr(device_status), s.cuda_stream),
-              "dsa_pool_scores")
+        else:
+            _need_on(out, torch.float32, "out", i)
+            if out.numel() != rows * n_pools:
+                raise ValueError(f"out must hold [{rows}, {n_pools}]")
+        check(_lib.load().dsa_pool_scores(q.data_ptr(), head_weights.data_ptr(), index_cache.data_ptr(),
+                                          block_tables.data_ptr(), max_blocks_per_seq, q_pos.data_ptr(), num_seqs,
+                                          rows_per_seq, num_heads, block_size, page_stride_bytes, kpool, n_pools,
+                                          out.data_ptr(), _ptr(device_status), at.raw), "dsa_pool_scores")
     return out
 
 
@@ -392,30 +421,30 @@ def decode_full(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
     """dsa_mla_decode_full: every row attends to its whole cache; seq_lens per row, or with
     verify_rows per sequence before its rows. Returns out (bf16 [R, H, 512]). Without a
     workspace one is allocated for the call."""
-    _need(q, torch.bfloat16, "q")
-    _need(k_cache, torch.uint8, "k_cache")
-    _need(v_cache, torch.uint8, "v_cache")
-    _need(block_tables, torch.int32, "block_tables")
-    _need(seq_lens, torch.int32, "seq_lens")
+    i = _device_of(q, "q")
+    _need_on(q, torch.bfloat16, "q", i)
+    _need_on(k_cache, torch.uint8, "k_cache", i)
+    _need_on(v_cache, torch.uint8, "v_cache", i)
+    _need_on(block_tables, torch.int32, "block_tables", i)
+    _need_on(seq_lens, torch.int32, "seq_lens", i)
     rows = num_seqs * rows_per_seq
     if q.numel() != rows * num_q_heads * LATENT or seq_lens.numel() != (num_seqs if verify_rows else rows):
         raise ValueError("q [R, num_q_heads, 512], seq_lens [R] ([num_seqs] for verify rows)")
     _table_rows(block_tables, max_blocks_per_seq, num_seqs)
-    with _on(q, k_cache, v_cache, block_tables, seq_lens, out, workspace):
-        s = _current(stream, q.device)
-        with torch.cuda.stream(s):
-            out = torch.empty_like(q) if out is None else out
-            if workspace is None:
-                workspace = alloc_full_workspace(num_seqs, rows_per_seq, num_q_heads, q.device)
-        _need(out, torch.bfloat16, "out")
-        _need(workspace, torch.uint8, "workspace")
+    with _Launch(i, stream) as at:
+        if out is None or workspace is None:
+            with at.allocating():
+                out = torch.empty_like(q) if out is None else out
+                if workspace is None:
+                    workspace = alloc_full_workspace(num_seqs, rows_per_seq, num_q_heads, q.device)
+        _need_on(out, torch.bfloat16, "out", i)
+        _need_on(workspace, torch.uint8, "workspace", i)
         if out.numel() != q.numel():
             raise ValueError("out [R, num_q_heads, 512]")
         check(_lib.load().dsa_mla_decode_full(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), int(max_blocks_per_seq), _ptr(seq_lens),
-            int(num_seqs), int(rows_per_seq), int(num_q_heads), int(block_size), int(cache_stride_bytes),
-            float(k_scale), float(v_scale), float(sm_scale), _ptr(out), int(verify_rows), _ptr(workspace),
-            workspace.numel(), s.cuda_stream), "dsa_mla_decode_full")
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks_per_seq,
+            seq_lens.data_ptr(), num_seqs, rows_per_seq, num_q_heads, block_size, cache_stride_bytes, k_scale, v_scale,
+            sm_scale, out.data_ptr(), verify_rows, workspace.data_ptr(), workspace.numel(), at.raw), "dsa_mla_decode_full")
     return out
 
 
