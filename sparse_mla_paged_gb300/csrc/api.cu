@@ -219,15 +219,23 @@ bool encode_cache_map(const void* base, size_t mem_bytes, CUtensorMap* m) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map of a paged cache, [page][row of the page][512 bytes], pages enough to span the
+// Rows of a tensor-map box that stays within a page and fills 128-token tiles evenly, for pages
+// of 16, 32, 64 or 128 tokens or a multiple of 128; 0 for others.
+int32_t box_rows(int32_t block_size) {
+    if (block_size >= 16 && 128 % block_size == 0) return block_size;
+    return block_size % 128 == 0 ? 128 : 0;
+}
+
+// 3-D map of a paged cache, [page][row of the page][row_bytes], pages enough to span the
 // device's memory, read as boxes of 128 bytes x `rows` rows of one page into the
 // 128-byte-swizzled operand layout; a page outside the map (a negative one) gives zeros.
-bool encode_page_map(const void* base, size_t mem_bytes, int32_t block_size, int64_t stride, int32_t rows, CUtensorMap* m) {
+bool encode_page_map(const void* base, size_t mem_bytes, int32_t row_bytes, int32_t block_size, int64_t stride, int32_t rows,
+                     CUtensorMap* m) {
     const auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t pages = std::min<cuuint64_t>(mem_bytes / static_cast<size_t>(stride) + 1, (1ull << 31) - 1);
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(block_size), pages};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kLatent), static_cast<cuuint64_t>(stride)};
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(block_size), pages};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(stride)};
     const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(rows), 1};
     const cuuint32_t estride[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estride,
@@ -703,7 +711,7 @@ int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* n
     p.rows = rows;
     p.block_size = block_size;
     p.eps = eps;
-    return from_cuda(launch_index_write(p, static_cast<cudaStream_t>(stream)));
+    return from_cuda(launch_index_write(p, d->sms, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* index_cache, const int32_t* block_tables,
@@ -744,7 +752,14 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.kpool = kpool;
     p.n_pools = n_pools;
-    return from_cuda(launch_pool_scores(p, d->sms, static_cast<cudaStream_t>(stream)));
+    // Boxes also need tiles of 128 tokens, that is pools that divide them.
+    p.box_rows = 128 % kpool == 0 ? box_rows(block_size) : 0;
+    CUtensorMap tmap;
+    std::memset(&tmap, 0, sizeof tmap);
+    if (p.box_rows > 0 &&
+        !encode_page_map(index_cache, d->mem_bytes, kIndexDim, block_size, page_stride_bytes, p.box_rows, &tmap))
+        p.box_rows = 0;
+    return from_cuda(launch_pool_scores(p, tmap, d->sms, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -819,16 +834,13 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     p.kv_same = k_cache == v_cache ? 1 : 0;
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;
-    // Tensor-map boxes hold rows of one page and fill tiles evenly: a page of 16, 32, 64 or 128
-    // tokens, or of a multiple of 128. Other page sizes take per-thread copies.
-    if (block_size >= 16 && full::kTile % block_size == 0) p.box_rows = block_size;
-    else if (block_size % full::kTile == 0) p.box_rows = full::kTile;
+    p.box_rows = box_rows(block_size);  // other page sizes take per-thread copies
     CUtensorMap kmap, vmap;
     std::memset(&kmap, 0, sizeof kmap);
     std::memset(&vmap, 0, sizeof vmap);
     if (p.box_rows > 0 &&
-        !(encode_page_map(k_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &kmap) &&
-          (p.kv_same || encode_page_map(v_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &vmap))))
+        !(encode_page_map(k_cache, d->mem_bytes, kLatent, block_size, cache_stride_bytes, p.box_rows, &kmap) &&
+          (p.kv_same || encode_page_map(v_cache, d->mem_bytes, kLatent, block_size, cache_stride_bytes, p.box_rows, &vmap))))
         p.box_rows = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = from_cuda(launch_full_plan(p, s));

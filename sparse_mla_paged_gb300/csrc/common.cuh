@@ -247,6 +247,7 @@ struct PoolScoresParams {
     int* status;               // or null
     int64_t page_stride;
     int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, kpool, n_pools;
+    int32_t box_rows;          // tokens of a tensor-map box, 0: per-thread copies
 };
 
 // Launchers (each defined next to its kernel).
@@ -272,9 +273,11 @@ int32_t check_device();  // DSA_OK when the current device is an sm_103 with the
 cudaError_t select_kernel_setup();
 cudaError_t plan_kernel_setup();
 cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_index_write(const IndexWriteParams& p, cudaStream_t stream);
+cudaError_t launch_index_write(const IndexWriteParams& p, int sms, cudaStream_t stream);
 cudaError_t pool_scores_kernel_setup();
-cudaError_t launch_pool_scores(const PoolScoresParams& p, int sms, cudaStream_t stream);
+// tmap: 3-D tensor map of the pages' codes ([page][row][128 bytes], box 128 bytes x p.box_rows
+// rows), read only when p.box_rows > 0.
+cudaError_t launch_pool_scores(const PoolScoresParams& p, const CUtensorMap& tmap, int sms, cudaStream_t stream);
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t decode_kernel_setup_64();
 cudaError_t decode_kernel_setup_128();

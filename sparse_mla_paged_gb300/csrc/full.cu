@@ -453,9 +453,7 @@ __device__ void run_softmax(const Cta& c) {
             c.wait(BAR_SFULL, tau & 1);
             tc_fence_after();
             uint32_t v[kHalfCols];
-#pragma unroll
-            for (int i = 0; i < kHalfCols / 32; ++i)
-                tmem_ld_x32(c.tmem + lane_base + kTmemS + half * kHalfCols + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * i));
+            tmem_ld_x64(c.tmem + lane_base + kTmemS + half * kHalfCols, v);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(BAR_SEMPTY));
@@ -494,50 +492,61 @@ __device__ void run_softmax(const Cta& c) {
             for (int j = 0; j < kScores; ++j) hm4[j & 3] = fmaxf(hm4[j & 3], x[j]);
             float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
             hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1));
-            if (term == 0) hm_s[half * kHeadsPerCta + hq] = hmax;
-            named_bar_sync_id(kBarPair0 + q4, 64);
-            const float tm = fmaxf(hm_s[hq], hm_s[kHeadsPerCta + hq]);
-            // The reference moves when the tile's max exceeds it by more than the margin or
-            // lies far below it (never for a tile of which the pair sees nothing).
-            const bool change = tm > m_ref + kRescaleMargin ||
-                                (tm < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && tm != kNegInf);
-            float alpha = 1.0f;
-            if (change) {
-                const float m_new = fmaxf(tm + kRescaleSlack, m_top - kRescaleFloor);
-                alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
-                l_part *= alpha;
-                m_ref = m_new;
-                m_top = fmaxf(m_top, m_new);
-            }
-            const float* alpha_t = alpha_s + (tau & 1) * kHeadsPerCta;
-            if (term == 0 && half == 0) alpha_s[(tau & 1) * kHeadsPerCta + hq] = alpha;
-            const uint32_t changed = __ballot_sync(0xffffffffu, change);
-            if (half == 0 && lane == 0) flag_s[(tau & 1) * 4 + q4] = changed;
-            const bool any_change = named_bar_any<kBarSoftmax, kSoftmaxThreads>(change);
-            bool resc[2] = {false, false};
-            if (any_change && t > s.t0) {
-                const uint4 f = *reinterpret_cast<const uint4*>(flag_s + (tau & 1) * 4);
-                resc[0] = (f.x | f.y) != 0u;
-                resc[1] = (f.z | f.w) != 0u;
-            }
-
+            // A tile mostly leaves every pair's reference where it is, so P' is formed with it at
+            // once; one barrier then tells whether any half of any pair's scores asks for a
+            // move (the maximum exceeds the reference by more than the margin, or lies far below
+            // it). Only then the halves are compared, references move and P' is formed again.
+            const bool ask = hmax > m_ref + kRescaleMargin ||
+                             (hmax < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && hmax != kNegInf);
             uint32_t hw[kScores / 4], lw[kScores / 4];
-            float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
+            float fresh;
+            bool resc[2] = {false, false};
+            const float* alpha_t = alpha_s + (tau & 1) * kHeadsPerCta;
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+                float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
 #pragma unroll
-            for (int g = 0; g < kScores / 4; ++g) {
-                float ph[4], pl[4];
+                for (int g = 0; g < kScores / 4; ++g) {
+                    float ph[4], pl[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float pp = ex2_approx(x[4 * g + e] + off);
-                    ls4[e] += pp;
-                    ph[e] = hi_part(pp);
-                    pl[e] = pp - ph[e];
+                    for (int e = 0; e < 4; ++e) {
+                        const float pp = ex2_approx(x[4 * g + e] + off);
+                        ls4[e] += pp;
+                        ph[e] = hi_part(pp);
+                        pl[e] = pp - ph[e];
+                    }
+                    hw[g] = pack_e4m3x4(ph[0], ph[1], ph[2], ph[3]);
+                    lw[g] = pack_e4m3x4(pl[0], pl[1], pl[2], pl[3]);
                 }
-                hw[g] = pack_e4m3x4(ph[0], ph[1], ph[2], ph[3]);
-                lw[g] = pack_e4m3x4(pl[0], pl[1], pl[2], pl[3]);
+                fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+                if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(ask)) break;
+                if (term == 0) hm_s[half * kHeadsPerCta + hq] = hmax;
+                named_bar_sync_id(kBarPair0 + q4, 64);
+                const float tm = fmaxf(hm_s[hq], hm_s[kHeadsPerCta + hq]);
+                const bool change = tm > m_ref + kRescaleMargin ||
+                                    (tm < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && tm != kNegInf);
+                float alpha = 1.0f;
+                if (change) {
+                    const float m_new = fmaxf(tm + kRescaleSlack, m_top - kRescaleFloor);
+                    alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
+                    l_part *= alpha;
+                    m_ref = m_new;
+                    m_top = fmaxf(m_top, m_new);
+                }
+                if (term == 0 && half == 0) alpha_s[(tau & 1) * kHeadsPerCta + hq] = alpha;
+                const uint32_t changed = __ballot_sync(0xffffffffu, change);
+                if (half == 0 && lane == 0) flag_s[(tau & 1) * 4 + q4] = changed;
+                // Also keeps the next tile's maxima from overwriting these.
+                const bool any_change = named_bar_any<kBarSoftmax, kSoftmaxThreads>(change);
+                if (!any_change) break;
+                if (t > s.t0) {
+                    const uint4 f = *reinterpret_cast<const uint4*>(flag_s + (tau & 1) * 4);
+                    resc[0] = (f.x | f.y) != 0u;
+                    resc[1] = (f.z | f.w) != 0u;
+                }
             }
-            l_part += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+            l_part += fresh;
             if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
             pv_seen = false;
             const uint32_t pb = c.sbase + kOffP + (tau & 1) * 2 * kPTermBytes;

@@ -99,7 +99,10 @@ __device__ void make_plan(const Params& p) {
     // Range c starts at tile floor(c*T/ctas), which lies in unit k for the c with
     // ceil(start[k]*ctas/T) <= c < ceil(start[k+1]*ctas/T).
     for (int32_t k = threadIdx.x; k < live; k += kPrologueThreads) {
-        const int64_t c0 = (p.plan.start[k] * ctas + tiles - 1) / tiles, c1 = (p.plan.start[k + 1] * ctas + tiles - 1) / tiles;
+        const int64_t n0 = p.plan.start[k] * ctas + tiles - 1, n1 = p.plan.start[k + 1] * ctas + tiles - 1;
+        const bool narrow = n1 >> 32 == 0;  // a 64-bit division is a long sequence
+        const uint32_t d = static_cast<uint32_t>(tiles);
+        const int64_t c0 = narrow ? static_cast<uint32_t>(n0) / d : n0 / tiles, c1 = narrow ? static_cast<uint32_t>(n1) / d : n1 / tiles;
         for (int64_t c = c0; c < c1; ++c) p.plan.cta_k[c] = k;
     }
 }
@@ -188,62 +191,76 @@ __global__ void __launch_bounds__(kPrologueThreads) full_prologue_kernel(const P
     else prepare(p, blockIdx.x - 1, stage);
 }
 
+// The range that holds tile x. T*ctas fits 32 bits but for the longest caches, and a 64-bit
+// division is a long sequence.
+__device__ __forceinline__ int32_t range_of(const PlanHead& head, int64_t x) {
+    const int64_t n = (x + 1) * head.ctas - 1;
+    if (head.tiles * head.ctas < (int64_t{1} << 32)) return static_cast<int32_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(head.tiles));
+    return static_cast<int32_t>(n / head.tiles);
+}
+
 // ------------------------------------------------------------------------------------
 // Join of the pieces of split units
 // ------------------------------------------------------------------------------------
 constexpr int kCombineThreads = 256;
-constexpr int kCombineWarps = kCombineThreads / 32;  // one per group of 8 heads
-constexpr int kDims = 32;                            // dims of a block: the lanes of a warp
-constexpr int kChunk = 16;                           // pieces in flight at once
-static_assert(kCombineWarps * 8 == kHeadsPerCta, "a warp per 8-head group");
+constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kDims = 32;   // dims of a block: the lanes of a warp
+constexpr int kFlight = 4;  // pieces whose loads a warp has in flight
 
-// Block (unit, 32 dims). Partial k holds O_k / l_k (f16, E4M3 code units) and lse_k =
-// m_k + log2 l_k; out = v_scale * sum_k 2^(lse_k - M) O_k / sum_k 2^(lse_k - M). Pieces come
-// in chunks of 16 with all their loads in flight and a running maximum per head.
+// Partial k holds O_k / l_k (f16, E4M3 code units) and lse_k = m_k + log2 l_k; out = v_scale *
+// sum_k 2^(lse_k - M) O_k / sum_k 2^(lse_k - M). A warp folds pieces of 8 pairs x 32 dims, with
+// a running maximum per pair, kFlight pieces at a time.
+//   kSplit = 1: block (unit, 32 dims), a warp per 8-pair group, each over all pieces
+//   kSplit = 8: block (unit, 32 dims, 8-pair group), the warps share the pieces and join
+//               through shared memory; for few units, which the most pieces come with
+template <int kSplit>
 __global__ void __launch_bounds__(kCombineThreads) full_combine_kernel(const Params p) {
-    __shared__ float w_s[kCombineWarps][kChunk][8];
+    constexpr int kGroups = kCombineWarps / kSplit;  // 8-pair groups of a block
+    static_assert(kSplit == 1 || kGroups == 1, "one group, or one warp per group");
+    __shared__ float w_s[kCombineWarps][kFlight][8];
     __shared__ __align__(16) float a_s[kCombineWarps][8];
-    __shared__ __align__(16) __nv_bfloat16 out_s[kHeadsPerCta][kDims];
+    __shared__ float m_s[kCombineWarps][8], sum_s[kCombineWarps][8];
+    __shared__ float o_s[kSplit > 1 ? kSplit : 1][8][kDims + 1];
+    __shared__ __align__(16) __nv_bfloat16 out_s[8 * kGroups][kDims];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int32_t unit = blockIdx.x;
+    const int group = kSplit > 1 ? blockIdx.z : warp;  // of 8 pairs
+    const int part = kSplit > 1 ? warp : 0;            // this warp's share of the pieces
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int32_t k = p.plan.unit_k[unit];
     if (k < 0) return;  // zeros already
     const PlanHead head = *p.plan.head;
     const int64_t begin = p.plan.start[k], end = p.plan.start[k + 1];
-    // The range holding tile x is the last one starting at or before it.
-    const int32_t c_lo = static_cast<int32_t>(((begin + 1) * head.ctas - 1) / head.tiles);
-    const int32_t c_hi = static_cast<int32_t>((end * head.ctas - 1) / head.tiles);
+    // The range holding tile x is the last one starting at or before it: floor(((x + 1)*ctas - 1) / T).
+    const int32_t c_lo = range_of(head, begin), c_hi = range_of(head, end - 1);
     if (c_lo == c_hi) return;  // written whole
     // Every range between holds this unit first, and so may the first one.
     const int32_t slot_lo = 2 * c_lo + (p.plan.cta_k[c_lo] == k ? 0 : 1);
     auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot_lo : 2 * (c_lo + i)); };
     const int pieces = c_hi - c_lo + 1;
-    const __half* po = reinterpret_cast<const __half*>(p.part_o);
+    const uint4* po = reinterpret_cast<const uint4*>(p.part_o) + (static_cast<int64_t>(blockIdx.y) * 8 + group) * kDims + lane;
+    constexpr int64_t kPartVecs = kHeadsPerCta * kLatent / 8;
     float acc[8] = {};
-    float m_run = kNegInf, s_run = 0.0f;  // lanes 0..7: head 8*warp + lane
-    for (int k0 = 0; k0 < pieces; k0 += kChunk) {
-        uint4 raw[kChunk];
+    float m_run = kNegInf, s_run = 0.0f;  // lanes 0..7: pair 8*group + lane
+    for (int k0 = part; k0 < pieces; k0 += kSplit * kFlight) {
+        uint4 raw[kFlight];
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
+        for (int i = 0; i < kFlight; ++i) {
             raw[i] = make_uint4(0, 0, 0, 0);
-            if (k0 + i < pieces)
-                raw[i] = *reinterpret_cast<const uint4*>(
-                    po + slot(k0 + i) * kHeadsPerCta * kLatent +
-                    ((static_cast<int64_t>(blockIdx.y) * kCombineWarps + warp) * kDims + lane) * 8);
+            if (k0 + i * kSplit < pieces) raw[i] = po[slot(k0 + i * kSplit) * kPartVecs];
         }
-        __syncwarp();  // the previous chunk's weights are read
+        __syncwarp();  // the previous turn's weights are read
         if (lane < 8) {
-            float lse[kChunk], top = m_run;
+            float lse[kFlight], top = m_run;
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                lse[i] = k0 + i < pieces ? p.part_lse[slot(k0 + i) * kHeadsPerCta + warp * 8 + lane] : kNegInf;
+            for (int i = 0; i < kFlight; ++i) {
+                lse[i] = k0 + i * kSplit < pieces ? p.part_lse[slot(k0 + i * kSplit) * kHeadsPerCta + group * 8 + lane] : kNegInf;
                 top = fmaxf(top, lse[i]);
             }
             const float a = m_run != kNegInf ? exp2f(m_run - top) : 0.0f;
             s_run *= a;
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
+            for (int i = 0; i < kFlight; ++i) {
                 const float w = lse[i] != kNegInf ? exp2f(lse[i] - top) : 0.0f;
                 s_run += w;
                 w_s[warp][i][lane] = w;
@@ -255,8 +272,7 @@ __global__ void __launch_bounds__(kCombineThreads) full_combine_kernel(const Par
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] *= a_s[warp][e];
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            if (k0 + i >= pieces) continue;
+        for (int i = 0; i < kFlight; ++i) {
             const __half2* hv = reinterpret_cast<const __half2*>(&raw[i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -266,16 +282,38 @@ __global__ void __launch_bounds__(kCombineThreads) full_combine_kernel(const Par
             }
         }
     }
-    __syncwarp();
-    if (lane < 8) a_s[warp][lane] = s_run == 0.0f ? 0.0f : p.v_scale / s_run;
-    __syncwarp();
+    if (lane < 8) {
+        m_s[warp][lane] = m_run;
+        sum_s[warp][lane] = s_run;
+    }
+    if constexpr (kSplit > 1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out_s[warp * 8 + e][lane] = __float2bfloat16_rn(acc[e] * a_s[warp][e]);
+        for (int e = 0; e < 8; ++e) o_s[part][e][lane] = acc[e];
+        __syncthreads();
+        // Warp w joins pair w over the parts.
+        float top = kNegInf, sum = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i) top = fmaxf(top, m_s[i][warp]);
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i) {
+            const float w = m_s[i][warp] != kNegInf ? exp2f(m_s[i][warp] - top) : 0.0f;
+            sum = fmaf(w, sum_s[i][warp], sum);
+            o = fmaf(w, o_s[i][warp][lane], o);
+        }
+        out_s[warp][lane] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : o * (p.v_scale / sum));
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float sum = sum_s[warp][e];
+            out_s[warp * 8 + e][lane] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[e] * (p.v_scale / sum));
+        }
+    }
     __syncthreads();
     const int32_t seq = unit / p.groups, first = (unit % p.groups) * kHeadsPerCta;
-    const int hl = t / 4, c = (t % 4) * 8;
-    if (hl < p.pairs - first)
-        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(seq) * p.pairs + first + hl) * kLatent + blockIdx.y * kDims + c) =
+    const int hl = t / 4, c = (t % 4) * 8, pair = first + (kSplit > 1 ? group * 8 : 0) + hl;
+    if (hl < 8 * kGroups && pair < p.pairs)
+        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(seq) * p.pairs + pair) * kLatent + blockIdx.y * kDims + c) =
             *reinterpret_cast<const uint4*>(&out_s[hl][c]);
 }
 
@@ -287,7 +325,9 @@ cudaError_t full_plan_setup() {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(full::full_prologue_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(full::full_combine_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    e = cudaFuncSetAttribute(full::full_combine_kernel<1>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(full::full_combine_kernel<8>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
 }
 
 cudaError_t launch_full_plan(const full::Params& p, cudaStream_t stream) {
@@ -297,7 +337,9 @@ cudaError_t launch_full_plan(const full::Params& p, cudaStream_t stream) {
 
 cudaError_t launch_full_combine(const full::Params& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.units, kLatent / full::kDims);
+    // With fewer units than an eighth of the CTAs a unit comes in more than eight pieces.
+    const bool split = p.units * 8 <= p.max_ctas;
+    cfg.gridDim = dim3(p.units, kLatent / full::kDims, split ? kHeadsPerCta / 8 : 1);
     cfg.blockDim = dim3(full::kCombineThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -305,7 +347,7 @@ cudaError_t launch_full_combine(const full::Params& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, full::full_combine_kernel, p);
+    return split ? cudaLaunchKernelEx(&cfg, full::full_combine_kernel<8>, p) : cudaLaunchKernelEx(&cfg, full::full_combine_kernel<1>, p);
 }
 
 }  // namespace dsa

@@ -7,9 +7,11 @@
 //
 // Page p of the cache holds block_size rows of 128 codes, then block_size float32 scales.
 //
-// Sixteen lanes take one row, eight consecutive dims (one 16-byte load) each: both sums of
-// the norm and the maximum stay in registers and four shuffles. HBM-bound: 264 bytes read
-// and 132 written a row.
+// Eight lanes take one row, sixteen consecutive dims each (the norm's sums and the maximum
+// are three shuffles), and persistent blocks keep the weights in registers, a row's loads in
+// flight while the one before is written. Instructions, not bytes, bound a first version with
+// sixteen lanes a row, 64-bit divisions of the slot and no reuse of the weights (262144 rows:
+// 41 us of 16 at the HBM's rate).
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -17,7 +19,9 @@ namespace dsa {
 namespace {
 
 constexpr int kIndexWriteThreads = 256;
-constexpr int kRowsPerBlock = kIndexWriteThreads / 16;
+constexpr int kLanes = 8;                  // of a row
+constexpr int kDims = kIndexDim / kLanes;  // of a lane: 16
+constexpr int kRowsPerBlock = kIndexWriteThreads / kLanes;
 
 __device__ __forceinline__ void unpack8(const uint4 v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -28,9 +32,9 @@ __device__ __forceinline__ void unpack8(const uint4 v, float* f) {
     }
 }
 
-__device__ __forceinline__ float sum16(float x) {
+__device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
@@ -41,54 +45,93 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+template <bool kNorm>
 __global__ void __launch_bounds__(kIndexWriteThreads) index_write_kernel(const IndexWriteParams p) {
-    const int sub = threadIdx.x & 15;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 4);
-    const bool in = row < p.rows;  // both half-warps stay for the shuffles
-    const long long slot = in ? p.slots[row] : -1;
-    float y[8] = {};
-    if (slot >= 0) unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + row * kIndexDim) + sub), y);
-    if (p.weight) {
-        float w[8], b[8] = {};
-        unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + sub), w);
-        if (p.bias) unpack8(__ldg(reinterpret_cast<const uint4*>(p.bias) + sub), b);
-        float s = 0.0f;
+    const int sub = threadIdx.x % kLanes;
+    float w[kDims], b[kDims];
+    if constexpr (kNorm) {
+        const uint4* ws = reinterpret_cast<const uint4*>(p.weight) + 2 * sub;
+        unpack8(__ldg(ws), w);
+        unpack8(__ldg(ws + 1), w + 8);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += y[k];
-        const float mean = sum16(s) * (1.0f / kIndexDim);
-        float ss = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            y[k] -= mean;
-            ss = fmaf(y[k], y[k], ss);
+        for (int k = 0; k < kDims; ++k) b[k] = 0.0f;
+        if (p.bias) {
+            const uint4* bs = reinterpret_cast<const uint4*>(p.bias) + 2 * sub;
+            unpack8(__ldg(bs), b);
+            unpack8(__ldg(bs + 1), b + 8);
         }
-        const float inv = 1.0f / sqrtf(sum16(ss) * (1.0f / kIndexDim) + p.eps);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = fmaf(y[k] * inv, w[k], b[k]);
     }
-    float top = 0x1p-100f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowsPerBlock;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + threadIdx.x / kLanes;
+    long long slot = -1;
+    uint4 raw[2] = {};
+    auto fetch = [&](int64_t r) {
+        slot = r < p.rows ? p.slots[r] : -1;
+        if (r < p.rows) {
+            const uint4* x = reinterpret_cast<const uint4*>(p.x + r * kIndexDim) + 2 * sub;
+            raw[0] = __ldg(x);
+            raw[1] = __ldg(x + 1);
+        }
+    };
+    fetch(row);
+    // The whole warp stays while any of its rows is left (the shuffles need it).
+    while (__any_sync(0xffffffffu, row < p.rows)) {
+        float y[kDims];
+        unpack8(raw[0], y);
+        unpack8(raw[1], y + 8);
+        const long long at = slot;
+        row += step;
+        fetch(row);
+        if constexpr (kNorm) {
+            float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max_nan(top, fabsf(y[k]));
+            for (int k = 0; k < kDims; ++k) s += y[k];
+            const float mean = row_sum(s) * (1.0f / kIndexDim);
+            float ss = 0.0f;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (slot < 0) return;
-    const float inv = 448.0f / top;
-    uint32_t c[2];
+            for (int k = 0; k < kDims; ++k) {
+                y[k] -= mean;
+                ss = fmaf(y[k], y[k], ss);
+            }
+            const float inv = rsqrtf(row_sum(ss) * (1.0f / kIndexDim) + p.eps);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        c[k] = f32x2_to_e4m3x2(y[4 * k] * inv, y[4 * k + 1] * inv) |
-               (f32x2_to_e4m3x2(y[4 * k + 2] * inv, y[4 * k + 3] * inv) << 16);
-    uint8_t* page = p.cache + (slot / p.block_size) * p.page_stride;
-    const int64_t off = slot % p.block_size;
-    reinterpret_cast<uint2*>(page + off * kIndexDim)[sub] = make_uint2(c[0], c[1]);
-    if (sub == 0) reinterpret_cast<float*>(page + static_cast<int64_t>(p.block_size) * kIndexDim)[off] = top / 448.0f;
+            for (int k = 0; k < kDims; ++k) y[k] = fmaf(y[k] * inv, w[k], b[k]);
+        }
+        float top = 0x1p-100f;
+#pragma unroll
+        for (int k = 0; k < kDims; ++k) top = max_nan(top, fabsf(y[k]));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float inv = 448.0f / top;
+        uint32_t c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            c[k] = f32x2_to_e4m3x2(y[4 * k] * inv, y[4 * k + 1] * inv) |
+                   (f32x2_to_e4m3x2(y[4 * k + 2] * inv, y[4 * k + 3] * inv) << 16);
+        if (at >= 0) {
+            int64_t page, off;
+            if (at >> 32 == 0) {  // a 64-bit division is a long sequence
+                const uint32_t u = static_cast<uint32_t>(at), bs = static_cast<uint32_t>(p.block_size), q = u / bs;
+                page = q;
+                off = u - q * bs;
+            } else {
+                page = at / p.block_size;
+                off = at % p.block_size;
+            }
+            uint8_t* dst = p.cache + page * p.page_stride;
+            reinterpret_cast<uint4*>(dst + off * kIndexDim)[sub] = make_uint4(c[0], c[1], c[2], c[3]);
+            if (sub == 0) reinterpret_cast<float*>(dst + static_cast<int64_t>(p.block_size) * kIndexDim)[off] = top / 448.0f;
+        }
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_index_write(const IndexWriteParams& p, cudaStream_t stream) {
-    const int64_t blocks = (static_cast<int64_t>(p.rows) + kRowsPerBlock - 1) / kRowsPerBlock;
-    index_write_kernel<<<static_cast<unsigned>(blocks), kIndexWriteThreads, 0, stream>>>(p);
+cudaError_t launch_index_write(const IndexWriteParams& p, int sms, cudaStream_t stream) {
+    const int64_t all = (static_cast<int64_t>(p.rows) + kRowsPerBlock - 1) / kRowsPerBlock;
+    const unsigned blocks = static_cast<unsigned>(all < 3 * sms ? all : 3 * sms);  // resident at once
+    if (p.weight) index_write_kernel<true><<<blocks, kIndexWriteThreads, 0, stream>>>(p);
+    else index_write_kernel<false><<<blocks, kIndexWriteThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -7,6 +7,10 @@
 //   table[s][have(s)+i] = free[g0(s)+i] (or -1 past the free list), g0 = exclusive sum of want - have
 //   row of token i of s: pos = base(s)+i, slot = table[s][pos/bs]*bs + pos%bs, len = pos+1
 //
+// Lengths and positions fit 32 bits (the table's room does), divisions are 32-bit, and a lane
+// works on four rows at once, 32 apart, so that their searches and page loads overlap and
+// their stores stay coalesced.
+//
 // One launch. Both prefix sums (tokens, pages) over the requests are made by every block for
 // itself in shared memory: 8 bytes a request, served by L2 after the first block, cost less
 // than a second launch. Rows and new table entries are then spread over all blocks. A packed
@@ -22,30 +26,36 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kTurns = 4;                    // rows that a lane works on at once
+constexpr int kRowsPerWarp = 32 * kTurns;
 
 __device__ __forceinline__ int32_t saturate(int64_t x) { return x > INT_MAX ? INT_MAX : static_cast<int32_t>(x); }
 
 // Token counts of a request as the plan uses them; `bad` when they had to be cut.
 struct Request {
-    int64_t base, fresh;   // cached and new tokens
-    int32_t have, want;    // pages before and after, at most the table's width
+    uint32_t base, fresh;  // cached and new tokens
+    uint32_t have, want;   // pages before and after, at most the table's width
     bool bad;
 };
+__device__ __forceinline__ uint32_t pages_of(const PlanParams& p, uint32_t tokens) {
+    const uint32_t bs = static_cast<uint32_t>(p.block_size);
+    const uint32_t q = tokens / bs;
+    return min(q + (tokens != q * bs ? 1u : 0u), static_cast<uint32_t>(p.max_blocks));
+}
 __device__ __forceinline__ Request request(const PlanParams& p, int32_t s) {
     Request r;
     const int32_t b = p.base_lens[s], n = p.new_lens[s];
     r.base = b < 0 ? 0 : b;
     r.fresh = n < 0 ? 0 : n;
     r.bad = b < 0 || n < 0;
-    if (p.rows_per_seq > 0 && r.fresh > p.rows_per_seq) {
+    if (p.rows_per_seq > 0 && r.fresh > static_cast<uint32_t>(p.rows_per_seq)) {
         r.fresh = p.rows_per_seq;
         r.bad = true;
     }
-    const int64_t have = (r.base + p.block_size - 1) / p.block_size;
-    const int64_t want = (r.base + r.fresh + p.block_size - 1) / p.block_size;
-    r.bad |= want > p.max_blocks;
-    r.have = static_cast<int32_t>(have < p.max_blocks ? have : p.max_blocks);
-    r.want = static_cast<int32_t>(want < p.max_blocks ? want : p.max_blocks);
+    const uint32_t all = r.base + r.fresh;  // below 2^32
+    r.bad |= all > static_cast<uint32_t>(p.max_blocks) * static_cast<uint32_t>(p.block_size);
+    r.have = pages_of(p, r.base);
+    r.want = pages_of(p, all);
     return r;
 }
 
@@ -105,8 +115,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         cp += r.want - r.have;
         bad |= r.bad;
         // The page that the first new token shares with cached ones has to be there already.
-        if (blockIdx.x == 0 && r.fresh > 0 && r.base % p.block_size != 0 && r.base / p.block_size < p.max_blocks)
-            bad |= p.tables[static_cast<int64_t>(s) * p.max_blocks + r.base / p.block_size] < 0;
+        if (blockIdx.x == 0 && r.fresh > 0) {
+            const uint32_t blk = r.base / static_cast<uint32_t>(p.block_size);
+            if (blk < r.have) bad |= p.tables[static_cast<int64_t>(s) * p.max_blocks + blk] < 0;
+        }
     }
     if (hi == n && (lo < n || (n == 0 && tid == 0))) {  // the last thread with a request; no request: thread 0
         t0[n] = saturate(ct);
@@ -123,41 +135,57 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
 
     const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
-    for (int64_t e = first; e < all_pages; e += step) {
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; e < all_pages; e += step) {
         const int32_t s = last_at_most(g0, n, static_cast<int32_t>(e));
         const int64_t have = request(p, s).have;
         p.tables[static_cast<int64_t>(s) * p.max_blocks + have + (e - g0[s])] = e < p.num_free ? p.free_pages[e] : -1;
     }
-    for (int64_t row = first; row < p.rows; row += step) {
-        int32_t s = -1;
-        int64_t i = 0;
-        if (p.rows_per_seq > 0) {
-            s = static_cast<int32_t>(row / p.rows_per_seq);
-            i = row % p.rows_per_seq;
-        } else if (row < all_tokens) {
-            s = last_at_most(t0, n, static_cast<int32_t>(row));
-            i = row - t0[s];
-        }
-        int64_t slot = -1, pos = -1;
-        if (s >= 0) {
-            const Request r = request(p, s);
-            pos = r.base + i;
-            const int64_t blk = pos / p.block_size;
-            if (i >= r.fresh || blk >= p.max_blocks) {
-                s = -1;
-                pos = -1;
-            } else {
-                const int64_t g = g0[s] + blk - r.have;
-                const int32_t page = blk < r.have ? p.tables[static_cast<int64_t>(s) * p.max_blocks + blk]
-                                                  : (g < p.num_free ? p.free_pages[g] : -1);
-                if (page >= 0) slot = static_cast<int64_t>(page) * p.block_size + pos % p.block_size;
+    const uint32_t bs = static_cast<uint32_t>(p.block_size);
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kPlanWarps;
+    for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kPlanWarps + warp) * kRowsPerWarp; r0 < p.rows; r0 += warps * kRowsPerWarp) {
+        int32_t seq[kTurns];
+        uint32_t pos[kTurns], off[kTurns];
+        int32_t page[kTurns];
+#pragma unroll
+        for (int j = 0; j < kTurns; ++j) {
+            const int64_t row = r0 + 32 * j + lane;
+            int32_t s = -1;
+            uint32_t i = 0;
+            if (row < p.rows) {
+                if (p.rows_per_seq > 0) {
+                    s = static_cast<int32_t>(row) / p.rows_per_seq;
+                    i = static_cast<uint32_t>(static_cast<int32_t>(row) - s * p.rows_per_seq);
+                } else if (row < all_tokens) {
+                    s = last_at_most(t0, n, static_cast<int32_t>(row));
+                    i = static_cast<uint32_t>(static_cast<int32_t>(row) - t0[s]);
+                }
+            }
+            seq[j] = -1;
+            pos[j] = 0xFFFFFFFFu;
+            off[j] = 0;
+            page[j] = -1;
+            if (s >= 0) {
+                const Request r = request(p, s);
+                const uint32_t at = r.base + i, blk = at / bs;
+                if (i < r.fresh && blk < static_cast<uint32_t>(p.max_blocks)) {
+                    seq[j] = s;
+                    pos[j] = at;
+                    off[j] = at - blk * bs;
+                    const int64_t g = static_cast<int64_t>(g0[s]) + blk - r.have;
+                    if (blk < r.have) page[j] = p.tables[static_cast<int64_t>(s) * p.max_blocks + blk];
+                    else if (g < p.num_free) page[j] = p.free_pages[g];
+                }
             }
         }
-        p.slots[row] = slot;
-        p.positions[row] = static_cast<int32_t>(pos);
-        p.row_lens[row] = static_cast<int32_t>(pos + 1);
-        p.row_seqs[row] = s;
+#pragma unroll
+        for (int j = 0; j < kTurns; ++j) {
+            const int64_t row = r0 + 32 * j + lane;
+            if (row >= p.rows) continue;
+            p.slots[row] = page[j] >= 0 ? static_cast<int64_t>(page[j]) * p.block_size + off[j] : -1;
+            p.positions[row] = static_cast<int32_t>(pos[j]);
+            p.row_lens[row] = static_cast<int32_t>(pos[j] + 1u);
+            p.row_seqs[row] = seq[j];
+        }
     }
 }
 
@@ -169,9 +197,11 @@ cudaError_t plan_kernel_setup() {
 }
 
 cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream) {
-    // Four rows a thread before another block is worth its own prefix sums.
-    const int64_t want = (static_cast<int64_t>(p.rows) + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-    const int blocks = static_cast<int>(want < 1 ? 1 : (want > 2 * sms ? 2 * sms : want));
+    // Four rows a thread before another block is worth its own prefix sums, and no more blocks
+    // than run at once.
+    const int64_t want = (static_cast<int64_t>(p.rows) + kTurns * kPlanThreads - 1) / (kTurns * kPlanThreads);
+    const int most = (p.num_seqs <= 4096 ? 4 : 1) * sms;
+    const int blocks = static_cast<int>(want < 1 ? 1 : (want > most ? most : want));
     plan_kernel<<<blocks, kPlanThreads, 2 * (p.num_seqs + 1) * 4, stream>>>(p);
     return cudaGetLastError();
 }

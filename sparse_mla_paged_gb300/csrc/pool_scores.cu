@@ -19,9 +19,15 @@
 // persistent block (scores of different tokens are independent: nothing to join). Each block
 // sums the units' tiles for itself, 4 bytes a row from L2, which costs less than a launch or
 // a workspace for a plan. Warps of a block: epilogue (four per 128 tokens, TMEM lane quarters;
-// they also write the queries' operand of each unit), one that issues the MMAs, four that copy
-// 16-byte pieces of key rows into a ring of tiles in the 128-byte-swizzled operand layout and
-// run ahead over units.
+// they also write the queries' operand of each unit), one that issues the MMAs, two that load
+// key tiles into a ring in the 128-byte-swizzled operand layout and run ahead over units: one
+// of them with tensor-map boxes of a page's rows when pages, pools and tiles fit each other,
+// else both with 16-byte copies.
+//
+// Shared memory's bandwidth is what the tile loop competes for (a tile is written once and
+// read twice, by the hi and the lo product, with the queries each time): the weights therefore
+// stay in registers, a warp's columns being the same in every tile. Read from shared memory
+// for every tile they cost as much of it as the MMAs (pooled 128k 413 us, prefill 588).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -31,24 +37,30 @@ namespace dsa {
 namespace {
 
 constexpr int kTile = 128;                       // tokens of a tile: MMA M
-constexpr int kLoadWarps = 4;                    // 32 tokens of a tile each
+constexpr int kLoadWarps = 2;                    // copies: 64 tokens of a tile each
+constexpr int kLoadTurns = 2;                    // of 32 tokens
 constexpr int kTileBytes = kTile * kIndexDim;    // 16 KB of codes
 constexpr int kBarEpilogue = 1;
 constexpr int kFillPools = 4096;                 // pools of one piece of the fill with -inf
+constexpr int kChunk = 16;                       // columns of a tensor-memory load
 
 // Variants by the columns (rows x padded heads) that one unit's MMAs take: MMA N.
 template <int kCols>
 struct Shape {
-    static constexpr int kCtas = kCols <= 128 ? 2 : 1;                            // blocks per SM
-    static constexpr int kStages = kCols == 64 ? 5 : (kCols == 128 ? 4 : 8);
-    static constexpr int kEpiWarps = kCols <= 128 ? 4 : 8;
+    static constexpr int kCtas = kCols == 64 ? 2 : 1;  // blocks per SM
+    static constexpr int kStages = kCols == 64 ? 5 : 10;
+    static constexpr int kEpiWarps = kCols / 16;       // 64 columns, whose weights fit its registers, a warp
+    static constexpr int kSets = kEpiWarps / 4;        // warps that share a lane quarter
+    static constexpr int kWeights = kCols / kSets;     // columns of a warp: 64
+    static constexpr int kDBufs = 4;
     static constexpr int kMmaWarp = kEpiWarps;
     static constexpr int kLoadWarp0 = kMmaWarp + 1;
     static constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
     static constexpr int kMaxRows = kCols / 16;
-    // A scale slot is written again 2*kStages tiles later: by then the MMA of the tile kStages
-    // before it has run, hence the epilogue two tiles before that one has read its scales.
+    // A scale slot is written again kScaleSlots tiles later: by then the MMA kStages tiles before
+    // that has run, hence the epilogue kDBufs tiles before it has read its scales.
     static constexpr int kScaleSlots = 2 * kStages;
+    static_assert(kScaleSlots >= kStages + kDBufs, "scale slots");
     static constexpr int kOffQ = kStages * kTileBytes;                      // [2 terms][cols][128 codes]
     static constexpr int kOffScale = kOffQ + 2 * kCols * kIndexDim;         // float [slots][128]
     static constexpr int kOffW = kOffScale + kScaleSlots * kTile * 4;       // float [cols]
@@ -56,12 +68,12 @@ struct Shape {
     static constexpr int kOffVis = kOffToken + kMaxRows * kTile * 4;        // int32 [rows] visible pools of a row
     static constexpr int kOffScan = kOffVis + kMaxRows * 4;                 // int64 [16] warp sums, then what they find
     static constexpr int kOffBars = kOffScan + 20 * 8;
-    static constexpr int BAR_FULL = 0, BAR_EMPTY = kStages, BAR_DFULL = 2 * kStages, BAR_DEMPTY = BAR_DFULL + 2,
-                         BAR_QFULL = BAR_DEMPTY + 2, BAR_DRAIN = BAR_QFULL + 1, kNumBars = BAR_DRAIN + 1;
+    static constexpr int BAR_FULL = 0, BAR_EMPTY = kStages, BAR_DFULL = 2 * kStages, BAR_DEMPTY = BAR_DFULL + kDBufs,
+                         BAR_QFULL = BAR_DEMPTY + kDBufs, BAR_DRAIN = BAR_QFULL + 1, kNumBars = BAR_DRAIN + 1;
     static constexpr int kOffTmem = kOffBars + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmem + 4;
     static constexpr int kSmem = kOffAbort + 4 + 1024;                      // slack for the 1024-byte alignment
-    static constexpr uint32_t kTmemCols = 2 * kCols;                        // two D buffers
+    static constexpr uint32_t kTmemCols = kDBufs * kCols;
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kCtas * kTmemCols <= 512, "blocks per SM");
 };
 
@@ -73,16 +85,44 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-// acc += w * (max(x0, 0), max(x1, 0)), both halves in one instruction.
-__device__ __forceinline__ void fma_relu2(uint64_t& acc, uint64_t w, uint32_t x0, uint32_t x1) {
-    const uint32_t a = __float_as_uint(max_nan(__uint_as_float(x0), 0.0f));
-    const uint32_t b = __float_as_uint(max_nan(__uint_as_float(x1), 0.0f));
-    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%2, %3};\n\tfma.rn.f32x2 %0, x, %1, %0;\n\t}" : "+l"(acc) : "l"(w), "r"(a), "r"(b));
+// acc += w * (a, b), both halves in one instruction.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t w, float a, float b) {
+    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%2, %3};\n\tfma.rn.f32x2 %0, x, %1, %0;\n\t}" : "+l"(acc) : "l"(w), "f"(a), "f"(b));
+}
+// acc0 += w0 * relu(x0, x1), acc1 += w1/2 * 2 relu(x2, x3). One pair as max(x, 0) on the
+// integer/compare pipe (half rate), the other as x + |x| on the FMA pipe, since either alone
+// would be what the epilogue waits for; the second pair's weights are stored halved. Both
+// keep a NaN.
+__device__ __forceinline__ void fma_relu4(uint64_t& acc0, uint64_t& acc1, uint64_t w0, uint64_t half_w1, const uint32_t* x) {
+    fma2(acc0, w0, max_nan(__uint_as_float(x[0]), 0.0f), max_nan(__uint_as_float(x[1]), 0.0f));
+    const float x2 = __uint_as_float(x[2]), x3 = __uint_as_float(x[3]);
+    fma2(acc1, half_w1, x2 + fabsf(x2), x3 + fabsf(x3));
 }
 __device__ __forceinline__ float sum2(uint64_t a) {
     return __uint_as_float(static_cast<uint32_t>(a)) + __uint_as_float(static_cast<uint32_t>(a >> 32));
 }
 
+// Columns of a lane in two steps: the load, and the wait that makes its registers valid (they
+// are operands of the wait so that no use moves ahead of it).
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&v)[kChunk]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void wait_columns(uint32_t (&v)[kChunk]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :: "memory");
+}
+__device__ __forceinline__ void tma_box3(uint32_t dst, const void* tmap, int32_t y, int32_t z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst), "l"(tmap), "r"(0), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 // One unit as a block sees it.
 struct Unit {
     int32_t seq, row0, rows;  // rows [row0, row0 + rows) of sequence seq
@@ -252,64 +292,136 @@ __device__ void load_queries(const Block<kCols>& b, const Unit& x) {
                 *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
                 *reinterpret_cast<uint2*>(at + kCols * kIndexDim) = make_uint2(lo[0], lo[1]);
                 if (sub == 0)
-                    w_s[col] = broken ? __uint_as_float(0x7FC00000u)
-                                      : w[i] * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    w_s[col] = broken ? __uint_as_float(0x7FC00000u)  // halved in every second pair: fma_relu4
+                                      : w[i] * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (col & 2 ? 0.5f : 1.0f);
             }
         }
     }
 }
 
-// Copy warps: warp w takes tokens 32w .. 32w+31 of every tile; lane l resolves the page of
-// token 32w + l (a tile ahead of its copies) and copies its scale.
+// Load by tensor-map boxes (first load warp): lane l has box l of every tile, p.box_rows rows
+// of one page, its codes by the map and its scales by a plain bulk copy.
+template <int kCols>
+__device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
+    using S = Shape<kCols>;
+    const PoolScoresParams& p = b.p;
+    const int lane = threadIdx.x & 31;
+    const bool mine = lane * p.box_rows < kTile;
+    const uint32_t box_codes = static_cast<uint32_t>(p.box_rows) * kIndexDim, box_scales = static_cast<uint32_t>(p.box_rows) * 4u;
+    uint32_t tau = 0;
+    bool stop = false;
+    b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
+        const int32_t limit = x.seen * p.kpool;
+        const int32_t* table = p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq;
+        // This lane's page of tile t and the row its box starts at (asked for a tile ahead).
+        auto look = [&](int32_t t, int32_t* row, bool* live) -> int32_t {
+            const int32_t pos = t * kTile + lane * p.box_rows;
+            *live = mine && t < t1 && pos < limit;
+            if (!*live) return -1;
+            const int32_t blk = pos / p.block_size;
+            *row = pos - blk * p.block_size;
+            return p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq ? __ldg(table + blk) : -1;
+        };
+        int32_t row_next = 0;
+        bool live_next;
+        int32_t page_next = look(t0, &row_next, &live_next);
+        for (int32_t t = t0; t < t1 && !stop; ++t, ++tau) {
+            const int32_t page = page_next, row = row_next;
+            const bool live = live_next;
+            page_next = look(t + 1, &row_next, &live_next);
+            const int e = static_cast<int>(tau % S::kStages);
+            if (tau >= S::kStages) b.wait(S::BAR_EMPTY + e, (tau / S::kStages - 1) & 1);
+            // After a failed wait nothing more is issued (the drain below finds what is in flight).
+            if (__shfl_sync(0xffffffffu, *b.abort_flag, 0)) {
+                stop = true;
+                break;
+            }
+            float* scales = reinterpret_cast<float*>(b.smem + S::kOffScale) + (tau % S::kScaleSlots) * kTile + lane * p.box_rows;
+            const bool good = live && page >= 0;
+            if (live && !good) {  // tokens without a page score -inf
+                for (int i = 0; i < p.box_rows; ++i) scales[i] = kNegInf;
+                if (p.status) atomicCAS(p.status, 0, kStatusBounds);
+            }
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, good));
+            if (lane == 0) mbar_arrive_expect_tx(b.bar(S::BAR_FULL + e), boxes * (box_codes + box_scales));
+            __syncwarp();
+            if (good) {
+                tma_box3(b.sbase + e * kTileBytes + lane * box_codes, tmap, row, page, b.bar(S::BAR_FULL + e));
+                bulk_g2s(smem_u32(scales), p.cache + page * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + row * 4,
+                         box_scales, b.bar(S::BAR_FULL + e));
+            }
+            __syncwarp();
+        }
+    });
+    // No copy into shared memory is in flight when the block exits: the last tiles' bytes.
+    if (lane == 0) {
+        for (uint32_t i = tau > S::kStages ? tau - S::kStages : 0; i < tau; ++i) {
+            const uint64_t since = globaltimer_ns();
+            while (!mbar_try_wait(b.bar(S::BAR_FULL + static_cast<int>(i % S::kStages)), (i / S::kStages) & 1) &&
+                   globaltimer_ns() - since < kDrainLimitNs) {
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// Copy warps: warp w takes tokens 64w .. 64w+63 of every tile; lane l resolves the pages of
+// tokens 64w + l and 64w + 32 + l (a tile ahead of their copies) and copies their scales.
 template <int kCols>
 __device__ void run_load(const Block<kCols>& b) {
     using S = Shape<kCols>;
     const PoolScoresParams& p = b.p;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - S::kLoadWarp0;
     const int tokens = b.per_tile * p.kpool;
-    const int tk = 32 * w + lane;
+    const int tk0 = 64 * w + lane;
     constexpr int64_t kNone = -1, kBad = -2;
     uint32_t tau = 0;
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
-        const int64_t limit = static_cast<int64_t>(x.seen) * p.kpool;
+        const int32_t limit = x.seen * p.kpool;
         const int32_t* table = p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq;
-        // Page and row of this lane's token of tile t, as the byte offsets of its codes and scale.
-        auto resolve = [&](int32_t t, int64_t& code, int64_t& scale) {
-            code = scale = kNone;
-            const int64_t pos = static_cast<int64_t>(t) * tokens + tk;
+        // Byte offset of the codes of this lane's token of turn i, tile t, and the distance from
+        // there to its scale.
+        auto resolve = [&](int32_t t, int i, int64_t& code, int64_t& to_scale) {
+            code = kNone;
+            to_scale = 0;
+            const int tk = tk0 + 32 * i;
+            const int32_t pos = t * tokens + tk;
             if (t >= t1 || tk >= tokens || pos >= limit) return;
-            const int32_t blk = static_cast<int32_t>(pos) / p.block_size, off = static_cast<int32_t>(pos) - blk * p.block_size;
+            const int32_t blk = pos / p.block_size, off = pos - blk * p.block_size;
             const int32_t page = (p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq) ? __ldg(table + blk) : -1;
-            if (page < 0) {
-                code = kBad;
-                return;
-            }
-            const int64_t at = page * p.page_stride;
-            code = at + static_cast<int64_t>(off) * kIndexDim;
-            scale = at + static_cast<int64_t>(p.block_size) * kIndexDim + off * 4;
+            code = page < 0 ? kBad : page * p.page_stride + static_cast<int64_t>(off) * kIndexDim;
+            to_scale = static_cast<int64_t>(p.block_size) * kIndexDim - static_cast<int64_t>(off) * (kIndexDim - 4);
         };
-        int64_t code, scale, next_code, next_scale;
-        resolve(t0, next_code, next_scale);
+        int64_t code[kLoadTurns], next_code[kLoadTurns], to_scale[kLoadTurns], next_to[kLoadTurns];
+#pragma unroll
+        for (int i = 0; i < kLoadTurns; ++i) resolve(t0, i, next_code[i], next_to[i]);
         for (int32_t t = t0; t < t1; ++t, ++tau) {
-            code = next_code;
-            scale = next_scale;
-            resolve(t + 1, next_code, next_scale);
+#pragma unroll
+            for (int i = 0; i < kLoadTurns; ++i) {
+                code[i] = next_code[i];
+                to_scale[i] = next_to[i];
+                resolve(t + 1, i, next_code[i], next_to[i]);
+            }
             const int e = static_cast<int>(tau % S::kStages);
             if (tau >= S::kStages) b.wait(S::BAR_EMPTY + e, (tau / S::kStages - 1) & 1);
-            const uint32_t dst = b.sbase + e * kTileBytes;
+            const uint32_t dst = b.sbase + e * kTileBytes + 64 * w * kIndexDim;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = 4 * i + (lane >> 3), c = lane & 7;
-                const int64_t at = __shfl_sync(0xffffffffu, code, row);
-                const uint32_t d = (32 * w + row) * kIndexDim + ((c ^ (row & 7)) << 4);
-                cp_async_16_zfill(dst + d, p.cache + (at >= 0 ? at + c * 16 : 0), at >= 0 ? 16u : 0u);
-            }
-            float* slot = reinterpret_cast<float*>(b.smem + S::kOffScale) + (tau % S::kScaleSlots) * kTile + tk;
-            if (scale >= 0) {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot)), "l"(p.cache + scale) : "memory");
-            } else {
-                *slot = kNegInf;  // a token without a page scores -inf
-                if (code == kBad && p.status) atomicCAS(p.status, 0, kStatusBounds);
+            for (int i = 0; i < kLoadTurns; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = 4 * j + (lane >> 3), c = lane & 7;
+                    const int64_t at = __shfl_sync(0xffffffffu, code[i], row);
+                    const uint32_t d = (32 * i + row) * kIndexDim + ((c ^ (row & 7)) << 4);
+                    cp_async_16_zfill(dst + d, p.cache + (at >= 0 ? at + c * 16 : 0), at >= 0 ? 16u : 0u);
+                }
+                float* slot = reinterpret_cast<float*>(b.smem + S::kOffScale) + (tau % S::kScaleSlots) * kTile + tk0 + 32 * i;
+                if (code[i] >= 0) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot)),
+                                 "l"(p.cache + code[i] + to_scale[i]) : "memory");
+                } else {
+                    *slot = kNegInf;  // a token without a page scores -inf
+                    if (code[i] == kBad && p.status) atomicCAS(p.status, 0, kStatusBounds);
+                }
             }
             cp_async_arrive_noinc(b.bar(S::BAR_FULL + e));
             __syncwarp();
@@ -330,9 +442,9 @@ __device__ void run_mma(const Block<kCols>& b, uint32_t tmem) {
                                (static_cast<uint32_t>(x.rows * kHeads - 16) >> 3 << 17);  // N = rows x heads
         b.wait(S::BAR_QFULL, entered++ & 1);
         for (int32_t t = t0; t < t1; ++t, ++tau) {
-            const int e = static_cast<int>(tau % S::kStages), d = tau & 1;
+            const int e = static_cast<int>(tau % S::kStages), d = static_cast<int>(tau % S::kDBufs);
             b.wait(S::BAR_FULL + e, (tau / S::kStages) & 1);
-            if (tau >= 2) b.wait(S::BAR_DEMPTY + d, ((tau >> 1) - 1) & 1);
+            if (tau >= S::kDBufs) b.wait(S::BAR_DEMPTY + d, (tau / S::kDBufs - 1) & 1);
             fence_proxy_async_smem();
             tc_fence_after();
             const uint64_t k = smem_desc(b.sbase + e * kTileBytes, 16, 1024, kSwizzle128B);
@@ -361,7 +473,9 @@ template <int kHeads, int kCols>
 __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
     using S = Shape<kCols>;
     const PoolScoresParams& p = b.p;
-    constexpr int kSets = S::kEpiWarps / 4;  // warps that share a lane quarter, each with its share of the rows
+    constexpr bool kHalves = kHeads > S::kWeights;                // two warps have half of a row each
+    constexpr int kRows = kHalves ? 1 : S::kWeights / kHeads;     // rows of a warp
+    constexpr int kRowChunks = (kHalves ? S::kWeights : kHeads) / kChunk, kChunks = S::kWeights / kChunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tk = threadIdx.x & 127, set = threadIdx.x >> 7;
     const float* w_s = reinterpret_cast<const float*>(b.smem + S::kOffW);
     const float* scale_s = reinterpret_cast<const float*>(b.smem + S::kOffScale);
@@ -370,57 +484,77 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
     const bool in_lanes = p.kpool <= 32 && (p.kpool & (p.kpool - 1)) == 0;  // a pool's tokens in one warp
     const int pool_tk = tk / p.kpool;
     const bool writer = tk % p.kpool == 0;
-    constexpr int kChunk = kHeads < 32 ? kHeads : 32;
+    const int row_first = kHalves ? 0 : set * kRows;
     uint32_t tau = 0;
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
         // The unit before is done with: its last D buffer was full, so its MMAs have read the
-        // queries, and every epilogue warp is past its weights.
+        // queries, and every epilogue warp has its weights.
         named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
         load_queries<kHeads, kCols>(b, x);
         if (threadIdx.x < x.rows) vis_s[threadIdx.x] = b.visible(x.row0 + threadIdx.x);
         fence_proxy_async_smem();
         named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
         if (lane == 0) mbar_arrive(b.bar(S::BAR_QFULL));
-        const int r_lo = set * x.rows / kSets, r_hi = (set + 1) * x.rows / kSets;
+        const int mine = min(max(x.rows - row_first, 0), kRows);  // rows of this warp in the unit
+        uint64_t w[S::kWeights / 2];
+#pragma unroll
+        for (int i = 0; i < S::kWeights / 4; ++i) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(w_s + set * S::kWeights + 4 * i);
+            w[2 * i] = v.x;
+            w[2 * i + 1] = v.y;
+        }
         for (int32_t t = t0; t < t1; ++t, ++tau) {
-            const int d = tau & 1;
+            const int d = static_cast<int>(tau % S::kDBufs);
             const int32_t pool_t = t * b.per_tile;
-            b.wait(S::BAR_DFULL + d, (tau >> 1) & 1);
+            b.wait(S::BAR_DFULL + d, (tau / S::kDBufs) & 1);
             tc_fence_after();
             const float scale = scale_s[(tau % S::kScaleSlots) * kTile + tk];
-            for (int r = r_lo; r < r_hi; ++r) {
-                uint64_t acc[4] = {0, 0, 0, 0};
+            // Chunks of columns, the next one's load in flight while one is summed. The columns
+            // of rows that the unit lacks hold anything; their sums are not used.
+            const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + d * kCols + set * S::kWeights;
+            uint32_t v[2][kChunk];
+            float sums[kRows];
+            if (mine > 0) load_columns(base, v[0]);
 #pragma unroll
-                for (int c0 = 0; c0 < kHeads; c0 += kChunk) {
-                    uint32_t v[kChunk];
-                    const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + d * kCols + r * kHeads + c0;
-                    if constexpr (kChunk == 32) tmem_ld_x32(at, v); else tmem_ld_x16(at, v);
+            for (int r = 0; r < kRows; ++r) {
+                if (r < mine) {
+                    uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int c = 0; c < kChunk; c += 4) {
-                        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(w_s + r * kHeads + c0 + c);
-                        fma_relu2(acc[(c >> 1) & 3], w.x, v[c], v[c + 1]);
-                        fma_relu2(acc[((c >> 1) + 1) & 3], w.y, v[c + 2], v[c + 3]);
+                    for (int i = r * kRowChunks; i < (r + 1) * kRowChunks; ++i) {
+                        wait_columns(v[i & 1]);
+                        if (i + 1 < kChunks) load_columns(base + (i + 1) * kChunk, v[(i + 1) & 1]);
+#pragma unroll
+                        for (int c = 0; c < kChunk; c += 4)
+                            fma_relu4(acc[(c >> 1) & 3], acc[((c >> 1) + 1) & 3], w[(i * kChunk + c) / 2], w[(i * kChunk + c) / 2 + 1],
+                                      v[i & 1] + c);
                     }
+                    sums[r] = (sum2(acc[0]) + sum2(acc[1])) + (sum2(acc[2]) + sum2(acc[3]));
                 }
-                if (r == r_hi - 1) {  // the buffer's last values are in registers
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + d));
-                }
-                float s = ((sum2(acc[0]) + sum2(acc[1])) + (sum2(acc[2]) + sum2(acc[3]))) * scale;
-                if (scale == kNegInf) s = kNegInf;
+            }
+            if (mine < kRows && mine > 0) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");  // the load past the last row
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + d));
+            if constexpr (kHalves) {
+                // The second half's sums, double-buffered: written again two tiles on, past the next barrier.
+                float* half_s = token_s + (tau & 1) * kTile;
+                if (set == 1) half_s[tk] = sums[0];
+                named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
+                if (set == 0) sums[0] += half_s[tk];
+            }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (r >= mine || (kHalves && set == 1)) break;
+                float s = scale == kNegInf ? kNegInf : sums[r] * scale;
                 if (in_lanes) {
                     for (int o = 1; o < p.kpool; o <<= 1) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
                     const int32_t pool = pool_t + pool_tk;
                     if (writer && pool < p.n_pools)
-                        p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = pool < vis_s[r] ? s : kNegInf;
+                        p.scores[static_cast<int64_t>(x.row0 + row_first + r) * p.n_pools + pool] =
+                            pool < vis_s[row_first + r] ? s : kNegInf;
                 } else {
-                    token_s[r * kTile + tk] = s;
+                    token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = s;
                 }
-            }
-            if (r_lo == r_hi) {  // fewer rows than sets of warps
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + d));
             }
             if (!in_lanes) {
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
@@ -430,7 +564,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                     if (pool >= p.n_pools) continue;
                     float s = kNegInf;
                     if (pool < vis_s[r])
-                        for (int j = 0; j < p.kpool; ++j) s = max_nan(s, token_s[r * kTile + k * p.kpool + j]);
+                        for (int j = 0; j < p.kpool; ++j) s = max_nan(s, token_s[(kHalves ? 2 : r) * kTile + k * p.kpool + j]);
                     p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
                 }
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
@@ -453,7 +587,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
 
 template <int kHeads, int kCols>
 __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
-    pool_scores_kernel(const PoolScoresParams p, int32_t groups, int32_t group_rows) {
+    pool_scores_kernel(const PoolScoresParams p, const __grid_constant__ CUtensorMap tmap, int32_t groups, int32_t group_rows) {
     using S = Shape<kCols>;
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -465,10 +599,11 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
     b.per_tile = kTile / p.kpool;
     if (tid == 0) {
         for (int e = 0; e < S::kStages; ++e) {
-            mbar_init(b.bar(S::BAR_FULL + e), kLoadWarps * 33);  // 32 lanes' copies and a plain arrival per warp
+            // boxes: one arrival with the bytes to come; copies: every lane's, and a plain one per warp
+            mbar_init(b.bar(S::BAR_FULL + e), p.box_rows > 0 ? 1 : kLoadWarps * 33);
             mbar_init(b.bar(S::BAR_EMPTY + e), 1);
         }
-        for (int d = 0; d < 2; ++d) {
+        for (int d = 0; d < S::kDBufs; ++d) {
             mbar_init(b.bar(S::BAR_DFULL + d), 2);  // the MMAs' commit, and the MMA warp passing on the scales
             mbar_init(b.bar(S::BAR_DEMPTY + d), S::kEpiWarps);
         }
@@ -476,6 +611,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
         mbar_init(b.bar(S::BAR_DRAIN), 1);
         *b.abort_flag = 0;
         fence_mbar_init();
+        if (p.box_rows > 0) prefetch_tmap(&tmap);
     }
     if (warp == S::kMmaWarp) {
         tmem_alloc(b.sbase + S::kOffTmem, S::kTmemCols);
@@ -485,9 +621,13 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
     share(b);  // two block barriers
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kOffTmem);
-    if (warp < S::kEpiWarps) run_epilogue<kHeads, kCols>(b, tmem);
-    else if (warp == S::kMmaWarp) run_mma<kHeads, kCols>(b, tmem);
-    else run_load(b);
+    if (warp < S::kEpiWarps) {
+        run_epilogue<kHeads, kCols>(b, tmem);
+    } else {
+        if (warp == S::kMmaWarp) run_mma<kHeads, kCols>(b, tmem);
+        else if (p.box_rows > 0 && warp == S::kLoadWarp0) run_load_boxes(b, &tmap);
+        else if (p.box_rows == 0 && warp < S::kLoadWarp0 + kLoadWarps) run_load(b);
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == S::kMmaWarp) {
@@ -501,8 +641,7 @@ template <int kHeads, typename F>
 cudaError_t with_cols(int cols, F&& f) {
     if constexpr (kHeads <= 64)
         if (cols <= 64) return f(pool_scores_kernel<kHeads, 64>, Shape<64>{});
-    if (cols <= 128) return f(pool_scores_kernel<kHeads, 128>, Shape<128>{});
-    return f(pool_scores_kernel<kHeads, 256>, Shape<256>{});
+    return f(pool_scores_kernel<kHeads, 128>, Shape<128>{});
 }
 template <typename F>
 cudaError_t with_kernel(int padded, int cols, F&& f) {
@@ -518,9 +657,10 @@ cudaError_t with_kernel(int padded, int cols, F&& f) {
 
 cudaError_t pool_scores_kernel_setup() {
     for (int heads = 16; heads <= 128; heads *= 2)
-        for (int cols = heads < 64 ? 64 : heads; cols <= 256; cols *= 2) {
+        for (int cols = heads < 128 ? 64 : 128; cols <= 128; cols *= 2) {
             const cudaError_t e = with_kernel(heads, cols, [](auto* kernel, auto shape) {
-                cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shape.kSmem);
+                using S = decltype(shape);
+                const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
                 if (r != cudaSuccess) return r;
                 return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
             });
@@ -529,17 +669,18 @@ cudaError_t pool_scores_kernel_setup() {
     return cudaSuccess;
 }
 
-cudaError_t launch_pool_scores(const PoolScoresParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_pool_scores(const PoolScoresParams& p, const CUtensorMap& tmap, int sms, cudaStream_t stream) {
     // Heads are padded to 16, 32, 64 or 128 columns; a unit takes as many rows as its columns
-    // hold, and the columns follow from what rows there are: more rows read a key tile once
-    // and keep the tensor cores from waiting for shared memory (N = 64: 48 cycles per MMA
-    // where its arithmetic takes 32; 256: 128 of 128).
+    // hold, 128 when there are rows (or heads) enough: a key tile is then read from memory once
+    // for all of them, and an MMA of N = 128 takes 64 cycles, one of N = 64 48 of which its
+    // arithmetic fills 32.
     const int padded = p.heads <= 16 ? 16 : (p.heads <= 32 ? 32 : (p.heads <= 64 ? 64 : 128));
     const int64_t all = static_cast<int64_t>(p.rows_per_seq) * padded;
-    const int cols = all <= 64 && padded <= 64 ? 64 : (all <= 128 ? 128 : 256);
+    const int cols = all <= 64 ? 64 : 128;
     const int32_t group_rows = cols / padded, groups = (p.rows_per_seq + group_rows - 1) / group_rows;
     return with_kernel(padded, cols, [&](auto* kernel, auto shape) {
-        kernel<<<sms * shape.kCtas, shape.kThreads, shape.kSmem, stream>>>(p, groups, group_rows);
+        using S = decltype(shape);
+        kernel<<<sms * S::kCtas, S::kThreads, S::kSmem, stream>>>(p, tmap, groups, group_rows);
         return cudaGetLastError();
     });
 }
