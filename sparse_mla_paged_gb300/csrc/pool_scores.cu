@@ -20,9 +20,9 @@
 // sums the units' tiles for itself, 4 bytes a row from L2, which costs less than a launch or
 // a workspace for a plan. Warps of a block: epilogue (four per 128 tokens, TMEM lane quarters;
 // they also write the queries' operand of each unit), one that issues the MMAs, two that load
-// key tiles into a ring in the 128-byte-swizzled operand layout and run ahead over units: one
-// of them with tensor-map boxes of a page's rows when pages, pools and tiles fit each other,
-// else both with 16-byte copies.
+// key tiles into a ring in the 128-byte-swizzled operand layout and run ahead over units: with
+// tensor-map boxes of a page's rows when pages, pools and tiles fit each other, else
+// with 16-byte copies.
 //
 // Shared memory's bandwidth is what the tile loop competes for (a tile is written once and
 // read twice, by the hi and the lo product, with the queries each time): the weights therefore
@@ -59,7 +59,7 @@ struct Shape {
     static constexpr int kMaxRows = kCols / 16;
     // A scale slot is written again kScaleSlots tiles later: by then the MMA kStages tiles before
     // that has run, hence the epilogue kDBufs tiles before it has read its scales.
-    static constexpr int kScaleSlots = 2 * kStages;
+    static constexpr int kScaleSlots = 16;
     static_assert(kScaleSlots >= kStages + kDBufs, "scale slots");
     static constexpr int kOffQ = kStages * kTileBytes;                      // [2 terms][cols][128 codes]
     static constexpr int kOffScale = kOffQ + 2 * kCols * kIndexDim;         // float [slots][128]
@@ -299,13 +299,16 @@ __device__ void load_queries(const Block<kCols>& b, const Unit& x) {
     }
 }
 
-// Load by tensor-map boxes (first load warp): lane l has box l of every tile, p.box_rows rows
-// of one page, its codes by the map and its scales by a plain bulk copy.
+// Load by tensor-map boxes: load warp w takes every second tile from its w-th on; lane l looks
+// up the page of box l (p.box_rows rows of one page; two of its tiles ahead), then one lane
+// issues each box, its codes by the map and its scales by a plain bulk copy. (Issued by the
+// boxes' own lanes the copies are serialised at a higher cost.)
 template <int kCols>
 __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
     using S = Shape<kCols>;
     const PoolScoresParams& p = b.p;
     const int lane = threadIdx.x & 31;
+    const uint32_t w = (threadIdx.x >> 5) - S::kLoadWarp0;
     const bool mine = lane * p.box_rows < kTile;
     const uint32_t box_codes = static_cast<uint32_t>(p.box_rows) * kIndexDim, box_scales = static_cast<uint32_t>(p.box_rows) * 4u;
     uint32_t tau = 0;
@@ -313,52 +316,57 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
         const int32_t limit = x.seen * p.kpool;
         const int32_t* table = p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq;
-        // This lane's page of tile t and the row its box starts at (asked for a tile ahead).
-        auto look = [&](int32_t t, int32_t* row, bool* live) -> int32_t {
+        // This lane's page of tile t (-1: bad, -2: nothing that a row sees) and the row its box starts at.
+        auto look = [&](int32_t t, int32_t* row) -> int32_t {
             const int32_t pos = t * kTile + lane * p.box_rows;
-            *live = mine && t < t1 && pos < limit;
-            if (!*live) return -1;
+            *row = 0;
+            if (!mine || t >= t1 || pos >= limit) return -2;
             const int32_t blk = pos / p.block_size;
             *row = pos - blk * p.block_size;
-            return p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq ? __ldg(table + blk) : -1;
+            return p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq ? max(__ldg(table + blk), -1) : -1;
         };
-        int32_t row_next = 0;
-        bool live_next;
-        int32_t page_next = look(t0, &row_next, &live_next);
-        for (int32_t t = t0; t < t1 && !stop; ++t, ++tau) {
+        const int32_t own = t0 + static_cast<int32_t>((w - tau) & 1u);  // this warp's first tile here
+        int32_t row_next, page_next = look(own, &row_next);
+        for (int32_t t = own; t < t1 && !stop; t += 2) {
+            const uint32_t ta = tau + static_cast<uint32_t>(t - t0);
             const int32_t page = page_next, row = row_next;
-            const bool live = live_next;
-            page_next = look(t + 1, &row_next, &live_next);
-            const int e = static_cast<int>(tau % S::kStages);
-            if (tau >= S::kStages) b.wait(S::BAR_EMPTY + e, (tau / S::kStages - 1) & 1);
+            page_next = look(t + 2, &row_next);
+            const uint32_t e = ta % S::kStages;
+            if (ta >= S::kStages) b.wait(S::BAR_EMPTY + e, (ta / S::kStages - 1) & 1);
             // After a failed wait nothing more is issued (the drain below finds what is in flight).
             if (__shfl_sync(0xffffffffu, *b.abort_flag, 0)) {
                 stop = true;
                 break;
             }
-            float* scales = reinterpret_cast<float*>(b.smem + S::kOffScale) + (tau % S::kScaleSlots) * kTile + lane * p.box_rows;
-            const bool good = live && page >= 0;
-            if (live && !good) {  // tokens without a page score -inf
-                for (int i = 0; i < p.box_rows; ++i) scales[i] = kNegInf;
+            float* scales = reinterpret_cast<float*>(b.smem + S::kOffScale) + (ta % S::kScaleSlots) * kTile;
+            if (page == -1) {  // tokens without a page score -inf
+                for (int i = 0; i < p.box_rows; ++i) scales[lane * p.box_rows + i] = kNegInf;
                 if (p.status) atomicCAS(p.status, 0, kStatusBounds);
             }
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, good));
-            if (lane == 0) mbar_arrive_expect_tx(b.bar(S::BAR_FULL + e), boxes * (box_codes + box_scales));
-            __syncwarp();
-            if (good) {
-                tma_box3(b.sbase + e * kTileBytes + lane * box_codes, tmap, row, page, b.bar(S::BAR_FULL + e));
-                bulk_g2s(smem_u32(scales), p.cache + page * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + row * 4,
-                         box_scales, b.bar(S::BAR_FULL + e));
+            uint32_t boxes = __ballot_sync(0xffffffffu, page >= 0);
+            const uint32_t full = b.bar(S::BAR_FULL + e);
+            if (lane == 0) mbar_arrive_expect_tx(full, __popc(boxes) * (box_codes + box_scales));
+            for (; boxes != 0u; boxes &= boxes - 1u) {
+                const int box = __ffs(boxes) - 1;
+                const int32_t pg = __shfl_sync(0xffffffffu, page, box), rw = __shfl_sync(0xffffffffu, row, box);
+                if (lane == 0) {
+                    tma_box3(b.sbase + e * kTileBytes + box * box_codes, tmap, rw, pg, full);
+                    bulk_g2s(smem_u32(scales) + box * box_scales,
+                             p.cache + pg * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + rw * 4, box_scales, full);
+                }
             }
             __syncwarp();
         }
+        tau += static_cast<uint32_t>(t1 - t0);
     });
-    // No copy into shared memory is in flight when the block exits: the last tiles' bytes.
+    // No copy into shared memory is in flight when the block exits: the last tiles' bytes (after
+    // an abort some of them were never asked for: their waits end at the limit).
     if (lane == 0) {
         for (uint32_t i = tau > S::kStages ? tau - S::kStages : 0; i < tau; ++i) {
+            if ((i & 1u) != w) continue;
             const uint64_t since = globaltimer_ns();
             while (!mbar_try_wait(b.bar(S::BAR_FULL + static_cast<int>(i % S::kStages)), (i / S::kStages) & 1) &&
-                   globaltimer_ns() - since < kDrainLimitNs) {
+                   globaltimer_ns() - since < (stop ? kDrainLimitNs / S::kStages : kDrainLimitNs)) {
             }
         }
     }
@@ -496,6 +504,10 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
         if (lane == 0) mbar_arrive(b.bar(S::BAR_QFULL));
         const int mine = min(max(x.rows - row_first, 0), kRows);  // rows of this warp in the unit
+        float* out = p.scores + static_cast<int64_t>(x.row0 + row_first) * p.n_pools;
+        int32_t vis[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) vis[r] = r < mine ? vis_s[row_first + r] : 0;
         uint64_t w[S::kWeights / 2];
 #pragma unroll
         for (int i = 0; i < S::kWeights / 4; ++i) {
@@ -547,11 +559,11 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                 if (r >= mine || (kHalves && set == 1)) break;
                 float s = scale == kNegInf ? kNegInf : sums[r] * scale;
                 if (in_lanes) {
-                    for (int o = 1; o < p.kpool; o <<= 1) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1)
+                        if (p.kpool > o) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
                     const int32_t pool = pool_t + pool_tk;
-                    if (writer && pool < p.n_pools)
-                        p.scores[static_cast<int64_t>(x.row0 + row_first + r) * p.n_pools + pool] =
-                            pool < vis_s[row_first + r] ? s : kNegInf;
+                    if (writer && pool < p.n_pools) out[static_cast<int64_t>(r) * p.n_pools + pool] = pool < vis[r] ? s : kNegInf;
                 } else {
                     token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = s;
                 }
@@ -625,8 +637,8 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
         run_epilogue<kHeads, kCols>(b, tmem);
     } else {
         if (warp == S::kMmaWarp) run_mma<kHeads, kCols>(b, tmem);
-        else if (p.box_rows > 0 && warp == S::kLoadWarp0) run_load_boxes(b, &tmap);
-        else if (p.box_rows == 0 && warp < S::kLoadWarp0 + kLoadWarps) run_load(b);
+        else if (p.box_rows > 0) run_load_boxes(b, &tmap);
+        else run_load(b);
     }
     tc_fence_before();
     __syncthreads();
