@@ -85,21 +85,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-// acc += w * (a, b), both halves in one instruction.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t w, float a, float b) {
-    asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%2, %3};\n\tfma.rn.f32x2 %0, x, %1, %0;\n\t}" : "+l"(acc) : "l"(w), "f"(a), "f"(b));
-}
-// acc0 += w0 * relu(x0, x1), acc1 += w1/2 * 2 relu(x2, x3). One pair as max(x, 0) on the
-// integer/compare pipe (half rate), the other as x + |x| on the FMA pipe, since either alone
-// would be what the epilogue waits for; the second pair's weights are stored halved. Both
-// keep a NaN.
-__device__ __forceinline__ void fma_relu4(uint64_t& acc0, uint64_t& acc1, uint64_t w0, uint64_t half_w1, const uint32_t* x) {
-    fma2(acc0, w0, max_nan(__uint_as_float(x[0]), 0.0f), max_nan(__uint_as_float(x[1]), 0.0f));
+// acc[k] += w[k] * relu(x[k]) of four columns. Two as max(x, 0) on the compare pipe (half
+// rate), two as x + |x| on the FMA pipe, so that neither is what the epilogue waits for; the
+// weights of the latter are stored halved. Both keep a NaN. (Packed two-wide FMAs need moves
+// to pair their operands up and come to more instructions.)
+__device__ __forceinline__ void fma_relu4(float (&acc)[4], const float* w, const uint32_t* x) {
     const float x2 = __uint_as_float(x[2]), x3 = __uint_as_float(x[3]);
-    fma2(acc1, half_w1, x2 + fabsf(x2), x3 + fabsf(x3));
-}
-__device__ __forceinline__ float sum2(uint64_t a) {
-    return __uint_as_float(static_cast<uint32_t>(a)) + __uint_as_float(static_cast<uint32_t>(a >> 32));
+    acc[0] = fmaf(w[0], max_nan(__uint_as_float(x[0]), 0.0f), acc[0]);
+    acc[1] = fmaf(w[1], max_nan(__uint_as_float(x[1]), 0.0f), acc[1]);
+    acc[2] = fmaf(w[2], x2 + fabsf(x2), acc[2]);
+    acc[3] = fmaf(w[3], x3 + fabsf(x3), acc[3]);
 }
 
 // Columns of a lane in two steps: the load, and the wait that makes its registers valid (they
@@ -508,13 +503,9 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         int32_t vis[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) vis[r] = r < mine ? vis_s[row_first + r] : 0;
-        uint64_t w[S::kWeights / 2];
+        float w[S::kWeights];
 #pragma unroll
-        for (int i = 0; i < S::kWeights / 4; ++i) {
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(w_s + set * S::kWeights + 4 * i);
-            w[2 * i] = v.x;
-            w[2 * i + 1] = v.y;
-        }
+        for (int i = 0; i < S::kWeights; ++i) w[i] = w_s[set * S::kWeights + i];
         for (int32_t t = t0; t < t1; ++t, ++tau) {
             const int d = static_cast<int>(tau % S::kDBufs);
             const int32_t pool_t = t * b.per_tile;
@@ -530,17 +521,15 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 if (r < mine) {
-                    uint64_t acc[4] = {0, 0, 0, 0};
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int i = r * kRowChunks; i < (r + 1) * kRowChunks; ++i) {
                         wait_columns(v[i & 1]);
                         if (i + 1 < kChunks) load_columns(base + (i + 1) * kChunk, v[(i + 1) & 1]);
 #pragma unroll
-                        for (int c = 0; c < kChunk; c += 4)
-                            fma_relu4(acc[(c >> 1) & 3], acc[((c >> 1) + 1) & 3], w[(i * kChunk + c) / 2], w[(i * kChunk + c) / 2 + 1],
-                                      v[i & 1] + c);
+                        for (int c = 0; c < kChunk; c += 4) fma_relu4(acc, w + i * kChunk + c, v[i & 1] + c);
                     }
-                    sums[r] = (sum2(acc[0]) + sum2(acc[1])) + (sum2(acc[2]) + sum2(acc[3]));
+                    sums[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
                 }
             }
             if (mine < kRows && mine > 0) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");  // the load past the last row
