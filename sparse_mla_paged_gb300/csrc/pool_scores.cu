@@ -97,6 +97,22 @@ __device__ __forceinline__ void fma_relu4(float (&acc)[4], const float* w, const
     acc[3] = fmaf(w[3], x3 + fabsf(x3), acc[3]);
 }
 
+// Maximum over the kpool (1, 2, 4, .., 32) neighbouring lanes of a pool, in every first one.
+__device__ __forceinline__ float pool_max(float s, int32_t kpool) {
+    auto step = [&](int o) { s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o)); };
+    if (kpool == 1) return s;
+    step(1);
+    if (kpool == 2) return s;
+    step(2);
+    if (kpool == 4) return s;
+    step(4);
+    if (kpool == 8) return s;
+    step(8);
+    if (kpool == 16) return s;
+    step(16);
+    return s;
+}
+
 // Columns of a lane in two steps: the load, and the wait that makes its registers valid (they
 // are operands of the wait so that no use moves ahead of it).
 __device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&v)[kChunk]) {
@@ -499,10 +515,13 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
         if (lane == 0) mbar_arrive(b.bar(S::BAR_QFULL));
         const int mine = min(max(x.rows - row_first, 0), kRows);  // rows of this warp in the unit
-        float* out = p.scores + static_cast<int64_t>(x.row0 + row_first) * p.n_pools;
+        // This lane's pool of the tile at pool p is out[p], there for p < room and seen by row r
+        // for p < vis[r].
+        float* out = p.scores + static_cast<int64_t>(x.row0 + row_first) * p.n_pools + pool_tk;
+        const int32_t room = writer ? p.n_pools - pool_tk : 0;
         int32_t vis[kRows];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) vis[r] = r < mine ? vis_s[row_first + r] : 0;
+        for (int r = 0; r < kRows; ++r) vis[r] = r < mine ? vis_s[row_first + r] - pool_tk : 0;
         float w[S::kWeights];
 #pragma unroll
         for (int i = 0; i < S::kWeights; ++i) w[i] = w_s[set * S::kWeights + i];
@@ -548,11 +567,8 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                 if (r >= mine || (kHalves && set == 1)) break;
                 float s = scale == kNegInf ? kNegInf : sums[r] * scale;
                 if (in_lanes) {
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1)
-                        if (p.kpool > o) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
-                    const int32_t pool = pool_t + pool_tk;
-                    if (writer && pool < p.n_pools) out[static_cast<int64_t>(r) * p.n_pools + pool] = pool < vis[r] ? s : kNegInf;
+                    s = pool_max(s, p.kpool);
+                    if (pool_t < room) out[static_cast<int64_t>(r) * p.n_pools + pool_t] = pool_t < vis[r] ? s : kNegInf;
                 } else {
                     token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = s;
                 }

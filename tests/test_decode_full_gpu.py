@@ -83,6 +83,14 @@ def test_full(api, n, rps, heads, lens, bs):
     Case(n, rps, heads, lens, bs).check(api)
 
 
+@pytest.mark.parametrize("n,rps,heads,lens,bs,two", [
+    (2, 1, 64, [130001, 90000], 64, False), (1, 1, 128, [120000], 128, False), (40, 1, 16, [9000, 300, 5000, 1, 0], 64, False),
+    (1, 2, 8, [150000, 149000], 48, False), (3, 1, 40, [20000, 40000, 127], 32, True)])
+def test_long_rows(api, n, rps, heads, lens, bs, two):
+    """Rows long enough that every CTA runs many tiles through its ring, over several units."""
+    Case(n, rps, heads, lens, bs, two=two).check(api)
+
+
 @pytest.mark.parametrize("n,rps,heads,base,bs", [
     (2, 4, 16, [700, 126], 64), (3, 4, 64, [0, 63, 500], 64), (1, 2, 128, [255], 64), (2, 3, 20, [1000, 62], 48), (4, 5, 8, [0], 64)])
 def test_verify_rows(api, n, rps, heads, base, bs):

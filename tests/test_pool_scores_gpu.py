@@ -84,6 +84,15 @@ def test_scores(api, n, rps, heads, q_pos, bs, kpool):
     Case(n, rps, heads, q_pos, bs, kpool).check(api)
 
 
+@pytest.mark.parametrize("n,rps,heads,q_pos,bs,kpool", [
+    (3, 1, 64, [299999, 150001, 200000], 64, 4), (1, 2, 64, [400000, 399999], 128, 4), (1, 3, 24, [200001], 32, 2),
+    (1, 1, 128, [260000], 64, 1), (2, 1, 32, [150000, 300001], 48, 3), (1, 2, 100, [260000, 80000], 64, 5),
+    (40, 1, 16, [30000, 7000, 1], 64, 8)])
+def test_long_rows(api, n, rps, heads, q_pos, bs, kpool):
+    """Rows long enough that every block runs many tiles through its ring, over several units."""
+    Case(n, rps, heads, q_pos, bs, kpool).check(api)
+
+
 @pytest.mark.parametrize("heads,kpool", [(64, 4), (20, 3), (128, 1)])
 def test_whole_numbers_are_exact(api, heads, kpool):
     Case(3, 2, heads, [700, 701, 10, 11, 1500, 1501], kpool=kpool, whole=True).check(api, exact=True)
