@@ -19,7 +19,7 @@
 // persistent block (scores of different tokens are independent: nothing to join). Each block
 // sums the units' tiles for itself, 4 bytes a row from L2, which costs less than a launch or
 // a workspace for a plan. Warps of a block: epilogue (four per 128 tokens, TMEM lane quarters;
-// they also write the queries' operand of each unit), one that issues the MMAs, two that load
+// they also write the queries' operand of each unit), one or two that issue the MMAs, two that load
 // key tiles into a ring in the 128-byte-swizzled operand layout and run ahead over units: with
 // tensor-map boxes of a page's rows when pages, pools and tiles fit each other, else
 // with 16-byte copies.
@@ -53,8 +53,13 @@ struct Shape {
     static constexpr int kSets = kEpiWarps / 4;        // warps that share a lane quarter
     static constexpr int kWeights = kCols / kSets;     // columns of a warp: 64
     static constexpr int kDBufs = 4;
-    static constexpr int kMmaWarp = kEpiWarps;
-    static constexpr int kLoadWarp0 = kMmaWarp + 1;
+    // MMA warps, and load warps of boxes, that take tiles in turn. Each has to meet every phase of
+    // its barriers (a wait for a phase that has not begun passes as the one before it), so the
+    // ring and the D buffers are a multiple of them: a slot is always the same warp's.
+    static constexpr int kMmaWarps = kCols == 64 ? 1 : 2;
+    static_assert(kStages % kMmaWarps == 0 && kDBufs % kMmaWarps == 0, "slots belong to warps");
+    static constexpr int kMmaWarp0 = kEpiWarps;
+    static constexpr int kLoadWarp0 = kMmaWarp0 + kMmaWarps;
     static constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
     static constexpr int kMaxRows = kCols / 16;
     // A scale slot is written again kScaleSlots tiles later: by then the MMA kStages tiles before
@@ -69,7 +74,7 @@ struct Shape {
     static constexpr int kOffScan = kOffVis + kMaxRows * 4;                 // int64 [16] warp sums, then what they find
     static constexpr int kOffBars = kOffScan + 20 * 8;
     static constexpr int BAR_FULL = 0, BAR_EMPTY = kStages, BAR_DFULL = 2 * kStages, BAR_DEMPTY = BAR_DFULL + kDBufs,
-                         BAR_QFULL = BAR_DEMPTY + kDBufs, BAR_DRAIN = BAR_QFULL + 1, kNumBars = BAR_DRAIN + 1;
+                         BAR_QFULL = BAR_DEMPTY + kDBufs, BAR_QSEEN = BAR_QFULL + 1, BAR_DRAIN = BAR_QSEEN + 1, kNumBars = BAR_DRAIN + 1;
     static constexpr int kOffTmem = kOffBars + kNumBars * 8;
     static constexpr int kOffAbort = kOffTmem + 4;
     static constexpr int kSmem = kOffAbort + 4 + 1024;                      // slack for the 1024-byte alignment
@@ -310,10 +315,10 @@ __device__ void load_queries(const Block<kCols>& b, const Unit& x) {
     }
 }
 
-// Load by tensor-map boxes: load warp w takes every second tile from its w-th on; lane l looks
-// up the page of box l (p.box_rows rows of one page; two of its tiles ahead), then one lane
-// issues each box, its codes by the map and its scales by a plain bulk copy. (Issued by the
-// boxes' own lanes the copies are serialised at a higher cost.)
+// Load by tensor-map boxes: load warp w takes every kMmaWarps-th tile from its w-th on; lane l
+// has box l, p.box_rows rows of one page (looked up a tile of its own ahead): the codes by the
+// map, the scales by a plain bulk copy. (One lane issuing all boxes in turn was slower: pooled
+// 128k 414 us.)
 template <int kCols>
 __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
     using S = Shape<kCols>;
@@ -336,12 +341,12 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
             *row = pos - blk * p.block_size;
             return p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq ? max(__ldg(table + blk), -1) : -1;
         };
-        const int32_t own = t0 + static_cast<int32_t>((w - tau) & 1u);  // this warp's first tile here
+        const int32_t own = t0 + static_cast<int32_t>((w - tau) & (S::kMmaWarps - 1));  // this warp's first tile here
         int32_t row_next, page_next = look(own, &row_next);
-        for (int32_t t = own; t < t1 && !stop; t += 2) {
+        for (int32_t t = own; t < t1 && !stop; t += S::kMmaWarps) {
             const uint32_t ta = tau + static_cast<uint32_t>(t - t0);
             const int32_t page = page_next, row = row_next;
-            page_next = look(t + 2, &row_next);
+            page_next = look(t + S::kMmaWarps, &row_next);
             const uint32_t e = ta % S::kStages;
             if (ta >= S::kStages) b.wait(S::BAR_EMPTY + e, (ta / S::kStages - 1) & 1);
             // After a failed wait nothing more is issued (the drain below finds what is in flight).
@@ -354,17 +359,14 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
                 for (int i = 0; i < p.box_rows; ++i) scales[lane * p.box_rows + i] = kNegInf;
                 if (p.status) atomicCAS(p.status, 0, kStatusBounds);
             }
-            uint32_t boxes = __ballot_sync(0xffffffffu, page >= 0);
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
             const uint32_t full = b.bar(S::BAR_FULL + e);
-            if (lane == 0) mbar_arrive_expect_tx(full, __popc(boxes) * (box_codes + box_scales));
-            for (; boxes != 0u; boxes &= boxes - 1u) {
-                const int box = __ffs(boxes) - 1;
-                const int32_t pg = __shfl_sync(0xffffffffu, page, box), rw = __shfl_sync(0xffffffffu, row, box);
-                if (lane == 0) {
-                    tma_box3(b.sbase + e * kTileBytes + box * box_codes, tmap, rw, pg, full);
-                    bulk_g2s(smem_u32(scales) + box * box_scales,
-                             p.cache + pg * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + rw * 4, box_scales, full);
-                }
+            if (lane == 0) mbar_arrive_expect_tx(full, boxes * (box_codes + box_scales));
+            __syncwarp();
+            if (page >= 0) {
+                tma_box3(b.sbase + e * kTileBytes + lane * box_codes, tmap, row, page, full);
+                bulk_g2s(smem_u32(scales) + lane * box_scales,
+                         p.cache + page * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + row * 4, box_scales, full);
             }
             __syncwarp();
         }
@@ -374,7 +376,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
     // an abort some of them were never asked for: their waits end at the limit).
     if (lane == 0) {
         for (uint32_t i = tau > S::kStages ? tau - S::kStages : 0; i < tau; ++i) {
-            if ((i & 1u) != w) continue;
+            if ((i & (S::kMmaWarps - 1)) != w) continue;
             const uint64_t since = globaltimer_ns();
             while (!mbar_try_wait(b.bar(S::BAR_FULL + static_cast<int>(i % S::kStages)), (i / S::kStages) & 1) &&
                    globaltimer_ns() - since < (stop ? kDrainLimitNs / S::kStages : kDrainLimitNs)) {
@@ -450,9 +452,12 @@ __device__ void run_load(const Block<kCols>& b) {
     cp_async_wait_all();
 }
 
+// MMA warp w issues every kMmaWarps-th tile from its w-th on: a tile's waits, fence, issue and
+// commits are one chain of some 900 cycles, more than the MMAs of 128 columns take.
 template <int kHeads, int kCols>
 __device__ void run_mma(const Block<kCols>& b, uint32_t tmem) {
     using S = Shape<kCols>;
+    const uint32_t w = (threadIdx.x >> 5) - S::kMmaWarp0;
     const uint32_t el = elect_one();
     const uint64_t q = smem_desc(b.sbase + S::kOffQ, 16, 1024, kSwizzle128B);
     uint32_t tau = 0, entered = 0;
@@ -460,10 +465,12 @@ __device__ void run_mma(const Block<kCols>& b, uint32_t tmem) {
         const uint32_t idesc = idesc_e4m3(kTile, 16, false, false) +
                                (static_cast<uint32_t>(x.rows * kHeads - 16) >> 3 << 17);  // N = rows x heads
         b.wait(S::BAR_QFULL, entered++ & 1);
-        for (int32_t t = t0; t < t1; ++t, ++tau) {
-            const int e = static_cast<int>(tau % S::kStages), d = static_cast<int>(tau % S::kDBufs);
-            b.wait(S::BAR_FULL + e, (tau / S::kStages) & 1);
-            if (tau >= S::kDBufs) b.wait(S::BAR_DEMPTY + d, (tau / S::kDBufs - 1) & 1);
+        if (el) mbar_arrive(b.bar(S::BAR_QSEEN));  // a warp without a tile here must not miss the phase
+        for (int32_t t = t0 + static_cast<int32_t>((w - tau) & (S::kMmaWarps - 1)); t < t1; t += S::kMmaWarps) {
+            const uint32_t ta = tau + static_cast<uint32_t>(t - t0);
+            const int e = static_cast<int>(ta % S::kStages), d = static_cast<int>(ta % S::kDBufs);
+            b.wait(S::BAR_FULL + e, (ta / S::kStages) & 1);
+            if (ta >= S::kDBufs) b.wait(S::BAR_DEMPTY + d, (ta / S::kDBufs - 1) & 1);
             fence_proxy_async_smem();
             tc_fence_after();
             const uint64_t k = smem_desc(b.sbase + e * kTileBytes, 16, 1024, kSwizzle128B);
@@ -479,6 +486,7 @@ __device__ void run_mma(const Block<kCols>& b, uint32_t tmem) {
             tc_commit_el(b.bar(S::BAR_DFULL + d), el);
             if (el) mbar_arrive(b.bar(S::BAR_DFULL + d));
         }
+        tau += static_cast<uint32_t>(t1 - t0);
     });
     // Every MMA has completed before the block gives its tensor memory back.
     tc_commit_el(b.bar(S::BAR_DRAIN), el);
@@ -504,8 +512,10 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
     const int pool_tk = tk / p.kpool;
     const bool writer = tk % p.kpool == 0;
     const int row_first = kHalves ? 0 : set * kRows;
-    uint32_t tau = 0;
+    uint32_t tau = 0, entered = 0;
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
+        if (entered > 0) b.wait(S::BAR_QSEEN, (entered - 1) & 1);
+        ++entered;
         // The unit before is done with: its last D buffer was full, so its MMAs have read the
         // queries, and every epilogue warp has its weights.
         named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
@@ -625,12 +635,13 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
             mbar_init(b.bar(S::BAR_DEMPTY + d), S::kEpiWarps);
         }
         mbar_init(b.bar(S::BAR_QFULL), S::kEpiWarps);
-        mbar_init(b.bar(S::BAR_DRAIN), 1);
+        mbar_init(b.bar(S::BAR_QSEEN), S::kMmaWarps);
+        mbar_init(b.bar(S::BAR_DRAIN), S::kMmaWarps);
         *b.abort_flag = 0;
         fence_mbar_init();
         if (p.box_rows > 0) prefetch_tmap(&tmap);
     }
-    if (warp == S::kMmaWarp) {
+    if (warp == S::kMmaWarp0) {
         tmem_alloc(b.sbase + S::kOffTmem, S::kTmemCols);
         tmem_relinquish();
     }
@@ -641,13 +652,13 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
     if (warp < S::kEpiWarps) {
         run_epilogue<kHeads, kCols>(b, tmem);
     } else {
-        if (warp == S::kMmaWarp) run_mma<kHeads, kCols>(b, tmem);
-        else if (p.box_rows > 0) run_load_boxes(b, &tmap);
-        else run_load(b);
+        if (warp < S::kLoadWarp0) run_mma<kHeads, kCols>(b, tmem);
+        else if (p.box_rows == 0) run_load(b);
+        else if (warp < S::kLoadWarp0 + S::kMmaWarps) run_load_boxes(b, &tmap);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == S::kMmaWarp) {
+    if (warp == S::kMmaWarp0) {
         tc_fence_after();
         tmem_dealloc(tmem, S::kTmemCols);
     }
