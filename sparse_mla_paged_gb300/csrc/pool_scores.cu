@@ -48,7 +48,7 @@ constexpr int kChunk = 16;                       // columns of a tensor-memory l
 template <int kCols>
 struct Shape {
     static constexpr int kCtas = kCols == 64 ? 2 : 1;  // blocks per SM
-    static constexpr int kStages = kCols == 64 ? 5 : 10;
+    static constexpr int kStages = kCols == 64 ? 4 : 10;
     static constexpr int kEpiWarps = kCols / 16;       // 64 columns, whose weights fit its registers, a warp
     static constexpr int kSets = kEpiWarps / 4;        // warps that share a lane quarter
     static constexpr int kWeights = kCols / kSets;     // columns of a warp: 64
@@ -56,7 +56,7 @@ struct Shape {
     // MMA warps, and load warps of boxes, that take tiles in turn. Each has to meet every phase of
     // its barriers (a wait for a phase that has not begun passes as the one before it), so the
     // ring and the D buffers are a multiple of them: a slot is always the same warp's.
-    static constexpr int kMmaWarps = kCols == 64 ? 1 : 2;
+    static constexpr int kMmaWarps = 2;
     static_assert(kStages % kMmaWarps == 0 && kDBufs % kMmaWarps == 0, "slots belong to warps");
     static constexpr int kMmaWarp0 = kEpiWarps;
     static constexpr int kLoadWarp0 = kMmaWarp0 + kMmaWarps;
