@@ -13,7 +13,7 @@
 //   load     tiles into a ring of three, [4 blocks of 128 dims][128 tokens][128 bytes] with
 //            the 128-byte swizzle: one warp with tensor-map boxes of a page's rows when pages
 //            and tiles fit each other, else four warps with 16-byte copies
-//   MMA      one warp: Q.K^T of a tile and P.V of the tile before, whichever is ready
+//   MMA      one warp for Q.K^T, one for P.V
 //   softmax  eight warps, two per TMEM lane quarter; the same warps write the output
 //
 // A tile that holds tokens which some row of the unit does not see ("edge" tile: the last
@@ -84,8 +84,8 @@ constexpr float kNegInf = -__builtin_huge_valf();
 template <bool kTma>
 struct Roles {
     static constexpr int kLoadWarps = kTma ? 1 : 4;
-    static constexpr int kMmaWarp = kLoadWarps;
-    static constexpr int kSoftmax0 = kMmaWarp + 1;
+    static constexpr int kMmaWarp = kLoadWarps;  // Q.K^T; the next one P.V
+    static constexpr int kSoftmax0 = kMmaWarp + 2;
     static constexpr int kThreads = (kSoftmax0 + kSoftmaxWarps) * 32;
 };
 
@@ -230,97 +230,78 @@ __device__ void run_load_copies(const Cta& c) {
 }
 
 // ------------------------------------------------------------------------------------
-// MMA warp: runs converged, one elected lane issues
+// MMA warps, one for Q.K^T and one for P.V (converged, one elected lane issues). The issue of
+// an MMA blocks while the tensor core's queue is full, so one warp for both products left the
+// core idle during its waits, fences and commits, some 800 of 3350 cycles a tile.
 // ------------------------------------------------------------------------------------
-__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) != 0);
-}
-
-__device__ void run_mma(const Cta& c) {
+__device__ void run_qk(const Cta& c) {
     const Params& p = c.p;
     const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
     const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
-    const uint32_t idq = idesc_e4m3(128, kTile, false, false);
-    const uint32_t idp = idesc_e4m3(128, kHeadsPerCta, true, false);
+    const uint32_t idesc = idesc_e4m3(128, kTile, false, false);
     const uint32_t el = elect_one();
-    int units = 0;  // entered so far
-
-    const uint64_t pdesc0 = smem_desc(c.sbase + kOffP, 1024, 128, kSwizzleNone);
-    auto issue_pv = [&](uint32_t tp, bool first) {
-        const int pb = tp & 1, e = static_cast<int>(tp % slots);
-        c.wait(BAR_PFULL0 + pb, (tp >> 1) & 1);
-        if (first && units > 0) c.wait(BAR_OEMPTY, (units - 1) & 1);
-        tc_fence_after();
-        // V^T: 128 dims of block mc x 32 tokens (four 8-token swizzle groups of 1 KB), MN-major.
-        // P'^T: 64 pairs x 32 tokens, K-major core matrices.
-        const uint64_t vdesc = smem_desc(c.sbase + e * slot_bytes + (p.kv_same ? 0u : kTileBytes), kBlockBytes, 1024, kSwizzle128B);
-        const uint64_t pdesc = pdesc0 + static_cast<uint64_t>((pb * 2 * kPTermBytes) >> 4);
-#pragma unroll
-        for (int mc = 0; mc < 4; ++mc) {
-#pragma unroll
-            for (int ks = 0; ks < kTile / 32; ++ks) {
-                const uint64_t a = vdesc + static_cast<uint64_t>((mc * kBlockBytes + ks * 4096) >> 4);
-                const uint64_t bh = pdesc + static_cast<uint64_t>((ks * 2048) >> 4);
-                const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + ks * 2048) >> 4);
-                const uint32_t d = c.tmem + kTmemO + mc * 64;
-                if (ks == 0) mma_e4m3_el(d, a, bh, idp, first ? 0u : 1u, el);
-                else mma_e4m3_acc_el(d, a, bh, idp, el);
-                mma_e4m3_acc_el(d, a, bl, idp, el);
-            }
-        }
-        tc_commit_el(c.bar(BAR_PVDONE0 + pb), el);
-        tc_commit_el(c.bar(BAR_EMPTY0 + e), el);
-    };
-    auto issue_qk = [&](uint32_t tq) {
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint64_t kdesc = smem_desc(c.sbase + static_cast<uint32_t>(tq % slots) * slot_bytes, 16, 1024, kSwizzle128B);
-        const uint32_t d = c.tmem + kTmemS;
-        mma_e4m3_ta_el(d, c.tmem + kTmemQ, kdesc, idq, 0u, el);
-#pragma unroll
-        for (int ks = 1; ks < 16; ++ks)
-            mma_e4m3_ta_acc_el(d, c.tmem + kTmemQ + ks * 8,
-                               kdesc + static_cast<uint64_t>(((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), idq, el);
-        tc_commit_el(c.bar(BAR_SFULL), el);
-    };
-    auto qk_ready = [&](uint32_t tq) {
-        return warp_poll(c.bar(BAR_FULL0 + static_cast<int>(tq % slots)), (tq / slots) & 1) &&
-               (tq == 0 || warp_poll(c.bar(BAR_SEMPTY), (tq - 1) & 1));
-    };
-
-    uint32_t tau = 0;
+    uint32_t tau = 0, units = 0;
     for (int32_t k = c.first_k;; ++k) {
         const Segment s = c.seg(k);
-        c.wait(BAR_QFULL, units & 1);
-        tc_fence_after();
+        c.wait(BAR_QFULL, units++ & 1);
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
-            // Q.K of this tile and P.V of the one before are independent: whichever is ready.
-            bool qk = false, pv = t == s.t0;
-            const uint64_t t_start = globaltimer_ns();
-            while (!qk || !pv) {
-                if (!qk && qk_ready(tau)) {
-                    issue_qk(tau);
-                    if (t == s.t1 - 1) tc_commit_el(c.bar(BAR_QEMPTY), el);
-                    qk = true;
-                }
-                if (!pv && warp_poll(c.bar(BAR_PFULL0 + ((tau - 1) & 1)), ((tau - 1) >> 1) & 1)) {
-                    issue_pv(tau - 1, t - 1 == s.t0);
-                    pv = true;
-                }
-                if (!qk || !pv) {
-                    if (__shfl_sync(0xffffffffu, (*c.abort_flag != 0) || globaltimer_ns() - t_start > kWaitNs, 0)) {
-                        c.fail(kStatusTimeout);
-                        break;
-                    }
-                    if (!pv) mbar_try_wait_hint(c.bar(BAR_PFULL0 + ((tau - 1) & 1)), ((tau - 1) >> 1) & 1, kPollHintNs);
-                    else mbar_try_wait_hint(c.bar(BAR_FULL0 + static_cast<int>(tau % slots)), (tau / slots) & 1, kPollHintNs);
-                }
-            }
+            c.wait(BAR_FULL0 + static_cast<int>(tau % slots), (tau / slots) & 1);
+            if (tau > 0) c.wait(BAR_SEMPTY, (tau - 1) & 1);
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint64_t kdesc = smem_desc(c.sbase + static_cast<uint32_t>(tau % slots) * slot_bytes, 16, 1024, kSwizzle128B);
+            const uint32_t d = c.tmem + kTmemS;
+            mma_e4m3_ta_el(d, c.tmem + kTmemQ, kdesc, idesc, 0u, el);
+#pragma unroll
+            for (int ks = 1; ks < 16; ++ks)
+                mma_e4m3_ta_acc_el(d, c.tmem + kTmemQ + ks * 8,
+                                   kdesc + static_cast<uint64_t>(((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), idesc, el);
+            tc_commit_el(c.bar(BAR_SFULL), el);
+            if (t == s.t1 - 1) tc_commit_el(c.bar(BAR_QEMPTY), el);
         }
-        issue_pv(tau - 1, s.t1 - s.t0 == 1);
-        ++units;
         if (s.last) break;
     }
+    tc_commit_el(c.bar(BAR_DRAIN), el);
+}
+
+__device__ void run_pv(const Cta& c) {
+    const Params& p = c.p;
+    const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
+    const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
+    const uint32_t idesc = idesc_e4m3(128, kHeadsPerCta, true, false);
+    const uint32_t el = elect_one();
+    const uint64_t pdesc0 = smem_desc(c.sbase + kOffP, 1024, 128, kSwizzleNone);
+    uint32_t tau = 0, units = 0;
+    for (int32_t k = c.first_k;; ++k, ++units) {
+        const Segment s = c.seg(k);
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int pb = tau & 1, e = static_cast<int>(tau % slots);
+            c.wait(BAR_PFULL0 + pb, (tau >> 1) & 1);
+            if (t == s.t0 && units > 0) c.wait(BAR_OEMPTY, (units - 1) & 1);
+            tc_fence_after();
+            // V^T: 128 dims of block mc x 32 tokens (four 8-token swizzle groups of 1 KB), MN-major.
+            // P'^T: 64 pairs x 32 tokens, K-major core matrices.
+            const uint64_t vdesc = smem_desc(c.sbase + e * slot_bytes + (p.kv_same ? 0u : kTileBytes), kBlockBytes, 1024, kSwizzle128B);
+            const uint64_t pdesc = pdesc0 + static_cast<uint64_t>((pb * 2 * kPTermBytes) >> 4);
+#pragma unroll
+            for (int mc = 0; mc < 4; ++mc) {
+#pragma unroll
+                for (int ks = 0; ks < kTile / 32; ++ks) {
+                    const uint64_t a = vdesc + static_cast<uint64_t>((mc * kBlockBytes + ks * 4096) >> 4);
+                    const uint64_t bh = pdesc + static_cast<uint64_t>((ks * 2048) >> 4);
+                    const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + ks * 2048) >> 4);
+                    const uint32_t d = c.tmem + kTmemO + mc * 64;
+                    if (ks == 0) mma_e4m3_el(d, a, bh, idesc, t == s.t0 ? 0u : 1u, el);
+                    else mma_e4m3_acc_el(d, a, bh, idesc, el);
+                    mma_e4m3_acc_el(d, a, bl, idesc, el);
+                }
+            }
+            tc_commit_el(c.bar(BAR_PVDONE0 + pb), el);
+            tc_commit_el(c.bar(BAR_EMPTY0 + e), el);
+        }
+        if (s.last) break;
+    }
+    tc_commit_el(c.bar(BAR_DRAIN), el);
 }
 
 // ------------------------------------------------------------------------------------
@@ -668,7 +649,7 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
         mbar_init(c.bar(BAR_QFULL), kSoftmaxWarps);
         mbar_init(c.bar(BAR_QEMPTY), 1);
         mbar_init(c.bar(BAR_OEMPTY), kSoftmaxWarps);
-        mbar_init(c.bar(BAR_DRAIN), 1);
+        mbar_init(c.bar(BAR_DRAIN), 2);
         mbar_init(c.bar(BAR_DONE), kSoftmaxWarps);
         *c.abort_flag = 0;
         fence_mbar_init();
@@ -697,10 +678,10 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
         if (warp < R::kLoadWarps) {
             if constexpr (kTma) run_load_tma(c, &kmap, &vmap);
             else run_load_copies(c);
-        } else if (warp == R::kMmaWarp) {
-            run_mma(c);
+        } else if (warp < R::kSoftmax0) {
+            if (warp == R::kMmaWarp) run_qk(c);
+            else run_pv(c);
             // Until every MMA has completed and the softmax warps have read tensor memory.
-            tc_commit_el(c.bar(BAR_DRAIN), elect_one());
             uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(c.bar(BAR_DRAIN), 0) && globaltimer_ns() - t0 < kDrainLimitNs) {
             }
