@@ -226,19 +226,33 @@ int32_t box_rows(int32_t block_size) {
     return block_size % 128 == 0 ? 128 : 0;
 }
 
-// 3-D map of a paged cache, [page][row of the page][row_bytes], pages enough to span the
-// device's memory, read as boxes of 128 bytes x `rows` rows of one page into the
-// 128-byte-swizzled operand layout; a page outside the map (a negative one) gives zeros.
-bool encode_page_map(const void* base, size_t mem_bytes, int32_t row_bytes, int32_t block_size, int64_t stride, int32_t rows,
-                     CUtensorMap* m) {
+// 3-D map of an index cache's codes, [page][row of the page][128 bytes], pages enough to span
+// the device's memory, read as boxes of `rows` rows of one page into the 128-byte-swizzled
+// operand layout; a page outside the map (a negative one) gives zeros.
+bool encode_page_map(const void* base, size_t mem_bytes, int32_t block_size, int64_t stride, int32_t rows, CUtensorMap* m) {
     const auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t pages = std::min<cuuint64_t>(mem_bytes / static_cast<size_t>(stride) + 1, (1ull << 31) - 1);
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(block_size), pages};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(stride)};
+    const cuuint64_t dims[3] = {kIndexDim, static_cast<cuuint64_t>(block_size), pages};
+    const cuuint64_t strides[2] = {kIndexDim, static_cast<cuuint64_t>(stride)};
     const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(rows), 1};
     const cuuint32_t estride[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 5-D map of a paged latent cache, [page][group of 8 rows][block of 128 bytes][row][128 bytes]:
+// a box of whole groups lands as the groups' swizzle atoms in order (full.cu's tile layout).
+bool encode_group_map(const void* base, size_t mem_bytes, int32_t block_size, int64_t stride, int32_t rows, CUtensorMap* m) {
+    const auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t pages = std::min<cuuint64_t>(mem_bytes / static_cast<size_t>(stride) + 1, (1ull << 31) - 1);
+    const cuuint64_t dims[5] = {128, 8, kLatent / 128, static_cast<cuuint64_t>(block_size / 8), pages};
+    const cuuint64_t strides[4] = {kLatent, 128, 8 * kLatent, static_cast<cuuint64_t>(stride)};
+    const cuuint32_t box[5] = {128, 8, kLatent / 128, static_cast<cuuint32_t>(rows / 8), 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -757,7 +771,7 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     CUtensorMap tmap;
     std::memset(&tmap, 0, sizeof tmap);
     if (p.box_rows > 0 &&
-        !encode_page_map(index_cache, d->mem_bytes, kIndexDim, block_size, page_stride_bytes, p.box_rows, &tmap))
+        !encode_page_map(index_cache, d->mem_bytes, block_size, page_stride_bytes, p.box_rows, &tmap))
         p.box_rows = 0;
     return from_cuda(launch_pool_scores(p, tmap, d->sms, static_cast<cudaStream_t>(stream)));
 }
@@ -834,13 +848,13 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     p.kv_same = k_cache == v_cache ? 1 : 0;
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;
-    p.box_rows = box_rows(block_size);  // other page sizes take per-thread copies
+    p.box_rows = std::min(box_rows(block_size), 32);  // other page sizes take per-thread copies
     CUtensorMap kmap, vmap;
     std::memset(&kmap, 0, sizeof kmap);
     std::memset(&vmap, 0, sizeof vmap);
     if (p.box_rows > 0 &&
-        !(encode_page_map(k_cache, d->mem_bytes, kLatent, block_size, cache_stride_bytes, p.box_rows, &kmap) &&
-          (p.kv_same || encode_page_map(v_cache, d->mem_bytes, kLatent, block_size, cache_stride_bytes, p.box_rows, &vmap))))
+        !(encode_group_map(k_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &kmap) &&
+          (p.kv_same || encode_group_map(v_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &vmap))))
         p.box_rows = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = from_cuda(launch_full_plan(p, s));

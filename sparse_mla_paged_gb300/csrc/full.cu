@@ -10,9 +10,10 @@
 // terms; O^T[512 x 64 pairs] accumulates in tensor memory in FP32, rescaled only when a
 // pair's reference maximum m moves (kRescale* in common.cuh).
 //
-//   load     tiles into a ring of three, [4 blocks of 128 dims][128 tokens][128 bytes] with
-//            the 128-byte swizzle: one warp with tensor-map boxes of a page's rows when pages
-//            and tiles fit each other, else four warps with 16-byte copies
+//   load     tiles into a ring of three, [16 groups of 8 tokens][4 blocks of 128 dims][8 tokens]
+//            [128 bytes] with the 128-byte swizzle, each in four quarters of 32 tokens that are
+//            refilled as soon as their P.V is done: one warp with tensor-map boxes of a page's
+//            rows when pages and tiles fit each other, else four warps with 16-byte copies
 //   MMA      one warp for Q.K^T, one for P.V
 //   softmax  eight warps, two per TMEM lane quarter; the same warps write the output
 //
@@ -33,8 +34,14 @@ namespace full {
 namespace {
 
 constexpr int kTileBytes = kTile * kLatent;  // 64 KB
-constexpr int kBlockBytes = kTile * 128;     // one block of 128 dims
+constexpr int kGroupBytes = 8 * kLatent;     // 8 tokens: four 1 KB swizzle atoms, one per 128 dims
 constexpr int kRingTiles = 3;
+// Quarters of a tile. A slot is held from its load until its P.V is done, and three slots over
+// that time are the most tiles that pass: loading and releasing quarters takes three quarters
+// of a P.V and most of the load's 64 KB out of it.
+constexpr int kQuarters = 4;
+constexpr int kQuarterTokens = kTile / kQuarters;  // 32: K of one MMA of P.V
+constexpr int kQuarterBytes = kTileBytes / kQuarters;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
 constexpr int kHalfCols = kTile / 2;         // S columns per softmax warp
@@ -45,17 +52,16 @@ constexpr int kBarSoftmax = 1;
 constexpr int kBarPair0 = 2;  // 2..5: the two softmax warps of a lane quarter
 
 constexpr int kOffP = kRingTiles * kTileBytes;               // P' [2 buffers][hi, lo]; epilogue staging
-constexpr int kOffHm = kOffP + 4 * kPTermBytes;              // float [2 token halves][64] tile maxima
+constexpr int kOffHm = kOffP + 4 * kPTermBytes;              // float [2 token halves][64] tile maxima; row sums at the end
 constexpr int kOffAlpha = kOffHm + 2 * kHeadsPerCta * 4;     // float [2 tile parities][64] rescale factors
-constexpr int kOffL = kOffAlpha + 2 * kHeadsPerCta * 4;      // float [2 token halves][64] row sums
-constexpr int kOffF = kOffL + 2 * kHeadsPerCta * 4;          // float [64] output factors
+constexpr int kOffF = kOffAlpha + 2 * kHeadsPerCta * 4;      // float [64] output factors
 constexpr int kOffFlags = kOffF + kHeadsPerCta * 4;          // u32 [2 tile parities][4 lane quarters]
 constexpr int kOffBroken = kOffFlags + 2 * 4 * 4;            // 128 bits: an edge tile's tokens with a NaN code
 constexpr int kOffBars = kOffBroken + kTile / 8;
 enum {
     BAR_FULL0 = 0,                        // ring slot loaded
-    BAR_EMPTY0 = BAR_FULL0 + kRingTiles,  // ring slot free: its P.V is done
-    BAR_SFULL = BAR_EMPTY0 + kRingTiles,  // S written
+    BAR_EMPTY0 = BAR_FULL0 + kRingTiles,  // quarter of a ring slot free: its P.V is done
+    BAR_SFULL = BAR_EMPTY0 + kRingTiles * kQuarters,  // S written
     BAR_SEMPTY,                           // S read
     BAR_PFULL0,                           // 2: P' buffer written
     BAR_PVDONE0 = BAR_PFULL0 + 2,         // 2: the P.V reading it is done
@@ -89,10 +95,11 @@ struct Roles {
     static constexpr int kThreads = (kSoftmax0 + kSoftmaxWarps) * 32;
 };
 
-__device__ __forceinline__ void tma_box3(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+// Box of whole 8-token groups of one page ([group][128-dim block][8 rows][128 bytes]).
+__device__ __forceinline__ void tma_groups(uint32_t dst, const void* tmap, int32_t group, int32_t page, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-            "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];" ::
+            "r"(dst), "l"(tmap), "r"(0), "r"(group), "r"(page), "r"(bar)
         : "memory");
 }
 
@@ -126,13 +133,13 @@ __device__ __forceinline__ int32_t page_of(const Params& p, int32_t seq, int32_t
 }
 
 // ------------------------------------------------------------------------------------
-// load: tensor-map boxes (warp 0; lane = 4*box + block of 128 dims)
+// load: tensor-map boxes (warp 0; lane l has box l of a tile, p.box_rows <= 32 tokens)
 // ------------------------------------------------------------------------------------
 __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtensorMap* vmap) {
     const Params& p = c.p;
-    const int lane = threadIdx.x & 31, box = lane >> 2, kb = lane & 3;
-    const bool mine = box * p.box_rows < kTile;
-    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * 128u;
+    const int lane = threadIdx.x & 31;
+    const int quarter = lane * p.box_rows / kQuarterTokens;  // kQuarters and up: no box
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kLatent;
     const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
     const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
     uint32_t tau = 0;
@@ -143,44 +150,50 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtens
         // This lane's page of tile t (requested a tile ahead), its first row there, and
         // whether any row of the unit sees the box.
         auto look = [&](int32_t t, int32_t* row, bool* live) {
-            const int32_t pos = t * kTile + box * p.box_rows;
-            *live = mine && t < s.t1 && pos < s.max_len;
+            const int32_t pos = t * kTile + lane * p.box_rows;
+            *live = quarter < kQuarters && t < s.t1 && pos < s.max_len;
             return *live ? page_of(p, seq, pos, row) : -1;
         };
         int32_t row = 0, row_next = 0;
         bool live, live_next;
         int32_t page_next = look(s.t0, &row_next, &live_next);
-        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+        for (int32_t t = s.t0; t < s.t1 && !stop; ++t, ++tau) {
             const int32_t page = page_next;
             row = row_next;
             live = live_next;
             page_next = look(t + 1, &row_next, &live_next);
             if (live && page < 0) atomicCAS(p.status, 0, kStatusBounds);
             const int e = static_cast<int>(tau % slots);
-            if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e, (tau / slots - 1) & 1);
-            // After a failed wait nothing more is issued (the drain below finds what is in flight).
-            if (__shfl_sync(0xffffffffu, *c.abort_flag, 0)) {
-                stop = true;
-                break;
+            const uint32_t full = c.bar(BAR_FULL0 + e);
+            const uint32_t lives = __ballot_sync(0xffffffffu, live);
+#pragma unroll 1
+            for (int j = 0; j < kQuarters; ++j) {
+                if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e * kQuarters + j, (tau / slots - 1) & 1);
+                // After a failed wait nothing more is issued (the drain below finds what is in flight).
+                if (__shfl_sync(0xffffffffu, *c.abort_flag, 0)) {
+                    stop = true;
+                    break;
+                }
+                const uint32_t boxes = __popc(lives & __ballot_sync(0xffffffffu, quarter == j)) * (p.kv_same ? 1 : 2);
+                if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes);
+                __syncwarp();
+                if (live && quarter == j) {  // a negative page lies outside the map: zeros
+                    const uint32_t dst = c.sbase + e * slot_bytes + lane * box_bytes;
+                    tma_groups(dst, kmap, row >> 3, page, full);
+                    if (!p.kv_same) tma_groups(dst + kTileBytes, vmap, row >> 3, page, full);
+                }
+                __syncwarp();
             }
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, live)) * (p.kv_same ? 1 : 2);
-            if (lane == 0) mbar_arrive_expect_tx(c.bar(BAR_FULL0 + e), boxes * box_bytes);
-            __syncwarp();
-            if (live) {  // a negative page lies outside the map: zeros
-                const uint32_t dst = c.sbase + e * slot_bytes + kb * kBlockBytes + box * box_bytes;
-                tma_box3(dst, kmap, kb * 128, row, page, c.bar(BAR_FULL0 + e));
-                if (!p.kv_same) tma_box3(dst + kTileBytes, vmap, kb * 128, row, page, c.bar(BAR_FULL0 + e));
-            }
-            __syncwarp();
         }
         if (s.last) break;
     }
-    // No copy into shared memory is in flight when the CTA exits: the last tiles' bytes.
+    // No copy into shared memory is in flight when the CTA exits: the last tiles' bytes (after
+    // an abort a quarter may never have been asked for: its wait ends at the limit).
     if (lane == 0) {
         for (uint32_t i = tau > static_cast<uint32_t>(slots) ? tau - slots : 0; i < tau; ++i) {
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(c.bar(BAR_FULL0 + static_cast<int>(i % slots)), (i / slots) & 1) &&
-                   globaltimer_ns() - t0 < kDrainLimitNs) {
+                   globaltimer_ns() - t0 < kDrainLimitNs / (stop ? kRingTiles : 1)) {
             }
         }
     }
@@ -188,7 +201,7 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtens
 }
 
 // ------------------------------------------------------------------------------------
-// load: 16-byte copies (warps 0-3, 32 tokens of a tile each; lane l resolves token l's page)
+// load: 16-byte copies (warps 0-3, a quarter of a tile each; lane l resolves token l's page)
 // ------------------------------------------------------------------------------------
 __device__ void run_load_copies(const Cta& c) {
     const Params& p = c.p;
@@ -200,7 +213,7 @@ __device__ void run_load_copies(const Cta& c) {
         const Segment s = c.seg(k);
         const int32_t seq = s.unit / p.groups;
         auto look = [&](int32_t t) -> int64_t {
-            const int32_t pos = t * kTile + 32 * w + lane;
+            const int32_t pos = t * kTile + kQuarterTokens * w + lane;
             if (t >= s.t1 || pos >= s.max_len) return -1;
             int32_t row;
             const int32_t page = page_of(p, seq, pos, &row);
@@ -212,12 +225,12 @@ __device__ void run_load_copies(const Cta& c) {
             const int64_t mine = next;
             next = look(t + 1);
             const int e = static_cast<int>(tau % slots);
-            if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e, (tau / slots - 1) & 1);
-            const uint32_t dst = c.sbase + e * slot_bytes + (lane >> 3) * kBlockBytes + 32 * w * 128;
+            if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e * kQuarters + w, (tau / slots - 1) & 1);
+            const uint32_t dst = c.sbase + e * slot_bytes + w * kQuarterBytes + (lane >> 3) * 1024;
 #pragma unroll 8
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < kQuarterTokens; ++j) {
                 const int64_t at = __shfl_sync(0xffffffffu, mine, j);
-                const uint32_t d = dst + j * 128 + (((lane & 7) ^ (j & 7)) << 4);
+                const uint32_t d = dst + (j >> 3) * kGroupBytes + (j & 7) * 128 + (((lane & 7) ^ (j & 7)) << 4);
                 const uint64_t src = at >= 0 ? static_cast<uint64_t>(at) + lane * 16 : 0;
                 cp_async_16_zfill(d, p.k_cache + src, at >= 0 ? 16u : 0u);
                 if (!p.kv_same) cp_async_16_zfill(d + kTileBytes, p.v_cache + src, at >= 0 ? 16u : 0u);
@@ -249,13 +262,13 @@ __device__ void run_qk(const Cta& c) {
             if (tau > 0) c.wait(BAR_SEMPTY, (tau - 1) & 1);
             fence_proxy_async_smem();
             tc_fence_after();
-            const uint64_t kdesc = smem_desc(c.sbase + static_cast<uint32_t>(tau % slots) * slot_bytes, 16, 1024, kSwizzle128B);
+            const uint64_t kdesc = smem_desc(c.sbase + static_cast<uint32_t>(tau % slots) * slot_bytes, 16, kGroupBytes, kSwizzle128B);
             const uint32_t d = c.tmem + kTmemS;
             mma_e4m3_ta_el(d, c.tmem + kTmemQ, kdesc, idesc, 0u, el);
 #pragma unroll
             for (int ks = 1; ks < 16; ++ks)
                 mma_e4m3_ta_acc_el(d, c.tmem + kTmemQ + ks * 8,
-                                   kdesc + static_cast<uint64_t>(((ks >> 2) * kBlockBytes + (ks & 3) * 32) >> 4), idesc, el);
+                                   kdesc + static_cast<uint64_t>(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc, el);
             tc_commit_el(c.bar(BAR_SFULL), el);
             if (t == s.t1 - 1) tc_commit_el(c.bar(BAR_QEMPTY), el);
         }
@@ -279,25 +292,25 @@ __device__ void run_pv(const Cta& c) {
             c.wait(BAR_PFULL0 + pb, (tau >> 1) & 1);
             if (t == s.t0 && units > 0) c.wait(BAR_OEMPTY, (units - 1) & 1);
             tc_fence_after();
-            // V^T: 128 dims of block mc x 32 tokens (four 8-token swizzle groups of 1 KB), MN-major.
-            // P'^T: 64 pairs x 32 tokens, K-major core matrices.
-            const uint64_t vdesc = smem_desc(c.sbase + e * slot_bytes + (p.kv_same ? 0u : kTileBytes), kBlockBytes, 1024, kSwizzle128B);
+            // V^T: 128 dims of block mc x the 32 tokens of a quarter (four 8-token swizzle groups),
+            // MN-major. P'^T: 64 pairs x 32 tokens, K-major core matrices.
+            const uint64_t vdesc = smem_desc(c.sbase + e * slot_bytes + (p.kv_same ? 0u : kTileBytes), 1024, kGroupBytes, kSwizzle128B);
             const uint64_t pdesc = pdesc0 + static_cast<uint64_t>((pb * 2 * kPTermBytes) >> 4);
 #pragma unroll
-            for (int mc = 0; mc < 4; ++mc) {
+            for (int j = 0; j < kQuarters; ++j) {
+                const uint64_t bh = pdesc + static_cast<uint64_t>((j * 2048) >> 4);
+                const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + j * 2048) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < kTile / 32; ++ks) {
-                    const uint64_t a = vdesc + static_cast<uint64_t>((mc * kBlockBytes + ks * 4096) >> 4);
-                    const uint64_t bh = pdesc + static_cast<uint64_t>((ks * 2048) >> 4);
-                    const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + ks * 2048) >> 4);
+                for (int mc = 0; mc < 4; ++mc) {
+                    const uint64_t a = vdesc + static_cast<uint64_t>((j * kQuarterBytes + mc * 1024) >> 4);
                     const uint32_t d = c.tmem + kTmemO + mc * 64;
-                    if (ks == 0) mma_e4m3_el(d, a, bh, idesc, t == s.t0 ? 0u : 1u, el);
+                    if (j == 0) mma_e4m3_el(d, a, bh, idesc, t == s.t0 ? 0u : 1u, el);
                     else mma_e4m3_acc_el(d, a, bh, idesc, el);
                     mma_e4m3_acc_el(d, a, bl, idesc, el);
                 }
+                if (j == kQuarters - 1) tc_commit_el(c.bar(BAR_PVDONE0 + pb), el);
+                tc_commit_el(c.bar(BAR_EMPTY0 + e * kQuarters + j), el);
             }
-            tc_commit_el(c.bar(BAR_PVDONE0 + pb), el);
-            tc_commit_el(c.bar(BAR_EMPTY0 + e), el);
         }
         if (s.last) break;
     }
@@ -324,7 +337,8 @@ __device__ __forceinline__ bool clean_token(uint8_t* v_tile, int token, int part
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         // blocks 2*part and 2*part + 1 of 128 dims, all eight 16-byte pieces of the token's row
-        at[i] = reinterpret_cast<uint4*>(v_tile + (2 * part + (i >> 3)) * kBlockBytes + token * 128 + (i & 7) * 16);
+        at[i] = reinterpret_cast<uint4*>(v_tile + (token >> 3) * kGroupBytes + (2 * part + (i >> 3)) * 1024 + (token & 7) * 128 +
+                                         (i & 7) * 16);
         if (!hidden) {
             const uint4 v = *at[i];
             nan |= ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
@@ -366,7 +380,6 @@ __device__ void run_softmax(const Cta& c) {
     const int hq = 16 * q4 + (lane >> 1);          // pair of this thread within the unit
     float* hm_s = reinterpret_cast<float*>(c.smem + kOffHm);
     float* alpha_s = reinterpret_cast<float*>(c.smem + kOffAlpha);
-    float* l_s = reinterpret_cast<float*>(c.smem + kOffL);
     float* f_s = reinterpret_cast<float*>(c.smem + kOffF);
     uint32_t* flag_s = reinterpret_cast<uint32_t*>(c.smem + kOffFlags);
     uint16_t* broken_s = reinterpret_cast<uint16_t*>(c.smem + kOffBroken);
@@ -577,11 +590,11 @@ __device__ void run_softmax(const Cta& c) {
         pv_seen = true;
         tc_fence_after();
         const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
-        if (term == 0) l_s[half * kHeadsPerCta + hq] = lpair;
+        if (term == 0) hm_s[half * kHeadsPerCta + hq] = lpair;
         named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
         const bool whole = s.part < 0;
         if (term == 0 && half == 0) {
-            const float l = l_s[hq] + l_s[kHeadsPerCta + hq];
+            const float l = hm_s[hq] + hm_s[kHeadsPerCta + hq];
             f_s[hq] = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
             if (!whole) p.part_lse[s.part * kHeadsPerCta + hq] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
         }
@@ -619,7 +632,7 @@ __device__ void run_softmax(const Cta& c) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(c.bar(BAR_OEMPTY));
-        // The staging area is the P buffer; l_s and f_s are used again.
+        // The staging area is the P buffer; hm_s and f_s are used again.
         named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
         ++units;
         if (s.last) break;
@@ -636,10 +649,9 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     Cta c{p, smem, smem_u32(smem), 0u, reinterpret_cast<volatile int*>(smem + kOffAbort)};
 
     if (tid == 0) {
-        for (int e = 0; e < kRingTiles; ++e) {
-            mbar_init(c.bar(BAR_FULL0 + e), kTma ? 1 : 32 * R::kLoadWarps);
-            mbar_init(c.bar(BAR_EMPTY0 + e), 1);
-        }
+        // boxes: one arrival per quarter, with the bytes to come; copies: one per lane
+        for (int e = 0; e < kRingTiles; ++e) mbar_init(c.bar(BAR_FULL0 + e), kTma ? kQuarters : 32 * R::kLoadWarps);
+        for (int e = 0; e < kRingTiles * kQuarters; ++e) mbar_init(c.bar(BAR_EMPTY0 + e), 1);
         mbar_init(c.bar(BAR_SFULL), 1);
         mbar_init(c.bar(BAR_SEMPTY), kSoftmaxWarps);
         for (int i = 0; i < 2; ++i) {

@@ -81,7 +81,7 @@ struct Params {
     int64_t cache_stride;
     int32_t num_seqs, rows_per_seq, heads, pairs, groups, units, max_ctas;
     int32_t block_size, max_blocks_per_seq, verify_rows;
-    int32_t box_rows;          // tokens of a tensor-map box, 0: per-thread copies
+    int32_t box_rows;          // tokens of a tensor-map box (16 or 32), 0: per-thread copies
     int32_t kv_same;
     float score_scale;         // sm_scale * k_scale * log2(e)
     float v_scale;
@@ -124,8 +124,8 @@ __device__ __forceinline__ Segment segment(const Params& p, int64_t begin, int64
 }  // namespace full
 
 cudaError_t full_setup();
-// kmap / vmap: 3-D tensor maps of the caches ([page][row][512 bytes], box 128 bytes x
-// p.box_rows rows), read only when p.box_rows > 0.
+// kmap / vmap: 5-D tensor maps of the caches ([page][group of 8 rows][128-byte block][row]
+// [128 bytes], boxes of whole groups, p.box_rows rows), read only when p.box_rows > 0.
 cudaError_t launch_full(const full::Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream);
 cudaError_t full_plan_setup();
 cudaError_t launch_full_plan(const full::Params& p, cudaStream_t stream);
