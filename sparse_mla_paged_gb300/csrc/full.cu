@@ -12,7 +12,7 @@
 //
 //   load     tiles into a ring of three, [16 groups of 8 tokens][4 blocks of 128 dims][8 tokens]
 //            [128 bytes] with the 128-byte swizzle, each in four quarters of 32 tokens that are
-//            refilled as soon as their P.V is done: one warp with tensor-map boxes of a page's
+//            refilled as soon as their P.V is done: two warps with tensor-map boxes of a page's
 //            rows when pages and tiles fit each other, else four warps with 16-byte copies
 //   MMA      one warp for Q.K^T, one for P.V
 //   softmax  eight warps, two per TMEM lane quarter; the same warps write the output
@@ -86,10 +86,10 @@ constexpr uint32_t kTmemS = 384;
 constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// Warps of the two variants (tensor-map boxes need one loading warp).
+// Warps of the two variants.
 template <bool kTma>
 struct Roles {
-    static constexpr int kLoadWarps = kTma ? 1 : 4;
+    static constexpr int kLoadWarps = kTma ? 2 : 4;
     static constexpr int kMmaWarp = kLoadWarps;  // Q.K^T; the next one P.V
     static constexpr int kSoftmax0 = kMmaWarp + 2;
     static constexpr int kThreads = (kSoftmax0 + kSoftmaxWarps) * 32;
@@ -133,11 +133,13 @@ __device__ __forceinline__ int32_t page_of(const Params& p, int32_t seq, int32_t
 }
 
 // ------------------------------------------------------------------------------------
-// load: tensor-map boxes (warp 0; lane l has box l of a tile, p.box_rows <= 32 tokens)
+// load: tensor-map boxes (warps 0 and 1, two quarters of every tile each: one warp's chain of
+// waits and issues, some 2300 cycles a tile, would be what the ring waits for; lane l has box
+// l of a tile, p.box_rows <= 32 tokens)
 // ------------------------------------------------------------------------------------
 __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtensorMap* vmap) {
     const Params& p = c.p;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, q0 = 2 * (threadIdx.x >> 5);
     const int quarter = lane * p.box_rows / kQuarterTokens;  // kQuarters and up: no box
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kLatent;
     const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
@@ -151,7 +153,7 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtens
         // whether any row of the unit sees the box.
         auto look = [&](int32_t t, int32_t* row, bool* live) {
             const int32_t pos = t * kTile + lane * p.box_rows;
-            *live = quarter < kQuarters && t < s.t1 && pos < s.max_len;
+            *live = (quarter == q0 || quarter == q0 + 1) && t < s.t1 && pos < s.max_len;
             return *live ? page_of(p, seq, pos, row) : -1;
         };
         int32_t row = 0, row_next = 0;
@@ -167,7 +169,7 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtens
             const uint32_t full = c.bar(BAR_FULL0 + e);
             const uint32_t lives = __ballot_sync(0xffffffffu, live);
 #pragma unroll 1
-            for (int j = 0; j < kQuarters; ++j) {
+            for (int j = q0; j < q0 + 2; ++j) {
                 if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e * kQuarters + j, (tau / slots - 1) & 1);
                 // After a failed wait nothing more is issued (the drain below finds what is in flight).
                 if (__shfl_sync(0xffffffffu, *c.abort_flag, 0)) {
