@@ -823,13 +823,12 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     p.seq_lens = seq_lens;
     p.out = static_cast<uint16_t*>(out);
     p.status = reinterpret_cast<int*>(ws + L.status);
-    p.plan.head = reinterpret_cast<full::PlanHead*>(ws + L.head);
+    p.plan.cta = reinterpret_cast<full::CtaStart*>(ws + L.cta);
+    p.plan.pieces = reinterpret_cast<full::UnitPieces*>(ws + L.pieces);
     p.plan.start = reinterpret_cast<int64_t*>(ws + L.start);
     p.plan.unit = reinterpret_cast<int32_t*>(ws + L.unit);
     p.plan.max_len = reinterpret_cast<int32_t*>(ws + L.max_len);
     p.plan.min_len = reinterpret_cast<int32_t*>(ws + L.min_len);
-    p.plan.unit_k = reinterpret_cast<int32_t*>(ws + L.unit_k);
-    p.plan.cta_k = reinterpret_cast<int32_t*>(ws + L.cta_k);
     p.qimg = ws + L.qimg;
     p.qscale = reinterpret_cast<float*>(ws + L.qscale);
     p.part_o = reinterpret_cast<uint16_t*>(ws + L.part_o);

@@ -109,8 +109,7 @@ struct Cta {
     uint8_t* smem;
     uint32_t sbase, tmem;
     volatile int* abort_flag;
-    int64_t begin, end;  // tiles of the line
-    int32_t first_k;
+    CtaStart start;      // range and first segment
 
     __device__ uint32_t bar(int i) const { return sbase + kOffBars + 8 * i; }
     __device__ void fail(int code) const {
@@ -121,7 +120,12 @@ struct Cta {
         if (!mbar_wait(bar(b), parity, abort_flag, kWaitNs)) fail(kStatusTimeout);
         __syncwarp();
     }
-    __device__ Segment seg(int32_t k) const { return segment(p, begin, end, blockIdx.x, first_k, k); }
+    // The stretch after s (not its last).
+    __device__ Segment next(const Segment& s) const {
+        const int32_t k = s.k + 1;
+        return segment(start.begin, start.end, blockIdx.x, false, k, p.plan.unit[k], p.plan.start[k], p.plan.start[k + 1],
+                       p.plan.max_len[k], p.plan.min_len[k]);
+    }
 };
 
 // Page of the block that holds position pos, or -1 (reported).
@@ -146,8 +150,7 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtens
     const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
     uint32_t tau = 0;
     bool stop = false;
-    for (int32_t k = c.first_k; !stop; ++k) {
-        const Segment s = c.seg(k);
+    for (Segment s = c.start.first; !stop; s = c.next(s)) {
         const int32_t seq = s.unit / p.groups;
         // This lane's page of tile t (requested a tile ahead), its first row there, and
         // whether any row of the unit sees the box.
@@ -211,8 +214,7 @@ __device__ void run_load_copies(const Cta& c) {
     const int slots = p.kv_same ? kRingTiles : kRingTiles / 2;
     const uint32_t slot_bytes = p.kv_same ? kTileBytes : 2 * kTileBytes;
     uint32_t tau = 0;
-    for (int32_t k = c.first_k;; ++k) {
-        const Segment s = c.seg(k);
+    for (Segment s = c.start.first;; s = c.next(s)) {
         const int32_t seq = s.unit / p.groups;
         auto look = [&](int32_t t) -> int64_t {
             const int32_t pos = t * kTile + kQuarterTokens * w + lane;
@@ -256,8 +258,7 @@ __device__ void run_qk(const Cta& c) {
     const uint32_t idesc = idesc_e4m3(128, kTile, false, false);
     const uint32_t el = elect_one();
     uint32_t tau = 0, units = 0;
-    for (int32_t k = c.first_k;; ++k) {
-        const Segment s = c.seg(k);
+    for (Segment s = c.start.first;; s = c.next(s)) {
         c.wait(BAR_QFULL, units++ & 1);
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             c.wait(BAR_FULL0 + static_cast<int>(tau % slots), (tau / slots) & 1);
@@ -287,8 +288,7 @@ __device__ void run_pv(const Cta& c) {
     const uint32_t el = elect_one();
     const uint64_t pdesc0 = smem_desc(c.sbase + kOffP, 1024, 128, kSwizzleNone);
     uint32_t tau = 0, units = 0;
-    for (int32_t k = c.first_k;; ++k, ++units) {
-        const Segment s = c.seg(k);
+    for (Segment s = c.start.first;; s = c.next(s), ++units) {
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             const int pb = tau & 1, e = static_cast<int>(tau % slots);
             c.wait(BAR_PFULL0 + pb, (tau >> 1) & 1);
@@ -422,7 +422,7 @@ __device__ void run_softmax(const Cta& c) {
         return pair < p.pairs ? row_len(p, unit / p.groups, pair / p.heads, &over) : 0;
     };
 
-    Segment next = c.seg(c.first_k);
+    Segment next = c.start.first;
     float c_next = p.qscale[static_cast<int64_t>(next.unit) * kHeadsPerCta + hq];
     int32_t len_next = pair_len(next.unit);
     bool q_loaded = false;  // the unit's query operand was loaded during the unit before
@@ -432,7 +432,7 @@ __device__ void run_softmax(const Cta& c) {
         const float qs = c_next;
         const int32_t len = len_next;
         if (!s.last) {
-            next = c.seg(s.k + 1);
+            next = c.next(s);
             c_next = p.qscale[static_cast<int64_t>(next.unit) * kHeadsPerCta + hq];
             len_next = pair_len(next.unit);
         }
@@ -683,12 +683,8 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     // Everything above overlaps the prologue; its plan is read only after this.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const PlanHead head = *p.plan.head;
-    const int32_t cta = blockIdx.x;
-    if (cta < head.ctas) {
-        c.begin = cta * head.tiles / head.ctas;
-        c.end = (cta + 1) * head.tiles / head.ctas;
-        c.first_k = p.plan.cta_k[cta];
+    c.start = p.plan.cta[blockIdx.x];
+    if (c.start.begin < c.start.end) {
         if (warp < R::kLoadWarps) {
             if constexpr (kTma) run_load_tma(c, &kmap, &vmap);
             else run_load_copies(c);

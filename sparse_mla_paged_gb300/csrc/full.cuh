@@ -20,25 +20,39 @@ namespace full {
 constexpr int kTile = 128;
 constexpr int64_t kMaxLen = (int64_t{1} << 31) - 2 * kTile;  // positions stay in 32 bits
 
-struct PlanHead {
-    int64_t tiles;   // T
-    int32_t ctas;    // ranges that T is cut into (0 when T is 0)
-    int32_t live;    // units with a token
+// One CTA's stretch of one unit.
+struct Segment {
+    int32_t k, unit;           // live unit's number, its unit
+    int32_t t0, t1;            // tiles of the unit
+    int32_t max_len, min_len;  // of the unit's rows
+    int32_t part;              // partial slot, -1: the whole unit
+    int32_t last;              // the CTA's last unit
 };
 
-// The plan's arrays, indexed by a live unit's number k but for unit_k.
+// What a CTA starts with, in one load: its range (empty: begin = end) and its first segment.
+struct alignas(16) CtaStart {
+    int64_t begin, end;
+    Segment first;
+};
+
+// Where a unit's pieces are: ranges c_lo .. c_lo + pieces - 1, all in slot 2c but the first
+// one, in slot_lo (its CTA may have started in the unit before). Nothing to join below two.
+struct alignas(16) UnitPieces {
+    int32_t c_lo, slot_lo, pieces, pad;
+};
+
 struct PlanArrays {
-    PlanHead* head;
-    int64_t* start;     // [units + 1] first tile of live unit k on the line
-    int32_t* unit;      // [units] its unit
-    int32_t* max_len;   // [units] longest length of its rows
-    int32_t* min_len;   // [units] shortest
-    int32_t* unit_k;    // [units] k of each unit, -1 without a token
-    int32_t* cta_k;     // [ctas] live unit that a range starts in
+    CtaStart* cta;        // [max_ctas]
+    UnitPieces* pieces;   // [units]
+    // by a live unit's number k:
+    int64_t* start;       // [units + 1] its first tile on the line
+    int32_t* unit;        // [units]
+    int32_t* max_len;     // [units] longest length of its rows
+    int32_t* min_len;     // [units] shortest
 };
 
 struct Layout {
-    size_t status, head, start, unit, max_len, min_len, unit_k, cta_k, qimg, qscale, part_o, part_lse, total;
+    size_t status, cta, pieces, start, unit, max_len, min_len, qimg, qscale, part_o, part_lse, total;
 };
 
 inline Layout layout(int64_t units, int64_t ctas) {
@@ -50,13 +64,12 @@ inline Layout layout(int64_t units, int64_t ctas) {
         return at;
     };
     L.status = put(256);
-    L.head = put(sizeof(PlanHead));
+    L.cta = put(static_cast<size_t>(ctas) * sizeof(CtaStart));
+    L.pieces = put(static_cast<size_t>(units) * sizeof(UnitPieces));
     L.start = put(static_cast<size_t>(units + 1) * 8);
     L.unit = put(static_cast<size_t>(units) * 4);
     L.max_len = put(static_cast<size_t>(units) * 4);
     L.min_len = put(static_cast<size_t>(units) * 4);
-    L.unit_k = put(static_cast<size_t>(units) * 4);
-    L.cta_k = put(static_cast<size_t>(ctas) * 4);
     L.qimg = put(static_cast<size_t>(units) * kQImageBytes);
     L.qscale = put(static_cast<size_t>(units) * kHeadsPerCta * 4);
     L.part_o = put(static_cast<size_t>(2 * ctas) * kHeadsPerCta * kLatent * 2);
@@ -98,24 +111,17 @@ __device__ __forceinline__ int32_t row_len(const Params& p, int64_t seq, int32_t
     return n > 0 ? static_cast<int32_t>(n) : 0;
 }
 
-// One CTA's stretch of one unit.
-struct Segment {
-    int32_t k, unit;
-    int32_t t0, t1;            // tiles of the unit
-    int32_t max_len, min_len;  // of the unit's rows
-    int32_t part;              // partial slot, -1: the whole unit
-    bool last;                 // the CTA's last unit
-};
-__device__ __forceinline__ Segment segment(const Params& p, int64_t begin, int64_t end, int32_t cta, int32_t first_k, int32_t k) {
+// CTA's stretch of live unit k (tiles [b, e) of the line), given its range and its first unit.
+__device__ __forceinline__ Segment segment(int64_t begin, int64_t end, int32_t cta, bool first, int32_t k, int32_t unit, int64_t b,
+                                           int64_t e, int32_t max_len, int32_t min_len) {
     Segment s;
-    const int64_t b = p.plan.start[k], e = p.plan.start[k + 1];
     s.k = k;
-    s.unit = p.plan.unit[k];
-    s.max_len = p.plan.max_len[k];
-    s.min_len = p.plan.min_len[k];
+    s.unit = unit;
     s.t0 = static_cast<int32_t>((begin > b ? begin : b) - b);
     s.t1 = static_cast<int32_t>((end < e ? end : e) - b);
-    s.part = begin <= b && e <= end ? -1 : 2 * cta + (k == first_k ? 0 : 1);
+    s.max_len = max_len;
+    s.min_len = min_len;
+    s.part = begin <= b && e <= end ? -1 : 2 * cta + (first ? 0 : 1);
     s.last = e >= end;
     return s;
 }

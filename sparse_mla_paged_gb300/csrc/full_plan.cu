@@ -50,61 +50,92 @@ __device__ __forceinline__ void scan2(int64_t& a, int32_t& b, int64_t* sa, int32
     b = pb + ib - b;
 }
 
-// One block: the line of tiles (see full.cuh), units in order, kPrologueThreads at a time.
-__device__ void make_plan(const Params& p) {
+// n / d for n, d > 0. They fit 32 bits but for the longest caches, and a 64-bit division is a
+// long sequence. Out of line: the plan runs once, and what its code weighs in instruction
+// fetches is most of its time.
+__device__ __noinline__ int64_t quotient(int64_t n, int64_t d) {
+    if (n >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+
+// One block: the line of tiles (see full.cuh). Thread t has units [t*per, (t+1)*per): a sweep
+// sums their tiles, one scan gives every unit its place, a second sweep writes the units'
+// entries and which unit each range starts in (cta_k, shared memory), and thread c then writes
+// range c's.
+__device__ void make_plan(const Params& p, int32_t* cta_k) {
     __shared__ int64_t sa[kWarps];
     __shared__ int32_t sb[kWarps];
     if (threadIdx.x == 0) atomicExch(p.status, 0);
-    int64_t tiles = 0;
-    int32_t live = 0;
     bool any_over = false;
-    for (int32_t u0 = 0; u0 < p.units; u0 += kPrologueThreads) {
-        const int32_t u = u0 + threadIdx.x;
-        int32_t top = 0, low = 0;
-        if (u < p.units) {
-            const int32_t seq = u / p.groups, first = (u % p.groups) * kHeadsPerCta;
-            const int32_t r0 = first / p.heads, r1 = min(first + kHeadsPerCta, p.pairs) - 1;
-            low = INT32_MAX;
-            for (int32_t i = r0; i <= r1 / p.heads; ++i) {
-                bool over;
-                const int32_t n = row_len(p, seq, i, &over);
-                any_over |= over;
-                top = max(top, n);
-                low = min(low, n);
-            }
+    // Longest and shortest length of a unit's rows.
+    auto lengths = [&](int32_t u, int32_t* top, int32_t* low) {
+        const int32_t seq = u / p.groups, first = (u - seq * p.groups) * kHeadsPerCta;
+        const int32_t r0 = first / p.heads, r1 = (min(first + kHeadsPerCta, p.pairs) - 1) / p.heads;
+        *top = 0;
+        *low = INT32_MAX;
+        // Verify rows grow by one from the first to the last.
+#pragma unroll 1
+        for (int32_t i = r0; i <= r1; i += p.verify_rows && i < r1 ? r1 - r0 : 1) {
+            bool over;
+            const int32_t n = row_len(p, seq, i, &over);
+            any_over |= over;
+            *top = max(*top, n);
+            *low = min(*low, n);
         }
-        int64_t at = (top + kTile - 1) / kTile;
-        const int64_t mine = at;
-        int32_t k = top > 0 ? 1 : 0;
-        int64_t sum_t;
-        int32_t sum_k;
-        scan2(at, k, sa, sb, &sum_t, &sum_k);
-        if (u < p.units) {
-            p.plan.unit_k[u] = top > 0 ? live + k : -1;
-            if (top > 0) {
-                p.plan.start[live + k] = tiles + at;
-                p.plan.start[live + k + 1] = tiles + at + mine;  // the next unit writes the same value
-                p.plan.unit[live + k] = u;
-                p.plan.max_len[live + k] = top;
-                p.plan.min_len[live + k] = low;
-            }
-        }
-        tiles += sum_t;
-        live += sum_k;
+    };
+    const int32_t per = (p.units + kPrologueThreads - 1) / kPrologueThreads;
+    const int32_t lo = static_cast<int32_t>(min(static_cast<int64_t>(p.units), static_cast<int64_t>(threadIdx.x) * per));
+    const int32_t hi = min(p.units, lo + per);
+    int64_t at = 0;
+    int32_t k = 0, top = 0, low = 0;
+#pragma unroll 1
+    for (int32_t u = lo; u < hi; ++u) {
+        lengths(u, &top, &low);
+        at += (top + kTile - 1) / kTile;
+        k += top > 0 ? 1 : 0;
     }
+    int64_t tiles;
+    int32_t live;
+    scan2(at, k, sa, sb, &tiles, &live);
     const int32_t ctas = static_cast<int32_t>(min(tiles, static_cast<int64_t>(p.max_ctas)));
-    if (threadIdx.x == 0) *p.plan.head = PlanHead{tiles, ctas, live};
-    if (any_over) atomicCAS(p.status, 0, kStatusBounds);
-    __syncthreads();
-    // Range c starts at tile floor(c*T/ctas), which lies in unit k for the c with
-    // ceil(start[k]*ctas/T) <= c < ceil(start[k+1]*ctas/T).
-    for (int32_t k = threadIdx.x; k < live; k += kPrologueThreads) {
-        const int64_t n0 = p.plan.start[k] * ctas + tiles - 1, n1 = p.plan.start[k + 1] * ctas + tiles - 1;
-        const bool narrow = n1 >> 32 == 0;  // a 64-bit division is a long sequence
-        const uint32_t d = static_cast<uint32_t>(tiles);
-        const int64_t c0 = narrow ? static_cast<uint32_t>(n0) / d : n0 / tiles, c1 = narrow ? static_cast<uint32_t>(n1) / d : n1 / tiles;
-        for (int64_t c = c0; c < c1; ++c) p.plan.cta_k[c] = k;
+#pragma unroll 1
+    for (int32_t c = ctas + threadIdx.x; c < p.max_ctas; c += kPrologueThreads) p.plan.cta[c].begin = p.plan.cta[c].end = 0;
+    if (threadIdx.x == 0) p.plan.start[live] = tiles;
+#pragma unroll 1
+    for (int32_t u = lo; u < hi; ++u) {
+        if (hi - lo > 1) lengths(u, &top, &low);
+        UnitPieces q{0, 0, 0, 0};
+        if (top > 0) {
+            const int64_t b = at, e = at + (top + kTile - 1) / kTile;
+            p.plan.start[k] = b;
+            p.plan.unit[k] = u;
+            p.plan.max_len[k] = top;
+            p.plan.min_len[k] = low;
+            // Range c is tiles [floor(c*T/C), floor((c+1)*T/C)); the one holding tile x is
+            // floor(((x + 1)*C - 1) / T), and those that start in [b, e) are the c with
+            // ceil(b*C/T) <= c < ceil(e*C/T).
+            q.c_lo = static_cast<int32_t>(quotient((b + 1) * ctas - 1, tiles));
+            q.pieces = static_cast<int32_t>(quotient(e * ctas - 1, tiles)) - q.c_lo + 1;
+            const int32_t c0 = static_cast<int32_t>(quotient(b * ctas + tiles - 1, tiles));
+            const int32_t c1 = static_cast<int32_t>(quotient(e * ctas + tiles - 1, tiles));
+            q.slot_lo = 2 * q.c_lo + (c0 == q.c_lo ? 0 : 1);
+#pragma unroll 1
+            for (int32_t c = c0; c < c1; ++c) cta_k[c] = k;
+            at = e;
+            ++k;
+        }
+        p.plan.pieces[u] = q;
     }
+    __syncthreads();
+#pragma unroll 1
+    for (int32_t c = threadIdx.x; c < ctas; c += kPrologueThreads) {
+        const int32_t first = cta_k[c];
+        const int64_t begin = quotient(c * tiles, ctas), end = quotient((c + 1) * tiles, ctas);
+        p.plan.cta[c] = CtaStart{begin, end, segment(begin, end, c, true, first, p.plan.unit[first], p.plan.start[first],
+                                                     p.plan.start[first + 1], p.plan.max_len[first], p.plan.min_len[first])};
+    }
+    // The status was cleared before the scan's barriers.
+    if (any_over) atomicCAS(p.status, 0, kStatusBounds);
 }
 
 // Query operand of one unit, as the selected decode's prologue makes it: 8 warps x 8 pairs,
@@ -118,16 +149,6 @@ __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
     const int32_t seq = unit / p.groups, first = (unit % p.groups) * kHeadsPerCta;
     const int32_t valid = min(kHeadsPerCta, p.pairs - first);
     const int64_t pair0 = static_cast<int64_t>(seq) * p.pairs + first;
-    bool none = true;
-    for (int32_t i = first / p.heads; i <= (first + valid - 1) / p.heads; ++i) {
-        bool over;
-        none &= row_len(p, seq, i, &over) == 0;
-    }
-    if (none) {
-        uint4* o = reinterpret_cast<uint4*>(p.out + pair0 * kLatent);
-        for (int e = threadIdx.x; e < valid * kLatent / 8; e += kPrologueThreads) o[e] = make_uint4(0, 0, 0, 0);
-        return;
-    }
     uint4 raw[kHeadsPerCta / kWarps][2];
 #pragma unroll
     for (int i = 0; i < kHeadsPerCta / kWarps; ++i) {
@@ -138,6 +159,17 @@ __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
             raw[i][0] = src[0];
             raw[i][1] = src[1];
         }
+    }
+    bool none = true;  // checked while the queries are on their way
+#pragma unroll 1
+    for (int32_t i = first / p.heads; i <= (first + valid - 1) / p.heads; ++i) {
+        bool over;
+        none &= row_len(p, seq, i, &over) == 0;
+    }
+    if (none) {
+        uint4* o = reinterpret_cast<uint4*>(p.out + pair0 * kLatent);
+        for (int e = threadIdx.x; e < valid * kLatent / 8; e += kPrologueThreads) o[e] = make_uint4(0, 0, 0, 0);
+        return;
     }
 #pragma unroll
     for (int i = 0; i < kHeadsPerCta / kWarps; ++i) {
@@ -187,16 +219,8 @@ __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
 __global__ void __launch_bounds__(kPrologueThreads) full_prologue_kernel(const Params p) {
     extern __shared__ __align__(16) uint8_t stage[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0) make_plan(p);
+    if (blockIdx.x == 0) make_plan(p, reinterpret_cast<int32_t*>(stage));
     else prepare(p, blockIdx.x - 1, stage);
-}
-
-// The range that holds tile x. T*ctas fits 32 bits but for the longest caches, and a 64-bit
-// division is a long sequence.
-__device__ __forceinline__ int32_t range_of(const PlanHead& head, int64_t x) {
-    const int64_t n = (x + 1) * head.ctas - 1;
-    if (head.tiles * head.ctas < (int64_t{1} << 32)) return static_cast<int32_t>(static_cast<uint32_t>(n) / static_cast<uint32_t>(head.tiles));
-    return static_cast<int32_t>(n / head.tiles);
 }
 
 // ------------------------------------------------------------------------------------
@@ -214,7 +238,7 @@ constexpr int kFlight = 4;  // pieces whose loads a warp has in flight
 //   kSplit = 8: block (unit, 32 dims, 8-pair group), the warps share the pieces and join
 //               through shared memory; for few units, which the most pieces come with
 template <int kSplit>
-__global__ void __launch_bounds__(kCombineThreads) full_combine_kernel(const Params p) {
+__global__ void __launch_bounds__(kCombineThreads, 5) full_combine_kernel(const Params p) {
     constexpr int kGroups = kCombineWarps / kSplit;  // 8-pair groups of a block
     static_assert(kSplit == 1 || kGroups == 1, "one group, or one warp per group");
     __shared__ float w_s[kCombineWarps][kFlight][8];
@@ -227,17 +251,10 @@ __global__ void __launch_bounds__(kCombineThreads) full_combine_kernel(const Par
     const int group = kSplit > 1 ? blockIdx.z : warp;  // of 8 pairs
     const int part = kSplit > 1 ? warp : 0;            // this warp's share of the pieces
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int32_t k = p.plan.unit_k[unit];
-    if (k < 0) return;  // zeros already
-    const PlanHead head = *p.plan.head;
-    const int64_t begin = p.plan.start[k], end = p.plan.start[k + 1];
-    // The range holding tile x is the last one starting at or before it: floor(((x + 1)*ctas - 1) / T).
-    const int32_t c_lo = range_of(head, begin), c_hi = range_of(head, end - 1);
-    if (c_lo == c_hi) return;  // written whole
-    // Every range between holds this unit first, and so may the first one.
-    const int32_t slot_lo = 2 * c_lo + (p.plan.cta_k[c_lo] == k ? 0 : 1);
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? slot_lo : 2 * (c_lo + i)); };
-    const int pieces = c_hi - c_lo + 1;
+    const UnitPieces q = p.plan.pieces[unit];
+    const int pieces = q.pieces;
+    if (pieces < 2) return;  // written whole, or zeros already
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? q.slot_lo : 2 * (q.c_lo + i)); };
     const uint4* po = reinterpret_cast<const uint4*>(p.part_o) + (static_cast<int64_t>(blockIdx.y) * 8 + group) * kDims + lane;
     constexpr int64_t kPartVecs = kHeadsPerCta * kLatent / 8;
     float acc[8] = {};
