@@ -292,10 +292,10 @@ class StepPlan(NamedTuple):
 
 def alloc_step_plan(rows: int, device=None) -> StepPlan:
     """Output buffers of plan_step, to be kept from step to step (a captured step needs fixed ones)."""
-    # One allocation for all five: five of them cost more on the host than the plan on the GPU.
-    buf = torch.empty(5 * rows + 4, dtype=torch.int32, device=device or "cuda")
-    slots, positions, row_lens, row_seqs, info = buf.split_with_sizes((2 * rows, rows, rows, rows, 4))
-    return StepPlan(slots.view(torch.int64), positions, row_lens, row_seqs, info)
+    device, i32 = device or "cuda", torch.int32
+    return StepPlan(torch.empty(rows, dtype=torch.int64, device=device), torch.empty(rows, dtype=i32, device=device),
+                    torch.empty(rows, dtype=i32, device=device), torch.empty(rows, dtype=i32, device=device),
+                    torch.empty(4, dtype=i32, device=device))
 
 
 def plan_step(base_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor, block_size: int,
