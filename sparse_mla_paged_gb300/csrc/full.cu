@@ -123,8 +123,8 @@ struct Cta {
     // The stretch after s (not its last).
     __device__ Segment next(const Segment& s) const {
         const int32_t k = s.k + 1;
-        return segment(start.begin, start.end, blockIdx.x, false, k, p.plan.unit[k], p.plan.start[k], p.plan.start[k + 1],
-                       p.plan.max_len[k], p.plan.min_len[k]);
+        return segment(start.begin, start.end, start.gap, blockIdx.x, false, k, p.plan.unit[k], p.plan.start[k], p.plan.max_len[k],
+                       p.plan.min_len[k]);
     }
 };
 

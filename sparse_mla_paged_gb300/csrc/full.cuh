@@ -5,11 +5,13 @@
 // into groups of 64 whatever their rows, and a work unit is (sequence, group): few heads and
 // several verify rows fill one unit together. A unit's tokens are [0, max of its rows'
 // lengths); rows that see fewer mask theirs. The units with any token, in order, form a line
-// of 128-token tiles, T in all, that is cut into `ctas` equal ranges: CTA c takes tiles
-// [c*T/ctas, (c+1)*T/ctas). The lengths are on the device, so the plan is made there. A unit
-// inside one range is written straight to the output; one that several ranges share leaves a
-// partial per CTA (slot 2c for the CTA's first unit, 2c+1 for its last) that the combine
-// kernel joins.
+// of 128-token tiles with a gap of up to kGap tiles between units, T long, that is cut into
+// `ctas` equal ranges: CTA c takes the tiles in [c*T/ctas, (c+1)*T/ctas). A gap stands for what
+// a change of unit costs the CTA whose range holds it (output, query operand, first tile):
+// without it those CTAs finish last. The lengths are on the device, so the plan is made there.
+// A unit inside one range is written straight to the output; one that several ranges share
+// leaves a partial per CTA (slot 2c for the CTA's first unit, 2c+1 for its last) that the
+// combine kernel joins.
 #pragma once
 
 #include "common.cuh"
@@ -18,6 +20,7 @@ namespace dsa {
 namespace full {
 
 constexpr int kTile = 128;
+constexpr int kGap = 3;      // tiles of a unit change; less when a range has less than 8 of them a tile
 constexpr int64_t kMaxLen = (int64_t{1} << 31) - 2 * kTile;  // positions stay in 32 bits
 
 // One CTA's stretch of one unit.
@@ -33,6 +36,8 @@ struct Segment {
 struct alignas(16) CtaStart {
     int64_t begin, end;
     Segment first;
+    int64_t gap;
+    int64_t pad;
 };
 
 // Where a unit's pieces are: ranges c_lo .. c_lo + pieces - 1, all in slot 2c but the first
@@ -45,7 +50,7 @@ struct PlanArrays {
     CtaStart* cta;        // [max_ctas]
     UnitPieces* pieces;   // [units]
     // by a live unit's number k:
-    int64_t* start;       // [units + 1] its first tile on the line
+    int64_t* start;       // [units] its first tile on the line
     int32_t* unit;        // [units]
     int32_t* max_len;     // [units] longest length of its rows
     int32_t* min_len;     // [units] shortest
@@ -66,7 +71,7 @@ inline Layout layout(int64_t units, int64_t ctas) {
     L.status = put(256);
     L.cta = put(static_cast<size_t>(ctas) * sizeof(CtaStart));
     L.pieces = put(static_cast<size_t>(units) * sizeof(UnitPieces));
-    L.start = put(static_cast<size_t>(units + 1) * 8);
+    L.start = put(static_cast<size_t>(units) * 8);
     L.unit = put(static_cast<size_t>(units) * 4);
     L.max_len = put(static_cast<size_t>(units) * 4);
     L.min_len = put(static_cast<size_t>(units) * 4);
@@ -111,9 +116,10 @@ __device__ __forceinline__ int32_t row_len(const Params& p, int64_t seq, int32_t
     return n > 0 ? static_cast<int32_t>(n) : 0;
 }
 
-// CTA's stretch of live unit k (tiles [b, e) of the line), given its range and its first unit.
-__device__ __forceinline__ Segment segment(int64_t begin, int64_t end, int32_t cta, bool first, int32_t k, int32_t unit, int64_t b,
-                                           int64_t e, int32_t max_len, int32_t min_len) {
+// CTA's stretch of live unit k, whose first tile is b on the line, given the CTA's range.
+__device__ __forceinline__ Segment segment(int64_t begin, int64_t end, int64_t gap, int32_t cta, bool first, int32_t k, int32_t unit,
+                                           int64_t b, int32_t max_len, int32_t min_len) {
+    const int64_t e = b + (max_len + kTile - 1) / kTile;
     Segment s;
     s.k = k;
     s.unit = unit;
@@ -122,7 +128,7 @@ __device__ __forceinline__ Segment segment(int64_t begin, int64_t end, int32_t c
     s.max_len = max_len;
     s.min_len = min_len;
     s.part = begin <= b && e <= end ? -1 : 2 * cta + (first ? 0 : 1);
-    s.last = e >= end;
+    s.last = e + gap >= end;
     return s;
 }
 #endif

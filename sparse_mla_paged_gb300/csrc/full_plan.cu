@@ -98,30 +98,32 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
     int32_t live;
     scan2(at, k, sa, sb, &tiles, &live);
     const int32_t ctas = static_cast<int32_t>(min(tiles, static_cast<int64_t>(p.max_ctas)));
+    // At most an eighth of a range, so that no range lies inside a gap.
+    const int64_t gap = min(static_cast<int64_t>(kGap), tiles / (8 * p.max_ctas));
+    const int64_t line = tiles + gap * (live - 1);
 #pragma unroll 1
     for (int32_t c = ctas + threadIdx.x; c < p.max_ctas; c += kPrologueThreads) p.plan.cta[c].begin = p.plan.cta[c].end = 0;
-    if (threadIdx.x == 0) p.plan.start[live] = tiles;
 #pragma unroll 1
     for (int32_t u = lo; u < hi; ++u) {
         if (hi - lo > 1) lengths(u, &top, &low);
         UnitPieces q{0, 0, 0, 0};
         if (top > 0) {
-            const int64_t b = at, e = at + (top + kTile - 1) / kTile;
+            const int64_t b = at + gap * k, e = b + (top + kTile - 1) / kTile;
             p.plan.start[k] = b;
             p.plan.unit[k] = u;
             p.plan.max_len[k] = top;
             p.plan.min_len[k] = low;
-            // Range c is tiles [floor(c*T/C), floor((c+1)*T/C)); the one holding tile x is
-            // floor(((x + 1)*C - 1) / T), and those that start in [b, e) are the c with
-            // ceil(b*C/T) <= c < ceil(e*C/T).
-            q.c_lo = static_cast<int32_t>(quotient((b + 1) * ctas - 1, tiles));
-            q.pieces = static_cast<int32_t>(quotient(e * ctas - 1, tiles)) - q.c_lo + 1;
-            const int32_t c0 = static_cast<int32_t>(quotient(b * ctas + tiles - 1, tiles));
-            const int32_t c1 = static_cast<int32_t>(quotient(e * ctas + tiles - 1, tiles));
-            q.slot_lo = 2 * q.c_lo + (c0 == q.c_lo ? 0 : 1);
+            // Range c is [floor(c*T/C), floor((c+1)*T/C)); the one holding tile x is
+            // floor(((x + 1)*C - 1) / T). Unit k is the first of those that start after the unit
+            // before it ended and before it ends itself.
+            q.c_lo = static_cast<int32_t>(quotient((b + 1) * ctas - 1, line));
+            q.pieces = static_cast<int32_t>(quotient(e * ctas - 1, line)) - q.c_lo + 1;
+            const int32_t c0 = static_cast<int32_t>(quotient((k > 0 ? b - gap : 0) * ctas + line - 1, line));
+            const int32_t c1 = static_cast<int32_t>(quotient(e * ctas + line - 1, line));
+            q.slot_lo = 2 * q.c_lo + (c0 <= q.c_lo ? 0 : 1);
 #pragma unroll 1
             for (int32_t c = c0; c < c1; ++c) cta_k[c] = k;
-            at = e;
+            at += e - b;
             ++k;
         }
         p.plan.pieces[u] = q;
@@ -130,9 +132,9 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
 #pragma unroll 1
     for (int32_t c = threadIdx.x; c < ctas; c += kPrologueThreads) {
         const int32_t first = cta_k[c];
-        const int64_t begin = quotient(c * tiles, ctas), end = quotient((c + 1) * tiles, ctas);
-        p.plan.cta[c] = CtaStart{begin, end, segment(begin, end, c, true, first, p.plan.unit[first], p.plan.start[first],
-                                                     p.plan.start[first + 1], p.plan.max_len[first], p.plan.min_len[first])};
+        const int64_t begin = quotient(c * line, ctas), end = quotient((c + 1) * line, ctas);
+        p.plan.cta[c] = CtaStart{begin, end, segment(begin, end, gap, c, true, first, p.plan.unit[first], p.plan.start[first],
+                                                     p.plan.max_len[first], p.plan.min_len[first]), gap, 0};
     }
     // The status was cleared before the scan's barriers.
     if (any_over) atomicCAS(p.status, 0, kStatusBounds);
