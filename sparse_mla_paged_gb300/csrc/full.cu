@@ -322,13 +322,26 @@ __device__ void run_pv(const Cta& c) {
 // ------------------------------------------------------------------------------------
 // softmax / output warps
 // ------------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float x, float y) {
-    return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(x, y) << 16);
+// Two probabilities as two E4M3 terms each (hi: rounded to nearest; lo: what is left of the
+// float16 value, whose own rounding of 2^-12 is far below lo's 2^-9). Through float16 pairs
+// this takes five instructions where single floats take eight.
+__device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+    uint16_t h, l;
+    asm("{\n\t.reg .b32 v, r, d;\n\t"
+        "cvt.rn.f16x2.f32 v, %3, %2;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %0, v;\n\t"
+        "cvt.rn.f16x2.e4m3x2 r, %0;\n\t"
+        "sub.rn.f16x2 d, v, r;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 %1, d;\n\t}"
+        : "=&h"(h), "=h"(l)
+        : "f"(p0), "f"(p1));
+    hi = h;
+    lo = l;
 }
-// x rounded to 4 significant bits (round half up on the magnitude), an E4M3 value in its
-// normal range; the remainder is at most half a unit in its last place.
-__device__ __forceinline__ float hi_part(float x) {
-    return __uint_as_float((__float_as_uint(x) + 0x00080000u) & 0xFFF00000u);
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Makes one token's V bytes of an edge tile safe; returns whether it held a NaN code. Lanes
@@ -454,15 +467,15 @@ __device__ void run_softmax(const Cta& c) {
             __syncwarp();
             if (lane == 0) mbar_arrive(c.bar(BAR_SEMPTY));
 
-            // Scores of pair hq for tokens tok0 .. tok0+31 of the tile: this lane's term plus
-            // the neighbouring lane's other one.
+            // Dots of pair hq with tokens tok0 .. tok0+31 of the tile: this lane's term plus the
+            // neighbouring lane's other one; the score in log2 units is qs (> 0) times that.
             const int tok0 = half * kHalfCols + term * kScores;
             float x[kScores];
 #pragma unroll
             for (int j = 0; j < kScores; ++j) {
                 const float send = __uint_as_float(term ? v[j] : v[kScores + j]);
                 const float mine = __uint_as_float(term ? v[kScores + j] : v[j]);
-                x[j] = (mine + __shfl_xor_sync(0xffffffffu, send, 1)) * qs;
+                x[j] = mine + __shfl_xor_sync(0xffffffffu, send, 1);
             }
             if ((t + 1) * kTile > s.min_len) {  // an edge tile
                 uint8_t* v_tile = c.smem + static_cast<uint32_t>(tau % slots) * slot_bytes + (p.kv_same ? 0 : kTileBytes);
@@ -485,9 +498,9 @@ __device__ void run_softmax(const Cta& c) {
             }
             float hm4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-            for (int j = 0; j < kScores; ++j) hm4[j & 3] = fmaxf(hm4[j & 3], x[j]);
+            for (int j = 0; j < kScores; j += 2) hm4[(j >> 1) & 3] = max3(hm4[(j >> 1) & 3], x[j], x[j + 1]);
             float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
-            hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1));
+            hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1)) * qs;
             // A tile mostly leaves every pair's reference where it is, so P' is formed with it at
             // once; one barrier then tells whether any half of any pair's scores asks for a
             // move (the maximum exceeds the reference by more than the margin, or lies far below
@@ -504,16 +517,17 @@ __device__ void run_softmax(const Cta& c) {
                 const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
 #pragma unroll
                 for (int g = 0; g < kScores / 4; ++g) {
-                    float ph[4], pl[4];
+                    float pp[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float pp = ex2_approx(x[4 * g + e] + off);
-                        ls4[e] += pp;
-                        ph[e] = hi_part(pp);
-                        pl[e] = pp - ph[e];
+                        pp[e] = ex2_approx(fmaf(x[4 * g + e], qs, off));
+                        ls4[e] += pp[e];
                     }
-                    hw[g] = pack_e4m3x4(ph[0], ph[1], ph[2], ph[3]);
-                    lw[g] = pack_e4m3x4(pl[0], pl[1], pl[2], pl[3]);
+                    uint32_t h0, l0, h1, l1;
+                    split2(pp[0], pp[1], h0, l0);
+                    split2(pp[2], pp[3], h1, l1);
+                    hw[g] = h0 | h1 << 16;
+                    lw[g] = l0 | l1 << 16;
                 }
                 fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
                 if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(ask)) break;

@@ -143,9 +143,10 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
 // Query operand of one unit, as the selected decode's prologue makes it: 8 warps x 8 pairs,
 // lane l dims [16l, 16l+16); a head's bf16 query as two E4M3 terms after a scaling by a power
 // of two (exact for elements above 2^-10 of its largest), rows 2k and 2k+1 of a quarter the
-// two terms of pair 16q + k, stored chunk-major. A head with a NaN or an infinity gets zero
-// codes and a NaN scale, which makes all its scores NaN. A unit without a token writes its
-// zeros here.
+// two terms of pair 16q + k, stored chunk-major. The head's scale of its dots is positive (the
+// decode takes maxima of the dots): a negative score scale turns the codes' signs, a zero one
+// zeroes the codes. A head with a NaN or an infinity gets zero codes and a NaN scale, which
+// makes all its scores NaN. A unit without a token writes its zeros here.
 __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t seq = unit / p.groups, first = (unit % p.groups) * kHeadsPerCta;
@@ -186,7 +187,9 @@ __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
         const bool broken = E == 255;
         int e = amax > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
         e = e > 126 ? 126 : (e < -126 ? -126 : e);
-        const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+        const float back = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float sign = p.score_scale > 0.0f ? 1.0f : (p.score_scale < 0.0f ? -1.0f : 0.0f);
+        const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * sign;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -207,7 +210,8 @@ __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
             make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (lane == 0)
             p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hl] =
-                broken ? __uint_as_float(0x7FC00000u) : p.score_scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                broken || p.score_scale != p.score_scale ? __uint_as_float(0x7FC00000u)
+                                                         : fmaxf(fabsf(p.score_scale) * back, 0x1p-120f);
     }
     __syncthreads();
     uint8_t* img = p.qimg + static_cast<int64_t>(unit) * kQImageBytes;

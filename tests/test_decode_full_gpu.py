@@ -104,6 +104,14 @@ def test_buffers_and_tables(api):
     Case(3, 1, 64, [500, 20, 801], shared=True).check(api)
 
 
+def test_any_score_scale(api):
+    """Negative and zero scales, and ones that make scores large."""
+    for sm in (-(512 ** -0.5), 0.0, 0.3):
+        c = Case(2, 2, 24, [700, 300, 128, 0])
+        c.scales = (0.05, 0.05, sm)
+        c.check(api)
+
+
 def test_sharp_and_flat_scores(api):
     Case(2, 1, 64, [1500, 900], q_scale=12.0).check(api)
     Case(2, 1, 64, [1500, 900], q_scale=0.0).check(api)
