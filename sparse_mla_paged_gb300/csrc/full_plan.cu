@@ -10,7 +10,7 @@ namespace dsa {
 namespace full {
 namespace {
 
-constexpr int kPrologueThreads = 256;
+constexpr int kPrologueThreads = 512;
 constexpr int kWarps = kPrologueThreads / 32;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -140,7 +140,7 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
     if (any_over) atomicCAS(p.status, 0, kStatusBounds);
 }
 
-// Query operand of one unit, as the selected decode's prologue makes it: 8 warps x 8 pairs,
+// Query operand of one unit, as the selected decode's prologue makes it: 16 warps x 4 pairs,
 // lane l dims [16l, 16l+16); a head's bf16 query as two E4M3 terms after a scaling by a power
 // of two (exact for elements above 2^-10 of its largest), rows 2k and 2k+1 of a quarter the
 // two terms of pair 16q + k, stored chunk-major. The head's scale of its dots is positive (the
