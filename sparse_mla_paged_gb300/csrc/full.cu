@@ -696,7 +696,6 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     c.tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
     // Everything above overlaps the prologue; its plan is read only after this.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     c.start = p.plan.cta[blockIdx.x];
     if (c.start.begin < c.start.end) {
         if (warp < R::kLoadWarps) {
@@ -722,6 +721,8 @@ __global__ void __launch_bounds__(Roles<kTma>::kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // The join's blocks, let in while others compute, would take issue slots from them.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == R::kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(c.tmem, kTmemCols);
