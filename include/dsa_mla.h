@@ -344,8 +344,8 @@ int32_t dsa_mla_decode_static(const void* q, const void* k_cache, const void* v_
  *  base_lens, new_lens  int32 [num_seqs].  free_pages  int32 [num_free] page ids >= 0.
  *  block_tables  int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq >= 1.
  *  slots  int64 [max_rows], 8-byte aligned; positions, row_lens, row_seqs  int32 [max_rows].
- *  info   int32 [4]: rows with a token, pages taken, status, 0. A caller advances its free
- *         list by info[1]. The status is DSA_ERR_DEVICE_BOUNDS when a length is negative
+ *  info   int32 [4]: new tokens (cut to the rows there are), pages taken, status, 0. A caller
+ *         advances its free list by info[1]. The status is DSA_ERR_DEVICE_BOUNDS when a length is negative
  *         (taken as 0), a request has more new tokens than rows_per_seq (cut to it) or than
  *         its table holds (the tokens past the table have rows without a token), the packed
  *         rows exceed max_rows (the last ones are dropped; their pages are assigned), the
@@ -426,9 +426,9 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
  * DSA_ERR_DEVICE_BOUNDS and its positions are skipped), except:
  *  seq_lens     verify_rows = 0: int32 [R], len(r) = seq_lens[r]; verify_rows = 1: int32
  *               [num_seqs], len of row i of sequence s = seq_lens[s] + i + 1 (decode_k.rs,
- *               decode_k). A position past every row's length is never read; a NaN there or
- *               at a position that only other rows see does not reach a row's output, and
- *               one that a row sees makes that row NaN.
+ *               decode_k). What a position past a row's length holds, a NaN code in the
+ *               row's last page or one that only other rows see, does not reach the row's
+ *               output; a NaN code that it sees does.
  *  workspace    device memory, 256-byte aligned, at least
  *               dsa_mla_decode_full_workspace_bytes of the same num_seqs, rows_per_seq and
  *               num_q_heads. The call never allocates and can be captured. Its first 256

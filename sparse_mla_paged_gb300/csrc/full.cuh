@@ -56,6 +56,64 @@ struct PlanArrays {
     int32_t* min_len;     // [units] shortest
 };
 
+// ------------------------------------------------------------------------------------
+// The plan's arithmetic (host and device: the tests run it on the host).
+// ------------------------------------------------------------------------------------
+// n / d for n >= 0, d > 0. They fit 32 bits but for the longest caches, and a 64-bit division
+// is a long sequence. Out of line: the plan runs once, and what its code weighs in instruction
+// fetches is most of its time.
+#ifdef __CUDACC__
+__host__ __device__ __noinline__
+#endif
+static int64_t quotient(int64_t n, int64_t d) {
+    if (n >> 32 == 0 && d >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+
+struct Line {
+    int64_t length, gap;
+    int32_t ctas;  // ranges; none is empty
+};
+__host__ __device__ inline Line make_line(int64_t tiles, int32_t live, int32_t max_ctas) {
+    Line l;
+    l.ctas = static_cast<int32_t>(tiles < max_ctas ? tiles : max_ctas);
+    // At most an eighth of a range, so that no range lies inside a gap.
+    l.gap = tiles / (8 * max_ctas);
+    if (l.gap > kGap) l.gap = kGap;
+    l.length = tiles + l.gap * (live > 0 ? live - 1 : 0);
+    return l;
+}
+// Range c is [floor(c*T/C), floor((c+1)*T/C)).
+__host__ __device__ inline int64_t range_begin(const Line& l, int64_t c) { return quotient(c * l.length, l.ctas); }
+// Pieces of live unit k, at [b, e) of the line: the range that holds tile x is
+// floor(((x + 1)*C - 1) / T). The unit is the first of the ranges [*c0, *c1), which start
+// after the unit before it ended and before it ends itself.
+__host__ __device__ inline UnitPieces unit_pieces(const Line& l, int32_t k, int64_t b, int64_t e, int32_t* c0, int32_t* c1) {
+    UnitPieces q;
+    q.c_lo = static_cast<int32_t>(quotient((b + 1) * l.ctas - 1, l.length));
+    q.pieces = static_cast<int32_t>(quotient(e * l.ctas - 1, l.length)) - q.c_lo + 1;
+    *c0 = static_cast<int32_t>(quotient((k > 0 ? b - l.gap : 0) * l.ctas + l.length - 1, l.length));
+    *c1 = static_cast<int32_t>(quotient(e * l.ctas + l.length - 1, l.length));
+    q.slot_lo = 2 * q.c_lo + (*c0 <= q.c_lo ? 0 : 1);
+    q.pad = 0;
+    return q;
+}
+// CTA's stretch of live unit k, whose first tile is b on the line, given the CTA's range.
+__host__ __device__ inline Segment segment(int64_t begin, int64_t end, int64_t gap, int32_t cta, bool first, int32_t k, int32_t unit,
+                                           int64_t b, int32_t max_len, int32_t min_len) {
+    const int64_t e = b + (max_len + kTile - 1) / kTile;
+    Segment s;
+    s.k = k;
+    s.unit = unit;
+    s.t0 = static_cast<int32_t>((begin > b ? begin : b) - b);
+    s.t1 = static_cast<int32_t>((end < e ? end : e) - b);
+    s.max_len = max_len;
+    s.min_len = min_len;
+    s.part = begin <= b && e <= end ? -1 : 2 * cta + (first ? 0 : 1);
+    s.last = e + gap >= end;
+    return s;
+}
+
 struct Layout {
     size_t status, cta, pieces, start, unit, max_len, min_len, qimg, qscale, part_o, part_lse, total;
 };
@@ -114,22 +172,6 @@ __device__ __forceinline__ int32_t row_len(const Params& p, int64_t seq, int32_t
     *over = n > room;
     if (n > room) n = room;
     return n > 0 ? static_cast<int32_t>(n) : 0;
-}
-
-// CTA's stretch of live unit k, whose first tile is b on the line, given the CTA's range.
-__device__ __forceinline__ Segment segment(int64_t begin, int64_t end, int64_t gap, int32_t cta, bool first, int32_t k, int32_t unit,
-                                           int64_t b, int32_t max_len, int32_t min_len) {
-    const int64_t e = b + (max_len + kTile - 1) / kTile;
-    Segment s;
-    s.k = k;
-    s.unit = unit;
-    s.t0 = static_cast<int32_t>((begin > b ? begin : b) - b);
-    s.t1 = static_cast<int32_t>((end < e ? end : e) - b);
-    s.max_len = max_len;
-    s.min_len = min_len;
-    s.part = begin <= b && e <= end ? -1 : 2 * cta + (first ? 0 : 1);
-    s.last = e + gap >= end;
-    return s;
 }
 #endif
 

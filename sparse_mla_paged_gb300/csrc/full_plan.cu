@@ -50,14 +50,6 @@ __device__ __forceinline__ void scan2(int64_t& a, int32_t& b, int64_t* sa, int32
     b = pb + ib - b;
 }
 
-// n / d for n, d > 0. They fit 32 bits but for the longest caches, and a 64-bit division is a
-// long sequence. Out of line: the plan runs once, and what its code weighs in instruction
-// fetches is most of its time.
-__device__ __noinline__ int64_t quotient(int64_t n, int64_t d) {
-    if (n >> 32 == 0) return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
-    return n / d;
-}
-
 // One block: the line of tiles (see full.cuh). Thread t has units [t*per, (t+1)*per): a sweep
 // sums their tiles, one scan gives every unit its place, a second sweep writes the units'
 // entries and which unit each range starts in (cta_k, shared memory), and thread c then writes
@@ -97,30 +89,21 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
     int64_t tiles;
     int32_t live;
     scan2(at, k, sa, sb, &tiles, &live);
-    const int32_t ctas = static_cast<int32_t>(min(tiles, static_cast<int64_t>(p.max_ctas)));
-    // At most an eighth of a range, so that no range lies inside a gap.
-    const int64_t gap = min(static_cast<int64_t>(kGap), tiles / (8 * p.max_ctas));
-    const int64_t line = tiles + gap * (live - 1);
+    const Line line = make_line(tiles, live, p.max_ctas);
 #pragma unroll 1
-    for (int32_t c = ctas + threadIdx.x; c < p.max_ctas; c += kPrologueThreads) p.plan.cta[c].begin = p.plan.cta[c].end = 0;
+    for (int32_t c = line.ctas + threadIdx.x; c < p.max_ctas; c += kPrologueThreads) p.plan.cta[c].begin = p.plan.cta[c].end = 0;
 #pragma unroll 1
     for (int32_t u = lo; u < hi; ++u) {
         if (hi - lo > 1) lengths(u, &top, &low);
         UnitPieces q{0, 0, 0, 0};
         if (top > 0) {
-            const int64_t b = at + gap * k, e = b + (top + kTile - 1) / kTile;
+            const int64_t b = at + line.gap * k, e = b + (top + kTile - 1) / kTile;
             p.plan.start[k] = b;
             p.plan.unit[k] = u;
             p.plan.max_len[k] = top;
             p.plan.min_len[k] = low;
-            // Range c is [floor(c*T/C), floor((c+1)*T/C)); the one holding tile x is
-            // floor(((x + 1)*C - 1) / T). Unit k is the first of those that start after the unit
-            // before it ended and before it ends itself.
-            q.c_lo = static_cast<int32_t>(quotient((b + 1) * ctas - 1, line));
-            q.pieces = static_cast<int32_t>(quotient(e * ctas - 1, line)) - q.c_lo + 1;
-            const int32_t c0 = static_cast<int32_t>(quotient((k > 0 ? b - gap : 0) * ctas + line - 1, line));
-            const int32_t c1 = static_cast<int32_t>(quotient(e * ctas + line - 1, line));
-            q.slot_lo = 2 * q.c_lo + (c0 <= q.c_lo ? 0 : 1);
+            int32_t c0, c1;
+            q = unit_pieces(line, k, b, e, &c0, &c1);
 #pragma unroll 1
             for (int32_t c = c0; c < c1; ++c) cta_k[c] = k;
             at += e - b;
@@ -130,11 +113,11 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
     }
     __syncthreads();
 #pragma unroll 1
-    for (int32_t c = threadIdx.x; c < ctas; c += kPrologueThreads) {
+    for (int32_t c = threadIdx.x; c < line.ctas; c += kPrologueThreads) {
         const int32_t first = cta_k[c];
-        const int64_t begin = quotient(c * line, ctas), end = quotient((c + 1) * line, ctas);
-        p.plan.cta[c] = CtaStart{begin, end, segment(begin, end, gap, c, true, first, p.plan.unit[first], p.plan.start[first],
-                                                     p.plan.max_len[first], p.plan.min_len[first]), gap, 0};
+        const int64_t begin = range_begin(line, c), end = range_begin(line, c + 1);
+        p.plan.cta[c] = CtaStart{begin, end, segment(begin, end, line.gap, c, true, first, p.plan.unit[first], p.plan.start[first],
+                                                     p.plan.max_len[first], p.plan.min_len[first]), line.gap, 0};
     }
     // The status was cleared before the scan's barriers.
     if (any_over) atomicCAS(p.status, 0, kStatusBounds);

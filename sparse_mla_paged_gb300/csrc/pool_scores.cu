@@ -366,7 +366,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
             if (page >= 0) {
                 tma_box3(b.sbase + e * kTileBytes + lane * box_codes, tmap, row, page, full);
                 bulk_g2s(smem_u32(scales) + lane * box_scales,
-                         p.cache + page * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + row * 4, box_scales, full);
+                         p.cache + page * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + static_cast<int64_t>(row) * 4, box_scales, full);
             }
             __syncwarp();
         }

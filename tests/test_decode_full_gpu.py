@@ -78,7 +78,7 @@ class Case:
     (4, 1, 64, [0, 1, 0, 300], 64), (2, 1, 1, [700, 0], 64), (1, 1, 128, [1000], 64), (2, 1, 96, [333, 2000], 48),
     (1, 1, 200, [150], 16), (5, 2, 24, [0, 5, 100, 7, 300, 301, 64, 0, 513, 1], 100), (2, 4, 16, [700, 3, 0, 129, 1, 128, 900, 64], 64),
     (1, 3, 40, [1, 2, 3], 1), (1, 9, 8, [80 * i for i in range(9)], 128), (70, 1, 64, [100, 260, 33], 64),
-    (300, 1, 8, [40, 0, 129], 32), (1, 1, 64, [6000], 64), (2, 1, 64, [3000, 4500], 7)])
+    (300, 1, 8, [40, 0, 129], 32), (1, 1, 64, [6000], 64), (2, 1, 64, [900, 257], 256), (2, 2, 16, [900, 257, 1, 384], 384), (2, 1, 64, [3000, 4500], 7)])
 def test_full(api, n, rps, heads, lens, bs):
     Case(n, rps, heads, lens, bs).check(api)
 
@@ -101,6 +101,8 @@ def test_buffers_and_tables(api):
     Case(2, 1, 64, [500, 801], two=True).check(api)
     Case(2, 2, 24, [500, 801, 3, 64], two=True, pad=48).check(api)
     Case(2, 1, 64, [500, 801], pad=16 * 5, bs=16).check(api)
+    Case(2, 1, 64, [500, 801], two=True, bs=256, pad=32).check(api)
+    Case(1, 3, 24, [500, 801, 0], two=True, bs=20).check(api)
     Case(3, 1, 64, [500, 20, 801], shared=True).check(api)
 
 

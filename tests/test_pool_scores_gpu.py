@@ -79,7 +79,7 @@ class Case:
     (2, 4, 32, list(range(992, 1000)), 64, 4), (1, 3, 20, [5000, 4999, 17], 48, 3), (2, 1, 128, [1023, 300], 64, 8),
     (2, 3, 128, [300], 100, 5), (1, 7, 40, [900, 0, 5, 127, 128, 130, 890], 128, 16), (1, 1, 64, [2000], 1, 4),
     (1, 2, 64, [2000, 1999], 7, 7), (2, 1, 48, [640, 1300], 32, 128), (1, 1, 64, [900], 64, 127), (1, 1, 64, [900], 64, 65),
-    (1, 300, 16, list(range(300)), 64, 4), (1, 130, 64, list(range(200, 330)), 64, 4), (40, 1, 64, [100, 2000], 64, 4)])
+    (1, 300, 16, list(range(300)), 64, 4), (2, 1, 64, [900, 1300], 256, 4), (1, 2, 64, [2000, 5], 16, 4), (1, 1, 32, [1500], 384, 2), (1, 130, 64, list(range(200, 330)), 64, 4), (40, 1, 64, [100, 2000], 64, 4)])
 def test_scores(api, n, rps, heads, q_pos, bs, kpool):
     Case(n, rps, heads, q_pos, bs, kpool).check(api)
 
