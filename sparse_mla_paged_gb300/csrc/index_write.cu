@@ -32,6 +32,8 @@ __device__ __forceinline__ void unpack8(const uint4 v, float* f) {
     }
 }
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -83,19 +85,21 @@ __global__ void __launch_bounds__(kIndexWriteThreads) index_write_kernel(const I
         row += step;
         fetch(row);
         if constexpr (kNorm) {
-            float s = 0.0f;
+            // Two dims an instruction.
+            float2* y2 = reinterpret_cast<float2*>(y);
+            const float2 *w2 = reinterpret_cast<const float2*>(w), *b2 = reinterpret_cast<const float2*>(b);
+            float2 s = make_float2(0.0f, 0.0f), ss = s;
 #pragma unroll
-            for (int k = 0; k < kDims; ++k) s += y[k];
-            const float mean = row_sum(s) * (1.0f / kIndexDim);
-            float ss = 0.0f;
+            for (int k = 0; k < kDims / 2; ++k) s = __fadd2_rn(s, y2[k]);
+            const float2 mean = both(row_sum(s.x + s.y) * (-1.0f / kIndexDim));
 #pragma unroll
-            for (int k = 0; k < kDims; ++k) {
-                y[k] -= mean;
-                ss = fmaf(y[k], y[k], ss);
+            for (int k = 0; k < kDims / 2; ++k) {
+                y2[k] = __fadd2_rn(y2[k], mean);
+                ss = __ffma2_rn(y2[k], y2[k], ss);
             }
-            const float inv = rsqrtf(row_sum(ss) * (1.0f / kIndexDim) + p.eps);
+            const float2 inv = both(rsqrtf(row_sum(ss.x + ss.y) * (1.0f / kIndexDim) + p.eps));
 #pragma unroll
-            for (int k = 0; k < kDims; ++k) y[k] = fmaf(y[k] * inv, w[k], b[k]);
+            for (int k = 0; k < kDims / 2; ++k) y2[k] = __ffma2_rn(__fmul2_rn(y2[k], inv), w2[k], b2[k]);
         }
         float top = 0x1p-100f;
 #pragma unroll
