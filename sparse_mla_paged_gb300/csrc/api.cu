@@ -697,6 +697,7 @@ int32_t dsa_plan_step(const int32_t* base_lens, const int32_t* new_lens, int32_t
     p.num_free = num_free;
     p.block_size = block_size;
     p.max_blocks = max_blocks_per_seq;
+    p.by_block = fast_div(static_cast<uint32_t>(block_size));
     return from_cuda(launch_plan(p, d->sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -725,6 +726,7 @@ int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* n
     p.rows = rows;
     p.block_size = block_size;
     p.eps = eps;
+    p.by_block = fast_div(static_cast<uint32_t>(block_size));
     return from_cuda(launch_index_write(p, d->sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -766,6 +768,8 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.kpool = kpool;
     p.n_pools = n_pools;
+    p.by_block = fast_div(static_cast<uint32_t>(block_size));
+    p.by_kpool = fast_div(static_cast<uint32_t>(kpool));
     // Boxes also need tiles of 128 tokens, that is pools that divide them.
     p.box_rows = 128 % kpool == 0 ? box_rows(block_size) : 0;
     CUtensorMap tmap;
@@ -844,6 +848,7 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     p.block_size = block_size;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.verify_rows = verify_rows;
+    p.by_block = fast_div(static_cast<uint32_t>(block_size));
     p.kv_same = k_cache == v_cache ? 1 : 0;
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;

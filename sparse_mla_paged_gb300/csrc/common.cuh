@@ -44,6 +44,31 @@ constexpr float kRescaleFloor = 64.0f;
 constexpr int kStatusBounds = DSA_ERR_DEVICE_BOUNDS;
 constexpr int kStatusTimeout = DSA_ERR_TIMEOUT;
 
+// Division of any 32-bit x by a divisor known on the host, in five instructions (Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication", 1994, figure 4.1); the
+// plain one goes through the conversion and reciprocal units.
+struct FastDiv {
+    uint32_t d, m, s1, s2;
+};
+inline FastDiv fast_div(uint32_t d) {
+    uint32_t l = 0;
+    while (l < 32 && (uint64_t{1} << l) < d) ++l;
+    FastDiv f;
+    f.d = d;
+    f.m = static_cast<uint32_t>(((uint64_t{1} << 32) * ((uint64_t{1} << l) - d)) / d + 1);
+    f.s1 = l < 1 ? l : 1;
+    f.s2 = l < 1 ? 0 : l - 1;
+    return f;
+}
+__host__ __device__ inline uint32_t divide(uint32_t x, const FastDiv& f) {
+#ifdef __CUDA_ARCH__
+    const uint32_t t = __umulhi(f.m, x);
+#else
+    const uint32_t t = static_cast<uint32_t>((static_cast<uint64_t>(f.m) * x) >> 32);
+#endif
+    return (t + ((x - t) >> f.s1)) >> f.s2;
+}
+
 // ------------------------------------------------------------------------------------
 // Workspace layout (all offsets 256-byte aligned).
 // ------------------------------------------------------------------------------------
@@ -224,6 +249,7 @@ struct PlanParams {
     int32_t* row_seqs;         // [rows]
     int32_t* info;             // rows with a token, pages taken, status, 0
     int32_t num_seqs, rows_per_seq, rows, num_free, block_size, max_blocks;
+    FastDiv by_block;          // block_size
 };
 
 struct IndexWriteParams {
@@ -234,6 +260,7 @@ struct IndexWriteParams {
     uint8_t* cache;
     int64_t page_stride;
     int32_t rows, block_size;
+    FastDiv by_block;          // block_size
     float eps;
 };
 
@@ -248,6 +275,7 @@ struct PoolScoresParams {
     int64_t page_stride;
     int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, kpool, n_pools;
     int32_t box_rows;          // tokens of a tensor-map box, 0: per-thread copies
+    FastDiv by_block, by_kpool;
 };
 
 // Launchers (each defined next to its kernel).

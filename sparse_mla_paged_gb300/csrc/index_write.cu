@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(kIndexWriteThreads) index_write_kernel(const I
         if (at >= 0) {
             int64_t page, off;
             if (at >> 32 == 0) {  // a 64-bit division is a long sequence
-                const uint32_t u = static_cast<uint32_t>(at), bs = static_cast<uint32_t>(p.block_size), q = u / bs;
+                const uint32_t u = static_cast<uint32_t>(at), q = divide(u, p.by_block);
                 page = q;
-                off = u - q * bs;
+                off = u - q * p.by_block.d;
             } else {
                 page = at / p.block_size;
                 off = at % p.block_size;

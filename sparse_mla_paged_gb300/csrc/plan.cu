@@ -38,9 +38,8 @@ struct Request {
     bool bad;
 };
 __device__ __forceinline__ uint32_t pages_of(const PlanParams& p, uint32_t tokens) {
-    const uint32_t bs = static_cast<uint32_t>(p.block_size);
-    const uint32_t q = tokens / bs;
-    return min(q + (tokens != q * bs ? 1u : 0u), static_cast<uint32_t>(p.max_blocks));
+    const uint32_t q = divide(tokens, p.by_block);
+    return min(q + (tokens != q * p.by_block.d ? 1u : 0u), static_cast<uint32_t>(p.max_blocks));
 }
 __device__ __forceinline__ Request request(const PlanParams& p, int32_t s) {
     Request r;
@@ -116,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         bad |= r.bad;
         // The page that the first new token shares with cached ones has to be there already.
         if (blockIdx.x == 0 && r.fresh > 0) {
-            const uint32_t blk = r.base / static_cast<uint32_t>(p.block_size);
+            const uint32_t blk = divide(r.base, p.by_block);
             if (blk < r.have) bad |= p.tables[static_cast<int64_t>(s) * p.max_blocks + blk] < 0;
         }
     }
@@ -140,40 +139,52 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
         const int64_t have = request(p, s).have;
         p.tables[static_cast<int64_t>(s) * p.max_blocks + have + (e - g0[s])] = e < p.num_free ? p.free_pages[e] : -1;
     }
-    const uint32_t bs = static_cast<uint32_t>(p.block_size);
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kPlanWarps;
     for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kPlanWarps + warp) * kRowsPerWarp; r0 < p.rows; r0 += warps * kRowsPerWarp) {
-        int32_t seq[kTurns];
         uint32_t pos[kTurns], off[kTurns];
-        int32_t page[kTurns];
+        int32_t seq[kTurns], page[kTurns];
+        // Where token i of request s goes.
+        auto place = [&](int j, int32_t s, const Request& r, uint32_t i) {
+            const uint32_t at = r.base + i, blk = divide(at, p.by_block);
+            if (i >= r.fresh || blk >= static_cast<uint32_t>(p.max_blocks)) return;
+            seq[j] = s;
+            pos[j] = at;
+            off[j] = at - blk * p.by_block.d;
+            const int64_t g = static_cast<int64_t>(g0[s]) + blk - r.have;
+            if (blk < r.have) page[j] = p.tables[static_cast<int64_t>(s) * p.max_blocks + blk];
+            else if (g < p.num_free) page[j] = p.free_pages[g];
+        };
 #pragma unroll
         for (int j = 0; j < kTurns; ++j) {
-            const int64_t row = r0 + 32 * j + lane;
-            int32_t s = -1;
-            uint32_t i = 0;
-            if (row < p.rows) {
-                if (p.rows_per_seq > 0) {
-                    s = static_cast<int32_t>(row) / p.rows_per_seq;
-                    i = static_cast<uint32_t>(static_cast<int32_t>(row) - s * p.rows_per_seq);
-                } else if (row < all_tokens) {
-                    s = last_at_most(t0, n, static_cast<int32_t>(row));
-                    i = static_cast<uint32_t>(static_cast<int32_t>(row) - t0[s]);
-                }
-            }
-            seq[j] = -1;
+            seq[j] = page[j] = -1;
             pos[j] = 0xFFFFFFFFu;
             off[j] = 0;
-            page[j] = -1;
-            if (s >= 0) {
-                const Request r = request(p, s);
-                const uint32_t at = r.base + i, blk = at / bs;
-                if (i < r.fresh && blk < static_cast<uint32_t>(p.max_blocks)) {
-                    seq[j] = s;
-                    pos[j] = at;
-                    off[j] = at - blk * bs;
-                    const int64_t g = static_cast<int64_t>(g0[s]) + blk - r.have;
-                    if (blk < r.have) page[j] = p.tables[static_cast<int64_t>(s) * p.max_blocks + blk];
-                    else if (g < p.num_free) page[j] = p.free_pages[g];
+        }
+        if (p.rows_per_seq > 0) {
+#pragma unroll
+            for (int j = 0; j < kTurns; ++j) {
+                const int64_t row = r0 + 32 * j + lane;
+                if (row >= p.rows) continue;
+                const int32_t s = static_cast<int32_t>(row) / p.rows_per_seq;
+                place(j, s, request(p, s), static_cast<uint32_t>(static_cast<int32_t>(row) - s * p.rows_per_seq));
+            }
+        } else if (r0 < all_tokens) {
+            // A prompt's tokens mostly fill the warp's rows: one search then does for all.
+            const int32_t s0 = last_at_most(t0, n, static_cast<int32_t>(r0));
+            if (t0[s0 + 1] - r0 >= kRowsPerWarp) {
+                const Request r = request(p, s0);
+#pragma unroll
+                for (int j = 0; j < kTurns; ++j) {
+                    const int64_t row = r0 + 32 * j + lane;
+                    if (row < p.rows) place(j, s0, r, static_cast<uint32_t>(static_cast<int32_t>(row) - t0[s0]));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kTurns; ++j) {
+                    const int64_t row = r0 + 32 * j + lane;
+                    if (row >= p.rows || row >= all_tokens) continue;
+                    const int32_t s = last_at_most(t0, n, static_cast<int32_t>(row));
+                    place(j, s, request(p, s), static_cast<uint32_t>(static_cast<int32_t>(row) - t0[s]));
                 }
             }
         }

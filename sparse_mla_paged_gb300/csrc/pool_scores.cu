@@ -169,7 +169,7 @@ struct Block {
     }
     __device__ int32_t visible(int32_t row) const {
         const int32_t q = __ldg(p.q_pos + row);  // (q + 1) / kpool in 32 bits: q + 1 <= 2^31
-        return q < 0 ? 0 : min(static_cast<int32_t>((static_cast<uint32_t>(q) + 1u) / static_cast<uint32_t>(p.kpool)), p.n_pools);
+        return q < 0 ? 0 : min(static_cast<int32_t>(divide(static_cast<uint32_t>(q) + 1u, p.by_kpool)), p.n_pools);
     }
     __device__ Unit unit(int32_t u) const {
         Unit x;
@@ -337,7 +337,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
             const int32_t pos = t * kTile + lane * p.box_rows;
             *row = 0;
             if (!mine || t >= t1 || pos >= limit) return -2;
-            const int32_t blk = pos / p.block_size;
+            const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block));
             *row = pos - blk * p.block_size;
             return p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq ? max(__ldg(table + blk), -1) : -1;
         };
@@ -408,7 +408,7 @@ __device__ void run_load(const Block<kCols>& b) {
             const int tk = tk0 + 32 * i;
             const int32_t pos = t * tokens + tk;
             if (t >= t1 || tk >= tokens || pos >= limit) return;
-            const int32_t blk = pos / p.block_size, off = pos - blk * p.block_size;
+            const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block)), off = pos - blk * p.block_size;
             const int32_t page = (p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq) ? __ldg(table + blk) : -1;
             code = page < 0 ? kBad : page * p.page_stride + static_cast<int64_t>(off) * kIndexDim;
             to_scale = static_cast<int64_t>(p.block_size) * kIndexDim - static_cast<int64_t>(off) * (kIndexDim - 4);

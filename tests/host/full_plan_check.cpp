@@ -1,8 +1,8 @@
 // Host-side checks of the full-cache decode's work plan (csrc/full.cuh): walking every CTA's
 // stretches as the kernel does, every tile of every unit is covered exactly once, a unit is
 // either written whole by one CTA or leaves pieces in exactly the slots where the join looks
-// for them, and every range has a first unit and at least one tile. Exits non-zero on the
-// first failure.
+// for them, and every range has a first unit and at least one tile. Also the division by a
+// divisor known on the host (csrc/common.cuh). Exits non-zero on the first failure.
 #include <algorithm>
 #include <cstdio>
 #include <map>
@@ -86,6 +86,14 @@ int main() {
             }
         }
         CHECK(found == slots.size(), "trial %d: %zu of %zu slots", trial, found, slots.size());
+    }
+    for (int trial = 0; trial < 200000; ++trial) {
+        const uint32_t few[] = {1, 2, 3, 7, 16, 48, 64, 100, 127, 128, 0x7FFFFFFFu, 0x40000000u, 0x40000001u};
+        const uint32_t d = trial < 13 ? few[trial] : 1u + static_cast<uint32_t>(g() >> (33 + g() % 31)) % 0x7FFFFFFFu;
+        const dsa::FastDiv f = dsa::fast_div(d);
+        const uint32_t q = 0xFFFFFFFFu / d;
+        const uint32_t xs[] = {0, 1, d - 1, d, d + 1, q * d, q * d - 1, 0x7FFFFFFFu, 0x80000000u, 0xFFFFFFFFu, static_cast<uint32_t>(g())};
+        for (uint32_t x : xs) CHECK(dsa::divide(x, f) == x / d, "%u / %u", x, d);
     }
     std::printf("full plan ok\n");
     return 0;
