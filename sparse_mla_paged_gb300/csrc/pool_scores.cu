@@ -42,7 +42,6 @@ constexpr int kLoadTurns = 2;                    // of 32 tokens
 constexpr int kTileBytes = kTile * kIndexDim;    // 16 KB of codes
 constexpr int kBarEpilogue = 1;
 constexpr int kFillPools = 4096;                 // pools of one piece of the fill with -inf
-constexpr int kChunk = 16;                       // columns of a tensor-memory load
 
 // Variants by the columns (rows x padded heads) that one unit's MMAs take: MMA N.
 template <int kCols>
@@ -52,6 +51,7 @@ struct Shape {
     static constexpr int kEpiWarps = kCols / 16;       // 64 columns, whose weights fit its registers, a warp
     static constexpr int kSets = kEpiWarps / 4;        // warps that share a lane quarter
     static constexpr int kWeights = kCols / kSets;     // columns of a warp: 64
+    static constexpr int kChunk = kCols == 64 ? 8 : 16;  // columns of a tensor-memory load, as registers allow
     static constexpr int kDBufs = 4;
     // MMA warps, and load warps of boxes, that take tiles in turn. Each has to meet every phase of
     // its barriers (a wait for a phase that has not begun passes as the one before it), so the
@@ -102,32 +102,26 @@ __device__ __forceinline__ void fma_relu4(float (&acc)[4], const float* w, const
     acc[3] = fmaf(w[3], x3 + fabsf(x3), acc[3]);
 }
 
-// Maximum over the kpool (1, 2, 4, .., 32) neighbouring lanes of a pool, in every first one.
-__device__ __forceinline__ float pool_max(float s, int32_t kpool) {
-    auto step = [&](int o) { s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o)); };
-    if (kpool == 1) return s;
-    step(1);
-    if (kpool == 2) return s;
-    step(2);
-    if (kpool == 4) return s;
-    step(4);
-    if (kpool == 8) return s;
-    step(8);
-    if (kpool == 16) return s;
-    step(16);
-    return s;
-}
-
 // Columns of a lane in two steps: the load, and the wait that makes its registers valid (they
 // are operands of the wait so that no use moves ahead of it).
-__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&v)[kChunk]) {
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(at));
 }
-__device__ __forceinline__ void wait_columns(uint32_t (&v)[kChunk]) {
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(at));
+}
+__device__ __forceinline__ void wait_columns(uint32_t (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+                 :: "memory");
+}
+__device__ __forceinline__ void wait_columns(uint32_t (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
                    "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
@@ -502,6 +496,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
     const PoolScoresParams& p = b.p;
     constexpr bool kHalves = kHeads > S::kWeights;                // two warps have half of a row each
     constexpr int kRows = kHalves ? 1 : S::kWeights / kHeads;     // rows of a warp
+    constexpr int kChunk = S::kChunk;
     constexpr int kRowChunks = (kHalves ? S::kWeights : kHeads) / kChunk, kChunks = S::kWeights / kChunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tk = threadIdx.x & 127, set = threadIdx.x >> 7;
     const float* w_s = reinterpret_cast<const float*>(b.smem + S::kOffW);
@@ -509,6 +504,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
     float* token_s = reinterpret_cast<float*>(b.smem + S::kOffToken);
     int32_t* vis_s = reinterpret_cast<int32_t*>(b.smem + S::kOffVis);
     const bool in_lanes = p.kpool <= 32 && (p.kpool & (p.kpool - 1)) == 0;  // a pool's tokens in one warp
+    constexpr int kSteps = 5;  // exchanges for the maximum over a pool's lanes, those past its width without effect
     const int pool_tk = tk / p.kpool;
     const bool writer = tk % p.kpool == 0;
     const int row_first = kHalves ? 0 : set * kRows;
@@ -528,43 +524,74 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         // This lane's pool of the tile at pool p is out[p], there for p < room and seen by row r
         // for p < vis[r].
         float* out = p.scores + static_cast<int64_t>(x.row0 + row_first) * p.n_pools + pool_tk;
-        const int32_t room = writer ? p.n_pools - pool_tk : 0;
+        const int32_t room = in_lanes && writer && !(kHalves && set == 1) ? p.n_pools - pool_tk : 0;
         int32_t vis[kRows];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) vis[r] = r < mine ? vis_s[row_first + r] - pool_tk : 0;
         float w[S::kWeights];
 #pragma unroll
         for (int i = 0; i < S::kWeights; ++i) w[i] = w_s[set * S::kWeights + i];
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + set * S::kWeights;
+        // The tile before, whose pools' maxima are taken and stored between this one's FMAs, as
+        // the next tile's barrier is polled and its first columns fetched before the last FMAs:
+        // nothing that an epilogue warp waits for then stands alone (1024 rows of 64 heads over
+        // 32768 tokens: 465 -> 405 us; two tiles at once or twice the warps were slower).
+        float held[kRows] = {};
+        int32_t held_at = p.n_pools;
+        auto exchange = [&](int k) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float other = __shfl_xor_sync(0xffffffffu, held[r], 1 << k);
+                if (p.kpool > 1 << k) held[r] = max_nan(held[r], other);
+            }
+        };
+        auto store = [&]() {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                if (r < mine && held_at < room) out[static_cast<int64_t>(r) * p.n_pools + held_at] = held_at < vis[r] ? held[r] : kNegInf;
+        };
+        b.wait(S::BAR_DFULL + static_cast<int>(tau % S::kDBufs), (tau / S::kDBufs) & 1);
+        tc_fence_after();
+        uint32_t v[2][kChunk];
+        load_columns(lanes + tau % S::kDBufs * kCols, v[0]);
         for (int32_t t = t0; t < t1; ++t, ++tau) {
-            const int d = static_cast<int>(tau % S::kDBufs);
+            const uint32_t d = tau % S::kDBufs, d_next = (tau + 1) % S::kDBufs, turn_next = (tau + 1) / S::kDBufs & 1;
             const int32_t pool_t = t * b.per_tile;
-            b.wait(S::BAR_DFULL + d, (tau / S::kDBufs) & 1);
-            tc_fence_after();
             const float scale = scale_s[(tau % S::kScaleSlots) * kTile + tk];
             // Chunks of columns, the next one's load in flight while one is summed. The columns
             // of rows that the unit lacks hold anything; their sums are not used.
-            const uint32_t base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + d * kCols + set * S::kWeights;
-            uint32_t v[2][kChunk];
             float sums[kRows];
-            if (mine > 0) load_columns(base, v[0]);
+            bool ready = false;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                if (r < mine) {
-                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = r * kRowChunks; i < (r + 1) * kRowChunks; ++i) {
-                        wait_columns(v[i & 1]);
-                        if (i + 1 < kChunks) load_columns(base + (i + 1) * kChunk, v[(i + 1) & 1]);
-#pragma unroll
-                        for (int c = 0; c < kChunk; c += 4) fma_relu4(acc, w + i * kChunk + c, v[i & 1] + c);
+                for (int i = r * kRowChunks; i < (r + 1) * kRowChunks; ++i) {
+                    wait_columns(v[i & 1]);
+                    if (i + 1 < kChunks) {
+                        load_columns(lanes + d * kCols + (i + 1) * kChunk, v[(i + 1) & 1]);
+                        if (i + 2 == kChunks && t + 1 < t1) ready = mbar_test_wait(b.bar(S::BAR_DFULL + static_cast<int>(d_next)), turn_next);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + static_cast<int>(d)));
+                        if (t + 1 < t1) {
+                            if (!__all_sync(0xffffffffu, ready)) b.wait(S::BAR_DFULL + static_cast<int>(d_next), turn_next);
+                            tc_fence_after();
+                            load_columns(lanes + d_next * kCols, v[0]);
+                        }
                     }
-                    sums[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+                    for (int c = 0; c < kChunk; c += 4) {
+                        constexpr int kEvery = kChunks * kChunk / 4 / (kSteps + 1) + 1;  // fours of columns between exchanges
+                        const int four = (i * kChunk + c) / 4;
+                        if (four % kEvery == 0 && four / kEvery < kSteps) exchange(four / kEvery);
+                        fma_relu4(acc, w + i * kChunk + c, v[i & 1] + c);
+                    }
                 }
+                sums[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
             }
-            if (mine < kRows && mine > 0) asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");  // the load past the last row
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + d));
+            store();
             if constexpr (kHalves) {
                 // The second half's sums, double-buffered: written again two tiles on, past the next barrier.
                 float* half_s = token_s + (tau & 1) * kTile;
@@ -572,16 +599,11 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
                 if (set == 0) sums[0] += half_s[tk];
             }
+            held_at = pool_t;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                if (r >= mine || (kHalves && set == 1)) break;
-                float s = scale == kNegInf ? kNegInf : sums[r] * scale;
-                if (in_lanes) {
-                    s = pool_max(s, p.kpool);
-                    if (pool_t < room) out[static_cast<int64_t>(r) * p.n_pools + pool_t] = pool_t < vis[r] ? s : kNegInf;
-                } else {
-                    token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = s;
-                }
+                held[r] = scale == kNegInf ? kNegInf : sums[r] * scale;
+                if (!in_lanes && r < mine && !(kHalves && set == 1)) token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = held[r];
             }
             if (!in_lanes) {
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
@@ -597,6 +619,9 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
             }
         }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) exchange(k);
+        store();
     });
     // -inf past the tiles of each unit: pieces of kFillPools pools of a row, over all blocks.
     const int32_t pieces = (p.n_pools + kFillPools - 1) / kFillPools;
