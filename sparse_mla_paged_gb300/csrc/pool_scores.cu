@@ -41,7 +41,7 @@ constexpr int kLoadWarps = 2;                    // copies: 64 tokens of a tile 
 constexpr int kLoadTurns = 2;                    // of 32 tokens
 constexpr int kTileBytes = kTile * kIndexDim;    // 16 KB of codes
 constexpr int kBarEpilogue = 1;
-constexpr int kFillPools = 4096;                 // pools of one piece of the fill with -inf
+constexpr int kFillPools = 1024;                 // pools of one piece of the fill with -inf
 
 // Variants by the columns (rows x padded heads) that one unit's MMAs take: MMA N.
 template <int kCols>
@@ -309,6 +309,34 @@ __device__ void load_queries(const Block<kCols>& b, const Unit& x) {
     }
 }
 
+// -inf past the tiles of each unit: pieces of kFillPools pools of a row, over all blocks' load
+// warps, which are done before the rest of their block.
+template <int kCols>
+__device__ void fill(const Block<kCols>& b) {
+    using S = Shape<kCols>;
+    const PoolScoresParams& p = b.p;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - S::kLoadWarp0;
+    const int32_t pieces = (p.n_pools + kFillPools - 1) / kFillPools;
+    const int64_t items = static_cast<int64_t>(p.num_seqs) * p.rows_per_seq * pieces, step = static_cast<int64_t>(gridDim.x) * kLoadWarps;
+    // Each lane looks for one piece's part to fill; the warp then fills what its lanes found.
+    for (int64_t first = blockIdx.x + static_cast<int64_t>(gridDim.x) * w; first < items; first += 32 * step) {
+        const int64_t i = first + lane * step;
+        int64_t lo = 0, hi = 0;  // as offsets into scores
+        if (i < items) {
+            const int32_t row = static_cast<int32_t>(i / pieces), piece = static_cast<int32_t>(i % pieces);
+            const int32_t seq = row / p.rows_per_seq, g = (row - seq * p.rows_per_seq) / b.group_rows;
+            const int64_t done = b.unit(seq * b.groups + g).tiles * b.per_tile, at = static_cast<int64_t>(row) * p.n_pools;
+            lo = at + max(static_cast<int64_t>(piece) * kFillPools, done);
+            hi = at + min(static_cast<int64_t>(piece + 1) * kFillPools, static_cast<int64_t>(p.n_pools));
+        }
+        for (uint32_t some = __ballot_sync(0xffffffffu, lo < hi); some; some &= some - 1) {
+            const int from = __ffs(some) - 1;
+            const int64_t end = __shfl_sync(0xffffffffu, hi, from);
+            for (int64_t k = __shfl_sync(0xffffffffu, lo, from) + lane; k < end; k += 32) p.scores[k] = kNegInf;
+        }
+    }
+}
+
 // Load by tensor-map boxes: load warp w takes every kMmaWarps-th tile from its w-th on; lane l
 // has box l, p.box_rows rows of one page (looked up a tile of its own ahead): the codes by the
 // map, the scales by a plain bulk copy. (One lane issuing all boxes in turn was slower: pooled
@@ -366,6 +394,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
         }
         tau += static_cast<uint32_t>(t1 - t0);
     });
+    fill(b);
     // No copy into shared memory is in flight when the block exits: the last tiles' bytes (after
     // an abort some of them were never asked for: their waits end at the limit).
     if (lane == 0) {
@@ -443,6 +472,7 @@ __device__ void run_load(const Block<kCols>& b) {
             if (lane == 0) mbar_arrive(b.bar(S::BAR_FULL + e));  // releases the slots written by plain stores
         }
     });
+    fill(b);
     cp_async_wait_all();
 }
 
@@ -623,18 +653,6 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         for (int k = 0; k < kSteps; ++k) exchange(k);
         store();
     });
-    // -inf past the tiles of each unit: pieces of kFillPools pools of a row, over all blocks.
-    const int32_t pieces = (p.n_pools + kFillPools - 1) / kFillPools;
-    const int64_t items = static_cast<int64_t>(p.num_seqs) * p.rows_per_seq * pieces;
-    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-        const int32_t row = static_cast<int32_t>(i / pieces), piece = static_cast<int32_t>(i % pieces);
-        const int32_t seq = row / p.rows_per_seq, g = (row - seq * p.rows_per_seq) / b.group_rows;
-        const int64_t done = b.unit(seq * b.groups + g).tiles * b.per_tile;
-        const int64_t lo = max(static_cast<int64_t>(piece) * kFillPools, done);
-        const int64_t hi = min(static_cast<int64_t>(piece + 1) * kFillPools, static_cast<int64_t>(p.n_pools));
-        for (int64_t k = lo + threadIdx.x; k < hi; k += S::kEpiWarps * 32)
-            p.scores[static_cast<int64_t>(row) * p.n_pools + k] = kNegInf;
-    }
 }
 
 template <int kHeads, int kCols>
