@@ -395,7 +395,9 @@ int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* n
  * in q) the row's visible scores; the selector ranks NaN last.
  *  q             bf16 [R, num_heads, 128], R = num_seqs*rows_per_seq; 16-byte aligned.
  *  head_weights  float32 [R, num_heads], 4-byte aligned (any head or softmax scale folded in).
- *  index_cache   pages as dsa_index_write stores them; 16-byte aligned.
+ *                A finite weight times its head's largest |q| has to stay below 2^134.
+ *  index_cache   pages as dsa_index_write stores them; 16-byte aligned. A scale of -infinity,
+ *                which that call never stores, makes its position score -inf.
  *  block_tables, max_blocks_per_seq  as for dsa_mla_decode (0: one shared table).
  *  q_pos         int32 [R]; -1 sees nothing.
  *  scores        float32 [R, n_pools], 4-byte aligned; every element is written.
@@ -422,8 +424,8 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
  *   out[r,h,:] = sum_{j < len(r)} softmax_j(sm_scale * q[r,h,:].(k_scale*K_j)) (v_scale*V_j)
  *                and 0 when len(r) <= 0.
  * Arguments as dsa_mla_decode without the selection (any length the block table holds; a
- * length past max_blocks_per_seq*block_size, or a negative entry, is a device-side
- * DSA_ERR_DEVICE_BOUNDS and its positions are skipped), except:
+ * length past max_blocks_per_seq*block_size is cut to it and a negative entry's positions
+ * count as keys and values of zeros, both a device-side DSA_ERR_DEVICE_BOUNDS), except:
  *  seq_lens     verify_rows = 0: int32 [R], len(r) = seq_lens[r]; verify_rows = 1: int32
  *               [num_seqs], len of row i of sequence s = seq_lens[s] + i + 1 (decode_k.rs,
  *               decode_k). What a position past a row's length holds, a NaN code in the

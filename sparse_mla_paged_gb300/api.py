@@ -249,6 +249,12 @@ def _need_on(t: torch.Tensor, dtype, name: str, index: int):
         raise ValueError(f"{name} must be a contiguous tensor of {dtype} on cuda:{index}")
 
 
+def _fit(*sizes):
+    # ctypes would cut a larger number to its low 32 bits.
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError("sizes must be 32-bit numbers")
+
+
 class _Launch:
     """What a call needs of its device: makes it current for the call (when it is not), and
     gives the raw stream and the context in which its outputs are allocated (the given
@@ -315,6 +321,7 @@ def plan_step(base_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch
     rows = n * rows_per_seq if rows_per_seq else (max_rows if out is None else out.slots.numel())
     if rows is None or (max_rows is not None and max_rows != rows):
         raise ValueError("max_rows must be the number of rows to write (num_seqs*rows_per_seq unless packed)")
+    _fit(rows, rows_per_seq, free_pages.numel(), block_size, block_tables.shape[1])
     with _Launch(i, stream) as at:
         if out is None:
             with at.allocating():
@@ -355,6 +362,7 @@ def index_write(keys: torch.Tensor, slots: torch.Tensor, block_size: int, page_s
             _need_on(t, torch.bfloat16, n, i)
             if t.numel() != INDEX:
                 raise ValueError(f"{n} [128]")
+    _fit(rows, block_size)
     with _Launch(i, stream) as at:
         check(_lib.load().dsa_index_write(keys.data_ptr(), _ptr(norm_weight), _ptr(norm_bias), slots.data_ptr(), rows,
                                           eps, block_size, page_stride_bytes, index_cache.data_ptr(), at.raw),
@@ -380,6 +388,7 @@ def pool_scores(q: torch.Tensor, head_weights: torch.Tensor, index_cache: torch.
     _need_on(index_cache, torch.uint8, "index_cache", i)
     _need_on(block_tables, torch.int32, "block_tables", i)
     _need_on(q_pos, torch.int32, "q_pos", i)
+    _fit(num_seqs, rows_per_seq, num_heads, max_blocks_per_seq, block_size, kpool, n_pools)
     rows = num_seqs * rows_per_seq
     if q.numel() != rows * num_heads * INDEX or head_weights.numel() != rows * num_heads or q_pos.numel() != rows:
         raise ValueError("q [R, num_heads, 128], head_weights [R, num_heads], q_pos [R]")
@@ -427,6 +436,7 @@ def decode_full(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
     _need_on(v_cache, torch.uint8, "v_cache", i)
     _need_on(block_tables, torch.int32, "block_tables", i)
     _need_on(seq_lens, torch.int32, "seq_lens", i)
+    _fit(num_seqs, rows_per_seq, num_q_heads, max_blocks_per_seq, block_size)
     rows = num_seqs * rows_per_seq
     if q.numel() != rows * num_q_heads * LATENT or seq_lens.numel() != (num_seqs if verify_rows else rows):
         raise ValueError("q [R, num_q_heads, 512], seq_lens [R] ([num_seqs] for verify rows)")

@@ -128,12 +128,11 @@ struct Cta {
     }
 };
 
-// Page of the block that holds position pos, or -1 (reported).
+// Page of the block that holds position pos (negative: the caller reports it), and its row there.
 __device__ __forceinline__ int32_t page_of(const Params& p, int32_t seq, int32_t pos, int32_t* row) {
     const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block));
     *row = pos - blk * p.block_size;
-    const int32_t page = __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
-    return page;
+    return __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
 }
 
 // ------------------------------------------------------------------------------------

@@ -175,6 +175,10 @@ def test_bad_tables_are_reported(api):
     ws = api.alloc_full_workspace(2, 1, 64)
     got = c.run(api, workspace=ws)
     assert api.read_device_status(ws) == 6 and torch.equal(got[1], ok[1]) and torch.isfinite(got[0].float()).all()
+    spare = next(i for i in range(c.k.size // c.stride) if i not in c.tables)
+    c.k[spare * c.stride:(spare + 1) * c.stride] = 0                   # its positions: keys and values of zeros
+    c.tables[0, 4] = spare
+    assert_parity(got, c.want())
     c.tables[0, 4] = 0
     assert torch.isfinite(c.run(api, workspace=ws).float()).all() and api.read_device_status(ws) == 0
     a = c.device()
@@ -223,7 +227,7 @@ def test_refusals(api):
             api.decode_full(*[v if k == i else x for k, x in enumerate(a)])
         assert e.value.status == code
     for i, v in ((0, a[0].float()), (0, a[0][:, :32].contiguous()), (3, a[3].long()), (3, a[3][:, :1].contiguous()),
-                 (5, a[5].cpu()), (6, 2)):
+                 (5, a[5].cpu()), (6, 2), (9, 2**32 + c.bs)):
         with pytest.raises(ValueError):
             api.decode_full(*[v if k == i else x for k, x in enumerate(a)])
     with pytest.raises(ValueError):

@@ -115,4 +115,6 @@ def test_no_rows_and_refusals(api):
         api.index_write(x.float(), s, 4, 4 * 132, cache)
     with pytest.raises(ValueError):
         api.index_write(x, s, 4, 4 * 132, cache, norm_weight=x)
+    with pytest.raises(ValueError):
+        api.index_write(x, s, 2**32 + 4, 4 * 132, cache)
     assert (cache == 7).all()

@@ -139,6 +139,8 @@ def test_refusals(api):
         api.plan_step(i(1, 2), i(1, 2), i(5), 64, t, rows_per_seq=2, max_rows=5)
     with pytest.raises(ValueError):
         api.plan_step(i(1, 2).long(), i(1, 2), i(5), 64, t, rows_per_seq=2)
+    with pytest.raises(ValueError):
+        api.plan_step(i(1, 2), i(1, 2), i(5), 64, t, max_rows=2**32 + 2)
     with pytest.raises(api.DsaError) as e:
         api.plan_step(i(1, 2), i(1, 2), i(5), 0, t, rows_per_seq=2)
     assert e.value.status == 1

@@ -228,7 +228,7 @@ def test_refusals(api):
             api.pool_scores(*[v if k == i else x for k, x in enumerate(a)])
         assert e.value.status == code
     for i, v in ((0, a[0].float()), (0, a[0][:, :32].contiguous()), (1, a[1][:, :9].contiguous()), (3, a[3].long()),
-                 (3, a[3][:, :1].contiguous()), (5, a[5].cpu()), (6, 2)):
+                 (3, a[3][:, :1].contiguous()), (5, a[5].cpu()), (6, 2), (9, 2**32 + 64), (12, 2**32 + c.n_pools)):
         with pytest.raises(ValueError):
             api.pool_scores(*[v if k == i else x for k, x in enumerate(a)])
     with pytest.raises(ValueError):
