@@ -565,7 +565,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         // The tile before, whose pools' maxima are taken and stored between this one's FMAs, as
         // the next tile's barrier is polled and its first columns fetched before the last FMAs:
         // nothing that an epilogue warp waits for then stands alone (1024 rows of 64 heads over
-        // 32768 tokens: 465 -> 405 us; two tiles at once or twice the warps were slower).
+        // 32768 tokens: 465 -> 405 us, then; two tiles at once or twice the warps were slower).
         float held[kRows] = {};
         int32_t held_at = p.n_pools;
         auto exchange = [&](int k) {
@@ -600,16 +600,16 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                     wait_columns(v[i & 1]);
                     if (i + 1 < kChunks) {
                         load_columns(lanes + d * kCols + (i + 1) * kChunk, v[(i + 1) & 1]);
-                        if (i + 2 == kChunks && t + 1 < t1) ready = mbar_test_wait(b.bar(S::BAR_DFULL + static_cast<int>(d_next)), turn_next);
+                        if (i + 2 == kChunks) ready = mbar_test_wait(b.bar(S::BAR_DFULL + static_cast<int>(d_next)), turn_next) || t + 1 >= t1;
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + static_cast<int>(d)));
-                        if (t + 1 < t1) {
-                            if (!__all_sync(0xffffffffu, ready)) b.wait(S::BAR_DFULL + static_cast<int>(d_next), turn_next);
-                            tc_fence_after();
-                            load_columns(lanes + d_next * kCols, v[0]);
-                        }
+                        // Past the last tile the columns hold anything; they are not used. (Branches
+                        // between the FMAs cost more: one around three exchanges made prefill 514 us.)
+                        if (!__all_sync(0xffffffffu, ready)) b.wait(S::BAR_DFULL + static_cast<int>(d_next), turn_next);
+                        tc_fence_after();
+                        load_columns(lanes + d_next * kCols, v[0]);
                     }
 #pragma unroll
                     for (int c = 0; c < kChunk; c += 4) {
@@ -631,11 +631,11 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
             }
             held_at = pool_t;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                held[r] = scale == kNegInf ? kNegInf : sums[r] * scale;
-                if (!in_lanes && r < mine && !(kHalves && set == 1)) token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = held[r];
-            }
+            for (int r = 0; r < kRows; ++r) held[r] = scale == kNegInf ? kNegInf : sums[r] * scale;
             if (!in_lanes) {
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (r < mine && !(kHalves && set == 1)) token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = held[r];
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
                 for (int i = threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32) {
                     const int r = i / b.per_tile, k = i % b.per_tile;
@@ -649,6 +649,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
             }
         }
+        wait_columns(v[0]);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) exchange(k);
         store();
