@@ -219,11 +219,11 @@ bool encode_cache_map(const void* base, size_t mem_bytes, CUtensorMap* m) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tensor-map box that stays within a page and fills 128-token tiles evenly, for pages
-// of 16, 32, 64 or 128 tokens or a multiple of 128; 0 for others.
+// Rows of a tensor-map box: the largest power of two that divides both a page and a 128-token
+// tile, so that no box crosses either; 0 when that is less than the 8 rows of a swizzle atom.
 int32_t box_rows(int32_t block_size) {
-    if (block_size >= 16 && 128 % block_size == 0) return block_size;
-    return block_size % 128 == 0 ? 128 : 0;
+    const int32_t rows = std::min(block_size & -block_size, 128);
+    return rows >= 8 ? rows : 0;
 }
 
 // 3-D map of an index cache's codes, [page][row of the page][128 bytes], pages enough to span

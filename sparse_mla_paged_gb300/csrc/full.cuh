@@ -158,7 +158,7 @@ struct Params {
     int32_t num_seqs, rows_per_seq, heads, pairs, groups, units, max_ctas;
     int32_t block_size, max_blocks_per_seq, verify_rows;
     FastDiv by_block;          // block_size
-    int32_t box_rows;          // tokens of a tensor-map box (16 or 32), 0: per-thread copies
+    int32_t box_rows;          // tokens of a tensor-map box (8, 16 or 32), 0: per-thread copies
     int32_t kv_same;
     float score_scale;         // sm_scale * k_scale * log2(e)
     float v_scale;

@@ -190,6 +190,13 @@ def test_bad_tables_are_reported(api):
     assert api.read_device_status(ws) == 0 and torch.equal(got[1], ok[1]) and (got[0] == 0).all()
 
 
+@pytest.mark.parametrize("bs", [8, 12, 24, 40, 48, 56, 80, 96, 112, 160, 192])
+def test_page_sizes(api, bs):
+    """Pages that end inside a tile, with boxes of 8, 16 and 32 rows or none."""
+    Case(3, 2, 40, [900, 1000, 2 * bs, 2 * bs + 1, bs - 1, 0], bs=bs).check(api)
+    Case(1, 1, 64, [60000], bs=bs, pad=16).check(api)
+
+
 def test_streams_graphs_and_repeats(api):
     c = Case(3, 2, 24, [1200, 1201, 60, 0, 700, 701])
     a = c.device()

@@ -193,6 +193,14 @@ def test_far_pages(api):
     assert torch.equal(got, near)
 
 
+@pytest.mark.parametrize("kpool", [4, 3])
+@pytest.mark.parametrize("bs", [8, 12, 24, 40, 48, 56, 80, 96, 112, 160, 192])
+def test_page_sizes(api, bs, kpool):
+    """Pages that end inside a tile, with boxes of 8, 16, 32 and 64 rows or none."""
+    Case(3, 2, 32, [900, 1000, 2 * bs, 2 * bs + 1, bs - 1, -1], bs=bs, kpool=kpool).check(api)
+    Case(1, 1, 64, [200000], bs=bs, kpool=kpool, pad=16).check(api)
+
+
 def test_streams_graphs_and_repeats(api):
     c = Case(3, 2, 64, [1200, 1201, 60, 61, 700, 701])
     want = c.run(api)
