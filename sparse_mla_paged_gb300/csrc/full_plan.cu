@@ -1,5 +1,11 @@
 // Before and after the full-cache decode kernel: the prologue (work plan and query operands)
 // and the join of units that several CTAs shared.
+//
+// Both are bound by latency. The prologue (one block plans, one block per unit makes its
+// operand) takes about 5 us for 64 units, much of it instruction fetches of code that runs once:
+// the plan's loops are kept rolled and its divisions out of line, and 512 threads beat 256
+// (small calls 17.6 -> 17.0 us). The join takes 3 to 8 us with the partials in L2, by how
+// many pieces a unit has.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

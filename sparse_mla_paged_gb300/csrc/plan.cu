@@ -17,6 +17,13 @@
 // row finds its request by a binary search of the token prefix sums in shared memory. A new
 // page's id is read from the free list, not from the table entry that another block writes,
 // so no block waits for another. Block 0 alone reports what it finds wrong.
+//
+// Bound by latency and instruction issue, not by bytes: one token of each of 64 requests takes
+// 3.2 us; 256 packed prompts with 528 000 tokens 7.3 us (1.5 TB/s of the 20 bytes that a row has
+// written, 1.6 us at the HBM's rate; 55 % of the issue slots under a profiler). Four rows a lane,
+// one search for a warp's 128 rows where one prompt fills them, and divisions through a
+// multiplier made on the host were each a step from 11.4 us. More blocks repeat the prefix
+// sums, fewer leave SMs idle.
 #include <climits>
 
 #include "common.cuh"
