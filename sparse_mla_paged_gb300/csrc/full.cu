@@ -94,6 +94,12 @@ constexpr uint32_t kTmemO = 0;    // O^T: dims 128c.. of all 64 pairs at column 
 constexpr uint32_t kTmemQ = 256;  // query operand
 constexpr uint32_t kTmemS = 384;
 
+// A reference is this much above its tile's maximum. Each move costs the CTA about a
+// microsecond (the pipeline drains): with normal scores of deviation 1, 8 of 106 tiles of 64
+// pairs moved at the selected decode's 1 octave and moves of the asking pairs only (two contexts
+// of 512 thousand tokens: 205 us, now 199). The lowest tile maximum that a reference serves,
+// kRescaleDrop below it, is the same, and with it what a tail's terms lose at worst.
+constexpr float kSlack = 2.0f;
 constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -512,7 +518,7 @@ __device__ void run_softmax(const Cta& c) {
             float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
             hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1)) * qs;
             // A tile mostly leaves every pair's reference where it is, so P' is formed with it at
-            // once; one barrier then tells whether any half of any pair's scores asks for a
+            // once (but for a unit's first tile, which finds none); one barrier then tells whether any half of any pair's scores asks for a
             // move (the maximum exceeds the reference by more than the margin, or lies far below
             // it). Only then the halves are compared, references move and P' is formed again.
             const bool ask = hmax > m_ref + kRescaleMargin ||
@@ -523,32 +529,36 @@ __device__ void run_softmax(const Cta& c) {
             const float* alpha_t = alpha_s + (tau & 1) * kHeadsPerCta;
 #pragma unroll 1
             for (bool again = false;; again = true) {
-                float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
+                if (again || t > s.t0) {
+                    float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
 #pragma unroll
-                for (int g = 0; g < kScores / 4; ++g) {
-                    float pp[4];
+                    for (int g = 0; g < kScores / 4; ++g) {
+                        float pp[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pp[e] = ex2_approx(fmaf(x[4 * g + e], qs, off));
-                        ls4[e] += pp[e];
+                        for (int e = 0; e < 4; ++e) {
+                            pp[e] = ex2_approx(fmaf(x[4 * g + e], qs, off));
+                            ls4[e] += pp[e];
+                        }
+                        uint32_t h0, l0, h1, l1;
+                        split2(pp[0], pp[1], h0, l0);
+                        split2(pp[2], pp[3], h1, l1);
+                        hw[g] = h0 | h1 << 16;
+                        lw[g] = l0 | l1 << 16;
                     }
-                    uint32_t h0, l0, h1, l1;
-                    split2(pp[0], pp[1], h0, l0);
-                    split2(pp[2], pp[3], h1, l1);
-                    hw[g] = h0 | h1 << 16;
-                    lw[g] = l0 | l1 << 16;
+                    fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+                    if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(ask)) break;
                 }
-                fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
-                if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(ask)) break;
                 if (term == 0) hm_s[half * kHeadsPerCta + hq] = hmax;
                 named_bar_sync_id(kBarPair0 + q4, 64);
                 const float tm = fmaxf(hm_s[hq], hm_s[kHeadsPerCta + hq]);
-                const bool change = tm > m_ref + kRescaleMargin ||
+                // The move is paid for once any pair needs it: every pair whose reference rises with
+                // this tile takes its new one too, and seldom asks for a move of its own.
+                const bool change = tm + kSlack > m_ref ||
                                     (tm < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && tm != kNegInf);
                 float alpha = 1.0f;
                 if (change) {
-                    const float m_new = fmaxf(tm + kRescaleSlack, m_top - kRescaleFloor);
+                    const float m_new = fmaxf(tm + kSlack, m_top - kRescaleFloor);
                     alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
                     l_part *= alpha;
                     m_ref = m_new;
@@ -559,7 +569,7 @@ __device__ void run_softmax(const Cta& c) {
                 if (half == 0 && lane == 0) flag_s[(tau & 1) * 4 + q4] = changed;
                 // Also keeps the next tile's maxima from overwriting these.
                 const bool any_change = named_bar_any<kBarSoftmax, kSoftmaxThreads>(change);
-                if (!any_change) break;
+                if (!any_change && t > s.t0) break;
                 if (t > s.t0) {
                     const uint4 f = *reinterpret_cast<const uint4*>(flag_s + (tau & 1) * 4);
                     resc[0] = (f.x | f.y) != 0u;

@@ -190,6 +190,19 @@ def test_bad_tables_are_reported(api):
     assert api.read_device_status(ws) == 0 and torch.equal(got[1], ok[1]) and (got[0] == 0).all()
 
 
+@pytest.mark.parametrize("at", [0, 1700, 2999])
+def test_flat_tails(api, at):
+    """One dominant position, all others alike from 1/3 to 21 octaves below it, by head."""
+    c = Case(1, 1, 64, [3000], two=True)
+    one, half = torch.tensor([1.0, 0.5]).to(torch.float8_e4m3fn).view(torch.uint8).tolist()
+    c.k[:] = half
+    row = int(c.tables[0, at // 64]) * c.stride + at % 64 * 512
+    c.k[row:row + 512] = one
+    octaves = np.arange(1, 65) / 3
+    c.q = ref.bf16(np.broadcast_to((octaves / (512 * 0.5 * c.scales[0] * c.scales[2] * np.log2(np.e)))[None, :, None], (1, 64, 512)))
+    assert_parity(c.run(api), c.want())
+
+
 @pytest.mark.parametrize("bs", [8, 12, 24, 40, 48, 56, 80, 96, 112, 160, 192])
 def test_page_sizes(api, bs):
     """Pages that end inside a tile, with boxes of 8, 16 and 32 rows or none."""
