@@ -20,7 +20,7 @@ namespace dsa {
 namespace full {
 
 constexpr int kTile = 128;
-constexpr int kGap = 3;      // tiles of a unit change; less when a range has less than 8 of them a tile
+constexpr int kGap = 5;      // tiles that a unit change costs, at most a quarter of a range
 constexpr int64_t kMaxLen = (int64_t{1} << 31) - 2 * kTile;  // positions stay in 32 bits
 
 // One CTA's stretch of one unit.
@@ -77,8 +77,8 @@ struct Line {
 __host__ __device__ inline Line make_line(int64_t tiles, int32_t live, int32_t max_ctas) {
     Line l;
     l.ctas = static_cast<int32_t>(tiles < max_ctas ? tiles : max_ctas);
-    // At most an eighth of a range, so that no range lies inside a gap.
-    l.gap = tiles / (8 * max_ctas);
+    // At most a quarter of a range, so that no range lies inside a gap.
+    l.gap = tiles / (4 * max_ctas);
     if (l.gap > kGap) l.gap = kGap;
     l.length = tiles + l.gap * (live > 0 ? live - 1 : 0);
     return l;
