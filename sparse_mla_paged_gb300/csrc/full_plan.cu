@@ -19,6 +19,9 @@ namespace {
 
 constexpr int kPrologueThreads = 512;
 constexpr int kWarps = kPrologueThreads / 32;
+constexpr int kQuarterPairs = kHeadsPerCta / 4;
+static_assert(kWarps == kQuarterPairs, "a warp per pair");
+constexpr int kStageBytes = kQImageBytes / 4;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ void scan2(int64_t& a, int32_t& b, int64_t* sa, int32_t* sb, int64_t* ta, int32_t* tb) {
@@ -130,28 +133,25 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
     if (any_over) atomicCAS(p.status, 0, kStatusBounds);
 }
 
-// Query operand of one unit, as the selected decode's prologue makes it: 16 warps x 4 pairs,
-// lane l dims [16l, 16l+16); a head's bf16 query as two E4M3 terms after a scaling by a power
-// of two (exact for elements above 2^-10 of its largest), rows 2k and 2k+1 of a quarter the
-// two terms of pair 16q + k, stored chunk-major. The head's scale of its dots is positive (the
-// decode takes maxima of the dots): a negative score scale turns the codes' signs, a zero one
-// zeroes the codes. A head with a NaN or an infinity gets zero codes and a NaN scale, which
-// makes all its scores NaN. A unit without a token writes its zeros here.
-__device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
+// Query operand of a lane quarter of one unit, 16 of its pairs, as the selected decode's prologue
+// makes it: a warp per pair, lane l dims [16l, 16l+16); a head's bf16 query as two E4M3 terms
+// after a scaling by a power of two (exact for elements above 2^-10 of its largest), rows 2k and
+// 2k+1 of the quarter the two terms of its pair k, stored chunk-major. The head's scale of its
+// dots is positive (the decode takes maxima of the dots): a negative score scale turns the
+// codes' signs, a zero one zeroes the codes. A head with a NaN or an infinity gets zero codes and
+// a NaN scale, which makes all its scores NaN. A unit without a token writes its zeros here. (A
+// block per unit, four pairs a warp, ended a microsecond later than the plan does.)
+__device__ void prepare(const Params& p, int32_t unit, int quarter, uint8_t* stage) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hl = kQuarterPairs * quarter + warp;
     const int32_t seq = unit / p.groups, first = (unit % p.groups) * kHeadsPerCta;
     const int32_t valid = min(kHeadsPerCta, p.pairs - first);
-    const int64_t pair0 = static_cast<int64_t>(seq) * p.pairs + first;
-    uint4 raw[kHeadsPerCta / kWarps][2];
-#pragma unroll
-    for (int i = 0; i < kHeadsPerCta / kWarps; ++i) {
-        const int hl = warp + i * kWarps;
-        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-        if (hl < valid) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (pair0 + hl) * kLatent + lane * 16);
-            raw[i][0] = src[0];
-            raw[i][1] = src[1];
-        }
+    const int64_t pair = static_cast<int64_t>(seq) * p.pairs + first + hl;
+    uint4 raw[2] = {};
+    if (hl < valid) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + pair * kLatent + lane * 16);
+        raw[0] = src[0];
+        raw[1] = src[1];
     }
     bool none = true;  // checked while the queries are on their way
 #pragma unroll 1
@@ -160,63 +160,59 @@ __device__ void prepare(const Params& p, int32_t unit, uint8_t* stage) {
         none &= row_len(p, seq, i, &over) == 0;
     }
     if (none) {
-        uint4* o = reinterpret_cast<uint4*>(p.out + pair0 * kLatent);
-        for (int e = threadIdx.x; e < valid * kLatent / 8; e += kPrologueThreads) o[e] = make_uint4(0, 0, 0, 0);
+        if (hl < valid) {
+            uint4* o = reinterpret_cast<uint4*>(p.out + pair * kLatent + lane * 16);
+            o[0] = o[1] = make_uint4(0, 0, 0, 0);
+        }
         return;
     }
+    const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    uint32_t amax = 0;  // magnitudes as bits: NaN and infinity are the largest
 #pragma unroll
-    for (int i = 0; i < kHeadsPerCta / kWarps; ++i) {
-        const int hl = warp + i * kWarps;
-        const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w,
-                               raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
-        uint32_t amax = 0;  // magnitudes as bits: NaN and infinity are the largest
+    for (int k = 0; k < 8; ++k) amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    const int E = static_cast<int>(amax >> 23);
+    const bool broken = E == 255;
+    int e = amax > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
+    e = e > 126 ? 126 : (e < -126 ? -126 : e);
+    const float back = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const float sign = p.score_scale > 0.0f ? 1.0f : (p.score_scale < 0.0f ? -1.0f : 0.0f);
+    const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * sign;
+    uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const int E = static_cast<int>(amax >> 23);
-        const bool broken = E == 255;
-        int e = amax > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
-        e = e > 126 ? 126 : (e < -126 ? -126 : e);
-        const float back = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float sign = p.score_scale > 0.0f ? 1.0f : (p.score_scale < 0.0f ? -1.0f : 0.0f);
-        const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * sign;
-        uint32_t hi[4], lo[4];
+    for (int k = 0; k < 4; ++k) {
+        float vh[4], vl[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float vh[4], vl[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint32_t bits = m & 1 ? w[2 * k + m / 2] & 0xFFFF0000u : w[2 * k + m / 2] << 16;
-                const float v = broken ? 0.0f : __uint_as_float(bits) * sc;
-                vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
-                vl[m] = v - vh[m];
-            }
-            hi[k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
-            lo[k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
+        for (int m = 0; m < 4; ++m) {
+            const uint32_t bits = m & 1 ? w[2 * k + m / 2] & 0xFFFF0000u : w[2 * k + m / 2] << 16;
+            const float v = broken ? 0.0f : __uint_as_float(bits) * sc;
+            vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
+            vl[m] = v - vh[m];
         }
-        const int rh = 32 * (hl >> 4) + 2 * (hl & 15);
-        *reinterpret_cast<uint4*>(stage + rh * 512 + ((lane ^ (rh & 31)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(stage + (rh + 1) * 512 + ((lane ^ ((rh + 1) & 31)) << 4)) =
-            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if (lane == 0)
-            p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hl] =
-                broken || p.score_scale != p.score_scale ? __uint_as_float(0x7FC00000u)
-                                                         : fmaxf(fabsf(p.score_scale) * back, 0x1p-120f);
+        hi[k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
+        lo[k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
     }
+    const int r = 2 * warp;
+    *reinterpret_cast<uint4*>(stage + r * 512 + ((lane ^ r) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(stage + (r + 1) * 512 + ((lane ^ (r + 1)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (lane == 0)
+        p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hl] =
+            broken || p.score_scale != p.score_scale ? __uint_as_float(0x7FC00000u)
+                                                     : fmaxf(fabsf(p.score_scale) * back, 0x1p-120f);
     __syncthreads();
-    uint8_t* img = p.qimg + static_cast<int64_t>(unit) * kQImageBytes;
-    for (int k = threadIdx.x; k < kQImageBytes / 16; k += kPrologueThreads) {
-        const int c = k >> 7, r = k & 127;
-        *reinterpret_cast<uint4*>(img + c * 2048 + r * 16) =
-            *reinterpret_cast<const uint4*>(stage + r * 512 + ((c ^ (r & 31)) << 4));
+    uint8_t* img = p.qimg + static_cast<int64_t>(unit) * kQImageBytes + quarter * 32 * 16;
+    for (int k = threadIdx.x; k < kQImageBytes / 4 / 16; k += kPrologueThreads) {
+        const int c = k >> 5, row = k & 31;
+        *reinterpret_cast<uint4*>(img + c * 2048 + row * 16) = *reinterpret_cast<const uint4*>(stage + row * 512 + ((c ^ row) << 4));
     }
 }
 
 __global__ void __launch_bounds__(kPrologueThreads) full_prologue_kernel(const Params p) {
     extern __shared__ __align__(16) uint8_t stage[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0) make_plan(p, reinterpret_cast<int32_t*>(stage));
-    else prepare(p, blockIdx.x - 1, stage);
+    const int b = blockIdx.x - 1;
+    if (b < 0) make_plan(p, reinterpret_cast<int32_t*>(stage));
+    else prepare(p, b >> 2, b & 3, stage);
 }
 
 // ------------------------------------------------------------------------------------
@@ -334,9 +330,7 @@ __global__ void __launch_bounds__(kCombineThreads, 5) full_combine_kernel(const 
 }  // namespace full
 
 cudaError_t full_plan_setup() {
-    cudaError_t e = cudaFuncSetAttribute(full::full_prologue_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQImageBytes);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(full::full_prologue_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    cudaError_t e = cudaFuncSetAttribute(full::full_prologue_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(full::full_combine_kernel<1>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
@@ -344,7 +338,7 @@ cudaError_t full_plan_setup() {
 }
 
 cudaError_t launch_full_plan(const full::Params& p, cudaStream_t stream) {
-    full::full_prologue_kernel<<<p.units + 1, full::kPrologueThreads, kQImageBytes, stream>>>(p);
+    full::full_prologue_kernel<<<4 * p.units + 1, full::kPrologueThreads, full::kStageBytes, stream>>>(p);
     return cudaGetLastError();
 }
 
