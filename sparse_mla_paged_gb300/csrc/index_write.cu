@@ -109,12 +109,30 @@ __global__ void __launch_bounds__(kIndexWriteThreads) index_write_kernel(const I
         for (int k = 0; k < kDims; ++k) top = max_nan(top, fabsf(y[k]));
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float inv = 448.0f / top;
+        // Without a norm a key's y / s = 448 y / top often lies exactly between two codes (both are
+        // bf16 numbers); a reciprocal's rounding would then choose for the even code. One correction
+        // with the remainder of 7/8 y (exact in float32) by top / 512 finds the midpoint itself; none
+        // with an infinite top, whose remainders would be NaN. A norm's y has no such ties, and
+        // the correction would cost 0.8 us of 262144 rows' 21.9.
+        const float2 inv = both((kNorm ? 448.0f : 512.0f) / top);
+        const float2 back = both(top < __builtin_huge_valf() ? top * (-1.0f / 512.0f) : 0.0f);
         uint32_t c[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            c[k] = f32x2_to_e4m3x2(y[4 * k] * inv, y[4 * k + 1] * inv) |
-                   (f32x2_to_e4m3x2(y[4 * k + 2] * inv, y[4 * k + 3] * inv) << 16);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t pair[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float2 x = reinterpret_cast<const float2*>(y)[2 * k + m];
+                if constexpr (kNorm) {
+                    x = __fmul2_rn(x, inv);
+                } else {
+                    const float2 z = __fmul2_rn(x, both(0.875f)), q = __fmul2_rn(z, inv);
+                    x = __ffma2_rn(__ffma2_rn(q, back, z), inv, q);
+                }
+                pair[m] = f32x2_to_e4m3x2(x.x, x.y);
+            }
+            c[k] = pair[0] | pair[1] << 16;
+        }
         if (at >= 0) {
             int64_t page, off;
             if (at >> 32 == 0) {  // a 64-bit division is a long sequence

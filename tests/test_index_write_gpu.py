@@ -71,6 +71,24 @@ def test_writer(api, rows, bs, pad, scale, norm):
     check(api, x, w if norm else None, b if norm == 2 else None, slots, bs, pad - pad % 16)
 
 
+def test_midpoints_between_codes(api):
+    """Keys that lie exactly between two codes round to the even one, also where 1 / s is inexact."""
+    rows = np.zeros((48, 128))
+    for i in range(48):
+        step = (3, 5, 7)[i % 3] * 2.0 ** (i - 24)                           # s; the largest key is 448 of it
+        rows[i] = np.tile((np.arange(8, 16) + 0.5) * 2.0 ** (i % 4), 16) * step * np.where(np.arange(128) % 3, 1, -1)
+        rows[i, 5] = 448 * step
+    x = ref.bf16(rows)
+    assert np.array_equal(ref.f64(x), rows)
+    stride = api.index_page_stride(48)
+    cache = torch.zeros(stride, dtype=torch.uint8, device="cuda")
+    api.index_write(x.cuda(), torch.arange(48, device="cuda"), 48, stride, cache)
+    codes, scales = ref.index_page(cache.cpu().numpy(), 0, 48, stride)
+    vals, s = ref.index_keys(rows, None, None, 0.0)
+    assert np.array_equal(scales, s.astype(np.float32)) and np.array_equal(scales.astype(np.float64), s)
+    assert np.array_equal(codes, oracle.e4m3_encode(vals))
+
+
 def test_extreme_values(api):
     rows = np.zeros((6, 128))
     rows[1] = 3.0                                  # constant: nothing left after the mean
