@@ -27,12 +27,12 @@
 // MMAs of 64 cycles, its P.V 32 of 48 (N = 64 computes for 32, but reads 6 KB of operands), 2560
 // cycles, and the softmax chain of a tile 2200 beside it; a tile takes some 2900. On long work
 // the GPU runs at its power limit, at 1640 to 1790 MHz. Measured (plan and join included): two
-// contexts of 512 thousand tokens with 128 heads 205 us, 1320 TFLOP/s (each product counted
+// contexts of 512 thousand tokens with 128 heads 199 us, 1360 TFLOP/s (each product counted
 // once; 141 us at the rate of a BF16 product); 64 rows of 64 heads over 8 to 32 thousand tokens
-// 139 us, 4.7 TB/s; 32 sequences of four rows of 16 heads over 16384 tokens 71 us; one row over
-// 777 tokens 17 us, of which the tiles are 3. One warp issuing both products: 235, 156 and 79 us
-// (227, 151 and 76 with V's tile kept in the collector for the second term of P'); sixteen
-// softmax warps were slower too.
+// 132 us, 4.9 TB/s in all and 6 in the middle; 32 sequences of four rows of 16 heads over 16384
+// tokens 68 us, 9 of them before the first scores and 10 after the first CTAs' last; one row over
+// 777 tokens 16 us. One warp issuing both products took 15 % more (10 % with V's tile kept in the
+// collector for the second term of P'); sixteen softmax warps were slower too.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -1,12 +1,12 @@
 // Before and after the full-cache decode kernel: the prologue (work plan and query operands)
 // and the join of units that several CTAs shared.
 //
-// Both are bound by latency. The prologue (one block plans, one block per unit makes its
-// operand) takes 6.5 to 7.5 us alone and cold, for 1 as for 64 units, much of it instruction
-// fetches of code that runs once: the plan's loops are kept rolled and its divisions out of line,
-// and 512 threads beat 256 (32 units of 16384 tokens 71.7 against 72.3 us a call). The join takes
-// 5 to 10 us alone, by how many pieces the units have; it starts when the last block of the
-// decode is at its end, and its partials come from L2.
+// Both are bound by latency. The prologue (one block plans, four per unit make its operand)
+// ends some 4 us after its start, much of that instruction fetches of code that runs once: the
+// plan's loops are kept rolled and its divisions out of line, and 512 threads beat 256 (32 units of
+// 16384 tokens 71.7 against 72.3 us a call). The join takes 5 to 10 us alone and cold, by how
+// many pieces the units have, 1.5 to 4 in a call; it starts when the last block of the decode is
+// at its end, and its partials come from L2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -3,15 +3,15 @@
 // index cache that the pool scores read.
 //
 //   y = (x - mean x) / sqrt(mean (x - mean x)^2 + eps) * w + b      (or y = x)
-//   s = max(max|y|, 2^-100) / 448,   code = E4M3(y / s)
+//   s = max(max|y|, 2^-100) / 448,   code = E4M3(y / s), midpoints to the even code
 //
 // Page p of the cache holds block_size rows of 128 codes, then block_size float32 scales.
 //
 // Eight lanes take one row, sixteen consecutive dims each (the norm's sums and the maximum
 // are three shuffles), and persistent blocks keep the weights in registers, a row's loads in
 // flight while the one before is written. Instructions bound it rather than bytes: 262144 rows
-// with the norm take 22.1 us (4.7 TB/s of the 104 MB read and written, which the HBM moves in
-// 15.5 us; 61 % of the issue slots under a profiler), 64 rows 2.0 us. With sixteen lanes a row,
+// with the norm take 21.8 us (4.8 TB/s of the 104 MB read and written, which the HBM moves in
+// 15.5 us; 61 % of the issue slots under a profiler), 64 rows 1.9 us. With sixteen lanes a row,
 // 64-bit divisions of the slot and no reuse of the weights it took 41 us; two dims an
 // instruction in the norm were the last step, from 24. More blocks per SM with fewer registers
 // each were no faster.
