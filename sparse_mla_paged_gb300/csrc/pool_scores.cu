@@ -15,8 +15,9 @@
 // shuffles between neighbouring lanes. The power of two goes into the head's weight.
 //
 // A unit is a group of rows of one sequence; its 128-token tiles up to the last pool that one
-// of its rows sees stand on a line, unit after unit, that is cut into equal ranges, one per
-// persistent block (scores of different tokens are independent: nothing to join). Each block
+// of its rows sees stand on a line, unit after unit with gaps between (kGap), that is cut into
+// equal ranges, one per persistent block (scores of different tokens are independent: nothing to
+// join). Each block
 // sums the units' tiles for itself, 4 bytes a row from L2, which costs less than a launch or
 // a workspace for a plan. Warps of a block: epilogue (four per 128 tokens, TMEM lane quarters;
 // they also write the queries' operand of each unit), one or two that issue the MMAs, two that load
@@ -34,7 +35,7 @@
 // TFLOP/s with the two terms counted once, 0.79 of the rate of a BF16 product; there the issue
 // slots are 62 % busy, the tensor pipe 58 %, and shared memory about three quarters (an MMA of
 // N = 128 reads its operands for as long as it computes, and tiles are written beside it). 64
-// rows over 8 to 32 thousand tokens 35.5 us, 25.4 of them at the HBM's rate; the rest is the
+// rows over 8 to 32 thousand tokens 33.6 us, 25.4 of them at the HBM's rate; the rest is the
 // launch, the shares, the queries' operand and the first tiles, one after another, which is all
 // of a small call's 8 us. One MMA warp for 128 columns: prefill 440 us.
 #include <cuda_bf16.h>
@@ -50,6 +51,13 @@ constexpr int kLoadWarps = 2;                    // copies: 64 tokens of a tile 
 constexpr int kLoadTurns = 2;                    // of 32 tokens
 constexpr int kTileBytes = kTile * kIndexDim;    // 16 KB of codes
 constexpr int kBarEpilogue = 1;
+// Starting a unit (queries, weights, an empty pipeline) costs its block the time of several
+// tiles; so many places of the line after each unit hold none, so that the block that starts one
+// has fewer tiles. With less than two tiles a block (by the pools that there are room for) the
+// starts run side by side anyway and gaps would only crowd the tiles. 64 rows of 64 heads
+// over 8 to 32 thousand tokens 35.4 -> 33.6 us, 17 rows of 48 heads over 6 to 20 thousand 14.9 ->
+// 12.6; with gaps also below, 23 rows over 1 to 2 thousand would take 9.0 instead of 8.4.
+constexpr int kGap = 6;
 constexpr int kFillPools = 1024;                 // pools of one piece of the fill with -inf
 
 // Variants by the columns (rows x padded heads) that one unit's MMAs take: MMA N.
@@ -157,6 +165,7 @@ struct Block {
     uint32_t sbase;
     volatile int* abort_flag;
     int32_t groups, group_rows, units, per_tile;  // units of a sequence, rows of a unit, units, pools of a tile
+    int32_t gap;                                  // places on the line after each unit that hold no tile
     int64_t begin, end;                           // this block's range of the line
     int32_t unit0;                                // unit that it starts in, and where that unit starts
     int64_t start0;
@@ -195,8 +204,8 @@ struct Block {
             const Unit x = unit(u);
             if (x.tiles > 0) {
                 const int64_t t0 = begin > at ? begin - at : 0, t1 = min(end - at, x.tiles);
-                f(x, static_cast<int32_t>(t0), static_cast<int32_t>(t1));
-                at += x.tiles;
+                if (t0 < t1) f(x, static_cast<int32_t>(t0), static_cast<int32_t>(t1));
+                at += x.tiles + gap;
                 ++u;
             } else {
                 const int32_t v = u + 1 + static_cast<int32_t>(threadIdx.x & 31);
@@ -207,7 +216,7 @@ struct Block {
     }
 };
 
-// This block's equal share of the line of tiles.
+// This block's equal share of the line of tiles and gaps.
 template <int kCols>
 __device__ void share(Block<kCols>& b) {
     using S = Shape<kCols>;
@@ -219,7 +228,10 @@ __device__ void share(Block<kCols>& b) {
     const int32_t lo = min(static_cast<int64_t>(b.units), static_cast<int64_t>(threadIdx.x) * per), hi = min(b.units, lo + per);
     int64_t mine = 0;
 #pragma unroll 4
-    for (int32_t u = lo; u < hi; ++u) mine += b.unit(u).tiles;
+    for (int32_t u = lo; u < hi; ++u) {
+        const int64_t n = b.unit(u).tiles;
+        mine += n > 0 ? n + b.gap : 0;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -241,9 +253,9 @@ __device__ void share(Block<kCols>& b) {
     if (b.begin < b.end && at <= b.begin && b.begin < at + mine) {  // the one thread whose units hold the first tile
         int32_t u = lo;
         for (;; ++u) {
-            const int64_t n = b.unit(u).tiles;
-            if (b.begin < at + n) break;
-            at += n;
+            const int64_t n = b.unit(u).tiles, w = n > 0 ? n + b.gap : 0;
+            if (b.begin < at + w) break;
+            at += w;
         }
         found[0] = u;
         found[1] = at;
@@ -667,7 +679,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
 
 template <int kHeads, int kCols>
 __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
-    pool_scores_kernel(const PoolScoresParams p, const __grid_constant__ CUtensorMap tmap, int32_t groups, int32_t group_rows) {
+    pool_scores_kernel(const PoolScoresParams p, const __grid_constant__ CUtensorMap tmap, int32_t groups, int32_t group_rows, int32_t gap) {
     using S = Shape<kCols>;
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -675,6 +687,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
     Block<kCols> b{p, smem, smem_u32(smem), reinterpret_cast<volatile int*>(smem + S::kOffAbort)};
     b.groups = groups;
     b.group_rows = group_rows;
+    b.gap = gap;
     b.units = p.num_seqs * groups;
     b.per_tile = kTile / p.kpool;
     if (tid == 0) {
@@ -761,7 +774,9 @@ cudaError_t launch_pool_scores(const PoolScoresParams& p, const CUtensorMap& tma
     const int32_t group_rows = cols / padded, groups = (p.rows_per_seq + group_rows - 1) / group_rows;
     return with_kernel(padded, cols, [&](auto* kernel, auto shape) {
         using S = decltype(shape);
-        kernel<<<sms * S::kCtas, S::kThreads, S::kSmem, stream>>>(p, tmap, groups, group_rows);
+        const int64_t ctas = static_cast<int64_t>(sms) * S::kCtas, unit_tiles = p.n_pools / (kTile / p.kpool) + 1;
+        const int32_t gap = static_cast<int64_t>(p.num_seqs) * groups >= 2 * ctas / unit_tiles ? kGap : 0;
+        kernel<<<sms * S::kCtas, S::kThreads, S::kSmem, stream>>>(p, tmap, groups, group_rows, gap);
         return cudaGetLastError();
     });
 }
