@@ -770,6 +770,7 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     p.n_pools = n_pools;
     p.by_block = fast_div(static_cast<uint32_t>(block_size));
     p.by_kpool = fast_div(static_cast<uint32_t>(kpool));
+    p.by_tile = fast_div(static_cast<uint32_t>(128 / kpool));
     // Boxes also need tiles of 128 tokens, that is pools that divide them.
     p.box_rows = 128 % kpool == 0 ? box_rows(block_size) : 0;
     CUtensorMap tmap;

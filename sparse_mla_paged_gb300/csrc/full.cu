@@ -232,18 +232,19 @@ __device__ void run_load_copies(const Cta& c) {
     uint32_t tau = 0;
     for (Segment s = c.start.first;; s = c.next(s)) {
         const int32_t seq = s.unit / p.groups;
-        auto look = [&](int32_t t) -> int64_t {
+        // This lane's page and row there (-1: no token). What is made of them is left to the next
+        // tile: using the page here would wait for its load.
+        auto look = [&](int32_t t, int32_t* row) -> int32_t {
             const int32_t pos = t * kTile + kQuarterTokens * w + lane;
-            if (t >= s.t1 || pos >= s.max_len) return -1;
-            int32_t row;
-            const int32_t page = page_of(p, seq, pos, &row);
-            if (page < 0) atomicCAS(p.status, 0, kStatusBounds);
-            return page < 0 ? -1 : page * p.cache_stride + static_cast<int64_t>(row) * kLatent;
+            *row = -1;
+            return t < s.t1 && pos < s.max_len ? page_of(p, seq, pos, row) : 0;
         };
-        int64_t next = look(s.t0);
+        int32_t row_next, page_next = look(s.t0, &row_next);
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
-            const int64_t mine = next;
-            next = look(t + 1);
+            const int32_t page = page_next, row = row_next;
+            page_next = look(t + 1, &row_next);
+            if (page < 0) atomicCAS(p.status, 0, kStatusBounds);
+            const int64_t mine = page < 0 || row < 0 ? -1 : page * p.cache_stride + static_cast<int64_t>(row) * kLatent;
             const int e = static_cast<int>(tau % slots);
             if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e * kQuarters + w, (tau / slots - 1) & 1);
             const uint32_t dst = c.sbase + e * slot_bytes + w * kQuarterBytes + (lane >> 3) * 1024;

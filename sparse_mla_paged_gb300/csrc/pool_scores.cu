@@ -86,8 +86,8 @@ struct Shape {
     static constexpr int kOffQ = kStages * kTileBytes;                      // [2 terms][cols][128 codes]
     static constexpr int kOffScale = kOffQ + 2 * kCols * kIndexDim;         // float [slots][128]
     static constexpr int kOffW = kOffScale + kScaleSlots * kTile * 4;       // float [cols]
-    static constexpr int kOffToken = kOffW + kCols * 4;                     // float [rows][128] token scores
-    static constexpr int kOffVis = kOffToken + kMaxRows * kTile * 4;        // int32 [rows] visible pools of a row
+    static constexpr int kOffToken = kOffW + kCols * 4;                     // float [2][rows][128] token scores
+    static constexpr int kOffVis = kOffToken + 2 * kMaxRows * kTile * 4;    // int32 [rows] visible pools of a row
     static constexpr int kOffScan = kOffVis + kMaxRows * 4;                 // int64 [16] warp sums, then what they find
     static constexpr int kOffBars = kOffScan + 20 * 8;
     static constexpr int BAR_FULL = 0, BAR_EMPTY = kStages, BAR_DFULL = 2 * kStages, BAR_DEMPTY = BAR_DFULL + kDBufs,
@@ -444,28 +444,28 @@ __device__ void run_load(const Block<kCols>& b) {
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
         const int32_t limit = x.seen * p.kpool;
         const int32_t* table = p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq;
-        // Byte offset of the codes of this lane's token of turn i, tile t, and the distance from
-        // there to its scale.
-        auto resolve = [&](int32_t t, int i, int64_t& code, int64_t& to_scale) {
-            code = kNone;
-            to_scale = 0;
+        // Page and row there of this lane's token of turn i, tile t (row -1: none). What is made of
+        // them is left to the next turn: using the page here would wait for its load.
+        auto look = [&](int32_t t, int i, int32_t& page, int32_t& row) {
+            row = -1;
             const int tk = tk0 + 32 * i;
             const int32_t pos = t * tokens + tk;
             if (t >= t1 || tk >= tokens || pos >= limit) return;
-            const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block)), off = pos - blk * p.block_size;
-            const int32_t page = (p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq) ? __ldg(table + blk) : -1;
-            code = page < 0 ? kBad : page * p.page_stride + static_cast<int64_t>(off) * kIndexDim;
-            to_scale = static_cast<int64_t>(p.block_size) * kIndexDim - static_cast<int64_t>(off) * (kIndexDim - 4);
+            const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block));
+            row = pos - blk * p.block_size;
+            page = (p.max_blocks_per_seq == 0 || blk < p.max_blocks_per_seq) ? __ldg(table + blk) : -1;
         };
-        int64_t code[kLoadTurns], next_code[kLoadTurns], to_scale[kLoadTurns], next_to[kLoadTurns];
+        int64_t code[kLoadTurns], to_scale[kLoadTurns];  // offset of a token's codes, and from there to its scale
+        int32_t next_page[kLoadTurns] = {}, next_row[kLoadTurns];
 #pragma unroll
-        for (int i = 0; i < kLoadTurns; ++i) resolve(t0, i, next_code[i], next_to[i]);
+        for (int i = 0; i < kLoadTurns; ++i) look(t0, i, next_page[i], next_row[i]);
         for (int32_t t = t0; t < t1; ++t, ++tau) {
 #pragma unroll
             for (int i = 0; i < kLoadTurns; ++i) {
-                code[i] = next_code[i];
-                to_scale[i] = next_to[i];
-                resolve(t + 1, i, next_code[i], next_to[i]);
+                const int64_t row = next_row[i];
+                code[i] = row < 0 ? kNone : (next_page[i] < 0 ? kBad : next_page[i] * p.page_stride + row * kIndexDim);
+                to_scale[i] = static_cast<int64_t>(p.block_size) * kIndexDim - row * (kIndexDim - 4);
+                look(t + 1, i, next_page[i], next_row[i]);
             }
             const int e = static_cast<int>(tau % S::kStages);
             if (tau >= S::kStages) b.wait(S::BAR_EMPTY + e, (tau / S::kStages - 1) & 1);
@@ -601,6 +601,21 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
             for (int r = 0; r < kRows; ++r)
                 if (r < mine && held_at < room) out[static_cast<int64_t>(r) * p.n_pools + held_at] = held_at < vis[r] ? held[r] : kNegInf;
         };
+        // Pools that do not lie in one warp's lanes: a tile's token scores go through shared memory.
+        auto token_row = [](uint32_t turn, int row) { return kHalves ? 2 + (turn & 1) : (turn & 1) * S::kMaxRows + row; };
+        auto pools = [&](int32_t pool_t, uint32_t turn) {
+            for (int i = threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32) {
+                const int r = static_cast<int>(divide(static_cast<uint32_t>(i), p.by_tile)), k = i - r * b.per_tile;
+                const int32_t pool = pool_t + k;
+                if (pool >= p.n_pools) continue;
+                float s = kNegInf;
+                if (pool < vis_s[r]) {
+                    const float* from = token_s + token_row(turn, r) * kTile + k * p.kpool;
+                    for (int j = 0; j < p.kpool; ++j) s = max_nan(s, from[j]);
+                }
+                p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
+            }
+        };
         b.wait(S::BAR_DFULL + static_cast<int>(tau % S::kDBufs), (tau / S::kDBufs) & 1);
         tc_fence_after();
         uint32_t v[2][kChunk];
@@ -656,20 +671,14 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
             if (!in_lanes) {
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
-                    if (r < mine && !(kHalves && set == 1)) token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = held[r];
-                named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
-                for (int i = threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32) {
-                    const int r = i / b.per_tile, k = i % b.per_tile;
-                    const int32_t pool = pool_t + k;
-                    if (pool >= p.n_pools) continue;
-                    float s = kNegInf;
-                    if (pool < vis_s[r])
-                        for (int j = 0; j < p.kpool; ++j) s = max_nan(s, token_s[(kHalves ? 2 : r) * kTile + k * p.kpool + j]);
-                    p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
-                }
+                    if (r < mine && !(kHalves && set == 1)) token_s[token_row(tau, r + row_first) * kTile + tk] = held[r];
+                // The tile before: its tokens' scores were stored a tile ago, its buffer is
+                // written again past the next barrier.
+                if (t > t0) pools(pool_t - b.per_tile, tau - 1);
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
             }
         }
+        if (!in_lanes) pools((t1 - 1) * b.per_tile, tau - 1);
         wait_columns(v[0]);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) exchange(k);
