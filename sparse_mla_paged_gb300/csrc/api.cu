@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 #include <vector>
 
 #include "common.cuh"
@@ -770,14 +771,24 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     p.n_pools = n_pools;
     p.by_block = fast_div(static_cast<uint32_t>(block_size));
     p.by_kpool = fast_div(static_cast<uint32_t>(kpool));
-    p.by_tile = fast_div(static_cast<uint32_t>(128 / kpool));
-    // Boxes also need tiles of 128 tokens, that is pools that divide them.
-    p.box_rows = 128 % kpool == 0 ? box_rows(block_size) : 0;
+    // A tile is as many whole pools as 128 tokens hold, with boxes as many as fill whole boxes
+    // too: the largest tile, then the largest boxes, of 8 rows or more (234 rows of 20 heads over
+    // 90000 tokens: boxes of 32 rows 149 us, of 4 rows 357, copies 244; so boxes are worth it from
+    // 80 tokens a tile).
+    int32_t tokens = 128 / kpool * kpool;
+    for (int32_t rows = 128, most = 79; rows >= 8; rows /= 2) {
+        const int32_t both = rows / std::gcd(rows, kpool) * kpool;
+        if (block_size % rows != 0 || both > 128 || 128 / both * both <= most) continue;
+        most = tokens = 128 / both * both;
+        p.box_rows = rows;
+    }
+    p.per_tile = tokens / kpool;
+    p.by_tile = fast_div(static_cast<uint32_t>(p.per_tile));
     CUtensorMap tmap;
     std::memset(&tmap, 0, sizeof tmap);
     if (p.box_rows > 0 &&
         !encode_page_map(index_cache, d->mem_bytes, block_size, page_stride_bytes, p.box_rows, &tmap))
-        p.box_rows = 0;
+        p.box_rows = 0;  // copies take any tile
     return from_cuda(launch_pool_scores(p, tmap, d->sms, static_cast<cudaStream_t>(stream)));
 }
 

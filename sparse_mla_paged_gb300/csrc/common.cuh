@@ -276,7 +276,8 @@ struct PoolScoresParams {
     int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, kpool, n_pools;
     int32_t box_rows;          // tokens of a tensor-map box, 0: per-thread copies
     FastDiv by_block, by_kpool;
-    FastDiv by_tile;           // pools of a 128-token tile
+    int32_t per_tile;          // pools of a tile
+    FastDiv by_tile;           // per_tile
 };
 
 // Launchers (each defined next to its kernel).

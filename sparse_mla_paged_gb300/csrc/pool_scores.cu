@@ -368,7 +368,8 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
     const PoolScoresParams& p = b.p;
     const int lane = threadIdx.x & 31;
     const uint32_t w = (threadIdx.x >> 5) - S::kLoadWarp0;
-    const bool mine = lane * p.box_rows < kTile;
+    const int tokens = b.per_tile * p.kpool;
+    const bool mine = lane * p.box_rows < tokens;
     const uint32_t box_codes = static_cast<uint32_t>(p.box_rows) * kIndexDim, box_scales = static_cast<uint32_t>(p.box_rows) * 4u;
     uint32_t tau = 0;
     bool stop = false;
@@ -377,7 +378,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
         const int32_t* table = p.block_tables + static_cast<int64_t>(x.seq) * p.max_blocks_per_seq;
         // This lane's page of tile t (-1: bad, -2: nothing that a row sees) and the row its box starts at.
         auto look = [&](int32_t t, int32_t* row) -> int32_t {
-            const int32_t pos = t * kTile + lane * p.box_rows;
+            const int32_t pos = t * tokens + lane * p.box_rows;
             *row = 0;
             if (!mine || t >= t1 || pos >= limit) return -2;
             const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block));
@@ -603,17 +604,24 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
         };
         // Pools that do not lie in one warp's lanes: a tile's token scores go through shared memory.
         auto token_row = [](uint32_t turn, int row) { return kHalves ? 2 + (turn & 1) : (turn & 1) * S::kMaxRows + row; };
+        // A warp takes a pool of more than 16 tokens (pools of 64, 234 rows of 20 heads over 90
+        // thousand tokens: 273 us, 404 with a thread each), a thread one of fewer.
         auto pools = [&](int32_t pool_t, uint32_t turn) {
-            for (int i = threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32) {
+            const bool wide = p.kpool > 16;
+            const int step = wide ? 32 : 1;
+            for (int i = wide ? warp : threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32 / step) {
                 const int r = static_cast<int>(divide(static_cast<uint32_t>(i), p.by_tile)), k = i - r * b.per_tile;
                 const int32_t pool = pool_t + k;
                 if (pool >= p.n_pools) continue;
                 float s = kNegInf;
                 if (pool < vis_s[r]) {
                     const float* from = token_s + token_row(turn, r) * kTile + k * p.kpool;
-                    for (int j = 0; j < p.kpool; ++j) s = max_nan(s, from[j]);
+                    for (int j = wide ? lane : 0; j < p.kpool; j += step) s = max_nan(s, from[j]);
+                    if (wide)
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
                 }
-                p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
+                if (!wide || lane == 0) p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
             }
         };
         b.wait(S::BAR_DFULL + static_cast<int>(tau % S::kDBufs), (tau / S::kDBufs) & 1);
@@ -698,7 +706,7 @@ __global__ void __launch_bounds__(Shape<kCols>::kThreads, Shape<kCols>::kCtas)
     b.group_rows = group_rows;
     b.gap = gap;
     b.units = p.num_seqs * groups;
-    b.per_tile = kTile / p.kpool;
+    b.per_tile = p.per_tile;
     if (tid == 0) {
         for (int e = 0; e < S::kStages; ++e) {
             // boxes: one arrival with the bytes to come; copies: every lane's, and a plain one per warp
@@ -783,7 +791,7 @@ cudaError_t launch_pool_scores(const PoolScoresParams& p, const CUtensorMap& tma
     const int32_t group_rows = cols / padded, groups = (p.rows_per_seq + group_rows - 1) / group_rows;
     return with_kernel(padded, cols, [&](auto* kernel, auto shape) {
         using S = decltype(shape);
-        const int64_t ctas = static_cast<int64_t>(sms) * S::kCtas, unit_tiles = p.n_pools / (kTile / p.kpool) + 1;
+        const int64_t ctas = static_cast<int64_t>(sms) * S::kCtas, unit_tiles = p.n_pools / p.per_tile + 1;
         const int32_t gap = static_cast<int64_t>(p.num_seqs) * groups >= 2 * ctas / unit_tiles ? kGap : 0;
         kernel<<<sms * S::kCtas, S::kThreads, S::kSmem, stream>>>(p, tmap, groups, group_rows, gap);
         return cudaGetLastError();
