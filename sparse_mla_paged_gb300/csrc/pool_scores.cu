@@ -86,8 +86,8 @@ struct Shape {
     static constexpr int kOffQ = kStages * kTileBytes;                      // [2 terms][cols][128 codes]
     static constexpr int kOffScale = kOffQ + 2 * kCols * kIndexDim;         // float [slots][128]
     static constexpr int kOffW = kOffScale + kScaleSlots * kTile * 4;       // float [cols]
-    static constexpr int kOffToken = kOffW + kCols * 4;                     // float [2][rows][128] token scores
-    static constexpr int kOffVis = kOffToken + 2 * kMaxRows * kTile * 4;    // int32 [rows] visible pools of a row
+    static constexpr int kOffToken = kOffW + kCols * 4;                     // float [rows][128] token scores
+    static constexpr int kOffVis = kOffToken + kMaxRows * kTile * 4;        // int32 [rows] visible pools of a row
     static constexpr int kOffScan = kOffVis + kMaxRows * 4;                 // int64 [16] warp sums, then what they find
     static constexpr int kOffBars = kOffScan + 20 * 8;
     static constexpr int BAR_FULL = 0, BAR_EMPTY = kStages, BAR_DFULL = 2 * kStages, BAR_DEMPTY = BAR_DFULL + kDBufs,
@@ -602,28 +602,6 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
             for (int r = 0; r < kRows; ++r)
                 if (r < mine && held_at < room) out[static_cast<int64_t>(r) * p.n_pools + held_at] = held_at < vis[r] ? held[r] : kNegInf;
         };
-        // Pools that do not lie in one warp's lanes: a tile's token scores go through shared memory.
-        auto token_row = [](uint32_t turn, int row) { return kHalves ? 2 + (turn & 1) : (turn & 1) * S::kMaxRows + row; };
-        // A warp takes a pool of more than 16 tokens (pools of 64, 234 rows of 20 heads over 90
-        // thousand tokens: 273 us, 404 with a thread each), a thread one of fewer.
-        auto pools = [&](int32_t pool_t, uint32_t turn) {
-            const bool wide = p.kpool > 16;
-            const int step = wide ? 32 : 1;
-            for (int i = wide ? warp : threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32 / step) {
-                const int r = static_cast<int>(divide(static_cast<uint32_t>(i), p.by_tile)), k = i - r * b.per_tile;
-                const int32_t pool = pool_t + k;
-                if (pool >= p.n_pools) continue;
-                float s = kNegInf;
-                if (pool < vis_s[r]) {
-                    const float* from = token_s + token_row(turn, r) * kTile + k * p.kpool;
-                    for (int j = wide ? lane : 0; j < p.kpool; j += step) s = max_nan(s, from[j]);
-                    if (wide)
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
-                }
-                if (!wide || lane == 0) p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
-            }
-        };
         b.wait(S::BAR_DFULL + static_cast<int>(tau % S::kDBufs), (tau / S::kDBufs) & 1);
         tc_fence_after();
         uint32_t v[2][kChunk];
@@ -679,14 +657,31 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
             if (!in_lanes) {
 #pragma unroll
                 for (int r = 0; r < kRows; ++r)
-                    if (r < mine && !(kHalves && set == 1)) token_s[token_row(tau, r + row_first) * kTile + tk] = held[r];
-                // The tile before: its tokens' scores were stored a tile ago, its buffer is
-                // written again past the next barrier.
-                if (t > t0) pools(pool_t - b.per_tile, tau - 1);
+                    if (r < mine && !(kHalves && set == 1)) token_s[(kHalves ? 2 : row_first + r) * kTile + tk] = held[r];
+                named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
+                // Pools that do not lie in one warp's lanes. A warp takes one of more than 16 tokens
+                // (of 64, 234 rows of 20 heads over 90 thousand tokens: 273 us, 404 with a thread
+                // each), a thread one of fewer. (Read a tile later, with one barrier, they took
+                // 1.5 % less, but the code beside the tile loop cost all others 1.5 % more.)
+                const bool wide = p.kpool > 16;
+                const int step = wide ? 32 : 1;
+                for (int i = wide ? warp : threadIdx.x; i < x.rows * b.per_tile; i += S::kEpiWarps * 32 / step) {
+                    const int r = static_cast<int>(divide(static_cast<uint32_t>(i), p.by_tile)), k = i - r * b.per_tile;
+                    const int32_t pool = pool_t + k;
+                    if (pool >= p.n_pools) continue;
+                    float s = kNegInf;
+                    if (pool < vis_s[r]) {
+                        const float* from = token_s + (kHalves ? 2 : r) * kTile + k * p.kpool;
+                        for (int j = wide ? lane : 0; j < p.kpool; j += step) s = max_nan(s, from[j]);
+                        if (wide)
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) s = max_nan(s, __shfl_xor_sync(0xffffffffu, s, o));
+                    }
+                    if (!wide || lane == 0) p.scores[static_cast<int64_t>(x.row0 + r) * p.n_pools + pool] = s;
+                }
                 named_bar_sync<kBarEpilogue, S::kEpiWarps * 32>();
             }
         }
-        if (!in_lanes) pools((t1 - 1) * b.per_tile, tau - 1);
         wait_columns(v[0]);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) exchange(k);
