@@ -17,21 +17,20 @@
 // A unit is a group of rows of one sequence; its 128-token tiles up to the last pool that one
 // of its rows sees stand on a line, unit after unit with gaps between (kGap), that is cut into
 // equal ranges, one per persistent block (scores of different tokens are independent: nothing to
-// join). Each block
-// sums the units' tiles for itself, 4 bytes a row from L2, which costs less than a launch or
-// a workspace for a plan. Warps of a block: epilogue (four per 128 tokens, TMEM lane quarters;
-// they also write the queries' operand of each unit), one or two that issue the MMAs, two that load
-// key tiles into a ring in the 128-byte-swizzled operand layout and run ahead over units: with
-// tensor-map boxes of a page's rows when pages, pools and tiles fit each other, else
-// with 16-byte copies.
+// join). Each block sums the units' tiles for itself, 4 bytes a row from L2, which costs less than
+// a launch or a workspace for a plan. Warps of a block: epilogue (four per 128 tokens, TMEM lane
+// quarters; they also write the queries' operand of each unit), two that issue the MMAs, two that
+// load key tiles into a ring in the 128-byte-swizzled operand layout and run ahead over units:
+// with tensor-map boxes of a page's rows when pages, pools and tiles fit each other, else with
+// 16-byte copies.
 //
 // Shared memory's bandwidth is what the tile loop competes for (a tile is written once and
 // read twice, by the hi and the lo product, with the queries each time): the weights therefore
 // stay in registers, a warp's columns being the same in every tile. Read from shared memory
 // for every tile they cost as much of it as the MMAs (pooled 128k 413 us, prefill 588).
 //
-// Measured, 64 heads: 128 rows over 131072 tokens each (pooled 128k) 330 us, 6.8 TB/s, what a
-// copy of the keys would take. 1024 rows over one cache of 32768 tokens (prefill) 374 us, 1510
+// Measured, 64 heads: 128 rows over 131072 tokens each (pooled 128k) 327 us, 6.8 TB/s, what a
+// copy of the keys would take. 1024 rows over one cache of 32768 tokens (prefill) 370 us, 1530
 // TFLOP/s with the two terms counted once, 0.79 of the rate of a BF16 product; there the issue
 // slots are 62 % busy, the tensor pipe 58 %, and shared memory about three quarters (an MMA of
 // N = 128 reads its operands for as long as it computes, and tiles are written beside it). 64
