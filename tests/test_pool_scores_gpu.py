@@ -201,6 +201,14 @@ def test_page_sizes(api, bs, kpool):
     Case(1, 1, 64, [200000], bs=bs, kpool=kpool, pad=16).check(api)
 
 
+@pytest.mark.parametrize("bs,kpool", [(32, 24), (64, 20), (16, 6), (64, 48), (24, 56), (128, 40), (64, 100), (16, 9), (8, 64), (64, 112)])
+def test_tiles_of_whole_pools(api, bs, kpool):
+    """Tiles of 72 to 128 tokens, by boxes and by copies, pools over several warps' lanes."""
+    Case(3, 2, 32, [900, 1000, 2 * kpool - 1, 2 * kpool, kpool - 2, -1], bs=bs, kpool=kpool).check(api)
+    Case(1, 1, 128, [3000], bs=bs, kpool=kpool).check(api)
+    Case(2, 1, 64, [150000, 90001], bs=bs, kpool=kpool).check(api)
+
+
 def test_streams_graphs_and_repeats(api):
     c = Case(3, 2, 64, [1200, 1201, 60, 61, 700, 701])
     want = c.run(api)
