@@ -9,7 +9,7 @@
 // queries of up to 128/heads rows of one sequence the B operand (N = rows x heads). A BF16
 // query is two E4M3 terms (hi = its top 4 significant bits after scaling its head by a power
 // of two, lo = the rest), both accumulated into the same FP32 columns, so the product is
-// exact but for elements below 2^-10 of their head's largest. With tokens as rows of D, a
+// exact but for elements below 2^-11 of their head's largest. With tokens as rows of D, a
 // token's heads lie in one thread's columns: the relu, the weighted sum over heads and the
 // key's scale need no exchange between threads, and the maximum over a pool's tokens is a few
 // shuffles between neighbouring lanes. The power of two goes into the head's weight.
@@ -296,11 +296,11 @@ __device__ void load_queries(const Block<kCols>& b, const Unit& x) {
             for (int k = 0; k < 4; ++k) top = max(top, max((u[k] << 16) & 0x7FFFFFFFu, u[k] & 0x7FFF0000u));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // e with top * 2^e in [128, 256); a head with a NaN or an infinity gets zero codes and
-            // a NaN weight, which makes all its row's scores NaN.
+            // e with top * 2^e in [240, 480), whose first four bits are E4M3 numbers; a head with a NaN
+            // or an infinity gets zero codes and a NaN weight, which makes all its row's scores NaN.
             const int E = static_cast<int>(top >> 23);
             const bool broken = E == 255;
-            int e = top > 0u ? 134 - E : 0;
+            int e = top > 0u ? ((top & 0x7FFFFFu) < 0x700000u ? 135 : 134) - E : 0;
             e = e > 126 ? 126 : (e < -126 ? -126 : e);
             const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
             uint32_t hi[2], lo[2];
