@@ -39,6 +39,8 @@ constexpr float kRescaleMargin = 1.75f;
 constexpr float kRescaleSlack = 1.0f;
 constexpr float kRescaleDrop = 8.0f;
 constexpr float kRescaleFloor = 64.0f;
+// The share of a row's sum of P' that the E4M3 terms of P' far below the reference may lose.
+constexpr float kLostShare = 0x1p-8f;
 
 // Device status codes mirror dsa_status.
 constexpr int kStatusBounds = DSA_ERR_DEVICE_BOUNDS;

@@ -98,8 +98,18 @@ constexpr uint32_t kTmemS = 384;
 // microsecond (the pipeline drains): with normal scores of deviation 1, 8 of 106 tiles of 64
 // pairs moved at the selected decode's 1 octave and moves of the asking pairs only (two contexts
 // of 512 thousand tokens: 205 us, now 199). The lowest tile maximum that a reference serves,
-// kRescaleDrop below it, is the same, and with it what a tail's terms lose at worst.
+// kRescaleDrop below it, is the same.
 constexpr float kSlack = 2.0f;
+// What the two E4M3 terms of a P' lose: 2^-10 at most (it itself when below), beside 1.2 * 2^-9 of
+// it. The row sum takes P' whole, so a tile far below its pair's reference would be counted but not
+// added: 128 terms of 2^-11 weigh 2^-4, as much as a 512th of a row whose sum is the 2^5 of one
+// maximum. Each thread therefore keeps an account per pair, kLostShare (common.cuh) of its P'
+// less what their terms may lose. While the four threads of a pair have one in credit together,
+// less than kLostShare of the row is lost; a thread that sees its own run out asks, and a pair that
+// could not pay for one more tile moves its reference down to that tile. (A tile that holds 2^5
+// pays for itself: 2^5 * kLostShare = 128 * 2^-10.) Scores of deviation 1 never ask; of
+// deviation 2 in natural units, 56 of 128 tiles of 64 pairs move a reference, 25 without it.
+constexpr float kMostLost = kScores * 0x1p-10f;  // by a thread in a tile
 constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -474,6 +484,7 @@ __device__ void run_softmax(const Cta& c) {
         float m_ref = kNegInf;  // reference max of the pair (log2 units)
         float m_top = kNegInf;  // highest reference so far
         float l_part = 0.0f;    // this thread's share of the sum of P'
+        float credit = 0.0f;    // and its account of what the terms may have lost of it
 
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             c.wait(BAR_SFULL, tau & 1);
@@ -521,11 +532,12 @@ __device__ void run_softmax(const Cta& c) {
             // A tile mostly leaves every pair's reference where it is, so P' is formed with it at
             // once (but for a unit's first tile, which finds none); one barrier then tells whether any half of any pair's scores asks for a
             // move (the maximum exceeds the reference by more than the margin, or lies far below
-            // it). Only then the halves are compared, references move and P' is formed again.
+            // it, or the account runs out). Only then the halves are compared, references move and
+            // P' is formed again.
             const bool ask = hmax > m_ref + kRescaleMargin ||
                              (hmax < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && hmax != kNegInf);
             uint32_t hw[kScores / 4], lw[kScores / 4];
-            float fresh;
+            float fresh, earned = 0.0f;
             bool resc[2] = {false, false};
             const float* alpha_t = alpha_s + (tau & 1) * kHeadsPerCta;
 #pragma unroll 1
@@ -548,22 +560,37 @@ __device__ void run_softmax(const Cta& c) {
                         lw[g] = l0 | l1 << 16;
                     }
                     fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
-                    if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(ask)) break;
+                    earned = fmaf(fresh, kLostShare, -fminf(fresh, kMostLost));
+                    if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(
+                                     ask || (credit + earned < 0.0f && m_ref > m_top - kRescaleFloor)))
+                        break;
                 }
-                if (term == 0) hm_s[half * kHeadsPerCta + hq] = hmax;
+                // The halves' accounts go through words that are free here: the output factors,
+                // and the rescale factors of the tile before, which every warp has applied.
+                float* const credit_s = alpha_s + ((tau + 1) & 1) * kHeadsPerCta;
+                const float credit2 = credit + earned + __shfl_xor_sync(0xffffffffu, credit + earned, 1);
+                if (term == 0) {
+                    hm_s[half * kHeadsPerCta + hq] = hmax;
+                    (half == 0 ? f_s : credit_s)[hq] = credit2;
+                }
                 named_bar_sync_id(kBarPair0 + q4, 64);
                 const float tm = fmaxf(hm_s[hq], hm_s[kHeadsPerCta + hq]);
+                const float credit4 = f_s[hq] + credit_s[hq];
                 // The move is paid for once any pair needs it: every pair whose reference rises with
                 // this tile takes its new one too, and seldom asks for a move of its own.
-                const bool change = tm + kSlack > m_ref ||
-                                    (tm < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && tm != kNegInf);
+                const bool rise = tm + kSlack > m_ref;
+                const bool change = rise || ((tm < m_ref - kRescaleDrop || (tm < m_ref - kSlack && credit4 < 4.0f * kMostLost)) &&
+                                             m_ref > m_top - kRescaleFloor && tm != kNegInf);
                 float alpha = 1.0f;
                 if (change) {
-                    const float m_new = fmaxf(tm + kSlack, m_top - kRescaleFloor);
+                    const float m_new = fmaxf(tm + (rise ? kSlack : kRescaleSlack), m_top - kRescaleFloor);
                     alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
                     l_part *= alpha;
+                    credit *= alpha;
                     m_ref = m_new;
                     m_top = fmaxf(m_top, m_new);
+                } else {
+                    credit = fmaf(0.25f, credit4, -earned);  // in equal parts: who asked gets what the others do not need
                 }
                 if (term == 0 && half == 0) alpha_s[(tau & 1) * kHeadsPerCta + hq] = alpha;
                 const uint32_t changed = __ballot_sync(0xffffffffu, change);
@@ -578,6 +605,7 @@ __device__ void run_softmax(const Cta& c) {
                 }
             }
             l_part += fresh;
+            credit += earned;
             if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
             pv_seen = false;
             const uint32_t pb = c.sbase + kOffP + (tau & 1) * 2 * kPTermBytes;
