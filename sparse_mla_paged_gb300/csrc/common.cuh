@@ -31,7 +31,8 @@ constexpr int64_t kMaxFullRowHeads = 1 << 22;  // dsa_mla_decode_full: rows * he
 // tile max exceeds m by more than kRescaleMargin (so P' stays below
 // 2^(kPBias + kRescaleMargin) < 448, the E4M3 maximum) and also when the tile max falls
 // more than kRescaleDrop below m (so a tile far under an earlier maximum gets its own
-// exponent window instead of sinking into E4M3's subnormal range and below it). A
+// exponent window instead of sinking into E4M3's subnormal range and below it), or below m
+// when what such tiles may have lost passes kLostShare of the row (full.cu, decode.cu). A
 // downward reset never takes m more than kRescaleFloor below the highest reference of the
 // head, which keeps the rescaled FP32 accumulator far from overflow.
 constexpr float kPBias = 7.0f;

@@ -76,13 +76,22 @@ constexpr int kSlotsKV = kRingBytes / kKvTileBytes;              // tiles in fli
 constexpr int kSBufs = 128 / kTileTokens;                        // S buffers in TMEM columns 384..511
 constexpr int kHalfCols = kTileTokens / 2;                       // S columns per softmax warp
 constexpr int kScores = kHalfCols / 2;                           // scores per softmax thread per tile
+// What the two E4M3 terms of a thread's P' lose in a tile at most, beside 2^-9 of each: 1.5 * 2^-10
+// a token (hi_part's remainder below E4M3's normal range). The row sum takes P' whole, so terms far
+// below the reference would be counted but not added: each thread keeps an account per head,
+// kLostShare (common.cuh) of its P' less that, and when the four threads of a head together could
+// not pay for two more tiles the reference moves down to the next tile that lies below it. (A
+// tile with a P' of 2^6 pays for itself: 2^6 * kLostShare > 128 * 1.5 * 2^-10.) The accounts are
+// added up behind a tile's block barrier and used in the next tile: used in the same tile they
+// cost pooled 128k 2.7 %, so 1.4.
+constexpr float kMostLost = kScores * 1.5f * 0x1p-10f;
 constexpr int kPTermBytes = kHeadsPerCta * kTileTokens;          // one E4M3 term of P'^T
 static_assert(kSlotsKV <= 6 && kSBufs >= 1 && kScores % 16 == 0, "tile geometry");
 constexpr int kOffRing = 0;
 constexpr int kOffP = kOffRing + kRingBytes;                     // P' [2 buffers][hi, lo]; epilogue staging
 constexpr int kOffHm = kOffP + 4 * kPTermBytes;                  // float [2 token halves][64] tile maxima
 constexpr int kOffAlpha = kOffHm + 2 * kHeadsPerCta * 4;         // float [2 tile parities][64] rescale factors
-constexpr int kOffL = kOffAlpha + 2 * kHeadsPerCta * 4;          // float [2 token halves][64] row sums
+constexpr int kOffL = kOffAlpha + 2 * kHeadsPerCta * 4;          // float [2 token halves][64] accounts; row sums at the end
 constexpr int kOffF = kOffL + 2 * kHeadsPerCta * 4;              // float [64] output factors
 constexpr int kOffFlags = kOffF + kHeadsPerCta * 4;              // u32 [2 tile parities][4 lane quarters]
 constexpr int kOffBars = kOffFlags + 2 * 4 * 4;
@@ -639,6 +648,8 @@ __device__ void run_softmax(const DecodeParams& p, uint8_t* smem, uint32_t sbase
         float m_ref = kNegInf;  // reference max of head hq (log2 units)
         float m_top = kNegInf;  // highest reference of head hq so far
         float l_part = 0.0f;    // this thread's share of the row sum of P'
+        float credit = 0.0f;    // and its account of what the terms may have lost of it
+        bool poor = false;      // the head's account could not pay for two more tiles
 
         for (int t = 0; t < tl.ntiles; ++t, ++tau) {
             // The next unit's query image was written by the prologue long before and has
@@ -686,22 +697,30 @@ __device__ void run_softmax(const DecodeParams& p, uint8_t* smem, uint32_t sbase
             // passes after reading it).
             float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
             hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1));
-            if (term == 0) hm_s[half * kHeadsPerCta + hq] = hmax;
+            const float credit2 = credit + __shfl_xor_sync(0xffffffffu, credit, 1);
+            if (term == 0) {
+                hm_s[half * kHeadsPerCta + hq] = hmax;
+                l_s[half * kHeadsPerCta + hq] = credit2;
+            }
             named_bar_sync_id(kBarPair0 + q4, 64);
             const float tm = fmaxf(hm_s[hq], hm_s[kHeadsPerCta + hq]);
+            const bool low = poor && tm < m_ref - kRescaleSlack;
             if (st == 0 && (tau == 2 || tau == 3)) DSA_TRACE_AT(p, 73 + 8 * (tau - 2));
             // Reset the reference of head hq when the tile max exceeds it by more than the
-            // margin, or lies more than kRescaleDrop below it; O and the row sums are
-            // rescaled by 2^(m_old - m_new). Every thread of the head's pair computes the
-            // same values; the factors are published (double-buffered by tile parity: a
-            // buffer is rewritten two tiles later, after every reader passed the next
-            // block barrier) and one block barrier tells every warp whether any changed.
-            const bool change = tm > m_ref + kRescaleMargin || (tm < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor);
+            // margin, or lies more than kRescaleDrop below it, or below it with a poor account;
+            // O, the row sums and the accounts are rescaled by 2^(m_old - m_new). Every thread
+            // of the head's pair computes the same values; the factors are published
+            // (double-buffered by tile parity: a buffer is rewritten two tiles later, after
+            // every reader passed the next block barrier) and one block barrier tells every
+            // warp whether any changed.
+            const bool change = tm > m_ref + kRescaleMargin ||
+                                ((tm < m_ref - kRescaleDrop || low) && m_ref > m_top - kRescaleFloor);
             float alpha = 1.0f;
             if (change) {
-                const float m_new = fmaxf(tm + kRescaleSlack, m_top - kRescaleFloor);
+                const float m_new = fmaxf(low ? tm : tm + kRescaleSlack, m_top - kRescaleFloor);
                 alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
                 l_part *= alpha;
+                credit *= alpha;
                 m_ref = m_new;
                 m_top = fmaxf(m_top, m_new);
             }
@@ -710,8 +729,12 @@ __device__ void run_softmax(const DecodeParams& p, uint8_t* smem, uint32_t sbase
             // Which of this lane quarter's 16 heads changed (both warps of the pair agree).
             const uint32_t changed = __ballot_sync(0xffffffffu, change);
             if (half == 0 && lane == 0) flag_s[(tau & 1) * 4 + q4] = changed;
+            // The head's account without this tile (after a unit's first tile there is none yet). The
+            // buffer is rewritten after the block barrier, as the maxima are.
+            const float credit4 = l_s[hq] + l_s[kHeadsPerCta + hq];
             const bool any_change = named_bar_any<kBarSoftmax, kSoftmaxThreads>(change);
             if (st == 0 && (tau == 2 || tau == 3)) DSA_TRACE_AT(p, 77 + 8 * (tau - 2));
+            poor = t > 0 && credit4 * alpha < 8.0f * kMostLost;
             // 32-head blocks of O^T that need rescaling before this tile's P.V: heads 0-31
             // live in lane quarters 0-1, heads 32-63 in 2-3 (uniform over the softmax warps).
             bool resc[2] = {false, false};
@@ -738,7 +761,9 @@ __device__ void run_softmax(const DecodeParams& p, uint8_t* smem, uint32_t sbase
                 hw[g] = pack_e4m3x4(ph[0], ph[1], ph[2], ph[3]);
                 lw[g] = pack_e4m3x4(pl[0], pl[1], pl[2], pl[3]);
             }
-            l_part += (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+            const float fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+            l_part += fresh;
+            credit = fmaf(fresh, kLostShare, credit - kMostLost);
             if (st == 0 && (tau == 2 || tau == 3)) DSA_TRACE_AT(p, 74 + 8 * (tau - 2));
             // P buffer tau%2 is free once the P.V two tiles back has finished reading it.
             if (tau >= 2 && !pv_seen) warp_wait(p, barp(BAR_PVDONE0 + (tau & 1)), ((tau >> 1) - 1) & 1, abort_flag);

@@ -7,6 +7,11 @@ below) or 1.22 * 2^-9 of it (float16, then two E4M3 terms). A pair's account hol
 its P' less the former, 2^-10 for each of a thread's 32 tokens and at most their sum; it stays
 above zero, so the former are kLostShare of the row at most. With values of magnitude 1 an output
 is off by kLostShare + 1.22 * 2^-9 in all.
+
+The selected decode: a term is off by at most 1.5 * 2^-10 or 2^-9 of it (test_split_bounds_cpu.py). Its
+account is looked at two tiles later, with the most that these may lose kept back, but not
+before a row's third tile: it may be overdrawn by one tile's most, 128 * 1.5 * 2^-10 of a row
+whose sum is 2^6 at least: another 0.0030 of it.
 """
 import os
 import re
@@ -69,6 +74,40 @@ def full(x, vs, account=True, tile=128):
     return [o / l for o in out]
 
 
+def _split_selected(p):
+    h = ((p.view(torch.int32) + 0x80000) & ~0xFFFFF).view(torch.float32)
+    return _e4m3(h) + _e4m3(p - h)
+
+
+def selected(x, vs, account=True, tile=128):
+    """The same as decode.cu forms it."""
+    lost = tile / 4 * 1.5 * 2.0 ** -10
+    n = x.shape[0]
+    m = torch.full((n,), -np.inf)
+    top, l, credit = m.clone(), torch.zeros(n, dtype=torch.float64), torch.zeros(n, dtype=torch.float64)
+    out = [torch.zeros(n, dtype=torch.float64) for _ in vs]
+    poor = torch.zeros(n, dtype=torch.bool)
+    for t0 in range(0, x.shape[1], tile):
+        tm = x[:, t0:t0 + tile].max(1).values
+        first, rise, free = m == -np.inf, tm > m + MARGIN, m > top - FLOOR
+        over = poor & (tm < m - LOW) & account
+        change = rise | (free & ((tm < m - DROP) | over))
+        m_new = torch.where(change, torch.maximum(torch.where(over, tm, tm + LOW), top - FLOOR), m)
+        a = torch.where(first, 0.0, torch.exp2((m - m_new).double()))
+        poor = (credit * a < 8 * lost) & (t0 > 0)
+        m, top = m_new, torch.maximum(top, m_new)
+        p = torch.exp2(x[:, t0:t0 + tile] - m[:, None] + BIAS)
+        q = p.double().view(n, 4, -1).sum(2)
+        credit = torch.where(first, 0.0, credit * a) + (q * SHARE - q.clamp(max=lost)).sum(1)
+        l = l * a + p.double().sum(1)
+        r = _split_selected(p).double()
+        out = [o * a + (r * v[:, t0:t0 + tile]).sum(1) for o, v in zip(out, vs)]
+    return [o / l for o in out]
+
+
+SELECTED_BOUND = SHARE + 128 * 1.5 * 2.0 ** -10 / 64 + 2.0 ** -9
+
+
 def rows(n, first, peak):
     """log2 scores: the first position and every 128th above a background of zeros."""
     x = torch.zeros(len(first), n)
@@ -124,3 +163,30 @@ def test_full_tails_that_fall_tile_by_tile():
         x = -step * torch.arange(n).div(128, rounding_mode="floor").float().repeat(8, 1)
         x[:, 0] += torch.linspace(0, 14, 8)
         assert worst(full, x) <= SHARE + 1.22 * 2.0 ** -9
+
+
+@pytest.mark.parametrize("tile", [64, 128])
+@pytest.mark.parametrize("n", [1024, 2048, 8192])
+def test_selected_sinks_and_peaks(n, tile):
+    x = rows(n, *zip(*FAMILY)).float()
+    assert worst(selected, x, tile=tile) <= SELECTED_BOUND
+
+
+def test_selected_loses_more_without_the_account():
+    x = rows(8192, *zip(*FAMILY)).float()
+    assert worst(selected, x, account=False) > 0.05
+    assert worst(selected, x[:, :2048], account=False) > 0.025
+
+
+@pytest.mark.parametrize("tile", [64, 128])
+def test_selected_other_scores(tile):
+    """Normal ones of several deviations, with and without a sink; tails that fall tile by tile."""
+    g = torch.Generator().manual_seed(5)
+    for deviation in (0.5, 1.0, 2.0, 4.0, 8.0):
+        x = torch.randn(64, 4096, generator=g) * deviation * 1.4427
+        x[:32, 0] = 4 * deviation + 12
+        assert worst(selected, x, tile=tile) <= SELECTED_BOUND
+    for step in (0.25, 1.0, 3.0, 7.5):
+        x = -step * torch.arange(8192).div(tile, rounding_mode="floor").float().repeat(8, 1)
+        x[:, 0] += torch.linspace(0, 14, 8)
+        assert worst(selected, x, tile=tile) <= SELECTED_BOUND

@@ -8,7 +8,8 @@ their own, all ones, every output is 1.
 
 Bounds, on outputs of magnitude 1 at most: the whole-cache decode loses 2^-8 of a row and 1.22 *
 2^-9 of each term (test_lost_mass_cpu.py), rounds a split row's parts to float16 (2^-12 each) and
-the output to bf16 (2^-9): 8.6e-3 with the exponentials' 2^-20.
+the output to bf16 (2^-9): 8.6e-3 with the exponentials' 2^-18. The selected decode: 2^-8 and one tile's
+128 * 1.5 * 2^-10 of a row's 2^6, 2^-9 of each term, then the same.
 """
 import numpy as np
 import pytest
@@ -16,6 +17,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 FULL_BOUND = 2.0 ** -8 + 1.22 * 2.0 ** -9 + 2.0 ** -12 + 2.0 ** -9 + 2.0 ** -18
+SELECTED_BOUND = 2.0 ** -8 + 128 * 1.5 * 2.0 ** -16 + 2.0 ** -9 + 2.0 ** -12 + 2.0 ** -9 + 2.0 ** -18
 ONE = 0x38  # 1.0
 FRACTIONS = [0, 150, 200, 240, 256, 290, 320, 333, 350, 384, 420, 460, 500]  # of 512: the peaks' level
 
@@ -91,3 +93,20 @@ def test_whole_cache_peaks_anywhere(api):
         for values in (r.k, r.ones):
             got = api.decode_full(r.q, r.k, values, r.tables, 0, lens, 152, 1, 64, 64, 64 * 512, 1.0, 1.0, r.sm)
             r.check(got, FULL_BOUND, ones=values is r.ones)
+
+
+@pytest.mark.parametrize("tile", [64, 128])
+@pytest.mark.parametrize("width,ctas", [(1024, 1), (2048, 1), (2048, 2), (2048, 3), (2048, 0), (8192, 1), (8192, 2), (8191, 7)])
+def test_selected(api, width, ctas, tile):
+    """Every position selected, in order; one row on one block, two, three and many."""
+    n = 1 if ctas else 40
+    ws = api.alloc_workspace(n, 1, 64, width, num_ctas=ctas)
+    sel = torch.arange(width, dtype=torch.int32, device="cuda").repeat(n, 1)
+    lens = torch.full((n,), width, dtype=torch.int32, device="cuda")
+    for peak in FRACTIONS:
+        r = Rows(n, width, peak)
+        for values in (r.k, r.ones):
+            got = api.decode_ws(r.q, r.k, values, r.tables, 0, lens, sel, n, 1, 64, 64, 64 * 512, 1.0, 1.0, r.sm,
+                                torch.empty_like(r.q), ws, num_ctas=ctas, tile_tokens=tile)
+            r.check(got, SELECTED_BOUND, ones=values is r.ones)
+        assert api.read_device_status(ws) == 0
