@@ -462,9 +462,15 @@ __device__ void run_softmax(const Cta& c) {
         return pair < p.pairs ? row_len(p, unit / p.groups, pair / p.heads, &over) : 0;
     };
 
+    // What turns its dots into log2 scores. A broken query's is NaN, which would also reach the
+    // -inf of hidden tokens: a pair that sees none (a padding row) takes 1 and stays at zero.
+    auto pair_scale = [&](int32_t unit, int32_t len) {
+        return len > 0 ? p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hq] : 1.0f;
+    };
+
     Segment next = c.start.first;
-    float c_next = p.qscale[static_cast<int64_t>(next.unit) * kHeadsPerCta + hq];
     int32_t len_next = pair_len(next.unit);
+    float c_next = pair_scale(next.unit, len_next);
     bool q_loaded = false;  // the unit's query operand was loaded during the unit before
     bool pv_seen = false;   // the P.V two tiles back was already waited for
     for (;;) {
@@ -473,8 +479,8 @@ __device__ void run_softmax(const Cta& c) {
         const int32_t len = len_next;
         if (!s.last) {
             next = c.next(s);
-            c_next = p.qscale[static_cast<int64_t>(next.unit) * kHeadsPerCta + hq];
             len_next = pair_len(next.unit);
+            c_next = pair_scale(next.unit, len_next);
         }
         if (!q_loaded) {
             if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
