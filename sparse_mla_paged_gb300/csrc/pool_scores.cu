@@ -402,6 +402,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
                 for (int i = 0; i < p.box_rows; ++i) scales[lane * p.box_rows + i] = kNegInf;
                 if (p.status) atomicCAS(p.status, 0, kStatusBounds);
             }
+            __syncwarp();  // lane 0's arrival releases these stores too
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
             const uint32_t full = b.bar(S::BAR_FULL + e);
             if (lane == 0) mbar_arrive_expect_tx(full, boxes * (box_codes + box_scales));
