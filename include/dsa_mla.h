@@ -449,6 +449,16 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
                             void* stream);
 
 /*
+ * dsa_set_wait_limit: the longest time in nanoseconds that one wait inside the kernels of
+ * dsa_pool_scores and dsa_mla_decode_full may take, for later calls of the calling host
+ * thread (a captured call keeps the limit of its capture); one second by default (0) and
+ * at most.
+ * A wait that runs out ends the call with DSA_ERR_TIMEOUT on the device and results that
+ * are not to be used. dsa_mla_decode_ws takes its limit per call (wait_limit_ns).
+ */
+int32_t dsa_set_wait_limit(uint64_t limit_ns);
+
+/*
  * Device status of the latest call on a caller workspace (dsa_mla_decode_ws /
  * dsa_mla_decode_host / dsa_mla_decode_full), on the library workspace of the current device
  * (dsa_last_device_status), or on the fixed array of dsa_mla_decode_static

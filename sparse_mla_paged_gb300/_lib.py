@@ -25,6 +25,7 @@ STATUS = {
 DSA_OK = 0
 
 _P, _I32, _I64, _F32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_U64 = ctypes.c_uint64
 
 
 class DecodeOptions(ctypes.Structure):
@@ -56,6 +57,7 @@ SIGNATURES = {
     "dsa_mla_decode_full_workspace_bytes": ([_I32, _I32, _I32], _SZ),
     "dsa_mla_decode_full": ([_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P, _I32, _P,
                              _SZ, _P], _I32),
+    "dsa_set_wait_limit": ([_U64], _I32),
     "dsa_absorb_q": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "dsa_absorb_o": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "dsa_read_device_status": ([_P, _P, _P], _I32),

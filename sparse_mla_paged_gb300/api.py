@@ -7,6 +7,7 @@ raise DsaError on a non-OK status.
 from __future__ import annotations
 
 import contextlib
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -368,6 +369,25 @@ def index_write(keys: torch.Tensor, slots: torch.Tensor, block_size: int, page_s
                                           eps, block_size, page_stride_bytes, index_cache.data_ptr(), at.raw),
               "dsa_index_write")
     return index_cache
+
+
+_wait_limits = threading.local()
+
+
+@contextlib.contextmanager
+def wait_limit(limit_ns: int):
+    """dsa_set_wait_limit for this thread's pool_scores and decode_full calls inside the block
+    (0: the default), the limit outside it after that."""
+    if not 0 <= limit_ns < 1 << 64:
+        raise ValueError("limit_ns must be a 64-bit number of nanoseconds")
+    outer = getattr(_wait_limits, "ns", 0)
+    check(_lib.load().dsa_set_wait_limit(limit_ns), "dsa_set_wait_limit")
+    _wait_limits.ns = limit_ns
+    try:
+        yield
+    finally:
+        _wait_limits.ns = outer
+        check(_lib.load().dsa_set_wait_limit(outer), "dsa_set_wait_limit")
 
 
 def _table_rows(block_tables, max_blocks_per_seq, num_seqs):

@@ -131,7 +131,8 @@ struct CallOptions {
     cudaEvent_t ev0 = nullptr, ev1 = nullptr;
 };
 
-constexpr uint64_t kDefaultWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
+// dsa_set_wait_limit: the calling thread's, for the entry points without options.
+thread_local uint64_t g_wait_limit_ns = kDefaultWaitLimitNs;
 
 int32_t read_options(const dsa_decode_options* o, CallOptions* out) {
     CallOptions c;
@@ -784,6 +785,7 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     }
     p.per_tile = tokens / kpool;
     p.by_tile = fast_div(static_cast<uint32_t>(p.per_tile));
+    p.wait_limit_ns = g_wait_limit_ns;
     CUtensorMap tmap;
     std::memset(&tmap, 0, sizeof tmap);
     if (p.box_rows > 0 &&
@@ -864,6 +866,7 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     p.kv_same = k_cache == v_cache ? 1 : 0;
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;
+    p.wait_limit_ns = g_wait_limit_ns;
     p.box_rows = std::min(box_rows(block_size), 32);  // other page sizes take per-thread copies
     CUtensorMap kmap, vmap;
     std::memset(&kmap, 0, sizeof kmap);
@@ -877,6 +880,11 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     if (st == DSA_OK) st = from_cuda(launch_full(p, kmap, vmap, s));
     if (st == DSA_OK) st = from_cuda(launch_full_combine(p, s));
     return st;
+}
+
+int32_t dsa_set_wait_limit(uint64_t limit_ns) {
+    g_wait_limit_ns = limit_ns == 0 || limit_ns > kDefaultWaitLimitNs ? kDefaultWaitLimitNs : limit_ns;
+    return DSA_OK;
 }
 
 int32_t dsa_read_device_status(const void* workspace, int32_t* status_out, void* stream) {

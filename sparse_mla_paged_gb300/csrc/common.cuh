@@ -46,6 +46,7 @@ constexpr float kLostShare = 0x1p-8f;
 // Device status codes mirror dsa_status.
 constexpr int kStatusBounds = DSA_ERR_DEVICE_BOUNDS;
 constexpr int kStatusTimeout = DSA_ERR_TIMEOUT;
+constexpr uint64_t kDefaultWaitLimitNs = 1000ull * 1000ull * 1000ull;  // of a pipeline wait: 1 s
 
 // Division of any 32-bit x by a divisor known on the host, in five instructions (Granlund and
 // Montgomery, "Division by Invariant Integers using Multiplication", 1994, figure 4.1); the
@@ -281,6 +282,7 @@ struct PoolScoresParams {
     FastDiv by_block, by_kpool;
     int32_t per_tile;          // pools of a tile
     FastDiv by_tile;           // per_tile
+    uint64_t wait_limit_ns;    // per pipeline wait
 };
 
 // Launchers (each defined next to its kernel).

@@ -110,7 +110,6 @@ constexpr float kSlack = 2.0f;
 // pays for itself: 2^5 * kLostShare = 128 * 2^-10.) Scores of deviation 1 never ask; of
 // deviation 2 in natural units, 56 of 128 tiles of 64 pairs move a reference, 25 without it.
 constexpr float kMostLost = kScores * 0x1p-10f;  // by a thread in a tile
-constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Warps of the two variants.
@@ -144,7 +143,7 @@ struct Cta {
         *abort_flag = 1;
     }
     __device__ void wait(int b, uint32_t parity) const {
-        if (!mbar_wait(bar(b), parity, abort_flag, kWaitNs)) fail(kStatusTimeout);
+        if (!mbar_wait(bar(b), parity, abort_flag, p.wait_limit_ns)) fail(kStatusTimeout);
         __syncwarp();
     }
     // The stretch after s (not its last).

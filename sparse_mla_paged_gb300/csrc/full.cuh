@@ -162,6 +162,7 @@ struct Params {
     int32_t kv_same;
     float score_scale;         // sm_scale * k_scale * log2(e)
     float v_scale;
+    uint64_t wait_limit_ns;
 };
 
 #ifdef __CUDACC__

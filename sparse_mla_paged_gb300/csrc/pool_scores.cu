@@ -98,7 +98,6 @@ struct Shape {
     static_assert(kCtas * (kSmem + 1024) <= 228 * 1024 && kCtas * kTmemCols <= 512, "blocks per SM");
 };
 
-constexpr uint64_t kWaitNs = 1000ull * 1000ull * 1000ull;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -175,7 +174,13 @@ struct Block {
         *abort_flag = 1;
     }
     __device__ void wait(int b, uint32_t parity) const {
-        if (!mbar_wait(bar(b), parity, abort_flag, kWaitNs)) fail(kStatusTimeout);
+        if (!mbar_wait(bar(b), parity, abort_flag, p.wait_limit_ns)) fail(kStatusTimeout);
+        __syncwarp();
+    }
+    // The epilogue's: the longest limit, or less once another warp gave up (the call's own limit
+    // between its FMAs makes 1024 rows over 32768 tokens 390 to 405 us, 378 without).
+    __device__ void epilogue_wait(int b, uint32_t parity) const {
+        if (!mbar_wait(bar(b), parity, abort_flag, kDefaultWaitLimitNs)) fail(kStatusTimeout);
         __syncwarp();
     }
     __device__ int32_t visible(int32_t row) const {
@@ -370,7 +375,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
     const int tokens = b.per_tile * p.kpool;
     const bool mine = lane * p.box_rows < tokens;
     const uint32_t box_codes = static_cast<uint32_t>(p.box_rows) * kIndexDim, box_scales = static_cast<uint32_t>(p.box_rows) * 4u;
-    uint32_t tau = 0;
+    uint32_t tau = 0, issued = 0;  // tiles so far, and past the last one that this warp asked for
     bool stop = false;
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
         const int32_t limit = x.seen * p.kpool;
@@ -413,18 +418,20 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
                          p.cache + page * p.page_stride + static_cast<int64_t>(p.block_size) * kIndexDim + static_cast<int64_t>(row) * 4, box_scales, full);
             }
             __syncwarp();
+            issued = ta + 1;
         }
         tau += static_cast<uint32_t>(t1 - t0);
     });
     fill(b);
-    // No copy into shared memory is in flight when the block exits: the last tiles' bytes (after
-    // an abort some of them were never asked for: their waits end at the limit).
+    // No copy into shared memory is in flight when the block exits: the bytes of the last tiles
+    // that were asked for. (Waited for by the tiles of the whole range, which an abort leaves
+    // unasked, a slot's wait could have been for a phase of the other parity and passed at once.)
     if (lane == 0) {
-        for (uint32_t i = tau > S::kStages ? tau - S::kStages : 0; i < tau; ++i) {
+        for (uint32_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i) {
             if ((i & (S::kMmaWarps - 1)) != w) continue;
             const uint64_t since = globaltimer_ns();
             while (!mbar_try_wait(b.bar(S::BAR_FULL + static_cast<int>(i % S::kStages)), (i / S::kStages) & 1) &&
-                   globaltimer_ns() - since < (stop ? kDrainLimitNs / S::kStages : kDrainLimitNs)) {
+                   globaltimer_ns() - since < kDrainLimitNs) {
             }
         }
     }
@@ -562,7 +569,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
     const int row_first = kHalves ? 0 : set * kRows;
     uint32_t tau = 0, entered = 0;
     b.stretches([&](const Unit& x, int32_t t0, int32_t t1) {
-        if (entered > 0) b.wait(S::BAR_QSEEN, (entered - 1) & 1);
+        if (entered > 0) b.epilogue_wait(S::BAR_QSEEN, (entered - 1) & 1);
         ++entered;
         // The unit before is done with: its last D buffer was full, so its MMAs have read the
         // queries, and every epilogue warp has its weights.
@@ -602,7 +609,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
             for (int r = 0; r < kRows; ++r)
                 if (r < mine && held_at < room) out[static_cast<int64_t>(r) * p.n_pools + held_at] = held_at < vis[r] ? held[r] : kNegInf;
         };
-        b.wait(S::BAR_DFULL + static_cast<int>(tau % S::kDBufs), (tau / S::kDBufs) & 1);
+        b.epilogue_wait(S::BAR_DFULL + static_cast<int>(tau % S::kDBufs), (tau / S::kDBufs) & 1);
         tc_fence_after();
         uint32_t v[2][kChunk];
         load_columns(lanes + tau % S::kDBufs * kCols, v[0]);
@@ -629,7 +636,7 @@ __device__ void run_epilogue(const Block<kCols>& b, uint32_t tmem) {
                         if (lane == 0) mbar_arrive(b.bar(S::BAR_DEMPTY + static_cast<int>(d)));
                         // Past the last tile the columns hold anything; they are not used. (Branches
                         // between the FMAs cost more: one around three exchanges made prefill 514 us.)
-                        if (!__all_sync(0xffffffffu, ready)) b.wait(S::BAR_DFULL + static_cast<int>(d_next), turn_next);
+                        if (!__all_sync(0xffffffffu, ready)) b.epilogue_wait(S::BAR_DFULL + static_cast<int>(d_next), turn_next);
                         tc_fence_after();
                         load_columns(lanes + d_next * kCols, v[0]);
                     }
