@@ -33,7 +33,7 @@
  *    max_blocks_per_seq, a pipeline wait that ran out of time) do not fault: the kernel
  *    skips the access and records the first such status in the workspace's status
  *    word, read back with dsa_read_device_status / dsa_last_device_status /
- *    dsa_static_device_status. The output of a call that recorded a device status is
+ *    dsa_static_device_status / dsa_step_device_status. The output of a call that recorded a device status is
  *    undefined.
  */
 #ifndef DSA_MLA_H
@@ -401,7 +401,8 @@ int32_t dsa_index_write(const void* keys, const void* norm_weight, const void* n
  *  block_tables, max_blocks_per_seq  as for dsa_mla_decode (0: one shared table).
  *  q_pos         int32 [R]; -1 sees nothing.
  *  scores        float32 [R, n_pools], 4-byte aligned; every element is written.
- *  device_status int32 device word or null: DSA_ERR_DEVICE_BOUNDS is put there (when it
+ *  device_status int32 device word, or null for the device's own, which
+ *                dsa_step_device_status reads: DSA_ERR_DEVICE_BOUNDS is put there (when it
  *                holds 0) if a visible position's block-table entry is negative or past
  *                max_blocks_per_seq (the pool's score is then -inf or that of its other
  *                positions), DSA_ERR_TIMEOUT if a pipeline wait ran out of time. The call
@@ -434,8 +435,9 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
  *  workspace    device memory, 256-byte aligned, at least
  *               dsa_mla_decode_full_workspace_bytes of the same num_seqs, rows_per_seq and
  *               num_q_heads. The call never allocates and can be captured. Its first 256
- *               bytes hold the device status word (dsa_read_device_status). Calls that may
- *               overlap on the GPU need workspaces of their own.
+ *               bytes hold the device status word (dsa_read_device_status); what is recorded
+ *               there also goes to dsa_step_device_status. Calls that may overlap on the GPU
+ *               need workspaces of their own.
  *  num_seqs*rows_per_seq*num_q_heads at most 2^22 (DSA_ERR_UNSUPPORTED above).
  */
 size_t dsa_mla_decode_full_workspace_bytes(int32_t num_seqs, int32_t rows_per_seq,
@@ -469,6 +471,15 @@ int32_t dsa_set_wait_limit(uint64_t limit_ns);
 int32_t dsa_read_device_status(const void* workspace, int32_t* status_out, void* stream);
 int32_t dsa_last_device_status(int32_t* status_out, void* stream);
 int32_t dsa_static_device_status(int32_t* status_out, void* stream);
+
+/*
+ * The first device status that dsa_pool_scores calls without a device_status word or any
+ * dsa_mla_decode_full calls recorded on the current device since this was last called (by
+ * any host thread), and clears it: one check after a step, whoever keeps its workspaces.
+ * Synchronises the stream, writes the status to *status_out and returns DSA_OK, or
+ * returns DSA_ERR_CUDA. Calls on other streams count once their work has run.
+ */
+int32_t dsa_step_device_status(int32_t* status_out, void* stream);
 
 #ifdef __cplusplus
 }

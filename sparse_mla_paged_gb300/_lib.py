@@ -60,6 +60,7 @@ SIGNATURES = {
     "dsa_set_wait_limit": ([_U64], _I32),
     "dsa_absorb_q": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "dsa_absorb_o": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
+    "dsa_step_device_status": ([_P, _P], _I32),
     "dsa_read_device_status": ([_P, _P, _P], _I32),
     "dsa_last_device_status": ([_P, _P], _I32),
     "dsa_static_device_status": ([_P, _P], _I32),

@@ -401,7 +401,8 @@ def pool_scores(q: torch.Tensor, head_weights: torch.Tensor, index_cache: torch.
                 block_size: int, page_stride_bytes: int, kpool: int, n_pools: int, out=None, device_status=None,
                 stream=None) -> torch.Tensor:
     """dsa_pool_scores: float32 [R, n_pools], per row the maximum over each pool's kpool positions of
-    scale_j * sum_h head_weights[h] * max(0, q[h] . k_j); -inf for pools that end after q_pos."""
+    scale_j * sum_h head_weights[h] * max(0, q[h] . k_j); -inf for pools that end after q_pos.
+    Without a device_status word (int32 [1]) step_device_status tells of bad pages."""
     i = _device_of(q, "q")
     _need_on(q, torch.bfloat16, "q", i)
     _need_on(head_weights, torch.float32, "head_weights", i)
@@ -449,7 +450,7 @@ def decode_full(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
                 stream=None) -> torch.Tensor:
     """dsa_mla_decode_full: every row attends to its whole cache; seq_lens per row, or with
     verify_rows per sequence before its rows. Returns out (bf16 [R, H, 512]). Without a
-    workspace one is allocated for the call."""
+    workspace one is allocated for the call. step_device_status tells of bad pages and lengths."""
     i = _device_of(q, "q")
     _need_on(q, torch.bfloat16, "q", i)
     _need_on(k_cache, torch.uint8, "k_cache", i)
@@ -488,6 +489,14 @@ def read_device_status(workspace: torch.Tensor, stream=None) -> int:
 def last_device_status(stream=None) -> int:
     v = _lib.ctypes.c_int32(0)
     check(_lib.load().dsa_last_device_status(_lib.ctypes.byref(v), _stream(stream)), "dsa_last_device_status")
+    return int(v.value)
+
+
+def step_device_status(stream=None) -> int:
+    """First device status of pool_scores calls without a device_status and of decode_full calls on
+    the current device since this was last called; clears it."""
+    v = _lib.ctypes.c_int32(0)
+    check(_lib.load().dsa_step_device_status(_lib.ctypes.byref(v), _stream(stream)), "dsa_step_device_status")
     return int(v.value)
 
 

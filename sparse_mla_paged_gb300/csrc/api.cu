@@ -26,7 +26,13 @@ struct DeviceState {
     size_t mem_bytes = 0;     // device memory size: bounds the rows a cache tensor map spans
     void* ws = nullptr;       // library-owned workspace
     size_t ws_bytes = 0;
+    int* step_status = nullptr;  // address of g_step_status
 };
+
+// First status of the calls that dsa_step_device_status covers, and the one last read.
+__device__ int g_step_status[2];
+
+__global__ void take_step_status() { g_step_status[1] = atomicExch(g_step_status, 0); }
 
 std::mutex g_mu;
 std::vector<DeviceState> g_devices;
@@ -97,7 +103,10 @@ int32_t current_device(DeviceState** out) {
         if (major != 10 || minor != 3) {
             d.status = DSA_ERR_UNSUPPORTED;
         } else {
-            d.status = from_cuda(decode_kernel_setup_64());
+            void* word = nullptr;
+            d.status = from_cuda(cudaGetSymbolAddress(&word, g_step_status));
+            d.step_status = static_cast<int*>(word);
+            if (d.status == DSA_OK) d.status = from_cuda(decode_kernel_setup_64());
             if (d.status == DSA_OK) d.status = from_cuda(decode_kernel_setup_128());
             if (d.status == DSA_OK) d.status = from_cuda(prologue_kernel_setup());
             if (d.status == DSA_OK) d.status = from_cuda(combine_kernel_setup());
@@ -761,7 +770,7 @@ int32_t dsa_pool_scores(const void* q, const float* head_weights, const void* in
     p.block_tables = block_tables;
     p.q_pos = q_pos;
     p.scores = scores;
-    p.status = device_status;
+    p.status = device_status ? device_status : d->step_status;
     p.page_stride = page_stride_bytes;
     p.num_seqs = num_seqs;
     p.rows_per_seq = rows_per_seq;
@@ -841,6 +850,7 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     p.seq_lens = seq_lens;
     p.out = static_cast<uint16_t*>(out);
     p.status = reinterpret_cast<int*>(ws + L.status);
+    p.step_status = d->step_status;
     p.plan.cta = reinterpret_cast<full::CtaStart*>(ws + L.cta);
     p.plan.pieces = reinterpret_cast<full::UnitPieces*>(ws + L.pieces);
     p.plan.start = reinterpret_cast<int64_t*>(ws + L.start);
@@ -896,6 +906,18 @@ int32_t dsa_read_device_status(const void* workspace, int32_t* status_out, void*
         return DSA_ERR_CUDA;
     *status_out = v;
     return DSA_OK;
+}
+
+int32_t dsa_step_device_status(int32_t* status_out, void* stream) {
+    if (!status_out) return DSA_ERR_INVALID_ARGUMENT;
+    DeviceState* d = nullptr;
+    int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    static std::mutex mu;  // readers share the second word
+    std::lock_guard<std::mutex> lock(mu);
+    take_step_status<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>();
+    st = from_cuda(cudaGetLastError());
+    return st == DSA_OK ? dsa_read_device_status(d->step_status + 1, status_out, stream) : st;
 }
 
 int32_t dsa_last_device_status(int32_t* status_out, void* stream) {

@@ -275,7 +275,7 @@ struct PoolScoresParams {
     const int32_t* block_tables;
     const int32_t* q_pos;      // [R]
     float* scores;             // [R, n_pools]
-    int* status;               // or null
+    int* status;
     int64_t page_stride;
     int32_t num_seqs, rows_per_seq, heads, block_size, max_blocks_per_seq, kpool, n_pools;
     int32_t box_rows;          // tokens of a tensor-map box, 0: per-thread copies

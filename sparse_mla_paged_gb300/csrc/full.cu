@@ -139,7 +139,7 @@ struct Cta {
 
     __device__ uint32_t bar(int i) const { return sbase + kOffBars + 8 * i; }
     __device__ void fail(int code) const {
-        atomicCAS(p.status, 0, code);
+        report(p, code);
         *abort_flag = 1;
     }
     __device__ void wait(int b, uint32_t parity) const {
@@ -192,7 +192,7 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* kmap, const CUtens
             row = row_next;
             live = live_next;
             page_next = look(t + 1, &row_next, &live_next);
-            if (live && page < 0) atomicCAS(p.status, 0, kStatusBounds);
+            if (live && page < 0) report(p, kStatusBounds);
             const int e = static_cast<int>(tau % slots);
             const uint32_t full = c.bar(BAR_FULL0 + e);
             const uint32_t lives = __ballot_sync(0xffffffffu, live);
@@ -252,7 +252,7 @@ __device__ void run_load_copies(const Cta& c) {
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             const int32_t page = page_next, row = row_next;
             page_next = look(t + 1, &row_next);
-            if (page < 0) atomicCAS(p.status, 0, kStatusBounds);
+            if (page < 0) report(p, kStatusBounds);
             const int64_t mine = page < 0 || row < 0 ? -1 : page * p.cache_stride + static_cast<int64_t>(row) * kLatent;
             const int e = static_cast<int>(tau % slots);
             if (tau >= static_cast<uint32_t>(slots)) c.wait(BAR_EMPTY0 + e * kQuarters + w, (tau / slots - 1) & 1);

@@ -148,7 +148,8 @@ struct Params {
     const int32_t* block_tables;
     const int32_t* seq_lens;   // [R], or [num_seqs] before the verify rows
     uint16_t* out;             // bf16 bits [R, heads, 512]
-    int* status;
+    int* status;               // of the call, in its workspace
+    int* step_status;          // of the device, see dsa_step_device_status
     PlanArrays plan;
     uint8_t* qimg;             // [units, 64 KB]
     float* qscale;             // [units, 64]
@@ -166,6 +167,10 @@ struct Params {
 };
 
 #ifdef __CUDACC__
+__device__ __forceinline__ void report(const Params& p, int code) {
+    atomicCAS(p.status, 0, code);
+    atomicCAS(p.step_status, 0, code);
+}
 // Tokens that a row sees. `given` may pass the block table's room: *over says so.
 __device__ __forceinline__ int32_t row_len(const Params& p, int64_t seq, int32_t i, bool* over) {
     int64_t n = p.verify_rows ? static_cast<int64_t>(p.seq_lens[seq]) + i + 1 : p.seq_lens[seq * p.rows_per_seq + i];

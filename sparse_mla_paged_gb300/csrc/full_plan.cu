@@ -130,7 +130,7 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
                                                      p.plan.max_len[first], p.plan.min_len[first]), line.gap, 0};
     }
     // The status was cleared before the scan's barriers.
-    if (any_over) atomicCAS(p.status, 0, kStatusBounds);
+    if (any_over) report(p, kStatusBounds);
 }
 
 // Query operand of a lane quarter of one unit, 16 of its pairs, as the selected decode's prologue

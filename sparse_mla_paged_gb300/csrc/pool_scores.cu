@@ -170,7 +170,7 @@ struct Block {
 
     __device__ uint32_t bar(int i) const { return sbase + S::kOffBars + 8 * i; }
     __device__ void fail(int code) const {
-        if (p.status) atomicCAS(p.status, 0, code);
+        atomicCAS(p.status, 0, code);
         *abort_flag = 1;
     }
     __device__ void wait(int b, uint32_t parity) const {
@@ -405,7 +405,7 @@ __device__ void run_load_boxes(const Block<kCols>& b, const CUtensorMap* tmap) {
             float* scales = reinterpret_cast<float*>(b.smem + S::kOffScale) + (ta % S::kScaleSlots) * kTile;
             if (page == -1) {  // tokens without a page score -inf
                 for (int i = 0; i < p.box_rows; ++i) scales[lane * p.box_rows + i] = kNegInf;
-                if (p.status) atomicCAS(p.status, 0, kStatusBounds);
+                atomicCAS(p.status, 0, kStatusBounds);
             }
             __syncwarp();  // lane 0's arrival releases these stores too
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
@@ -493,7 +493,7 @@ __device__ void run_load(const Block<kCols>& b) {
                                  "l"(p.cache + code[i] + to_scale[i]) : "memory");
                 } else {
                     *slot = kNegInf;  // a token without a page scores -inf
-                    if (code[i] == kBad && p.status) atomicCAS(p.status, 0, kStatusBounds);
+                    if (code[i] == kBad) atomicCAS(p.status, 0, kStatusBounds);
                 }
             }
             cp_async_arrive_noinc(b.bar(S::BAR_FULL + e));
