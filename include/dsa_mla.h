@@ -345,12 +345,16 @@ int32_t dsa_mla_decode_static(const void* q, const void* k_cache, const void* v_
  *  block_tables  int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq >= 1.
  *  slots  int64 [max_rows], 8-byte aligned; positions, row_lens, row_seqs  int32 [max_rows].
  *  info   int32 [4]: new tokens (cut to the rows there are), pages taken, status, 0. A caller
- *         advances its free list by info[1]. The status is DSA_ERR_DEVICE_BOUNDS when a length is negative
- *         (taken as 0), a request has more new tokens than rows_per_seq (cut to it) or than
- *         its table holds (the tokens past the table have rows without a token), the packed
- *         rows exceed max_rows (the last ones are dropped; their pages are assigned), the
- *         free pages run out (their table entries become -1, the slots of their tokens too)
- *         or a table entry that cached tokens already need is negative; else DSA_OK.
+ *         advances its free list by info[1] before the next step (a captured call's free_pages
+ *         and num_free stay those of its capture: the caller moves the remaining ids to the
+ *         front of the buffer before a replay, as it writes that step's lengths). The status
+ *         is DSA_ERR_DEVICE_BOUNDS when a length is negative (taken as 0), a request has more
+ *         new tokens than rows_per_seq (cut to it) or more tokens in all than its table holds
+ *         (new tokens past the table have rows without a token), the packed rows exceed
+ *         max_rows (the last ones are dropped; their pages are assigned), the free pages run
+ *         out (their table entries become -1, the slots of their tokens too) or the page that
+ *         a request's first new token shares with cached ones is negative in the table (no
+ *         other entry of cached tokens is read); else DSA_OK.
  *  num_seqs 0..DSA_MAX_PLAN_SEQS, num_free >= 0, max_rows >= 0; max_blocks_per_seq*
  *  block_size below 2^31 (DSA_ERR_UNSUPPORTED otherwise). Pointers to empty arrays may be
  *  null. The call is idempotent: run again on the same input it writes the same values.

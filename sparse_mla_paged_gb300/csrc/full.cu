@@ -349,8 +349,8 @@ __device__ void run_pv(const Cta& c) {
 // softmax / output warps
 // ------------------------------------------------------------------------------------
 // Two probabilities as two E4M3 terms each (hi: rounded to nearest; lo: what is left of the
-// float16 value, whose own rounding of 2^-12 is far below lo's 2^-9). Through float16 pairs
-// this takes five instructions where single floats take eight.
+// float16 value, whose own rounding of 2^-12 is far below lo's 2^-9 of P'; kMostLost has what small
+// ones lose). Through float16 pairs this takes five instructions where single floats take eight.
 __device__ __forceinline__ void split2(float p0, float p1, uint32_t& hi, uint32_t& lo) {
     uint16_t h, l;
     asm("{\n\t.reg .b32 v, r, d;\n\t"

@@ -135,12 +135,13 @@ __device__ void make_plan(const Params& p, int32_t* cta_k) {
 
 // Query operand of a lane quarter of one unit, 16 of its pairs, as the selected decode's prologue
 // makes it: a warp per pair, lane l dims [16l, 16l+16); a head's bf16 query as two E4M3 terms
-// after a scaling by a power of two (exact for elements above 2^-10 of its largest), rows 2k and
-// 2k+1 of the quarter the two terms of its pair k, stored chunk-major. The head's scale of its
-// dots is positive (the decode takes maxima of the dots): a negative score scale turns the
-// codes' signs, a zero one zeroes the codes. A head with a NaN or an infinity gets zero codes and
-// a NaN scale, which makes all its scores NaN. A unit without a token writes its zeros here. (A
-// block per unit, four pairs a warp, ended a microsecond later than the plan does.)
+// after a scaling by a power of two (exact for elements from 2^-9 of its largest, smaller ones off
+// by 2^-16 of it at most), rows 2k and 2k+1 of the quarter the two terms of its pair k, stored
+// chunk-major. The head's scale of its dots is positive (the decode takes maxima of the dots): a
+// negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or
+// an infinity gets zero codes and a NaN scale, which makes all its scores NaN. A unit without a
+// token writes its zeros here. (A block per unit, four pairs a warp, ended a microsecond later
+// than the plan does.)
 __device__ void prepare(const Params& p, int32_t unit, int quarter, uint8_t* stage) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hl = kQuarterPairs * quarter + warp;

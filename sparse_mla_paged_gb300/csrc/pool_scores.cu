@@ -9,10 +9,11 @@
 // queries of up to 128/heads rows of one sequence the B operand (N = rows x heads). A BF16
 // query is two E4M3 terms (hi = its top 4 significant bits after scaling its head by a power
 // of two, lo = the rest), both accumulated into the same FP32 columns, so the product is
-// exact but for elements below 2^-11 of their head's largest. With tokens as rows of D, a
-// token's heads lie in one thread's columns: the relu, the weighted sum over heads and the
-// key's scale need no exchange between threads, and the maximum over a pool's tokens is a few
-// shuffles between neighbouring lanes. The power of two goes into the head's weight.
+// exact but for elements below 2^-9.9 of their head's largest (they may be off by 2^-16.9 of it:
+// a third term would cost half as many MMAs again). With tokens as rows of D, a token's heads
+// lie in one thread's columns: the relu, the weighted sum over heads and the key's scale need no
+// exchange between threads, and the maximum over a pool's tokens is a few shuffles between
+// neighbouring lanes. The power of two goes into the head's weight.
 //
 // A unit is a group of rows of one sequence; its 128-token tiles up to the last pool that one
 // of its rows sees stand on a line, unit after unit with gaps between (kGap), that is cut into
