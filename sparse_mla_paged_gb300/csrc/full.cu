@@ -26,13 +26,15 @@
 // What bounds it is the tensor core with its operands from shared memory: a tile's Q.K^T takes 16
 // MMAs of 64 cycles, its P.V 32 of 48 (N = 64 computes for 32, but reads 6 KB of operands), 2560
 // cycles, and the softmax chain of a tile 2200 beside it; a tile takes some 2900. On long work
-// the GPU runs at its power limit, at 1640 to 1790 MHz. Measured (plan and join included): two
-// contexts of 512 thousand tokens with 128 heads 199 us, 1360 TFLOP/s (each product counted
-// once; 141 us at the rate of a BF16 product); 64 rows of 64 heads over 8 to 32 thousand tokens
-// 132 us, 4.9 TB/s in all and 6 in the middle; 32 sequences of four rows of 16 heads over 16384
-// tokens 68 us, 9 of them before the first scores and 10 after the first CTAs' last; one row over
-// 777 tokens 16 us. One warp issuing both products took 15 % more (10 % with V's tile kept in the
-// collector for the second term of P'); sixteen softmax warps were slower too.
+// the GPU runs at its power limit, at 1640 to 1790 MHz. Measured (plan and join included, in
+// bursts): two contexts of 512 thousand tokens with 128 heads 200 us, 1350 TFLOP/s (each product
+// counted once; 141 us at the rate of a BF16 product; 218 at the power limit); 64 rows of 64
+// heads over 8 to 32 thousand tokens 134 us (143), 4.9 TB/s in all and 6 in the middle; 32
+// sequences of four rows of 16 heads over 16384 tokens 68 us, 9 of them before the first scores
+// and 10 after the first CTAs' last; one row over 777 tokens 16 us; 128 requests of 200 to 2048
+// tokens 46 us, most of it unit changes. With K and V apart the ring holds one tile of both, and
+// the ragged rows take 326 us. One warp issuing both products took 15 % more (10 % with V's tile
+// kept in the collector for the second term of P'); sixteen softmax warps were slower too.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,8 +66,8 @@ constexpr int kBarPair0 = 2;  // 2..5: the two softmax warps of a lane quarter
 
 constexpr int kOffP = kRingTiles * kTileBytes;               // P' [2 buffers][hi, lo]; epilogue staging
 constexpr int kOffHm = kOffP + 4 * kPTermBytes;              // float [2 token halves][64] tile maxima; row sums at the end
-constexpr int kOffAlpha = kOffHm + 2 * kHeadsPerCta * 4;     // float [2 tile parities][64] rescale factors
-constexpr int kOffF = kOffAlpha + 2 * kHeadsPerCta * 4;      // float [64] output factors
+constexpr int kOffAlpha = kOffHm + 2 * kHeadsPerCta * 4;     // float [2 tile parities][64] rescale factors; accounts in passing
+constexpr int kOffF = kOffAlpha + 2 * kHeadsPerCta * 4;      // float [64] output factors; accounts in passing
 constexpr int kOffFlags = kOffF + kHeadsPerCta * 4;          // u32 [2 tile parities][4 lane quarters]
 constexpr int kOffBroken = kOffFlags + 2 * 4 * 4;            // 128 bits: an edge tile's tokens with a NaN code
 constexpr int kOffBars = kOffBroken + kTile / 8;
@@ -97,7 +99,7 @@ constexpr uint32_t kTmemS = 384;
 // A reference is this much above its tile's maximum. Each move costs the CTA about a
 // microsecond (the pipeline drains): with normal scores of deviation 1, 8 of 106 tiles of 64
 // pairs moved at the selected decode's 1 octave and moves of the asking pairs only (two contexts
-// of 512 thousand tokens: 205 us, now 199). The lowest tile maximum that a reference serves,
+// of 512 thousand tokens: 205 us, 199 with them). The lowest tile maximum that a reference serves,
 // kRescaleDrop below it, is the same.
 constexpr float kSlack = 2.0f;
 // What the two E4M3 terms of a P' lose: 2^-10 at most (it itself when below), beside 1.2 * 2^-9 of

@@ -9,12 +9,12 @@
 //
 // Eight lanes take one row, sixteen consecutive dims each (the norm's sums and the maximum
 // are three shuffles), and persistent blocks keep the weights in registers, a row's loads in
-// flight while the one before is written. Instructions bound it rather than bytes: 262144 rows
-// with the norm take 21.8 us (4.8 TB/s of the 104 MB read and written, which the HBM moves in
-// 15.5 us; 61 % of the issue slots under a profiler), 64 rows 1.9 us. With sixteen lanes a row,
-// 64-bit divisions of the slot and no reuse of the weights it took 41 us; two dims an
-// instruction in the norm were the last step, from 24. More blocks per SM with fewer registers
-// each were no faster.
+// flight while the one before is written. A row's chain of dependent instructions bounds it
+// rather than bytes: 262144 rows with the norm take 22 us (4.7 TB/s of the 104 MB read and
+// written, which the HBM moves in 15.5 us; 61 % of the issue slots under a profiler), without it
+// 23, 64 rows 1.9 us. With sixteen lanes a row, 64-bit divisions of the slot and no reuse of the
+// weights it took 41 us; two dims an instruction in the norm were the last step, from 24. More
+// blocks per SM with fewer registers each were no faster.
 #include "common.cuh"
 #include "ptx.cuh"
 

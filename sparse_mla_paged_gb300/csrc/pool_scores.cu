@@ -31,11 +31,12 @@
 // for every tile they cost as much of it as the MMAs (pooled 128k 413 us, prefill 588).
 //
 // Measured, 64 heads: 128 rows over 131072 tokens each (pooled 128k) 327 us, 6.8 TB/s, what a
-// copy of the keys would take. 1024 rows over one cache of 32768 tokens (prefill) 370 us, 1530
-// TFLOP/s with the two terms counted once, 0.79 of the rate of a BF16 product; there the issue
+// copy of the keys would take. 1024 rows over one cache of 32768 tokens (prefill) 378 us in
+// bursts, 1490 TFLOP/s with the two terms counted once, 0.78 of the rate of a BF16 product (403 us
+// in a long loop, at the power limit); there the issue
 // slots are 62 % busy, the tensor pipe 58 %, and shared memory about three quarters (an MMA of
 // N = 128 reads its operands for as long as it computes, and tiles are written beside it). 64
-// rows over 8 to 32 thousand tokens 33.6 us, 25.4 of them at the HBM's rate; the rest is the
+// rows over 8 to 32 thousand tokens 34 us, 25.4 of them at the HBM's rate; the rest is the
 // launch, the shares, the queries' operand and the first tiles, one after another, which is all
 // of a small call's 8 us. One MMA warp for 128 columns: prefill 440 us.
 #include <cuda_bf16.h>
