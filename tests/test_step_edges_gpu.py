@@ -77,6 +77,7 @@ def test_first_call_of_a_process_is_captured(api, which):
 def test_threads(api):
     """Four host threads, a stream each, the same inputs: every result is the one alone."""
     c, s = full.Case(3, 2, 40, [900, 1, 0, 2000, 64, 333]), scores.Case(2, 2, 64, [5000, 300, 20, 4000])
+    api.step_device_status()  # what other tests left
     want = c.run(api), s.run(api)
     torch.cuda.synchronize()
     bad = []
