@@ -466,7 +466,8 @@ __device__ void run_softmax(const Cta& c) {
     // What turns its dots into log2 scores. A broken query's is NaN, which would also reach the
     // -inf of hidden tokens: a pair that sees none (a padding row) takes 1 and stays at zero.
     auto pair_scale = [&](int32_t unit, int32_t len) {
-        return len > 0 ? p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hq] : 1.0f;
+        const float given = p.qscale[static_cast<int64_t>(unit) * kHeadsPerCta + hq];  // beside the length's load
+        return len > 0 ? given : 1.0f;
     };
 
     Segment next = c.start.first;
@@ -537,10 +538,10 @@ __device__ void run_softmax(const Cta& c) {
             float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
             hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1)) * qs;
             // A tile mostly leaves every pair's reference where it is, so P' is formed with it at
-            // once (but for a unit's first tile, which finds none); one barrier then tells whether any half of any pair's scores asks for a
-            // move (the maximum exceeds the reference by more than the margin, or lies far below
-            // it, or the account runs out). Only then the halves are compared, references move and
-            // P' is formed again.
+            // once (but for a unit's first tile, which finds none); one barrier then tells whether
+            // any half of any pair's scores asks for a move (the maximum exceeds the reference by
+            // more than the margin, or lies far below it, or the account runs out). Only then the
+            // halves are compared, references move and P' is formed again.
             const bool ask = hmax > m_ref + kRescaleMargin ||
                              (hmax < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && hmax != kNegInf);
             uint32_t hw[kScores / 4], lw[kScores / 4];
