@@ -63,7 +63,8 @@ typedef enum dsa_status {
 #define DSA_INDEX_DIM 128        /* width of an index key */
 #define DSA_MAX_INDEX_HEADS 128  /* dsa_pool_scores: num_heads */
 #define DSA_MAX_KPOOL 128        /* dsa_pool_scores: kpool */
-#define DSA_MAX_PLAN_SEQS 16384  /* dsa_plan_step: num_seqs */
+#define DSA_MAX_PLAN_SEQS 16384  /* dsa_plan_step and the page operators: num_seqs, num_forks */
+#define DSA_MAX_PAGE_POOLS 16    /* page operators: num_pools */
 
 /* Version of this ABI (incremented on any incompatible change). */
 int32_t dsa_abi_version(void);
@@ -453,6 +454,118 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
                             float k_scale, float v_scale, float sm_scale, void* out,
                             int32_t verify_rows, void* workspace, size_t workspace_bytes,
                             void* stream);
+
+/*
+ * Page operators: what becomes of a cache's pages between the steps that dsa_plan_step plans. A
+ * page has one number in every pool (the latent cache, the index cache, ...) and every layer of
+ * it. A request's references to pages are its block-table entries 0 .. ceil(len/block_size) - 1.
+ *  page_shares  int32 [num_pages]: the requests that share a page beyond the one that an unshared
+ *               page belongs to, 0 for pages that are free or that dsa_plan_step took, which
+ *               therefore has nothing to write there. It starts as zeros and only these calls
+ *               change it.
+ *  free list    free_pages int32 [num_pages], the first num_free of them page numbers, -1 behind:
+ *               the buffer that dsa_plan_step and dsa_fork_pages take pages from the front of.
+ *  info         int32 [4], written by the call; info[2] is DSA_OK or DSA_ERR_DEVICE_BOUNDS.
+ *  workspace    device memory, 256-byte aligned, at least dsa_pages_workspace_bytes(num_pages),
+ *               zero before its first use; calls leave what they need of it zero. Calls that may
+ *               overlap on the GPU need workspaces of their own (and requests, pages and lists of
+ *               their own).
+ * Tables are int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq >= 1; a length below 0 or past
+ * max_blocks_per_seq*block_size is cut to the range and sets info[2]. num_seqs 0..DSA_MAX_PLAN_SEQS;
+ * num_pages 1..2^30; max_blocks_per_seq*block_size and the entries of all tables / 128 below 2^31
+ * (DSA_ERR_UNSUPPORTED otherwise). Pointers to empty arrays may be null. None of the calls
+ * allocates; all can be captured. The source pages have no counterpart to them: their host
+ * assigns pages (decode_k.rs, decode_k).
+ */
+typedef struct dsa_page_pool {
+    void* base;                 /* page 0 of layer 0; 16-byte aligned */
+    int64_t page_stride_bytes;  /* from a page to the next; a multiple of 16 */
+    int64_t layer_stride_bytes; /* from a layer to the next; a multiple of 16 (read when layers > 1) */
+    int64_t page_bytes;         /* of a page in one layer; a multiple of 16, 16 .. either stride */
+    int32_t layers;             /* >= 1 */
+    int32_t reserved;           /* must be 0 */
+} dsa_page_pool;
+
+size_t dsa_pages_workspace_bytes(int32_t num_pages);
+
+/*
+ * dsa_copy_pages: page dst_pages[i] becomes a copy of page src_pages[i], in every pool and layer,
+ * i < count. A pair with a negative page is left out (padding), as is one with a page past
+ * num_pages, which dsa_step_device_status tells of as DSA_ERR_DEVICE_BOUNDS. Pairs run side by
+ * side: a page that two pairs write, or that one writes and another reads, comes out as a mix of
+ * both (no other page is touched).
+ *  pools  [num_pools], in host memory, read before the call returns; 1..DSA_MAX_PAGE_POOLS.
+ *  src_pages, dst_pages  int32 [count], count >= 0.
+ *  count times the 16 KB pieces of a page below 2^32 (DSA_ERR_UNSUPPORTED otherwise).
+ */
+int32_t dsa_copy_pages(const dsa_page_pool* pools, int32_t num_pools, const int32_t* src_pages,
+                       const int32_t* dst_pages, int32_t count, int32_t num_pages, void* stream);
+
+/*
+ * dsa_fork_pages: request children[f] goes on from the lens[parents[f]] tokens of request parents[f],
+ * f < num_forks (samples of one prompt, beams). The parent's full pages become the child's too and
+ * gain a share each; its last page, when partly filled, is copied in all pools to the next page of
+ * free_pages (in the order of f), which takes its place in the child's table. Other entries of the
+ * child's row stay as they are: release what it held first. Lengths are the caller's, as for
+ * dsa_plan_step.
+ *  parents, children  int32 [num_forks], num_forks 0..DSA_MAX_PLAN_SEQS; a negative number leaves
+ *               the fork out. A child that an earlier fork names too, or that is some fork's
+ *               parent, is not forked (info[2]), nor is a request past num_seqs.
+ *  free_pages   int32 [num_free]; a partly filled page that finds no page there leaves -1 in the
+ *               child's table, as does a page of the parent outside [0, num_pages) (info[2] in
+ *               both cases).
+ *  info         forks made, pages taken from the front of free_pages, status, 0.
+ *  num_forks times the 16 KB pieces of a page below 2^32.
+ */
+int32_t dsa_fork_pages(const dsa_page_pool* pools, int32_t num_pools, const int32_t* parents,
+                       const int32_t* children, int32_t num_forks, const int32_t* lens,
+                       int32_t num_seqs, int32_t block_size, int32_t* block_tables,
+                       int32_t max_blocks_per_seq, const int32_t* free_pages, int32_t num_free,
+                       int32_t* page_shares, int32_t num_pages, int32_t* info, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_release_pages: request s keeps keep_lens[s] of its lens[s] tokens (0: it ends; fewer: rejected
+ * drafts; lens[s] or more: all of them). Its references to pages ceil(keep/block_size) ..
+ * ceil(len/block_size) - 1 go, and their table entries become -1: one reference less on a shared
+ * page, and a page that loses its last is free. (A request that went back into a page that others
+ * still share may not write there: fork it to another row, which copies that page, and end it.)
+ * The free list, whose first *taken pages have been taken since, is brought up to date in place:
+ * the freed pages, in ascending order, fill its first *taken places and go on behind its end; where
+ * they do not fill them, the list's last pages follow in order. Places behind it become -1, so that a
+ * captured dsa_plan_step whose num_free is the buffer's size gives tokens no slot when the list is
+ * short.
+ *  keep_lens    int32 [num_seqs]; below 0 counts as 0 and sets info[2].
+ *  num_free     int32 [1], read and written.
+ *  taken        int32 [1] (dsa_plan_step's or dsa_fork_pages' info + 1), or null: none.
+ *  info         references given back, pages freed, status, pages in the list. The status is
+ *               also DSA_ERR_DEVICE_BOUNDS for an entry past num_pages (left out; a negative one, which
+ *               a plan leaves that found no page, is left out silently), for more references to a page
+ *               than it has (freed once), for a *num_free or *taken out of range (cut to it), for a
+ *               list past num_pages (cut).
+ */
+int32_t dsa_release_pages(int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* lens,
+                          const int32_t* keep_lens, int32_t num_seqs, int32_t block_size,
+                          int32_t* page_shares, int32_t num_pages, int32_t* free_pages,
+                          int32_t* num_free, const int32_t* taken, int32_t* info, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_compact_pages: the n pages that the requests' tables name (live pages) move to the pool's
+ * first n pages: the live pages from n on, in ascending order, are copied in all pools to the dead
+ * pages below n, in ascending order, and tables and shares follow. Pages that no table names end up
+ * free: shares 0, and the free list is n .. num_pages - 1. What lies in pages from n on afterwards
+ * is not to be used.
+ *  free_pages   int32 [num_pages]; num_free  int32 [1]; both written.
+ *  info         live pages, pages moved, status (an entry past num_pages sets it and stays; a negative
+ *               one stays), free pages.
+ *  num_pages times the 16 KB pieces of a page below 2^32.
+ */
+int32_t dsa_compact_pages(const dsa_page_pool* pools, int32_t num_pools, int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* lens, int32_t num_seqs,
+                          int32_t block_size, int32_t* page_shares, int32_t num_pages,
+                          int32_t* free_pages, int32_t* num_free, int32_t* info, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /*
  * dsa_set_wait_limit: the longest time in nanoseconds that one wait inside the kernels of

@@ -35,6 +35,13 @@ class DecodeOptions(ctypes.Structure):
                 ("ev_begin", ctypes.c_void_p), ("ev_end", ctypes.c_void_p)]
 
 
+class PagePool(ctypes.Structure):
+    """dsa_page_pool (include/dsa_mla.h)."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride_bytes", ctypes.c_int64), ("layer_stride_bytes", ctypes.c_int64),
+                ("page_bytes", ctypes.c_int64), ("layers", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+_POOLS = [ctypes.POINTER(PagePool), _I32]
 _DECODE_ARGS = [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P]
 SIGNATURES = {
     "dsa_abi_version": ([], _I32),
@@ -57,6 +64,11 @@ SIGNATURES = {
     "dsa_mla_decode_full_workspace_bytes": ([_I32, _I32, _I32], _SZ),
     "dsa_mla_decode_full": ([_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P, _I32, _P,
                              _SZ, _P], _I32),
+    "dsa_pages_workspace_bytes": ([_I32], _SZ),
+    "dsa_copy_pages": (_POOLS + [_P, _P, _I32, _I32, _P], _I32),
+    "dsa_fork_pages": (_POOLS + [_P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _I32, _P, _P, _SZ, _P], _I32),
+    "dsa_release_pages": ([_P, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P], _I32),
+    "dsa_compact_pages": (_POOLS + [_P, _I32, _P, _I32, _I32, _P, _I32, _P, _P, _P, _P, _SZ, _P], _I32),
     "dsa_set_wait_limit": ([_U64], _I32),
     "dsa_absorb_q": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),
     "dsa_absorb_o": ([_P, _P, _I32, _I32, _I32, _I32, _I32, _P, _I32, _P], _I32),

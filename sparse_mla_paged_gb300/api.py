@@ -17,6 +17,7 @@ from ._lib import DsaError, check  # noqa: F401
 
 LATENT = 512
 INDEX = 128
+MAX_PAGE_POOLS = 16
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -477,6 +478,153 @@ def decode_full(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
             seq_lens.data_ptr(), num_seqs, rows_per_seq, num_q_heads, block_size, cache_stride_bytes, k_scale, v_scale,
             sm_scale, out.data_ptr(), verify_rows, workspace.data_ptr(), workspace.numel(), at.raw), "dsa_mla_decode_full")
     return out
+
+
+def pages_workspace_bytes(num_pages: int) -> int:
+    _fit(num_pages)
+    return int(_lib.load().dsa_pages_workspace_bytes(int(num_pages)))
+
+
+def alloc_pages_workspace(num_pages: int, device=None) -> torch.Tensor:
+    """A workspace for fork_pages, release_pages and compact_pages, to be kept from call to call (one
+    per stream or captured graph)."""
+    n = pages_workspace_bytes(num_pages)
+    if n == 0:
+        raise DsaError(2, "dsa_pages_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _pools(pools, index):
+    """dsa_page_pool array of cache tensors uint8 [num_pages, page bytes] or [layers, num_pages, page
+    bytes], any strides but a page's own bytes together; and their number of pages."""
+    if isinstance(pools, torch.Tensor) or len(pools) == 0:
+        raise ValueError("pools must be a sequence of cache tensors")
+    if len(pools) > MAX_PAGE_POOLS:
+        raise DsaError(2, f"more than {MAX_PAGE_POOLS} pools")
+    out = (_lib.PagePool * len(pools))()
+    num_pages = pools[0].shape[-2] if pools[0].dim() > 1 else 0
+    for p, t in zip(out, pools):
+        if t.get_device() != index or t.dtype != torch.uint8 or t.dim() not in (2, 3) or t.shape[-2] != num_pages or t.stride(-1) != 1:
+            raise ValueError(f"a pool must be torch.uint8 [num_pages, bytes] or [layers, num_pages, bytes] on cuda:{index}, "
+                             "the bytes of a page together and num_pages the same in all")
+        p.base, p.page_stride_bytes, p.page_bytes = t.data_ptr(), t.stride(-2), t.shape[-1]
+        p.layers = t.shape[0] if t.dim() == 3 else 1
+        p.layer_stride_bytes = t.stride(0) if t.dim() == 3 else 0
+    return out, num_pages
+
+
+def _requests(block_tables, lens, index):
+    _need_on(block_tables, torch.int32, "block_tables", index)
+    _need_on(lens, torch.int32, "lens", index)
+    if block_tables.dim() != 2 or block_tables.shape[0] != lens.numel():
+        raise ValueError("block_tables [num_seqs, max_blocks_per_seq], lens [num_seqs]")
+
+
+def _books(at, num_pages, info, workspace, device):
+    """The info words and the workspace of a page operator's call, made where not given."""
+    if info is None or workspace is None:
+        with at.allocating():
+            info = torch.empty(4, dtype=torch.int32, device=device) if info is None else info
+            workspace = alloc_pages_workspace(num_pages, device) if workspace is None else workspace
+    _need_on(info, torch.int32, "info", at.index)
+    _need_on(workspace, torch.uint8, "workspace", at.index)
+    if info.numel() < 4:
+        raise ValueError("info [4]")
+    return info, workspace
+
+
+def _counted(page_shares, free_pages, num_free, num_pages, index):
+    for t, n in ((page_shares, "page_shares"), (free_pages, "free_pages"), (num_free, "num_free")):
+        _need_on(t, torch.int32, n, index)
+    if page_shares.numel() != num_pages or free_pages.numel() != num_pages or num_free.numel() != 1:
+        raise ValueError("page_shares [num_pages], free_pages [num_pages], num_free [1]")
+
+
+def copy_pages(pools, src_pages: torch.Tensor, dst_pages: torch.Tensor, stream=None) -> None:
+    """dsa_copy_pages: page dst_pages[i] of every pool and layer becomes a copy of page src_pages[i];
+    pairs with a negative page are left out. pools: cache tensors uint8 [num_pages, page bytes] or
+    [layers, num_pages, page bytes]. step_device_status tells of pages past the pools."""
+    i = _device_of(src_pages, "src_pages")
+    _need_on(src_pages, torch.int32, "src_pages", i)
+    _need_on(dst_pages, torch.int32, "dst_pages", i)
+    if src_pages.numel() != dst_pages.numel():
+        raise ValueError("src_pages [count], dst_pages [count]")
+    table, num_pages = _pools(pools, i)
+    _fit(src_pages.numel(), num_pages)
+    with _Launch(i, stream) as at:
+        check(_lib.load().dsa_copy_pages(table, len(pools), src_pages.data_ptr(), dst_pages.data_ptr(), src_pages.numel(),
+                                         num_pages, at.raw), "dsa_copy_pages")
+
+
+def fork_pages(pools, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor, block_size: int,
+               block_tables: torch.Tensor, free_pages: torch.Tensor, page_shares: torch.Tensor, info=None, workspace=None,
+               stream=None) -> torch.Tensor:
+    """dsa_fork_pages: request children[f] goes on from request parents[f]'s lens tokens: full pages are
+    shared (page_shares, block_tables, in place), a partly filled last page is copied to the next of
+    free_pages. Returns info, int32 [4]: forks made, pages taken off free_pages, status, 0."""
+    i = _device_of(parents, "parents")
+    for t, n in ((parents, "parents"), (children, "children"), (free_pages, "free_pages"), (page_shares, "page_shares")):
+        _need_on(t, torch.int32, n, i)
+    _requests(block_tables, lens, i)
+    table, num_pages = _pools(pools, i)
+    if parents.numel() != children.numel() or page_shares.numel() != num_pages:
+        raise ValueError("parents [num_forks], children [num_forks], page_shares [num_pages]")
+    _fit(parents.numel(), lens.numel(), block_size, block_tables.shape[1], free_pages.numel(), num_pages)
+    with _Launch(i, stream) as at:
+        info, workspace = _books(at, num_pages, info, workspace, parents.device)
+        check(_lib.load().dsa_fork_pages(table, len(pools), parents.data_ptr(), children.data_ptr(), parents.numel(),
+                                         lens.data_ptr(), lens.numel(), block_size, block_tables.data_ptr(),
+                                         block_tables.shape[1], free_pages.data_ptr(), free_pages.numel(),
+                                         page_shares.data_ptr(), num_pages, info.data_ptr(), workspace.data_ptr(),
+                                         workspace.numel(), at.raw), "dsa_fork_pages")
+    return info
+
+
+def release_pages(block_tables: torch.Tensor, lens: torch.Tensor, keep_lens: torch.Tensor, block_size: int,
+                  page_shares: torch.Tensor, free_pages: torch.Tensor, num_free: torch.Tensor, taken=None, info=None,
+                  workspace=None, stream=None) -> torch.Tensor:
+    """dsa_release_pages: request s gives back its pages behind keep_lens[s] tokens (block_tables,
+    page_shares); the pages that nobody holds any more take the place of the `taken` ones (int32 [1], such
+    as plan.info[1:2]) in the free list free_pages [num_pages], num_free [1]. All in place. Returns info,
+    int32 [4]: references given back, pages freed, status, pages in the list."""
+    i = _device_of(block_tables, "block_tables")
+    _requests(block_tables, lens, i)
+    _need_on(keep_lens, torch.int32, "keep_lens", i)
+    num_pages = page_shares.numel()
+    _counted(page_shares, free_pages, num_free, num_pages, i)
+    if keep_lens.numel() != lens.numel():
+        raise ValueError("lens [num_seqs], keep_lens [num_seqs]")
+    if taken is not None:
+        _need_on(taken, torch.int32, "taken", i)
+        if taken.numel() != 1:
+            raise ValueError("taken [1]")
+    _fit(lens.numel(), block_size, block_tables.shape[1], num_pages)
+    with _Launch(i, stream) as at:
+        info, workspace = _books(at, num_pages, info, workspace, lens.device)
+        check(_lib.load().dsa_release_pages(block_tables.data_ptr(), block_tables.shape[1], lens.data_ptr(), keep_lens.data_ptr(),
+                                            lens.numel(), block_size, page_shares.data_ptr(), num_pages, free_pages.data_ptr(),
+                                            num_free.data_ptr(), _ptr(taken), info.data_ptr(), workspace.data_ptr(),
+                                            workspace.numel(), at.raw), "dsa_release_pages")
+    return info
+
+
+def compact_pages(pools, block_tables: torch.Tensor, lens: torch.Tensor, block_size: int, page_shares: torch.Tensor,
+                  free_pages: torch.Tensor, num_free: torch.Tensor, info=None, workspace=None, stream=None) -> torch.Tensor:
+    """dsa_compact_pages: the n pages that the requests' tables name move to the pools' first n pages;
+    tables, shares and the free list follow. All in place. Returns info, int32 [4]: live pages, pages
+    moved, status, free pages."""
+    i = _device_of(block_tables, "block_tables")
+    _requests(block_tables, lens, i)
+    table, num_pages = _pools(pools, i)
+    _counted(page_shares, free_pages, num_free, num_pages, i)
+    _fit(lens.numel(), block_size, block_tables.shape[1], num_pages)
+    with _Launch(i, stream) as at:
+        info, workspace = _books(at, num_pages, info, workspace, lens.device)
+        check(_lib.load().dsa_compact_pages(table, len(pools), block_tables.data_ptr(), block_tables.shape[1], lens.data_ptr(),
+                                            lens.numel(), block_size, page_shares.data_ptr(), num_pages, free_pages.data_ptr(),
+                                            num_free.data_ptr(), info.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                            at.raw), "dsa_compact_pages")
+    return info
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:

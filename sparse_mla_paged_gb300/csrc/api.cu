@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "full.cuh"
+#include "pages.cuh"
 
 using namespace dsa;
 
@@ -115,6 +116,7 @@ int32_t current_device(DeviceState** out) {
             if (d.status == DSA_OK) d.status = from_cuda(pool_scores_kernel_setup());
             if (d.status == DSA_OK) d.status = from_cuda(full_setup());
             if (d.status == DSA_OK) d.status = from_cuda(full_plan_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(pages_setup());
         }
         d.checked = true;
     }
@@ -441,6 +443,15 @@ Args make_args(const void* q, const void* k_cache, const void* v_cache, const in
 int32_t dsa::check_device() {
     DeviceState* d = nullptr;
     return current_device(&d);
+}
+
+int32_t dsa::device_info(int* sms, int** step_status) {
+    DeviceState* d = nullptr;
+    const int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    *sms = d->sms;
+    *step_status = d->step_status;
+    return DSA_OK;
 }
 
 extern "C" {

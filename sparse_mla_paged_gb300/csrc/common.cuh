@@ -305,6 +305,8 @@ cudaError_t launch_decode_128(const DecodeParams& p, const CUtensorMap& kmap, co
 cudaError_t launch_combine(const CombineParams& p, int units, int max_pieces, cudaStream_t stream);
 cudaError_t launch_latent_write(const LatentWriteParams& p, cudaStream_t stream);
 int32_t check_device();  // DSA_OK when the current device is an sm_103 with the kernels loaded
+// As check_device, with the device's SMs and the address of its step status word.
+int32_t device_info(int* sms, int** step_status);
 cudaError_t select_kernel_setup();
 cudaError_t plan_kernel_setup();
 cudaError_t launch_plan(const PlanParams& p, int sms, cudaStream_t stream);

@@ -1,0 +1,501 @@
+// Pages of a paged cache: copied, forked (shared by a further request), released to the free list
+// and compacted to the pool's front. Whatever runs side by side here is sums, minima and bits of
+// whole numbers, so results do not depend on an order: pages are listed by their number.
+//
+// The books (tables, shares, free list) are bound by latency: a launch each for what every block
+// has to know of the others'. Page data is bound by HBM.
+#include "pages.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace pages {
+namespace {
+
+constexpr int kMarkThreads = 256;
+constexpr int kListThreads = 1024;
+constexpr int kListWarps = kListThreads / 32;
+constexpr int kForkThreads = 1024;
+
+__device__ __forceinline__ void report(int* status) { atomicCAS(status, 0, DSA_ERR_DEVICE_BOUNDS); }
+__device__ __forceinline__ void wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Length of request s, cut to what its table holds.
+__device__ __forceinline__ int32_t clamped(const Tables& t, int32_t n, bool* bad) {
+    const int64_t room = static_cast<int64_t>(t.max_blocks) * t.block_size;
+    *bad |= n < 0 || n > room;
+    if (n > room) n = static_cast<int32_t>(room);
+    return n < 0 ? 0 : n;
+}
+__device__ __forceinline__ int32_t pages_of(const Tables& t, int32_t n) {
+    return static_cast<int32_t>(divide(static_cast<uint32_t>(n) + static_cast<uint32_t>(t.block_size) - 1u, t.by_block));
+}
+
+// One chunk of one page: item of pair (src, dst).
+__device__ __forceinline__ void copy_chunk(const Pools& pools, uint32_t rest, int32_t src, int32_t dst) {
+    int j = 0;
+    while (j + 1 < pools.count && rest >= pools.pool[j + 1].first) ++j;
+    const Pool& pool = pools.pool[j];
+    rest -= pool.first;
+    const uint32_t layer = divide(rest, pool.by_chunks), chunk = rest - layer * pool.by_chunks.d;
+    const int64_t at = static_cast<int64_t>(layer) * pool.layer_stride + static_cast<int64_t>(chunk) * kChunkVecs * 16;
+    const uint4* s = reinterpret_cast<const uint4*>(pool.base + src * pool.page_stride + at);
+    uint4* d = reinterpret_cast<uint4*>(pool.base + dst * pool.page_stride + at);
+    const uint32_t n = min(kChunkVecs, pool.vecs - chunk * kChunkVecs);
+    uint4 v[kCopyVecs];
+#pragma unroll
+    for (int i = 0; i < kCopyVecs; ++i)
+        if (threadIdx.x + i * kCopyThreads < n) v[i] = __ldcs(s + threadIdx.x + i * kCopyThreads);
+#pragma unroll
+    for (int i = 0; i < kCopyVecs; ++i)
+        if (threadIdx.x + i * kCopyThreads < n) __stcs(d + threadIdx.x + i * kCopyThreads, v[i]);
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+    const uint32_t items = static_cast<uint32_t>(p.count) * p.pools.items;
+    for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const uint32_t pair = divide(static_cast<uint32_t>(it), p.pools.by_items);
+        const int32_t src = p.src[pair], dst = p.dst[pair];
+        if (src < 0 || dst < 0) continue;
+        if (src >= p.num_pages || dst >= p.num_pages) {
+            if (threadIdx.x == 0) report(p.status);
+            continue;
+        }
+        if (src != dst) copy_chunk(p.pools, static_cast<uint32_t>(it) - pair * p.pools.items, src, dst);
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// fork
+// ------------------------------------------------------------------------------------
+// Sum of v over the block's threads before this one; *total over all. Ends with the sums read.
+template <int kWarps>
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int32_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int32_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const int32_t x = sums[w];
+        if (w < warp) before += x;
+        all += x;
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - v;
+}
+
+// One block: which forks are made (its child is named by no earlier fork and is nobody's parent),
+// how many pages each shares and which fresh page takes its last, partly filled one.
+__global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_constant__ ForkParams p) {
+    extern __shared__ int32_t first_child[];  // [num_seqs] first fork that names the child
+    __shared__ int32_t sums[kForkThreads / 32];
+    uint32_t* parent_bits = reinterpret_cast<uint32_t*>(first_child + p.t.num_seqs);
+    let_next();
+    const int tid = threadIdx.x;
+    const int32_t n = p.t.num_seqs;
+    for (int32_t i = tid; i < n; i += kForkThreads) first_child[i] = INT32_MAX;
+    for (int32_t i = tid; i < (n + 31) / 32; i += kForkThreads) parent_bits[i] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int32_t f = tid; f < p.forks; f += kForkThreads) {
+        const int32_t a = p.parents[f], c = p.children[f];
+        if (a < 0 || c < 0) continue;
+        if (a >= n || c >= n) {
+            bad = true;
+            continue;
+        }
+        atomicMin(first_child + c, f);
+        atomicOr(parent_bits + (a >> 5), 1u << (a & 31));
+    }
+    __syncthreads();
+    int32_t taken = 0, made_here = 0;
+    for (int32_t f0 = 0; f0 < p.forks; f0 += kForkThreads) {
+        const int32_t f = f0 + tid;
+        int32_t src = -1, whole = -1;
+        if (f < p.forks) {
+            const int32_t a = p.parents[f], c = p.children[f];
+            if (a >= 0 && c >= 0 && a < n && c < n) {
+                if (first_child[c] != f || (parent_bits[c >> 5] >> (c & 31) & 1u)) {
+                    bad = true;
+                } else {
+                    const int32_t len = clamped(p.t, p.t.lens[a], &bad);
+                    whole = static_cast<int32_t>(divide(static_cast<uint32_t>(len), p.t.by_block));
+                    ++made_here;
+                    if (len > whole * p.t.block_size) {
+                        src = p.t.entries[static_cast<int64_t>(a) * p.t.max_blocks + whole];
+                        int32_t* mine = p.t.entries + static_cast<int64_t>(c) * p.t.max_blocks + whole;
+                        if (src < 0 || src >= p.t.num_pages) {
+                            *mine = src = -1;
+                            bad = true;
+                        }
+                    }
+                }
+            }
+        }
+        int32_t total;
+        const int32_t at = taken + block_scan<kForkThreads / 32>(src >= 0 ? 1 : 0, sums, &total);
+        taken += total;
+        if (f < p.forks) {
+            int32_t dst = -1;
+            if (src >= 0) {
+                if (at < p.num_free) dst = p.free_pages[at];
+                if (dst < 0 || dst >= p.t.num_pages) {
+                    dst = -1;
+                    bad = true;
+                }
+                p.t.entries[static_cast<int64_t>(p.children[f]) * p.t.max_blocks + whole] = dst;
+            }
+            p.src[f] = src;
+            p.dst[f] = dst;
+            p.whole[f] = whole;
+        }
+    }
+    int32_t made;
+    block_scan<kForkThreads / 32>(made_here, sums, &made);
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        p.info[0] = made;
+        p.info[1] = min(taken, p.num_free);
+        p.info[2] = bad ? DSA_ERR_DEVICE_BOUNDS : DSA_OK;
+        p.info[3] = 0;
+    }
+}
+
+// Table entries of the forks' whole pages (a chunk of a row per turn), then the copied pages.
+__global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ ForkParams p) {
+    wait_prior();
+    constexpr int kRow = kCopyThreads;  // entries of a turn
+    const int32_t row_turns = (p.t.max_blocks + kRow - 1) / kRow;
+    const int64_t turns = static_cast<int64_t>(p.forks) * row_turns;
+    const uint32_t items = static_cast<uint32_t>(p.forks) * p.pools.items;
+    for (int64_t it = blockIdx.x; it < turns + items; it += gridDim.x) {
+        if (it < turns) {
+            const int32_t f = static_cast<int32_t>(it / row_turns);
+            const int32_t col = static_cast<int32_t>(it - static_cast<int64_t>(f) * row_turns) * kRow + threadIdx.x;
+            if (col >= p.whole[f]) continue;
+            const int32_t page = p.t.entries[static_cast<int64_t>(p.parents[f]) * p.t.max_blocks + col];
+            const bool good = page >= 0 && page < p.t.num_pages;
+            p.t.entries[static_cast<int64_t>(p.children[f]) * p.t.max_blocks + col] = good ? page : -1;
+            if (good) atomicAdd(p.shares + page, 1);
+            else report(p.info + 2);
+            continue;
+        }
+        const uint32_t at = static_cast<uint32_t>(it - turns), f = divide(at, p.pools.by_items);
+        const int32_t src = p.src[f], dst = p.dst[f];
+        if (src >= 0 && dst >= 0 && src != dst) copy_chunk(p.pools, at - f * p.pools.items, src, dst);
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// release, compact: marks
+// ------------------------------------------------------------------------------------
+// A warp per chunk of a request's table.
+template <class F>
+__device__ __forceinline__ void for_entries(const Tables& t, F&& each) {
+    const int lane = threadIdx.x & 31;
+    const int64_t turn = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    if (turn >= static_cast<int64_t>(t.num_seqs) * t.chunks) return;
+    const int32_t s = static_cast<int32_t>(divide(static_cast<uint32_t>(turn), t.by_chunks));
+    each(s, static_cast<int32_t>(turn - static_cast<int64_t>(s) * t.chunks) * kEntries, lane);
+}
+
+// Every reference that goes lowers its page's shares; the one that finds none left marks the page.
+__global__ void __launch_bounds__(kMarkThreads) release_mark_kernel(const __grid_constant__ ReleaseParams p) {
+    let_next();
+    for_entries(p.t, [&](int32_t s, int32_t col0, int lane) {
+        bool bad = false;
+        const int32_t len = clamped(p.t, p.t.lens[s], &bad);
+        int32_t keep = p.keep_lens[s];
+        bad |= keep < 0;
+        keep = min(max(keep, 0), len);
+        const int32_t lo = pages_of(p.t, keep), hi = pages_of(p.t, len);
+        int32_t* row = p.t.entries + static_cast<int64_t>(s) * p.t.max_blocks;
+        int32_t refs = 0;
+        if (col0 < hi && col0 + kEntries > lo) {
+            int32_t page[kEntries / 32], before[kEntries / 32];
+#pragma unroll
+            for (int i = 0; i < kEntries / 32; ++i) {
+                const int32_t col = col0 + 32 * i + lane;
+                page[i] = col >= lo && col < hi ? row[col] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < kEntries / 32; ++i) {
+                const int32_t col = col0 + 32 * i + lane;
+                if (col >= lo && col < hi) row[col] = -1;
+                before[i] = 1;
+                if (page[i] >= p.t.num_pages) {
+                    bad = true;
+                } else if (page[i] >= 0) {
+                    ++refs;
+                    before[i] = atomicSub(p.shares + page[i], 1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kEntries / 32; ++i) {
+                if (before[i] == 0) atomicOr(p.marks + (page[i] >> 5), 1u << (page[i] & 31));
+                bad |= before[i] < 0;
+            }
+            refs = __reduce_add_sync(0xffffffffu, refs);
+            if (lane == 0 && refs > 0) atomicAdd(&p.head->refs, refs);
+        }
+        if (bad) report(&p.head->status);
+    });
+}
+
+__global__ void __launch_bounds__(kMarkThreads) compact_mark_kernel(const __grid_constant__ CompactParams p) {
+    let_next();
+    for_entries(p.t, [&](int32_t s, int32_t col0, int lane) {
+        bool bad = false;
+        const int32_t hi = pages_of(p.t, clamped(p.t, p.t.lens[s], &bad));
+        const int32_t* row = p.t.entries + static_cast<int64_t>(s) * p.t.max_blocks;
+#pragma unroll
+        for (int i = 0; i < kEntries / 32; ++i) {
+            const int32_t col = col0 + 32 * i + lane;
+            const int32_t page = col < hi ? row[col] : -1;
+            if (page >= p.t.num_pages) bad = true;
+            else if (page >= 0) atomicOr(p.marks + (page >> 5), 1u << (page & 31));
+        }
+        if (bad) report(&p.head->status);
+    });
+}
+
+// ------------------------------------------------------------------------------------
+// release, compact: pages in order
+// ------------------------------------------------------------------------------------
+// The marks of all pages are counted by every block (a bit per page: 32 KB for 262144 pages),
+// which takes less time than a launch between counting and listing; a block then lists the pages
+// of its own words, a warp 32 words at a time.
+
+// Marked pages below page `limit` in words [0, w1).
+__device__ __forceinline__ int32_t marked(const uint32_t* marks, int32_t w1, int32_t limit) {
+    int32_t n = 0;
+    for (int32_t w = 4 * threadIdx.x; w < w1; w += 4 * kListThreads) {
+        const uint4 v = *reinterpret_cast<const uint4*>(marks + w);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int32_t left = limit - (w + i) * 32;
+            if (w + i < w1 && left > 0) n += __popc(left >= 32 ? x[i] : x[i] & ((1u << left) - 1u));
+        }
+    }
+    return n;
+}
+
+// each(page, is it marked, marked pages before it) for the pages of this block's words, a page
+// a lane; `before` marked pages precede the block's.
+template <class F>
+__device__ __forceinline__ void for_pages(const uint32_t* marks, int32_t w0, int32_t w1, int32_t num_pages, int32_t before, int32_t* sums,
+                                          F&& each) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int32_t base = w0; base < w1; base += kListThreads) {
+        const int32_t w = base + threadIdx.x;
+        const uint32_t mine = w < w1 ? marks[w] : 0u;
+        int32_t total;
+        const int32_t at = before + block_scan<kListWarps>(__popc(mine), sums, &total);
+        before += total;
+        const int32_t words = min(32, w1 - base - 32 * warp);
+        for (int j = 0; j < words; ++j) {
+            const uint32_t bits = __shfl_sync(0xffffffffu, mine, j);
+            const int32_t first = __shfl_sync(0xffffffffu, at, j);
+            const int32_t page = (base + 32 * warp + j) * 32 + lane;
+            if (page < num_pages) each(page, (bits >> lane & 1u) != 0u, first + __popc(bits & ((1u << lane) - 1u)));
+        }
+    }
+}
+
+__device__ __forceinline__ void block_words(int32_t words, int32_t* w0, int32_t* w1) {
+    const int32_t per = (words / 4 + gridDim.x - 1) / gridDim.x * 4;
+    *w0 = min(words, static_cast<int32_t>(blockIdx.x) * per);
+    *w1 = min(words, *w0 + per);
+}
+
+// Whether this block is the last one to come here.
+__device__ __forceinline__ bool last_block(int32_t* ticket) {
+    __shared__ bool last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(ticket, 1) == static_cast<int32_t>(gridDim.x) - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    return last;
+}
+
+__global__ void __launch_bounds__(kListThreads) release_list_kernel(const __grid_constant__ ReleaseParams p) {
+    __shared__ int32_t sums[kListWarps];
+    wait_prior();
+    const int32_t words = static_cast<int32_t>((static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4);
+    int32_t w0, w1, freed, before;
+    block_words(words, &w0, &w1);
+    block_scan<kListWarps>(marked(p.marks, words, INT32_MAX), sums, &freed);
+    block_scan<kListWarps>(marked(p.marks, w0, INT32_MAX), sums, &before);
+    const int32_t had = *p.num_free, count = min(max(had, 0), p.t.num_pages);
+    const int32_t want = p.taken ? *p.taken : 0, taken = min(max(want, 0), count);
+    bool bad = had != count || want != taken;
+    const int64_t after = static_cast<int64_t>(count) - taken + freed;
+    const int32_t now = static_cast<int32_t>(min(after, static_cast<int64_t>(p.t.num_pages)));
+    bad |= now != after;
+    for_pages(p.marks, w0, w1, p.t.num_pages, before, sums, [&](int32_t page, bool mine, int32_t k) {
+        if (!mine) return;
+        p.shares[page] = 0;
+        const int64_t at = k < taken ? k : static_cast<int64_t>(count) - taken + k;
+        if (at < p.t.num_pages) p.free_pages[at] = page;
+    });
+    if (blockIdx.x == 0) {
+        const int32_t gap = max(0, taken - freed), moved = min(gap, count - taken);
+        for (int32_t i = threadIdx.x; i < moved; i += kListThreads) p.free_pages[freed + i] = p.free_pages[count - moved + i];
+        __syncthreads();
+        for (int32_t i = now + threadIdx.x; i < count; i += kListThreads) p.free_pages[i] = -1;
+    }
+    if (!last_block(&p.head->ticket)) return;
+    for (int32_t w = threadIdx.x; w < words / 4; w += kListThreads) reinterpret_cast<uint4*>(p.marks)[w] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) {
+        p.info[0] = p.head->refs;
+        p.info[1] = freed;
+        p.info[2] = bad || p.head->status != 0 ? DSA_ERR_DEVICE_BOUNDS : DSA_OK;
+        p.info[3] = now;
+        *p.num_free = now;
+        p.head->refs = p.head->status = p.head->ticket = 0;
+    }
+}
+
+// Pages from the number of live ones on that are live move, in order, to the dead ones below it.
+__global__ void __launch_bounds__(kListThreads) compact_list_kernel(const __grid_constant__ CompactParams p) {
+    __shared__ int32_t sums[kListWarps];
+    wait_prior();
+    let_next();
+    const int32_t words = static_cast<int32_t>((static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4);
+    int32_t w0, w1, live, before, low;
+    block_words(words, &w0, &w1);
+    block_scan<kListWarps>(marked(p.marks, words, INT32_MAX), sums, &live);
+    block_scan<kListWarps>(marked(p.marks, w0, INT32_MAX), sums, &before);
+    block_scan<kListWarps>(marked(p.marks, words, live), sums, &low);  // live pages that stay
+    for_pages(p.marks, w0, w1, p.t.num_pages, before, sums, [&](int32_t page, bool mine, int32_t k) {
+        if (page >= live) {
+            if (mine) {
+                p.rank[page] = k - low;
+                p.src[k - low] = page;
+            } else {
+                p.shares[page] = 0;
+            }
+        } else if (!mine) {
+            p.dst[page - k] = page;
+        }
+        p.free_pages[page] = page < p.t.num_pages - live ? page + live : -1;
+    });
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.head->live = live;
+        p.head->moved = live - low;
+        p.info[0] = live;
+        p.info[1] = live - low;
+        p.info[2] = p.head->status;
+        p.info[3] = p.t.num_pages - live;
+        *p.num_free = p.t.num_pages - live;
+    }
+}
+
+// Shares, table entries and data of the pages that move; the marks are cleared for the next call.
+__global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_constant__ CompactParams p) {
+    wait_prior();
+    const int32_t live = p.head->live, moved = p.head->moved;
+    const int64_t tid = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, threads = static_cast<int64_t>(gridDim.x) * kCopyThreads;
+    const int64_t words = (static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4;
+    for (int64_t w = tid; w < words; w += threads) p.marks[w] = 0;
+    for (int64_t k = tid; k < moved; k += threads) {
+        p.shares[p.dst[k]] = p.shares[p.src[k]];
+        p.shares[p.src[k]] = 0;
+    }
+    if (moved > 0) {
+        const int64_t turns = static_cast<int64_t>(p.t.num_seqs) * p.t.chunks;
+        const int lane = threadIdx.x & 31;
+        for (int64_t turn = tid >> 5; turn < turns; turn += threads >> 5) {
+            const int32_t s = static_cast<int32_t>(divide(static_cast<uint32_t>(turn), p.t.by_chunks));
+            const int32_t col0 = static_cast<int32_t>(turn - static_cast<int64_t>(s) * p.t.chunks) * kEntries;
+            bool bad = false;
+            const int32_t hi = pages_of(p.t, clamped(p.t, p.t.lens[s], &bad));
+            int32_t* row = p.t.entries + static_cast<int64_t>(s) * p.t.max_blocks;
+#pragma unroll
+            for (int i = 0; i < kEntries / 32; ++i) {
+                const int32_t col = col0 + 32 * i + lane;
+                const int32_t page = col < hi ? row[col] : -1;
+                if (page >= live && page < p.t.num_pages) row[col] = p.dst[p.rank[page]];
+            }
+        }
+        const uint64_t items = static_cast<uint64_t>(moved) * p.pools.items;
+        for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+            const uint32_t k = divide(static_cast<uint32_t>(it), p.pools.by_items);
+            copy_chunk(p.pools, static_cast<uint32_t>(it) - k * p.pools.items, p.src[k], p.dst[k]);
+        }
+    }
+    if (last_block(&p.head->ticket) && threadIdx.x == 0) p.head->status = p.head->ticket = 0;
+}
+
+template <class P>
+cudaError_t launch_after(void (*kernel)(P), int blocks, int threads, const P& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+int at_most(int64_t want, int most) { return static_cast<int>(want < 1 ? 1 : (want < most ? want : most)); }
+int mark_blocks(const Tables& t) {
+    return at_most((static_cast<int64_t>(t.num_seqs) * t.chunks + kMarkThreads / 32 - 1) / (kMarkThreads / 32), INT32_MAX);
+}
+int list_blocks(const Tables& t, int sms) { return at_most((mark_words(t.num_pages) + kListThreads - 1) / kListThreads, sms); }
+
+}  // namespace
+}  // namespace pages
+
+cudaError_t pages_setup() {
+    return cudaFuncSetAttribute(pages::fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                DSA_MAX_PLAN_SEQS * 4 + DSA_MAX_PLAN_SEQS / 8);
+}
+
+cudaError_t launch_copy_pages(const pages::CopyParams& p, int sms, cudaStream_t stream) {
+    const int blocks = pages::at_most(static_cast<int64_t>(p.count) * p.pools.items, 8 * sms);
+    pages::copy_kernel<<<blocks, pages::kCopyThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fork_pages(const pages::ForkParams& p, int sms, cudaStream_t stream) {
+    const int smem = p.t.num_seqs * 4 + (p.t.num_seqs + 31) / 32 * 4;
+    pages::fork_plan_kernel<<<1, pages::kForkThreads, smem, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int64_t turns = (p.t.max_blocks + pages::kCopyThreads - 1) / pages::kCopyThreads;
+    return pages::launch_after(pages::fork_kernel, pages::at_most(p.forks * (turns + p.pools.items), 8 * sms), pages::kCopyThreads, p, stream);
+}
+
+cudaError_t launch_release_pages(const pages::ReleaseParams& p, int sms, cudaStream_t stream) {
+    pages::release_mark_kernel<<<pages::mark_blocks(p.t), pages::kMarkThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return pages::launch_after(pages::release_list_kernel, pages::list_blocks(p.t, sms), pages::kListThreads, p, stream);
+}
+
+cudaError_t launch_compact_pages(const pages::CompactParams& p, int sms, cudaStream_t stream) {
+    pages::compact_mark_kernel<<<pages::mark_blocks(p.t), pages::kMarkThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = pages::launch_after(pages::compact_list_kernel, pages::list_blocks(p.t, sms), pages::kListThreads, p, stream);
+    if (e != cudaSuccess) return e;
+    return pages::launch_after(pages::compact_kernel, 8 * sms, pages::kCopyThreads, p, stream);
+}
+
+}  // namespace dsa
