@@ -456,6 +456,38 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
                             void* stream);
 
 /*
+ * dsa_mla_prefill: the attention of chunks of new tokens over their requests' paged caches, for
+ * prompts (whole or in parts) and for steps that mix them with decoding requests. Rows are packed
+ * as dsa_plan_step packs them with rows_per_seq = 0: the new_lens[0] new tokens of request 0, then
+ * those of request 1, ... Row t, the i-th new token of request s, sees what the cache held before
+ * and the new tokens up to itself, which the cache writer has stored already (decode_k.rs, decode_k:
+ * each row's visible length is its own position plus one):
+ *   out[t,h,:] = sum_{j < n} softmax_j(sm_scale * q[t,h,:].(k_scale*K_j)) (v_scale*V_j),
+ *                n = base_lens[s] + i + 1.
+ * Rows behind the last request's tokens are left as they were. Arguments as for
+ * dsa_mla_decode_full, except:
+ *  q, out       bf16 [max_rows, num_q_heads, 512].
+ *  base_lens, new_lens  int32 [num_seqs], any lengths from 0 on, as dsa_plan_step takes them.
+ *               One below 0 counts as 0, and new tokens past max_rows are left out, both a
+ *               device-side DSA_ERR_DEVICE_BOUNDS, as for dsa_plan_step; a row that would see past
+ *               max_blocks_per_seq*block_size and a negative block-table entry are taken as
+ *               dsa_mla_decode_full takes them.
+ *  A NaN code reaches the rows that see its position, no others.
+ *  workspace    device memory, 256-byte aligned, at least dsa_mla_prefill_workspace_bytes of the
+ *               same num_seqs, max_rows and num_q_heads; status, capture and overlapping calls as
+ *               for dsa_mla_decode_full.
+ *  num_seqs 1..DSA_MAX_PLAN_SEQS, max_rows >= 1, max_rows*num_q_heads at most 2^25
+ *  (DSA_ERR_UNSUPPORTED above).
+ */
+size_t dsa_mla_prefill_workspace_bytes(int32_t num_seqs, int32_t max_rows, int32_t num_q_heads);
+int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                        const int32_t* base_lens, const int32_t* new_lens, int32_t num_seqs,
+                        int32_t max_rows, int32_t num_q_heads, int32_t block_size,
+                        int64_t cache_stride_bytes, float k_scale, float v_scale, float sm_scale,
+                        void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Page operators: what becomes of a cache's pages between the steps that dsa_plan_step plans. A
  * page has one number in every pool (the latent cache, the index cache, ...) and every layer of
  * it. A request's references to pages are its block-table entries 0 .. ceil(len/block_size) - 1.

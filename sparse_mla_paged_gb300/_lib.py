@@ -64,6 +64,8 @@ SIGNATURES = {
     "dsa_mla_decode_full_workspace_bytes": ([_I32, _I32, _I32], _SZ),
     "dsa_mla_decode_full": ([_P, _P, _P, _P, _I32, _P, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P, _I32, _P,
                              _SZ, _P], _I32),
+    "dsa_mla_prefill_workspace_bytes": ([_I32, _I32, _I32], _SZ),
+    "dsa_mla_prefill": ([_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P, _P, _SZ, _P], _I32),
     "dsa_pages_workspace_bytes": ([_I32], _SZ),
     "dsa_copy_pages": (_POOLS + [_P, _P, _I32, _I32, _P], _I32),
     "dsa_fork_pages": (_POOLS + [_P, _P, _I32, _P, _I32, _I32, _P, _I32, _P, _I32, _P, _I32, _P, _P, _SZ, _P], _I32),

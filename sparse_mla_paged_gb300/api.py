@@ -480,6 +480,58 @@ def decode_full(q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
     return out
 
 
+def prefill_workspace_bytes(num_seqs: int, max_rows: int, num_q_heads: int) -> int:
+    _fit(num_seqs, max_rows, num_q_heads)
+    return int(_lib.load().dsa_mla_prefill_workspace_bytes(int(num_seqs), int(max_rows), int(num_q_heads)))
+
+
+def alloc_prefill_workspace(num_seqs: int, max_rows: int, num_q_heads: int, device=None) -> torch.Tensor:
+    """A workspace for prefill, to be kept from call to call (one per stream or captured graph)."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = prefill_workspace_bytes(num_seqs, max_rows, num_q_heads)
+    if n == 0:
+        raise DsaError(2, "dsa_mla_prefill_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def prefill(q, k_cache, v_cache, block_tables, max_blocks_per_seq, base_lens, new_lens, num_q_heads, block_size,
+            cache_stride_bytes, k_scale, v_scale, sm_scale, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """dsa_mla_prefill: rows packed as plan_step packs them (the new_lens[0] new tokens of request 0, then
+    those of request 1, ...); the i-th new token of request s attends to the first base_lens[s] + i + 1
+    tokens of its cache. Returns out (bf16 [max_rows, H, 512]); rows behind the last request's tokens are
+    left as they were. Without a workspace one is allocated for the call. step_device_status tells of
+    bad pages and lengths."""
+    i = _device_of(q, "q")
+    _need_on(q, torch.bfloat16, "q", i)
+    _need_on(k_cache, torch.uint8, "k_cache", i)
+    _need_on(v_cache, torch.uint8, "v_cache", i)
+    _need_on(block_tables, torch.int32, "block_tables", i)
+    _need_on(base_lens, torch.int32, "base_lens", i)
+    _need_on(new_lens, torch.int32, "new_lens", i)
+    n = base_lens.numel()
+    if num_q_heads < 1 or q.numel() % (num_q_heads * LATENT) or new_lens.numel() != n:
+        raise ValueError("q [max_rows, num_q_heads, 512], base_lens [num_seqs], new_lens [num_seqs]")
+    rows = q.numel() // (num_q_heads * LATENT)
+    _fit(n, rows, num_q_heads, max_blocks_per_seq, block_size)
+    _table_rows(block_tables, max_blocks_per_seq, n)
+    with _Launch(i, stream) as at:
+        if out is None or workspace is None:
+            with at.allocating():
+                out = torch.empty_like(q) if out is None else out
+                if workspace is None:
+                    workspace = alloc_prefill_workspace(n, rows, num_q_heads, q.device)
+        _need_on(out, torch.bfloat16, "out", i)
+        _need_on(workspace, torch.uint8, "workspace", i)
+        if out.numel() != q.numel():
+            raise ValueError("out [max_rows, num_q_heads, 512]")
+        check(_lib.load().dsa_mla_prefill(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks_per_seq,
+            base_lens.data_ptr(), new_lens.data_ptr(), n, rows, num_q_heads, block_size, cache_stride_bytes, k_scale, v_scale,
+            sm_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel(), at.raw), "dsa_mla_prefill")
+    return out
+
+
 def pages_workspace_bytes(num_pages: int) -> int:
     _fit(num_pages)
     return int(_lib.load().dsa_pages_workspace_bytes(int(num_pages)))

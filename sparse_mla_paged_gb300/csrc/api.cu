@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "full.cuh"
 #include "pages.cuh"
+#include "prefill.cuh"
 
 using namespace dsa;
 
@@ -901,6 +902,58 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
     if (st == DSA_OK) st = from_cuda(launch_full(p, kmap, vmap, s));
     if (st == DSA_OK) st = from_cuda(launch_full_combine(p, s));
     return st;
+}
+
+namespace {
+bool prefill_fits(int32_t num_seqs, int32_t max_rows, int32_t num_q_heads) {
+    return num_seqs <= DSA_MAX_PLAN_SEQS && max_rows <= kMaxPrefillRowHeads / num_q_heads;
+}
+}  // namespace
+
+size_t dsa_mla_prefill_workspace_bytes(int32_t num_seqs, int32_t max_rows, int32_t num_q_heads) {
+    if (num_seqs < 1 || max_rows < 1 || num_q_heads < 1 || !prefill_fits(num_seqs, max_rows, num_q_heads)) return 0;
+    DeviceState* d = nullptr;
+    return current_device(&d) == DSA_OK ? prefill::layout().total : 0;
+}
+
+int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                        int32_t max_blocks_per_seq, const int32_t* base_lens, const int32_t* new_lens, int32_t num_seqs,
+                        int32_t max_rows, int32_t num_q_heads, int32_t block_size, int64_t cache_stride_bytes, float k_scale,
+                        float v_scale, float sm_scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !block_tables || !base_lens || !new_lens || !out || !workspace) return DSA_ERR_INVALID_ARGUMENT;
+    if (num_seqs < 1 || max_rows < 1 || num_q_heads < 1 || block_size < 1 || max_blocks_per_seq < 0) return DSA_ERR_INVALID_ARGUMENT;
+    if (cache_stride_bytes < static_cast<int64_t>(block_size) * kLatent || cache_stride_bytes % 16 != 0)
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+        !aligned(base_lens, 4) || !aligned(new_lens, 4) || !aligned(workspace, 256))
+        return DSA_ERR_INVALID_ARGUMENT;
+    if (!prefill_fits(num_seqs, max_rows, num_q_heads)) return DSA_ERR_UNSUPPORTED;
+    DeviceState* d = nullptr;
+    const int32_t st = current_device(&d);
+    if (st != DSA_OK) return st;
+    if (workspace_bytes < prefill::layout().total) return DSA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    prefill::Params p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.block_tables = block_tables;
+    p.base_lens = base_lens;
+    p.new_lens = new_lens;
+    p.out = static_cast<uint16_t*>(out);
+    p.status = reinterpret_cast<int*>(ws);
+    p.step_status = d->step_status;
+    p.cache_stride = cache_stride_bytes;
+    p.num_seqs = num_seqs;
+    p.max_rows = max_rows;
+    p.heads = num_q_heads;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.by_block = fast_div(static_cast<uint32_t>(block_size));
+    p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
+    p.v_scale = v_scale;
+    p.wait_limit_ns = g_wait_limit_ns;
+    return from_cuda(launch_prefill(p, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t dsa_set_wait_limit(uint64_t limit_ns) {

@@ -24,6 +24,7 @@ constexpr int kHeadsPerCta = 64;       // query heads per work unit
 constexpr int kQImageBytes = 2 * kHeadsPerCta * kLatent;  // 64 KB
 constexpr int kBitmapWords = 8192;     // resolve bitmap: seq_len up to 262144 tokens
 constexpr int kResolveThreads = 256;
+constexpr int64_t kMaxPrefillRowHeads = 1 << 25;  // dsa_mla_prefill: rows * heads of a call
 constexpr int64_t kMaxFullRowHeads = 1 << 22;  // dsa_mla_decode_full: rows * heads of a call
 
 // Probabilities are carried as P' = 2^(x - m + kPBias) (x, m in log2 units) split into two

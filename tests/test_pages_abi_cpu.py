@@ -1,4 +1,4 @@
-"""Host-side refusals of the page operators: each bad argument is answered before any CUDA call."""
+"""Host-side refusals of the page operators and the prompt-chunk attention: each bad argument is answered before any CUDA call."""
 import ctypes
 
 import pytest
@@ -89,3 +89,22 @@ def test_workspace_of_bad_sizes_is_zero(lib):
 
 def test_pool_struct_layout():
     assert ctypes.sizeof(_lib.PagePool) == 40 and _lib.PagePool.layers.offset == 32
+
+
+PREFILL = dict(q=0x10000, k=0x20000, v=0x20000, bt=0x30000, mbps=8, base=0x40000, new=0x48000, n=2, rows=20, heads=16, bs=64,
+               stride=64 * 512, ks=0.05, vs=0.05, sm=0.04, out=0x50000, ws=0x60000, wsb=1 << 40)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(q=0), 1), (dict(k=0), 1), (dict(v=0), 1), (dict(bt=0), 1), (dict(mbps=-1), 1), (dict(base=0), 1), (dict(new=0), 1), (dict(n=0), 1),
+    (dict(rows=0), 1), (dict(heads=0), 1), (dict(bs=0), 1), (dict(stride=64 * 512 - 16), 1), (dict(stride=64 * 512 + 8), 1),
+    (dict(out=0), 1), (dict(ws=0), 1), (dict(ws=0x60010), 1), (dict(q=0x10008), 1), (dict(k=0x20008), 1), (dict(v=0x20008), 1),
+    (dict(bt=0x30002), 1), (dict(base=0x40002), 1), (dict(new=0x48002), 1), (dict(out=0x50008), 1), (dict(n=16385), 2),
+    (dict(rows=1 << 20, heads=33), 2), (dict(rows=2**31 - 1, heads=2**31 - 1), 2)])
+def test_prefill_rejects_on_host(lib, over, code):
+    assert lib.dsa_mla_prefill(*dict(PREFILL, **over).values(), None) == code
+
+
+def test_prefill_workspace_of_bad_shapes_is_zero(lib):
+    f = lib.dsa_mla_prefill_workspace_bytes
+    assert f(0, 1, 1) == 0 and f(1, 0, 1) == 0 and f(1, 1, 0) == 0 and f(16385, 1, 1) == 0 and f(1, 1 << 20, 33) == 0
