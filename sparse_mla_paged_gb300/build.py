@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdsa_mla.so")
 SOURCES = ["api.cu", "prologue.cu", "decode.cu", "combine.cu", "static_scratch.cu", "latent_write.cu", "select.cu",
            "absorb.cu", "plan.cu", "index_write.cu", "pool_scores.cu", "full_plan.cu", "full.cu", "pages.cu",
-           "api_pages.cu", "prefill.cu"]
+           "api_pages.cu", "prefill_plan.cu", "prefill.cu"]
 # Translation units: (source, object, extra flags); decode.cu is built once per tile size.
 UNITS = [("api.cu", "api.o", []), ("prologue.cu", "prologue.o", []),
          ("decode.cu", "decode64.o", ["-DDSA_TILE=64"]), ("decode.cu", "decode128.o", ["-DDSA_TILE=128"]),
@@ -27,7 +27,8 @@ UNITS = [("api.cu", "api.o", []), ("prologue.cu", "prologue.o", []),
          ("latent_write.cu", "latent_write.o", []), ("select.cu", "select.o", []), ("absorb.cu", "absorb.o", []),
          ("plan.cu", "plan.o", []), ("index_write.cu", "index_write.o", []), ("pool_scores.cu", "pool_scores.o", []),
          ("full_plan.cu", "full_plan.o", []), ("full.cu", "full.o", []), ("pages.cu", "pages.o", []),
-         ("api_pages.cu", "api_pages.o", []), ("prefill.cu", "prefill.o", [])]
+         ("api_pages.cu", "api_pages.o", []), ("prefill_plan.cu", "prefill_plan.o", []),
+         ("prefill.cu", "prefill.o", [])]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -118,6 +118,8 @@ int32_t current_device(DeviceState** out) {
             if (d.status == DSA_OK) d.status = from_cuda(full_setup());
             if (d.status == DSA_OK) d.status = from_cuda(full_plan_setup());
             if (d.status == DSA_OK) d.status = from_cuda(pages_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(prefill_setup());
+            if (d.status == DSA_OK) d.status = from_cuda(prefill_plan_setup(sms / 2));
         }
         d.checked = true;
     }
@@ -257,14 +259,16 @@ bool encode_page_map(const void* base, size_t mem_bytes, int32_t block_size, int
 }
 
 // 5-D map of a paged latent cache, [page][group of 8 rows][block of 128 bytes][row][128 bytes]:
-// a box of whole groups lands as the groups' swizzle atoms in order (full.cu's tile layout).
-bool encode_group_map(const void* base, size_t mem_bytes, int32_t block_size, int64_t stride, int32_t rows, CUtensorMap* m) {
+// a box of whole groups and `blocks` blocks lands as the groups' swizzle atoms in order (full.cu's
+// and prefill.cu's tile layouts).
+bool encode_group_map(const void* base, size_t mem_bytes, int32_t block_size, int64_t stride, int32_t rows, CUtensorMap* m,
+                      int32_t blocks = kLatent / 128) {
     const auto fn = tensor_map_encoder();
     if (!fn) return false;
     const cuuint64_t pages = std::min<cuuint64_t>(mem_bytes / static_cast<size_t>(stride) + 1, (1ull << 31) - 1);
     const cuuint64_t dims[5] = {128, 8, kLatent / 128, static_cast<cuuint64_t>(block_size / 8), pages};
     const cuuint64_t strides[4] = {kLatent, 128, 8 * kLatent, static_cast<cuuint64_t>(stride)};
-    const cuuint32_t box[5] = {128, 8, kLatent / 128, static_cast<cuuint32_t>(rows / 8), 1};
+    const cuuint32_t box[5] = {128, 8, static_cast<cuuint32_t>(blocks), static_cast<cuuint32_t>(rows / 8), 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void*>(base), dims, strides, box, estride,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -913,7 +917,8 @@ bool prefill_fits(int32_t num_seqs, int32_t max_rows, int32_t num_q_heads) {
 size_t dsa_mla_prefill_workspace_bytes(int32_t num_seqs, int32_t max_rows, int32_t num_q_heads) {
     if (num_seqs < 1 || max_rows < 1 || num_q_heads < 1 || !prefill_fits(num_seqs, max_rows, num_q_heads)) return 0;
     DeviceState* d = nullptr;
-    return current_device(&d) == DSA_OK ? prefill::layout().total : 0;
+    if (current_device(&d) != DSA_OK) return 0;
+    return prefill::layout(prefill::max_units(num_seqs, max_rows, num_q_heads), d->sms / 2).total;
 }
 
 int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
@@ -929,9 +934,11 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
         return DSA_ERR_INVALID_ARGUMENT;
     if (!prefill_fits(num_seqs, max_rows, num_q_heads)) return DSA_ERR_UNSUPPORTED;
     DeviceState* d = nullptr;
-    const int32_t st = current_device(&d);
+    int32_t st = current_device(&d);
     if (st != DSA_OK) return st;
-    if (workspace_bytes < prefill::layout().total) return DSA_ERR_WORKSPACE;
+    const int64_t units = prefill::max_units(num_seqs, max_rows, num_q_heads);
+    const prefill::Layout L = prefill::layout(units, d->sms / 2);
+    if (workspace_bytes < L.total) return DSA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     prefill::Params p{};
     p.q = static_cast<const uint16_t*>(q);
@@ -941,19 +948,42 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
     p.base_lens = base_lens;
     p.new_lens = new_lens;
     p.out = static_cast<uint16_t*>(out);
-    p.status = reinterpret_cast<int*>(ws);
+    p.status = reinterpret_cast<int*>(ws + L.status);
     p.step_status = d->step_status;
+    p.starts = reinterpret_cast<prefill::Start*>(ws + L.starts);
+    p.joins = reinterpret_cast<prefill::Join*>(ws + L.joins);
+    p.units = reinterpret_cast<prefill::Unit*>(ws + L.units);
+    p.qimg = ws + L.qimg;
+    p.part_o = reinterpret_cast<uint16_t*>(ws + L.part_o);
+    p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
     p.cache_stride = cache_stride_bytes;
+    p.clusters = d->sms / 2;
+    // With fewer units than an eighth of the ranges a unit comes in more than eight pieces.
+    p.few_units = units * 8 <= p.clusters ? 1 : 0;
+    const int64_t room = max_blocks_per_seq > 0 ? static_cast<int64_t>(max_blocks_per_seq) * block_size : full::kMaxLen;
+    p.room = static_cast<int32_t>(std::min(room, full::kMaxLen));
     p.num_seqs = num_seqs;
     p.max_rows = max_rows;
     p.heads = num_q_heads;
     p.block_size = block_size;
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.by_block = fast_div(static_cast<uint32_t>(block_size));
+    p.by_heads = fast_div(static_cast<uint32_t>(num_q_heads));
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;
     p.wait_limit_ns = g_wait_limit_ns;
-    return from_cuda(launch_prefill(p, static_cast<cudaStream_t>(stream)));
+    p.box_rows = std::min(box_rows(block_size), 32);  // other page sizes take per-thread copies
+    CUtensorMap kmap, vmap;
+    std::memset(&kmap, 0, sizeof kmap);
+    std::memset(&vmap, 0, sizeof vmap);
+    if (p.box_rows > 0 && !(encode_group_map(k_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &kmap) &&
+                            encode_group_map(v_cache, d->mem_bytes, block_size, cache_stride_bytes, p.box_rows, &vmap, kLatent / 256)))
+        p.box_rows = 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = from_cuda(launch_prefill_plan(p, s));
+    if (st == DSA_OK) st = from_cuda(launch_prefill(p, kmap, vmap, s));
+    if (st == DSA_OK) st = from_cuda(launch_prefill_join(p, s));
+    return st;
 }
 
 int32_t dsa_set_wait_limit(uint64_t limit_ns) {

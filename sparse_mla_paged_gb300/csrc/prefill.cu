@@ -1,120 +1,954 @@
-// Attention of packed prompt chunks over their paged latent caches: row t of request s, its i-th
-// new token, sees the positions below base[s] + i + 1.
+// Attention of packed prompt chunks over their paged latent caches: row t, the i-th new token of
+// request s, sees the positions below base[s] + i + 1.
 //
 //   out[t,h,:] = sum_{j < base[s]+i+1} softmax_j(sm_scale * q[t,h,:] . (k_scale*K_j)) (v_scale*V_j)
 //
-// A block per row and eight heads, a warp per head, a lane per 16 dims; one pass over the tokens
-// with a running maximum and sum in FP32.
+// A cluster of two CTAs works on one unit of 128 (row, head) pairs at a time (see prefill.cuh), and
+// both products are MMAs of the pair of SMs (cta_group::2). Arithmetic as in the full decode: the
+// cached E4M3 codes are the operands, a query is two E4M3 terms, P' = 2^(x - m + kPBias) two more.
+//
+//   S[256 query rows x 128 tokens] = Q K^T   each CTA holds the rows of its 64 pairs x {hi, lo} in
+//       tensor memory and brings 64 of the tile's tokens, all dims
+//   O^T[512 dims x 128 pairs] += V^T P'^T    each CTA accumulates 256 dims of all 128 pairs, brings
+//       those dims of the tile's tokens and the P' of its 64 pairs
+//
+// so that a CTA softmaxes its own pairs and no probability leaves it, while the second product has
+// N = 128 (full.cu: 64): 6 KB of operands for 64 cycles of arithmetic, not for 32.
+//
+//   warp 0, 1    load K and V tiles into rings of three each ([16 groups of 8 tokens][blocks of 128
+//                dims][8 tokens][128 bytes], 128-byte swizzle): tensor-map boxes of a page's rows
+//                when pages and tiles fit each other, else 16-byte copies
+//   warp 2, 3    issue Q K^T and P V (rank 0); tell rank 0 of the loaded K tiles (rank 1)
+//   warps 4-11   softmax, two per TMEM lane quarter
+//   warps 12-15  rescale O when a reference moves, write a unit's output, make the query operand of
+//                the next unit
+//
+// A reference that moves in one CTA rescales columns of O in both. The CTA that asks writes the
+// factors into both; the warp that issues P V finds its mark before the tile's product, has
+// warps 12-15 of both CTAs rescale, and goes on. Tiles that no pair asks in pay nothing for it.
+//
+// A tile that holds tokens which some row of the unit does not see is masked per pair, and its V
+// bytes are made safe before P V reads them: a hidden token's zero weight would not silence a NaN
+// code. Tokens past every row are cleared; one with a NaN code that only later rows see is cleared and
+// its score made NaN for the pairs that see it.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include "prefill.cuh"
+#include "ptx.cuh"
+#include "softmax.cuh"
 
 namespace dsa {
 namespace prefill {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kCtaPairs = kPairs / 2;
+constexpr int kSlots = 3;                           // of each ring
+constexpr int kKeyTokens = kTile / 2;               // tokens of a tile that a CTA brings as keys
+constexpr int kDims = kLatent / 2;                  // dims that it brings as values
+constexpr int kSlotBytes = kKeyTokens * kLatent;    // 32 KB
+static_assert(kSlotBytes == kTile * kDims, "both halves of a tile");
+constexpr int kKGroup = 8 * kLatent;                // bytes of 8 tokens
+constexpr int kVGroup = 8 * kDims;
+constexpr int kSoftmax0 = 4, kSoftmaxWarps = 8;
+constexpr int kEpilogue0 = 12, kEpilogueWarps = 4;
+constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
+constexpr int kThreads = (kEpilogue0 + kEpilogueWarps) * 32;
+constexpr int kHalfCols = kTile / 2;                // S columns per softmax warp
+static_assert(kScores == kHalfCols / 2, "scores per softmax thread: 32, one bit each of a word");
+constexpr int kPTermBytes = kCtaPairs * kTile;
 
-__device__ __forceinline__ void report(const Params& p) {
-    atomicCAS(p.status, 0, kStatusBounds);
-    atomicCAS(p.step_status, 0, kStatusBounds);
+constexpr int kBarSoftmax = 1;
+constexpr int kBarPair0 = 2;  // 2..5: the two softmax warps of a lane quarter
+
+constexpr int kOffV = kSlots * kSlotBytes;
+constexpr int kOffP = 2 * kSlots * kSlotBytes;               // P' [2 buffers][hi, lo]
+constexpr int kOffHm = kOffP + 4 * kPTermBytes;              // float2 [2 token halves][64] tile maximum, account; row sums at the end
+constexpr int kOffAlpha = kOffHm + 2 * kCtaPairs * 8;        // float [2 tile parities][128] rescale factors, of both CTAs
+constexpr int kOffF = kOffAlpha + 2 * kPairs * 4;            // float [128] output factors, of both CTAs
+constexpr int kOffScale = kOffF + kPairs * 4;                // u8 [2 unit parities][64] exponents of the queries' scales
+constexpr int kOffFlags = kOffScale + 2 * kCtaPairs;         // u32 [2 tile parities][2 CTAs][4 lane quarters] tile that moved a reference
+constexpr int kOffBroken = kOffFlags + 2 * 2 * 4 * 4;        // u32 [2 unit parities][4] tokens from the unit's shortest row on with a NaN code
+constexpr int kOffEvent = kOffBroken + 2 * 4 * 4;            // u32: a tile's number + 1 to rescale before, 0: the unit is done
+constexpr int kOffTmem = kOffEvent + 4;
+constexpr int kOffAbort = kOffTmem + 4;
+constexpr int kOffBars = (kOffAbort + 4 + 7) / 8 * 8;
+// (both): in either CTA; (0): in rank 0, both CTAs arrive.
+enum {
+    BAR_KFULL0 = 0,                    // own half of a K slot loaded
+    BAR_VFULL0 = BAR_KFULL0 + kSlots,  // own half of a V slot loaded
+    BAR_KPEER0 = BAR_VFULL0 + kSlots,  // (0) rank 1's half of a K slot loaded
+    BAR_KEMPTY0 = BAR_KPEER0 + kSlots, // (both) its Q K^T is done
+    BAR_VEMPTY0 = BAR_KEMPTY0 + kSlots,// (both) its P V is done
+    BAR_PFULL0 = BAR_VEMPTY0 + kSlots, // (0) 2: P' buffers written, V there
+    BAR_PVDONE0 = BAR_PFULL0 + 2,      // (both) 2: the P V reading it is done
+    BAR_SFULL = BAR_PVDONE0 + 2,       // (both) S written
+    BAR_SEMPTY,                        // (0) S read
+    BAR_QFULL,                         // (0) query operands in place
+    BAR_QEMPTY,                        // (both) the unit's last Q K^T is done
+    BAR_EVENT,                         // (both) something for the epilogue warps
+    BAR_OFREE,                         // (0) they did it
+    BAR_FFULL,                         // (both) output factors written
+    BAR_FEMPTY,                        // (both) and used
+    BAR_DRAIN,                         // (0) every MMA is done
+    kNumBars
+};
+constexpr int kSmem = kOffBars + kNumBars * 8;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 0;    // O^T: dims 128c.. of this CTA's 256, all pairs, at column 128c
+constexpr uint32_t kTmemQ = 256;  // query operand
+constexpr uint32_t kTmemS = 384;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// A cluster's stretch of one unit.
+struct Segment {
+    int32_t k, t0, t1;  // unit's number, tiles of it
+    int32_t part;       // partial slot, -1: the whole unit
+    int32_t max_len, min_len;
+    bool last;
+    Unit u;
+};
+
+// What every role of a CTA has in hand.
+struct Cta {
+    const Params& p;
+    uint8_t* smem;
+    uint32_t sbase, rank, cluster;
+    volatile int* abort_flag;
+    uint32_t tmem;
+    int64_t begin, end;
+    int32_t gap;
+
+    __device__ uint32_t bar(int i) const { return sbase + kOffBars + 8 * i; }
+    __device__ void fail(int code) const {
+        report(p, code);
+        *abort_flag = 1;
+        st_cluster(map_rank(sbase + kOffAbort, rank ^ 1u), 1u);
+    }
+    __device__ void wait(int b, uint32_t parity) const {
+        if (!mbar_wait_cluster(bar(b), parity, abort_flag, p.wait_limit_ns)) fail(kStatusTimeout);
+        __syncwarp();
+    }
+    __device__ void arrive(int b, uint32_t to) const { mbar_arrive_cluster(map_rank(bar(b), to)); }
+
+    __device__ Segment segment(int32_t k, const Unit& u, bool first) const {
+        Segment s;
+        s.u = u;
+        s.k = k;
+        s.max_len = pair_len(p, u.base, u.first + u.valid - 1);
+        s.min_len = pair_len(p, u.base, u.first);
+        const int64_t e = u.start + (s.max_len + kTile - 1) / kTile;
+        s.t0 = static_cast<int32_t>((begin > u.start ? begin : u.start) - u.start);
+        s.t1 = static_cast<int32_t>((end < e ? end : e) - u.start);
+        s.part = begin <= u.start && e <= end ? -1 : 2 * static_cast<int32_t>(cluster) + (first ? 0 : 1);
+        s.last = e + gap >= end;
+        return s;
+    }
+    __device__ Segment first() const {
+        const Start& st = p.starts[cluster];
+        return segment(st.k, st.unit, true);
+    }
+    __device__ Segment next(const Segment& s) const { return segment(s.k + 1, p.units[s.k + 1], false); }
+};
+
+// Page of the block that holds position pos (negative: the caller reports it), and its row there.
+__device__ __forceinline__ int32_t page_of(const Params& p, int32_t seq, int32_t pos, int32_t* row) {
+    const int32_t blk = static_cast<int32_t>(divide(static_cast<uint32_t>(pos), p.by_block));
+    *row = pos - blk * p.block_size;
+    return __ldg(p.block_tables + static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk);
 }
 
-__device__ __forceinline__ void decode16(const uint4& c, float (&v)[16]) {
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+// Box of whole 8-token groups of one page, from 128-byte block `block` on.
+__device__ __forceinline__ void tma_groups(uint32_t dst, const void* tmap, int32_t block, int32_t group, int32_t page, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4, %5}], [%6];" ::
+            "r"(dst), "l"(tmap), "r"(0), "r"(block), "r"(group), "r"(page), "r"(bar)
+        : "memory");
+}
+
+// ------------------------------------------------------------------------------------
+// load: warp 0 keys (64 tokens of a tile), warp 1 values (256 dims)
+// ------------------------------------------------------------------------------------
+template <bool kValues>
+__device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
+    constexpr int kTokens = kValues ? kTile : kKeyTokens;
+    constexpr int kFull = kValues ? BAR_VFULL0 : BAR_KFULL0, kEmpty = kValues ? BAR_VEMPTY0 : BAR_KEMPTY0;
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * (kValues ? kDims : kLatent);
+    const uint32_t ring = c.sbase + (kValues ? kOffV : 0);
+    const int32_t block = kValues ? static_cast<int32_t>(c.rank) * (kDims / 128) : 0;
+    const int32_t pos0 = lane * p.box_rows + (kValues ? 0 : static_cast<int32_t>(c.rank) * kKeyTokens);
+    const bool have = lane * p.box_rows < kTokens;  // a box of this lane's in every tile
+    uint32_t tau = 0;
+    bool stop = false;
+    for (Segment s = c.first(); !stop; s = c.next(s)) {
+        // This lane's page of tile t (requested a tile ahead), its first row there, and whether any
+        // row of the unit sees the box.
+        auto look = [&](int32_t t, int32_t* row, bool* live) {
+            const int32_t pos = t * kTile + pos0;
+            *live = have && t < s.t1 && pos < s.max_len;
+            return *live ? page_of(p, s.u.seq, pos, row) : -1;
+        };
+        int32_t row_next = 0;
+        bool live_next;
+        int32_t page_next = look(s.t0, &row_next, &live_next);
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int32_t page = page_next, row = row_next;
+            const bool live = live_next;
+            page_next = look(t + 1, &row_next, &live_next);
+            if (live && page < 0) report(p, kStatusBounds);
+            const int e = static_cast<int>(tau % kSlots);
+            if (tau >= kSlots) c.wait(kEmpty + e, (tau / kSlots - 1) & 1);
+            // After a failed wait nothing more is issued (the drain below finds what is in flight).
+            if (__any_sync(0xffffffffu, *c.abort_flag != 0)) {
+                stop = true;
+                break;
+            }
+            const uint32_t full = c.bar(kFull + e), boxes = __popc(__ballot_sync(0xffffffffu, live));
+            if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes);
+            __syncwarp();
+            if (live) tma_groups(ring + e * kSlotBytes + lane * box_bytes, tmap, block, row >> 3, page, full);  // a negative page lies outside the map: zeros
+            __syncwarp();
+        }
+        if (s.last) break;
+    }
+    // No copy into shared memory is in flight when the CTA exits.
+    if (lane == 0) {
+        for (uint32_t i = tau > kSlots ? tau - kSlots : 0; i < tau; ++i) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(c.bar(kFull + static_cast<int>(i % kSlots)), (i / kSlots) & 1) && globaltimer_ns() - t0 < kDrainLimitNs) {
+            }
+        }
+    }
+    __syncwarp();
+}
+
+// The same by 16-byte copies: a key row per instruction, or the halves of two value rows.
+template <bool kValues>
+__device__ void run_load_copies(const Cta& c) {
+    constexpr int kTokens = kValues ? kTile : kKeyTokens;
+    constexpr int kFull = kValues ? BAR_VFULL0 : BAR_KFULL0, kEmpty = kValues ? BAR_VEMPTY0 : BAR_KEMPTY0;
+    constexpr int kGroup = kValues ? kVGroup : kKGroup;
+    constexpr int kEach = kTokens / 32;            // tokens that a lane looks up
+    constexpr int kRows = kValues ? 2 : 1;         // per instruction
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31;
+    const int sub = kValues ? lane >> 4 : 0, piece = kValues ? lane & 15 : lane;
+    const uint8_t* cache = (kValues ? p.v_cache + c.rank * kDims : p.k_cache) + piece * 16;
+    const uint32_t ring = c.sbase + (kValues ? kOffV : 0) + (piece >> 3) * 1024;
+    const int32_t pos0 = lane + (kValues ? 0 : static_cast<int32_t>(c.rank) * kKeyTokens);
+    uint32_t tau = 0;
+    for (Segment s = c.first();; s = c.next(s)) {
+        int32_t row_next[kEach], page_next[kEach];
+        // Pages and rows there (row -1: no token). What is made of them is left to the next tile:
+        // using a page here would wait for its load.
+        auto look = [&](int32_t t) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        __nv_fp8_e4m3 f;
-        f.__x = static_cast<__nv_fp8_storage_t>(w[i >> 2] >> (8 * (i & 3)));
-        v[i] = static_cast<float>(f);
+            for (int i = 0; i < kEach; ++i) {
+                const int32_t pos = t * kTile + pos0 + 32 * i;
+                row_next[i] = -1;
+                page_next[i] = t < s.t1 && pos < s.max_len ? page_of(p, s.u.seq, pos, &row_next[i]) : 0;
+            }
+        };
+        look(s.t0);
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            int64_t mine[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                if (page_next[i] < 0) report(p, kStatusBounds);
+                mine[i] = page_next[i] < 0 || row_next[i] < 0 ? -1 : page_next[i] * p.cache_stride + static_cast<int64_t>(row_next[i]) * kLatent;
+            }
+            look(t + 1);
+            const int e = static_cast<int>(tau % kSlots);
+            if (tau >= kSlots) c.wait(kEmpty + e, (tau / kSlots - 1) & 1);
+            const uint32_t dst = ring + e * kSlotBytes;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+#pragma unroll 4
+                for (int j = 0; j < 32; j += kRows) {
+                    const int64_t at = __shfl_sync(0xffffffffu, mine[i], j + sub);
+                    const int tok = 32 * i + j + sub;
+                    const uint32_t d = dst + (tok >> 3) * kGroup + (tok & 7) * 128 + (((piece & 7) ^ (tok & 7)) << 4);
+                    cp_async_16_zfill(d, cache + (at >= 0 ? at : 0), at >= 0 ? 16u : 0u);
+                }
+            }
+            cp_async_arrive_noinc(c.bar(kFull + e));
+        }
+        if (s.last) break;
+    }
+    cp_async_wait_all();
+}
+
+// ------------------------------------------------------------------------------------
+// MMA warps of rank 0 (converged, one elected lane issues)
+// ------------------------------------------------------------------------------------
+__device__ void run_qk(const Cta& c) {
+    const uint32_t idesc = idesc_e4m3(256, kTile, false, false);
+    const uint32_t el = elect_one();
+    uint32_t tau = 0, units = 0;
+    for (Segment s = c.first();; s = c.next(s)) {
+        c.wait(BAR_QFULL, units++ & 1);
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int e = static_cast<int>(tau % kSlots);
+            c.wait(BAR_KFULL0 + e, (tau / kSlots) & 1);
+            c.wait(BAR_KPEER0 + e, (tau / kSlots) & 1);
+            if (tau > 0) c.wait(BAR_SEMPTY, (tau - 1) & 1);
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint64_t kdesc = smem_desc(c.sbase + e * kSlotBytes, 16, kKGroup, kSwizzle128B);
+            const uint32_t d = c.tmem + kTmemS;
+#pragma unroll
+            for (int ks = 0; ks < 16; ++ks)
+                mma_pair_ts_el(d, c.tmem + kTmemQ + ks * 8, kdesc + static_cast<uint64_t>(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), idesc,
+                               ks > 0 ? 1u : 0u, el);
+            commit_both_el(c.bar(BAR_SFULL), el);
+            commit_both_el(c.bar(BAR_KEMPTY0 + e), el);
+            if (t == s.t1 - 1) commit_both_el(c.bar(BAR_QEMPTY), el);
+        }
+        if (s.last) break;
+    }
+    commit_own_el(c.bar(BAR_DRAIN), el);
+}
+
+__device__ void run_pv(const Cta& c) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t idesc = idesc_e4m3(256, kPairs, true, false);
+    const uint32_t el = elect_one();
+    const uint64_t pdesc0 = smem_desc(c.sbase + kOffP, 1024, 128, kSwizzleNone);
+    const volatile uint32_t* flags = reinterpret_cast<const volatile uint32_t*>(c.smem + kOffFlags);
+    uint32_t tau = 0, events = 0;
+    // Has the epilogue warps of both CTAs do what `event` says.
+    auto post = [&](uint32_t event) {
+        if (lane < 2) {
+            st_cluster(map_rank(c.sbase + kOffEvent, lane), event);
+            c.arrive(BAR_EVENT, lane);
+        }
+        __syncwarp();
+        ++events;
+    };
+    for (Segment s = c.first();; s = c.next(s)) {
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int pb = tau & 1, e = static_cast<int>(tau % kSlots);
+            c.wait(BAR_PFULL0 + pb, (tau >> 1) & 1);
+            if (t == s.t0) {
+                if (events > 0) c.wait(BAR_OFREE, (events - 1) & 1);  // the unit before has been read
+            } else if (__any_sync(0xffffffffu, flags[pb * 8 + (lane & 7)] == tau + 1)) {
+                post(tau + 1);
+                c.wait(BAR_OFREE, (events - 1) & 1);
+            }
+            fence_proxy_async_smem();
+            tc_fence_after();
+            // V^T: 128 dims of block mc x 32 tokens (four 8-token swizzle groups), MN-major.
+            // P'^T: 64 pairs of each CTA x 32 tokens, K-major core matrices.
+            const uint64_t vdesc = smem_desc(c.sbase + kOffV + e * kSlotBytes, 1024, kVGroup, kSwizzle128B);
+            const uint64_t pdesc = pdesc0 + static_cast<uint64_t>((pb * 2 * kPTermBytes) >> 4);
+#pragma unroll
+            for (int j = 0; j < kTile / 32; ++j) {
+                const uint64_t bh = pdesc + static_cast<uint64_t>((j * 2048) >> 4);
+                const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + j * 2048) >> 4);
+#pragma unroll
+                for (int mc = 0; mc < kDims / 128; ++mc) {
+                    const uint64_t a = vdesc + static_cast<uint64_t>((j * 4 * kVGroup + mc * 1024) >> 4);
+                    const uint32_t d = c.tmem + kTmemO + mc * kPairs;
+                    mma_pair_ss_el(d, a, bh, idesc, j > 0 || t > s.t0 ? 1u : 0u, el);
+                    mma_pair_ss_el(d, a, bl, idesc, 1u, el);
+                }
+            }
+            commit_both_el(c.bar(BAR_PVDONE0 + pb), el);
+            commit_both_el(c.bar(BAR_VEMPTY0 + e), el);
+        }
+        post(0);
+        if (s.last) break;
+    }
+    commit_own_el(c.bar(BAR_DRAIN), el);
+}
+
+// Rank 1: its half of each K slot, to rank 0.
+__device__ void run_forward(const Cta& c) {
+    const int lane = threadIdx.x & 31;
+    uint32_t tau = 0;
+    for (Segment s = c.first();; s = c.next(s)) {
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            const int e = static_cast<int>(tau % kSlots);
+            c.wait(BAR_KFULL0 + e, (tau / kSlots) & 1);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) c.arrive(BAR_KPEER0 + e, 0);
+        }
+        if (s.last) break;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) prefill_kernel(const Params p) {
-    __shared__ int32_t seq_s, row_s;
+// ------------------------------------------------------------------------------------
+// softmax warps
+// ------------------------------------------------------------------------------------
+__device__ void run_softmax(const Cta& c) {
+    const Params& p = c.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x;
-    if (threadIdx.x == 0) {
-        int64_t at = 0;
-        int32_t s = 0;
-        for (; s < p.num_seqs; ++s) {
-            const int32_t n = max(p.new_lens[s], 0);
-            if (row < at + n) break;
-            at += n;
+    const int sw = warp - kSoftmax0;               // 0..7
+    const int q4 = warp & 3;                       // TMEM lane quarter
+    const int half = sw >> 2;                      // token half of each tile
+    const int term = lane & 1;                     // 0: hi row, 1: lo row
+    const int hq = 16 * q4 + (lane >> 1);          // pair of this thread within the CTA
+    const int pair = static_cast<int>(c.rank) * kCtaPairs + hq;  // and within the unit
+    float2* hm_s = reinterpret_cast<float2*>(c.smem + kOffHm);
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    // This thread's first 16-byte row in a P' term: K-major core matrices of 8 pairs x 16 tokens.
+    const uint32_t p_off = (((half * kHalfCols + term * kScores) / 16) * 8 + (hq >> 3)) * 128 + (hq & 7) * 16;
+    uint32_t tau = 0, units = 0;
+    bool pv_seen = false;  // the P.V two tiles back was already waited for
+
+    Segment next = c.first();
+    for (;; ++units) {
+        const Segment s = next;
+        if (!s.last) next = c.next(s);
+        const int32_t len = pair < s.u.valid ? pair_len(p, s.u.base, s.u.first + pair) : 0;
+        float qs = 0.0f;        // what turns dots into log2 scores, known with the first tile
+        float m_ref = kNegInf;  // reference max of the pair (log2 units)
+        float m_top = kNegInf;  // highest reference so far
+        float l_part = 0.0f;    // this thread's share of the sum of P'
+        float credit = 0.0f;    // and its account of what the terms may have lost of it
+
+        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+            c.wait(BAR_SFULL, tau & 1);
+            tc_fence_after();
+            // Dots of pair hq with tokens tok0 .. tok0+31 of the tile: this lane's term plus the
+            // neighbouring lane's other one; the score in log2 units is qs (> 0) times that.
+            const int tok0 = half * kHalfCols + term * kScores;
+            float x[kScores];
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                uint32_t a[16], b[16];
+                tmem_ld_x16(c.tmem + lane_base + kTmemS + half * kHalfCols + 16 * part, a);
+                tmem_ld_x16(c.tmem + lane_base + kTmemS + half * kHalfCols + kScores + 16 * part, b);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float send = __uint_as_float(term ? a[j] : b[j]);
+                    const float mine = __uint_as_float(term ? b[j] : a[j]);
+                    x[16 * part + j] = mine + __shfl_xor_sync(0xffffffffu, send, 1);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) c.arrive(BAR_SEMPTY, 0);
+            if (t == s.t0) {
+                // A broken query's scale is NaN, which would also reach the -inf of hidden tokens: a
+                // pair that sees none (behind the unit's last) takes 1 and stays at zero.
+                const uint32_t e = c.smem[kOffScale + (units & 1) * kCtaPairs + hq];
+                qs = e == 255 || p.score_scale != p.score_scale ? __uint_as_float(0x7FC00000u)
+                                                                : fmaxf(fabsf(p.score_scale) * __uint_as_float(e << 23), 0x1p-120f);
+                if (len == 0) qs = 1.0f;
+            }
+            const int v_slot = static_cast<int>(tau % kSlots);
+            if ((t + 1) * kTile > s.min_len) {  // an edge tile
+                uint8_t* v_tile = c.smem + kOffV + v_slot * kSlotBytes;
+                const uint32_t* broken = reinterpret_cast<const uint32_t*>(c.smem + kOffBroken) + (units & 1) * 4;
+                auto is_broken = [&](int32_t pos) {
+                    const int32_t i = pos - s.min_len;
+                    return i >= 0 && i < kPairs && (broken[i >> 5] >> (i & 31) & 1u) != 0u;
+                };
+                // This lane's token of the warp's sixteen: 128 of its dims here.
+                const int token = 16 * sw + (lane & 15);
+                const int32_t pos = t * kTile + token;
+                const bool clear = pos >= s.max_len || is_broken(pos);
+                if (__any_sync(0xffffffffu, clear)) {
+                    c.wait(BAR_VFULL0 + v_slot, (tau / kSlots) & 1);
+                    if (clear) {
+                        uint4* at = reinterpret_cast<uint4*>(v_tile + (token >> 3) * kVGroup + (lane >> 4) * 1024 + (token & 7) * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) at[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+                const int32_t lim = len - t * kTile;
+                const uint32_t any = broken[0] | broken[1] | broken[2] | broken[3];
+#pragma unroll
+                for (int j = 0; j < kScores; ++j) {
+                    if (tok0 + j >= lim) x[j] = kNegInf;
+                    else if (any != 0u && is_broken(t * kTile + tok0 + j)) x[j] = __uint_as_float(0x7FC00000u);
+                }
+            }
+            float hm4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+            for (int j = 0; j < kScores; j += 2) hm4[(j >> 1) & 3] = max3(hm4[(j >> 1) & 3], x[j], x[j + 1]);
+            float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
+            hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1)) * qs;
+            // As in the full decode: P' is formed with the reference as it is (but for a unit's first
+            // tile), one barrier tells whether any half of any pair's scores asks for a move, and
+            // only then the halves are compared, references move and P' is formed again.
+            const bool ask = hmax > m_ref + kRescaleMargin ||
+                             (hmax < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && hmax != kNegInf);
+            uint32_t hw[kScores / 4], lw[kScores / 4];
+            float fresh, earned = 0.0f;
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+                if (again || t > s.t0) {
+                    float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
+#pragma unroll
+                    for (int g = 0; g < kScores / 4; ++g) {
+                        float pp[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            pp[e] = ex2_approx(fmaf(x[4 * g + e], qs, off));
+                            ls4[e] += pp[e];
+                        }
+                        uint32_t h0, l0, h1, l1;
+                        split2(pp[0], pp[1], h0, l0);
+                        split2(pp[2], pp[3], h1, l1);
+                        hw[g] = h0 | h1 << 16;
+                        lw[g] = l0 | l1 << 16;
+                    }
+                    fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+                    earned = fmaf(fresh, kLostShare, -fminf(fresh, kMostLost));
+                    if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(
+                                     ask || (credit + earned < 0.0f && m_ref > m_top - kRescaleFloor)))
+                        break;
+                }
+                const float credit2 = credit + earned + __shfl_xor_sync(0xffffffffu, credit + earned, 1);
+                if (term == 0) hm_s[half * kCtaPairs + hq] = make_float2(hmax, credit2);
+                named_bar_sync_id(kBarPair0 + q4, 64);
+                const float2 h0 = hm_s[hq], h1 = hm_s[kCtaPairs + hq];
+                const float tm = fmaxf(h0.x, h1.x), credit4 = h0.y + h1.y;
+                // The move is paid for once any pair needs it: every pair whose reference rises with
+                // this tile takes its new one too, and seldom asks for a move of its own.
+                const bool rise = tm + kSlack > m_ref;
+                const bool change = rise || ((tm < m_ref - kRescaleDrop || (tm < m_ref - kSlack && credit4 < 4.0f * kMostLost)) &&
+                                             m_ref > m_top - kRescaleFloor && tm != kNegInf);
+                float alpha = 1.0f;
+                if (change) {
+                    const float m_new = fmaxf(tm + (rise ? kSlack : kRescaleSlack), m_top - kRescaleFloor);
+                    alpha = m_ref == kNegInf ? 0.0f : ex2_approx(m_ref - m_new);
+                    l_part *= alpha;
+                    credit *= alpha;
+                    m_ref = m_new;
+                    m_top = fmaxf(m_top, m_new);
+                } else {
+                    credit = fmaf(0.25f, credit4, -earned);  // in equal parts: who asked gets what the others do not need
+                }
+                if (t > s.t0 && half == 0) {
+                    // Factors and the tile's mark into both CTAs (the words' last readers were done
+                    // before the P.V two tiles back).
+                    if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
+                    pv_seen = true;
+                    const uint32_t changed = __ballot_sync(0xffffffffu, change);
+                    const uint32_t to = map_rank(c.sbase, term);  // a lane of each pair per CTA
+                    st_cluster(to + kOffAlpha + ((tau & 1) * kPairs + pair) * 4, __float_as_uint(alpha));
+                    if (lane < 2 && changed != 0u)
+                        st_cluster(to + kOffFlags + (((tau & 1) * 2 + c.rank) * 4 + q4) * 4, tau + 1);
+                    __syncwarp();
+                }
+                // Also keeps the next tile's maxima from overwriting these.
+                if (!named_bar_any<kBarSoftmax, kSoftmaxThreads>(change) && t > s.t0) break;
+            }
+            l_part += fresh;
+            credit += earned;
+            if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
+            pv_seen = false;
+            const uint32_t pb = c.sbase + kOffP + (tau & 1) * 2 * kPTermBytes;
+#pragma unroll
+            for (int i = 0; i < kScores / 16; ++i) {
+                st_shared_v4(pb + p_off + i * 1024, hw[4 * i], hw[4 * i + 1], hw[4 * i + 2], hw[4 * i + 3]);
+                st_shared_v4(pb + kPTermBytes + p_off + i * 1024, lw[4 * i], lw[4 * i + 1], lw[4 * i + 2], lw[4 * i + 3]);
+            }
+            c.wait(BAR_VFULL0 + v_slot, (tau / kSlots) & 1);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) c.arrive(BAR_PFULL0 + (tau & 1), 0);
         }
-        seq_s = s;
-        row_s = static_cast<int32_t>(row - at);
-        if (blockIdx.y == 0) {
-            if (s < p.num_seqs) {
-                if (p.base_lens[s] < 0 || p.new_lens[s] < 0) report(p);
-            } else if (row == 0 || row == p.max_rows - 1) {
-                for (int32_t i = 0; i < p.num_seqs; ++i)
-                    if (p.new_lens[i] < 0) report(p);
-            }
-            if (row == p.max_rows - 1) {
-                int64_t all = 0;
-                for (int32_t i = 0; i < p.num_seqs; ++i) all += max(p.new_lens[i], 0);
-                if (all > p.max_rows) report(p);
-            }
+
+        // ---- the unit's output factors, to both CTAs ----
+        const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
+        if (term == 0) hm_s[half * kCtaPairs + hq].x = lpair;
+        named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
+        if (half == 0) {
+            if (units > 0) c.wait(BAR_FEMPTY, (units - 1) & 1);
+            const float l = hm_s[hq].x + hm_s[kCtaPairs + hq].x;
+            const bool whole = s.part < 0;
+            const float f = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
+            st_cluster(map_rank(c.sbase, term) + kOffF + pair * 4, __float_as_uint(f));
+            if (!whole && term == 0) p.part_lse[s.part * kPairs + pair] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
+            __syncwarp();
+            if (lane < 2) c.arrive(BAR_FFULL, lane);
+        }
+        named_bar_sync<kBarSoftmax, kSoftmaxThreads>();  // the sums are read
+        if (s.last) break;
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// epilogue warps: O's rescales and output, query operands
+// ------------------------------------------------------------------------------------
+constexpr int kPrepPairs = 4;   // pairs of a step, their loads in flight together
+constexpr int kPrepSteps = kCtaPairs / kEpilogueWarps / kPrepPairs;
+
+// Query operand rows of kPrepPairs of this warp's 16 pairs: lane l has dims [16l, 16l+16). A
+// head's bf16 query becomes two E4M3 terms after a scaling by a power of two (exact for elements from
+// 2^-9 of its largest, smaller ones off by 2^-16 of it at most), rows 2k and 2k+1 the terms of pair
+// k, stored chunk-major. The scale of its dots is positive (maxima are taken of the dots): a
+// negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or an
+// infinity gets zero codes and a NaN scale (exponent 255), which makes all its scores NaN.
+__device__ void prepare(const Cta& c, const Unit& u, int parity, int step, uint8_t* img) {
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const int h0 = 16 * q4 + kPrepPairs * step;
+    uint4 raw[kPrepPairs][2];
+#pragma unroll
+    for (int i = 0; i < kPrepPairs; ++i) {
+        const int pair = static_cast<int>(c.rank) * kCtaPairs + h0 + i;
+        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
+        if (pair < u.valid) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (u.pair0 + pair) * kLatent + lane * 16);
+            raw[i][0] = src[0];
+            raw[i][1] = src[1];
         }
     }
+    const float sign = p.score_scale > 0.0f ? 1.0f : (p.score_scale < 0.0f ? -1.0f : 0.0f);
+#pragma unroll
+    for (int i = 0; i < kPrepPairs; ++i) {
+        const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w, raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+        uint32_t amax = 0;  // magnitudes as bits: NaN and infinity are the largest
+#pragma unroll
+        for (int k = 0; k < 8; ++k) amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        const int E = static_cast<int>(amax >> 23);
+        const bool broken = E == 255;
+        int e = amax > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
+        e = e > 126 ? 126 : (e < -126 ? -126 : e);
+        const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * sign;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float vh[4], vl[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t bits = m & 1 ? w[2 * k + m / 2] & 0xFFFF0000u : w[2 * k + m / 2] << 16;
+                const float v = broken ? 0.0f : __uint_as_float(bits) * sc;
+                vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
+                vl[m] = v - vh[m];
+            }
+            hi[k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
+            lo[k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
+        }
+        uint4* at = reinterpret_cast<uint4*>(img + lane * 2048 + 2 * (h0 + i) * 16);
+        __stcg(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        __stcg(at + 1, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        if (lane == 0) c.smem[kOffScale + parity * kCtaPairs + h0 + i] = broken ? 255 : static_cast<uint8_t>(127 - e);
+    }
+    __syncwarp();
+}
+
+// Which of the tokens from the unit's shortest row on to its longest one's end hold a NaN code; both
+// CTAs find out for themselves. One word of 32 tokens per warp.
+__device__ void find_broken(const Cta& c, const Segment& s, int parity) {
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const int32_t first = s.min_len + 32 * q4, count = min(32, s.max_len - first);
+    uint32_t word = 0;
+    if (count > 0) {
+        int32_t row = 0;
+        const int32_t page = lane < count ? page_of(p, s.u.seq, first + lane, &row) : -1;
+        const int64_t mine = page < 0 ? -1 : page * p.cache_stride + static_cast<int64_t>(row) * kLatent;
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const int64_t at = __shfl_sync(0xffffffffu, mine, i);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (at >= 0) v = *reinterpret_cast<const uint4*>(p.v_cache + at + lane * 16);
+            const uint32_t nan = ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                 ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
+            if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) word |= 1u << i;
+        }
+    }
+    if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = word;
+    __syncwarp();
+}
+
+__device__ void run_epilogue(const Cta& c) {
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    uint8_t* images = p.qimg + static_cast<int64_t>(blockIdx.x) * 2 * kQImageBytes;
+    uint32_t tau = 0, units = 0, events = 0;
+
+    auto load_q = [&](int parity) {
+        const uint4* src = reinterpret_cast<const uint4*>(images + static_cast<int64_t>(parity) * kQImageBytes + (q4 * 32 + lane) * 16);
+#pragma unroll 1
+        for (int part = 0; part < 4; ++part) {
+            uint32_t a[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = __ldcg(src + (part * 8 + i) * (2048 / 16));
+                a[4 * i] = v.x;
+                a[4 * i + 1] = v.y;
+                a[4 * i + 2] = v.z;
+                a[4 * i + 3] = v.w;
+            }
+            tmem_st_x32(c.tmem + lane_base + kTmemQ + part * 32, a);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) c.arrive(BAR_QFULL, 0);
+    };
+    auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_cluster(c.bar(b), parity)) != 0; };
+
+    Segment next = c.first();
+    for (int step = 0; step < kPrepSteps; ++step) prepare(c, next.u, 0, step, images);
+    find_broken(c, next, 0);
+    load_q(0);
+    for (;; ++units) {
+        const Segment s = next;
+        int step = 0;            // of the next unit's operand; past the last one it waits for its place
+        bool q_loaded = s.last;
+        if (!s.last) next = c.next(s);
+        tau += s.t1 - s.t0;
+        for (;;) {
+            if (!ready(BAR_EVENT, events & 1)) {
+                const int parity = (units + 1) & 1;
+                if (!s.last && step < kPrepSteps) {
+                    prepare(c, next.u, parity, step++, images + static_cast<int64_t>(parity) * kQImageBytes);
+                    continue;
+                }
+                if (!s.last && step == kPrepSteps) {
+                    find_broken(c, next, parity);
+                    ++step;
+                    continue;
+                }
+                if (!q_loaded) {
+                    // The operand's place is free before the unit's last event.
+                    const uint64_t t0 = globaltimer_ns();
+                    bool event = false;
+                    while (!ready(BAR_QEMPTY, units & 1)) {
+                        event = __all_sync(0xffffffffu, mbar_try_cluster(c.bar(BAR_EVENT), events & 1, 500)) != 0;
+                        if (event || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
+                        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > p.wait_limit_ns)) {
+                            c.fail(kStatusTimeout);
+                            break;
+                        }
+                    }
+                    __syncwarp();
+                    if (!event) {
+                        load_q(parity);
+                        q_loaded = true;
+                        continue;
+                    }
+                } else {
+                    c.wait(BAR_EVENT, events & 1);
+                }
+            }
+            const uint32_t event = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffEvent);
+            ++events;
+            if (event == 0u || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
+            // Tile event - 1 moved references: rescale O after the product before it.
+            const uint32_t at = event - 1;
+            c.wait(BAR_PVDONE0 + ((at - 1) & 1), ((at - 1) >> 1) & 1);
+            tc_fence_after();
+            const volatile uint32_t* flags = reinterpret_cast<const volatile uint32_t*>(c.smem + kOffFlags) + (at & 1) * 8;
+            const float* alpha = reinterpret_cast<const float*>(c.smem + kOffAlpha) + (at & 1) * kPairs;
+#pragma unroll 1
+            for (int b = 0; b < kPairs / 32; ++b) {  // 32 pairs of two lane quarters
+                if (flags[2 * b] != event && flags[2 * b + 1] != event) continue;
+                const uint32_t ta = c.tmem + lane_base + kTmemO + b * 32;
+                uint32_t o0[32], o1[32];
+                tmem_ld_2x32(ta, ta + kPairs, o0, o1);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float f = alpha[b * 32 + i];
+                    o0[i] = __float_as_uint(__uint_as_float(o0[i]) * f);
+                    o1[i] = __float_as_uint(__uint_as_float(o1[i]) * f);
+                }
+                tmem_st_x32(ta, o0);
+                tmem_st_x32(ta + kPairs, o1);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) c.arrive(BAR_OFREE, 0);
+        }
+        // After an abort the other roles are let go without results.
+        if (!q_loaded) {
+            while (!s.last && step < kPrepSteps) prepare(c, next.u, (units + 1) & 1, step, images + static_cast<int64_t>((units + 1) & 1) * kQImageBytes), ++step;
+            if (!s.last && step == kPrepSteps) find_broken(c, next, (units + 1) & 1);
+            c.wait(BAR_QEMPTY, units & 1);
+            load_q((units + 1) & 1);
+        }
+
+        // ---- output of the unit ----
+        c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
+        c.wait(BAR_FFULL, units & 1);
+        tc_fence_after();
+        const float* f_s = reinterpret_cast<const float*>(c.smem + kOffF);
+        const bool whole = s.part < 0;
+#pragma unroll 1
+        for (int g = 0; g < 2 * kPairs / 32; ++g) {
+            const int mc = g >> 2, col0 = (g & 3) * 32;
+            const int dim0 = static_cast<int>(c.rank) * kDims + mc * 128 + q4 * 32;
+            uint32_t v[32];
+            tmem_ld_x32(c.tmem + lane_base + kTmemO + mc * kPairs + col0, v);
+            if (whole) {
+                // Neighbouring lanes exchange pairs and dims, so that a store has two dims of a pair.
+                const int odd = lane & 1;
+                uint16_t* at = p.out + (s.u.pair0 + col0 + odd) * kLatent + dim0 + (lane & ~1);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float a = __uint_as_float(v[i]) * f_s[col0 + i], b = __uint_as_float(v[i + 1]) * f_s[col0 + i + 1];
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    const __nv_bfloat162 r = odd ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
+                    if (col0 + i + odd < s.u.valid) *reinterpret_cast<__nv_bfloat162*>(at + i * kLatent) = r;
+                }
+            } else {
+                uint16_t* part = p.part_o + static_cast<int64_t>(s.part) * kPairs * kLatent;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 hv = __floats2half2_rn(__uint_as_float(v[i + 2 * e]) * f_s[col0 + i + 2 * e],
+                                                             __uint_as_float(v[i + 2 * e + 1]) * f_s[col0 + i + 2 * e + 1]);
+                        h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                    }
+                    *reinterpret_cast<uint4*>(part + ((static_cast<int64_t>(dim0 / 32) * (kPairs / 8) + (col0 + i) / 8) * 32 + lane) * 8) =
+                        make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) c.arrive(BAR_OFREE, 0);
+        if (lane < 2) c.arrive(BAR_FEMPTY, lane);
+        if (s.last) break;
+    }
+}
+
+template <bool kTma>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap kmap,
+                                                              const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5;
+    Cta c{p, smem, smem_u32(smem), cluster_rank(), blockIdx.x >> 1, reinterpret_cast<volatile int*>(smem + kOffAbort)};
+
+    if (tid == 0) {
+        for (int e = 0; e < kSlots; ++e) {
+            mbar_init(c.bar(BAR_KFULL0 + e), kTma ? 1 : 32);
+            mbar_init(c.bar(BAR_VFULL0 + e), kTma ? 1 : 32);
+            mbar_init(c.bar(BAR_KPEER0 + e), 1);
+            mbar_init(c.bar(BAR_KEMPTY0 + e), 1);
+            mbar_init(c.bar(BAR_VEMPTY0 + e), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(c.bar(BAR_PFULL0 + i), 2 * kSoftmaxWarps);
+            mbar_init(c.bar(BAR_PVDONE0 + i), 1);
+        }
+        mbar_init(c.bar(BAR_SFULL), 1);
+        mbar_init(c.bar(BAR_SEMPTY), 2 * kSoftmaxWarps);
+        mbar_init(c.bar(BAR_QFULL), 2 * kEpilogueWarps);
+        mbar_init(c.bar(BAR_QEMPTY), 1);
+        mbar_init(c.bar(BAR_EVENT), 1);
+        mbar_init(c.bar(BAR_OFREE), 2 * kEpilogueWarps);
+        mbar_init(c.bar(BAR_FFULL), kSoftmaxWarps);  // the first token half's, of both CTAs
+        mbar_init(c.bar(BAR_FEMPTY), 2 * kEpilogueWarps);
+        mbar_init(c.bar(BAR_DRAIN), 2);
+        for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(smem + kOffFlags)[i] = 0;
+        *c.abort_flag = 0;
+        fence_mbar_init();
+        if (kTma) {
+            prefetch_tmap(&kmap);
+            prefetch_tmap(&vmap);
+        }
+    }
+    if (warp == 2) {
+        tmem_alloc_pair(c.sbase + kOffTmem, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
     __syncthreads();
-    const int32_t seq = seq_s, h = blockIdx.y * (kThreads / 32) + warp;
-    if (seq >= p.num_seqs || h >= p.heads) return;
-    int64_t len = static_cast<int64_t>(max(p.base_lens[seq], 0)) + row_s + 1;
-    const int64_t room = p.max_blocks_per_seq > 0 ? static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size : INT32_MAX - 256;
-    if (len > room) {
-        len = room;
-        if (lane == 0) report(p);
-    }
-    const int64_t at = (row * p.heads + h) * kLatent + lane * 16;
-    float q[16], o[16] = {};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __uint_as_float(static_cast<uint32_t>(p.q[at + i]) << 16);
-    float m = -INFINITY, l = 0.0f;
-    for (int32_t j = 0; j < len; ++j) {
-        const uint32_t blk = divide(j, p.by_block);
-        const int32_t page = p.block_tables[static_cast<int64_t>(seq) * p.max_blocks_per_seq + blk];
-        uint4 kc = make_uint4(0, 0, 0, 0), vc = kc;
-        if (page >= 0) {
-            const int64_t off = page * p.cache_stride + static_cast<int64_t>(j - blk * p.block_size) * kLatent + lane * 16;
-            kc = *reinterpret_cast<const uint4*>(p.k_cache + off);
-            vc = *reinterpret_cast<const uint4*>(p.v_cache + off);
-        } else if (lane == 0) {
-            report(p);
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    c.tmem = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
+    // Everything above overlaps the plan; it is read only after this.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    c.begin = p.starts[c.cluster].begin;
+    c.end = p.starts[c.cluster].end;
+    c.gap = p.starts[c.cluster].gap;
+    if ((c.sbase & 1023u) != 0u) {  // the swizzled operands count on it
+        if (tid == 0) report(p, DSA_ERR_UNSUPPORTED);
+    } else if (c.begin < c.end) {
+        if (warp == 0) {
+            if constexpr (kTma) run_load_tma<false>(c, &kmap);
+            else run_load_copies<false>(c);
+        } else if (warp == 1) {
+            if constexpr (kTma) run_load_tma<true>(c, &vmap);
+            else run_load_copies<true>(c);
+        } else if (warp < kSoftmax0) {
+            if (c.rank == 0) {
+                if (warp == 2) run_qk(c);
+                else run_pv(c);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(c.bar(BAR_DRAIN), 0) && globaltimer_ns() - t0 < kDrainLimitNs) {
+                }
+                __syncwarp();
+            } else if (warp == 2) {
+                run_forward(c);
+            }
+        } else if (warp < kEpilogue0) {
+            run_softmax(c);
+        } else {
+            run_epilogue(c);
         }
-        float k[16], dot = 0.0f;
-        decode16(kc, k);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) dot = fmaf(q[i], k[i], dot);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-        const float s = dot * p.score_scale, top = fmaxf(m, s);
-        const float a = exp2f(m - top), e = exp2f(s - top);
-        m = top;
-        l = fmaf(l, a, e);
-        decode16(vc, k);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fmaf(o[i], a, e * k[i]);
     }
-    const float f = p.v_scale / l;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(len > 0 ? o[i] * f : 0.0f);
-        p.out[at + i] = __bfloat16_as_ushort(b);
+    tc_fence_before();
+    __syncthreads();
+    // Neither CTA leaves while the other may still reach into it.
+    cluster_arrive();
+    cluster_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(c.tmem, kTmemCols);
     }
+}
+
+template <bool kTma>
+cudaError_t setup() {
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaFuncGetAttributes(&attr, prefill_kernel<kTma>);
+    if (e != cudaSuccess) return e;
+    if (attr.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(prefill_kernel<kTma>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(prefill_kernel<kTma>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
 }
 
 }  // namespace
 }  // namespace prefill
 
-cudaError_t launch_prefill(const prefill::Params& p, cudaStream_t stream) {
-    cudaError_t e = cudaMemsetAsync(p.status, 0, 4, stream);
-    if (e != cudaSuccess) return e;
-    const dim3 grid(p.max_rows, (p.heads + prefill::kThreads / 32 - 1) / (prefill::kThreads / 32));
-    prefill::prefill_kernel<<<grid, prefill::kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t prefill_setup() {
+    const cudaError_t e = prefill::setup<true>();
+    return e != cudaSuccess ? e : prefill::setup<false>();
+}
+
+cudaError_t launch_prefill(const prefill::Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * p.clusters);
+    cfg.blockDim = dim3(prefill::kThreads);
+    cfg.dynamicSmemBytes = prefill::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return p.box_rows > 0 ? cudaLaunchKernelEx(&cfg, prefill::prefill_kernel<true>, p, kmap, vmap)
+                          : cudaLaunchKernelEx(&cfg, prefill::prefill_kernel<false>, p, kmap, vmap);
 }
 
 }  // namespace dsa
