@@ -129,9 +129,10 @@ struct Cta {
         st_cluster(map_rank(sbase + kOffAbort, rank ^ 1u), 1u);
     }
     __device__ void wait(int b, uint32_t parity) const {
-        if (!mbar_wait_cluster(bar(b), parity, abort_flag, p.wait_limit_ns)) fail(kStatusTimeout);
+        if (!mbar_wait(bar(b), parity, abort_flag, p.wait_limit_ns)) fail(kStatusTimeout);
         __syncwarp();
     }
+    // Says nothing of shared memory that the other CTA's threads have written (fence_cluster).
     __device__ void arrive(int b, uint32_t to) const { mbar_arrive_cluster(map_rank(bar(b), to)); }
 
     __device__ Segment segment(int32_t k, const Unit& u, bool first) const {
@@ -324,7 +325,9 @@ __device__ void run_pv(const Cta& c) {
     // Has the epilogue warps of both CTAs do what `event` says.
     auto post = [&](uint32_t event) {
         if (lane < 2) {
+            fence_cluster();  // with the factors and marks that this warp has found
             st_cluster(map_rank(c.sbase + kOffEvent, lane), event);
+            fence_cluster();
             c.arrive(BAR_EVENT, lane);
         }
         __syncwarp();
@@ -423,8 +426,8 @@ __device__ void run_softmax(const Cta& c) {
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
                 uint32_t a[16], b[16];
-                tmem_ld_x16(c.tmem + lane_base + kTmemS + half * kHalfCols + 16 * part, a);
-                tmem_ld_x16(c.tmem + lane_base + kTmemS + half * kHalfCols + kScores + 16 * part, b);
+                const uint32_t at = c.tmem + lane_base + kTmemS + half * kHalfCols + 16 * part;
+                tmem_ld_2x16(at, at + kScores, a, b);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float send = __uint_as_float(term ? a[j] : b[j]);
@@ -540,6 +543,7 @@ __device__ void run_softmax(const Cta& c) {
                     st_cluster(to + kOffAlpha + ((tau & 1) * kPairs + pair) * 4, __float_as_uint(alpha));
                     if (lane < 2 && changed != 0u)
                         st_cluster(to + kOffFlags + (((tau & 1) * 2 + c.rank) * 4 + q4) * 4, tau + 1);
+                    fence_cluster();
                     __syncwarp();
                 }
                 // Also keeps the next tile's maxima from overwriting these.
@@ -571,6 +575,7 @@ __device__ void run_softmax(const Cta& c) {
             const bool whole = s.part < 0;
             const float f = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
             st_cluster(map_rank(c.sbase, term) + kOffF + pair * 4, __float_as_uint(f));
+            fence_cluster();
             if (!whole && term == 0) p.part_lse[s.part * kPairs + pair] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
             __syncwarp();
             if (lane < 2) c.arrive(BAR_FFULL, lane);
@@ -694,7 +699,7 @@ __device__ void run_epilogue(const Cta& c) {
         __syncwarp();
         if (lane == 0) c.arrive(BAR_QFULL, 0);
     };
-    auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_cluster(c.bar(b), parity)) != 0; };
+    auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(c.bar(b), parity)) != 0; };
 
     Segment next = c.first();
     for (int step = 0; step < kPrepSteps; ++step) prepare(c, next.u, 0, step, images);
@@ -723,7 +728,7 @@ __device__ void run_epilogue(const Cta& c) {
                     const uint64_t t0 = globaltimer_ns();
                     bool event = false;
                     while (!ready(BAR_QEMPTY, units & 1)) {
-                        event = __all_sync(0xffffffffu, mbar_try_cluster(c.bar(BAR_EVENT), events & 1, 500)) != 0;
+                        event = __all_sync(0xffffffffu, mbar_try_wait_hint(c.bar(BAR_EVENT), events & 1, 500)) != 0;
                         if (event || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
                         if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > p.wait_limit_ns)) {
                             c.fail(kStatusTimeout);
@@ -740,6 +745,7 @@ __device__ void run_epilogue(const Cta& c) {
                     c.wait(BAR_EVENT, events & 1);
                 }
             }
+            fence_cluster();
             const uint32_t event = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffEvent);
             ++events;
             if (event == 0u || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
@@ -780,6 +786,7 @@ __device__ void run_epilogue(const Cta& c) {
         // ---- output of the unit ----
         c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
         c.wait(BAR_FFULL, units & 1);
+        fence_cluster();
         tc_fence_after();
         const float* f_s = reinterpret_cast<const float*>(c.smem + kOffF);
         const bool whole = s.part < 0;
