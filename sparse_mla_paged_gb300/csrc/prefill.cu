@@ -20,8 +20,8 @@
 //                when pages and tiles fit each other, else 16-byte copies
 //   warp 2, 3    issue Q K^T and P V (rank 0); tell rank 0 of the loaded K tiles (rank 1)
 //   warps 4-11   softmax, two per TMEM lane quarter
-//   warps 12-15  rescale O when a reference moves, write a unit's output, make the query operand of
-//                the next unit
+//   warps 12-15  rescale O when a reference moves, write a unit's output
+//   warps 16-19  make the next unit's query operand and put it in place
 //
 // A reference that moves in one CTA rescales columns of O in both. The CTA that asks writes the
 // factors into both; the warp that issues P V finds its mark before the tile's product, has
@@ -54,13 +54,15 @@ constexpr int kVGroup = 8 * kDims;
 constexpr int kSoftmax0 = 4, kSoftmaxWarps = 8;
 constexpr int kEpilogue0 = 12, kEpilogueWarps = 4;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kThreads = (kEpilogue0 + kEpilogueWarps) * 32;
+constexpr int kQuery0 = 16, kQueryWarps = 4;
+constexpr int kThreads = (kQuery0 + kQueryWarps) * 32;
 constexpr int kHalfCols = kTile / 2;                // S columns per softmax warp
 static_assert(kScores == kHalfCols / 2, "scores per softmax thread: 32, one bit each of a word");
 constexpr int kPTermBytes = kCtaPairs * kTile;
 
 constexpr int kBarSoftmax = 1;
 constexpr int kBarPair0 = 2;  // 2..5: the two softmax warps of a lane quarter
+constexpr int kBarFirst = 6;  // the first unit's query operand is made
 
 constexpr int kOffV = kSlots * kSlotBytes;
 constexpr int kOffP = 2 * kSlots * kSlotBytes;               // P' [2 buffers][hi, lo]
@@ -91,7 +93,8 @@ enum {
     BAR_OFREE,                         // (0) they did it
     BAR_FFULL,                         // (both) output factors written
     BAR_FEMPTY,                        // (both) and used
-    BAR_DRAIN,                         // (0) every MMA is done
+    BAR_UDONE0,                        // 2: the softmax warps are done with a unit (by its parity)
+    BAR_DRAIN = BAR_UDONE0 + 2,        // (0) every MMA is done
     kNumBars
 };
 constexpr int kSmem = kOffBars + kNumBars * 8;
@@ -148,11 +151,22 @@ struct Cta {
         s.last = e + gap >= end;
         return s;
     }
-    __device__ Segment first() const {
-        const Start& st = p.starts[cluster];
-        return segment(st.k, st.unit, true);
+};
+
+// A role's way through its cluster's units; the next one's record is asked for a unit ahead.
+struct Walk {
+    const Cta& c;
+    Segment s;
+    Unit ahead;
+    __device__ explicit Walk(const Cta& cta) : c(cta) {
+        const Start& st = c.p.starts[c.cluster];
+        s = c.segment(st.k, st.unit, true);
+        ahead = c.p.units[s.k + 1];
     }
-    __device__ Segment next(const Segment& s) const { return segment(s.k + 1, p.units[s.k + 1], false); }
+    __device__ void advance() {
+        s = c.segment(s.k + 1, ahead, false);
+        ahead = c.p.units[s.k + 1];
+    }
 };
 
 // Page of the block that holds position pos (negative: the caller reports it), and its row there.
@@ -186,7 +200,8 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
     const bool have = lane * p.box_rows < kTokens;  // a box of this lane's in every tile
     uint32_t tau = 0;
     bool stop = false;
-    for (Segment s = c.first(); !stop; s = c.next(s)) {
+    for (Walk w(c); !stop; w.advance()) {
+        const Segment& s = w.s;
         // This lane's page of tile t (requested a tile ahead), its first row there, and whether any
         // row of the unit sees the box.
         auto look = [&](int32_t t, int32_t* row, bool* live) {
@@ -243,7 +258,8 @@ __device__ void run_load_copies(const Cta& c) {
     const uint32_t ring = c.sbase + (kValues ? kOffV : 0) + (piece >> 3) * 1024;
     const int32_t pos0 = lane + (kValues ? 0 : static_cast<int32_t>(c.rank) * kKeyTokens);
     uint32_t tau = 0;
-    for (Segment s = c.first();; s = c.next(s)) {
+    for (Walk w(c);; w.advance()) {
+        const Segment& s = w.s;
         int32_t row_next[kEach], page_next[kEach];
         // Pages and rows there (row -1: no token). What is made of them is left to the next tile:
         // using a page here would wait for its load.
@@ -291,7 +307,8 @@ __device__ void run_qk(const Cta& c) {
     const uint32_t idesc = idesc_e4m3(256, kTile, false, false);
     const uint32_t el = elect_one();
     uint32_t tau = 0, units = 0;
-    for (Segment s = c.first();; s = c.next(s)) {
+    for (Walk w(c);; w.advance()) {
+        const Segment& s = w.s;
         c.wait(BAR_QFULL, units++ & 1);
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             const int e = static_cast<int>(tau % kSlots);
@@ -325,15 +342,15 @@ __device__ void run_pv(const Cta& c) {
     // Has the epilogue warps of both CTAs do what `event` says.
     auto post = [&](uint32_t event) {
         if (lane < 2) {
-            fence_cluster();  // with the factors and marks that this warp has found
-            st_cluster(map_rank(c.sbase + kOffEvent, lane), event);
-            fence_cluster();
-            c.arrive(BAR_EVENT, lane);
+            const uint32_t bar = map_rank(c.bar(BAR_EVENT), lane);
+            mbar_arrive_expect_cluster(bar, 4);
+            st_async(map_rank(c.sbase + kOffEvent, lane), event, bar);
         }
         __syncwarp();
         ++events;
     };
-    for (Segment s = c.first();; s = c.next(s)) {
+    for (Walk w(c);; w.advance()) {
+        const Segment& s = w.s;
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             const int pb = tau & 1, e = static_cast<int>(tau % kSlots);
             c.wait(BAR_PFULL0 + pb, (tau >> 1) & 1);
@@ -374,7 +391,8 @@ __device__ void run_pv(const Cta& c) {
 __device__ void run_forward(const Cta& c) {
     const int lane = threadIdx.x & 31;
     uint32_t tau = 0;
-    for (Segment s = c.first();; s = c.next(s)) {
+    for (Walk w(c);; w.advance()) {
+        const Segment& s = w.s;
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             const int e = static_cast<int>(tau % kSlots);
             c.wait(BAR_KFULL0 + e, (tau / kSlots) & 1);
@@ -405,10 +423,8 @@ __device__ void run_softmax(const Cta& c) {
     uint32_t tau = 0, units = 0;
     bool pv_seen = false;  // the P.V two tiles back was already waited for
 
-    Segment next = c.first();
-    for (;; ++units) {
-        const Segment s = next;
-        if (!s.last) next = c.next(s);
+    for (Walk w(c);; w.advance(), ++units) {
+        const Segment& s = w.s;
         const int32_t len = pair < s.u.valid ? pair_len(p, s.u.base, s.u.first + pair) : 0;
         float qs = 0.0f;        // what turns dots into log2 scores, known with the first tile
         float m_ref = kNegInf;  // reference max of the pair (log2 units)
@@ -574,33 +590,31 @@ __device__ void run_softmax(const Cta& c) {
             const float l = hm_s[hq].x + hm_s[kCtaPairs + hq].x;
             const bool whole = s.part < 0;
             const float f = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
-            st_cluster(map_rank(c.sbase, term) + kOffF + pair * 4, __float_as_uint(f));
-            fence_cluster();
+            if (sw == 0 && lane == 0) mbar_arrive_expect_tx(c.bar(BAR_FFULL), kPairs * 4);
+            st_async(map_rank(c.sbase, term) + kOffF + pair * 4, __float_as_uint(f), map_rank(c.bar(BAR_FFULL), term));
             if (!whole && term == 0) p.part_lse[s.part * kPairs + pair] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
-            __syncwarp();
-            if (lane < 2) c.arrive(BAR_FFULL, lane);
         }
+        if (lane == 0) mbar_arrive(c.bar(BAR_UDONE0 + (units & 1)));
         named_bar_sync<kBarSoftmax, kSoftmaxThreads>();  // the sums are read
         if (s.last) break;
     }
 }
 
 // ------------------------------------------------------------------------------------
-// epilogue warps: O's rescales and output, query operands
+// query warps
 // ------------------------------------------------------------------------------------
-constexpr int kPrepPairs = 4;   // pairs of a step, their loads in flight together
-constexpr int kPrepSteps = kCtaPairs / kEpilogueWarps / kPrepPairs;
+constexpr int kPrepPairs = 4;   // pairs whose loads are in flight together
+static_assert((kSoftmaxWarps + kEpilogueWarps + kQueryWarps) * kPrepPairs == kCtaPairs, "the first unit's, a turn of all these warps");
 
-// Query operand rows of kPrepPairs of this warp's 16 pairs: lane l has dims [16l, 16l+16). A
+// Query operand rows of kPrepPairs pairs from h0 on: lane l has dims [16l, 16l+16). A
 // head's bf16 query becomes two E4M3 terms after a scaling by a power of two (exact for elements from
 // 2^-9 of its largest, smaller ones off by 2^-16 of it at most), rows 2k and 2k+1 the terms of pair
 // k, stored chunk-major. The scale of its dots is positive (maxima are taken of the dots): a
 // negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or an
 // infinity gets zero codes and a NaN scale (exponent 255), which makes all its scores NaN.
-__device__ void prepare(const Cta& c, const Unit& u, int parity, int step, uint8_t* img) {
+__device__ void prepare(const Cta& c, const Unit& u, int parity, int h0, uint8_t* img) {
     const Params& p = c.p;
-    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
-    const int h0 = 16 * q4 + kPrepPairs * step;
+    const int lane = threadIdx.x & 31;
     uint4 raw[kPrepPairs][2];
 #pragma unroll
     for (int i = 0; i < kPrepPairs; ++i) {
@@ -672,84 +686,71 @@ __device__ void find_broken(const Cta& c, const Segment& s, int parity) {
     __syncwarp();
 }
 
-__device__ void run_epilogue(const Cta& c) {
-    const Params& p = c.p;
-    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
-    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
-    uint8_t* images = p.qimg + static_cast<int64_t>(blockIdx.x) * 2 * kQImageBytes;
-    uint32_t tau = 0, units = 0, events = 0;
+__device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
+    return c.p.qimg + (static_cast<int64_t>(blockIdx.x) * 2 + parity) * kQImageBytes;
+}
+// The first unit's operand is made by all warps that have nothing to do yet.
+__device__ void prepare_first(const Cta& c) {
+    prepare(c, c.p.starts[c.cluster].unit, 0, ((threadIdx.x >> 5) - kSoftmax0) * kPrepPairs, query_image(c, 0));
+    named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
+}
 
-    auto load_q = [&](int parity) {
-        const uint4* src = reinterpret_cast<const uint4*>(images + static_cast<int64_t>(parity) * kQImageBytes + (q4 * 32 + lane) * 16);
+__device__ void run_query(const Cta& c) {
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ;
+    Walk w(c);
+    for (uint32_t units = 0;; ++units, w.advance()) {
+        const int parity = units & 1;
+        uint8_t* img = query_image(c, parity);
+        // The scales and marks of the unit before the last are read. (One barrier for both parities
+        // could pass two phases meanwhile.)
+        if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
+        if (units > 0) {
 #pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
-            uint32_t a[32];
+            for (int h = 0; h < kCtaPairs / kQueryWarps; h += kPrepPairs) prepare(c, w.s.u, parity, q4 * (kCtaPairs / kQueryWarps) + h, img);
+        }
+        find_broken(c, w.s, parity);
+        if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
+        const uint4* src = reinterpret_cast<const uint4*>(img + (q4 * 32 + lane) * 16);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            uint32_t a[2][32];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 v = __ldcg(src + (part * 8 + i) * (2048 / 16));
-                a[4 * i] = v.x;
-                a[4 * i + 1] = v.y;
-                a[4 * i + 2] = v.z;
-                a[4 * i + 3] = v.w;
+            for (int i = 0; i < 16; ++i) {
+                const uint4 v = __ldcg(src + (part * 16 + i) * (2048 / 16));
+                a[i >> 3][4 * (i & 7)] = v.x;
+                a[i >> 3][4 * (i & 7) + 1] = v.y;
+                a[i >> 3][4 * (i & 7) + 2] = v.z;
+                a[i >> 3][4 * (i & 7) + 3] = v.w;
             }
-            tmem_st_x32(c.tmem + lane_base + kTmemQ + part * 32, a);
+            tmem_st_x32(place + part * 64, a[0]);
+            tmem_st_x32(place + part * 64 + 32, a[1]);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) c.arrive(BAR_QFULL, 0);
-    };
-    auto ready = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(c.bar(b), parity)) != 0; };
+        if (w.s.last) break;
+    }
+}
 
-    Segment next = c.first();
-    for (int step = 0; step < kPrepSteps; ++step) prepare(c, next.u, 0, step, images);
-    find_broken(c, next, 0);
-    load_q(0);
-    for (;; ++units) {
-        const Segment s = next;
-        int step = 0;            // of the next unit's operand; past the last one it waits for its place
-        bool q_loaded = s.last;
-        if (!s.last) next = c.next(s);
+// ------------------------------------------------------------------------------------
+// epilogue warps: O's rescales and output
+// ------------------------------------------------------------------------------------
+__device__ void run_epilogue(const Cta& c) {
+    const Params& p = c.p;
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
+    uint32_t tau = 0, units = 0, events = 0;
+    for (Walk w(c);; w.advance(), ++units) {
+        const Segment& s = w.s;
         tau += s.t1 - s.t0;
         for (;;) {
-            if (!ready(BAR_EVENT, events & 1)) {
-                const int parity = (units + 1) & 1;
-                if (!s.last && step < kPrepSteps) {
-                    prepare(c, next.u, parity, step++, images + static_cast<int64_t>(parity) * kQImageBytes);
-                    continue;
-                }
-                if (!s.last && step == kPrepSteps) {
-                    find_broken(c, next, parity);
-                    ++step;
-                    continue;
-                }
-                if (!q_loaded) {
-                    // The operand's place is free before the unit's last event.
-                    const uint64_t t0 = globaltimer_ns();
-                    bool event = false;
-                    while (!ready(BAR_QEMPTY, units & 1)) {
-                        event = __all_sync(0xffffffffu, mbar_try_wait_hint(c.bar(BAR_EVENT), events & 1, 500)) != 0;
-                        if (event || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
-                        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > p.wait_limit_ns)) {
-                            c.fail(kStatusTimeout);
-                            break;
-                        }
-                    }
-                    __syncwarp();
-                    if (!event) {
-                        load_q(parity);
-                        q_loaded = true;
-                        continue;
-                    }
-                } else {
-                    c.wait(BAR_EVENT, events & 1);
-                }
-            }
-            fence_cluster();
+            c.wait(BAR_EVENT, events++ & 1);
             const uint32_t event = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffEvent);
-            ++events;
             if (event == 0u || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
             // Tile event - 1 moved references: rescale O after the product before it.
+            fence_cluster();
             const uint32_t at = event - 1;
             c.wait(BAR_PVDONE0 + ((at - 1) & 1), ((at - 1) >> 1) & 1);
             tc_fence_after();
@@ -775,18 +776,10 @@ __device__ void run_epilogue(const Cta& c) {
             __syncwarp();
             if (lane == 0) c.arrive(BAR_OFREE, 0);
         }
-        // After an abort the other roles are let go without results.
-        if (!q_loaded) {
-            while (!s.last && step < kPrepSteps) prepare(c, next.u, (units + 1) & 1, step, images + static_cast<int64_t>((units + 1) & 1) * kQImageBytes), ++step;
-            if (!s.last && step == kPrepSteps) find_broken(c, next, (units + 1) & 1);
-            c.wait(BAR_QEMPTY, units & 1);
-            load_q((units + 1) & 1);
-        }
 
         // ---- output of the unit ----
         c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
         c.wait(BAR_FFULL, units & 1);
-        fence_cluster();
         tc_fence_after();
         const float* f_s = reinterpret_cast<const float*>(c.smem + kOffF);
         const bool whole = s.part < 0;
@@ -849,14 +842,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) {
             mbar_init(c.bar(BAR_PFULL0 + i), 2 * kSoftmaxWarps);
             mbar_init(c.bar(BAR_PVDONE0 + i), 1);
+            mbar_init(c.bar(BAR_UDONE0 + i), kSoftmaxWarps);
         }
         mbar_init(c.bar(BAR_SFULL), 1);
         mbar_init(c.bar(BAR_SEMPTY), 2 * kSoftmaxWarps);
-        mbar_init(c.bar(BAR_QFULL), 2 * kEpilogueWarps);
+        mbar_init(c.bar(BAR_QFULL), 2 * kQueryWarps);
         mbar_init(c.bar(BAR_QEMPTY), 1);
         mbar_init(c.bar(BAR_EVENT), 1);
         mbar_init(c.bar(BAR_OFREE), 2 * kEpilogueWarps);
-        mbar_init(c.bar(BAR_FFULL), kSoftmaxWarps);  // the first token half's, of both CTAs
+        mbar_init(c.bar(BAR_FFULL), 1);  // and the factors' bytes
         mbar_init(c.bar(BAR_FEMPTY), 2 * kEpilogueWarps);
         mbar_init(c.bar(BAR_DRAIN), 2);
         for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(smem + kOffFlags)[i] = 0;
@@ -903,9 +897,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 run_forward(c);
             }
         } else if (warp < kEpilogue0) {
+            prepare_first(c);
             run_softmax(c);
-        } else {
+        } else if (warp < kQuery0) {
+            prepare_first(c);
             run_epilogue(c);
+        } else {
+            prepare_first(c);
+            run_query(c);
         }
     }
     tc_fence_before();

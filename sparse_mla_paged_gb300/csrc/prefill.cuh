@@ -16,7 +16,7 @@ namespace prefill {
 
 constexpr int kPairs = 128;  // (row, head) pairs of a unit, 64 in each CTA of a cluster
 constexpr int kTile = full::kTile;
-constexpr int kGap = 2;      // tiles that a unit change costs, at most a quarter of a range
+constexpr int kGap = 3;      // tiles that a unit change costs, at most a quarter of a range
 
 struct alignas(16) Unit {
     int64_t start;  // its first tile on the line
@@ -49,7 +49,7 @@ inline Layout layout(int64_t units, int64_t clusters) {
     L.status = put(256);
     L.starts = put(static_cast<size_t>(clusters) * sizeof(Start));
     L.joins = put(static_cast<size_t>(clusters) * sizeof(Join));
-    L.units = put(static_cast<size_t>(units) * sizeof(Unit));
+    L.units = put(static_cast<size_t>(units + 1) * sizeof(Unit));  // read one ahead
     L.qimg = put(static_cast<size_t>(2 * 2 * clusters) * kQImageBytes);
     L.part_o = put(static_cast<size_t>(2 * clusters) * kPairs * kLatent * 2);
     L.part_lse = put(static_cast<size_t>(2 * clusters) * kPairs * 4);
