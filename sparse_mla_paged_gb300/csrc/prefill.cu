@@ -153,20 +153,20 @@ struct Cta {
     }
 };
 
-// A role's way through its cluster's units; the next one's record is asked for a unit ahead.
+// A role's way through its cluster's units; records are brought into L1 a unit or more ahead.
 struct Walk {
     const Cta& c;
     Segment s;
-    Unit ahead;
     __device__ explicit Walk(const Cta& cta) : c(cta) {
         const Start& st = c.p.starts[c.cluster];
         s = c.segment(st.k, st.unit, true);
-        ahead = c.p.units[s.k + 1];
+        prefetch();
     }
     __device__ void advance() {
-        s = c.segment(s.k + 1, ahead, false);
-        ahead = c.p.units[s.k + 1];
+        s = c.segment(s.k + 1, c.p.units[s.k + 1], false);
+        prefetch();
     }
+    __device__ void prefetch() const { asm volatile("prefetch.global.L1 [%0];" ::"l"(c.p.units + s.k + 1)); }
 };
 
 // Page of the block that holds position pos (negative: the caller reports it), and its row there.
@@ -466,29 +466,34 @@ __device__ void run_softmax(const Cta& c) {
             if ((t + 1) * kTile > s.min_len) {  // an edge tile
                 uint8_t* v_tile = c.smem + kOffV + v_slot * kSlotBytes;
                 const uint32_t* broken = reinterpret_cast<const uint32_t*>(c.smem + kOffBroken) + (units & 1) * 4;
-                auto is_broken = [&](int32_t pos) {
+                // 32 of those marks from position pos on.
+                auto marks = [&](int32_t pos) -> uint32_t {
                     const int32_t i = pos - s.min_len;
-                    return i >= 0 && i < kPairs && (broken[i >> 5] >> (i & 31) & 1u) != 0u;
+                    if (i <= -32 || i >= kPairs) return 0;
+                    const uint32_t lo = i >= 0 ? broken[i >> 5] : 0, hi = i < kPairs - 32 ? broken[(i + 32) >> 5] : 0;
+                    return __funnelshift_r(lo, hi, i & 31);
                 };
-                // This lane's token of the warp's sixteen: 128 of its dims here.
-                const int token = 16 * sw + (lane & 15);
-                const int32_t pos = t * kTile + token;
-                const bool clear = pos >= s.max_len || is_broken(pos);
-                if (__any_sync(0xffffffffu, clear)) {
+                // The warp's sixteen tokens: 256 of their dims are here, 8 lanes to 128 of them.
+                const int32_t pos0 = t * kTile + 16 * sw;
+                const uint32_t gone = (pos0 + 16 <= s.max_len ? 0u : ~0u << max(s.max_len - pos0, 0)) | marks(pos0);
+                if ((gone & 0xFFFFu) != 0u) {
                     c.wait(BAR_VFULL0 + v_slot, (tau / kSlots) & 1);
-                    if (clear) {
-                        uint4* at = reinterpret_cast<uint4*>(v_tile + (token >> 3) * kVGroup + (lane >> 4) * 1024 + (token & 7) * 128);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) at[i] = make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < 8; ++i) {
+                        const int token = (4 * i + (lane >> 3)) & 15, block = i >> 2;
+                        if (gone >> token & 1u)
+                            *reinterpret_cast<uint4*>(v_tile + ((16 * sw + token) >> 3) * kVGroup + block * 1024 + (token & 7) * 128 +
+                                                      (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
-                    __syncwarp();
                 }
-                const int32_t lim = len - t * kTile;
-                const uint32_t any = broken[0] | broken[1] | broken[2] | broken[3];
+                const int32_t lim = len - t * kTile - tok0;  // this thread's scores before it are seen
+                const uint32_t hidden = lim >= 32 ? 0u : lim <= 0 ? ~0u : ~0u << lim;
+                const uint32_t nan = marks(t * kTile + tok0) & ~hidden;
 #pragma unroll
-                for (int j = 0; j < kScores; ++j) {
-                    if (tok0 + j >= lim) x[j] = kNegInf;
-                    else if (any != 0u && is_broken(t * kTile + tok0 + j)) x[j] = __uint_as_float(0x7FC00000u);
+                for (int j = 0; j < kScores; ++j) x[j] = hidden >> j & 1u ? kNegInf : x[j];
+                if (__any_sync(0xffffffffu, nan != 0u)) {
+#pragma unroll
+                    for (int j = 0; j < kScores; ++j) x[j] = nan >> j & 1u ? __uint_as_float(0x7FC00000u) : x[j];
                 }
             }
             float hm4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
@@ -606,30 +611,47 @@ __device__ void run_softmax(const Cta& c) {
 constexpr int kPrepPairs = 4;   // pairs whose loads are in flight together
 static_assert((kSoftmaxWarps + kEpilogueWarps + kQueryWarps) * kPrepPairs == kCtaPairs, "the first unit's, a turn of all these warps");
 
-// Query operand rows of kPrepPairs pairs from h0 on: lane l has dims [16l, 16l+16). A
+// Query operand rows of a warp's kPrepPairs or more pairs: lane l has dims [16l, 16l+16). A
 // head's bf16 query becomes two E4M3 terms after a scaling by a power of two (exact for elements from
 // 2^-9 of its largest, smaller ones off by 2^-16 of it at most), rows 2k and 2k+1 the terms of pair
 // k, stored chunk-major. The scale of its dots is positive (maxima are taken of the dots): a
 // negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or an
 // infinity gets zero codes and a NaN scale (exponent 255), which makes all its scores NaN.
-__device__ void prepare(const Cta& c, const Unit& u, int parity, int h0, uint8_t* img) {
+// The loop over pairs stays rolled: unrolled, its code is fetched anew for each unit, which took
+// longer than all else here (18700 against TIMED cycles for 16 pairs).
+struct Query {
+    uint4 a, b;
+};
+__device__ __forceinline__ Query ask_query(const Cta& c, const Unit& u, int h) {
+    const int pair = static_cast<int>(c.rank) * kCtaPairs + h;
+    Query x{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (pair < u.valid) {
+        const uint4* src = reinterpret_cast<const uint4*>(c.p.q + (u.pair0 + pair) * kLatent + (threadIdx.x & 31) * 16);
+        x.a = __ldcs(src);
+        x.b = __ldcs(src + 1);
+    }
+    return x;
+}
+struct Ahead {  // pairs whose loads are in flight
+    Query x[kPrepPairs];
+};
+__device__ __forceinline__ Ahead ask_queries(const Cta& c, const Unit& u, int h0) {
+    Ahead q;
+#pragma unroll
+    for (int i = 0; i < kPrepPairs; ++i) q.x[i] = ask_query(c, u, h0 + i);
+    return q;
+}
+__device__ __forceinline__ void make_operand(const Cta& c, const Unit& u, Ahead q, int parity, int h0, int count, uint8_t* img) {
     const Params& p = c.p;
     const int lane = threadIdx.x & 31;
-    uint4 raw[kPrepPairs][2];
-#pragma unroll
-    for (int i = 0; i < kPrepPairs; ++i) {
-        const int pair = static_cast<int>(c.rank) * kCtaPairs + h0 + i;
-        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-        if (pair < u.valid) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (u.pair0 + pair) * kLatent + lane * 16);
-            raw[i][0] = src[0];
-            raw[i][1] = src[1];
-        }
-    }
     const float sign = p.score_scale > 0.0f ? 1.0f : (p.score_scale < 0.0f ? -1.0f : 0.0f);
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        const Query x = q.x[0];
 #pragma unroll
-    for (int i = 0; i < kPrepPairs; ++i) {
-        const uint32_t w[8] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w, raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w};
+        for (int k = 1; k < kPrepPairs; ++k) q.x[k - 1] = q.x[k];
+        if (i + kPrepPairs < count) q.x[kPrepPairs - 1] = ask_query(c, u, h0 + i + kPrepPairs);
+        const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
         uint32_t amax = 0;  // magnitudes as bits: NaN and infinity are the largest
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
@@ -653,9 +675,10 @@ __device__ void prepare(const Cta& c, const Unit& u, int parity, int h0, uint8_t
             hi[k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
             lo[k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
         }
-        uint4* at = reinterpret_cast<uint4*>(img + lane * 2048 + 2 * (h0 + i) * 16);
-        __stcg(at, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        __stcg(at + 1, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+        // both rows' 16 bytes, one sector
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(img + lane * 2048 + 2 * (h0 + i) * 16), "r"(hi[0]),
+                     "r"(hi[1]), "r"(hi[2]), "r"(hi[3]), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                     : "memory");
         if (lane == 0) c.smem[kOffScale + parity * kCtaPairs + h0 + i] = broken ? 255 : static_cast<uint8_t>(127 - e);
     }
     __syncwarp();
@@ -691,12 +714,15 @@ __device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
 }
 // The first unit's operand is made by all warps that have nothing to do yet.
 __device__ void prepare_first(const Cta& c) {
-    prepare(c, c.p.starts[c.cluster].unit, 0, ((threadIdx.x >> 5) - kSoftmax0) * kPrepPairs, query_image(c, 0));
+    const int h0 = ((threadIdx.x >> 5) - kSoftmax0) * kPrepPairs;
+    const Unit& u = c.p.starts[c.cluster].unit;
+    make_operand(c, u, ask_queries(c, u, h0), 0, h0, kPrepPairs, query_image(c, 0));
     named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
 }
 
 __device__ void run_query(const Cta& c) {
     const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    constexpr int kOwn = kCtaPairs / kQueryWarps;  // pairs of a warp
     const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ;
     Walk w(c);
     for (uint32_t units = 0;; ++units, w.advance()) {
@@ -704,11 +730,10 @@ __device__ void run_query(const Cta& c) {
         uint8_t* img = query_image(c, parity);
         // The scales and marks of the unit before the last are read. (One barrier for both parities
         // could pass two phases meanwhile.)
+        Ahead x{};
+        if (units > 0) x = ask_queries(c, w.s.u, q4 * kOwn);
         if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
-        if (units > 0) {
-#pragma unroll 1
-            for (int h = 0; h < kCtaPairs / kQueryWarps; h += kPrepPairs) prepare(c, w.s.u, parity, q4 * (kCtaPairs / kQueryWarps) + h, img);
-        }
+        if (units > 0) make_operand(c, w.s.u, x, parity, q4 * kOwn, kOwn, img);
         find_broken(c, w.s, parity);
         if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
         const uint4* src = reinterpret_cast<const uint4*>(img + (q4 * 32 + lane) * 16);
@@ -784,36 +809,42 @@ __device__ void run_epilogue(const Cta& c) {
         const float* f_s = reinterpret_cast<const float*>(c.smem + kOffF);
         const bool whole = s.part < 0;
 #pragma unroll 1
-        for (int g = 0; g < 2 * kPairs / 32; ++g) {
-            const int mc = g >> 2, col0 = (g & 3) * 32;
-            const int dim0 = static_cast<int>(c.rank) * kDims + mc * 128 + q4 * 32;
-            uint32_t v[32];
-            tmem_ld_x32(c.tmem + lane_base + kTmemO + mc * kPairs + col0, v);
+        for (int g = 0; g < kPairs / 32; ++g) {
+            uint32_t v[2][32];  // of both blocks of 128 dims
+            tmem_ld_2x32(c.tmem + lane_base + kTmemO + 32 * g, c.tmem + lane_base + kTmemO + kPairs + 32 * g, v[0], v[1]);
+            const int dim0 = static_cast<int>(c.rank) * kDims + q4 * 32;
             if (whole) {
                 // Neighbouring lanes exchange pairs and dims, so that a store has two dims of a pair.
                 const int odd = lane & 1;
-                uint16_t* at = p.out + (s.u.pair0 + col0 + odd) * kLatent + dim0 + (lane & ~1);
+                uint16_t* at = p.out + (s.u.pair0 + 32 * g + odd) * kLatent + dim0 + (lane & ~1);
+                const int left = s.u.valid - 32 * g - odd;
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const float a = __uint_as_float(v[i]) * f_s[col0 + i], b = __uint_as_float(v[i + 1]) * f_s[col0 + i + 1];
-                    const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                    const __nv_bfloat162 r = odd ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-                    if (col0 + i + odd < s.u.valid) *reinterpret_cast<__nv_bfloat162*>(at + i * kLatent) = r;
+                    const float2 f = *reinterpret_cast<const float2*>(f_s + 32 * g + i);
+#pragma unroll
+                    for (int mc = 0; mc < 2; ++mc) {
+                        const float a = __uint_as_float(v[mc][i]) * f.x, b = __uint_as_float(v[mc][i + 1]) * f.y;
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                        const __nv_bfloat162 r = odd ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
+                        if (i < left) *reinterpret_cast<__nv_bfloat162*>(at + i * kLatent + mc * 128) = r;
+                    }
                 }
             } else {
                 uint16_t* part = p.part_o + static_cast<int64_t>(s.part) * kPairs * kLatent;
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t h[4];
+                for (int mc = 0; mc < 2; ++mc)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 hv = __floats2half2_rn(__uint_as_float(v[i + 2 * e]) * f_s[col0 + i + 2 * e],
-                                                             __uint_as_float(v[i + 2 * e + 1]) * f_s[col0 + i + 2 * e + 1]);
-                        h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = *reinterpret_cast<const float2*>(f_s + 32 * g + i + 2 * e);
+                            const __half2 hv = __floats2half2_rn(__uint_as_float(v[mc][i + 2 * e]) * f.x, __uint_as_float(v[mc][i + 2 * e + 1]) * f.y);
+                            h[e] = *reinterpret_cast<const uint32_t*>(&hv);
+                        }
+                        *reinterpret_cast<uint4*>(part + ((static_cast<int64_t>(dim0 / 32 + 4 * mc) * (kPairs / 8) + 4 * g + i / 8) * 32 + lane) * 8) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
                     }
-                    *reinterpret_cast<uint4*>(part + ((static_cast<int64_t>(dim0 / 32) * (kPairs / 8) + (col0 + i) / 8) * 32 + lane) * 8) =
-                        make_uint4(h[0], h[1], h[2], h[3]);
-                }
             }
         }
         tc_fence_before();
