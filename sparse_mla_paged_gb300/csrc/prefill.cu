@@ -642,51 +642,72 @@ __device__ __forceinline__ Ahead ask_queries(const Cta& c, const Unit& u, int h0
     return q;
 }
 __device__ __forceinline__ void make_operand(const Cta& c, const Unit& u, Ahead q, int parity, int h0, int count, uint8_t* img) {
+    constexpr int kTurn = 2;  // pairs side by side: one's instructions alone wait for one another
     const Params& p = c.p;
     const int lane = threadIdx.x & 31;
     const float sign = p.score_scale > 0.0f ? 1.0f : (p.score_scale < 0.0f ? -1.0f : 0.0f);
 #pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-        const Query x = q.x[0];
+    for (int i = 0; i < count; i += kTurn) {
+        uint32_t w[kTurn][8], amax[kTurn];
 #pragma unroll
-        for (int k = 1; k < kPrepPairs; ++k) q.x[k - 1] = q.x[k];
-        if (i + kPrepPairs < count) q.x[kPrepPairs - 1] = ask_query(c, u, h0 + i + kPrepPairs);
-        const uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
-        uint32_t amax = 0;  // magnitudes as bits: NaN and infinity are the largest
+        for (int j = 0; j < kTurn; ++j) {
+            const uint4 a = q.x[j].a, b = q.x[j].b;
+            const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            amax[j] = 0;  // magnitudes as bits: NaN and infinity are the largest
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
-        amax = __reduce_max_sync(0xffffffffu, amax);
-        const int E = static_cast<int>(amax >> 23);
-        const bool broken = E == 255;
-        int e = amax > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
-        e = e > 126 ? 126 : (e < -126 ? -126 : e);
-        const float sc = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * sign;
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float vh[4], vl[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint32_t bits = m & 1 ? w[2 * k + m / 2] & 0xFFFF0000u : w[2 * k + m / 2] << 16;
-                const float v = broken ? 0.0f : __uint_as_float(bits) * sc;
-                vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
-                vl[m] = v - vh[m];
+            for (int k = 0; k < 8; ++k) {
+                w[j][k] = v[k];
+                amax[j] = max(amax[j], max(v[k] << 16 & 0x7FFFFFFFu, v[k] & 0x7FFF0000u));
             }
-            hi[k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
-            lo[k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
         }
-        // both rows' 16 bytes, one sector
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(img + lane * 2048 + 2 * (h0 + i) * 16), "r"(hi[0]),
-                     "r"(hi[1]), "r"(hi[2]), "r"(hi[3]), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
-                     : "memory");
-        if (lane == 0) c.smem[kOffScale + parity * kCtaPairs + h0 + i] = broken ? 255 : static_cast<uint8_t>(127 - e);
+#pragma unroll
+        for (int k = kTurn; k < kPrepPairs; ++k) q.x[k - kTurn] = q.x[k];
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j)
+            if (i + kPrepPairs + j < count) q.x[kPrepPairs - kTurn + j] = ask_query(c, u, h0 + i + kPrepPairs + j);
+        float sc[kTurn];
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j) amax[j] = __reduce_max_sync(0xffffffffu, amax[j]);
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j) {
+            const int E = static_cast<int>(amax[j] >> 23);
+            int e = amax[j] > 0u ? 134 - E : 0;  // amax * 2^e in [128, 256)
+            e = e > 126 ? 126 : (e < -126 ? -126 : e);
+            sc[j] = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * sign;
+            if (E == 255) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[j][k] = 0;
+            }
+            if (lane == 0) c.smem[kOffScale + parity * kCtaPairs + h0 + i + j] = E == 255 ? 255 : static_cast<uint8_t>(127 - e);
+        }
+        uint32_t hi[kTurn][4], lo[kTurn][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < kTurn; ++j) {
+                float vh[4], vl[4];
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t two = w[j][2 * k + m / 2];
+                    const float v = __uint_as_float(m & 1 ? two & 0xFFFF0000u : two << 16) * sc[j];
+                    vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
+                    vl[m] = v - vh[m];
+                }
+                hi[j][k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
+                lo[j][k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
+            }
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j)  // both rows' 16 bytes, one sector
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(img + lane * 2048 + 2 * (h0 + i + j) * 16),
+                         "r"(hi[j][0]), "r"(hi[j][1]), "r"(hi[j][2]), "r"(hi[j][3]), "r"(lo[j][0]), "r"(lo[j][1]), "r"(lo[j][2]), "r"(lo[j][3])
+                         : "memory");
     }
     __syncwarp();
 }
 
 // Which of the tokens from the unit's shortest row on to its longest one's end hold a NaN code; both
 // CTAs find out for themselves. One word of 32 tokens per warp.
-__device__ void find_broken(const Cta& c, const Segment& s, int parity) {
+__device__ uint32_t find_broken(const Cta& c, const Segment& s) {
     const Params& p = c.p;
     const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
     const int32_t first = s.min_len + 32 * q4, count = min(32, s.max_len - first);
@@ -705,8 +726,7 @@ __device__ void find_broken(const Cta& c, const Segment& s, int parity) {
             if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) word |= 1u << i;
         }
     }
-    if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = word;
-    __syncwarp();
+    return word;
 }
 
 __device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
@@ -732,9 +752,10 @@ __device__ void run_query(const Cta& c) {
         // could pass two phases meanwhile.)
         Ahead x{};
         if (units > 0) x = ask_queries(c, w.s.u, q4 * kOwn);
+        const uint32_t broken = find_broken(c, w.s);
         if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
         if (units > 0) make_operand(c, w.s.u, x, parity, q4 * kOwn, kOwn, img);
-        find_broken(c, w.s, parity);
+        if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = broken;
         if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
         const uint4* src = reinterpret_cast<const uint4*>(img + (q4 * 32 + lane) * 16);
 #pragma unroll 1
