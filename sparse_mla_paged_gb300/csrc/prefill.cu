@@ -750,6 +750,12 @@ __device__ void run_query(const Cta& c) {
         uint8_t* img = query_image(c, parity);
         // The scales and marks of the unit before the last are read. (One barrier for both parities
         // could pass two phases meanwhile.)
+        // The next unit's queries, one after another in memory, into L2.
+        if (!w.s.last && lane == 0) {
+            const Unit& u = c.p.units[w.s.k + 1];
+            const int first = static_cast<int>(c.rank) * kCtaPairs + q4 * kOwn, count = min(kOwn, u.valid - first);
+            if (count > 0) bulk_prefetch_l2(c.p.q + (u.pair0 + first) * kLatent, count * kLatent * 2);
+        }
         Ahead x{};
         if (units > 0) x = ask_queries(c, w.s.u, q4 * kOwn);
         const uint32_t broken = find_broken(c, w.s);

@@ -16,7 +16,7 @@ namespace prefill {
 
 constexpr int kPairs = 128;  // (row, head) pairs of a unit, 64 in each CTA of a cluster
 constexpr int kTile = full::kTile;
-constexpr int kGap = 3;      // tiles that a unit change costs, at most a quarter of a range
+constexpr int kGap = 6;      // tiles that a unit change costs, at most a quarter of a range
 
 struct alignas(16) Unit {
     int64_t start;  // its first tile on the line
