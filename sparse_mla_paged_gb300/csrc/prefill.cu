@@ -423,16 +423,30 @@ __device__ void run_softmax(const Cta& c) {
     uint32_t tau = 0, units = 0;
     bool pv_seen = false;  // the P.V two tiles back was already waited for
 
-    for (Walk w(c);; w.advance(), ++units) {
-        const Segment& s = w.s;
-        const int32_t len = pair < s.u.valid ? pair_len(p, s.u.base, s.u.first + pair) : 0;
+    const int32_t k0 = p.starts[c.cluster].k;
+    for (;; ++units) {
+        // The tile loop keeps few of the unit's numbers (registers are short here); what else it needs,
+        // seldom, it takes from the record again, which stays in L1.
+        auto unit = [&] { return c.segment(k0 + units, p.units[k0 + units], units == 0); };
+        auto seen_by = [&](const Segment& s) { return pair < s.u.valid ? pair_len(p, s.u.base, s.u.first + pair) : 0; };
+        int32_t t, t1, edge;  // tiles; the first with tokens that some row does not see
+        bool none;            // the pair sees nothing
+        {
+            const Segment s = unit();
+            t = s.t0;
+            t1 = s.t1;
+            edge = s.min_len / kTile;
+            none = seen_by(s) == 0;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(p.units + k0 + units + 1));
+        }
+        bool first = true;      // tile of the unit here
         float qs = 0.0f;        // what turns dots into log2 scores, known with the first tile
         float m_ref = kNegInf;  // reference max of the pair (log2 units)
         float m_top = kNegInf;  // highest reference so far
         float l_part = 0.0f;    // this thread's share of the sum of P'
         float credit = 0.0f;    // and its account of what the terms may have lost of it
 
-        for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
+        for (; t < t1; ++t, ++tau, first = false) {
             c.wait(BAR_SFULL, tau & 1);
             tc_fence_after();
             // Dots of pair hq with tokens tok0 .. tok0+31 of the tile: this lane's term plus the
@@ -454,16 +468,17 @@ __device__ void run_softmax(const Cta& c) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) c.arrive(BAR_SEMPTY, 0);
-            if (t == s.t0) {
+            if (first) {
                 // A broken query's scale is NaN, which would also reach the -inf of hidden tokens: a
                 // pair that sees none (behind the unit's last) takes 1 and stays at zero.
                 const uint32_t e = c.smem[kOffScale + (units & 1) * kCtaPairs + hq];
                 qs = e == 255 || p.score_scale != p.score_scale ? __uint_as_float(0x7FC00000u)
                                                                 : fmaxf(fabsf(p.score_scale) * __uint_as_float(e << 23), 0x1p-120f);
-                if (len == 0) qs = 1.0f;
+                if (none) qs = 1.0f;
             }
             const int v_slot = static_cast<int>(tau % kSlots);
-            if ((t + 1) * kTile > s.min_len) {  // an edge tile
+            if (t >= edge) {
+                const Segment s = unit();
                 uint8_t* v_tile = c.smem + kOffV + v_slot * kSlotBytes;
                 const uint32_t* broken = reinterpret_cast<const uint32_t*>(c.smem + kOffBroken) + (units & 1) * 4;
                 // 32 of those marks from position pos on.
@@ -486,7 +501,7 @@ __device__ void run_softmax(const Cta& c) {
                                                       (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
-                const int32_t lim = len - t * kTile - tok0;  // this thread's scores before it are seen
+                const int32_t lim = seen_by(s) - t * kTile - tok0;  // this thread's scores before it are seen
                 const uint32_t hidden = lim >= 32 ? 0u : lim <= 0 ? ~0u : ~0u << lim;
                 const uint32_t nan = marks(t * kTile + tok0) & ~hidden;
 #pragma unroll
@@ -503,14 +518,15 @@ __device__ void run_softmax(const Cta& c) {
             hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1)) * qs;
             // As in the full decode: P' is formed with the reference as it is (but for a unit's first
             // tile), one barrier tells whether any half of any pair's scores asks for a move, and
-            // only then the halves are compared, references move and P' is formed again.
-            const bool ask = hmax > m_ref + kRescaleMargin ||
-                             (hmax < m_ref - kRescaleDrop && m_ref > m_top - kRescaleFloor && hmax != kNegInf);
+            // only then the halves are compared, references move and P' is formed again. A tile far
+            // below its reference asks when the account runs out, not before: the last tile of a unit
+            // often holds few tokens that are seen.
+            const bool ask = hmax > m_ref + kRescaleMargin;
             uint32_t hw[kScores / 4], lw[kScores / 4];
             float fresh, earned = 0.0f;
 #pragma unroll 1
             for (bool again = false;; again = true) {
-                if (again || t > s.t0) {
+                if (again || !first) {
                     float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                     const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
 #pragma unroll
@@ -554,7 +570,7 @@ __device__ void run_softmax(const Cta& c) {
                 } else {
                     credit = fmaf(0.25f, credit4, -earned);  // in equal parts: who asked gets what the others do not need
                 }
-                if (t > s.t0 && half == 0) {
+                if (!first && half == 0) {
                     // Factors and the tile's mark into both CTAs (the words' last readers were done
                     // before the P.V two tiles back).
                     if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
@@ -568,7 +584,7 @@ __device__ void run_softmax(const Cta& c) {
                     __syncwarp();
                 }
                 // Also keeps the next tile's maxima from overwriting these.
-                if (!named_bar_any<kBarSoftmax, kSoftmaxThreads>(change) && t > s.t0) break;
+                if (!named_bar_any<kBarSoftmax, kSoftmaxThreads>(change) && !first) break;
             }
             l_part += fresh;
             credit += earned;
@@ -587,6 +603,7 @@ __device__ void run_softmax(const Cta& c) {
         }
 
         // ---- the unit's output factors, to both CTAs ----
+        const Segment s = unit();
         const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
         if (term == 0) hm_s[half * kCtaPairs + hq].x = lpair;
         named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
