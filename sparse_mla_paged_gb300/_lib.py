@@ -41,7 +41,7 @@ class PagePool(ctypes.Structure):
                 ("page_bytes", ctypes.c_int64), ("layers", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-_POOLS = [ctypes.POINTER(PagePool), _I32]
+_POOLS = [_P, _I32]  # an array of PagePool, or its bytes
 _DECODE_ARGS = [_P, _P, _P, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _I32, _I64, _F32, _F32, _F32, _P]
 SIGNATURES = {
     "dsa_abi_version": ([], _I32),

@@ -7,6 +7,7 @@ raise DsaError on a non-OK status.
 from __future__ import annotations
 
 import contextlib
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -274,7 +275,7 @@ class _Launch:
             self.stream = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.raw, device=index)
 
     def __enter__(self):
-        if torch.cuda.current_device() != self.index:
+        if torch._C._cuda_getDevice() != self.index:
             self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
         return self
@@ -546,48 +547,73 @@ def alloc_pages_workspace(num_pages: int, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
+_POOL_FORMATS = [struct.Struct("=" + "qqqqii" * n) for n in range(MAX_PAGE_POOLS + 1)]
+
+
 def _pools(pools, index):
-    """dsa_page_pool array of cache tensors uint8 [num_pages, page bytes] or [layers, num_pages, page
-    bytes], any strides but a page's own bytes together; and their number of pages."""
-    if isinstance(pools, torch.Tensor) or len(pools) == 0:
+    """dsa_page_pool array (as bytes) of cache tensors uint8 [num_pages, page bytes] or [layers,
+    num_pages, page bytes], any strides but a page's own bytes together; and their number of pages."""
+    n = 0 if isinstance(pools, torch.Tensor) else len(pools)
+    if n == 0:
         raise ValueError("pools must be a sequence of cache tensors")
-    if len(pools) > MAX_PAGE_POOLS:
+    if n > MAX_PAGE_POOLS:
         raise DsaError(2, f"more than {MAX_PAGE_POOLS} pools")
-    out = (_lib.PagePool * len(pools))()
-    num_pages = pools[0].shape[-2] if pools[0].dim() > 1 else 0
-    for p, t in zip(out, pools):
-        if t.get_device() != index or t.dtype != torch.uint8 or t.dim() not in (2, 3) or t.shape[-2] != num_pages or t.stride(-1) != 1:
+    fields, num_pages = [], None
+    for t in pools:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2:
+            (pages, width), (page, one), layers, layer = shape, stride, 1, 0
+        elif len(shape) == 3:
+            (layers, pages, width), (layer, page, one) = shape, stride
+        else:
+            pages = None
+        if num_pages is None:
+            num_pages = pages
+        if pages is None or pages != num_pages or one != 1 or t.dtype is not torch.uint8 or t.get_device() != index:
             raise ValueError(f"a pool must be torch.uint8 [num_pages, bytes] or [layers, num_pages, bytes] on cuda:{index}, "
                              "the bytes of a page together and num_pages the same in all")
-        p.base, p.page_stride_bytes, p.page_bytes = t.data_ptr(), t.stride(-2), t.shape[-1]
-        p.layers = t.shape[0] if t.dim() == 3 else 1
-        p.layer_stride_bytes = t.stride(0) if t.dim() == 3 else 0
-    return out, num_pages
+        if layers > 0x7FFFFFFF:
+            raise ValueError("sizes must be 32-bit numbers")
+        fields += (t.data_ptr(), page, layer, width, layers, 0)
+    return _POOL_FORMATS[n].pack(*fields), num_pages
 
 
-def _requests(block_tables, lens, index):
-    _need_on(block_tables, torch.int32, "block_tables", index)
-    _need_on(lens, torch.int32, "lens", index)
-    if block_tables.dim() != 2 or block_tables.shape[0] != lens.numel():
-        raise ValueError("block_tables [num_seqs, max_blocks_per_seq], lens [num_seqs]")
+def _need_ints(index, tensors, names):
+    for t in tensors:
+        if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+            for t, n in zip(tensors, names):
+                _need_on(t, torch.int32, n, index)
 
 
 def _books(at, num_pages, info, workspace, device):
     """The info words and the workspace of a page operator's call, made where not given."""
-    if info is None or workspace is None:
+    if info is None:
+        if at.stream is None:
+            info = torch.empty(4, dtype=torch.int32, device=device)
+        else:
+            with at.allocating():
+                info = torch.empty(4, dtype=torch.int32, device=device)
+    else:
+        _need_on(info, torch.int32, "info", at.index)
+        if info.numel() < 4:
+            raise ValueError("info [4]")
+    if workspace is None:
         with at.allocating():
-            info = torch.empty(4, dtype=torch.int32, device=device) if info is None else info
-            workspace = alloc_pages_workspace(num_pages, device) if workspace is None else workspace
-    _need_on(info, torch.int32, "info", at.index)
-    _need_on(workspace, torch.uint8, "workspace", at.index)
-    if info.numel() < 4:
-        raise ValueError("info [4]")
+            workspace = alloc_pages_workspace(num_pages, device)
+    else:
+        _need_on(workspace, torch.uint8, "workspace", at.index)
     return info, workspace
 
 
-def _counted(page_shares, free_pages, num_free, num_pages, index):
-    for t, n in ((page_shares, "page_shares"), (free_pages, "free_pages"), (num_free, "num_free")):
-        _need_on(t, torch.int32, n, index)
+def _rows_of(block_tables, lens):
+    """num_seqs and max_blocks_per_seq of the requests' tables."""
+    shape, n = block_tables.shape, lens.numel()
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError("block_tables [num_seqs, max_blocks_per_seq], lens [num_seqs]")
+    return n, shape[1]
+
+
+def _counted(page_shares, free_pages, num_free, num_pages):
     if page_shares.numel() != num_pages or free_pages.numel() != num_pages or num_free.numel() != 1:
         raise ValueError("page_shares [num_pages], free_pages [num_pages], num_free [1]")
 
@@ -597,15 +623,15 @@ def copy_pages(pools, src_pages: torch.Tensor, dst_pages: torch.Tensor, stream=N
     pairs with a negative page are left out. pools: cache tensors uint8 [num_pages, page bytes] or
     [layers, num_pages, page bytes]. step_device_status tells of pages past the pools."""
     i = _device_of(src_pages, "src_pages")
-    _need_on(src_pages, torch.int32, "src_pages", i)
-    _need_on(dst_pages, torch.int32, "dst_pages", i)
-    if src_pages.numel() != dst_pages.numel():
+    _need_ints(i, (src_pages, dst_pages), ("src_pages", "dst_pages"))
+    count = src_pages.numel()
+    if count != dst_pages.numel():
         raise ValueError("src_pages [count], dst_pages [count]")
     table, num_pages = _pools(pools, i)
-    _fit(src_pages.numel(), num_pages)
+    _fit(count, num_pages)
     with _Launch(i, stream) as at:
-        check(_lib.load().dsa_copy_pages(table, len(pools), src_pages.data_ptr(), dst_pages.data_ptr(), src_pages.numel(),
-                                         num_pages, at.raw), "dsa_copy_pages")
+        check(_lib.load().dsa_copy_pages(table, len(pools), src_pages.data_ptr(), dst_pages.data_ptr(), count, num_pages, at.raw),
+              "dsa_copy_pages")
 
 
 def fork_pages(pools, parents: torch.Tensor, children: torch.Tensor, lens: torch.Tensor, block_size: int,
@@ -615,18 +641,18 @@ def fork_pages(pools, parents: torch.Tensor, children: torch.Tensor, lens: torch
     shared (page_shares, block_tables, in place), a partly filled last page is copied to the next of
     free_pages. Returns info, int32 [4]: forks made, pages taken off free_pages, status, 0."""
     i = _device_of(parents, "parents")
-    for t, n in ((parents, "parents"), (children, "children"), (free_pages, "free_pages"), (page_shares, "page_shares")):
-        _need_on(t, torch.int32, n, i)
-    _requests(block_tables, lens, i)
+    _need_ints(i, (parents, children, lens, block_tables, free_pages, page_shares),
+               ("parents", "children", "lens", "block_tables", "free_pages", "page_shares"))
+    n, blocks = _rows_of(block_tables, lens)
     table, num_pages = _pools(pools, i)
-    if parents.numel() != children.numel() or page_shares.numel() != num_pages:
+    forks, free = parents.numel(), free_pages.numel()
+    if forks != children.numel() or page_shares.numel() != num_pages:
         raise ValueError("parents [num_forks], children [num_forks], page_shares [num_pages]")
-    _fit(parents.numel(), lens.numel(), block_size, block_tables.shape[1], free_pages.numel(), num_pages)
+    _fit(forks, n, block_size, blocks, free, num_pages)
     with _Launch(i, stream) as at:
         info, workspace = _books(at, num_pages, info, workspace, parents.device)
-        check(_lib.load().dsa_fork_pages(table, len(pools), parents.data_ptr(), children.data_ptr(), parents.numel(),
-                                         lens.data_ptr(), lens.numel(), block_size, block_tables.data_ptr(),
-                                         block_tables.shape[1], free_pages.data_ptr(), free_pages.numel(),
+        check(_lib.load().dsa_fork_pages(table, len(pools), parents.data_ptr(), children.data_ptr(), forks, lens.data_ptr(), n,
+                                         block_size, block_tables.data_ptr(), blocks, free_pages.data_ptr(), free,
                                          page_shares.data_ptr(), num_pages, info.data_ptr(), workspace.data_ptr(),
                                          workspace.numel(), at.raw), "dsa_fork_pages")
     return info
@@ -640,23 +666,24 @@ def release_pages(block_tables: torch.Tensor, lens: torch.Tensor, keep_lens: tor
     as plan.info[1:2]) in the free list free_pages [num_pages], num_free [1]. All in place. Returns info,
     int32 [4]: references given back, pages freed, status, pages in the list."""
     i = _device_of(block_tables, "block_tables")
-    _requests(block_tables, lens, i)
-    _need_on(keep_lens, torch.int32, "keep_lens", i)
+    _need_ints(i, (block_tables, lens, keep_lens, page_shares, free_pages, num_free),
+               ("block_tables", "lens", "keep_lens", "page_shares", "free_pages", "num_free"))
+    n, blocks = _rows_of(block_tables, lens)
     num_pages = page_shares.numel()
-    _counted(page_shares, free_pages, num_free, num_pages, i)
-    if keep_lens.numel() != lens.numel():
+    _counted(page_shares, free_pages, num_free, num_pages)
+    if keep_lens.numel() != n:
         raise ValueError("lens [num_seqs], keep_lens [num_seqs]")
     if taken is not None:
         _need_on(taken, torch.int32, "taken", i)
         if taken.numel() != 1:
             raise ValueError("taken [1]")
-    _fit(lens.numel(), block_size, block_tables.shape[1], num_pages)
+    _fit(n, block_size, blocks, num_pages)
     with _Launch(i, stream) as at:
         info, workspace = _books(at, num_pages, info, workspace, lens.device)
-        check(_lib.load().dsa_release_pages(block_tables.data_ptr(), block_tables.shape[1], lens.data_ptr(), keep_lens.data_ptr(),
-                                            lens.numel(), block_size, page_shares.data_ptr(), num_pages, free_pages.data_ptr(),
-                                            num_free.data_ptr(), _ptr(taken), info.data_ptr(), workspace.data_ptr(),
-                                            workspace.numel(), at.raw), "dsa_release_pages")
+        check(_lib.load().dsa_release_pages(block_tables.data_ptr(), blocks, lens.data_ptr(), keep_lens.data_ptr(), n, block_size,
+                                            page_shares.data_ptr(), num_pages, free_pages.data_ptr(), num_free.data_ptr(),
+                                            _ptr(taken), info.data_ptr(), workspace.data_ptr(), workspace.numel(), at.raw),
+              "dsa_release_pages")
     return info
 
 
@@ -666,16 +693,18 @@ def compact_pages(pools, block_tables: torch.Tensor, lens: torch.Tensor, block_s
     tables, shares and the free list follow. All in place. Returns info, int32 [4]: live pages, pages
     moved, status, free pages."""
     i = _device_of(block_tables, "block_tables")
-    _requests(block_tables, lens, i)
+    _need_ints(i, (block_tables, lens, page_shares, free_pages, num_free),
+               ("block_tables", "lens", "page_shares", "free_pages", "num_free"))
+    n, blocks = _rows_of(block_tables, lens)
     table, num_pages = _pools(pools, i)
-    _counted(page_shares, free_pages, num_free, num_pages, i)
-    _fit(lens.numel(), block_size, block_tables.shape[1], num_pages)
+    _counted(page_shares, free_pages, num_free, num_pages)
+    _fit(n, block_size, blocks, num_pages)
     with _Launch(i, stream) as at:
         info, workspace = _books(at, num_pages, info, workspace, lens.device)
-        check(_lib.load().dsa_compact_pages(table, len(pools), block_tables.data_ptr(), block_tables.shape[1], lens.data_ptr(),
-                                            lens.numel(), block_size, page_shares.data_ptr(), num_pages, free_pages.data_ptr(),
-                                            num_free.data_ptr(), info.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                            at.raw), "dsa_compact_pages")
+        check(_lib.load().dsa_compact_pages(table, len(pools), block_tables.data_ptr(), blocks, lens.data_ptr(), n, block_size,
+                                            page_shares.data_ptr(), num_pages, free_pages.data_ptr(), num_free.data_ptr(),
+                                            info.data_ptr(), workspace.data_ptr(), workspace.numel(), at.raw),
+              "dsa_compact_pages")
     return info
 
 
