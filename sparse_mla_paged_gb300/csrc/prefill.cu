@@ -243,19 +243,18 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
     __syncwarp();
 }
 
-// The same by 16-byte copies: a key row per instruction, or the halves of two value rows.
+// The same by 16-byte copies: an instruction brings 128 bytes of each of four rows, so that a row's
+// address is found once for all its blocks.
 template <bool kValues>
 __device__ void run_load_copies(const Cta& c) {
     constexpr int kTokens = kValues ? kTile : kKeyTokens;
     constexpr int kFull = kValues ? BAR_VFULL0 : BAR_KFULL0, kEmpty = kValues ? BAR_VEMPTY0 : BAR_KEMPTY0;
     constexpr int kGroup = kValues ? kVGroup : kKGroup;
-    constexpr int kEach = kTokens / 32;            // tokens that a lane looks up
-    constexpr int kRows = kValues ? 2 : 1;         // per instruction
+    constexpr int kEach = kTokens / 32;  // tokens that a lane looks up
     const Params& p = c.p;
-    const int lane = threadIdx.x & 31;
-    const int sub = kValues ? lane >> 4 : 0, piece = kValues ? lane & 15 : lane;
+    const int lane = threadIdx.x & 31, sub = lane >> 3, piece = lane & 7;
     const uint8_t* cache = (kValues ? p.v_cache + c.rank * kDims : p.k_cache) + piece * 16;
-    const uint32_t ring = c.sbase + (kValues ? kOffV : 0) + (piece >> 3) * 1024;
+    const uint32_t ring = c.sbase + (kValues ? kOffV : 0);
     const int32_t pos0 = lane + (kValues ? 0 : static_cast<int32_t>(c.rank) * kKeyTokens);
     uint32_t tau = 0;
     for (Walk w(c);; w.advance()) {
@@ -282,15 +281,18 @@ __device__ void run_load_copies(const Cta& c) {
             look(t + 1);
             const int e = static_cast<int>(tau % kSlots);
             if (tau >= kSlots) c.wait(kEmpty + e, (tau / kSlots - 1) & 1);
-            const uint32_t dst = ring + e * kSlotBytes;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-#pragma unroll 4
-                for (int j = 0; j < 32; j += kRows) {
+                // Rows j and j + 4 of an 8-row group in turn.
+                const uint32_t dst = ring + e * kSlotBytes + 4 * i * kGroup + sub * 128 + ((piece ^ sub) << 4);
+#pragma unroll 2
+                for (int j = 0; j < 32; j += 4) {
                     const int64_t at = __shfl_sync(0xffffffffu, mine[i], j + sub);
-                    const int tok = 32 * i + j + sub;
-                    const uint32_t d = dst + (tok >> 3) * kGroup + (tok & 7) * 128 + (((piece & 7) ^ (tok & 7)) << 4);
-                    cp_async_16_zfill(d, cache + (at >= 0 ? at : 0), at >= 0 ? 16u : 0u);
+                    const uint8_t* src = cache + (at >= 0 ? at : 0);
+                    const uint32_t size = at >= 0 ? 16u : 0u;
+                    const uint32_t d = (dst + (j >> 3) * kGroup + (j & 4) * 128) ^ ((j & 4) << 4);
+#pragma unroll
+                    for (int b = 0; b < (kValues ? kDims : kLatent) / 128; ++b) cp_async_16_zfill(d + b * 1024, src + b * 128, size);
                 }
             }
             cp_async_arrive_noinc(c.bar(kFull + e));
