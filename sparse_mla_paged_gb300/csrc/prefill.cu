@@ -20,9 +20,11 @@
 //                when pages and tiles fit each other, else 16-byte copies
 //   warp 2, 3    issue Q K^T and P V (rank 0); tell rank 0 of the loaded K tiles (rank 1)
 //   warps 4-11   softmax, two per TMEM lane quarter
-//   warps 12-15  rescale O when a reference moves, write a unit's output
-//   warps 16-19  make the next unit's query operand and put it in place
+//   warps 12-15  make the next unit's query operand and put it in place, rescale O when a reference
+//                moves, write a unit's output
 //
+// (The queries by four warps of their own, at 96 registers a thread instead of 128, took 4 % more
+// on long units and on short ones.)
 // A reference that moves in one CTA rescales columns of O in both. The CTA that asks writes the
 // factors into both; the warp that issues P V finds its mark before the tile's product, has
 // warps 12-15 of both CTAs rescale, and goes on. Tiles that no pair asks in pay nothing for it.
@@ -54,8 +56,7 @@ constexpr int kVGroup = 8 * kDims;
 constexpr int kSoftmax0 = 4, kSoftmaxWarps = 8;
 constexpr int kEpilogue0 = 12, kEpilogueWarps = 4;
 constexpr int kSoftmaxThreads = kSoftmaxWarps * 32;
-constexpr int kQuery0 = 16, kQueryWarps = 4;
-constexpr int kThreads = (kQuery0 + kQueryWarps) * 32;
+constexpr int kThreads = (kEpilogue0 + kEpilogueWarps) * 32;
 constexpr int kHalfCols = kTile / 2;                // S columns per softmax warp
 static_assert(kScores == kHalfCols / 2, "scores per softmax thread: 32, one bit each of a word");
 constexpr int kPTermBytes = kCtaPairs * kTile;
@@ -625,10 +626,11 @@ __device__ void run_softmax(const Cta& c) {
 }
 
 // ------------------------------------------------------------------------------------
-// query warps
+// query operands (epilogue warps)
 // ------------------------------------------------------------------------------------
-constexpr int kPrepPairs = 4;   // pairs whose loads are in flight together
-static_assert((kSoftmaxWarps + kEpilogueWarps + kQueryWarps) * kPrepPairs == kCtaPairs, "the first unit's, a turn of all these warps");
+constexpr int kPrepPairs = 4;                         // pairs whose loads are in flight together
+constexpr int kOwnPairs = kCtaPairs / kEpilogueWarps; // pairs of a warp
+static_assert(kPrepPairs * (kSoftmaxWarps + 2 * kEpilogueWarps) == kCtaPairs, "the first unit's: a turn of all warps and another of these");
 
 // Query operand rows of a warp's kPrepPairs or more pairs: lane l has dims [16l, 16l+16). A
 // head's bf16 query becomes two E4M3 terms after a scaling by a power of two (exact for elements from
@@ -637,7 +639,7 @@ static_assert((kSoftmaxWarps + kEpilogueWarps + kQueryWarps) * kPrepPairs == kCt
 // negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or an
 // infinity gets zero codes and a NaN scale (exponent 255), which makes all its scores NaN.
 // The loop over pairs stays rolled: unrolled, its code is fetched anew for each unit, which took
-// longer than all else here (18700 against TIMED cycles for 16 pairs).
+// longer than all else here (18700 cycles for 16 pairs against 10600).
 struct Query {
     uint4 a, b;
 };
@@ -753,56 +755,61 @@ __device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
 }
 // The first unit's operand is made by all warps that have nothing to do yet.
 __device__ void prepare_first(const Cta& c) {
-    const int h0 = ((threadIdx.x >> 5) - kSoftmax0) * kPrepPairs;
     const Unit& u = c.p.starts[c.cluster].unit;
+    const int warp = threadIdx.x >> 5;
+    int h0 = (warp - kSoftmax0) * kPrepPairs;
     make_operand(c, u, ask_queries(c, u, h0), 0, h0, kPrepPairs, query_image(c, 0));
+    if (warp >= kEpilogue0) {
+        h0 += kEpilogueWarps * kPrepPairs;
+        make_operand(c, u, ask_queries(c, u, h0), 0, h0, kPrepPairs, query_image(c, 0));
+    }
     named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
 }
 
-__device__ void run_query(const Cta& c) {
-    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
-    constexpr int kOwn = kCtaPairs / kQueryWarps;  // pairs of a warp
-    const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ;
-    Walk w(c);
-    for (uint32_t units = 0;; ++units, w.advance()) {
-        const int parity = units & 1;
-        uint8_t* img = query_image(c, parity);
-        // The scales and marks of the unit before the last are read. (One barrier for both parities
-        // could pass two phases meanwhile.)
-        // The next unit's queries, one after another in memory, into L2.
-        if (!w.s.last && lane == 0) {
-            const Unit& u = c.p.units[w.s.k + 1];
-            const int first = static_cast<int>(c.rank) * kCtaPairs + q4 * kOwn, count = min(kOwn, u.valid - first);
-            if (count > 0) bulk_prefetch_l2(c.p.q + (u.pair0 + first) * kLatent, count * kLatent * 2);
-        }
-        Ahead x{};
-        if (units > 0) x = ask_queries(c, w.s.u, q4 * kOwn);
-        const uint32_t broken = find_broken(c, w.s);
-        if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
-        if (units > 0) make_operand(c, w.s.u, x, parity, q4 * kOwn, kOwn, img);
-        if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = broken;
-        if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
-        const uint4* src = reinterpret_cast<const uint4*>(img + (q4 * 32 + lane) * 16);
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-            uint32_t a[2][32];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint4 v = __ldcg(src + (part * 16 + i) * (2048 / 16));
-                a[i >> 3][4 * (i & 7)] = v.x;
-                a[i >> 3][4 * (i & 7) + 1] = v.y;
-                a[i >> 3][4 * (i & 7) + 2] = v.z;
-                a[i >> 3][4 * (i & 7) + 3] = v.w;
-            }
-            tmem_st_x32(place + part * 64, a[0]);
-            tmem_st_x32(place + part * 64 + 32, a[1]);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) c.arrive(BAR_QFULL, 0);
-        if (w.s.last) break;
+// This warp's pairs of unit number `units` of the cluster, s: scales, marks and operand image.
+__device__ void prepare_query(const Cta& c, const Segment& s, uint32_t units) {
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3, parity = units & 1;
+    // The next unit's queries, one after another in memory, into L2.
+    if (!s.last && lane == 0) {
+        const Unit& u = c.p.units[s.k + 1];
+        const int first = static_cast<int>(c.rank) * kCtaPairs + q4 * kOwnPairs, count = min(kOwnPairs, u.valid - first);
+        if (count > 0) bulk_prefetch_l2(c.p.q + (u.pair0 + first) * kLatent, count * kLatent * 2);
     }
+    Ahead x{};
+    if (units > 0) x = ask_queries(c, s.u, q4 * kOwnPairs);
+    const uint32_t broken = find_broken(c, s);
+    // The scales and marks of the unit before the last are read. (One barrier for both parities
+    // could pass two phases meanwhile.)
+    if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
+    if (units > 0) make_operand(c, s.u, x, parity, q4 * kOwnPairs, kOwnPairs, query_image(c, parity));
+    if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = broken;
+    __syncwarp();
+}
+
+// Its image into tensor memory, once the unit before has no more use for the place.
+__device__ void place_query(const Cta& c, uint32_t units) {
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ;
+    const uint4* src = reinterpret_cast<const uint4*>(query_image(c, units & 1) + (q4 * 32 + lane) * 16);
+    if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        uint32_t a[2][32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint4 v = __ldcg(src + (part * 16 + i) * (2048 / 16));
+            a[i >> 3][4 * (i & 7)] = v.x;
+            a[i >> 3][4 * (i & 7) + 1] = v.y;
+            a[i >> 3][4 * (i & 7) + 2] = v.z;
+            a[i >> 3][4 * (i & 7) + 3] = v.w;
+        }
+        tmem_st_x32(place + part * 64, a[0]);
+        tmem_st_x32(place + part * 64 + 32, a[1]);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) c.arrive(BAR_QFULL, 0);
 }
 
 // ------------------------------------------------------------------------------------
@@ -813,9 +820,16 @@ __device__ void run_epilogue(const Cta& c) {
     const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     uint32_t tau = 0, units = 0, events = 0;
-    for (Walk w(c);; w.advance(), ++units) {
+    Walk w(c), ahead(c);
+    prepare_query(c, w.s, 0);
+    place_query(c, 0);
+    for (;; w.advance(), ++units) {
         const Segment& s = w.s;
         tau += s.t1 - s.t0;
+        if (!s.last) {
+            ahead.advance();
+            prepare_query(c, ahead.s, units + 1);
+        }
         for (;;) {
             c.wait(BAR_EVENT, events++ & 1);
             const uint32_t event = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffEvent);
@@ -847,6 +861,8 @@ __device__ void run_epilogue(const Cta& c) {
             __syncwarp();
             if (lane == 0) c.arrive(BAR_OFREE, 0);
         }
+
+        if (!s.last) place_query(c, units + 1);  // while the last P.V runs
 
         // ---- output of the unit ----
         c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
@@ -923,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         mbar_init(c.bar(BAR_SFULL), 1);
         mbar_init(c.bar(BAR_SEMPTY), 2 * kSoftmaxWarps);
-        mbar_init(c.bar(BAR_QFULL), 2 * kQueryWarps);
+        mbar_init(c.bar(BAR_QFULL), 2 * kEpilogueWarps);
         mbar_init(c.bar(BAR_QEMPTY), 1);
         mbar_init(c.bar(BAR_EVENT), 1);
         mbar_init(c.bar(BAR_OFREE), 2 * kEpilogueWarps);
@@ -976,12 +992,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         } else if (warp < kEpilogue0) {
             prepare_first(c);
             run_softmax(c);
-        } else if (warp < kQuery0) {
-            prepare_first(c);
-            run_epilogue(c);
         } else {
             prepare_first(c);
-            run_query(c);
+            run_epilogue(c);
         }
     }
     tc_fence_before();
