@@ -74,7 +74,8 @@ constexpr int kOffScale = kOffF + kPairs * 4;                // u8 [2 unit parit
 constexpr int kOffFlags = kOffScale + 2 * kCtaPairs;         // u32 [2 tile parities][2 CTAs][4 lane quarters] tile that moved a reference
 constexpr int kOffBroken = kOffFlags + 2 * 2 * 4 * 4;        // u32 [2 unit parities][4] tokens from the unit's shortest row on with a NaN code
 constexpr int kOffEvent = kOffBroken + 2 * 4 * 4;            // u32: a tile's number + 1 to rescale before, 0: the unit is done
-constexpr int kOffTmem = kOffEvent + 4;
+constexpr int kOffProgress = kOffEvent + 4;                  // u32: key tiles asked for
+constexpr int kOffTmem = kOffProgress + 4;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffBars = (kOffAbort + 4 + 7) / 8 * 8;
 // (both): in either CTA; (0): in rank 0, both CTAs arrive.
@@ -135,6 +136,16 @@ struct Cta {
     __device__ void wait(int b, uint32_t parity) const {
         if (!mbar_wait(bar(b), parity, abort_flag, p.wait_limit_ns)) fail(kStatusTimeout);
         __syncwarp();
+    }
+    __device__ volatile uint32_t* progress() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffProgress); }
+    // As wait, for what may take longer than a wait is allowed (a unit of very many tiles): the limit
+    // runs anew while tiles come in.
+    __device__ void wait_long(int b, uint32_t parity) const {
+        for (uint32_t seen = ~0u; *progress() != seen && !*abort_flag;) {
+            seen = *progress();
+            if (mbar_wait(bar(b), parity, abort_flag, p.wait_limit_ns) || p.wait_limit_ns < kPollHintNs) break;
+        }
+        wait(b, parity);
     }
     // Says nothing of shared memory that the other CTA's threads have written (fence_cluster).
     __device__ void arrive(int b, uint32_t to) const { mbar_arrive_cluster(map_rank(bar(b), to)); }
@@ -220,6 +231,7 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
             if (live && page < 0) report(p, kStatusBounds);
             const int e = static_cast<int>(tau % kSlots);
             if (tau >= kSlots) c.wait(kEmpty + e, (tau / kSlots - 1) & 1);
+            if (!kValues && lane == 0) *c.progress() = tau;
             // After a failed wait nothing more is issued (the drain below finds what is in flight).
             if (__any_sync(0xffffffffu, *c.abort_flag != 0)) {
                 stop = true;
@@ -282,6 +294,7 @@ __device__ void run_load_copies(const Cta& c) {
             look(t + 1);
             const int e = static_cast<int>(tau % kSlots);
             if (tau >= kSlots) c.wait(kEmpty + e, (tau / kSlots - 1) & 1);
+            if (!kValues && lane == 0) *c.progress() = tau;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 // Rows j and j + 4 of an 8-row group in turn.
@@ -718,10 +731,11 @@ __device__ __forceinline__ void make_operand(const Cta& c, const Unit& u, Ahead 
                 lo[j][k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
             }
 #pragma unroll
-        for (int j = 0; j < kTurn; ++j)  // both rows' 16 bytes, one sector
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(img + lane * 2048 + 2 * (h0 + i + j) * 16),
-                         "r"(hi[j][0]), "r"(hi[j][1]), "r"(hi[j][2]), "r"(hi[j][3]), "r"(lo[j][0]), "r"(lo[j][1]), "r"(lo[j][2]), "r"(lo[j][3])
-                         : "memory");
+        for (int j = 0; j < kTurn; ++j) {  // both rows' 16 bytes, one sector, one store
+            auto two = [](uint32_t a, uint32_t b) { return static_cast<unsigned long long>(b) << 32 | a; };
+            *reinterpret_cast<ulonglong4_32a*>(img + lane * 2048 + 2 * (h0 + i + j) * 16) =
+                ulonglong4_32a{two(hi[j][0], hi[j][1]), two(hi[j][2], hi[j][3]), two(lo[j][0], lo[j][1]), two(lo[j][2], lo[j][3])};
+        }
     }
     __syncwarp();
 }
@@ -831,7 +845,7 @@ __device__ void run_epilogue(const Cta& c) {
             prepare_query(c, ahead.s, units + 1);
         }
         for (;;) {
-            c.wait(BAR_EVENT, events++ & 1);
+            c.wait_long(BAR_EVENT, events++ & 1);
             const uint32_t event = *reinterpret_cast<volatile uint32_t*>(c.smem + kOffEvent);
             if (event == 0u || __any_sync(0xffffffffu, *c.abort_flag != 0)) break;
             // Tile event - 1 moved references: rescale O after the product before it.
@@ -947,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(c.bar(BAR_FEMPTY), 2 * kEpilogueWarps);
         mbar_init(c.bar(BAR_DRAIN), 2);
         for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(smem + kOffFlags)[i] = 0;
+        *c.progress() = 0;
         *c.abort_flag = 0;
         fence_mbar_init();
         if (kTma) {
