@@ -550,7 +550,7 @@ def alloc_pages_workspace(num_pages: int, device=None) -> torch.Tensor:
 _POOL_FORMATS = [struct.Struct("=" + "qqqqii" * n) for n in range(MAX_PAGE_POOLS + 1)]
 
 
-def _pools(pools, index):
+def _pools(pools, index, _u8=torch.uint8):
     """dsa_page_pool array (as bytes) of cache tensors uint8 [num_pages, page bytes] or [layers,
     num_pages, page bytes], any strides but a page's own bytes together; and their number of pages."""
     n = 0 if isinstance(pools, torch.Tensor) else len(pools)
@@ -569,7 +569,7 @@ def _pools(pools, index):
             pages = None
         if num_pages is None:
             num_pages = pages
-        if pages is None or pages != num_pages or one != 1 or t.dtype is not torch.uint8 or t.get_device() != index:
+        if pages is None or pages != num_pages or one != 1 or t.dtype is not _u8 or t.get_device() != index:
             raise ValueError(f"a pool must be torch.uint8 [num_pages, bytes] or [layers, num_pages, bytes] on cuda:{index}, "
                              "the bytes of a page together and num_pages the same in all")
         if layers > 0x7FFFFFFF:
@@ -578,21 +578,25 @@ def _pools(pools, index):
     return _POOL_FORMATS[n].pack(*fields), num_pages
 
 
-def _need_ints(index, tensors, names):
+def _need_ints(index, tensors, names, _i32=torch.int32):
+    # One pass for all; names only when one is refused.
     for t in tensors:
-        if t.dtype is not torch.int32 or t.get_device() != index or not t.is_contiguous():
+        if t.dtype is not _i32 or t.get_device() != index or not t.is_contiguous():
             for t, n in zip(tensors, names):
-                _need_on(t, torch.int32, n, index)
+                _need_on(t, _i32, n, index)
+
+
+_FOUR = (4,)
 
 
 def _books(at, num_pages, info, workspace, device):
     """The info words and the workspace of a page operator's call, made where not given."""
     if info is None:
         if at.stream is None:
-            info = torch.empty(4, dtype=torch.int32, device=device)
+            info = torch.empty(_FOUR, dtype=torch.int32, device=device)
         else:
             with at.allocating():
-                info = torch.empty(4, dtype=torch.int32, device=device)
+                info = torch.empty(_FOUR, dtype=torch.int32, device=device)
     else:
         _need_on(info, torch.int32, "info", at.index)
         if info.numel() < 4:
@@ -628,7 +632,8 @@ def copy_pages(pools, src_pages: torch.Tensor, dst_pages: torch.Tensor, stream=N
     if count != dst_pages.numel():
         raise ValueError("src_pages [count], dst_pages [count]")
     table, num_pages = _pools(pools, i)
-    _fit(count, num_pages)
+    if (count | num_pages) >> 31:
+        _fit(count, num_pages)
     with _Launch(i, stream) as at:
         check(_lib.load().dsa_copy_pages(table, len(pools), src_pages.data_ptr(), dst_pages.data_ptr(), count, num_pages, at.raw),
               "dsa_copy_pages")
@@ -648,7 +653,8 @@ def fork_pages(pools, parents: torch.Tensor, children: torch.Tensor, lens: torch
     forks, free = parents.numel(), free_pages.numel()
     if forks != children.numel() or page_shares.numel() != num_pages:
         raise ValueError("parents [num_forks], children [num_forks], page_shares [num_pages]")
-    _fit(forks, n, block_size, blocks, free, num_pages)
+    if (forks | n | block_size | blocks | free | num_pages) >> 31:  # a size past 32 bits, or a negative one
+        _fit(forks, n, block_size, blocks, free, num_pages)
     with _Launch(i, stream) as at:
         info, workspace = _books(at, num_pages, info, workspace, parents.device)
         check(_lib.load().dsa_fork_pages(table, len(pools), parents.data_ptr(), children.data_ptr(), forks, lens.data_ptr(), n,
@@ -677,7 +683,8 @@ def release_pages(block_tables: torch.Tensor, lens: torch.Tensor, keep_lens: tor
         _need_on(taken, torch.int32, "taken", i)
         if taken.numel() != 1:
             raise ValueError("taken [1]")
-    _fit(n, block_size, blocks, num_pages)
+    if (n | block_size | blocks | num_pages) >> 31:
+        _fit(n, block_size, blocks, num_pages)
     with _Launch(i, stream) as at:
         info, workspace = _books(at, num_pages, info, workspace, lens.device)
         check(_lib.load().dsa_release_pages(block_tables.data_ptr(), blocks, lens.data_ptr(), keep_lens.data_ptr(), n, block_size,
@@ -698,7 +705,8 @@ def compact_pages(pools, block_tables: torch.Tensor, lens: torch.Tensor, block_s
     n, blocks = _rows_of(block_tables, lens)
     table, num_pages = _pools(pools, i)
     _counted(page_shares, free_pages, num_free, num_pages)
-    _fit(n, block_size, blocks, num_pages)
+    if (n | block_size | blocks | num_pages) >> 31:
+        _fit(n, block_size, blocks, num_pages)
     with _Launch(i, stream) as at:
         info, workspace = _books(at, num_pages, info, workspace, lens.device)
         check(_lib.load().dsa_compact_pages(table, len(pools), block_tables.data_ptr(), blocks, lens.data_ptr(), n, block_size,
