@@ -14,7 +14,7 @@ namespace {
 constexpr int kMarkThreads = 256;
 constexpr int kListThreads = 1024;
 constexpr int kListWarps = kListThreads / 32;
-constexpr int kForkThreads = 1024;
+constexpr int kFewForks = 128;  // up to so many take a block of as many threads, whose barriers are cheaper
 
 __device__ __forceinline__ void report(int* status) { atomicCAS(status, 0, DSA_ERR_DEVICE_BOUNDS); }
 __device__ __forceinline__ void wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -94,6 +94,7 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int32_t*
 
 // One block: which forks are made (its child is named by no earlier fork and is nobody's parent),
 // how many pages each shares and which fresh page takes its last, partly filled one.
+template <int kForkThreads>
 __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_constant__ ForkParams p) {
     extern __shared__ int32_t first_child[];  // [num_seqs] first fork that names the child
     __shared__ int32_t sums[kForkThreads / 32];
@@ -272,49 +273,86 @@ __global__ void __launch_bounds__(kMarkThreads) compact_mark_kernel(const __grid
 // ------------------------------------------------------------------------------------
 // The marks of all pages are counted by every block (a bit per page: 32 KB for 262144 pages),
 // which takes less time than a launch between counting and listing; a block then lists the pages
-// of its own words, a warp 32 words at a time.
+// of its own words, kBlockWords a turn, a warp eight of them. (Blocks of 1024 words, with a warp's
+// words visited whether they had marks or not, took 10.9 us for 64 requests' drafts, not 6.7.)
+constexpr int kBlockWords = 256;
+constexpr int kWarpWords = kBlockWords / kListWarps;
 
-// Marked pages below page `limit` in words [0, w1).
-__device__ __forceinline__ int32_t marked(const uint32_t* marks, int32_t w1, int32_t limit) {
-    int32_t n = 0;
-    for (int32_t w = 4 * threadIdx.x; w < w1; w += 4 * kListThreads) {
+// Sums of two values over the block.
+__device__ __forceinline__ int2 block_sums(int a, int b, int2* sums) {
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = make_int2(a, b);
+    __syncthreads();
+    const int2 mine = sums[threadIdx.x & 31];  // a lane for each of the 32 warps
+    const int2 r = make_int2(__reduce_add_sync(0xffffffffu, mine.x), __reduce_add_sync(0xffffffffu, mine.y));
+    __syncthreads();
+    return r;
+}
+static_assert(kListWarps == 32, "a lane for each warp");
+
+// Marked pages: x all, y those of the words before w0.
+__device__ __forceinline__ int2 count_marks(const uint32_t* marks, int32_t words, int32_t w0, int2* sums) {
+    int all = 0, before = 0;
+    for (int32_t w = 4 * threadIdx.x; w < words; w += 4 * kListThreads) {
+        const uint4 v = *reinterpret_cast<const uint4*>(marks + w);
+        const int n = __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
+        all += n;
+        if (w < w0) before += n;  // both multiples of 4
+    }
+    return block_sums(all, before, sums);
+}
+// Marked pages below page `limit`.
+__device__ __forceinline__ int32_t count_below(const uint32_t* marks, int32_t limit, int2* sums) {
+    int n = 0;
+    for (int32_t w = 4 * threadIdx.x; w < (limit + 31) / 32; w += 4 * kListThreads) {
         const uint4 v = *reinterpret_cast<const uint4*>(marks + w);
         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int32_t left = limit - (w + i) * 32;
-            if (w + i < w1 && left > 0) n += __popc(left >= 32 ? x[i] : x[i] & ((1u << left) - 1u));
+            if (left > 0) n += __popc(left >= 32 ? x[i] : x[i] & ((1u << left) - 1u));
         }
     }
-    return n;
+    return block_sums(n, 0, sums).x;
 }
 
-// each(page, is it marked, marked pages before it) for the pages of this block's words, a page
-// a lane; `before` marked pages precede the block's.
-template <class F>
-__device__ __forceinline__ void for_pages(const uint32_t* marks, int32_t w0, int32_t w1, int32_t num_pages, int32_t before, int32_t* sums,
-                                          F&& each) {
+// This block's turns.
+__device__ __forceinline__ int2 block_turns(int32_t words) {
+    const int32_t turns = (words + kBlockWords - 1) / kBlockWords, each = (turns + gridDim.x - 1) / gridDim.x;
+    const int32_t first = min(turns, static_cast<int32_t>(blockIdx.x) * each);
+    return make_int2(first, min(turns, first + each));
+}
+// each(page, is it marked, marked pages before it) for the pages of words [w0, w0 + kBlockWords), a
+// page a lane; `before` marked pages precede them. Returns the marked pages up to their end. With
+// kMarked only words with marked pages are visited.
+template <bool kMarked, class F>
+__device__ __forceinline__ int32_t for_pages(const uint32_t* marks, int32_t w0, int32_t words, int32_t num_pages, int32_t before, F&& each) {
+    __shared__ int32_t firsts[kListWarps];
+    __syncthreads();  // the turn before has read them
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int32_t base = w0; base < w1; base += kListThreads) {
-        const int32_t w = base + threadIdx.x;
-        const uint32_t mine = w < w1 ? marks[w] : 0u;
-        int32_t total;
-        const int32_t at = before + block_scan<kListWarps>(__popc(mine), sums, &total);
-        before += total;
-        const int32_t words = min(32, w1 - base - 32 * warp);
-        for (int j = 0; j < words; ++j) {
-            const uint32_t bits = __shfl_sync(0xffffffffu, mine, j);
-            const int32_t first = __shfl_sync(0xffffffffu, at, j);
-            const int32_t page = (base + 32 * warp + j) * 32 + lane;
-            if (page < num_pages) each(page, (bits >> lane & 1u) != 0u, first + __popc(bits & ((1u << lane) - 1u)));
-        }
+    const int32_t base = w0 + warp * kWarpWords;
+    const uint32_t mine = lane < kWarpWords && base + lane < words ? marks[base + lane] : 0u;
+    int32_t inc = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < kWarpWords; o <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
     }
-}
-
-__device__ __forceinline__ void block_words(int32_t words, int32_t* w0, int32_t* w1) {
-    const int32_t per = (words / 4 + gridDim.x - 1) / gridDim.x * 4;
-    *w0 = min(words, static_cast<int32_t>(blockIdx.x) * per);
-    *w1 = min(words, *w0 + per);
+    if (lane == kWarpWords - 1) firsts[warp] = inc;
+    __syncthreads();
+    const int32_t of_warp = firsts[lane];
+    const int32_t at = before + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0) + inc - __popc(mine);
+    uint32_t visit = kMarked ? __ballot_sync(0xffffffffu, mine != 0u) : (1u << kWarpWords) - 1u;
+    while (visit != 0u) {
+        const int j = __ffs(visit) - 1;
+        visit &= visit - 1u;
+        const uint32_t bits = __shfl_sync(0xffffffffu, mine, j);
+        const int32_t first = __shfl_sync(0xffffffffu, at, j);
+        const int32_t page = (base + j) * 32 + lane;
+        if (page < num_pages) each(page, (bits >> lane & 1u) != 0u, first + __popc(bits & ((1u << lane) - 1u)));
+    }
+    return before + __reduce_add_sync(0xffffffffu, of_warp);
 }
 
 // Whether this block is the last one to come here.
@@ -331,25 +369,26 @@ __device__ __forceinline__ bool last_block(int32_t* ticket) {
 }
 
 __global__ void __launch_bounds__(kListThreads) release_list_kernel(const __grid_constant__ ReleaseParams p) {
-    __shared__ int32_t sums[kListWarps];
+    __shared__ int2 sums[kListWarps];
     wait_prior();
     const int32_t words = static_cast<int32_t>((static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4);
-    int32_t w0, w1, freed, before;
-    block_words(words, &w0, &w1);
-    block_scan<kListWarps>(marked(p.marks, words, INT32_MAX), sums, &freed);
-    block_scan<kListWarps>(marked(p.marks, w0, INT32_MAX), sums, &before);
+    const int2 turns = block_turns(words);
+    const int2 counts = count_marks(p.marks, words, turns.x * kBlockWords, sums);
+    const int32_t freed = counts.x;
+    int32_t before = counts.y;
     const int32_t had = *p.num_free, count = min(max(had, 0), p.t.num_pages);
     const int32_t want = p.taken ? *p.taken : 0, taken = min(max(want, 0), count);
     bool bad = had != count || want != taken;
     const int64_t after = static_cast<int64_t>(count) - taken + freed;
     const int32_t now = static_cast<int32_t>(min(after, static_cast<int64_t>(p.t.num_pages)));
     bad |= now != after;
-    for_pages(p.marks, w0, w1, p.t.num_pages, before, sums, [&](int32_t page, bool mine, int32_t k) {
-        if (!mine) return;
-        p.shares[page] = 0;
-        const int64_t at = k < taken ? k : static_cast<int64_t>(count) - taken + k;
-        if (at < p.t.num_pages) p.free_pages[at] = page;
-    });
+    for (int32_t turn = turns.x; turn < turns.y; ++turn)
+        before = for_pages<true>(p.marks, turn * kBlockWords, words, p.t.num_pages, before, [&](int32_t page, bool mine, int32_t k) {
+            if (!mine) return;
+            p.shares[page] = 0;
+            const int64_t at = k < taken ? k : static_cast<int64_t>(count) - taken + k;
+            if (at < p.t.num_pages) p.free_pages[at] = page;
+        });
     if (blockIdx.x == 0) {
         const int32_t gap = max(0, taken - freed), moved = min(gap, count - taken);
         for (int32_t i = threadIdx.x; i < moved; i += kListThreads) p.free_pages[freed + i] = p.free_pages[count - moved + i];
@@ -370,28 +409,28 @@ __global__ void __launch_bounds__(kListThreads) release_list_kernel(const __grid
 
 // Pages from the number of live ones on that are live move, in order, to the dead ones below it.
 __global__ void __launch_bounds__(kListThreads) compact_list_kernel(const __grid_constant__ CompactParams p) {
-    __shared__ int32_t sums[kListWarps];
+    __shared__ int2 sums[kListWarps];
     wait_prior();
     let_next();
     const int32_t words = static_cast<int32_t>((static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4);
-    int32_t w0, w1, live, before, low;
-    block_words(words, &w0, &w1);
-    block_scan<kListWarps>(marked(p.marks, words, INT32_MAX), sums, &live);
-    block_scan<kListWarps>(marked(p.marks, w0, INT32_MAX), sums, &before);
-    block_scan<kListWarps>(marked(p.marks, words, live), sums, &low);  // live pages that stay
-    for_pages(p.marks, w0, w1, p.t.num_pages, before, sums, [&](int32_t page, bool mine, int32_t k) {
-        if (page >= live) {
-            if (mine) {
-                p.rank[page] = k - low;
-                p.src[k - low] = page;
-            } else {
-                p.shares[page] = 0;
+    const int2 turns = block_turns(words);
+    const int2 counts = count_marks(p.marks, words, turns.x * kBlockWords, sums);
+    const int32_t live = counts.x, low = count_below(p.marks, live, sums);  // of them, those that stay
+    int32_t before = counts.y;
+    for (int32_t turn = turns.x; turn < turns.y; ++turn)
+        before = for_pages<false>(p.marks, turn * kBlockWords, words, p.t.num_pages, before, [&](int32_t page, bool mine, int32_t k) {
+            if (page >= live) {
+                if (mine) {
+                    p.rank[page] = k - low;
+                    p.src[k - low] = page;
+                } else {
+                    p.shares[page] = 0;
+                }
+            } else if (!mine) {
+                p.dst[page - k] = page;
             }
-        } else if (!mine) {
-            p.dst[page - k] = page;
-        }
-        p.free_pages[page] = page < p.t.num_pages - live ? page + live : -1;
-    });
+            p.free_pages[page] = page < p.t.num_pages - live ? page + live : -1;
+        });
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.head->live = live;
         p.head->moved = live - low;
@@ -457,14 +496,17 @@ int at_most(int64_t want, int most) { return static_cast<int>(want < 1 ? 1 : (wa
 int mark_blocks(const Tables& t) {
     return at_most((static_cast<int64_t>(t.num_seqs) * t.chunks + kMarkThreads / 32 - 1) / (kMarkThreads / 32), INT32_MAX);
 }
-int list_blocks(const Tables& t, int sms) { return at_most((mark_words(t.num_pages) + kListThreads - 1) / kListThreads, sms); }
+// No more blocks than run at once: each reads all marks.
+int list_blocks(const Tables& t, int sms) { return at_most((mark_words(t.num_pages) + kBlockWords - 1) / kBlockWords, sms); }
 
 }  // namespace
 }  // namespace pages
 
 cudaError_t pages_setup() {
-    return cudaFuncSetAttribute(pages::fork_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                DSA_MAX_PLAN_SEQS * 4 + DSA_MAX_PLAN_SEQS / 8);
+    const int smem = DSA_MAX_PLAN_SEQS * 4 + DSA_MAX_PLAN_SEQS / 8;
+    const cudaError_t e = cudaFuncSetAttribute(pages::fork_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(pages::fork_plan_kernel<pages::kFewForks>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 cudaError_t launch_copy_pages(const pages::CopyParams& p, int sms, cudaStream_t stream) {
@@ -475,7 +517,8 @@ cudaError_t launch_copy_pages(const pages::CopyParams& p, int sms, cudaStream_t 
 
 cudaError_t launch_fork_pages(const pages::ForkParams& p, int sms, cudaStream_t stream) {
     const int smem = p.t.num_seqs * 4 + (p.t.num_seqs + 31) / 32 * 4;
-    pages::fork_plan_kernel<<<1, pages::kForkThreads, smem, stream>>>(p);
+    if (p.forks <= pages::kFewForks) pages::fork_plan_kernel<pages::kFewForks><<<1, pages::kFewForks, smem, stream>>>(p);
+    else pages::fork_plan_kernel<1024><<<1, 1024, smem, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t turns = (p.t.max_blocks + pages::kCopyThreads - 1) / pages::kCopyThreads;

@@ -252,6 +252,34 @@ def test_release_of_many_pages(api):
         assert info[2] == 0 and not bool(ws[:256 + 32 * 600].any())
 
 
+def test_books_of_a_large_pool(api):
+    """More pages than one turn of every listing block: 3 million, against sets on the GPU's own side."""
+    pages, n, blocks = 3000001, 40, 4000
+    order = torch.randperm(pages, device="cuda").to(torch.int32)
+    tables = order[:n * blocks].view(n, blocks).clone()
+    lens = torch.full((n,), blocks * 16, dtype=torch.int32, device="cuda")
+    keeps = torch.where(torch.arange(n, device="cuda") % 2 == 0, lens, 0).to(torch.int32)
+    shares = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    free = torch.full((pages,), -1, dtype=torch.int32, device="cuda")
+    count = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = api.alloc_pages_workspace(pages)
+    gone, kept = tables[1::2].reshape(-1).sort().values, tables[::2].clone()
+    info = api.release_pages(tables, lens, keeps, 16, shares, free, count, workspace=ws)
+    assert info.tolist() == [n // 2 * blocks, n // 2 * blocks, 0, n // 2 * blocks]
+    assert torch.equal(free[:len(gone)], gone) and (free[len(gone):] == -1).all() and torch.equal(tables[::2], kept)
+    pool = torch.arange(pages, dtype=torch.int32, device="cuda").view(torch.uint8).view(pages, 4).repeat(1, 4)
+    info = api.compact_pages([pool], tables, keeps, 16, shares, free, count, workspace=ws)
+    m = n // 2 * blocks
+    assert info.tolist() == [m, int((kept >= m).sum()), 0, pages - m] and count.item() == pages - m
+    assert torch.equal(tables[::2].reshape(-1).sort().values, torch.arange(m, dtype=torch.int32, device="cuda"))
+    held = pool.view(torch.int32)[:, 0]
+    assert torch.equal(held[tables[::2].long()], kept)
+    moved = kept >= m
+    assert torch.equal(tables[::2][~moved], kept[~moved])
+    assert torch.equal(tables[::2][moved][kept[moved].argsort()], tables[::2][moved].sort().values)  # in order
+    assert torch.equal(free[:pages - m], torch.arange(m, pages, dtype=torch.int32, device="cuda"))
+
+
 @pytest.mark.parametrize("what", ["given back twice", "too often", "past the pages", "negative entry", "length", "negative keep",
                                   "negative count", "count", "taken", "negative taken", "full list"])
 def test_release_refusals(api, what):
