@@ -357,7 +357,7 @@ __device__ void run_pv(const Cta& c) {
     uint32_t tau = 0, events = 0;
     // Has the epilogue warps of both CTAs do what `event` says.
     auto post = [&](uint32_t event) {
-        if (lane < 2) {
+        if (lane < 2 && !*c.abort_flag) {  // (after an abort nobody waits for one event before the next)
             const uint32_t bar = map_rank(c.bar(BAR_EVENT), lane);
             mbar_arrive_expect_cluster(bar, 4);
             st_async(map_rank(c.sbase + kOffEvent, lane), event, bar);
@@ -622,7 +622,7 @@ __device__ void run_softmax(const Cta& c) {
         const Segment s = unit();
         const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
         if (term == 0) hm_s[half * kCtaPairs + hq].x = lpair;
-        named_bar_sync<kBarSoftmax, kSoftmaxThreads>();
+        if (named_bar_any<kBarSoftmax, kSoftmaxThreads>(*c.abort_flag != 0)) return;  // all eight warps end together
         if (half == 0) {
             if (units > 0) c.wait(BAR_FEMPTY, (units - 1) & 1);
             const float l = hm_s[hq].x + hm_s[kCtaPairs + hq].x;
@@ -1010,6 +1010,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         } else {
             prepare_first(c);
             run_epilogue(c);
+        }
+    }
+    if (*c.abort_flag != 0) {  // words on their way to the other CTA, which nobody waited for, arrive
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 20000) {
         }
     }
     tc_fence_before();
