@@ -960,6 +960,9 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
     p.clusters = d->sms / 2;
     // With fewer units than an eighth of the ranges a unit comes in more than eight pieces.
     p.few_units = units * 8 <= p.clusters ? 1 : 0;
+    p.most_joins = static_cast<int32_t>(std::min<int64_t>(units, p.clusters));
+    // A block of 256 threads, with cheaper barriers, while they have one request and a few units each.
+    p.small_plan = num_seqs <= 256 && units <= 1024 ? 1 : 0;
     const int64_t room = max_blocks_per_seq > 0 ? static_cast<int64_t>(max_blocks_per_seq) * block_size : full::kMaxLen;
     p.room = static_cast<int32_t>(std::min(room, full::kMaxLen));
     p.num_seqs = num_seqs;

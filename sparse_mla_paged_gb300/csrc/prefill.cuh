@@ -29,10 +29,10 @@ struct alignas(16) Start {
     int32_t gap, k, pad[2];
     Unit unit;  // number k
 };
-// Pieces of the unit that range c holds the first tile of and others go on with (0: none): in the
-// partial slots 2c or 2c + 1 (slot_lo), then 2(c + 1), 2(c + 2), ...
+// Pieces of a unit that range c starts and others go on with (0: none): in the partial slots 2c or
+// 2c + 1 (slot_lo), then 2(c + 1), 2(c + 2), ...
 struct alignas(16) Join {
-    int32_t unit, slot_lo, pieces, pad;
+    int32_t unit, slot_lo, pieces, c;
 };
 
 struct Layout {
@@ -72,14 +72,16 @@ struct Params {
     int* status;               // of the call, in its workspace
     int* step_status;          // of the device, see dsa_step_device_status
     Start* starts;             // [clusters]
-    Join* joins;               // [clusters]
+    Join* joins;               // [most_joins], in any order
     Unit* units;               // [units]
     uint8_t* qimg;             // [2 * clusters CTAs][2 units in turn][64 KB] query operands
     uint16_t* part_o;          // f16 bits [2 * clusters][16 blocks of 32 dims][16 groups of 8 pairs][32 dims][8 pairs]
     float* part_lse;           // [2 * clusters][128]
     int64_t cache_stride;
     int32_t num_seqs, max_rows, heads, block_size, max_blocks_per_seq, clusters;
+    int32_t most_joins;        // units, or ranges, whichever are fewer
     int32_t few_units;         // units come in more than eight pieces each
+    int32_t small_plan;        // few requests and units
     int32_t box_rows;          // tokens of a tensor-map box (8, 16 or 32), 0: per-thread copies
     FastDiv by_block, by_heads;
     int32_t room;              // tokens that a table holds

@@ -10,10 +10,11 @@ namespace dsa {
 namespace prefill {
 namespace {
 
-constexpr int kPlanThreads = 1024;  // 32 warps: scan() has a lane for each
+constexpr int kFewThreads = 256, kManyThreads = 1024;  // of a plan's block
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// Sum of v over the threads before this one; *total over all.
+// Sum of v over the threads before this one; *total over all. A lane for each warp.
+template <int kWarps>
 __device__ __forceinline__ int64_t scan(int64_t v, int64_t* sums, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t inc = v;
@@ -25,7 +26,7 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t* sums, int64_t* total
     __syncthreads();  // the previous scan's sums are read
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    int64_t mine = sums[lane];
+    int64_t mine = lane < kWarps ? sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, mine, o);
@@ -38,16 +39,22 @@ __device__ __forceinline__ int64_t scan(int64_t v, int64_t* sums, int64_t* total
 
 // One block. Threads share the requests (a scan gives each its first row, another its first unit),
 // then the units in equal parts, whatever request they belong to.
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid_constant__ Params p) {
     extern __shared__ int32_t mem[];
-    __shared__ int64_t sums[32];
+    constexpr int kWarps = kPlanThreads / 32;
+    __shared__ int64_t sums[kWarps];
+    __shared__ int32_t joins;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int32_t n = p.num_seqs, tid = threadIdx.x;
     int32_t* row0 = mem;              // [n + 1] first rows, cut to the rows there are
     int32_t* unit0 = row0 + n + 1;    // [n + 1] first units
     int32_t* range_k = unit0 + n + 1; // [clusters] unit that each range starts in
-    if (tid == 0) atomicExch(p.status, 0);
-    for (int32_t c = tid; c < p.clusters; c += kPlanThreads) p.joins[c].pieces = 0;
+    if (tid == 0) {
+        atomicExch(p.status, 0);
+        joins = 0;
+    }
+    for (int32_t j = tid; j < p.most_joins; j += kPlanThreads) p.joins[j].pieces = 0;
 
     const int32_t per = (n + kPlanThreads - 1) / kPlanThreads;
     const int32_t lo = min(n, tid * per), hi = min(n, lo + per);
@@ -58,7 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
         bad |= k < 0;
         mine += max(k, 0);
     }
-    int64_t at = scan(mine, sums, &total);
+    int64_t at = scan<kWarps>(mine, sums, &total);
     bad |= total > p.max_rows;
     auto cut = [&](int64_t row) { return static_cast<int32_t>(row < p.max_rows ? row : p.max_rows); };
     mine = 0;
@@ -70,7 +77,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
         bad |= base < 0 || (k > 0 && static_cast<int64_t>(base) + k > p.room);
         mine += (static_cast<int64_t>(k) * p.heads + kPairs - 1) / kPairs;
     }
-    int64_t unit = scan(mine, sums, &total);
+    int64_t unit = scan<kWarps>(mine, sums, &total);
     for (int32_t s = lo; s < hi; ++s) {
         unit0[s] = static_cast<int32_t>(unit);
         const int32_t end = s + 1 < hi ? row0[s + 1] : cut(at);
@@ -104,7 +111,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
     int64_t tiles = 0;
     walk([&](int32_t, int32_t, int32_t, int32_t, int32_t, int32_t t) { tiles += t; });
     int64_t all;
-    int64_t before = scan(tiles, sums, &all);
+    int64_t before = scan<kWarps>(tiles, sums, &all);
     full::Line line;
     line.ctas = static_cast<int32_t>(all < p.clusters ? all : p.clusters);
     // At most a quarter of a range, so that no range lies inside a gap.
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
         int32_t c0, c1;
         const full::UnitPieces q = full::unit_pieces(line, u, b, e, &c0, &c1);
         for (int32_t c = c0; c < c1; ++c) range_k[c] = u;
-        if (q.pieces > 1) p.joins[q.c_lo] = Join{u, q.slot_lo, q.pieces, 0};
+        if (q.pieces > 1) p.joins[atomicAdd(&joins, 1)] = Join{u, q.slot_lo, q.pieces, q.c_lo};
     });
     __syncthreads();
     for (int32_t c = tid; c < p.clusters; c += kPlanThreads) {
@@ -146,8 +153,8 @@ constexpr int kFlight = 4;  // pieces whose loads a warp has in flight
 // Partial k holds O_k / l_k (f16, E4M3 code units) and lse_k = m_k + log2 l_k; out = v_scale *
 // sum_k 2^(lse_k - M) O_k / sum_k 2^(lse_k - M). A warp folds pieces of 8 pairs x 32 dims, with
 // a running maximum per pair, kFlight pieces at a time.
-//   kSplit = 1: block (range, 32 dims, 64 pairs), a warp per 8-pair group, each over all pieces
-//   kSplit = 8: block (range, 32 dims, 8-pair group), the warps share the pieces and join
+//   kSplit = 1: block (join, 32 dims, 64 pairs), a warp per 8-pair group, each over all pieces
+//   kSplit = 8: block (join, 32 dims, 8-pair group), the warps share the pieces and join
 //               through shared memory; for few units, which the most pieces come with
 template <int kSplit>
 __global__ void __launch_bounds__(kJoinThreads, 5) prefill_join_kernel(const __grid_constant__ Params p) {
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kJoinThreads, 5) prefill_join_kernel(const __g
     const int pieces = q.pieces;
     if (pieces < 2) return;
     const Unit u = p.units[q.unit];
-    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? q.slot_lo : 2 * (static_cast<int>(blockIdx.x) + i)); };
+    auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? q.slot_lo : 2 * (q.c + i)); };
     constexpr int64_t kPartVecs = kPairs * kLatent / 8;
     const uint4* po = reinterpret_cast<const uint4*>(p.part_o) + (static_cast<int64_t>(blockIdx.y) * (kPairs / 8) + group) * kDims + lane;
     float acc[8] = {};
@@ -250,7 +257,8 @@ __global__ void __launch_bounds__(kJoinThreads, 5) prefill_join_kernel(const __g
 
 cudaError_t prefill_plan_setup(int clusters) {
     const int smem = 2 * (DSA_MAX_PLAN_SEQS + 1) * 4 + clusters * 4;
-    cudaError_t e = cudaFuncSetAttribute(prefill::prefill_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(prefill::prefill_plan_kernel<prefill::kManyThreads>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(prefill::prefill_join_kernel<1>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
     if (e != cudaSuccess) return e;
@@ -258,13 +266,15 @@ cudaError_t prefill_plan_setup(int clusters) {
 }
 
 cudaError_t launch_prefill_plan(const prefill::Params& p, cudaStream_t stream) {
-    prefill::prefill_plan_kernel<<<1, prefill::kPlanThreads, 2 * (p.num_seqs + 1) * 4 + p.clusters * 4, stream>>>(p);
+    const int smem = 2 * (p.num_seqs + 1) * 4 + p.clusters * 4;
+    if (p.small_plan) prefill::prefill_plan_kernel<prefill::kFewThreads><<<1, prefill::kFewThreads, smem, stream>>>(p);
+    else prefill::prefill_plan_kernel<prefill::kManyThreads><<<1, prefill::kManyThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_prefill_join(const prefill::Params& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.clusters, kLatent / prefill::kDims, p.few_units ? prefill::kPairs / 8 : 2);
+    cfg.gridDim = dim3(p.most_joins, kLatent / prefill::kDims, p.few_units ? prefill::kPairs / 8 : 2);
     cfg.blockDim = dim3(prefill::kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
