@@ -601,7 +601,7 @@ int32_t dsa_compact_pages(const dsa_page_pool* pools, int32_t num_pools, int32_t
 
 /*
  * dsa_set_wait_limit: the longest time in nanoseconds that one wait inside the kernels of
- * dsa_pool_scores and dsa_mla_decode_full may take, for later calls of the calling host
+ * dsa_pool_scores, dsa_mla_decode_full and dsa_mla_prefill may take, for later calls of the calling host
  * thread (a captured call keeps the limit of its capture); one second by default (0) and
  * at most.
  * A wait that runs out ends the call with DSA_ERR_TIMEOUT on the device and results that
@@ -611,7 +611,7 @@ int32_t dsa_set_wait_limit(uint64_t limit_ns);
 
 /*
  * Device status of the latest call on a caller workspace (dsa_mla_decode_ws /
- * dsa_mla_decode_host / dsa_mla_decode_full), on the library workspace of the current device
+ * dsa_mla_decode_host / dsa_mla_decode_full / dsa_mla_prefill), on the library workspace of the current device
  * (dsa_last_device_status), or on the fixed array of dsa_mla_decode_static
  * (dsa_static_device_status; like that entry point it allocates nothing). Each
  * synchronises the stream, writes the status to *status_out and returns DSA_OK, or
@@ -623,7 +623,7 @@ int32_t dsa_static_device_status(int32_t* status_out, void* stream);
 
 /*
  * The first device status that dsa_pool_scores calls without a device_status word or any
- * dsa_mla_decode_full calls recorded on the current device since this was last called (by
+ * dsa_mla_decode_full, dsa_mla_prefill or dsa_copy_pages calls recorded on the current device since this was last called (by
  * any host thread), and clears it: one check after a step, whoever keeps its workspaces.
  * Synchronises the stream, writes the status to *status_out and returns DSA_OK, or
  * returns DSA_ERR_CUDA. Calls on other streams count once their work has run.

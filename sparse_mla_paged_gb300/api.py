@@ -378,7 +378,7 @@ _wait_limits = threading.local()
 
 @contextlib.contextmanager
 def wait_limit(limit_ns: int):
-    """dsa_set_wait_limit for this thread's pool_scores and decode_full calls inside the block
+    """dsa_set_wait_limit for this thread's pool_scores, decode_full and prefill calls inside the block
     (0: the default), the limit outside it after that."""
     if not 0 <= limit_ns < 1 << 64:
         raise ValueError("limit_ns must be a 64-bit number of nanoseconds")
@@ -730,8 +730,8 @@ def last_device_status(stream=None) -> int:
 
 
 def step_device_status(stream=None) -> int:
-    """First device status of pool_scores calls without a device_status and of decode_full calls on
-    the current device since this was last called; clears it."""
+    """First device status of pool_scores calls without a device_status and of decode_full, prefill and
+    copy_pages calls on the current device since this was last called; clears it."""
     v = _lib.ctypes.c_int32(0)
     check(_lib.load().dsa_step_device_status(_lib.ctypes.byref(v), _stream(stream)), "dsa_step_device_status")
     return int(v.value)

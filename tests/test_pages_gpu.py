@@ -315,6 +315,22 @@ def test_release_refusals(api, what):
     assert info[2] == (0 if what == "negative entry" else ref.BOUNDS)
 
 
+def test_a_list_that_is_short(api):
+    """A plan over the whole buffer of a list with two pages: tokens without a page get no slot, and the
+    release that brings the list up to date reports it; what the plan did not get is left out."""
+    base, new = cu(np.array([0, 0], np.int32)), cu(np.array([20, 20], np.int32))
+    tables = torch.full((2, 4), 9, dtype=torch.int32, device="cuda")
+    free, count = cu(np.array([7, 3] + [-1] * 6, np.int32)), cu(np.array([2], np.int32))
+    plan = api.plan_step(base, new, free, 8, tables, max_rows=40)
+    assert plan.info.tolist()[:2] == [40, 6]
+    slots = plan.slots.tolist()
+    assert slots[:16] == list(range(56, 64)) + list(range(24, 32)) and slots[16:] == [-1] * 24
+    shares = torch.zeros(8, dtype=torch.int32, device="cuda")
+    info = api.release_pages(tables, new, cu(np.array([8, 0], np.int32)), 8, shares, free, count, taken=plan.info[1:2])
+    assert info.tolist() == [1, 1, ref.BOUNDS, 1] and free.tolist() == [3] + [-1] * 7
+    assert tables.tolist() == [[7, -1, -1, 9], [-1, -1, -1, 9]]
+
+
 def test_release_without_requests(api):
     free = np.arange(16, dtype=np.int32)
     run_release(api, np.zeros((0, 3), np.int32), [], [], 8, np.zeros(16, np.int32), free, 9, 4)
