@@ -15,16 +15,26 @@
 // so that a CTA softmaxes its own pairs and no probability leaves it, while the second product has
 // N = 128 (full.cu: 64): 6 KB of operands for 64 cycles of arithmetic, not for 32.
 //
-//   warp 0, 1    load K and V tiles into rings of three each ([16 groups of 8 tokens][blocks of 128
-//                dims][8 tokens][128 bytes], 128-byte swizzle): tensor-map boxes of a page's rows
-//                when pages and tiles fit each other, else 16-byte copies
+//   warp 0, 1    load K tiles into a ring of two and V tiles into one of four ([16 groups of 8
+//                tokens][blocks of 128 dims][8 tokens][128 bytes], 128-byte swizzle): tensor-map
+//                boxes of a page's rows when pages and tiles fit each other, else 16-byte copies
 //   warp 2, 3    issue Q K^T and P V (rank 0); tell rank 0 of the loaded K tiles (rank 1)
 //   warps 4-11   softmax, two per TMEM lane quarter
 //   warps 12-15  make the next unit's query operand and put it in place, rescale O when a reference
 //                moves, write a unit's output
 //
-// (The queries by four warps of their own, at 96 registers a thread instead of 128, took 4 % more
-// on long units and on short ones.)
+// Bound by the tensor pipe, and on long calls by the power that it may take: Q K^T counts twice for
+// the two query terms and P V twice for those of P', 4 x 128 x 128 x 512 multiply-adds of E4M3 per
+// unit and tile. 1024 rows of 64 heads after 31.7k cached tokens (4.5 TFLOP of bf16 arithmetic):
+// 2.44 ms in short bursts, 1820 TFLOP/s, 95 % of what a bf16 matrix product of the library
+// reaches; one prompt of 4096 rows, 795 us, 1380; 512 rows over 4096 tokens, 190 us, 1350.
+//
+// Measured beside this split: three K and three V slots, 1 to 4 % more (a value tile is held until
+// its softmax is done, a key tile is not); the queries by four warps of their own, at 96 registers
+// a thread instead of 128, 4 % more on long units and on short ones; O's dims as the outer
+// loop of P V, with either half let go early, 10 %; the next tile's scores read ahead, 5 %
+// (the registers); softmax loops with any test more, 2 to 7 %.
+//
 // A reference that moves in one CTA rescales columns of O in both. The CTA that asks writes the
 // factors into both; the warp that issues P V finds its mark before the tile's product, has
 // warps 12-15 of both CTAs rescale, and goes on. Tiles that no pair asks in pay nothing for it.
@@ -46,7 +56,7 @@ namespace prefill {
 namespace {
 
 constexpr int kCtaPairs = kPairs / 2;
-constexpr int kSlots = 3;                           // of each ring
+constexpr int kKeySlots = 2, kValueSlots = 4;       // of the rings
 constexpr int kKeyTokens = kTile / 2;               // tokens of a tile that a CTA brings as keys
 constexpr int kDims = kLatent / 2;                  // dims that it brings as values
 constexpr int kSlotBytes = kKeyTokens * kLatent;    // 32 KB
@@ -65,8 +75,8 @@ constexpr int kBarSoftmax = 1;
 constexpr int kBarPair0 = 2;  // 2..5: the two softmax warps of a lane quarter
 constexpr int kBarFirst = 6;  // the first unit's query operand is made
 
-constexpr int kOffV = kSlots * kSlotBytes;
-constexpr int kOffP = 2 * kSlots * kSlotBytes;               // P' [2 buffers][hi, lo]
+constexpr int kOffV = kKeySlots * kSlotBytes;
+constexpr int kOffP = (kKeySlots + kValueSlots) * kSlotBytes;  // P' [2 buffers][hi, lo]
 constexpr int kOffHm = kOffP + 4 * kPTermBytes;              // float2 [2 token halves][64] tile maximum, account; row sums at the end
 constexpr int kOffAlpha = kOffHm + 2 * kCtaPairs * 8;        // float [2 tile parities][128] rescale factors, of both CTAs
 constexpr int kOffF = kOffAlpha + 2 * kPairs * 4;            // float [128] output factors, of both CTAs
@@ -80,23 +90,23 @@ constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffBars = (kOffAbort + 4 + 7) / 8 * 8;
 // (both): in either CTA; (0): in rank 0, both CTAs arrive.
 enum {
-    BAR_KFULL0 = 0,                    // own half of a K slot loaded
-    BAR_VFULL0 = BAR_KFULL0 + kSlots,  // own half of a V slot loaded
-    BAR_KPEER0 = BAR_VFULL0 + kSlots,  // (0) rank 1's half of a K slot loaded
-    BAR_KEMPTY0 = BAR_KPEER0 + kSlots, // (both) its Q K^T is done
-    BAR_VEMPTY0 = BAR_KEMPTY0 + kSlots,// (both) its P V is done
-    BAR_PFULL0 = BAR_VEMPTY0 + kSlots, // (0) 2: P' buffers written, V there
-    BAR_PVDONE0 = BAR_PFULL0 + 2,      // (both) 2: the P V reading it is done
-    BAR_SFULL = BAR_PVDONE0 + 2,       // (both) S written
-    BAR_SEMPTY,                        // (0) S read
-    BAR_QFULL,                         // (0) query operands in place
-    BAR_QEMPTY,                        // (both) the unit's last Q K^T is done
-    BAR_EVENT,                         // (both) something for the epilogue warps
-    BAR_OFREE,                         // (0) they did it
-    BAR_FFULL,                         // (both) output factors written
-    BAR_FEMPTY,                        // (both) and used
-    BAR_UDONE0,                        // 2: the softmax warps are done with a unit (by its parity)
-    BAR_DRAIN = BAR_UDONE0 + 2,        // (0) every MMA is done
+    BAR_KFULL0 = 0,                          // own half of a K slot loaded
+    BAR_VFULL0 = BAR_KFULL0 + kKeySlots,     // own half of a V slot loaded
+    BAR_KPEER0 = BAR_VFULL0 + kValueSlots,   // (0) rank 1's half of a K slot loaded
+    BAR_KEMPTY0 = BAR_KPEER0 + kKeySlots,    // (both) its Q K^T is done
+    BAR_VEMPTY0 = BAR_KEMPTY0 + kKeySlots,   // (both) its P V is done
+    BAR_PFULL0 = BAR_VEMPTY0 + kValueSlots,  // (0) 2: P' buffers written, V there
+    BAR_PVDONE0 = BAR_PFULL0 + 2,            // (both) 2: the P V reading it is done
+    BAR_SFULL = BAR_PVDONE0 + 2,             // (both) S written
+    BAR_SEMPTY,                              // (0) S read
+    BAR_QFULL,                               // (0) query operands in place
+    BAR_QEMPTY,                              // (both) the unit's last Q K^T is done
+    BAR_EVENT,                               // (both) something for the epilogue warps
+    BAR_OFREE,                               // (0) they did it
+    BAR_FFULL,                               // (both) output factors written
+    BAR_FEMPTY,                              // (both) and used
+    BAR_UDONE0,                              // 2: the softmax warps are done with a unit (by its parity)
+    BAR_DRAIN = BAR_UDONE0 + 2,              // (0) every MMA is done
     kNumBars
 };
 constexpr int kSmem = kOffBars + kNumBars * 8;
@@ -203,6 +213,7 @@ template <bool kValues>
 __device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
     constexpr int kTokens = kValues ? kTile : kKeyTokens;
     constexpr int kFull = kValues ? BAR_VFULL0 : BAR_KFULL0, kEmpty = kValues ? BAR_VEMPTY0 : BAR_KEMPTY0;
+    constexpr int kSlots = kValues ? kValueSlots : kKeySlots;
     const Params& p = c.p;
     const int lane = threadIdx.x & 31;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * (kValues ? kDims : kLatent);
@@ -264,6 +275,7 @@ __device__ void run_load_copies(const Cta& c) {
     constexpr int kFull = kValues ? BAR_VFULL0 : BAR_KFULL0, kEmpty = kValues ? BAR_VEMPTY0 : BAR_KEMPTY0;
     constexpr int kGroup = kValues ? kVGroup : kKGroup;
     constexpr int kEach = kTokens / 32;  // tokens that a lane looks up
+    constexpr int kSlots = kValues ? kValueSlots : kKeySlots;
     const Params& p = c.p;
     const int lane = threadIdx.x & 31, sub = lane >> 3, piece = lane & 7;
     const uint8_t* cache = (kValues ? p.v_cache + c.rank * kDims : p.k_cache) + piece * 16;
@@ -320,6 +332,7 @@ __device__ void run_load_copies(const Cta& c) {
 // MMA warps of rank 0 (converged, one elected lane issues)
 // ------------------------------------------------------------------------------------
 __device__ void run_qk(const Cta& c) {
+    constexpr int kSlots = kKeySlots;
     const uint32_t idesc = idesc_e4m3(256, kTile, false, false);
     const uint32_t el = elect_one();
     uint32_t tau = 0, units = 0;
@@ -349,6 +362,7 @@ __device__ void run_qk(const Cta& c) {
 }
 
 __device__ void run_pv(const Cta& c) {
+    constexpr int kSlots = kValueSlots;
     const int lane = threadIdx.x & 31;
     const uint32_t idesc = idesc_e4m3(256, kPairs, true, false);
     const uint32_t el = elect_one();
@@ -405,6 +419,7 @@ __device__ void run_pv(const Cta& c) {
 
 // Rank 1: its half of each K slot, to rank 0.
 __device__ void run_forward(const Cta& c) {
+    constexpr int kSlots = kKeySlots;
     const int lane = threadIdx.x & 31;
     uint32_t tau = 0;
     for (Walk w(c);; w.advance()) {
@@ -424,6 +439,7 @@ __device__ void run_forward(const Cta& c) {
 // softmax warps
 // ------------------------------------------------------------------------------------
 __device__ void run_softmax(const Cta& c) {
+    constexpr int kSlots = kValueSlots;
     const Params& p = c.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sw = warp - kSoftmax0;               // 0..7
@@ -939,11 +955,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     Cta c{p, smem, smem_u32(smem), cluster_rank(), blockIdx.x >> 1, reinterpret_cast<volatile int*>(smem + kOffAbort)};
 
     if (tid == 0) {
-        for (int e = 0; e < kSlots; ++e) {
+        for (int e = 0; e < kKeySlots; ++e) {
             mbar_init(c.bar(BAR_KFULL0 + e), kTma ? 1 : 32);
-            mbar_init(c.bar(BAR_VFULL0 + e), kTma ? 1 : 32);
             mbar_init(c.bar(BAR_KPEER0 + e), 1);
             mbar_init(c.bar(BAR_KEMPTY0 + e), 1);
+        }
+        for (int e = 0; e < kValueSlots; ++e) {
+            mbar_init(c.bar(BAR_VFULL0 + e), kTma ? 1 : 32);
             mbar_init(c.bar(BAR_VEMPTY0 + e), 1);
         }
         for (int i = 0; i < 2; ++i) {
