@@ -267,21 +267,22 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
     __syncwarp();
 }
 
-// The same by 16-byte copies: an instruction brings 128 bytes of each of four rows, so that a row's
-// address is found once for all its blocks.
-template <bool kValues>
-__device__ void run_load_copies(const Cta& c) {
-    constexpr int kTokens = kValues ? kTile : kKeyTokens;
-    constexpr int kFull = kValues ? BAR_VFULL0 : BAR_KFULL0, kEmpty = kValues ? BAR_VEMPTY0 : BAR_KEMPTY0;
-    constexpr int kGroup = kValues ? kVGroup : kKGroup;
-    constexpr int kEach = kTokens / 32;  // tokens that a lane looks up
-    constexpr int kSlots = kValues ? kValueSlots : kKeySlots;
+// The same by 16-byte copies: an instruction brings 128 bytes of each of four rows. Both warps run one
+// code, for what they bring of a tile has one shape: four half rows of 256 bytes for each lane to
+// look up, of two tokens' keys or of four tokens' values. (2000 rows of 20 heads over pages of 100
+// tokens 134 us; with a code each 165, and more the more it was unrolled: the instruction cache
+// holds the softmax as well. Boxes, where a page takes them: 124.)
+__device__ void run_load_copies(const Cta& c, bool values) {
+    constexpr int kEach = 4;
     const Params& p = c.p;
     const int lane = threadIdx.x & 31, sub = lane >> 3, piece = lane & 7;
-    const uint8_t* cache = (kValues ? p.v_cache + c.rank * kDims : p.k_cache) + piece * 16;
-    const uint32_t ring = c.sbase + (kValues ? kOffV : 0);
-    const int32_t pos0 = lane + (kValues ? 0 : static_cast<int32_t>(c.rank) * kKeyTokens);
-    uint32_t tau = 0;
+    const int keys = values ? 0 : 1;
+    const uint32_t slots = values ? kValueSlots : kKeySlots, group = values ? kVGroup : kKGroup;
+    const int full = values ? BAR_VFULL0 : BAR_KFULL0, empty = values ? BAR_VEMPTY0 : BAR_KEMPTY0;
+    const uint8_t* cache = values ? p.v_cache + c.rank * kDims : p.k_cache;
+    const uint32_t ring = c.sbase + (values ? kOffV : 0) + sub * 128 + ((piece ^ sub) << 4);
+    const int32_t pos0 = lane + (values ? 0 : static_cast<int32_t>(c.rank) * kKeyTokens);
+    uint32_t e = 0, round = 0, tau = 0;
     for (Walk w(c);; w.advance()) {
         const Segment& s = w.s;
         int32_t row_next[kEach], page_next[kEach];
@@ -290,38 +291,43 @@ __device__ void run_load_copies(const Cta& c) {
         auto look = [&](int32_t t) {
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const int32_t pos = t * kTile + pos0 + 32 * i;
+                const int32_t pos = t * kTile + pos0 + 32 * (i >> keys);
                 row_next[i] = -1;
                 page_next[i] = t < s.t1 && pos < s.max_len ? page_of(p, s.u.seq, pos, &row_next[i]) : 0;
             }
         };
         look(s.t0);
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
-            int64_t mine[kEach];
+            const uint8_t* mine[kEach];
+            uint32_t live[kEach];  // lanes whose token there is
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 if (page_next[i] < 0) report(p, kStatusBounds);
-                mine[i] = page_next[i] < 0 || row_next[i] < 0 ? -1 : page_next[i] * p.cache_stride + static_cast<int64_t>(row_next[i]) * kLatent;
+                const bool there = page_next[i] >= 0 && row_next[i] >= 0;
+                live[i] = __ballot_sync(0xffffffffu, there) >> sub;
+                mine[i] = cache;
+                if (there) mine[i] += page_next[i] * p.cache_stride + static_cast<int64_t>(row_next[i]) * kLatent + (i & keys) * 256;
             }
             look(t + 1);
-            const int e = static_cast<int>(tau % kSlots);
-            if (tau >= kSlots) c.wait(kEmpty + e, (tau / kSlots - 1) & 1);
-            if (!kValues && lane == 0) *c.progress() = tau;
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                // Rows j and j + 4 of an 8-row group in turn.
-                const uint32_t dst = ring + e * kSlotBytes + 4 * i * kGroup + sub * 128 + ((piece ^ sub) << 4);
+            if (round > 0) c.wait(empty + e, (round - 1) & 1);
+            if (!values && lane == 0) *c.progress() = tau;
+            const uint32_t slot = ring + e * kSlotBytes;
 #pragma unroll 2
-                for (int j = 0; j < 32; j += 4) {
-                    const int64_t at = __shfl_sync(0xffffffffu, mine[i], j + sub);
-                    const uint8_t* src = cache + (at >= 0 ? at : 0);
-                    const uint32_t size = at >= 0 ? 16u : 0u;
-                    const uint32_t d = (dst + (j >> 3) * kGroup + (j & 4) * 128) ^ ((j & 4) << 4);
+            for (int j = 0; j < 32; j += 4) {
 #pragma unroll
-                    for (int b = 0; b < (kValues ? kDims : kLatent) / 128; ++b) cp_async_16_zfill(d + b * 1024, src + b * 128, size);
+                for (int i = 0; i < kEach; ++i) {
+                    // Rows j and j + 4 of an 8-row group in turn.
+                    const uint32_t dst = slot + 4 * (i >> keys) * group + (i & keys) * 2048;
+                    const auto half = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(mine[i]), j + sub);
+                    const uint8_t* src = reinterpret_cast<const uint8_t*>(half) + piece * 16;
+                    const uint32_t size = (live[i] >> j & 1u) * 16u;
+                    const uint32_t d = (dst + (j >> 3) * group + (j & 4) * 128) ^ ((j & 4) << 4);
+                    cp_async_16_zfill(d, src, size);
+                    cp_async_16_zfill(d + 1024, src + 128, size);
                 }
             }
-            cp_async_arrive_noinc(c.bar(kFull + e));
+            cp_async_arrive_noinc(c.bar(full + e));
+            if (++e == slots) e = 0, ++round;
         }
         if (s.last) break;
     }
@@ -1005,12 +1011,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if ((c.sbase & 1023u) != 0u) {  // the swizzled operands count on it
         if (tid == 0) report(p, DSA_ERR_UNSUPPORTED);
     } else if (c.begin < c.end) {
-        if (warp == 0) {
-            if constexpr (kTma) run_load_tma<false>(c, &kmap);
-            else run_load_copies<false>(c);
-        } else if (warp == 1) {
-            if constexpr (kTma) run_load_tma<true>(c, &vmap);
-            else run_load_copies<true>(c);
+        if (warp < 2) {
+            if constexpr (!kTma) run_load_copies(c, warp == 1);
+            else if (warp == 0) run_load_tma<false>(c, &kmap);
+            else run_load_tma<true>(c, &vmap);
         } else if (warp < kSoftmax0) {
             if (c.rank == 0) {
                 if (warp == 2) run_qk(c);
