@@ -402,7 +402,8 @@ __device__ void run_pv(const Cta& c) {
             // P'^T: 64 pairs of each CTA x 32 tokens, K-major core matrices.
             const uint64_t vdesc = smem_desc(c.sbase + kOffV + e * kSlotBytes, 1024, kVGroup, kSwizzle128B);
             const uint64_t pdesc = pdesc0 + static_cast<uint64_t>((pb * 2 * kPTermBytes) >> 4);
-#pragma unroll
+// (Rolled: 1 to 3 % less than four copies of the code.)
+#pragma unroll 1
             for (int j = 0; j < kTile / 32; ++j) {
                 const uint64_t bh = pdesc + static_cast<uint64_t>((j * 2048) >> 4);
                 const uint64_t bl = pdesc + static_cast<uint64_t>((kPTermBytes + j * 2048) >> 4);
