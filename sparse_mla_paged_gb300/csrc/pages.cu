@@ -3,7 +3,13 @@
 // whole numbers, so results do not depend on an order: pages are listed by their number.
 //
 // The books (tables, shares, free list) are bound by latency: a launch each for what every block
-// has to know of the others'. Page data is bound by HBM.
+// has to know of the others', the launches overlapped, and within each a few dependent loads and
+// barriers. 64 requests that give back their drafts 5 us (two launches), half of 256 requests with
+// 1.2 thousand pages each 15, a fork of four ways 4.4 (two launches), a pool of 380 pages compacted
+// 8 (three launches).
+// Page data is bound by HBM: 1024 pages of two pools in four layers, 338 MB read and written, 54 us,
+// 6.2 TB/s, 92 % of a plain copy's rate. Blocks of 256 threads with four 16-byte pieces in flight
+// each, eight blocks to an SM, are what it takes; pieces pass the caches by, as they are not read again.
 #include "pages.cuh"
 #include "ptx.cuh"
 
@@ -14,7 +20,9 @@ namespace {
 constexpr int kMarkThreads = 256;
 constexpr int kListThreads = 1024;
 constexpr int kListWarps = kListThreads / 32;
-constexpr int kFewForks = 128;  // up to so many take a block of as many threads, whose barriers are cheaper
+// Up to kFewForks forks are planned by a block of kForkThreads, whose barriers are cheaper (4 forks 4.4
+// us, 5.8 with kManyForkThreads; 240 forks 7.2 and 8.4; 512 forks 10.3 and 10.6; 1024 forks 16.2 and 14.9).
+constexpr int kFewForks = 512, kForkThreads = 256, kManyForkThreads = 1024;
 
 __device__ __forceinline__ void report(int* status) { atomicCAS(status, 0, DSA_ERR_DEVICE_BOUNDS); }
 __device__ __forceinline__ void wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -94,19 +102,19 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* sums, int32_t*
 
 // One block: which forks are made (its child is named by no earlier fork and is nobody's parent),
 // how many pages each shares and which fresh page takes its last, partly filled one.
-template <int kForkThreads>
-__global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_constant__ ForkParams p) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) fork_plan_kernel(const __grid_constant__ ForkParams p) {
     extern __shared__ int32_t first_child[];  // [num_seqs] first fork that names the child
-    __shared__ int32_t sums[kForkThreads / 32];
+    __shared__ int32_t sums[kThreads / 32];
     uint32_t* parent_bits = reinterpret_cast<uint32_t*>(first_child + p.t.num_seqs);
     let_next();
     const int tid = threadIdx.x;
     const int32_t n = p.t.num_seqs;
-    for (int32_t i = tid; i < n; i += kForkThreads) first_child[i] = INT32_MAX;
-    for (int32_t i = tid; i < (n + 31) / 32; i += kForkThreads) parent_bits[i] = 0;
+    for (int32_t i = tid; i < n; i += kThreads) first_child[i] = INT32_MAX;
+    for (int32_t i = tid; i < (n + 31) / 32; i += kThreads) parent_bits[i] = 0;
     __syncthreads();
     bool bad = false;
-    for (int32_t f = tid; f < p.forks; f += kForkThreads) {
+    for (int32_t f = tid; f < p.forks; f += kThreads) {
         const int32_t a = p.parents[f], c = p.children[f];
         if (a < 0 || c < 0) continue;
         if (a >= n || c >= n) {
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
     }
     __syncthreads();
     int32_t taken = 0, made_here = 0;
-    for (int32_t f0 = 0; f0 < p.forks; f0 += kForkThreads) {
+    for (int32_t f0 = 0; f0 < p.forks; f0 += kThreads) {
         const int32_t f = f0 + tid;
         int32_t src = -1, whole = -1;
         if (f < p.forks) {
@@ -142,7 +150,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
             }
         }
         int32_t total;
-        const int32_t at = taken + block_scan<kForkThreads / 32>(src >= 0 ? 1 : 0, sums, &total);
+        const int32_t at = taken + block_scan<kThreads / 32>(src >= 0 ? 1 : 0, sums, &total);
         taken += total;
         if (f < p.forks) {
             int32_t dst = -1;
@@ -160,7 +168,7 @@ __global__ void __launch_bounds__(kForkThreads) fork_plan_kernel(const __grid_co
         }
     }
     int32_t made;
-    block_scan<kForkThreads / 32>(made_here, sums, &made);
+    block_scan<kThreads / 32>(made_here, sums, &made);
     bad = __syncthreads_or(bad);
     if (tid == 0) {
         p.info[0] = made;
@@ -504,9 +512,9 @@ int list_blocks(const Tables& t, int sms) { return at_most((mark_words(t.num_pag
 
 cudaError_t pages_setup() {
     const int smem = DSA_MAX_PLAN_SEQS * 4 + DSA_MAX_PLAN_SEQS / 8;
-    const cudaError_t e = cudaFuncSetAttribute(pages::fork_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(pages::fork_plan_kernel<pages::kManyForkThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(pages::fork_plan_kernel<pages::kFewForks>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(pages::fork_plan_kernel<pages::kForkThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 cudaError_t launch_copy_pages(const pages::CopyParams& p, int sms, cudaStream_t stream) {
@@ -517,8 +525,8 @@ cudaError_t launch_copy_pages(const pages::CopyParams& p, int sms, cudaStream_t 
 
 cudaError_t launch_fork_pages(const pages::ForkParams& p, int sms, cudaStream_t stream) {
     const int smem = p.t.num_seqs * 4 + (p.t.num_seqs + 31) / 32 * 4;
-    if (p.forks <= pages::kFewForks) pages::fork_plan_kernel<pages::kFewForks><<<1, pages::kFewForks, smem, stream>>>(p);
-    else pages::fork_plan_kernel<1024><<<1, 1024, smem, stream>>>(p);
+    if (p.forks <= pages::kFewForks) pages::fork_plan_kernel<pages::kForkThreads><<<1, pages::kForkThreads, smem, stream>>>(p);
+    else pages::fork_plan_kernel<pages::kManyForkThreads><<<1, pages::kManyForkThreads, smem, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t turns = (p.t.max_blocks + pages::kCopyThreads - 1) / pages::kCopyThreads;
