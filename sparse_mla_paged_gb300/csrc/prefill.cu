@@ -714,8 +714,9 @@ __device__ __forceinline__ void make_operand(const Cta& c, const Unit& u, Ahead 
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 w[j][k] = v[k];
-                amax[j] = max(amax[j], max(v[k] << 16 & 0x7FFFFFFFu, v[k] & 0x7FFF0000u));
+                amax[j] = __vmaxu2(amax[j], v[k] & 0x7FFF7FFFu);
             }
+            amax[j] = max(amax[j] << 16, amax[j] & 0xFFFF0000u);
         }
 #pragma unroll
         for (int k = kTurn; k < kPrepPairs; ++k) q.x[k - kTurn] = q.x[k];
@@ -742,16 +743,17 @@ __device__ __forceinline__ void make_operand(const Cta& c, const Unit& u, Ahead 
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int j = 0; j < kTurn; ++j) {
-                float vh[4], vl[4];
+                uint32_t h2[2], l2[2];
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const uint32_t two = w[j][2 * k + m / 2];
-                    const float v = __uint_as_float(m & 1 ? two & 0xFFFF0000u : two << 16) * sc[j];
-                    vh[m] = __uint_as_float(__float_as_uint(v) & 0xFFF00000u);
-                    vl[m] = v - vh[m];
+                for (int m = 0; m < 2; ++m) {
+                    const uint32_t two = w[j][2 * k + m];
+                    const __half2 v = __floats2half2_rn(__uint_as_float(two << 16) * sc[j], __uint_as_float(two & 0xFFFF0000u) * sc[j]);
+                    h2[m] = *reinterpret_cast<const uint32_t*>(&v) & 0xFF80FF80u;
+                    const __half2 r = __hsub2(v, *reinterpret_cast<const __half2*>(&h2[m]));
+                    l2[m] = *reinterpret_cast<const uint32_t*>(&r);
                 }
-                hi[j][k] = f32x2_to_e4m3x2(vh[0], vh[1]) | (f32x2_to_e4m3x2(vh[2], vh[3]) << 16);
-                lo[j][k] = f32x2_to_e4m3x2(vl[0], vl[1]) | (f32x2_to_e4m3x2(vl[2], vl[3]) << 16);
+                hi[j][k] = f16x4_to_e4m3x4(h2[0], h2[1]);
+                lo[j][k] = f16x4_to_e4m3x4(l2[0], l2[1]);
             }
 #pragma unroll
         for (int j = 0; j < kTurn; ++j) {  // both rows' 16 bytes, one sector, one store
@@ -915,6 +917,7 @@ __device__ void run_epilogue(const Cta& c) {
             if (whole) {
                 // Neighbouring lanes exchange pairs and dims, so that a store has two dims of a pair.
                 const int odd = lane & 1;
+                const uint32_t pick = odd ? 0x3276u : 0x5410u;
                 uint16_t* at = p.out + (s.u.pair0 + 32 * g + odd) * kLatent + dim0 + (lane & ~1);
                 const int left = s.u.valid - 32 * g - odd;
 #pragma unroll
@@ -922,10 +925,10 @@ __device__ void run_epilogue(const Cta& c) {
                     const float2 f = *reinterpret_cast<const float2*>(f_s + 32 * g + i);
 #pragma unroll
                     for (int mc = 0; mc < 2; ++mc) {
-                        const float a = __uint_as_float(v[mc][i]) * f.x, b = __uint_as_float(v[mc][i + 1]) * f.y;
-                        const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                        const __nv_bfloat162 r = odd ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-                        if (i < left) *reinterpret_cast<__nv_bfloat162*>(at + i * kLatent + mc * 128) = r;
+                        const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[mc][i]) * f.x, __uint_as_float(v[mc][i + 1]) * f.y);
+                        const uint32_t mine = *reinterpret_cast<const uint32_t*>(&r);
+                        const uint32_t two = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
+                        if (i < left) *reinterpret_cast<uint32_t*>(at + i * kLatent + mc * 128) = two;
                     }
                 }
             } else {

@@ -533,6 +533,14 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float first, float second) {
         : "f"(second), "f"(first));
     return r;
 }
+// The same for two pairs of halves, lowest first.
+__device__ __forceinline__ uint32_t f16x4_to_e4m3x4(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 s, t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 s, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %2;\n\tmov.b32 %0, {s, t};\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
