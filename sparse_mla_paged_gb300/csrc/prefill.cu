@@ -666,7 +666,8 @@ __device__ void run_softmax(const Cta& c) {
 // ------------------------------------------------------------------------------------
 constexpr int kPrepPairs = 4;                         // pairs whose loads are in flight together
 constexpr int kOwnPairs = kCtaPairs / kEpilogueWarps; // pairs of a warp
-static_assert(kPrepPairs * (kSoftmaxWarps + 2 * kEpilogueWarps) == kCtaPairs, "the first unit's: a turn of all warps and another of these");
+constexpr int kFirstPairs = (kCtaPairs - kPrepPairs * kSoftmaxWarps) / kEpilogueWarps;  // of the first unit
+static_assert(kFirstPairs % kPrepPairs == 0 && kOwnPairs % kPrepPairs == 0, "whole turns");
 
 // Query operand rows of a warp's kPrepPairs or more pairs: lane l has dims [16l, 16l+16). A
 // head's bf16 query becomes two E4M3 terms after a scaling by a power of two (exact for elements from
@@ -792,16 +793,12 @@ __device__ uint32_t find_broken(const Cta& c, const Segment& s) {
 __device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
     return c.p.qimg + (static_cast<int64_t>(blockIdx.x) * 2 + parity) * kQImageBytes;
 }
-// The first unit's operand is made by all warps that have nothing to do yet.
-__device__ void prepare_first(const Cta& c) {
+// The first unit's operand is made by all warps that have nothing to do yet: kPrepPairs pairs by each
+// softmax warp, the others by the epilogue warps.
+__device__ void prepare_first(const Cta& c, int sw) {
     const Unit& u = c.p.starts[c.cluster].unit;
-    const int warp = threadIdx.x >> 5;
-    int h0 = (warp - kSoftmax0) * kPrepPairs;
+    const int h0 = sw * kPrepPairs;
     make_operand(c, u, ask_queries(c, u, h0), 0, h0, kPrepPairs, query_image(c, 0));
-    if (warp >= kEpilogue0) {
-        h0 += kEpilogueWarps * kPrepPairs;
-        make_operand(c, u, ask_queries(c, u, h0), 0, h0, kPrepPairs, query_image(c, 0));
-    }
     named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
 }
 
@@ -814,15 +811,16 @@ __device__ void prepare_query(const Cta& c, const Segment& s, uint32_t units) {
         const int first = static_cast<int>(c.rank) * kCtaPairs + q4 * kOwnPairs, count = min(kOwnPairs, u.valid - first);
         if (count > 0) bulk_prefetch_l2(c.p.q + (u.pair0 + first) * kLatent, count * kLatent * 2);
     }
-    Ahead x{};
-    if (units > 0) x = ask_queries(c, s.u, q4 * kOwnPairs);
+    const int count = units > 0 ? kOwnPairs : kFirstPairs, h0 = (units > 0 ? 0 : kSoftmaxWarps * kPrepPairs) + q4 * count;
+    const Ahead x = ask_queries(c, s.u, h0);
     const uint32_t broken = find_broken(c, s);
     // The scales and marks of the unit before the last are read. (One barrier for both parities
     // could pass two phases meanwhile.)
     if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
-    if (units > 0) make_operand(c, s.u, x, parity, q4 * kOwnPairs, kOwnPairs, query_image(c, parity));
+    make_operand(c, s.u, x, parity, h0, count, query_image(c, parity));
     if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = broken;
     __syncwarp();
+    if (units == 0) named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
 }
 
 // Its image into tensor memory, once the unit before has no more use for the place.
@@ -1031,10 +1029,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 run_forward(c);
             }
         } else if (warp < kEpilogue0) {
-            prepare_first(c);
+            prepare_first(c, warp - kSoftmax0);
             run_softmax(c);
         } else {
-            prepare_first(c);
             run_epilogue(c);
         }
     }
