@@ -26,8 +26,11 @@
 // Bound by the tensor pipe, and on long calls by the power that it may take: Q K^T counts twice for
 // the two query terms and P V twice for those of P', 4 x 128 x 128 x 512 multiply-adds of E4M3 per
 // unit and tile. 1024 rows of 64 heads after 31.7k cached tokens (4.5 TFLOP of bf16 arithmetic):
-// 2.44 ms in short bursts, 1820 TFLOP/s, 95 % of what a bf16 matrix product of the library
-// reaches; one prompt of 4096 rows, 795 us, 1380; 512 rows over 4096 tokens, 190 us, 1350.
+// 2.44 ms in short bursts, 1830 TFLOP/s, 95 % of what a bf16 matrix product of the library
+// reaches; one prompt of 4096 rows, 785 us, 1400; 512 rows over 4096 tokens, 186 us, 1380. There a
+// change of unit is what is lost: 9500 cycles between products with V, where tiles follow at 2700.
+// Short units are bound by the fetching of instructions: sixteen warps run nine programs, so loops
+// stay rolled and warps that do the same run the same code.
 //
 // Measured beside this split: three K and three V slots, 1 to 4 % more (a value tile is held until
 // its softmax is done, a key tile is not); the queries by four warps of their own, at 96 registers
@@ -676,7 +679,8 @@ static_assert(kFirstPairs % kPrepPairs == 0 && kOwnPairs % kPrepPairs == 0, "who
 // negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or an
 // infinity gets zero codes and a NaN scale (exponent 255), which makes all its scores NaN.
 // The loop over pairs stays rolled: unrolled, its code is fetched anew for each unit, which took
-// longer than all else here (18700 cycles for 16 pairs against 10600).
+// longer than all else here (18700 cycles for 16 pairs against 10600; 8500 now, with the terms
+// formed as packed halves, which hold a query's eight bits exactly from 2^-14 on: below, both are 0).
 struct Query {
     uint4 a, b;
 };
