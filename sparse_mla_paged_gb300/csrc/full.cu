@@ -98,6 +98,12 @@ constexpr uint32_t kTmemO = 0;    // O^T: dims 128c.. of all 64 pairs at column 
 constexpr uint32_t kTmemQ = 256;  // query operand
 constexpr uint32_t kTmemS = 384;
 
+// A reference is this much above its tile's maximum. Each move costs the CTA about a
+// microsecond (the pipeline drains): with normal scores of deviation 1, 8 of 106 tiles of 64
+// pairs moved at the selected decode's 1 octave and moves of the asking pairs only (two contexts
+// of 512 thousand tokens: 205 us, 199 with them). The lowest tile maximum that a reference serves,
+// kRescaleDrop below it, is the same.
+constexpr float kSlack = 2.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Warps of the two variants.

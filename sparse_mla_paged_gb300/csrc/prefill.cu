@@ -119,6 +119,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;    // O^T: dims 128c.. of this CTA's 256, all pairs, at column 128c
 constexpr uint32_t kTmemQ = 256;  // query operand
 constexpr uint32_t kTmemS = 384;
+constexpr float kSlack = 2.0f;  // a reference above its tile's maximum, as in the full decode: a move stops both products
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // A cluster's stretch of one unit.

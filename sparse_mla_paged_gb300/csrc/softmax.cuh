@@ -5,12 +5,6 @@
 
 namespace dsa {
 
-// A reference is this much above its tile's maximum. Each move costs the CTA about a
-// microsecond (the pipeline drains): with normal scores of deviation 1, 8 of 106 tiles of 64
-// pairs moved at the selected decode's 1 octave and moves of the asking pairs only (two contexts
-// of 512 thousand tokens: 205 us, 199 with them). The lowest tile maximum that a reference serves,
-// kRescaleDrop below it, is the same.
-constexpr float kSlack = 2.0f;
 // What the two E4M3 terms of a P' lose: 2^-10 at most (it itself when below), beside 1.2 * 2^-9 of
 // it. The row sum takes P' whole, so a tile far below its pair's reference would be counted but not
 // added: 128 terms of 2^-11 weigh 2^-4, as much as a 512th of a row whose sum is the 2^5 of one
