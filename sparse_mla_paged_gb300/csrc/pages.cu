@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const __grid_consta
 __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const __grid_constant__ ForkParams p) {
     wait_prior();
     constexpr int kRow = kCopyThreads;  // entries of a turn
-    const int32_t row_turns = (p.t.max_blocks + kRow - 1) / kRow;
+    const int32_t row_turns = static_cast<int32_t>((static_cast<uint32_t>(p.t.max_blocks) + kRow - 1u) / kRow);
     const int64_t turns = static_cast<int64_t>(p.forks) * row_turns;
     const uint32_t items = static_cast<uint32_t>(p.forks) * p.pools.items;
     for (int64_t it = blockIdx.x; it < turns + items; it += gridDim.x) {
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kMarkThreads) release_mark_kernel(const __grid
         const int32_t lo = pages_of(p.t, keep), hi = pages_of(p.t, len);
         int32_t* row = p.t.entries + static_cast<int64_t>(s) * p.t.max_blocks;
         int32_t refs = 0;
-        if (col0 < hi && col0 + kEntries > lo) {
+        if (col0 < hi && lo - col0 < kEntries) {
             int32_t page[kEntries / 32], before[kEntries / 32];
 #pragma unroll
             for (int i = 0; i < kEntries / 32; ++i) {
@@ -529,7 +529,7 @@ cudaError_t launch_fork_pages(const pages::ForkParams& p, int sms, cudaStream_t 
     else pages::fork_plan_kernel<pages::kManyForkThreads><<<1, pages::kManyForkThreads, smem, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t turns = (p.t.max_blocks + pages::kCopyThreads - 1) / pages::kCopyThreads;
+    const int64_t turns = (static_cast<int64_t>(p.t.max_blocks) + pages::kCopyThreads - 1) / pages::kCopyThreads;
     return pages::launch_after(pages::fork_kernel, pages::at_most(p.forks * (turns + p.pools.items), 8 * sms), pages::kCopyThreads, p, stream);
 }
 

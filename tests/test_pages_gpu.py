@@ -485,3 +485,36 @@ def test_other_stream(api):
     api.copy_pages(dev, src, dst, stream=side)
     side.synchronize()
     same_pools(dev, ref.copy(pools, range(10), range(15, 25)))
+
+
+def test_tables_of_two_billion_columns(api):
+    """Rows as wide as they may be, so that the turns over a row pass 31 bits when rounded up; of the
+    entries only those of the lengths are looked at."""
+    columns = 2**31 - 1
+    if torch.cuda.mem_get_info()[0] < 24 * 2**30:
+        pytest.skip("24 GB of device memory")
+    tables = torch.empty(2, columns, dtype=torch.int32, device="cuda")
+    tables[:, :8] = -1
+    tables[0, :3] = cu(np.array([5, 2, 7], np.int32))
+    pools = pools_of(np.random.default_rng(5), 9)
+    dev, shares = on_gpu(pools), torch.zeros(9, dtype=torch.int32, device="cuda")
+    lens = cu(np.array([3, 0], np.int32))
+    free = cu(np.array([0, 1, 3, 4, 6, 8, -1, -1, -1], np.int32))
+    info = api.fork_pages(dev, cu(np.array([0], np.int32)), cu(np.array([1], np.int32)), lens, 1, tables, free, shares)
+    assert info.tolist() == [1, 0, 0, 0]
+    assert tables[1, :8].tolist() == [5, 2, 7, -1, -1, -1, -1, -1]
+    assert shares.tolist() == [0, 0, 1, 0, 0, 1, 0, 1, 0]
+    lens[1] = 3
+    num_free = cu(np.array([6], np.int32))
+    info = api.release_pages(tables, lens, cu(np.array([0, 2], np.int32)), 1, shares, free, num_free)
+    assert info.tolist() == [4, 1, 0, 7]
+    assert tables[:, :4].tolist() == [[-1, -1, -1, -1], [5, 2, -1, -1]]
+    assert shares.tolist() == [0] * 9 and free[:7].tolist() == [0, 1, 3, 4, 6, 8, 7]
+    lens[0], lens[1] = 0, 2
+    info = api.compact_pages(dev, tables, lens, 1, shares, free, num_free)
+    assert info.tolist() == [2, 2, 0, 7]
+    assert tables[1, :2].tolist() == [1, 0] and free.tolist() == [2, 3, 4, 5, 6, 7, 8, -1, -1]
+    want = [p.copy() for p in pools]
+    for p in want:
+        p[:, 0], p[:, 1] = p[:, 2].copy(), p[:, 5].copy()
+    same_pools([d[..., :2, :] for d in dev], [w[:, :2] for w in want])
