@@ -19,16 +19,19 @@
 //                tokens][blocks of 128 dims][8 tokens][128 bytes], 128-byte swizzle): tensor-map
 //                boxes of a page's rows when pages and tiles fit each other, else 16-byte copies
 //   warp 2, 3    issue Q K^T and P V (rank 0); tell rank 0 of the loaded K tiles (rank 1)
-//   warps 4-11   softmax, two per TMEM lane quarter
-//   warps 12-15  make the next unit's query operand and put it in place, rescale O when a reference
-//                moves, write a unit's output
+//   warps 4-11   softmax, two per TMEM lane quarter; after a unit's last tile they put the next
+//                unit's query operand in place
+//   warps 12-15  make the next unit's query operand, rescale O when a reference moves, write a unit's
+//                output
 //
 // Bound by the tensor pipe, and on long calls by the power that it may take: Q K^T counts twice for
 // the two query terms and P V twice for those of P', 4 x 128 x 128 x 512 multiply-adds of E4M3 per
 // unit and tile. 1024 rows of 64 heads after 31.7k cached tokens (4.5 TFLOP of bf16 arithmetic):
 // 2.44 ms in short bursts, 1830 TFLOP/s, 95 % of what a bf16 matrix product of the library
-// reaches; one prompt of 4096 rows, 785 us, 1400; 512 rows over 4096 tokens, 186 us, 1380. There a
-// change of unit is what is lost: 9500 cycles between products with V, where tiles follow at 2700.
+// reaches; one prompt of 4096 rows, 785 us, 1400; 512 rows over 4096 tokens, 185 us, 1390. There a
+// change of unit is what is lost: 7000 cycles between products with V, where tiles follow at 2700.
+// (9500 with the operand put in place by warps 12-15 once the last product is issued; by them,
+// earlier, on an event of its own: 3 % more on short units, for one wait more.)
 // Short units are bound by the fetching of instructions: sixteen warps run nine programs, so loops
 // stay rolled and warps that do the same run the same code.
 //
@@ -104,7 +107,8 @@ enum {
     BAR_SEMPTY,                              // (0) S read
     BAR_QFULL,                               // (0) query operands in place
     BAR_QEMPTY,                              // (both) the unit's last Q K^T is done
-    BAR_EVENT,                               // (both) something for the epilogue warps
+    BAR_QMADE0,                              // 2: query operand made, by the unit's parity
+    BAR_EVENT = BAR_QMADE0 + 2,              // (both) something for the epilogue warps
     BAR_OFREE,                               // (0) they did it
     BAR_FFULL,                               // (both) output factors written
     BAR_FEMPTY,                              // (both) and used
@@ -449,6 +453,35 @@ __device__ void run_forward(const Cta& c) {
 // ------------------------------------------------------------------------------------
 // softmax warps
 // ------------------------------------------------------------------------------------
+__device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
+    return c.p.qimg + (static_cast<int64_t>(blockIdx.x) * 2 + parity) * kQImageBytes;
+}
+// Half of a lane quarter of unit number `units`' query operand into tensor memory, once it is made and
+// the unit before has no more use for the place.
+__device__ __forceinline__ void place_query(const Cta& c, uint32_t units, int half) {
+    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+    const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ + half * 64;
+    const uint4* src = reinterpret_cast<const uint4*>(query_image(c, units & 1) + half * (16 * 2048) + (q4 * 32 + lane) * 16);
+    c.wait(BAR_QMADE0 + (units & 1), (units >> 1) & 1);
+    if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
+    tc_fence_after();
+    uint32_t a[2][32];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint4 v = __ldcg(src + i * (2048 / 16));
+        a[i >> 3][4 * (i & 7)] = v.x;
+        a[i >> 3][4 * (i & 7) + 1] = v.y;
+        a[i >> 3][4 * (i & 7) + 2] = v.z;
+        a[i >> 3][4 * (i & 7) + 3] = v.w;
+    }
+    tmem_st_x32(place, a[0]);
+    tmem_st_x32(place + 32, a[1]);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) c.arrive(BAR_QFULL, 0);
+}
+
 __device__ void run_softmax(const Cta& c) {
     constexpr int kSlots = kValueSlots;
     const Params& p = c.p;
@@ -467,6 +500,7 @@ __device__ void run_softmax(const Cta& c) {
     bool pv_seen = false;  // the P.V two tiles back was already waited for
 
     const int32_t k0 = p.starts[c.cluster].k;
+    place_query(c, 0, half);
     for (;; ++units) {
         // The tile loop keeps few of the unit's numbers (registers are short here); what else it needs,
         // seldom, it takes from the record again, which stays in L1.
@@ -645,8 +679,10 @@ __device__ void run_softmax(const Cta& c) {
             if (lane == 0) c.arrive(BAR_PFULL0 + (tau & 1), 0);
         }
 
-        // ---- the unit's output factors, to both CTAs ----
         const Segment s = unit();
+        if (!s.last) place_query(c, units + 1, half);  // while the last P.V runs
+
+        // ---- the unit's output factors, to both CTAs ----
         const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
         if (term == 0) hm_s[half * kCtaPairs + hq].x = lpair;
         if (named_bar_any<kBarSoftmax, kSoftmaxThreads>(*c.abort_flag != 0)) return;  // all eight warps end together
@@ -795,9 +831,6 @@ __device__ uint32_t find_broken(const Cta& c, const Segment& s) {
     return word;
 }
 
-__device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
-    return c.p.qimg + (static_cast<int64_t>(blockIdx.x) * 2 + parity) * kQImageBytes;
-}
 // The first unit's operand is made by all warps that have nothing to do yet: kPrepPairs pairs by each
 // softmax warp, the others by the epilogue warps.
 __device__ void prepare_first(const Cta& c, int sw) {
@@ -826,32 +859,7 @@ __device__ void prepare_query(const Cta& c, const Segment& s, uint32_t units) {
     if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = broken;
     __syncwarp();
     if (units == 0) named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
-}
-
-// Its image into tensor memory, once the unit before has no more use for the place.
-__device__ void place_query(const Cta& c, uint32_t units) {
-    const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
-    const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ;
-    const uint4* src = reinterpret_cast<const uint4*>(query_image(c, units & 1) + (q4 * 32 + lane) * 16);
-    if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
-#pragma unroll 1
-    for (int part = 0; part < 2; ++part) {
-        uint32_t a[2][32];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint4 v = __ldcg(src + (part * 16 + i) * (2048 / 16));
-            a[i >> 3][4 * (i & 7)] = v.x;
-            a[i >> 3][4 * (i & 7) + 1] = v.y;
-            a[i >> 3][4 * (i & 7) + 2] = v.z;
-            a[i >> 3][4 * (i & 7) + 3] = v.w;
-        }
-        tmem_st_x32(place + part * 64, a[0]);
-        tmem_st_x32(place + part * 64 + 32, a[1]);
-    }
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) c.arrive(BAR_QFULL, 0);
+    if (lane == 0) mbar_arrive(c.bar(BAR_QMADE0 + parity));
 }
 
 // ------------------------------------------------------------------------------------
@@ -864,7 +872,6 @@ __device__ void run_epilogue(const Cta& c) {
     uint32_t tau = 0, units = 0, events = 0;
     Walk w(c), ahead(c);
     prepare_query(c, w.s, 0);
-    place_query(c, 0);
     for (;; w.advance(), ++units) {
         const Segment& s = w.s;
         tau += s.t1 - s.t0;
@@ -903,8 +910,6 @@ __device__ void run_epilogue(const Cta& c) {
             __syncwarp();
             if (lane == 0) c.arrive(BAR_OFREE, 0);
         }
-
-        if (!s.last) place_query(c, units + 1);  // while the last P.V runs
 
         // ---- output of the unit ----
         c.wait(BAR_PVDONE0 + ((tau - 1) & 1), ((tau - 1) >> 1) & 1);
@@ -981,10 +986,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             mbar_init(c.bar(BAR_PFULL0 + i), 2 * kSoftmaxWarps);
             mbar_init(c.bar(BAR_PVDONE0 + i), 1);
             mbar_init(c.bar(BAR_UDONE0 + i), kSoftmaxWarps);
+            mbar_init(c.bar(BAR_QMADE0 + i), kEpilogueWarps);
         }
         mbar_init(c.bar(BAR_SFULL), 1);
         mbar_init(c.bar(BAR_SEMPTY), 2 * kSoftmaxWarps);
-        mbar_init(c.bar(BAR_QFULL), 2 * kEpilogueWarps);
+        mbar_init(c.bar(BAR_QFULL), 2 * kSoftmaxWarps);
         mbar_init(c.bar(BAR_QEMPTY), 1);
         mbar_init(c.bar(BAR_EVENT), 1);
         mbar_init(c.bar(BAR_OFREE), 2 * kEpilogueWarps);
