@@ -381,11 +381,11 @@ __global__ void __launch_bounds__(kListThreads) release_list_kernel(const __grid
     wait_prior();
     const int32_t words = static_cast<int32_t>((static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4);
     const int2 turns = block_turns(words);
+    const int32_t had = *p.num_free, want = p.taken ? *p.taken : 0;  // on their way beside the marks
     const int2 counts = count_marks(p.marks, words, turns.x * kBlockWords, sums);
     const int32_t freed = counts.x;
     int32_t before = counts.y;
-    const int32_t had = *p.num_free, count = min(max(had, 0), p.t.num_pages);
-    const int32_t want = p.taken ? *p.taken : 0, taken = min(max(want, 0), count);
+    const int32_t count = min(max(had, 0), p.t.num_pages), taken = min(max(want, 0), count);
     bool bad = had != count || want != taken;
     const int64_t after = static_cast<int64_t>(count) - taken + freed;
     const int32_t now = static_cast<int32_t>(min(after, static_cast<int64_t>(p.t.num_pages)));
@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kListThreads) compact_list_kernel(const __grid
         p.info[0] = live;
         p.info[1] = live - low;
         p.info[2] = p.head->status;
+        p.head->status = 0;
         p.info[3] = p.t.num_pages - live;
         *p.num_free = p.t.num_pages - live;
     }
@@ -483,7 +484,6 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_cons
             copy_chunk(p.pools, static_cast<uint32_t>(it) - k * p.pools.items, p.src[k], p.dst[k]);
         }
     }
-    if (last_block(&p.head->ticket) && threadIdx.x == 0) p.head->status = p.head->ticket = 0;
 }
 
 template <class P>
