@@ -958,10 +958,10 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
     p.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
     p.cache_stride = cache_stride_bytes;
     p.clusters = d->sms / 2;
-    // With fewer units than an eighth of the ranges a unit comes in more than eight pieces. (Units of 2
-    // rows of 64 heads over 32k tokens, with eight warps a piece list and with one: 1 unit 31.4 and
-    // 40.4 us, 4 units 43.8 and 46.1, 9 units 72.9 and 68.2.)
-    p.few_units = units * 8 <= p.clusters ? 1 : 0;
+    // A piece list is long when units are few: eight warps share it then. (2 rows of 64 heads a unit, over
+    // 32k tokens, with eight warps a piece list and with one: 1 unit 31.4 and 40.4 us, 4 units 43.8
+    // and 46.1, 6 units 54.0 and 51.9, 7 units 58.9 and 55.2; 8 units of 2 tiles 22.2 and 18.1.)
+    p.few_units = units * 15 <= p.clusters ? 1 : 0;
     p.most_joins = static_cast<int32_t>(std::min<int64_t>(units, p.clusters));
     // A block of 256 threads, with cheaper barriers, while they have one request and a few units each
     // (5 rows of 16 heads 18.5 us, 19.7 with 1024 threads; 250 requests of 4 units each 135.5 both).

@@ -6,7 +6,7 @@
 // has to know of the others', the launches overlapped, and within each a few dependent loads and
 // barriers. 64 requests that give back their drafts 5 us (two launches), half of 256 requests with
 // 1.2 thousand pages each 15, a fork of four ways 4.4 (two launches), a pool of 380 pages compacted
-// 8 (three launches).
+// 7 (three launches).
 // Page data is bound by HBM: 1024 pages of two pools in four layers, 338 MB read and written, 54 us,
 // 6.2 TB/s, 92 % of a plain copy's rate. Blocks of 256 threads with four 16-byte pieces in flight
 // each, eight blocks to an SM, are what it takes; pieces pass the caches by, as they are not read again.

@@ -82,7 +82,7 @@ struct Params {
     int64_t cache_stride;
     int32_t num_seqs, max_rows, heads, block_size, max_blocks_per_seq, clusters;
     int32_t most_joins;        // units, or ranges, whichever are fewer
-    int32_t few_units;         // units come in more than eight pieces each
+    int32_t few_units;         // units may come in many pieces each
     int32_t small_plan;        // few requests and units
     int32_t box_rows;          // tokens of a tensor-map box (8, 16 or 32), 0: per-thread copies
     FastDiv by_block, by_heads;
