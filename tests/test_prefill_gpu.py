@@ -106,6 +106,13 @@ def test_long_chunks(api, base, new, heads, bs, two):
     c.check(api, rows)
 
 
+@pytest.mark.parametrize("new", [2, 8, 10, 13, 18])
+def test_units_in_many_pieces(api, new):
+    """One to nine units over the same 47 tiles: pieces by the dozen, or few, on either side of the
+    choice of a join."""
+    Case([6000 - new], [new], 64).check(api)
+
+
 def test_buffers_and_tables(api):
     Case([500, 3], [9, 40], 64, two=True).check(api)
     Case([500, 3], [9, 40], 24, two=True, pad=48).check(api)
