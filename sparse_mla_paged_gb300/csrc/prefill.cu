@@ -461,7 +461,8 @@ __device__ __forceinline__ uint8_t* query_image(const Cta& c, int parity) {
 __device__ __forceinline__ void place_query(const Cta& c, uint32_t units, int half) {
     const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
     const uint32_t place = c.tmem + (static_cast<uint32_t>(q4 * 32) << 16) + kTmemQ + half * 64;
-    const uint4* src = reinterpret_cast<const uint4*>(query_image(c, units & 1) + half * (16 * 2048) + (q4 * 32 + lane) * 16);
+    const int row = 2 * (16 * q4 + (lane & 15)) + (lane >> 4);  // 16 pairs' hi rows, then their lo rows
+    const uint4* src = reinterpret_cast<const uint4*>(query_image(c, units & 1) + half * (16 * 2048) + row * 16);
     c.wait(BAR_QMADE0 + (units & 1), (units >> 1) & 1);
     if (units > 0) c.wait(BAR_QEMPTY, (units - 1) & 1);
     tc_fence_after();
@@ -489,13 +490,13 @@ __device__ void run_softmax(const Cta& c) {
     const int sw = warp - kSoftmax0;               // 0..7
     const int q4 = warp & 3;                       // TMEM lane quarter
     const int half = sw >> 2;                      // token half of each tile
-    const int term = lane & 1;                     // 0: hi row, 1: lo row
-    const int hq = 16 * q4 + (lane >> 1);          // pair of this thread within the CTA
+    const int side = lane >> 4;                    // half of those tokens
+    const int hq = 16 * q4 + (lane & 15);          // pair of this thread within the CTA
     const int pair = static_cast<int>(c.rank) * kCtaPairs + hq;  // and within the unit
     float2* hm_s = reinterpret_cast<float2*>(c.smem + kOffHm);
     const uint32_t lane_base = static_cast<uint32_t>(q4 * 32) << 16;
     // This thread's first 16-byte row in a P' term: K-major core matrices of 8 pairs x 16 tokens.
-    const uint32_t p_off = (((half * kHalfCols + term * kScores) / 16) * 8 + (hq >> 3)) * 128 + (hq & 7) * 16;
+    const uint32_t p_off = (((half * kHalfCols + side * kScores) / 16) * 8 + (hq >> 3)) * 128 + (hq & 7) * 16;
     uint32_t tau = 0, units = 0;
     bool pv_seen = false;  // the P.V two tiles back was already waited for
 
@@ -526,21 +527,19 @@ __device__ void run_softmax(const Cta& c) {
         for (; t < t1; ++t, ++tau, first = false) {
             c.wait(BAR_SFULL, tau & 1);
             tc_fence_after();
-            // Dots of pair hq with tokens tok0 .. tok0+31 of the tile: this lane's term plus the
-            // neighbouring lane's other one; the score in log2 units is qs (> 0) times that.
-            const int tok0 = half * kHalfCols + term * kScores;
+            // Dots of pair hq with tokens tok0 .. tok0+31 of the tile: the hi term's row plus the lo
+            // term's, 16 lanes further on, both in this thread by the load's own shape. (By 32-lane loads
+            // of neighbouring rows and an exchange between their threads 7 % more, on calls at the power
+            // limit too.) The score in log2 units is qs (> 0) times that.
+            const int tok0 = half * kHalfCols + side * kScores;
             float x[kScores];
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
                 uint32_t a[16], b[16];
                 const uint32_t at = c.tmem + lane_base + kTmemS + half * kHalfCols + 16 * part;
-                tmem_ld_2x16(at, at + kScores, a, b);
+                tmem_ld_halves_2x16(at, at + (16u << 16), a, b);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float send = __uint_as_float(term ? a[j] : b[j]);
-                    const float mine = __uint_as_float(term ? b[j] : a[j]);
-                    x[16 * part + j] = mine + __shfl_xor_sync(0xffffffffu, send, 1);
-                }
+                for (int j = 0; j < 16; ++j) x[16 * part + j] = __uint_as_float(a[j]) + __uint_as_float(b[j]);
             }
             tc_fence_before();
             __syncwarp();
@@ -592,7 +591,7 @@ __device__ void run_softmax(const Cta& c) {
 #pragma unroll
             for (int j = 0; j < kScores; j += 2) hm4[(j >> 1) & 3] = max3(hm4[(j >> 1) & 3], x[j], x[j + 1]);
             float hmax = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
-            hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 1)) * qs;
+            hmax = fmaxf(hmax, __shfl_xor_sync(0xffffffffu, hmax, 16)) * qs;
             // As in the full decode: P' is formed with the reference as it is (but for a unit's first
             // tile), one barrier tells whether any half of any pair's scores asks for a move, and
             // only then the halves are compared, references move and P' is formed again. A tile far
@@ -626,8 +625,8 @@ __device__ void run_softmax(const Cta& c) {
                                      ask || (credit + earned < 0.0f && m_ref > m_top - kRescaleFloor)))
                         break;
                 }
-                const float credit2 = credit + earned + __shfl_xor_sync(0xffffffffu, credit + earned, 1);
-                if (term == 0) hm_s[half * kCtaPairs + hq] = make_float2(hmax, credit2);
+                const float credit2 = credit + earned + __shfl_xor_sync(0xffffffffu, credit + earned, 16);
+                if (side == 0) hm_s[half * kCtaPairs + hq] = make_float2(hmax, credit2);
                 named_bar_sync_id(kBarPair0 + q4, 64);
                 const float2 h0 = hm_s[hq], h1 = hm_s[kCtaPairs + hq];
                 const float tm = fmaxf(h0.x, h1.x), credit4 = h0.y + h1.y;
@@ -653,9 +652,9 @@ __device__ void run_softmax(const Cta& c) {
                     if (tau >= 2 && !pv_seen) c.wait(BAR_PVDONE0 + (tau & 1), ((tau >> 1) - 1) & 1);
                     pv_seen = true;
                     const uint32_t changed = __ballot_sync(0xffffffffu, change);
-                    const uint32_t to = map_rank(c.sbase, term);  // a lane of each pair per CTA
+                    const uint32_t to = map_rank(c.sbase, side);  // a lane of each pair per CTA
                     st_cluster(to + kOffAlpha + ((tau & 1) * kPairs + pair) * 4, __float_as_uint(alpha));
-                    if (lane < 2 && changed != 0u)
+                    if ((lane & 15) == 0 && changed != 0u)
                         st_cluster(to + kOffFlags + (((tau & 1) * 2 + c.rank) * 4 + q4) * 4, tau + 1);
                     fence_cluster();
                     __syncwarp();
@@ -683,8 +682,8 @@ __device__ void run_softmax(const Cta& c) {
         if (!s.last) place_query(c, units + 1, half);  // while the last P.V runs
 
         // ---- the unit's output factors, to both CTAs ----
-        const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 1);
-        if (term == 0) hm_s[half * kCtaPairs + hq].x = lpair;
+        const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 16);
+        if (side == 0) hm_s[half * kCtaPairs + hq].x = lpair;
         if (named_bar_any<kBarSoftmax, kSoftmaxThreads>(*c.abort_flag != 0)) return;  // all eight warps end together
         if (half == 0) {
             if (units > 0) c.wait(BAR_FEMPTY, (units - 1) & 1);
@@ -692,8 +691,8 @@ __device__ void run_softmax(const Cta& c) {
             const bool whole = s.part < 0;
             const float f = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
             if (sw == 0 && lane == 0) mbar_arrive_expect_tx(c.bar(BAR_FFULL), kPairs * 4);
-            st_async(map_rank(c.sbase, term) + kOffF + pair * 4, __float_as_uint(f), map_rank(c.bar(BAR_FFULL), term));
-            if (!whole && term == 0) p.part_lse[s.part * kPairs + pair] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
+            st_async(map_rank(c.sbase, side) + kOffF + pair * 4, __float_as_uint(f), map_rank(c.bar(BAR_FFULL), side));
+            if (!whole && side == 0) p.part_lse[s.part * kPairs + pair] = l == 0.0f ? kNegInf : m_ref + __log2f(l);
         }
         if (lane == 0) mbar_arrive(c.bar(BAR_UDONE0 + (units & 1)));
         named_bar_sync<kBarSoftmax, kSoftmaxThreads>();  // the sums are read
