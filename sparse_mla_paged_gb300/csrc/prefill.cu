@@ -539,7 +539,11 @@ __device__ void run_softmax(const Cta& c) {
                 const uint32_t at = c.tmem + lane_base + kTmemS + half * kHalfCols + 16 * part;
                 tmem_ld_halves_2x16(at, at + (16u << 16), a, b);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[16 * part + j] = __uint_as_float(a[j]) + __uint_as_float(b[j]);
+                for (int j = 0; j < 16; j += 2) {
+                    const float2 r = add_two({__uint_as_float(a[j]), __uint_as_float(a[j + 1])}, {__uint_as_float(b[j]), __uint_as_float(b[j + 1])});
+                    x[16 * part + j] = r.x;
+                    x[16 * part + j + 1] = r.y;
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -603,23 +607,22 @@ __device__ void run_softmax(const Cta& c) {
 #pragma unroll 1
             for (bool again = false;; again = true) {
                 if (again || !first) {
-                    float ls4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                     const float off = m_ref == kNegInf ? 0.0f : kPBias - m_ref;  // nothing seen so far: every x is -inf
 #pragma unroll
                     for (int g = 0; g < kScores / 4; ++g) {
-                        float pp[4];
+                        uint32_t h[2], l[2];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            pp[e] = ex2_approx(fmaf(x[4 * g + e], qs, off));
-                            ls4[e] += pp[e];
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 y = fma_two({x[4 * g + 2 * e], x[4 * g + 2 * e + 1]}, {qs, qs}, {off, off});
+                            const float2 pp = {ex2_approx(y.x), ex2_approx(y.y)};
+                            sum[e] = add_two(sum[e], pp);
+                            split2(pp.x, pp.y, h[e], l[e]);
                         }
-                        uint32_t h0, l0, h1, l1;
-                        split2(pp[0], pp[1], h0, l0);
-                        split2(pp[2], pp[3], h1, l1);
-                        hw[g] = h0 | h1 << 16;
-                        lw[g] = l0 | l1 << 16;
+                        hw[g] = h[0] | h[1] << 16;
+                        lw[g] = l[0] | l[1] << 16;
                     }
-                    fresh = (ls4[0] + ls4[1]) + (ls4[2] + ls4[3]);
+                    fresh = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     earned = fmaf(fresh, kLostShare, -fminf(fresh, kMostLost));
                     if (again || !named_bar_any<kBarSoftmax, kSoftmaxThreads>(
                                      ask || (credit + earned < 0.0f && m_ref > m_top - kRescaleFloor)))
