@@ -27,11 +27,12 @@
 // Bound by the tensor pipe, and on long calls by the power that it may take: Q K^T counts twice for
 // the two query terms and P V twice for those of P', 4 x 128 x 128 x 512 multiply-adds of E4M3 per
 // unit and tile. 1024 rows of 64 heads after 31.7k cached tokens (4.5 TFLOP of bf16 arithmetic):
-// 2.44 ms in short bursts, 1830 TFLOP/s, 95 % of what a bf16 matrix product of the library
-// reaches; one prompt of 4096 rows, 785 us, 1400; 512 rows over 4096 tokens, 185 us, 1390. There a
-// change of unit is what is lost: 7000 cycles between products with V, where tiles follow at 2700.
-// (9500 with the operand put in place by warps 12-15 once the last product is issued; by them,
-// earlier, on an event of its own: 3 % more on short units, for one wait more.)
+// 2.28 ms in short bursts, 1960 TFLOP/s (a bf16 matrix product of the library: 1924), 2.54 in a long
+// loop, at the power limit, 1760 (1725); one prompt of 4096 rows, 735 us, 1500; 512 rows over 4096
+// tokens, 173 us, 1490. There a change of unit is what is lost: some 7000 cycles between products
+// with V, where tiles follow at 2500. (9500 with the operand put in place by warps 12-15 once the last
+// product is issued; by them, earlier, on an event of its own: 3 % more on short units, for one
+// wait more.) Every instruction less in the softmax also saves power, and so time on long calls.
 // Short units are bound by the fetching of instructions: sixteen warps run nine programs, so loops
 // stay rolled and warps that do the same run the same code.
 //
