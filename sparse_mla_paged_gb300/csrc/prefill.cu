@@ -714,7 +714,7 @@ static_assert(kFirstPairs % kPrepPairs == 0 && kOwnPairs % kPrepPairs == 0, "who
 
 // Query operand rows of a warp's kPrepPairs or more pairs: lane l has dims [16l, 16l+16). A
 // head's bf16 query becomes two E4M3 terms after a scaling by a power of two (exact for elements from
-// 2^-9 of its largest, smaller ones off by 2^-16 of it at most), rows 2k and 2k+1 the terms of pair
+// 2^-9 of its largest, smaller ones off by 2^-16 of it at most), rows 2k and 2k+1 of the image the terms of pair
 // k, stored chunk-major. The scale of its dots is positive (maxima are taken of the dots): a
 // negative score scale turns the codes' signs, a zero one zeroes the codes. A head with a NaN or an
 // infinity gets zero codes and a NaN scale (exponent 255), which makes all its scores NaN.
