@@ -499,7 +499,8 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
  *               the buffer that dsa_plan_step and dsa_fork_pages take pages from the front of.
  *  info         int32 [4], written by the call; info[2] is DSA_OK or DSA_ERR_DEVICE_BOUNDS.
  *  workspace    device memory, 256-byte aligned, at least dsa_pages_workspace_bytes(num_pages),
- *               zero before its first use; calls leave what they need of it zero. Calls that may
+ *               zero before its first use; calls leave what they need of it zero, for a call of
+ *               any other num_pages that it is large enough for too. Calls that may
  *               overlap on the GPU need workspaces of their own (and requests, pages and lists of
  *               their own).
  * Tables are int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq >= 1; a length below 0 or past

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kMarkThreads) release_mark_kernel(const __grid
             }
 #pragma unroll
             for (int i = 0; i < kEntries / 32; ++i) {
-                if (before[i] == 0) atomicOr(p.marks + (page[i] >> 5), 1u << (page[i] & 31));
+                if (before[i] == 0) atomicOr(p.marks + mark_at(page[i] >> 5), 1u << (page[i] & 31));
                 bad |= before[i] < 0;
             }
             refs = __reduce_add_sync(0xffffffffu, refs);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kMarkThreads) compact_mark_kernel(const __grid
             const int32_t col = col0 + 32 * i + lane;
             const int32_t page = col < hi ? row[col] : -1;
             if (page >= p.t.num_pages) bad = true;
-            else if (page >= 0) atomicOr(p.marks + (page >> 5), 1u << (page & 31));
+            else if (page >= 0) atomicOr(p.marks + mark_at(page >> 5), 1u << (page & 31));
         }
         if (bad) report(&p.head->status);
     });
@@ -303,7 +303,7 @@ static_assert(kListWarps == 32, "a lane for each warp");
 __device__ __forceinline__ int2 count_marks(const uint32_t* marks, int32_t words, int32_t w0, int2* sums) {
     int all = 0, before = 0;
     for (int32_t w = 4 * threadIdx.x; w < words; w += 4 * kListThreads) {
-        const uint4 v = *reinterpret_cast<const uint4*>(marks + w);
+        const uint4 v = *reinterpret_cast<const uint4*>(marks + mark_at(w));
         const int n = __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w);
         all += n;
         if (w < w0) before += n;  // both multiples of 4
@@ -314,7 +314,7 @@ __device__ __forceinline__ int2 count_marks(const uint32_t* marks, int32_t words
 __device__ __forceinline__ int32_t count_below(const uint32_t* marks, int32_t limit, int2* sums) {
     int n = 0;
     for (int32_t w = 4 * threadIdx.x; w < (limit + 31) / 32; w += 4 * kListThreads) {
-        const uint4 v = *reinterpret_cast<const uint4*>(marks + w);
+        const uint4 v = *reinterpret_cast<const uint4*>(marks + mark_at(w));
         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -340,7 +340,7 @@ __device__ __forceinline__ int32_t for_pages(const uint32_t* marks, int32_t w0, 
     __syncthreads();  // the turn before has read them
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int32_t base = w0 + warp * kWarpWords;
-    const uint32_t mine = lane < kWarpWords && base + lane < words ? marks[base + lane] : 0u;
+    const uint32_t mine = lane < kWarpWords && base + lane < words ? marks[mark_at(base + lane)] : 0u;
     int32_t inc = __popc(mine);
 #pragma unroll
     for (int o = 1; o < kWarpWords; o <<= 1) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kListThreads) release_list_kernel(const __grid
         for (int32_t i = now + threadIdx.x; i < count; i += kListThreads) p.free_pages[i] = -1;
     }
     if (!last_block(&p.head->ticket)) return;
-    for (int32_t w = threadIdx.x; w < words / 4; w += kListThreads) reinterpret_cast<uint4*>(p.marks)[w] = make_uint4(0, 0, 0, 0);
+    for (int32_t w = 4 * threadIdx.x; w < words; w += 4 * kListThreads) *reinterpret_cast<uint4*>(p.marks + mark_at(w)) = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) {
         p.info[0] = p.head->refs;
         p.info[1] = freed;
@@ -429,13 +429,13 @@ __global__ void __launch_bounds__(kListThreads) compact_list_kernel(const __grid
         before = for_pages<false>(p.marks, turn * kBlockWords, words, p.t.num_pages, before, [&](int32_t page, bool mine, int32_t k) {
             if (page >= live) {
                 if (mine) {
-                    p.rank[page] = k - low;
-                    p.src[k - low] = page;
+                    p.rank[entry_at(page)] = k - low;
+                    p.src[entry_at(k - low)] = page;
                 } else {
                     p.shares[page] = 0;
                 }
             } else if (!mine) {
-                p.dst[page - k] = page;
+                p.dst[entry_at(page - k)] = page;
             }
             p.free_pages[page] = page < p.t.num_pages - live ? page + live : -1;
         });
@@ -457,10 +457,11 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_cons
     const int32_t live = p.head->live, moved = p.head->moved;
     const int64_t tid = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x, threads = static_cast<int64_t>(gridDim.x) * kCopyThreads;
     const int64_t words = (static_cast<int64_t>(p.t.num_pages) + 127) / 128 * 4;
-    for (int64_t w = tid; w < words; w += threads) p.marks[w] = 0;
+    for (int64_t w = tid; w < words; w += threads) p.marks[mark_at(w)] = 0;
     for (int64_t k = tid; k < moved; k += threads) {
-        p.shares[p.dst[k]] = p.shares[p.src[k]];
-        p.shares[p.src[k]] = 0;
+        const int32_t src = p.src[entry_at(k)];
+        p.shares[p.dst[entry_at(k)]] = p.shares[src];
+        p.shares[src] = 0;
     }
     if (moved > 0) {
         const int64_t turns = static_cast<int64_t>(p.t.num_seqs) * p.t.chunks;
@@ -475,13 +476,13 @@ __global__ void __launch_bounds__(kCopyThreads) compact_kernel(const __grid_cons
             for (int i = 0; i < kEntries / 32; ++i) {
                 const int32_t col = col0 + 32 * i + lane;
                 const int32_t page = col < hi ? row[col] : -1;
-                if (page >= live && page < p.t.num_pages) row[col] = p.dst[p.rank[page]];
+                if (page >= live && page < p.t.num_pages) row[col] = p.dst[entry_at(p.rank[entry_at(page)])];
             }
         }
         const uint64_t items = static_cast<uint64_t>(moved) * p.pools.items;
         for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
             const uint32_t k = divide(static_cast<uint32_t>(it), p.pools.by_items);
-            copy_chunk(p.pools, static_cast<uint32_t>(it) - k * p.pools.items, p.src[k], p.dst[k]);
+            copy_chunk(p.pools, static_cast<uint32_t>(it) - k * p.pools.items, p.src[entry_at(k)], p.dst[entry_at(k)]);
         }
     }
 }

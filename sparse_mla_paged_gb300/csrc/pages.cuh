@@ -38,26 +38,32 @@ struct Head {
     int32_t live, moved;
 };
 
+// Workspace: the head, then segments of kSegment pages each: their marks, then their entries of three
+// lists. Where a page's mark and entries lie does not depend on how many pages a call has, so that
+// calls on pools of different sizes may take turns with one workspace: no list's entry ever lies
+// where a mark is expected to be zero.
+constexpr uint32_t kSegment = 1 << 14;
+constexpr uint32_t kSegmentMarks = kSegment / 32;
+constexpr int64_t kSegmentWords = kSegmentMarks + 3 * kSegment;
+static_assert(kSegment >= DSA_MAX_PLAN_SEQS, "a fork's lists lie in the first segment");
+static_assert(kSegmentMarks % 4 == 0 && kSegmentWords % 4 == 0, "whole 16-byte pieces");
+
+// Place of mark word w behind the first one, and of a list's entry i behind its first.
+__host__ __device__ inline int64_t mark_at(uint32_t w) { return w / kSegmentMarks * kSegmentWords + w % kSegmentMarks; }
+__host__ __device__ inline int64_t entry_at(uint32_t i) { return i / kSegment * kSegmentWords + i % kSegment; }
+
+// Marks are a bit per page, in whole 16-byte pieces.
+inline int64_t mark_words(int64_t pages) { return (pages + 127) / 128 * 4; }
 struct Layout {
     size_t marks, rank, src, dst, total;
 };
-// Marks are a bit per page, in whole 16-byte pieces.
-inline int64_t mark_words(int64_t pages) { return (pages + 127) / 128 * 4; }
 inline Layout layout(int64_t pages) {
     Layout L;
-    size_t o = 256;
-    auto put = [&](size_t bytes) {
-        const size_t at = o;
-        o = align256(o + bytes);
-        return at;
-    };
-    L.marks = put(static_cast<size_t>(mark_words(pages)) * 4);
-    // Lists by page or by fork.
-    const size_t list = static_cast<size_t>(pages > DSA_MAX_PLAN_SEQS ? pages : DSA_MAX_PLAN_SEQS) * 4;
-    L.rank = put(list);
-    L.src = put(list);
-    L.dst = put(list);
-    L.total = o;
+    L.marks = 256;
+    L.rank = L.marks + kSegmentMarks * 4;
+    L.src = L.rank + kSegment * 4;
+    L.dst = L.src + kSegment * 4;
+    L.total = L.marks + static_cast<size_t>((pages + kSegment - 1) / kSegment * kSegmentWords) * 4;
     return L;
 }
 
@@ -101,7 +107,7 @@ struct ReleaseParams {
     int32_t* num_free;
     int32_t* info;
     Head* head;
-    uint32_t* marks;
+    uint32_t* marks;          // mark_at
 };
 
 struct CompactParams {
@@ -112,8 +118,8 @@ struct CompactParams {
     int32_t* num_free;
     int32_t* info;
     Head* head;
-    uint32_t* marks;
-    int32_t* rank;            // [num_pages] number of a page that moves
+    uint32_t* marks;          // mark_at
+    int32_t* rank;            // [num_pages] number of a page that moves (entry_at, as the next two)
     int32_t* src;             // [moved]
     int32_t* dst;
 };
