@@ -399,6 +399,7 @@ __device__ void run_pv(const Cta& c) {
         for (int32_t t = s.t0; t < s.t1; ++t, ++tau) {
             const int pb = tau & 1, e = static_cast<int>(tau % kSlots);
             c.wait(BAR_PFULL0 + pb, (tau >> 1) & 1);
+            fence_acquire_shared_cluster();  // the other CTA's marks and factors: a wait alone acquires from this CTA only
             if (t == s.t0) {
                 if (events > 0) c.wait(BAR_OFREE, (events - 1) & 1);  // the unit before has been read
             } else if (__any_sync(0xffffffffu, flags[pb * 8 + (lane & 7)] == tau + 1)) {
@@ -660,8 +661,8 @@ __device__ void run_softmax(const Cta& c) {
                     st_cluster(to + kOffAlpha + ((tau & 1) * kPairs + pair) * 4, __float_as_uint(alpha));
                     if ((lane & 15) == 0 && changed != 0u)
                         st_cluster(to + kOffFlags + (((tau & 1) * 2 + c.rank) * 4 + q4) * 4, tau + 1);
-                    fence_cluster();
                     __syncwarp();
+                    fence_cluster();  // of all lanes' words, by the lane that arrives
                 }
                 // Also keeps the next tile's maxima from overwriting these.
                 if (!named_bar_any<kBarSoftmax, kSoftmaxThreads>(change) && !first) break;

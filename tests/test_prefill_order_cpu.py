@@ -1,0 +1,40 @@
+"""What one CTA of a pair writes into the other's shared memory is ordered by fences that no result shows
+reliably when they are missing: the source is read for them (csrc/prefill.cu)."""
+import os
+import re
+
+from sparse_mla_paged_gb300 import build as B
+
+
+def body(name):
+    """The text of a __device__ function, without comments."""
+    with open(os.path.join(B.CSRC, "prefill.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    at = re.search(r"__device__ [\w ]*\b%s\(" % name, text).end()
+    depth, start = 0, text.index("{", at)
+    for i in range(start, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[start:i]
+    raise AssertionError(name)
+
+
+def in_order(text, *parts):
+    at = 0
+    for part in parts:
+        at = text.index(part, at) + len(part)
+
+
+def test_marks_are_acquired_from_the_cluster():
+    """The warp that issues P V: between the arrival of a tile's probabilities and the look at the marks."""
+    in_order(body("run_pv"), "c.wait(BAR_PFULL0", "fence_acquire_shared_cluster();", "flags[")
+
+
+def test_marks_are_released_to_the_cluster():
+    """The softmax: factors and marks of all lanes, then a fence by the lane that arrives."""
+    in_order(body("run_softmax"), "st_cluster(to + kOffAlpha", "st_cluster(to + kOffFlags", "__syncwarp();", "fence_cluster();",
+             "c.arrive(BAR_PFULL0")
+
+
+def test_events_are_acquired_by_the_epilogue():
+    in_order(body("run_epilogue"), "BAR_EVENT", "fence_cluster();", "kOffFlags", "kOffAlpha")
