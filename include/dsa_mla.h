@@ -472,7 +472,8 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
  *               device-side DSA_ERR_DEVICE_BOUNDS, as for dsa_plan_step; a row that would see past
  *               max_blocks_per_seq*block_size and a negative block-table entry are taken as
  *               dsa_mla_decode_full takes them.
- *  A NaN code reaches the rows that see its position, no others.
+ *  A NaN code reaches the rows that see its position, no others: in K all 512 dims of their
+ *               outputs, in V its own dim.
  *  workspace    device memory, 256-byte aligned, at least dsa_mla_prefill_workspace_bytes of the
  *               same num_seqs, max_rows and num_q_heads; status, capture and overlapping calls as
  *               for dsa_mla_decode_full.

@@ -48,8 +48,8 @@
 //
 // A tile that holds tokens which some row of the unit does not see is masked per pair, and its V
 // bytes are made safe before P V reads them: a hidden token's zero weight would not silence a NaN
-// code. Tokens past every row are cleared; one with a NaN code that only later rows see is cleared and
-// its score made NaN for the pairs that see it.
+// code. Tokens past every row are cleared; of one that only later rows see the NaN codes are cleared,
+// and the warps that write the unit's output put a NaN into their dims of the rows that see it.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -89,8 +89,12 @@ constexpr int kOffAlpha = kOffHm + 2 * kCtaPairs * 8;        // float [2 tile pa
 constexpr int kOffF = kOffAlpha + 2 * kPairs * 4;            // float [128] output factors, of both CTAs
 constexpr int kOffScale = kOffF + kPairs * 4;                // u8 [2 unit parities][64] exponents of the queries' scales
 constexpr int kOffFlags = kOffScale + 2 * kCtaPairs;         // u32 [2 tile parities][2 CTAs][4 lane quarters] tile that moved a reference
-constexpr int kOffBroken = kOffFlags + 2 * 2 * 4 * 4;        // u32 [2 unit parities][4] tokens from the unit's shortest row on with a NaN code
-constexpr int kOffEvent = kOffBroken + 2 * 4 * 4;            // u32: a tile's number + 1 to rescale before, 0: the unit is done
+// u32 [3 units in turn][4] tokens from the unit's shortest row on with a NaN code. (Not two in turn: an
+// epilogue warp may be at the next unit but one's when another still writes the output. One unit
+// further it is not, as P V waits for that output.)
+constexpr int kOffBroken = kOffFlags + 2 * 2 * 4 * 4;
+static_assert(kOffBroken % 16 == 0, "read as one piece");
+constexpr int kOffEvent = kOffBroken + 3 * 4 * 4;            // u32: a tile's number + 1 to rescale before, 0: the unit is done
 constexpr int kOffProgress = kOffEvent + 4;                  // u32: key tiles asked for
 constexpr int kOffTmem = kOffProgress + 4;
 constexpr int kOffAbort = kOffTmem + 4;
@@ -485,6 +489,13 @@ __device__ __forceinline__ void place_query(const Cta& c, uint32_t units, int ha
     if (lane == 0) c.arrive(BAR_QFULL, 0);
 }
 
+__device__ __forceinline__ uint32_t* broken_of(const Cta& c, uint32_t units) {
+    return reinterpret_cast<uint32_t*>(c.smem + kOffBroken) + units % 3 * 4;
+}
+// Bytes that are NaN codes: 128; and the word with zeros for them.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xFFu); }
+
 __device__ void run_softmax(const Cta& c) {
     constexpr int kSlots = kValueSlots;
     const Params& p = c.p;
@@ -562,7 +573,7 @@ __device__ void run_softmax(const Cta& c) {
             if (t >= edge) {
                 const Segment s = unit();
                 uint8_t* v_tile = c.smem + kOffV + v_slot * kSlotBytes;
-                const uint32_t* broken = reinterpret_cast<const uint32_t*>(c.smem + kOffBroken) + (units & 1) * 4;
+                const uint32_t* broken = broken_of(c, units);
                 // 32 of those marks from position pos on.
                 auto marks = [&](int32_t pos) -> uint32_t {
                     const int32_t i = pos - s.min_len;
@@ -572,26 +583,27 @@ __device__ void run_softmax(const Cta& c) {
                 };
                 // The warp's sixteen tokens: 256 of their dims are here, 8 lanes to 128 of them.
                 const int32_t pos0 = t * kTile + 16 * sw;
-                const uint32_t gone = (pos0 + 16 <= s.max_len ? 0u : ~0u << max(s.max_len - pos0, 0)) | marks(pos0);
-                if ((gone & 0xFFFFu) != 0u) {
+                const uint32_t past = pos0 + 16 <= s.max_len ? 0u : ~0u << max(s.max_len - pos0, 0), nan = marks(pos0);
+                if (((past | nan) & 0xFFFFu) != 0u) {
                     c.wait(BAR_VFULL0 + v_slot, (tau / kSlots) & 1);
-#pragma unroll
+// (Unrolled: 250 requests of 8 rows 123 -> 128.5 us.)
+#pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const int token = (4 * i + (lane >> 3)) & 15, block = i >> 2;
-                        if (gone >> token & 1u)
-                            *reinterpret_cast<uint4*>(v_tile + ((16 * sw + token) >> 3) * kVGroup + block * 1024 + (token & 7) * 128 +
-                                                      (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        uint4* at = reinterpret_cast<uint4*>(v_tile + ((16 * sw + token) >> 3) * kVGroup + block * 1024 + (token & 7) * 128 +
+                                                             (lane & 7) * 16);
+                        if (past >> token & 1u) {
+                            *at = make_uint4(0, 0, 0, 0);
+                        } else if (nan >> token & 1u) {
+                            const uint4 v = *at;
+                            *at = make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
+                        }
                     }
                 }
                 const int32_t lim = seen_by(s) - t * kTile - tok0;  // this thread's scores before it are seen
                 const uint32_t hidden = lim >= 32 ? 0u : lim <= 0 ? ~0u : ~0u << lim;
-                const uint32_t nan = marks(t * kTile + tok0) & ~hidden;
 #pragma unroll
                 for (int j = 0; j < kScores; ++j) x[j] = hidden >> j & 1u ? kNegInf : x[j];
-                if (__any_sync(0xffffffffu, nan != 0u)) {
-#pragma unroll
-                    for (int j = 0; j < kScores; ++j) x[j] = nan >> j & 1u ? __uint_as_float(0x7FC00000u) : x[j];
-                }
             }
             float hm4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
@@ -827,9 +839,8 @@ __device__ uint32_t find_broken(const Cta& c, const Segment& s) {
             const int64_t at = __shfl_sync(0xffffffffu, mine, i);
             uint4 v = make_uint4(0, 0, 0, 0);
             if (at >= 0) v = *reinterpret_cast<const uint4*>(p.v_cache + at + lane * 16);
-            const uint32_t nan = ((v.x & 0x7F7F7F7Fu) + 0x01010101u) | ((v.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                                 ((v.z & 0x7F7F7F7Fu) + 0x01010101u) | ((v.w & 0x7F7F7F7Fu) + 0x01010101u);
-            if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) word |= 1u << i;
+            const uint32_t nan = nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w);
+            if (__any_sync(0xffffffffu, nan != 0u)) word |= 1u << i;
         }
     }
     return word;
@@ -856,11 +867,11 @@ __device__ void prepare_query(const Cta& c, const Segment& s, uint32_t units) {
     const int count = units > 0 ? kOwnPairs : kFirstPairs, h0 = (units > 0 ? 0 : kSoftmaxWarps * kPrepPairs) + q4 * count;
     const Ahead x = ask_queries(c, s.u, h0);
     const uint32_t broken = find_broken(c, s);
-    // The scales and marks of the unit before the last are read. (One barrier for both parities
+    // The scales of the unit before the last are read. (One barrier for both parities
     // could pass two phases meanwhile.)
     if (units > 1) c.wait(BAR_UDONE0 + parity, ((units >> 1) - 1) & 1);
     make_operand(c, s.u, x, parity, h0, count, query_image(c, parity));
-    if (lane == 0) reinterpret_cast<uint32_t*>(c.smem + kOffBroken)[parity * 4 + q4] = broken;
+    if (lane == 0) broken_of(c, units)[q4] = broken;
     __syncwarp();
     if (units == 0) named_bar_sync<kBarFirst, kThreads - kSoftmax0 * 32>();
     if (lane == 0) mbar_arrive(c.bar(BAR_QMADE0 + parity));
@@ -959,6 +970,34 @@ __device__ void run_epilogue(const Cta& c) {
                         *reinterpret_cast<uint4*>(part + ((static_cast<int64_t>(dim0 / 32 + 4 * mc) * (kPairs / 8) + 4 * g + i / 8) * 32 + lane) * 8) =
                             make_uint4(h[0], h[1], h[2], h[3]);
                     }
+            }
+        }
+        // NaN codes that were taken out of their tiles, into the dims of the rows that see them (in one
+        // piece of a split unit: the join carries them on whatever the piece weighs).
+        const uint4 broken = *reinterpret_cast<const uint4*>(broken_of(c, units));
+        if ((broken.x | broken.y | broken.z | broken.w) != 0u) {
+            __syncwarp();  // a lane's output was stored by its neighbour
+#pragma unroll 1
+            for (int i = 0; i < kPairs; ++i) {
+                const int32_t pos = s.min_len + i, t = pos / kTile;
+                if ((broken_of(c, units)[i >> 5] >> (i & 31) & 1u) == 0u || t < s.t0 || t >= s.t1 || pos >= s.max_len) continue;
+                int32_t row;
+                const int32_t page = page_of(p, s.u.seq, pos, &row);
+                if (page < 0) continue;  // (after an abort the marks may be anything)
+                const int64_t before = static_cast<int64_t>(pos - s.u.base) * p.heads - s.u.first;  // pairs that do not see it
+#pragma unroll 1
+                for (int mc = 0; mc < 2; ++mc) {
+                    const int dim = static_cast<int>(c.rank) * kDims + q4 * 32 + mc * 128 + lane;
+                    const uint8_t code = p.v_cache[page * p.cache_stride + static_cast<int64_t>(row) * kLatent + dim];
+                    if ((code & 0x7F) != 0x7F) continue;
+#pragma unroll 1
+                    for (int pair = before > 0 ? static_cast<int>(before) : 0; pair < s.u.valid; ++pair) {
+                        uint16_t* at = whole ? p.out + (s.u.pair0 + pair) * kLatent + dim
+                                             : p.part_o + static_cast<int64_t>(s.part) * kPairs * kLatent +
+                                                   ((dim / 32 * (kPairs / 8) + pair / 8) * 32 + lane) * 8 + pair % 8;
+                        *at = 0x7FFF;  // a NaN in BF16 and in FP16
+                    }
+                }
             }
         }
         tc_fence_before();
