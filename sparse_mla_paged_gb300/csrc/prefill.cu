@@ -96,7 +96,8 @@ constexpr int kOffBroken = kOffFlags + 2 * 2 * 4 * 4;
 static_assert(kOffBroken % 16 == 0, "read as one piece");
 constexpr int kOffEvent = kOffBroken + 3 * 4 * 4;            // u32: a tile's number + 1 to rescale before, 0: the unit is done
 constexpr int kOffProgress = kOffEvent + 4;                  // u32: key tiles asked for
-constexpr int kOffTmem = kOffProgress + 4;
+constexpr int kOffSent = kOffProgress + 4;                   // u32 [2] units whose factors this CTA sent, events that it sent
+constexpr int kOffTmem = kOffSent + 2 * 4;
 constexpr int kOffAbort = kOffTmem + 4;
 constexpr int kOffBars = (kOffAbort + 4 + 7) / 8 * 8;
 // (both): in either CTA; (0): in rank 0, both CTAs arrive.
@@ -161,6 +162,7 @@ struct Cta {
         __syncwarp();
     }
     __device__ volatile uint32_t* progress() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffProgress); }
+    __device__ volatile uint32_t* sent() const { return reinterpret_cast<volatile uint32_t*>(smem + kOffSent); }
     // As wait, for what may take longer than a wait is allowed (a unit of very many tiles): the limit
     // runs anew while tiles come in.
     __device__ void wait_long(int b, uint32_t parity) const {
@@ -380,23 +382,26 @@ __device__ void run_qk(const Cta& c) {
     commit_own_el(c.bar(BAR_DRAIN), el);
 }
 
-__device__ void run_pv(const Cta& c) {
+// Returns the events that were sent.
+__device__ uint32_t run_pv(const Cta& c) {
     constexpr int kSlots = kValueSlots;
     const int lane = threadIdx.x & 31;
     const uint32_t idesc = idesc_e4m3(256, kPairs, true, false);
     const uint32_t el = elect_one();
     const uint64_t pdesc0 = smem_desc(c.sbase + kOffP, 1024, 128, kSwizzleNone);
     const volatile uint32_t* flags = reinterpret_cast<const volatile uint32_t*>(c.smem + kOffFlags);
-    uint32_t tau = 0, events = 0;
+    uint32_t tau = 0, events = 0, sent = 0;
     // Has the epilogue warps of both CTAs do what `event` says.
     auto post = [&](uint32_t event) {
-        if (lane < 2 && !*c.abort_flag) {  // (after an abort nobody waits for one event before the next)
+        ++events;
+        if (__any_sync(0xffffffffu, *c.abort_flag != 0)) return;  // nobody waits for one event before the next then
+        ++sent;
+        if (lane < 2) {
             const uint32_t bar = map_rank(c.bar(BAR_EVENT), lane);
             mbar_arrive_expect_cluster(bar, 4);
             st_async(map_rank(c.sbase + kOffEvent, lane), event, bar);
         }
         __syncwarp();
-        ++events;
     };
     for (Walk w(c);; w.advance()) {
         const Segment& s = w.s;
@@ -436,6 +441,7 @@ __device__ void run_pv(const Cta& c) {
         if (s.last) break;
     }
     commit_own_el(c.bar(BAR_DRAIN), el);
+    return sent;
 }
 
 // Rank 1: its half of each K slot, to rank 0.
@@ -496,7 +502,8 @@ __device__ __forceinline__ uint32_t* broken_of(const Cta& c, uint32_t units) {
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xFFu); }
 
-__device__ void run_softmax(const Cta& c) {
+// Returns the units whose factors were sent.
+__device__ uint32_t run_softmax(const Cta& c) {
     constexpr int kSlots = kValueSlots;
     const Params& p = c.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -701,9 +708,10 @@ __device__ void run_softmax(const Cta& c) {
         // ---- the unit's output factors, to both CTAs ----
         const float lpair = l_part + __shfl_xor_sync(0xffffffffu, l_part, 16);
         if (side == 0) hm_s[half * kCtaPairs + hq].x = lpair;
-        if (named_bar_any<kBarSoftmax, kSoftmaxThreads>(*c.abort_flag != 0)) return;  // all eight warps end together
+        if (half == 0 && units > 0) c.wait(BAR_FEMPTY, (units - 1) & 1);
+        // All eight warps end together, and send nothing before what they sent last has been used.
+        if (named_bar_any<kBarSoftmax, kSoftmaxThreads>(*c.abort_flag != 0)) return units;
         if (half == 0) {
-            if (units > 0) c.wait(BAR_FEMPTY, (units - 1) & 1);
             const float l = hm_s[hq].x + hm_s[kCtaPairs + hq].x;
             const bool whole = s.part < 0;
             const float f = l == 0.0f ? 0.0f : (whole ? p.v_scale : 1.0f) / l;  // nothing seen: zero; NaN stays
@@ -713,8 +721,27 @@ __device__ void run_softmax(const Cta& c) {
         }
         if (lane == 0) mbar_arrive(c.bar(BAR_UDONE0 + (units & 1)));
         named_bar_sync<kBarSoftmax, kSoftmaxThreads>();  // the sums are read
-        if (s.last) break;
+        if (s.last) return units + 1;
     }
+}
+
+// After an aborted call, when both CTAs have ended: what they sent and nobody waited for has arrived here.
+// A CTA sends neither an event nor a unit's factors before the last were used, so that each barrier has
+// one phase open at most, and the CTAs' factors are one unit apart at most: what a barrier was told to
+// expect and what comes are then brought into line.
+__device__ void receive_rest(const Cta& c) {
+    auto count = [&](int i, uint32_t rank) { return ld_cluster(map_rank(c.sbase + kOffSent + 4 * i, rank)); };
+    const uint32_t mine = count(0, c.rank), other = count(0, c.rank ^ 1u), events = count(1, 0);
+    constexpr uint32_t kBytes = kCtaPairs * 4;  // of a unit's factors from either CTA
+    if (mine > other) mbar_complete_tx(c.bar(BAR_FFULL), kBytes);
+    if (mine < other) mbar_arrive_expect_tx(c.bar(BAR_FFULL), kBytes);
+    const uint64_t t0 = globaltimer_ns();
+    auto wait = [&](int b, uint32_t phases) {
+        while (phases > 0 && !mbar_try_wait(c.bar(b), (phases - 1) & 1) && globaltimer_ns() - t0 < kDrainLimitNs) {
+        }
+    };
+    wait(BAR_FFULL, max(mine, other));
+    wait(BAR_EVENT, events);
 }
 
 // ------------------------------------------------------------------------------------
@@ -1041,6 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         mbar_init(c.bar(BAR_FEMPTY), 2 * kEpilogueWarps);
         mbar_init(c.bar(BAR_DRAIN), 2);
         for (int i = 0; i < 16; ++i) reinterpret_cast<uint32_t*>(smem + kOffFlags)[i] = 0;
+        for (int i = 0; i < 2; ++i) c.sent()[i] = 0;
         *c.progress() = 0;
         *c.abort_flag = 0;
         fence_mbar_init();
@@ -1074,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         } else if (warp < kSoftmax0) {
             if (c.rank == 0) {
                 if (warp == 2) run_qk(c);
-                else run_pv(c);
+                else c.sent()[1] = run_pv(c);
                 const uint64_t t0 = globaltimer_ns();
                 while (!mbar_try_wait(c.bar(BAR_DRAIN), 0) && globaltimer_ns() - t0 < kDrainLimitNs) {
                 }
@@ -1084,14 +1112,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             }
         } else if (warp < kEpilogue0) {
             prepare_first(c, warp - kSoftmax0);
-            run_softmax(c);
+            const uint32_t sent = run_softmax(c);
+            if (warp == kSoftmax0) c.sent()[0] = sent;
         } else {
             run_epilogue(c);
-        }
-    }
-    if (*c.abort_flag != 0) {  // words on their way to the other CTA, which nobody waited for, arrive
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 20000) {
         }
     }
     tc_fence_before();
@@ -1099,6 +1123,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // Neither CTA leaves while the other may still reach into it.
     cluster_arrive();
     cluster_wait();
+    if (*c.abort_flag != 0) {  // as both CTAs find by now
+        if (tid == 0) receive_rest(c);
+        __syncthreads();
+        cluster_arrive();  // the counts are read
+        cluster_wait();
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 2) {
         tc_fence_after();

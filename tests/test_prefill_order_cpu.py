@@ -10,7 +10,7 @@ def body(name):
     """The text of a __device__ function, without comments."""
     with open(os.path.join(B.CSRC, "prefill.cu")) as f:
         text = re.sub(r"//[^\n]*", "", f.read())
-    at = re.search(r"__device__ [\w ]*\b%s\(" % name, text).end()
+    at = re.search(r"(?:__device__|__global__) [\w (),]*\b%s\(" % name, text).end()
     depth, start = 0, text.index("{", at)
     for i in range(start, len(text)):
         depth += {"{": 1, "}": -1}.get(text[i], 0)
@@ -38,3 +38,14 @@ def test_marks_are_released_to_the_cluster():
 
 def test_events_are_acquired_by_the_epilogue():
     in_order(body("run_epilogue"), "BAR_EVENT", "fence_cluster();", "kOffFlags", "kOffAlpha")
+
+
+def test_nothing_is_sent_before_the_last_was_used():
+    """What a CTA sends to the other without a wait there: after an abort at most one unit's factors and one
+    event are on their way, and both are waited for before either CTA leaves."""
+    in_order(body("run_softmax"), "c.wait(BAR_FEMPTY", "abort_flag", "return units;", "st_async(")
+    in_order(body("run_pv"), "abort_flag", "return;", "st_async(")
+    in_order(body("receive_rest"), "BAR_FFULL", "wait(BAR_FFULL", "wait(BAR_EVENT")
+    end = body("prefill_kernel")
+    in_order(end, "run_softmax(c)", "cluster_wait();", "if (*c.abort_flag", "receive_rest(c);", "cluster_wait();", "tmem_dealloc_pair")
+    assert "globaltimer_ns() - t0 < 20000" not in end
