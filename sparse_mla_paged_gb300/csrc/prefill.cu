@@ -119,7 +119,7 @@ enum {
     BAR_FFULL,                               // (both) output factors written
     BAR_FEMPTY,                              // (both) and used
     BAR_UDONE0,                              // 2: the softmax warps are done with a unit (by its parity)
-    BAR_DRAIN = BAR_UDONE0 + 2,              // (0) every MMA is done
+    BAR_DRAIN = BAR_UDONE0 + 2,              // (both) every MMA is done
     kNumBars
 };
 constexpr int kSmem = kOffBars + kNumBars * 8;
@@ -379,7 +379,7 @@ __device__ void run_qk(const Cta& c) {
         }
         if (s.last) break;
     }
-    commit_own_el(c.bar(BAR_DRAIN), el);
+    commit_both_el(c.bar(BAR_DRAIN), el);
 }
 
 // Returns the events that were sent.
@@ -440,7 +440,7 @@ __device__ uint32_t run_pv(const Cta& c) {
         post(0);
         if (s.last) break;
     }
-    commit_own_el(c.bar(BAR_DRAIN), el);
+    commit_both_el(c.bar(BAR_DRAIN), el);
     return sent;
 }
 
@@ -1100,15 +1100,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             else if (warp == 0) run_load_tma<false>(c, &kmap);
             else run_load_tma<true>(c, &vmap);
         } else if (warp < kSoftmax0) {
-            if (c.rank == 0) {
-                if (warp == 2) run_qk(c);
-                else c.sent()[1] = run_pv(c);
+            if (warp == 2) {
+                if (c.rank == 0) run_qk(c);
+                else run_forward(c);
+            } else if (c.rank == 0) {
+                c.sent()[1] = run_pv(c);
+            }
+            // In both CTAs: products arrive at barriers of both, and for the last arrivals nobody else waits.
+            if (warp == 2 || c.rank == 0) {
                 const uint64_t t0 = globaltimer_ns();
                 while (!mbar_try_wait(c.bar(BAR_DRAIN), 0) && globaltimer_ns() - t0 < kDrainLimitNs) {
                 }
                 __syncwarp();
-            } else if (warp == 2) {
-                run_forward(c);
             }
         } else if (warp < kEpilogue0) {
             prepare_first(c, warp - kSoftmax0);

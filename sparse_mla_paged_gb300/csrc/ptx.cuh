@@ -376,7 +376,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 // The pair's MMAs (issued in the CTA of rank 0; each CTA's half of the operands at the same
 // shared-memory offsets) and commits, by the lane with el != 0. A commit reaches the barrier at the
-// same offset in both CTAs, or only the issuer's.
+// same offset in both CTAs.
 __device__ __forceinline__ void mma_pair_ss_el(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
                                                uint32_t el) {
     asm volatile(
@@ -405,15 +405,6 @@ __device__ __forceinline__ void commit_both_el(uint32_t bar, uint32_t el) {
         "h"(static_cast<uint16_t>(3)), "r"(el)
         : "memory");
 }
-__device__ __forceinline__ void commit_own_el(uint32_t bar, uint32_t el) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "setp.ne.b32 e, %1, 0;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-        "r"(el)
-        : "memory");
-}
-
 // Shared-memory matrix descriptor (tcgen05 form): start address, leading / stride byte
 // offsets (16-byte units), descriptor version 1, swizzle mode in bits 61-63
 // (0 none, 2 = 128-byte, 4 = 64-byte, 6 = 32-byte).

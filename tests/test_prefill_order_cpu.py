@@ -49,3 +49,10 @@ def test_nothing_is_sent_before_the_last_was_used():
     end = body("prefill_kernel")
     in_order(end, "run_softmax(c)", "cluster_wait();", "if (*c.abort_flag", "receive_rest(c);", "cluster_wait();", "tmem_dealloc_pair")
     assert "globaltimer_ns() - t0 < 20000" not in end
+
+
+def test_both_ctas_wait_for_the_last_products():
+    """A commit arrives at barriers of both CTAs: neither leaves before the last ones are there."""
+    for name in ("run_qk", "run_pv"):
+        in_order(body(name), "commit_both_el", "commit_both_el(c.bar(BAR_DRAIN)")
+    in_order(body("prefill_kernel"), "run_forward(c)", "if (warp == 2 || c.rank == 0)", "c.bar(BAR_DRAIN), 0)")
