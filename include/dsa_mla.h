@@ -474,6 +474,10 @@ int32_t dsa_mla_decode_full(const void* q, const void* k_cache, const void* v_ca
  *               dsa_mla_decode_full takes them.
  *  A NaN code reaches the rows that see its position, no others: in K all 512 dims of their
  *               outputs, in V its own dim.
+ *  Precision    as in the decodes, queries and probabilities are two 8-bit terms each: a query
+ *               element below 2^-9 of its head's largest is off by up to 2^-16 of that largest (with
+ *               one element 300 times the others 0.1 % of the output, 1000 times 0.2 %, 3000 times
+ *               1 %), and a row loses up to 2^-8 of its mass.
  *  workspace    device memory, 256-byte aligned, at least dsa_mla_prefill_workspace_bytes of the
  *               same num_seqs, max_rows and num_q_heads; status, capture and overlapping calls as
  *               for dsa_mla_decode_full.
