@@ -275,7 +275,7 @@ class _Launch:
             self.stream = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(self.raw, device=index)
 
     def __enter__(self):
-        if torch._C._cuda_getDevice() != self.index:
+        if torch.cuda.current_device() != self.index:
             self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
         return self
