@@ -74,12 +74,12 @@ struct Line {
     int64_t length, gap;
     int32_t ctas;  // ranges; none is empty
 };
-__host__ __device__ inline Line make_line(int64_t tiles, int32_t live, int32_t max_ctas) {
+__host__ __device__ inline Line make_line(int64_t tiles, int32_t live, int32_t max_ctas, int32_t most_gap = kGap) {
     Line l;
     l.ctas = static_cast<int32_t>(tiles < max_ctas ? tiles : max_ctas);
     // At most a quarter of a range, so that no range lies inside a gap.
     l.gap = tiles / (4 * max_ctas);
-    if (l.gap > kGap) l.gap = kGap;
+    if (l.gap > most_gap) l.gap = most_gap;
     l.length = tiles + l.gap * (live > 0 ? live - 1 : 0);
     return l;
 }

@@ -44,13 +44,13 @@ struct Head {
 // where a mark is expected to be zero.
 constexpr uint32_t kSegment = 1 << 14;
 constexpr uint32_t kSegmentMarks = kSegment / 32;
-constexpr int64_t kSegmentWords = kSegmentMarks + 3 * kSegment;
+constexpr uint32_t kSegmentWords = kSegmentMarks + 3 * kSegment;
 static_assert(kSegment >= DSA_MAX_PLAN_SEQS, "a fork's lists lie in the first segment");
 static_assert(kSegmentMarks % 4 == 0 && kSegmentWords % 4 == 0, "whole 16-byte pieces");
 
-// Place of mark word w behind the first one, and of a list's entry i behind its first.
-__host__ __device__ inline int64_t mark_at(uint32_t w) { return w / kSegmentMarks * kSegmentWords + w % kSegmentMarks; }
-__host__ __device__ inline int64_t entry_at(uint32_t i) { return i / kSegment * kSegmentWords + i % kSegment; }
+// Place of mark word w behind the first one, and of a list's entry i behind its first (below 2^32 for 2^30 pages).
+__host__ __device__ inline uint32_t mark_at(uint32_t w) { return w / kSegmentMarks * kSegmentWords + w % kSegmentMarks; }
+__host__ __device__ inline uint32_t entry_at(uint32_t i) { return i / kSegment * kSegmentWords + i % kSegment; }
 
 // Marks are a bit per page, in whole 16-byte pieces.
 inline int64_t mark_words(int64_t pages) { return (pages + 127) / 128 * 4; }
@@ -63,7 +63,7 @@ inline Layout layout(int64_t pages) {
     L.rank = L.marks + kSegmentMarks * 4;
     L.src = L.rank + kSegment * 4;
     L.dst = L.src + kSegment * 4;
-    L.total = L.marks + static_cast<size_t>((pages + kSegment - 1) / kSegment * kSegmentWords) * 4;
+    L.total = L.marks + static_cast<size_t>((pages + kSegment - 1) / kSegment) * kSegmentWords * 4;
     return L;
 }
 

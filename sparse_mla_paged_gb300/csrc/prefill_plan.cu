@@ -113,12 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefill_plan_kernel(const __grid
     walk([&](int32_t, int32_t, int32_t, int32_t, int32_t, int32_t t) { tiles += t; });
     int64_t all;
     int64_t before = scan<kWarps>(tiles, sums, &all);
-    full::Line line;
-    line.ctas = static_cast<int32_t>(all < p.clusters ? all : p.clusters);
-    // At most a quarter of a range, so that no range lies inside a gap.
-    line.gap = all / (4 * p.clusters);
-    if (line.gap > kGap) line.gap = kGap;
-    line.length = all + line.gap * (units > 0 ? units - 1 : 0);
+    const full::Line line = full::make_line(all, units, p.clusters, kGap);
     walk([&](int32_t u, int32_t s, int32_t base, int32_t first, int32_t valid, int32_t t) {
         const int64_t b = before + line.gap * u, e = b + t;
         before += t;
