@@ -47,7 +47,7 @@ def test_nothing_is_sent_before_the_last_was_used():
     in_order(body("run_pv"), "abort_flag", "return;", "st_async(")
     in_order(body("receive_rest"), "BAR_FFULL", "wait(BAR_FFULL", "wait(BAR_EVENT")
     end = body("prefill_kernel")
-    in_order(end, "run_softmax(c)", "cluster_wait();", "if (*c.abort_flag", "receive_rest(c);", "cluster_wait();", "tmem_dealloc_pair")
+    in_order(end, "run_softmax(c)", "cluster_wait();", "if (*c.abort_flag", "receive_rest(", "cluster_wait();", "tmem_dealloc_pair")
     assert "globaltimer_ns() - t0 < 20000" not in end
 
 
