@@ -593,7 +593,8 @@ int32_t dsa_release_pages(int32_t* block_tables, int32_t max_blocks_per_seq, con
  * first n pages: the live pages from n on, in ascending order, are copied in all pools to the dead
  * pages below n, in ascending order, and tables and shares follow. Pages that no table names end up
  * free: shares 0, and the free list is n .. num_pages - 1. What lies in pages from n on afterwards
- * is not to be used.
+ * is not to be used. A running loop does not need it, as any free page is as good as another: it is
+ * for a pool that is to become smaller, or to be saved or sent in one piece.
  *  free_pages   int32 [num_pages]; num_free  int32 [1]; both written.
  *  info         live pages, pages moved, status (an entry past num_pages sets it and stays; a negative
  *               one stays), free pages.

@@ -539,8 +539,8 @@ def pages_workspace_bytes(num_pages: int) -> int:
 
 
 def alloc_pages_workspace(num_pages: int, device=None) -> torch.Tensor:
-    """A workspace for fork_pages, release_pages and compact_pages, to be kept from call to call (one
-    per stream or captured graph)."""
+    """A workspace for fork_pages, release_pages and compact_pages on pools of up to num_pages pages, to be
+    kept from call to call (one per stream or captured graph)."""
     n = pages_workspace_bytes(num_pages)
     if n == 0:
         raise DsaError(2, "dsa_pages_workspace_bytes")
@@ -697,8 +697,8 @@ def release_pages(block_tables: torch.Tensor, lens: torch.Tensor, keep_lens: tor
 def compact_pages(pools, block_tables: torch.Tensor, lens: torch.Tensor, block_size: int, page_shares: torch.Tensor,
                   free_pages: torch.Tensor, num_free: torch.Tensor, info=None, workspace=None, stream=None) -> torch.Tensor:
     """dsa_compact_pages: the n pages that the requests' tables name move to the pools' first n pages;
-    tables, shares and the free list follow. All in place. Returns info, int32 [4]: live pages, pages
-    moved, status, free pages."""
+    tables, shares and the free list follow (before a pool becomes smaller, or is saved or sent in one
+    piece). All in place. Returns info, int32 [4]: live pages, pages moved, status, free pages."""
     i = _device_of(block_tables, "block_tables")
     _need_ints(i, (block_tables, lens, page_shares, free_pages, num_free),
                ("block_tables", "lens", "page_shares", "free_pages", "num_free"))

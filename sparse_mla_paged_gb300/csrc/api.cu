@@ -959,12 +959,13 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
     p.cache_stride = cache_stride_bytes;
     p.clusters = d->sms / 2;
     // A piece list is long when units are few: eight warps share it then. (2 rows of 64 heads a unit, over
-    // 32k tokens, with eight warps a piece list and with one: 1 unit 31.4 and 40.4 us, 4 units 43.8
-    // and 46.1, 6 units 54.0 and 51.9, 7 units 58.9 and 55.2; 8 units of 2 tiles 22.2 and 18.1.)
+    // 32k tokens, with eight warps a piece list and with one: 1 unit 26.8 and 36.2 us, 4 units 39.4
+    // and 39.6, 5 units 44.7 and 43.6, 7 units 53.9 and 50.2; 8 units of 2 tiles 22.3 and 18.0. A request
+    // may have a unit more than its rows fill, so the count here is one above these.)
     p.few_units = units * 15 <= p.clusters ? 1 : 0;
     p.most_joins = static_cast<int32_t>(std::min<int64_t>(units, p.clusters));
     // A block of 256 threads, with cheaper barriers, while they have one request and a few units each
-    // (5 rows of 16 heads 18.5 us, 19.7 with 1024 threads; 250 requests of 4 units each 135.5 both).
+    // (5 rows of 16 heads 17.4 us, 18.5 with 1024 threads; 250 requests of 4 units each 120.6 and 120.0).
     p.small_plan = num_seqs <= 256 && units <= 1024 ? 1 : 0;
     const int64_t room = max_blocks_per_seq > 0 ? static_cast<int64_t>(max_blocks_per_seq) * block_size : full::kMaxLen;
     p.room = static_cast<int32_t>(std::min(room, full::kMaxLen));
@@ -978,8 +979,8 @@ int32_t dsa_mla_prefill(const void* q, const void* k_cache, const void* v_cache,
     p.score_scale = sm_scale * k_scale * 1.4426950408889634f;
     p.v_scale = v_scale;
     p.wait_limit_ns = g_wait_limit_ns;
-    // Other page sizes take per-thread copies (2000 rows of 20 heads over pages of 8, 16 or 24 tokens:
-    // boxes 124 us, copies 131).
+    // Other page sizes take per-thread copies (2000 rows of 20 heads over pages of 8, 16 and 24 tokens:
+    // boxes 109, 107.5 and 112 us, copies 114.5, 113 and 116.5).
     p.box_rows = std::min(box_rows(block_size), 32);
     CUtensorMap kmap, vmap;
     std::memset(&kmap, 0, sizeof kmap);

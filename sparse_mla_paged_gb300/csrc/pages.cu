@@ -4,11 +4,11 @@
 //
 // The books (tables, shares, free list) are bound by latency: a launch each for what every block
 // has to know of the others', the launches overlapped, and within each a few dependent loads and
-// barriers. 64 requests that give back their drafts 5 us (two launches), half of 256 requests with
-// 1.2 thousand pages each 15, a fork of four ways 4.4 (two launches), a pool of 380 pages compacted
-// 7 (three launches).
-// Page data is bound by HBM: 1024 pages of two pools in four layers, 338 MB read and written, 54 us,
-// 6.2 TB/s, 92 % of a plain copy's rate. Blocks of 256 threads with four 16-byte pieces in flight
+// barriers. 64 requests that give back their drafts 6.9 us (two launches), half of 256 requests with
+// 1.2 thousand pages each 17.7, a fork of four ways 4.6 (two launches), a pool of 380 pages compacted
+// 8.9 (three launches), each measured with a copy of the books in front: 1.2 us, 4.0 in the second.
+// Page data is bound by HBM: 1024 pages of two pools in four layers, 338 MB read and written, 53 us,
+// 6.4 TB/s, 94 % of a plain copy's rate. Blocks of 256 threads with four 16-byte pieces in flight
 // each, eight blocks to an SM, are what it takes; pieces pass the caches by, as they are not read again.
 #include "pages.cuh"
 #include "ptx.cuh"

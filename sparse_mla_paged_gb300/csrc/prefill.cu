@@ -28,8 +28,8 @@
 // the two query terms and P V twice for those of P', 4 x 128 x 128 x 512 multiply-adds of E4M3 per
 // unit and tile. 1024 rows of 64 heads after 31.7k cached tokens (4.5 TFLOP of bf16 arithmetic):
 // 2.28 ms in short bursts, 1960 TFLOP/s (a bf16 matrix product of the library: 1924), 2.54 in a long
-// loop, at the power limit, 1760 (1725); one prompt of 4096 rows, 735 us, 1500; 512 rows over 4096
-// tokens, 173 us, 1490. There a change of unit is what is lost: some 7000 cycles between products
+// loop, at the power limit, 1760 (1725); one prompt of 4096 rows, 732 us, 1500; 512 rows over 4096
+// tokens, 168 us, 1530. There a change of unit is what is lost: some 7000 cycles between products
 // with V, where tiles follow at 2500. (9500 with the operand put in place by warps 12-15 once the last
 // product is issued; by them, earlier, on an event of its own: 3 % more on short units, for one
 // wait more.) Every instruction less in the softmax also saves power, and so time on long calls.
@@ -285,8 +285,8 @@ __device__ void run_load_tma(const Cta& c, const CUtensorMap* tmap) {
 // The same by 16-byte copies: an instruction brings 128 bytes of each of four rows. Both warps run one
 // code, for what they bring of a tile has one shape: four half rows of 256 bytes for each lane to
 // look up, of two tokens' keys or of four tokens' values. (2000 rows of 20 heads over pages of 100
-// tokens 134 us; with a code each 165, and more the more it was unrolled: the instruction cache
-// holds the softmax as well. Boxes, where a page takes them: 124.)
+// tokens 113 us; when it took 134, a code each took 165, and more the more it was unrolled: the
+// instruction cache holds the softmax as well. Boxes, where a page takes them: 107 to 112.)
 __device__ void run_load_copies(const Cta& c, bool values) {
     constexpr int kEach = 4;
     const Params& p = c.p;

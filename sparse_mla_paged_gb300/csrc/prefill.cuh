@@ -17,7 +17,8 @@ namespace prefill {
 constexpr int kPairs = 128;  // (row, head) pairs of a unit, 64 in each CTA of a cluster
 constexpr int kTile = full::kTile;
 // Tiles that a unit change costs, at most a quarter of a range. (One prompt of 4096 rows of 64 heads with
-// gaps of 3, 4, 5, 6 and 8 tiles: 1001, 880, 790, 780 and 798 us; 128 short requests: 116, 108, 100, 97, 97.)
+// gaps of 3, 4, 5, 6 and 8 tiles: 1003, 882, 796, 734 and 735 us; 128 short requests: 99, 96, 95, 95, 95; a mixed
+// batch: 1953, 1934, 1949, 1949, 1973.)
 constexpr int kGap = 6;
 
 struct alignas(16) Unit {
