@@ -593,7 +593,7 @@ __device__ uint32_t run_softmax(const Cta& c) {
                 const uint32_t past = pos0 + 16 <= s.max_len ? 0u : ~0u << max(s.max_len - pos0, 0), nan = marks(pos0);
                 if (((past | nan) & 0xFFFFu) != 0u) {
                     c.wait(BAR_VFULL0 + v_slot, (tau / kSlots) & 1);
-// (Unrolled: 250 requests of 8 rows 123 -> 128.5 us.)
+// (Unrolled: 250 requests of up to 8 rows 123 -> 128.5 us.)
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const int token = (4 * i + (lane >> 3)) & 15, block = i >> 2;
