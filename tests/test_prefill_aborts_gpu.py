@@ -39,7 +39,7 @@ def test_calls_that_give_up(api, base, new, heads, bs):
             with api.wait_limit(limit):
                 api.prefill(*a, out=out, workspace=ws)
             status = api.read_device_status(ws)
-            assert time.perf_counter() - t0 < 0.5  # nothing waited for what does not come
+            assert time.perf_counter() - t0 < 0.9  # a wait for what does not come takes 1 s
             assert status in (0, TIMEOUT) and api.step_device_status() == status
             ended.add(status)
             if status == 0:
